@@ -220,7 +220,8 @@ int scape_read_sparse(scape_handle* h, int w, uint32_t* idx, float* vals, uint64
 /* Message of the handle's last error ("" if none).  Valid until the next call
  * on the handle.  h == NULL gives the message of the last failure, on this
  * thread, of a call that has no handle: scape_create, scape_create_ex,
- * scape_unpack, scape_dense_adams_step, scape_step_noalloc. */
+ * scape_unpack, scape_dense_adams_step, scape_step_noalloc and the calls of
+ * the training objective. */
 const char* scape_last_error(const scape_handle* h);
 
 /* enable != 0: every later step records CUDA events around each kernel phase
@@ -354,6 +355,130 @@ typedef struct {
 
 int scape_step_noalloc(const scape_step_buffers* buffers, const void* const* grad_ptrs,
                        void* stream);
+
+/* ---- Training objective ------------------------------------------------------
+ * What the gradients of scape_step come from, where the trained model is a
+ * student of a larger one or a mixture of experts: the top logits that a
+ * teacher leaves behind, the loss of a student against them with its gradient,
+ * and an expert router with its balance loss and gradients.  All calls are
+ * stateless: pointers are DEVICE pointers owned by the caller unless said
+ * otherwise, nothing is allocated, the work is enqueued on "stream" and the
+ * call returns.  Argument errors give SCAPE_EINVAL and launch errors
+ * SCAPE_ECUDA, with the message in scape_last_error(NULL).  Results do not
+ * depend on how the GPU schedules the work: the same inputs give the same
+ * bits.
+ *
+ * Logits are rows of bf16, fp16 or fp32 elements, each row contiguous, rows
+ * row_stride elements apart (row_stride >= the row's length; any alignment of
+ * the element's own size).  -inf marks an element that is out of the running.
+ * Arithmetic is fp32: softmax statistics, sums and losses are held in fp32,
+ * gradients are rounded once to the logits' type. */
+enum { SCAPE_BF16 = 0, SCAPE_F16 = 1, SCAPE_F32 = 2 };
+
+/* The k largest logits of every row, in descending order, equal logits by
+ * ascending index (+0 and -0 are equal; NaN ranks above +inf), and the row's
+ * log-sum-exp at a temperature:
+ *   idx[r][i], vals[r][i] (logits' type, unchanged), lse[r] = log sum_j exp(x[r][j] / temperature)
+ * idx and vals are rows x k, contiguous; vals and lse may be NULL.
+ * 1 <= k <= min(vocab, 1024); 1 <= vocab < 2^31; rows = 0 is a no-op. */
+int scape_topk_logits(const void* logits, int dtype, uint64_t rows, uint64_t vocab,
+                      uint64_t row_stride, int k, float temperature, int32_t* idx, void* vals,
+                      float* lse, void* stream);
+
+/* Distillation from a teacher's top logits, mixed with the cross entropy of a
+ * hard label.  For one row x of student logits, with s = x / temperature,
+ * p = softmax(s), and the teacher's entries t_i = vals_i / temperature at the
+ * distinct coordinates idx_i:
+ *   teacher_lse == NULL:  q_i = exp(t_i) / sum_i exp(t_i)
+ *   else:                 q_i = exp(t_i - teacher_lse); what is left of the
+ *                         teacher's mass, q_rest = max(0, 1 - sum_i q_i), faces
+ *                         the student's mass p_rest on all coordinates not
+ *                         listed, as one bucket
+ *   KL   = sum_i q_i (log q_i - log p_idx_i) + q_rest (log q_rest - log p_rest)
+ *   CE   = log sum_j exp(x_j) - x_label
+ *   loss = row_weight * (kd_weight * temperature^2 * KL + ce_weight * CE)
+ *   grad = d loss / d x
+ * Entries with idx < 0 are empty and those with vals = -inf have q = 0; a row
+ * without any other entry has no KL term, nor has p_rest = 0 a bucket.  A label
+ * < 0 (by custom -100) leaves out the CE term.  A row of weight 0 is not read:
+ * its loss and gradient are 0 whatever it holds.  idx or label >= vocab is
+ * treated as empty and counted into *bad_count.  A coordinate listed twice in
+ * a row makes that row's results unspecified. */
+typedef struct {
+  const void* logits; /* rows x vocab, row_stride elements apart */
+  int dtype;          /* SCAPE_BF16, SCAPE_F16 or SCAPE_F32 */
+  int k;              /* teacher entries of a row, 0 <= k <= 1024 (0: no KL term) */
+  uint64_t rows;
+  uint64_t vocab; /* < 2^31 */
+  uint64_t row_stride;
+  const int32_t* idx; /* rows x k, contiguous */
+  const void* vals;   /* rows x k, contiguous, of type vals_dtype */
+  int vals_dtype;
+  float temperature; /* > 0 */
+  float kd_weight;
+  float ce_weight;
+  const float* teacher_lse; /* rows: log-sum-exp of the teacher's whole row at the same
+                               temperature (scape_topk_logits), or NULL */
+  const int64_t* labels;    /* rows, or NULL */
+  const float* row_weight;  /* rows, or NULL (all 1) */
+  float* loss;              /* rows, or NULL */
+  void* grad;               /* rows x vocab of the logits' type, or NULL (loss alone).  May be
+                               the logits themselves (same pointer and stride): they are then
+                               overwritten by their gradient. */
+  uint64_t grad_stride;
+  uint32_t* bad_count; /* one counter, added to, or NULL */
+} scape_distill_args;
+
+int scape_distill_loss(const scape_distill_args* args, void* stream);
+
+/* Expert routing.  tokens x experts logits; a token is live if valid (where
+ * given) is non-zero for it and one of its logits is above -inf.  For a live token,
+ * p = softmax(x) over the experts, and it goes to the k experts of largest
+ * logit (descending, equal logits by ascending expert) with weights
+ *   renormalize != 0: softmax over the k chosen logits;  else p at them.
+ * Tokens form groups: n_groups = G >= 1 and group g holds the tokens
+ * [cu_tokens[g], cu_tokens[g+1]) (G+1 ascending entries, cu_tokens[0] = 0 and
+ * cu_tokens[G] = tokens; empty groups are fine; a token outside all groups is
+ * not live), or cu_tokens = NULL and G = 1.  With T_g live tokens in group g,
+ * c_ge of their choices on expert e:
+ *   balance = mean over the groups with T_g > 0 of
+ *             sum_e (experts * c_ge / (k * T_g)) * (sum_t p_te / T_g)
+ *   z       = mean over the live tokens of (log sum_e exp(x_te))^2 */
+typedef struct {
+  const void* logits; /* tokens x experts, row_stride elements apart */
+  int dtype;
+  int k;           /* 1 <= k <= min(experts, 32) */
+  uint64_t tokens; /* < 2^31 */
+  int experts;     /* 1 <= experts <= 1024 */
+  int renormalize;
+  uint64_t row_stride;
+  const int32_t* cu_tokens; /* DEVICE, n_groups + 1, or NULL */
+  uint64_t n_groups;        /* >= 1, and n_groups * experts < 2^31; 1 without cu_tokens */
+  const uint8_t* valid;     /* tokens, or NULL */
+} scape_route_args;
+
+/* Bytes of device workspace that scape_route needs for these sizes (host call,
+ * no device work; pointers in args are not looked at). */
+int scape_route_workspace(const scape_route_args* args, uint64_t* bytes);
+
+/* Forward: idx and weights (tokens x k, contiguous; -1 and 0 for a token that
+ * is not live), counts (n_groups x experts), live (n_groups + 2: T_g of every
+ * group, their sum, the number of groups with T_g > 0) and losses (balance, z).
+ * The workspace (16-byte aligned) is scratch of this call: it needs no
+ * initial value and may be used again by later work of the same stream. */
+int scape_route(const scape_route_args* args, int32_t* idx, float* weights, int32_t* counts,
+                int32_t* live, float* losses, void* workspace, uint64_t workspace_bytes,
+                void* stream);
+
+/* Backward: grad (tokens x experts of the logits' type, grad_stride elements
+ * apart, not the logits themselves) of
+ *   sum d_weights * weights + d_losses[0] * balance + d_losses[1] * z
+ * where the counts are constants.  idx, counts and live are the forward's;
+ * d_weights (tokens x k) and d_losses (2) may be NULL (zero).  args->valid is
+ * not read (idx tells the live tokens).  Needs no workspace. */
+int scape_route_backward(const scape_route_args* args, const int32_t* idx, const int32_t* counts,
+                         const int32_t* live, const float* d_weights, const float* d_losses,
+                         void* grad, uint64_t grad_stride, void* stream);
 
 #ifdef __cplusplus
 }

@@ -14,7 +14,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libscape.so")
 DEBUG_LIB = os.path.join(HERE, "libscape_debug.so")
 SOURCES = ["scape_api.cu", "k_fused.cu", "k_select.cu", "k_dense.cu", "k_maskops.cu",
-           "scape_noalloc.cu"]
+           "scape_noalloc.cu", "k_topk.cu", "k_distill.cu", "k_route.cu"]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo",

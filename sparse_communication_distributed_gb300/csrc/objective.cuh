@@ -1,0 +1,180 @@
+// Device helpers of the training-objective operators (k_topk.cu, k_distill.cu,
+// k_route.cu): rows of bf16, fp16 or fp32 logits read in 16-byte vectors.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "../../include/scape.h"
+#include "scape_device.cuh"
+
+namespace scape {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
+
+// 2^x, relative error below 2^-22 (PTX ex2.approx); 2^-inf = +0, NaN stays NaN.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 16-byte load of a row that is read once.  Not the read-only path: a gradient
+// may overwrite the logits in the same kernel.
+__device__ __forceinline__ uint4 ld_row_u4(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
+// A maximum as the shift of a softmax: exp2((x - m) * c) of a row that holds
+// nothing but -inf is then exp2(-inf) = 0 and not NaN.
+__device__ __forceinline__ float shift_of(float m) { return m == neg_inf() ? 0.0f : m; }
+
+template <int DT>
+struct Elem;
+
+template <>
+struct Elem<SCAPE_BF16> {
+  using T = uint16_t;
+  static constexpr int kPerVec = 8;
+  static __device__ __forceinline__ float load(const T* p) { return bf16f(*p); }
+  static __device__ __forceinline__ T make(float f) {
+    return __bfloat16_as_ushort(__float2bfloat16_rn(f));
+  }
+  static __device__ __forceinline__ void unpack(const uint4 r, float (&f)[8]) {
+    f[0] = bf16lo(r.x); f[1] = bf16hi(r.x); f[2] = bf16lo(r.y); f[3] = bf16hi(r.y);
+    f[4] = bf16lo(r.z); f[5] = bf16hi(r.z); f[6] = bf16lo(r.w); f[7] = bf16hi(r.w);
+  }
+  static __device__ __forceinline__ uint32_t pack2(float a, float b) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+  }
+  static constexpr uint32_t kNegInf2 = 0xFF80FF80u;  // two lowest elements
+};
+
+template <>
+struct Elem<SCAPE_F16> {
+  using T = uint16_t;
+  static constexpr int kPerVec = 8;
+  static __device__ __forceinline__ float load(const T* p) {
+    return __half2float(__ushort_as_half(*p));
+  }
+  static __device__ __forceinline__ T make(float f) { return __half_as_ushort(__float2half_rn(f)); }
+  static __device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b) {
+    const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    a = t.x;
+    b = t.y;
+  }
+  static __device__ __forceinline__ void unpack(const uint4 r, float (&f)[8]) {
+    unpack2(r.x, f[0], f[1]); unpack2(r.y, f[2], f[3]);
+    unpack2(r.z, f[4], f[5]); unpack2(r.w, f[6], f[7]);
+  }
+  static __device__ __forceinline__ uint32_t pack2(float a, float b) {
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+  }
+  static constexpr uint32_t kNegInf2 = 0xFC00FC00u;
+};
+
+template <>
+struct Elem<SCAPE_F32> {
+  using T = float;
+  static constexpr int kPerVec = 4;
+  static __device__ __forceinline__ float load(const T* p) { return *p; }
+  static __device__ __forceinline__ T make(float f) { return f; }
+  static __device__ __forceinline__ void unpack(const uint4 r, float (&f)[4]) {
+    f[0] = __uint_as_float(r.x); f[1] = __uint_as_float(r.y);
+    f[2] = __uint_as_float(r.z); f[3] = __uint_as_float(r.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+  }
+  static constexpr uint32_t kNegInf2 = 0xFF800000u;  // (one element)
+};
+
+// One row seen as 16-byte vectors on 16-byte boundaries.  A row starts at any
+// element (odd vocabularies, views): vector v holds the elements
+// [v * kPerVec - shift, + kPerVec), and those outside [0, n) read as -inf.
+template <int DT>
+struct RowView {
+  using E = Elem<DT>;
+  using T = typename E::T;
+  const T* p;
+  int64_t n;
+  int shift;
+  __device__ __forceinline__ RowView(const void* base, int64_t first, int64_t len)
+      : p(static_cast<const T*>(base) + first), n(len) {
+    shift = (int)((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
+  }
+  __device__ __forceinline__ int64_t vectors() const {
+    return (n + shift + E::kPerVec - 1) / E::kPerVec;
+  }
+  __device__ __forceinline__ int64_t first_of(int64_t v) const { return v * E::kPerVec - shift; }
+  __device__ __forceinline__ bool whole(int64_t v) const {
+    const int64_t e = first_of(v);
+    return e >= 0 && e + E::kPerVec <= n;
+  }
+  __device__ __forceinline__ uint4 load(int64_t v) const {
+    const int64_t e = first_of(v);
+    if (e >= 0 && e + E::kPerVec <= n) return ld_row_u4(p + e);
+    float f[E::kPerVec];
+#pragma unroll
+    for (int j = 0; j < E::kPerVec; j++)
+      f[j] = (e + j >= 0 && e + j < n) ? E::load(p + e + j) : neg_inf();
+    return E::pack(f);
+  }
+};
+
+// Ordered key of a logit: unsigned comparison ranks as the values do, +0 and
+// -0 alike, NaN above +inf.  No logit has key 0.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  if (x != x) return 0xFFFFFFFFu;
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// Sum / maximum over the CTA; every thread receives it.  "buf" is shared
+// scratch of 32 entries; the calls contain two __syncthreads().
+template <class V>
+__device__ __forceinline__ V cta_sum(V x, V* buf) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+  const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  __syncthreads();
+  if (lane == 0) buf[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = lane < nw ? buf[lane] : V(0);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+  return x;
+}
+
+__device__ __forceinline__ float cta_max(float x, float* buf) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+  const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  __syncthreads();
+  if (lane == 0) buf[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = lane < nw ? buf[lane] : neg_inf();
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+  return x;
+}
+
+}  // namespace scape

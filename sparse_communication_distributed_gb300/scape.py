@@ -26,7 +26,8 @@ EXPORTS = ("scape_create", "scape_create_ex", "scape_step", "scape_step_host", "
            "scape_mask_async", "scape_destroy",
            "scape_info", "scape_read_state", "scape_load_state", "scape_read_sparse",
            "scape_last_error", "scape_profile", "scape_profile_read", "scape_step_noalloc",
-           "scape_dense_adams_step", "scape_mask_stats", "scape_unpack")
+           "scape_dense_adams_step", "scape_mask_stats", "scape_unpack", "scape_topk_logits",
+           "scape_distill_loss", "scape_route_workspace", "scape_route", "scape_route_backward")
 
 
 class ScapeError(RuntimeError):
@@ -61,6 +62,28 @@ class StepBuffers(ctypes.Structure):
                 ("mask_prev", ctypes.c_void_p), ("mask_next", ctypes.c_void_p),
                 ("vals", ctypes.c_void_p), ("vals_stride", ctypes.c_uint64),
                 ("bbar", ctypes.c_void_p), ("idx", ctypes.c_void_p), ("first_step", ctypes.c_int)]
+
+
+class DistillArgs(ctypes.Structure):
+    """scape_distill_args: arguments of scape_distill_loss."""
+    _fields_ = [("logits", ctypes.c_void_p), ("dtype", ctypes.c_int), ("k", ctypes.c_int),
+                ("rows", ctypes.c_uint64), ("vocab", ctypes.c_uint64),
+                ("row_stride", ctypes.c_uint64), ("idx", ctypes.c_void_p),
+                ("vals", ctypes.c_void_p), ("vals_dtype", ctypes.c_int),
+                ("temperature", ctypes.c_float), ("kd_weight", ctypes.c_float),
+                ("ce_weight", ctypes.c_float), ("teacher_lse", ctypes.c_void_p),
+                ("labels", ctypes.c_void_p), ("row_weight", ctypes.c_void_p),
+                ("loss", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("grad_stride", ctypes.c_uint64), ("bad_count", ctypes.c_void_p)]
+
+
+class RouteArgs(ctypes.Structure):
+    """scape_route_args: what scape_route and scape_route_backward share."""
+    _fields_ = [("logits", ctypes.c_void_p), ("dtype", ctypes.c_int), ("k", ctypes.c_int),
+                ("tokens", ctypes.c_uint64), ("experts", ctypes.c_int),
+                ("renormalize", ctypes.c_int), ("row_stride", ctypes.c_uint64),
+                ("cu_tokens", ctypes.c_void_p), ("n_groups", ctypes.c_uint64),
+                ("valid", ctypes.c_void_p)]
 
 
 _lib = None
@@ -106,6 +129,12 @@ def load_library(path: str = LIB_PATH):
     f32 = ctypes.c_float
     lib.scape_dense_adams_step.argtypes = [vp, vp, vp, ctypes.POINTER(vp), i32, u64, f32, f32, f32,
                                            f32, f32, vp]
+    lib.scape_topk_logits.argtypes = [vp, i32, u64, u64, u64, i32, f32, vp, vp, vp, vp]
+    lib.scape_distill_loss.argtypes = [ctypes.POINTER(DistillArgs), vp]
+    rp = ctypes.POINTER(RouteArgs)
+    lib.scape_route_workspace.argtypes = [rp, ctypes.POINTER(u64)]
+    lib.scape_route.argtypes = [rp, vp, vp, vp, vp, vp, vp, u64, vp]
+    lib.scape_route_backward.argtypes = [rp, vp, vp, vp, vp, vp, vp, u64, vp]
     _libs[path] = lib
     if path == LIB_PATH:
         _lib = lib
