@@ -45,6 +45,7 @@ struct DistillArgs {
   int k, vals_dtype;
   float tau, c;  // temperature, log2(e) / temperature
   float kd, ce;
+  int cluster, part_vecs;  // CTAs of a row, vectors of each one's part
 };
 
 __device__ __forceinline__ float load_val(const void* p, int dtype, int64_t i) {
@@ -224,6 +225,384 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
   }
 }
 
+// ---- Rows held on chip -------------------------------------------------------
+
+constexpr int kVecs = 8;                     // vectors of a row that a thread holds
+constexpr int kPart = kThreads * kVecs;      // vectors of a row that a CTA holds
+constexpr int kMaxCluster = 8;
+constexpr int kWarps = kThreads / 32;
+
+// What a row's statistics are made of.  A sum of exponentials is held relative
+// to a maximum: sum 2^((x - m) c), and sum1 the same at temperature 1.
+struct Part {
+  float m, s, s1;        // coordinates held in registers (with a bucket: those not listed)
+  float tm, ts, ts1;     // listed coordinates (bucket only)
+  float a;               // sum q_i (log q_i - s_i) over the listed coordinates of this part
+};
+
+__device__ __forceinline__ void join(float& m, float& s, float& s1, float m2, float s2, float s12,
+                                     float c) {
+  const float M = fmaxf(m, m2), sh = shift_of(M);
+  const float f = ex2((m - sh) * c), f2 = ex2((m2 - sh) * c);
+  const float g = ex2((m - sh) * kLog2e), g2 = ex2((m2 - sh) * kLog2e);
+  s = s * f + s2 * f2;
+  s1 = s1 * g + s12 * g2;
+  m = M;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Writes to the same place of another CTA's shared memory in the cluster.
+__device__ __forceinline__ void put_remote(const float* local, uint32_t rank, float v) {
+  uint32_t at = (uint32_t)__cvta_generic_to_shared(local), there;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(v) : "memory");
+}
+
+// A cluster of CTAs takes a row, each a part of at most kPart vectors, and
+// reads it once.  TWO: the exponentials at both temperatures are needed (hard
+// labels at temperature != 1).  BUCKET: the coordinates not listed form a
+// bucket; the listed ones are then taken out of the registers first and added
+// to the sums from the list, so that p_rest is a sum and not a difference.
+template <int DT, bool TWO, bool BUCKET>
+__global__ __launch_bounds__(kThreads, 2) void distill_parts(const DistillArgs a) {
+  using E = Elem<DT>;
+  using T = typename E::T;
+  constexpr int EPV = E::kPerVec;
+  __shared__ int32_t sidx[kMaxK];  // local coordinate in this part, -1: not here
+  __shared__ float sq[kMaxK], sx[kMaxK];
+  __shared__ uint32_t listed[BUCKET ? kPart * 8 / 32 : 1];  // a byte for each vector
+  __shared__ Part warps[kWarps];
+  __shared__ Part parts[kMaxCluster];
+  __shared__ float steacher[2];  // sum of q; whether there is any
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const uint32_t rank = a.cluster > 1 ? cluster_rank() : 0;
+  const int64_t row = blockIdx.x / (unsigned)a.cluster;
+  const RowView<DT> view(a.x, row * a.stride, a.V);
+  const int64_t nv = view.vectors();
+  const int64_t v0 = (int64_t)rank * a.part_vecs;
+  const int here = (int)max((int64_t)0, min((int64_t)a.part_vecs, nv - v0));  // vectors of this part
+  const int64_t e0 = view.first_of(v0);  // coordinate of the part's first element (may be < 0)
+  T* g = a.grad ? static_cast<T*>(a.grad) + row * a.gstride : nullptr;
+  const float w = a.weight ? a.weight[row] : 1.0f;
+  const bool same = g && ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(view.p)) & 15u) == 0;
+
+  auto store = [&](int i, const float (&f)[EPV]) {  // local vector i
+    const int64_t e = e0 + (int64_t)i * EPV;
+    if (same && e >= 0 && e + EPV <= a.V) {
+      *reinterpret_cast<uint4*>(g + e) = E::pack(f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < EPV; j++)
+        if (e + j >= 0 && e + j < a.V) g[e + j] = E::make(f[j]);
+    }
+  };
+  if (w == 0.0f) {  // the whole cluster agrees
+    const float zero[EPV] = {};
+    if (g)
+      for (int i = tid; i < here; i += kThreads) store(i, zero);
+    if (a.loss && tid == 0 && rank == 0) a.loss[row] = 0.0f;
+    return;
+  }
+  if (a.cluster > 1) cluster_arrive();  // "this CTA runs": its shared memory may be written
+
+  uint4 r[kVecs];
+#pragma unroll
+  for (int u = 0; u < kVecs; u++) {
+    const int i = u * kThreads + tid;
+    r[u] = i < here ? view.load(v0 + i) : make_uint4(E::kNegInf2, E::kNegInf2, E::kNegInf2, E::kNegInf2);
+  }
+  int64_t y = a.labels ? a.labels[row] : -1;
+  if (y >= a.V) {
+    if (a.bad && tid == 0 && rank == 0) atomicAdd(a.bad, 1u);
+    y = -1;
+  }
+  if (BUCKET) {
+    for (int i = tid; i < kPart * 8 / 32; i += kThreads) listed[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < a.k; i += kThreads) {
+      const int32_t e = a.idx[row * a.k + i];
+      const int64_t l = e - e0;
+      if (e >= 0 && e < a.V && l >= 0 && l < (int64_t)here * EPV) {
+        const int bit = (int)(l / EPV) * 8 + (int)(l % EPV);
+        atomicOr(&listed[bit >> 5], 1u << (bit & 31));
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kVecs; u++) {
+      const uint32_t bits = reinterpret_cast<const uint8_t*>(listed)[u * kThreads + tid];
+      if (bits) {
+        float x[EPV];
+        E::unpack(r[u], x);
+#pragma unroll
+        for (int j = 0; j < EPV; j++)
+          if (bits >> j & 1) x[j] = neg_inf();
+        r[u] = E::pack(x);
+      }
+    }
+  }
+
+  // the teacher: one warp, all entries; x at those of this part
+  Part mine{neg_inf(), 0.0f, 0.0f, neg_inf(), 0.0f, 0.0f, 0.0f};
+  if (wid == 0) {
+    float tm = neg_inf();
+    for (int i = lane; i < a.k; i += 32) {
+      const int32_t e = a.idx[row * a.k + i];
+      const int64_t l = e - e0;
+      float t = neg_inf();
+      bool in = false;
+      if (e >= a.V) {
+        if (a.bad && rank == 0) atomicAdd(a.bad, 1u);
+      } else if (e >= 0) {
+        t = load_val(a.vals, a.vals_dtype, row * a.k + i) / a.tau;
+        in = l >= 0 && l < (int64_t)here * EPV;
+        if (in) sx[i] = E::load(view.p + e);
+      }
+      sidx[i] = in ? (int32_t)l : -1;
+      sq[i] = t;
+      if (!(t <= tm)) tm = t;  // NaN stays
+    }
+    const bool has = __any_sync(kFull, tm != neg_inf());
+    float lt = 0.0f;
+    if (has) {
+      if (a.tlse) {
+        lt = a.tlse[row];
+      } else {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) tm = fmaxf(tm, __shfl_xor_sync(kFull, tm, o));
+        tm = shift_of(tm);
+        float z = 0.0f;
+        for (int i = lane; i < a.k; i += 32) z += expf(sq[i] - tm);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
+        lt = tm + logf(z);
+      }
+    }
+    float Q = 0.0f;
+    for (int i = lane; i < a.k; i += 32) {
+      const float logq = sq[i] - lt, q = has ? expf(logq) : 0.0f;
+      sq[i] = q;
+      Q += q;
+      if (sidx[i] < 0) continue;
+      const float x = sx[i];
+      if (q != 0.0f) mine.a += q * (logq - x / a.tau);
+      if (BUCKET) join(mine.tm, mine.ts, mine.ts1, x, 1.0f, 1.0f, a.c);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      Q += __shfl_xor_sync(kFull, Q, o);
+      mine.a += __shfl_xor_sync(kFull, mine.a, o);
+      if (BUCKET) {
+        const float m2 = __shfl_xor_sync(kFull, mine.tm, o), s2 = __shfl_xor_sync(kFull, mine.ts, o),
+                    s12 = __shfl_xor_sync(kFull, mine.ts1, o);
+        join(mine.tm, mine.ts, mine.ts1, m2, s2, s12, a.c);
+      }
+    }
+    if (lane == 0) {
+      steacher[0] = Q;
+      steacher[1] = has ? 1.0f : 0.0f;
+    }
+  }
+  const float xy = y >= 0 && tid == 0 ? E::load(view.p + y) : 0.0f;
+
+  // the part's statistics: a thread's, its warp's, the CTA's, the cluster's
+  {
+    float m = neg_inf();
+#pragma unroll
+    for (int u = 0; u < kVecs; u++) {
+      float x[EPV];
+      E::unpack(r[u], x);
+#pragma unroll
+      for (int j = 0; j < EPV; j++) m = fmaxf(m, x[j]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    const float sh = shift_of(m), mc = sh * a.c, mc1 = sh * kLog2e;
+    float s = 0.0f, s1 = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kVecs; u++) {
+      float x[EPV];
+      E::unpack(r[u], x);
+#pragma unroll
+      for (int j = 0; j < EPV; j++) {
+        s += ex2(fmaf(x[j], a.c, -mc));
+        if (TWO) s1 += ex2(fmaf(x[j], kLog2e, -mc1));
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      s += __shfl_xor_sync(kFull, s, o);
+      if (TWO) s1 += __shfl_xor_sync(kFull, s1, o);
+    }
+    mine.m = m;
+    mine.s = s;
+    mine.s1 = TWO ? s1 : s;
+  }
+  if (lane == 0) warps[wid] = mine;
+  __syncthreads();
+  if (wid == 0) {
+    Part q = warps[lane < kWarps ? lane : 0];
+    if (lane >= kWarps) q = Part{neg_inf(), 0.0f, 0.0f, neg_inf(), 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const float m2 = __shfl_xor_sync(kFull, q.m, o), s2 = __shfl_xor_sync(kFull, q.s, o),
+                  s12 = __shfl_xor_sync(kFull, q.s1, o);
+      join(q.m, q.s, q.s1, m2, s2, s12, a.c);
+    }
+    if (lane == 0) {
+      q.tm = warps[0].tm;
+      q.ts = warps[0].ts;
+      q.ts1 = warps[0].ts1;
+      q.a = warps[0].a;
+      warps[0] = q;
+      if (a.cluster == 1) parts[0] = q;
+    }
+    if (a.cluster > 1) {
+      __syncwarp();
+      cluster_wait();
+      const float* from = reinterpret_cast<const float*>(&warps[0]);
+      const float* to = reinterpret_cast<const float*>(&parts[rank]);
+      for (int i = lane; i < a.cluster * 7; i += 32) put_remote(to + i % 7, (uint32_t)(i / 7), from[i % 7]);
+    }
+  } else if (a.cluster > 1) {
+    cluster_wait();
+  }
+  if (a.cluster > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  Part t = parts[0];
+  for (int i = 1; i < a.cluster; i++) {
+    const Part q = parts[i];
+    join(t.m, t.s, t.s1, q.m, q.s, q.s1, a.c);
+    if (BUCKET) join(t.tm, t.ts, t.ts1, q.tm, q.ts, q.ts1, a.c);
+    t.a += q.a;
+  }
+  // the whole row: all = rest and listed
+  const float Q = steacher[0];
+  const bool has = steacher[1] != 0.0f;
+  float M = t.m, S = t.s, S1 = t.s1;
+  if (BUCKET) join(M, S, S1, t.tm, t.ts, t.ts1, a.c);
+  const float sh = shift_of(M), shr = shift_of(t.m);
+  const bool bucket = BUCKET && has && t.s > 0.0f;
+  const float qr = bucket ? fmaxf(0.0f, 1.0f - Q) : 0.0f;
+  if (a.loss && tid == 0 && rank == 0) {
+    const float L = sh / a.tau + logf(S);
+    float l = 0.0f;
+    if (has) {
+      float kl = t.a + Q * L;
+      if (qr > 0.0f) {  // log q_rest - log p_rest, both from what is listed
+        const float odds = t.ts / t.s * ex2((shift_of(t.tm) - shr) * a.c);
+        const float logp = odds < 1.0f ? log1pf(odds) : L - (shr / a.tau + logf(t.s));
+        kl += qr * (log1pf(-Q) + logp);
+      }
+      l = a.kd * a.tau * a.tau * kl;
+    }
+    if (y >= 0) l += a.ce * (sh + logf(S1) - xy);
+    a.loss[row] = w * l;
+  }
+  if (!g) return;
+
+  // gradient = K1 2^((x - m) c) + K2 2^((x - m) log2 e), m the maximum of what
+  // the registers hold; the listed coordinates and the label after that
+  const float A = has ? w * a.kd * a.tau : 0.0f, C1 = y >= 0 ? w * a.ce : 0.0f;
+  float K1 = A * Q / S, K2 = C1 / S1;
+  if (BUCKET) {
+    const float pr = t.s * ex2((shr - sh) * a.c) / S, pr1 = t.s1 * ex2((shr - sh) * kLog2e) / S1;
+    const float ptop = t.ts * ex2((shift_of(t.tm) - sh) * a.c) / S;
+    const float d = qr > 0.0f ? Q - ptop : Q * pr;  // (Q + q_rest) p_rest - q_rest, as Q + q_rest = 1
+    K1 = t.s > 0.0f ? A * d / t.s : 0.0f;
+    K2 = t.s1 > 0.0f ? C1 * pr1 / t.s1 : 0.0f;
+  }
+  if (!TWO) K1 += K2;
+  const float mc = shr * a.c, mc1 = shr * kLog2e;
+  auto grad_of = [&](float x) {
+    float v = K1 * ex2(fmaf(x, a.c, -mc));
+    if (TWO) v = fmaf(K2, ex2(fmaf(x, kLog2e, -mc1)), v);
+    return v;
+  };
+#pragma unroll
+  for (int u = 0; u < kVecs; u++) {
+    const int i = u * kThreads + tid;
+    if (i < here) {
+      float x[EPV];
+      E::unpack(r[u], x);
+#pragma unroll
+      for (int j = 0; j < EPV; j++) x[j] = grad_of(x[j]);
+      store(i, x);
+    }
+  }
+  const int64_t ly = y - e0;
+  const bool y_here = y >= 0 && ly >= 0 && ly < (int64_t)here * EPV;
+  bool y_listed = false;
+  float x_y = 0.0f;
+  if (y_here && tid == 0) x_y = xy;
+  __syncthreads();
+  for (int i = tid; i < a.k; i += kThreads) {
+    if (sidx[i] < 0) continue;
+    const float d = sx[i] - sh;
+    float v = A * ((Q + qr) * ex2(d * a.c) / S - sq[i]);
+    if (y >= 0) v += C1 * ex2(d * kLog2e) / S1;
+    if (y_here && sidx[i] == ly) {
+      v -= C1;
+      y_listed = true;
+    }
+    g[e0 + sidx[i]] = E::make(v);
+  }
+  if (y_here) {  // the same for the whole CTA
+    y_listed = __syncthreads_or(y_listed);
+    if (!y_listed && tid == 0) g[y] = E::make(grad_of(x_y) - C1);
+  }
+}
+
+template <int DT, bool TWO, bool BUCKET>
+cudaError_t launch_parts(const DistillArgs& a, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(a.rows * a.cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)a.cluster;
+  at.val.clusterDim.y = 1;
+  at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, distill_parts<DT, TWO, BUCKET>, a);
+}
+
+template <int DT>
+cudaError_t launch_distill(DistillArgs& a, cudaStream_t s) {
+  // vectors of a row, one more where it starts inside one
+  const int64_t nv = a.V / Elem<DT>::kPerVec + 2;
+  if (nv > (int64_t)kPart * kMaxCluster) {
+    const int64_t cap = (int64_t)num_sms() * 4;
+    distill_rows<DT><<<(unsigned)(a.rows < cap ? a.rows : cap), kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  a.cluster = 1;
+  while (nv > (int64_t)kPart * a.cluster) a.cluster *= 2;
+  a.part_vecs = (int)((nv + a.cluster - 1) / a.cluster);
+  const bool two = a.labels && a.tau != 1.0f, bucket = a.tlse != nullptr;
+  cudaError_t e;
+  if (two) e = bucket ? launch_parts<DT, true, true>(a, s) : launch_parts<DT, true, false>(a, s);
+  else e = bucket ? launch_parts<DT, false, true>(a, s) : launch_parts<DT, false, false>(a, s);
+  const cudaError_t last = cudaGetLastError();
+  return e != cudaSuccess ? e : last;
+}
+
 int fail(int code, const char* fmt, ...) {
   char buf[256];
   va_list ap;
@@ -286,16 +665,13 @@ SCAPE_API int scape_distill_loss(const scape_distill_args* args, void* stream) {
   a.gstride = (int64_t)q.grad_stride;
   a.k = q.k;
   a.vals_dtype = q.vals_dtype;
-  a.tau = q.temperature;
-  a.c = kLog2e / q.temperature;
+  a.tau = q.k > 0 ? q.temperature : 1.0f;  // without a teacher only the cross entropy is left
+  a.c = kLog2e / a.tau;
   a.kd = q.kd_weight;
   a.ce = q.ce_weight;
-  const uint64_t cap = (uint64_t)num_sms() * 4;
-  const unsigned grid = (unsigned)(q.rows < cap ? q.rows : cap);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (q.dtype == SCAPE_BF16) distill_rows<SCAPE_BF16><<<grid, kThreads, 0, s>>>(a);
-  else if (q.dtype == SCAPE_F16) distill_rows<SCAPE_F16><<<grid, kThreads, 0, s>>>(a);
-  else distill_rows<SCAPE_F32><<<grid, kThreads, 0, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? SCAPE_OK : fail(SCAPE_ECUDA, "distill_rows: %s", cudaGetErrorString(e));
+  const cudaError_t e = q.dtype == SCAPE_BF16  ? launch_distill<SCAPE_BF16>(a, s)
+                        : q.dtype == SCAPE_F16 ? launch_distill<SCAPE_F16>(a, s)
+                                               : launch_distill<SCAPE_F32>(a, s);
+  return e == cudaSuccess ? SCAPE_OK : fail(SCAPE_ECUDA, "distill: %s", cudaGetErrorString(e));
 }
