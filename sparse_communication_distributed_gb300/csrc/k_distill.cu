@@ -15,6 +15,7 @@
 //
 // A CTA takes a row: one pass for the running maxima and sums, one for the
 // gradient.
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -227,18 +228,37 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
 
 // ---- Rows held on chip -------------------------------------------------------
 
-constexpr int kVecs = 8;                     // vectors of a row that a thread holds
-constexpr int kPart = kThreads * kVecs;      // vectors of a row that a CTA holds
-constexpr int kMaxCluster = 8;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 16;
+
+// Threads of a CTA and vectors of a row that each of them holds, for long and
+// for short parts of a row.
+template <int NT_, int VECS_, int MINB_>
+struct Shape {
+  static constexpr int NT = NT_, VECS = VECS_, MINB = MINB_, PART = NT_ * VECS_;
+};
+using Wide = Shape<256, 16, 2>;
+using Narrow = Shape<128, 8, 8>;
 
 // What a row's statistics are made of.  A sum of exponentials is held relative
-// to a maximum: sum 2^((x - m) c), and sum1 the same at temperature 1.
+// to a maximum: s = sum 2^((x - m) c), and s1 the same at temperature 1.
 struct Part {
-  float m, s, s1;        // coordinates held in registers (with a bucket: those not listed)
-  float tm, ts, ts1;     // listed coordinates (bucket only)
-  float a;               // sum q_i (log q_i - s_i) over the listed coordinates of this part
+  float m, s, s1;     // coordinates held in registers (with a bucket: those not listed)
+  float tm, ts, ts1;  // listed coordinates (bucket only)
+  float b;            // over the listed coordinates of this part: sum u_i (t_i - base - s_i), u_i = exp(t_i - base)
+  float base, z;      // over all listed coordinates: base = max t_i (u_i then is relative to
+                      // teacher_lse with a bucket), z = sum u_i
+  float zp;           // sum u_i over those of this part
 };
+constexpr int kShared = 7;  // the leading members differ from part to part
+
+__device__ __forceinline__ float shfl_max(float x, int n) {
+  for (int o = n >> 1; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+  return x;
+}
+__device__ __forceinline__ float shfl_sum(float x, int n) {
+  for (int o = n >> 1; o; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+  return x;
+}
 
 __device__ __forceinline__ void join(float& m, float& s, float& s1, float m2, float s2, float s12,
                                      float c) {
@@ -268,310 +288,386 @@ __device__ __forceinline__ void put_remote(const float* local, uint32_t rank, fl
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(v) : "memory");
 }
 
-// A cluster of CTAs takes a row, each a part of at most kPart vectors, and
-// reads it once.  TWO: the exponentials at both temperatures are needed (hard
-// labels at temperature != 1).  BUCKET: the coordinates not listed form a
-// bucket; the listed ones are then taken out of the registers first and added
-// to the sums from the list, so that p_rest is a sum and not a difference.
-template <int DT, bool TWO, bool BUCKET>
-__global__ __launch_bounds__(kThreads, 2) void distill_parts(const DistillArgs a) {
+// A cluster of CTAs (often just one) takes a row, each CTA a part of at most
+// PART vectors, and reads it once; then the cluster takes another row.  A
+// thread keeps its vectors of the row in registers, and copies those of the
+// next row to its own places in shared memory meanwhile, so that loads run all
+// the time.  Each thread looks after up to two of the teacher's entries.  TWO:
+// exponentials at both temperatures are needed (hard labels at temperature !=
+// 1).  BUCKET: the coordinates not listed form a bucket; the listed ones are
+// then taken out of the registers first and added to the sums by the threads
+// that look after them, so that p_rest is a sum and not a difference.
+//
+// Buffers of shared memory are used in turn for one row and the next: between
+// two uses of one there are the other row's barriers.
+template <int DT, bool TWO, bool BUCKET, class SH>
+__global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillArgs a) {
   using E = Elem<DT>;
   using T = typename E::T;
-  constexpr int EPV = E::kPerVec;
-  __shared__ int32_t sidx[kMaxK];  // local coordinate in this part, -1: not here
-  __shared__ float sq[kMaxK], sx[kMaxK];
-  __shared__ uint32_t listed[BUCKET ? kPart * 8 / 32 : 1];  // a byte for each vector
-  __shared__ Part warps[kWarps];
-  __shared__ Part parts[kMaxCluster];
-  __shared__ float steacher[2];  // sum of q; whether there is any
+  constexpr int EPV = E::kPerVec, NT = SH::NT, VECS = SH::VECS, kWarps = NT / 32;
+  extern __shared__ __align__(16) uint4 next[];  // PART
+  __shared__ uint32_t listed[2][BUCKET ? SH::PART * 8 / 32 : 1];  // a byte for each vector
+  __shared__ Part warps[2][kWarps];
+  __shared__ Part parts[2][kMaxCluster];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const uint32_t rank = a.cluster > 1 ? cluster_rank() : 0;
-  const int64_t row = blockIdx.x / (unsigned)a.cluster;
-  const RowView<DT> view(a.x, row * a.stride, a.V);
-  const int64_t nv = view.vectors();
+  const int64_t step = gridDim.x / (unsigned)a.cluster;
   const int64_t v0 = (int64_t)rank * a.part_vecs;
-  const int here = (int)max((int64_t)0, min((int64_t)a.part_vecs, nv - v0));  // vectors of this part
-  const int64_t e0 = view.first_of(v0);  // coordinate of the part's first element (may be < 0)
-  T* g = a.grad ? static_cast<T*>(a.grad) + row * a.gstride : nullptr;
-  const float w = a.weight ? a.weight[row] : 1.0f;
-  const bool same = g && ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(view.p)) & 15u) == 0;
-
-  auto store = [&](int i, const float (&f)[EPV]) {  // local vector i
-    const int64_t e = e0 + (int64_t)i * EPV;
-    if (same && e >= 0 && e + EPV <= a.V) {
-      *reinterpret_cast<uint4*>(g + e) = E::pack(f);
-    } else {
-#pragma unroll
-      for (int j = 0; j < EPV; j++)
-        if (e + j >= 0 && e + j < a.V) g[e + j] = E::make(f[j]);
-    }
+  auto weight_of = [&](int64_t row) { return a.weight ? a.weight[row] : 1.0f; };
+  // The part of a row: "here" vectors, whole ones [lo, hi); the first element's
+  // coordinate (< 0 where the row starts inside its first vector).
+  struct Where {
+    int64_t e0;
+    int here, lo, hi;
   };
-  if (w == 0.0f) {  // the whole cluster agrees
-    const float zero[EPV] = {};
-    if (g)
-      for (int i = tid; i < here; i += kThreads) store(i, zero);
-    if (a.loss && tid == 0 && rank == 0) a.loss[row] = 0.0f;
-    return;
-  }
-  if (a.cluster > 1) cluster_arrive();  // "this CTA runs": its shared memory may be written
-
-  uint4 r[kVecs];
+  auto where = [&](const RowView<DT>& view) {
+    const int64_t nv = view.vectors();
+    Where w;
+    w.e0 = view.first_of(v0);
+    w.here = (int)max((int64_t)0, min((int64_t)a.part_vecs, nv - v0));
+    w.lo = w.e0 < 0 ? 1 : 0;
+    w.hi = (int)max((int64_t)0, min((int64_t)w.here, (a.V - w.e0) / EPV));
+    return w;
+  };
+  // starts the copies of this thread's vectors of a row; a ragged vector is put
+  // together from single loads
+  auto fetch = [&](int64_t row) {
+    const RowView<DT> view(a.x, row * a.stride, a.V);
+    const Where w = where(view);
+    const T* from = view.p + w.e0 + tid * EPV;
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(next + tid);
 #pragma unroll
-  for (int u = 0; u < kVecs; u++) {
-    const int i = u * kThreads + tid;
-    r[u] = i < here ? view.load(v0 + i) : make_uint4(E::kNegInf2, E::kNegInf2, E::kNegInf2, E::kNegInf2);
-  }
-  int64_t y = a.labels ? a.labels[row] : -1;
-  if (y >= a.V) {
-    if (a.bad && tid == 0 && rank == 0) atomicAdd(a.bad, 1u);
-    y = -1;
-  }
+    for (int u = 0; u < VECS; u++)
+      if (u * NT + tid < w.hi && (u > 0 || tid >= w.lo)) copy_async(to + u * NT * 16, from + u * NT * EPV);
+    if (w.lo == 1 && tid == 0 && w.here > 0) next[0] = view.load(v0);
+    if (w.here > w.hi && w.here > w.lo && (w.here - 1) % NT == tid)
+      next[w.here - 1] = view.load(v0 + w.here - 1);
+  };
+  if (a.cluster > 1) cluster_arrive();  // "this CTA runs": its shared memory may be written
+  bool met = a.cluster == 1;
   if (BUCKET) {
-    for (int i = tid; i < kPart * 8 / 32; i += kThreads) listed[i] = 0;
+    for (int i = tid; i < 2 * SH::PART * 8 / 32; i += NT) listed[0][i] = 0;
     __syncthreads();
-    for (int i = tid; i < a.k; i += kThreads) {
-      const int32_t e = a.idx[row * a.k + i];
-      const int64_t l = e - e0;
-      if (e >= 0 && e < a.V && l >= 0 && l < (int64_t)here * EPV) {
-        const int bit = (int)(l / EPV) * 8 + (int)(l % EPV);
-        atomicOr(&listed[bit >> 5], 1u << (bit & 31));
+  }
+  int turn = 0;
+  int64_t row = blockIdx.x / (unsigned)a.cluster;
+  float w = row < a.rows ? weight_of(row) : 0.0f;
+  if (w != 0.0f) fetch(row);
+  for (; row < a.rows; row += step) {
+    const RowView<DT> view(a.x, row * a.stride, a.V);
+    const Where at = where(view);
+    const int here = at.here;
+    const int64_t e0 = at.e0;
+    T* g = a.grad ? static_cast<T*>(a.grad) + row * a.gstride : nullptr;
+    // writes vector u of this thread
+    const bool same =
+        g && ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(view.p)) & 15u) == 0;
+    T* gt = g + e0 + tid * EPV;
+    auto store = [&](int u, const uint4 v) {
+      const int i = u * NT + tid;
+      if (same && i < at.hi && (u > 0 || tid >= at.lo)) {
+        *reinterpret_cast<uint4*>(gt + u * NT * EPV) = v;
+      } else if (i < here) {
+        const T* t = reinterpret_cast<const T*>(&v);
+        const int64_t e = e0 + (int64_t)i * EPV;
+#pragma unroll
+        for (int j = 0; j < EPV; j++)
+          if (e + j >= 0 && e + j < a.V) g[e + j] = t[j];
+      }
+    };
+    const int64_t row2 = row + step;
+    const float w_now = w;
+    w = row2 < a.rows ? weight_of(row2) : 0.0f;
+    if (w_now == 0.0f) {  // the whole cluster agrees
+      if (w != 0.0f) fetch(row2);
+      if (g) {
+#pragma unroll
+        for (int u = 0; u < VECS; u++) store(u, make_uint4(0, 0, 0, 0));
+      }
+      if (a.loss && tid == 0 && rank == 0) a.loss[row] = 0.0f;
+      continue;
+    }
+    // the teacher's entries of this thread: local coordinate (-1: not of this
+    // part), t, x
+    int el[2];
+    float et[2], ex[2];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const int i = h * NT + tid;
+      el[h] = -1;
+      et[h] = neg_inf();
+      ex[h] = 0.0f;
+      if (i < a.k) {
+        const int32_t e = a.idx[row * a.k + i];
+        const float v = load_val(a.vals, a.vals_dtype, row * a.k + i);
+        const int64_t l = e - e0;
+        if (e >= a.V) {
+          if (a.bad && rank == 0) atomicAdd(a.bad, 1u);
+        } else if (e >= 0) {
+          et[h] = v / a.tau;
+          if (l >= 0 && l < (int64_t)here * EPV) {
+            el[h] = (int)l;
+            ex[h] = E::load(view.p + e);
+            if (BUCKET) {
+              const int bit = el[h] / EPV * 8 + el[h] % EPV;
+              atomicOr(&listed[turn][bit >> 5], 1u << (bit & 31));
+            }
+          }
+        }
       }
     }
-    __syncthreads();
+    int64_t y = a.labels ? a.labels[row] : -1;
+    if (y >= a.V) {
+      if (a.bad && tid == 0 && rank == 0) atomicAdd(a.bad, 1u);
+      y = -1;
+    }
+    const float xy = y >= 0 && tid == 0 ? E::load(view.p + y) : 0.0f;
+    const float tlse = a.tlse ? a.tlse[row] : 0.0f;
+
+    copy_wait();
+    uint4 r[VECS];
 #pragma unroll
-    for (int u = 0; u < kVecs; u++) {
-      const uint32_t bits = reinterpret_cast<const uint8_t*>(listed)[u * kThreads + tid];
-      if (bits) {
+    for (int u = 0; u < VECS; u++) r[u] = u * NT + tid < here ? next[u * NT + tid] : neg_inf_vec<DT>();
+    if (BUCKET) {
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < VECS; u++) {
+        const uint32_t bits = reinterpret_cast<const uint8_t*>(listed[turn])[u * NT + tid];
+        if (bits) {
+          float x[EPV];
+          E::unpack(r[u], x);
+#pragma unroll
+          for (int j = 0; j < EPV; j++)
+            if (bits >> j & 1) x[j] = neg_inf();
+          r[u] = E::pack(x);
+        }
+      }
+    }
+    uint4 mx = r[0];
+#pragma unroll
+    for (int u = 1; u < VECS; u++) mx = max_vec<DT>(mx, r[u]);
+    Part q;
+    {
+      float x[EPV];
+      E::unpack(mx, x);
+      q.m = x[0];
+#pragma unroll
+      for (int j = 1; j < EPV; j++) q.m = fmaxf(q.m, x[j]);
+    }
+    if (w != 0.0f) fetch(row2);  // the registers hold this row
+
+    // a thread's statistics, relative to its warp's maximum
+    q.m = shfl_max(q.m, 32);
+    {
+      const float sh = shift_of(q.m);
+      const uint64_t c2 = pair(a.c, a.c), mc = pair(-sh * a.c, -sh * a.c);
+      const uint64_t l2 = pair(kLog2e, kLog2e), ml = pair(-sh * kLog2e, -sh * kLog2e);
+      uint64_t s = 0, s1 = 0;
+#pragma unroll
+      for (int u = 0; u < VECS; u++) {
+        if (u * NT >= here) break;
         float x[EPV];
         E::unpack(r[u], x);
 #pragma unroll
-        for (int j = 0; j < EPV; j++)
-          if (bits >> j & 1) x[j] = neg_inf();
-        r[u] = E::pack(x);
+        for (int j = 0; j < EPV; j += 2) {
+          const uint64_t xx = pair(x[j], x[j + 1]);
+          s = add2(s, ex2_2(fma2(xx, c2, mc)));
+          if (TWO) s1 = add2(s1, ex2_2(fma2(xx, l2, ml)));
+        }
       }
+      const float2 f = unpair(s), f1 = unpair(s1);
+      q.s = shfl_sum(f.x + f.y, 32);
+      q.s1 = TWO ? shfl_sum(f1.x + f1.y, 32) : q.s;
     }
-  }
-
-  // the teacher: one warp, all entries; x at those of this part
-  Part mine{neg_inf(), 0.0f, 0.0f, neg_inf(), 0.0f, 0.0f, 0.0f};
-  if (wid == 0) {
-    float tm = neg_inf();
-    for (int i = lane; i < a.k; i += 32) {
-      const int32_t e = a.idx[row * a.k + i];
-      const int64_t l = e - e0;
-      float t = neg_inf();
-      bool in = false;
-      if (e >= a.V) {
-        if (a.bad && rank == 0) atomicAdd(a.bad, 1u);
-      } else if (e >= 0) {
-        t = load_val(a.vals, a.vals_dtype, row * a.k + i) / a.tau;
-        in = l >= 0 && l < (int64_t)here * EPV;
-        if (in) sx[i] = E::load(view.p + e);
+    q.tm = q.base = neg_inf();
+    q.ts = q.ts1 = q.z = q.zp = q.b = 0.0f;
+    if (wid * 32 < a.k) {  // the teacher's entries of this warp
+      q.base = shfl_max(fmaxf(et[0], et[1]), 32);
+      const float base = BUCKET ? tlse : shift_of(q.base);
+      if (BUCKET) q.tm = shfl_max(fmaxf(el[0] >= 0 ? ex[0] : neg_inf(), el[1] >= 0 ? ex[1] : neg_inf()), 32);
+      const float tsh = shift_of(q.tm);
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const float u = expf(et[h] - base);
+        q.z += u;
+        if (el[h] >= 0) {
+          q.zp += u;
+          if (u != 0.0f) q.b += u * ((et[h] - base) - ex[h] / a.tau);
+          if (BUCKET) {
+            q.ts += ex2((ex[h] - tsh) * a.c);
+            if (TWO) q.ts1 += ex2((ex[h] - tsh) * kLog2e);
+          }
+        }
       }
-      sidx[i] = in ? (int32_t)l : -1;
-      sq[i] = t;
-      if (!(t <= tm)) tm = t;  // NaN stays
-    }
-    const bool has = __any_sync(kFull, tm != neg_inf());
-    float lt = 0.0f;
-    if (has) {
-      if (a.tlse) {
-        lt = a.tlse[row];
-      } else {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) tm = fmaxf(tm, __shfl_xor_sync(kFull, tm, o));
-        tm = shift_of(tm);
-        float z = 0.0f;
-        for (int i = lane; i < a.k; i += 32) z += expf(sq[i] - tm);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
-        lt = tm + logf(z);
-      }
-    }
-    float Q = 0.0f;
-    for (int i = lane; i < a.k; i += 32) {
-      const float logq = sq[i] - lt, q = has ? expf(logq) : 0.0f;
-      sq[i] = q;
-      Q += q;
-      if (sidx[i] < 0) continue;
-      const float x = sx[i];
-      if (q != 0.0f) mine.a += q * (logq - x / a.tau);
-      if (BUCKET) join(mine.tm, mine.ts, mine.ts1, x, 1.0f, 1.0f, a.c);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      Q += __shfl_xor_sync(kFull, Q, o);
-      mine.a += __shfl_xor_sync(kFull, mine.a, o);
+      q.z = shfl_sum(q.z, 32);
+      q.b = shfl_sum(q.b, 32);
+      if (!BUCKET) q.zp = shfl_sum(q.zp, 32);
       if (BUCKET) {
-        const float m2 = __shfl_xor_sync(kFull, mine.tm, o), s2 = __shfl_xor_sync(kFull, mine.ts, o),
-                    s12 = __shfl_xor_sync(kFull, mine.ts1, o);
-        join(mine.tm, mine.ts, mine.ts1, m2, s2, s12, a.c);
+        q.ts = shfl_sum(q.ts, 32);
+        q.ts1 = TWO ? shfl_sum(q.ts1, 32) : q.ts;
       }
     }
-    if (lane == 0) {
-      steacher[0] = Q;
-      steacher[1] = has ? 1.0f : 0.0f;
-    }
-  }
-  const float xy = y >= 0 && tid == 0 ? E::load(view.p + y) : 0.0f;
-
-  // the part's statistics: a thread's, its warp's, the CTA's, the cluster's
-  {
-    float m = neg_inf();
-#pragma unroll
-    for (int u = 0; u < kVecs; u++) {
-      float x[EPV];
-      E::unpack(r[u], x);
-#pragma unroll
-      for (int j = 0; j < EPV; j++) m = fmaxf(m, x[j]);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    const float sh = shift_of(m), mc = sh * a.c, mc1 = sh * kLog2e;
-    float s = 0.0f, s1 = 0.0f;
-#pragma unroll
-    for (int u = 0; u < kVecs; u++) {
-      float x[EPV];
-      E::unpack(r[u], x);
-#pragma unroll
-      for (int j = 0; j < EPV; j++) {
-        s += ex2(fmaf(x[j], a.c, -mc));
-        if (TWO) s1 += ex2(fmaf(x[j], kLog2e, -mc1));
-      }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      s += __shfl_xor_sync(kFull, s, o);
-      if (TWO) s1 += __shfl_xor_sync(kFull, s1, o);
-    }
-    mine.m = m;
-    mine.s = s;
-    mine.s1 = TWO ? s1 : s;
-  }
-  if (lane == 0) warps[wid] = mine;
-  __syncthreads();
-  if (wid == 0) {
-    Part q = warps[lane < kWarps ? lane : 0];
-    if (lane >= kWarps) q = Part{neg_inf(), 0.0f, 0.0f, neg_inf(), 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const float m2 = __shfl_xor_sync(kFull, q.m, o), s2 = __shfl_xor_sync(kFull, q.s, o),
-                  s12 = __shfl_xor_sync(kFull, q.s1, o);
-      join(q.m, q.s, q.s1, m2, s2, s12, a.c);
-    }
-    if (lane == 0) {
-      q.tm = warps[0].tm;
-      q.ts = warps[0].ts;
-      q.ts1 = warps[0].ts1;
-      q.a = warps[0].a;
-      warps[0] = q;
-      if (a.cluster == 1) parts[0] = q;
-    }
-    if (a.cluster > 1) {
-      __syncwarp();
-      cluster_wait();
-      const float* from = reinterpret_cast<const float*>(&warps[0]);
-      const float* to = reinterpret_cast<const float*>(&parts[rank]);
-      for (int i = lane; i < a.cluster * 7; i += 32) put_remote(to + i % 7, (uint32_t)(i / 7), from[i % 7]);
-    }
-  } else if (a.cluster > 1) {
-    cluster_wait();
-  }
-  if (a.cluster > 1) {
-    cluster_arrive();
-    cluster_wait();
-  } else {
+    if (lane == 0) warps[turn][wid] = q;
     __syncthreads();
-  }
-  Part t = parts[0];
-  for (int i = 1; i < a.cluster; i++) {
-    const Part q = parts[i];
-    join(t.m, t.s, t.s1, q.m, q.s, q.s1, a.c);
-    if (BUCKET) join(t.tm, t.ts, t.ts1, q.tm, q.ts, q.ts1, a.c);
-    t.a += q.a;
-  }
-  // the whole row: all = rest and listed
-  const float Q = steacher[0];
-  const bool has = steacher[1] != 0.0f;
-  float M = t.m, S = t.s, S1 = t.s1;
-  if (BUCKET) join(M, S, S1, t.tm, t.ts, t.ts1, a.c);
-  const float sh = shift_of(M), shr = shift_of(t.m);
-  const bool bucket = BUCKET && has && t.s > 0.0f;
-  const float qr = bucket ? fmaxf(0.0f, 1.0f - Q) : 0.0f;
-  if (a.loss && tid == 0 && rank == 0) {
-    const float L = sh / a.tau + logf(S);
-    float l = 0.0f;
-    if (has) {
-      float kl = t.a + Q * L;
-      if (qr > 0.0f) {  // log q_rest - log p_rest, both from what is listed
-        const float odds = t.ts / t.s * ex2((shift_of(t.tm) - shr) * a.c);
-        const float logp = odds < 1.0f ? log1pf(odds) : L - (shr / a.tau + logf(t.s));
-        kl += qr * (log1pf(-Q) + logp);
+    if (wid == 0) {  // the CTA's
+      if (lane < kWarps) q = warps[turn][lane];
+      const float base = shfl_max(q.base, kWarps);
+      const float m = shfl_max(q.m, kWarps), d = q.m - shift_of(m);
+      q.s = shfl_sum(q.s * ex2(d * a.c), kWarps);
+      q.s1 = TWO ? shfl_sum(q.s1 * ex2(d * kLog2e), kWarps) : q.s;
+      q.m = m;
+      if (BUCKET) {
+        const float tm = shfl_max(q.tm, kWarps), td = q.tm - shift_of(tm);
+        q.ts = shfl_sum(q.ts * ex2(td * a.c), kWarps);
+        q.ts1 = TWO ? shfl_sum(q.ts1 * ex2(td * kLog2e), kWarps) : q.ts;
+        q.tm = tm;
+        q.b = shfl_sum(q.b, kWarps);
+        q.z = shfl_sum(q.z, kWarps);
+      } else {
+        const float bd = shift_of(q.base) - shift_of(base);
+        const float f = expf(bd);
+        q.b = shfl_sum(q.z == 0.0f ? 0.0f : f * (q.b + bd * q.zp), kWarps);
+        q.z = shfl_sum(q.z == 0.0f ? 0.0f : f * q.z, kWarps);
       }
-      l = a.kd * a.tau * a.tau * kl;
+      q.base = base;
+      if (lane == 0) {
+        parts[turn][rank] = q;
+        warps[turn][0] = q;
+      }
+      if (a.cluster > 1) {
+        __syncwarp();
+        if (!met) cluster_wait();
+        const float* from = reinterpret_cast<const float*>(&warps[turn][0]);
+        const float* to = reinterpret_cast<const float*>(&parts[turn][rank]);
+        for (int i = lane; i < a.cluster * kShared; i += 32)
+          if (i / kShared != (int)rank) put_remote(to + i % kShared, (uint32_t)(i / kShared), from[i % kShared]);
+      }
+    } else if (!met) {
+      cluster_wait();
     }
-    if (y >= 0) l += a.ce * (sh + logf(S1) - xy);
-    a.loss[row] = w * l;
-  }
-  if (!g) return;
-
-  // gradient = K1 2^((x - m) c) + K2 2^((x - m) log2 e), m the maximum of what
-  // the registers hold; the listed coordinates and the label after that
-  const float A = has ? w * a.kd * a.tau : 0.0f, C1 = y >= 0 ? w * a.ce : 0.0f;
-  float K1 = A * Q / S, K2 = C1 / S1;
-  if (BUCKET) {
-    const float pr = t.s * ex2((shr - sh) * a.c) / S, pr1 = t.s1 * ex2((shr - sh) * kLog2e) / S1;
-    const float ptop = t.ts * ex2((shift_of(t.tm) - sh) * a.c) / S;
-    const float d = qr > 0.0f ? Q - ptop : Q * pr;  // (Q + q_rest) p_rest - q_rest, as Q + q_rest = 1
-    K1 = t.s > 0.0f ? A * d / t.s : 0.0f;
-    K2 = t.s1 > 0.0f ? C1 * pr1 / t.s1 : 0.0f;
-  }
-  if (!TWO) K1 += K2;
-  const float mc = shr * a.c, mc1 = shr * kLog2e;
-  auto grad_of = [&](float x) {
-    float v = K1 * ex2(fmaf(x, a.c, -mc));
-    if (TWO) v = fmaf(K2, ex2(fmaf(x, kLog2e, -mc1)), v);
-    return v;
-  };
+    met = true;
+    if (a.cluster > 1) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+    if (BUCKET) {  // clears this row's marks
 #pragma unroll
-  for (int u = 0; u < kVecs; u++) {
-    const int i = u * kThreads + tid;
-    if (i < here) {
+      for (int h = 0; h < 2; h++)
+        if (el[h] >= 0) listed[turn][(el[h] / EPV * 8) >> 5] = 0;
+    }
+    Part t = parts[turn][0];
+    for (int i = 1; i < a.cluster; i++) {
+      const Part p = parts[turn][i];
+      join(t.m, t.s, t.s1, p.m, p.s, p.s1, a.c);
+      if (BUCKET) join(t.tm, t.ts, t.ts1, p.tm, p.ts, p.ts1, a.c);
+      t.b += p.b;
+    }
+    t.z = parts[turn][rank].z;
+    t.base = parts[turn][rank].base;
+    turn ^= 1;
+    // the teacher: q_i = exp(t_i - lt), Q = sum q_i
+    const bool has = t.base != neg_inf() || t.z != t.z;
+    const float lt = BUCKET ? tlse : shift_of(t.base) + logf(t.z);
+    const float Q = BUCKET ? t.z : has ? 1.0f : 0.0f;
+    // the whole row: all = rest and listed
+    float M = t.m, S = t.s, S1 = t.s1;
+    if (BUCKET) join(M, S, S1, t.tm, t.ts, t.ts1, a.c);
+    const float sh = shift_of(M), shr = shift_of(t.m);
+    const bool bucket = BUCKET && has && t.s > 0.0f;
+    const float qr = bucket ? fmaxf(0.0f, 1.0f - Q) : 0.0f;
+    if (a.loss && tid == 0 && rank == 0) {
+      const float L = sh / a.tau + logf(S);
+      float l = 0.0f;
+      if (has) {  // sum q_i (t_i - lt - s_i) + L sum q_i
+        float kl = BUCKET ? t.b + Q * L : t.b / t.z + (L - logf(t.z));
+        if (qr > 0.0f) {  // log q_rest - log p_rest, both from what is listed
+          const float odds = t.ts / t.s * ex2((shift_of(t.tm) - shr) * a.c);
+          const float logp = odds < 1.0f ? log1pf(odds) : L - (shr / a.tau + logf(t.s));
+          kl += qr * (log1pf(-Q) + logp);
+        }
+        l = a.kd * a.tau * a.tau * kl;
+      }
+      if (y >= 0) l += a.ce * (sh + logf(S1) - xy);
+      a.loss[row] = w_now * l;
+    }
+    if (!g) continue;
+    // gradient = K1 2^((x - m) c) + K2 2^((x - m) log2 e), m the maximum of
+    // what the registers hold; the listed coordinates and the label after that
+    const float A = has ? w_now * a.kd * a.tau : 0.0f, C1 = y >= 0 ? w_now * a.ce : 0.0f;
+    float K1 = A * Q / S, K2 = C1 / S1;
+    if (BUCKET) {
+      const float pr = t.s * ex2((shr - sh) * a.c) / S;
+      const float pr1 = t.s1 * ex2((shr - sh) * kLog2e) / S1;
+      const float ptop = t.ts * ex2((shift_of(t.tm) - sh) * a.c) / S;
+      const float d = qr > 0.0f ? Q - ptop : Q * pr;  // (Q + q_rest) p_rest - q_rest; Q + q_rest = 1
+      K1 = t.s > 0.0f ? A * d / t.s : 0.0f;
+      K2 = t.s1 > 0.0f ? C1 * pr1 / t.s1 : 0.0f;
+    }
+    if (!TWO) K1 += K2;
+    const uint64_t c2 = pair(a.c, a.c), mc = pair(-shr * a.c, -shr * a.c), k1 = pair(K1, K1);
+    const uint64_t l2 = pair(kLog2e, kLog2e), ml = pair(-shr * kLog2e, -shr * kLog2e);
+    const uint64_t k2 = pair(K2, K2);
+    auto grad_of = [&](uint64_t x) {
+      uint64_t v = mul2(k1, ex2_2(fma2(x, c2, mc)));
+      if (TWO) v = fma2(k2, ex2_2(fma2(x, l2, ml)), v);
+      return v;
+    };
+#pragma unroll
+    for (int u = 0; u < VECS; u++) {
+      if (u * NT >= here) break;
       float x[EPV];
       E::unpack(r[u], x);
 #pragma unroll
-      for (int j = 0; j < EPV; j++) x[j] = grad_of(x[j]);
-      store(i, x);
+      for (int j = 0; j < EPV; j += 2) {
+        const float2 f = unpair(grad_of(pair(x[j], x[j + 1])));
+        x[j] = f.x;
+        x[j + 1] = f.y;
+      }
+      store(u, E::pack(x));
     }
-  }
-  const int64_t ly = y - e0;
-  const bool y_here = y >= 0 && ly >= 0 && ly < (int64_t)here * EPV;
-  bool y_listed = false;
-  float x_y = 0.0f;
-  if (y_here && tid == 0) x_y = xy;
-  __syncthreads();
-  for (int i = tid; i < a.k; i += kThreads) {
-    if (sidx[i] < 0) continue;
-    const float d = sx[i] - sh;
-    float v = A * ((Q + qr) * ex2(d * a.c) / S - sq[i]);
-    if (y >= 0) v += C1 * ex2(d * kLog2e) / S1;
-    if (y_here && sidx[i] == ly) {
-      v -= C1;
-      y_listed = true;
+    const int64_t ly = y - e0;
+    const bool y_here = y >= 0 && ly >= 0 && ly < (int64_t)here * EPV;
+    const bool y_listed = __syncthreads_or(y_here && (el[0] == ly || el[1] == ly));
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      if (el[h] < 0) continue;
+      const float d = ex[h] - sh, u = has ? expf(et[h] - lt) : 0.0f;
+      float v = A * ((Q + qr) * ex2(d * a.c) / S - u);
+      if (y >= 0) v += C1 * ex2(d * kLog2e) / S1;
+      if (y_here && el[h] == ly) v -= C1;
+      g[e0 + el[h]] = E::make(v);
     }
-    g[e0 + sidx[i]] = E::make(v);
+    if (y_here && !y_listed && tid == 0) g[y] = E::make(unpair(grad_of(pair(xy, xy))).x - C1);
   }
-  if (y_here) {  // the same for the whole CTA
-    y_listed = __syncthreads_or(y_listed);
-    if (!y_listed && tid == 0) g[y] = E::make(grad_of(x_y) - C1);
-  }
+  if (!met) cluster_wait();
 }
 
-template <int DT, bool TWO, bool BUCKET>
+template <int DT, bool TWO, bool BUCKET, class SH>
 cudaError_t launch_parts(const DistillArgs& a, cudaStream_t s) {
+  static std::atomic<uint64_t> configured{0};  // the shared-memory opt-in is per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
+  if (!(configured.load() & bit)) {
+    e = cudaFuncSetAttribute(distill_parts<DT, TWO, BUCKET, SH>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, SH::PART * 16);
+    if (e == cudaSuccess)  // clusters of 16
+      e = cudaFuncSetAttribute(distill_parts<DT, TWO, BUCKET, SH>,
+                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit);
+  }
+  // as many clusters as the GPU holds at once, evened out over the rounds
+  const int64_t slots = (int64_t)num_sms() * SH::MINB / a.cluster;
+  const int64_t rounds = (a.rows + slots - 1) / slots;
+  const int64_t clusters = (a.rows + rounds - 1) / rounds;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(a.rows * a.cluster));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3((unsigned)(clusters * a.cluster));
+  cfg.blockDim = dim3(SH::NT);
+  cfg.dynamicSmemBytes = SH::PART * 16;
   cfg.stream = s;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
@@ -580,25 +676,38 @@ cudaError_t launch_parts(const DistillArgs& a, cudaStream_t s) {
   at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = a.cluster > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, distill_parts<DT, TWO, BUCKET>, a);
+  return cudaLaunchKernelEx(&cfg, distill_parts<DT, TWO, BUCKET, SH>, a);
+}
+
+template <int DT, class SH>
+cudaError_t launch_sized(const DistillArgs& a, cudaStream_t s) {
+  const bool two = a.labels && a.tau != 1.0f, bucket = a.tlse != nullptr;
+  if (two) return bucket ? launch_parts<DT, true, true, SH>(a, s) : launch_parts<DT, true, false, SH>(a, s);
+  return bucket ? launch_parts<DT, false, true, SH>(a, s) : launch_parts<DT, false, false, SH>(a, s);
 }
 
 template <int DT>
 cudaError_t launch_distill(DistillArgs& a, cudaStream_t s) {
-  // vectors of a row, one more where it starts inside one
-  const int64_t nv = a.V / Elem<DT>::kPerVec + 2;
-  if (nv > (int64_t)kPart * kMaxCluster) {
+  // vectors of a row at most: one more where rows start inside one
+  constexpr int64_t EPV = Elem<DT>::kPerVec;
+  const bool whole = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && a.stride % EPV == 0;
+  const int64_t nv = (a.V + (whole ? 0 : EPV - 1) + EPV - 1) / EPV;
+  cudaError_t e;
+  if (nv > (int64_t)Wide::PART * kMaxCluster) {
     const int64_t cap = (int64_t)num_sms() * 4;
     distill_rows<DT><<<(unsigned)(a.rows < cap ? a.rows : cap), kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    e = cudaSuccess;
+  } else {
+    a.cluster = 1;
+    while (nv > (int64_t)Wide::PART * a.cluster) a.cluster *= 2;
+    // few rows: more CTAs for each, down to a vector or two a thread
+    while (a.cluster < 8 && a.rows * a.cluster * 2 <= num_sms() && nv > Narrow::NT * 2 * a.cluster)
+      a.cluster *= 2;
+    a.part_vecs = (int)((nv + a.cluster - 1) / a.cluster);
+    // a thread looks after two of the teacher's entries
+    const bool narrow = a.part_vecs <= Narrow::PART && a.k <= 2 * Narrow::NT;
+    e = narrow ? launch_sized<DT, Narrow>(a, s) : launch_sized<DT, Wide>(a, s);
   }
-  a.cluster = 1;
-  while (nv > (int64_t)kPart * a.cluster) a.cluster *= 2;
-  a.part_vecs = (int)((nv + a.cluster - 1) / a.cluster);
-  const bool two = a.labels && a.tau != 1.0f, bucket = a.tlse != nullptr;
-  cudaError_t e;
-  if (two) e = bucket ? launch_parts<DT, true, true>(a, s) : launch_parts<DT, true, false>(a, s);
-  else e = bucket ? launch_parts<DT, false, true>(a, s) : launch_parts<DT, false, false>(a, s);
   const cudaError_t last = cudaGetLastError();
   return e != cudaSuccess ? e : last;
 }

@@ -34,6 +34,46 @@ __device__ __forceinline__ uint4 ld_row_u4(const void* p) {
   return r;
 }
 
+// Pairs of fp32 in one register pair: one instruction for two operations.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t ex2_2(uint64_t v) {
+  const float2 f = unpair(v);
+  return pair(ex2(f.x), ex2(f.y));
+}
+
+// Asynchronous 16-byte copy to shared memory.  A thread that reads back only
+// what it copied itself needs no barrier, only its own wait.
+__device__ __forceinline__ void copy_async(uint32_t smem, const void* p) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(p) : "memory");
+}
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // A maximum as the shift of a softmax: exp2((x - m) * c) of a row that holds
 // nothing but -inf is then exp2(-inf) = 0 and not NaN.
 __device__ __forceinline__ float shift_of(float m) { return m == neg_inf() ? 0.0f : m; }
@@ -61,6 +101,11 @@ struct Elem<SCAPE_BF16> {
     return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
   }
   static constexpr uint32_t kNegInf2 = 0xFF80FF80u;  // two lowest elements
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 h = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a),
+                                     *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
 };
 
 template <>
@@ -88,6 +133,10 @@ struct Elem<SCAPE_F16> {
     return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
   }
   static constexpr uint32_t kNegInf2 = 0xFC00FC00u;
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    const __half2 h = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
 };
 
 template <>
@@ -105,7 +154,22 @@ struct Elem<SCAPE_F32> {
                       __float_as_uint(f[3]));
   }
   static constexpr uint32_t kNegInf2 = 0xFF800000u;  // (one element)
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }
 };
+
+// Element by element the larger one of two vectors (NaN loses).
+template <int DT>
+__device__ __forceinline__ uint4 max_vec(const uint4 a, const uint4 b) {
+  using E = Elem<DT>;
+  return make_uint4(E::max2(a.x, b.x), E::max2(a.y, b.y), E::max2(a.z, b.z), E::max2(a.w, b.w));
+}
+template <int DT>
+__device__ __forceinline__ uint4 neg_inf_vec() {
+  constexpr uint32_t n = Elem<DT>::kNegInf2;
+  return make_uint4(n, n, n, n);
+}
 
 // One row seen as 16-byte vectors on 16-byte boundaries.  A row starts at any
 // element (odd vocabularies, views): vector v holds the elements
