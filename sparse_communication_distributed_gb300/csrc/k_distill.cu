@@ -230,14 +230,18 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
 
 constexpr int kMaxCluster = 16;
 
-// Threads of a CTA and vectors of a row that each of them holds, for long and
-// for short parts of a row.
-template <int NT_, int VECS_, int MINB_>
+// Threads of a CTA, CTAs of an SM, vectors of a row that a CTA holds at most,
+// for long and for short parts of a row.  Three CTAs share an SM's shared
+// memory (twelve of the short kind), and while one waits for its row the others
+// compute.
+template <int NT_, int MINB_, int PART_>
 struct Shape {
-  static constexpr int NT = NT_, VECS = VECS_, MINB = MINB_, PART = NT_ * VECS_;
+  static constexpr int NT = NT_, MINB = MINB_, PART = PART_;
 };
-using Wide = Shape<256, 16, 2>;
-using Narrow = Shape<128, 8, 8>;
+using Wide = Shape<512, 3, 4096>;
+using Narrow = Shape<128, 12, 1024>;
+constexpr int kEnt = 2;  // teacher entries that a thread looks after
+static_assert(Wide::NT * kEnt == kMaxK, "every entry has a thread");
 
 // What a row's statistics are made of.  A sum of exponentials is held relative
 // to a maximum: s = sum 2^((x - m) c), and s1 the same at temperature 1.
@@ -289,24 +293,24 @@ __device__ __forceinline__ void put_remote(const float* local, uint32_t rank, fl
 }
 
 // A cluster of CTAs (often just one) takes a row, each CTA a part of at most
-// PART vectors, and reads it once; then the cluster takes another row.  A
-// thread keeps its vectors of the row in registers, and copies those of the
-// next row to its own places in shared memory meanwhile, so that loads run all
-// the time.  Each thread looks after up to two of the teacher's entries.  TWO:
-// exponentials at both temperatures are needed (hard labels at temperature !=
-// 1).  BUCKET: the coordinates not listed form a bucket; the listed ones are
-// then taken out of the registers first and added to the sums by the threads
-// that look after them, so that p_rest is a sum and not a difference.
+// PART vectors, and reads it once into shared memory; then the cluster takes
+// another row.  A thread works only on vectors that it copied itself, so that
+// it needs no barrier around them, and in its last pass over a row it starts
+// the copy of the next row's vector as soon as it has read the old one.  Each
+// thread looks after up to kEnt of the teacher's entries.  TWO: exponentials
+// at both temperatures are needed (hard labels at temperature != 1).  BUCKET:
+// the coordinates not listed form a bucket; the listed ones are then set to
+// -inf in shared memory first and added to the sums by the threads that look
+// after them, so that p_rest is a sum and not a difference.
 //
-// Buffers of shared memory are used in turn for one row and the next: between
+// The statistics' buffers are used in turn for one row and the next: between
 // two uses of one there are the other row's barriers.
 template <int DT, bool TWO, bool BUCKET, class SH>
 __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillArgs a) {
   using E = Elem<DT>;
   using T = typename E::T;
-  constexpr int EPV = E::kPerVec, NT = SH::NT, VECS = SH::VECS, kWarps = NT / 32;
-  extern __shared__ __align__(16) uint4 next[];  // PART
-  __shared__ uint32_t listed[2][BUCKET ? SH::PART * 8 / 32 : 1];  // a byte for each vector
+  constexpr int EPV = E::kPerVec, NT = SH::NT, kWarps = NT / 32;
+  extern __shared__ __align__(16) uint4 buf[];  // the part of the row
   __shared__ Part warps[2][kWarps];
   __shared__ Part parts[2][kMaxCluster];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -314,85 +318,89 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
   const int64_t step = gridDim.x / (unsigned)a.cluster;
   const int64_t v0 = (int64_t)rank * a.part_vecs;
   auto weight_of = [&](int64_t row) { return a.weight ? a.weight[row] : 1.0f; };
-  // The part of a row: "here" vectors, whole ones [lo, hi); the first element's
-  // coordinate (< 0 where the row starts inside its first vector).
+  // The part of a row: "here" vectors, whole ones [lo, hi); p is where its first
+  // vector starts (outside the row if that is ragged), e0 that coordinate.
   struct Where {
-    int64_t e0;
-    int here, lo, hi;
+    const T* p;
+    int e0, here, lo, hi;
   };
-  auto where = [&](const RowView<DT>& view) {
-    const int64_t nv = view.vectors();
+  auto where = [&](int64_t row) {
+    const RowView<DT> view(a.x, row * a.stride, a.V);
+    const int V = (int)a.V, first = (int)v0 * EPV - view.shift;
     Where w;
-    w.e0 = view.first_of(v0);
-    w.here = (int)max((int64_t)0, min((int64_t)a.part_vecs, nv - v0));
-    w.lo = w.e0 < 0 ? 1 : 0;
-    w.hi = (int)max((int64_t)0, min((int64_t)w.here, (a.V - w.e0) / EPV));
+    w.e0 = first;
+    w.p = view.p + first;
+    w.here = max(0, min(a.part_vecs, (V - first + EPV - 1) / EPV));
+    w.lo = first < 0 ? 1 : 0;
+    w.hi = max(0, min(w.here, (V - first) / EPV));
     return w;
   };
-  // starts the copies of this thread's vectors of a row; a ragged vector is put
-  // together from single loads
-  auto fetch = [&](int64_t row) {
-    const RowView<DT> view(a.x, row * a.stride, a.V);
-    const Where w = where(view);
-    const T* from = view.p + w.e0 + tid * EPV;
-    const uint32_t to = (uint32_t)__cvta_generic_to_shared(next + tid);
+  // starts the copy of one whole vector
+  const uint32_t buf_at = (uint32_t)__cvta_generic_to_shared(buf);
+  auto fetch = [&](const Where& w, int i) {
+    if (i >= w.lo && i < w.hi) copy_async(buf_at + i * 16, w.p + i * EPV);
+  };
+  // ... and puts ragged ones together from single loads
+  auto fetch_ragged = [&](const Where& w) {
+    auto one = [&](int i) {
+      float f[EPV];
 #pragma unroll
-    for (int u = 0; u < VECS; u++)
-      if (u * NT + tid < w.hi && (u > 0 || tid >= w.lo)) copy_async(to + u * NT * 16, from + u * NT * EPV);
-    if (w.lo == 1 && tid == 0 && w.here > 0) next[0] = view.load(v0);
-    if (w.here > w.hi && w.here > w.lo && (w.here - 1) % NT == tid)
-      next[w.here - 1] = view.load(v0 + w.here - 1);
+      for (int j = 0; j < EPV; j++) {
+        const int e = w.e0 + i * EPV + j;
+        f[j] = e >= 0 && e < (int)a.V ? E::load(w.p + i * EPV + j) : neg_inf();
+      }
+      buf[i] = E::pack(f);
+    };
+    if (w.lo == 1 && w.here > 0 && tid == 0) one(0);
+    if (w.here > w.hi && w.here > w.lo && (w.here - 1) % NT == tid) one(w.here - 1);
   };
   if (a.cluster > 1) cluster_arrive();  // "this CTA runs": its shared memory may be written
   bool met = a.cluster == 1;
-  if (BUCKET) {
-    for (int i = tid; i < 2 * SH::PART * 8 / 32; i += NT) listed[0][i] = 0;
-    __syncthreads();
-  }
   int turn = 0;
   int64_t row = blockIdx.x / (unsigned)a.cluster;
   float w = row < a.rows ? weight_of(row) : 0.0f;
-  if (w != 0.0f) fetch(row);
+  Where at = where(row < a.rows ? row : 0);
+  if (w != 0.0f) {
+    for (int i = tid; i < at.here; i += NT) fetch(at, i);
+    fetch_ragged(at);
+  }
   for (; row < a.rows; row += step) {
-    const RowView<DT> view(a.x, row * a.stride, a.V);
-    const Where at = where(view);
-    const int here = at.here;
-    const int64_t e0 = at.e0;
-    T* g = a.grad ? static_cast<T*>(a.grad) + row * a.gstride : nullptr;
-    // writes vector u of this thread
-    const bool same =
-        g && ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(view.p)) & 15u) == 0;
-    T* gt = g + e0 + tid * EPV;
-    auto store = [&](int u, const uint4 v) {
-      const int i = u * NT + tid;
-      if (same && i < at.hi && (u > 0 || tid >= at.lo)) {
-        *reinterpret_cast<uint4*>(gt + u * NT * EPV) = v;
-      } else if (i < here) {
-        const T* t = reinterpret_cast<const T*>(&v);
-        const int64_t e = e0 + (int64_t)i * EPV;
-#pragma unroll
-        for (int j = 0; j < EPV; j++)
-          if (e + j >= 0 && e + j < a.V) g[e + j] = t[j];
-      }
-    };
     const int64_t row2 = row + step;
     const float w_now = w;
+    const Where now = at;
+    const int here = now.here;
     w = row2 < a.rows ? weight_of(row2) : 0.0f;
-    if (w_now == 0.0f) {  // the whole cluster agrees
-      if (w != 0.0f) fetch(row2);
-      if (g) {
+    at = where(row2 < a.rows ? row2 : row);
+    if (w == 0.0f) at.hi = 0;  // nothing to copy
+    T* g = a.grad ? static_cast<T*>(a.grad) + row * a.gstride + now.e0 : nullptr;
+    // writes vector i of the part
+    const bool same = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(now.p)) & 15u) == 0;
+    auto store = [&](int i, const uint4 v) {
+      if (same && i >= now.lo && i < now.hi) {
+        *reinterpret_cast<uint4*>(g + i * EPV) = v;
+      } else {
+        const T* t = reinterpret_cast<const T*>(&v);
 #pragma unroll
-        for (int u = 0; u < VECS; u++) store(u, make_uint4(0, 0, 0, 0));
+        for (int j = 0; j < EPV; j++) {
+          const int e = now.e0 + i * EPV + j;
+          if (e >= 0 && e < (int)a.V) g[i * EPV + j] = t[j];
+        }
       }
+    };
+    if (w_now == 0.0f) {  // the whole cluster agrees
+      for (int i = tid; i < here; i += NT)
+        if (g) store(i, make_uint4(0, 0, 0, 0));
+      for (int i = tid; i < at.hi; i += NT) fetch(at, i);
+      if (w != 0.0f) fetch_ragged(at);
       if (a.loss && tid == 0 && rank == 0) a.loss[row] = 0.0f;
       continue;
     }
     // the teacher's entries of this thread: local coordinate (-1: not of this
     // part), t, x
-    int el[2];
-    float et[2], ex[2];
+    int el[kEnt];
+    float et[kEnt], ex[kEnt];
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
+    for (int h = 0; h < kEnt; h++) {
       const int i = h * NT + tid;
       el[h] = -1;
       et[h] = neg_inf();
@@ -400,18 +408,14 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
       if (i < a.k) {
         const int32_t e = a.idx[row * a.k + i];
         const float v = load_val(a.vals, a.vals_dtype, row * a.k + i);
-        const int64_t l = e - e0;
         if (e >= a.V) {
           if (a.bad && rank == 0) atomicAdd(a.bad, 1u);
         } else if (e >= 0) {
           et[h] = v / a.tau;
+          const int64_t l = (int64_t)e - now.e0;
           if (l >= 0 && l < (int64_t)here * EPV) {
             el[h] = (int)l;
-            ex[h] = E::load(view.p + e);
-            if (BUCKET) {
-              const int bit = el[h] / EPV * 8 + el[h] % EPV;
-              atomicOr(&listed[turn][bit >> 5], 1u << (bit & 31));
-            }
+            ex[h] = E::load(now.p + l);
           }
         }
       }
@@ -421,53 +425,40 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
       if (a.bad && tid == 0 && rank == 0) atomicAdd(a.bad, 1u);
       y = -1;
     }
-    const float xy = y >= 0 && tid == 0 ? E::load(view.p + y) : 0.0f;
+    const float xy = y >= 0 && tid == 0 ? E::load(now.p + ((int)y - now.e0)) : 0.0f;
     const float tlse = a.tlse ? a.tlse[row] : 0.0f;
-
     copy_wait();
-    uint4 r[VECS];
-#pragma unroll
-    for (int u = 0; u < VECS; u++) r[u] = u * NT + tid < here ? next[u * NT + tid] : neg_inf_vec<DT>();
     if (BUCKET) {
       __syncthreads();
 #pragma unroll
-      for (int u = 0; u < VECS; u++) {
-        const uint32_t bits = reinterpret_cast<const uint8_t*>(listed[turn])[u * NT + tid];
-        if (bits) {
-          float x[EPV];
-          E::unpack(r[u], x);
-#pragma unroll
-          for (int j = 0; j < EPV; j++)
-            if (bits >> j & 1) x[j] = neg_inf();
-          r[u] = E::pack(x);
-        }
-      }
+      for (int h = 0; h < kEnt; h++)
+        if (el[h] >= 0) reinterpret_cast<T*>(buf)[el[h]] = E::make(neg_inf());
+      __syncthreads();
     }
-    uint4 mx = r[0];
-#pragma unroll
-    for (int u = 1; u < VECS; u++) mx = max_vec<DT>(mx, r[u]);
+
+    // a thread's statistics, relative to its warp's maximum
     Part q;
     {
+      uint4 mx = neg_inf_vec<DT>();
+#pragma unroll 4
+      for (int i = tid; i < here; i += NT) mx = max_vec<DT>(mx, buf[i]);
       float x[EPV];
       E::unpack(mx, x);
       q.m = x[0];
 #pragma unroll
       for (int j = 1; j < EPV; j++) q.m = fmaxf(q.m, x[j]);
+      q.m = shfl_max(q.m, 32);
     }
-    if (w != 0.0f) fetch(row2);  // the registers hold this row
-
-    // a thread's statistics, relative to its warp's maximum
-    q.m = shfl_max(q.m, 32);
     {
       const float sh = shift_of(q.m);
       const uint64_t c2 = pair(a.c, a.c), mc = pair(-sh * a.c, -sh * a.c);
       const uint64_t l2 = pair(kLog2e, kLog2e), ml = pair(-sh * kLog2e, -sh * kLog2e);
       uint64_t s = 0, s1 = 0;
-#pragma unroll
-      for (int u = 0; u < VECS; u++) {
-        if (u * NT >= here) break;
+#pragma unroll 4
+      for (int i = tid; i < here; i += NT) {
         float x[EPV];
-        E::unpack(r[u], x);
+        E::unpack(buf[i], x);
+        if (!g) fetch(at, i);
 #pragma unroll
         for (int j = 0; j < EPV; j += 2) {
           const uint64_t xx = pair(x[j], x[j + 1]);
@@ -482,12 +473,18 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     q.tm = q.base = neg_inf();
     q.ts = q.ts1 = q.z = q.zp = q.b = 0.0f;
     if (wid * 32 < a.k) {  // the teacher's entries of this warp
-      q.base = shfl_max(fmaxf(et[0], et[1]), 32);
+      float tmax = et[0], xmax = el[0] >= 0 ? ex[0] : neg_inf();
+#pragma unroll
+      for (int h = 1; h < kEnt; h++) {
+        tmax = fmaxf(tmax, et[h]);
+        xmax = fmaxf(xmax, el[h] >= 0 ? ex[h] : neg_inf());
+      }
+      q.base = shfl_max(tmax, 32);
       const float base = BUCKET ? tlse : shift_of(q.base);
-      if (BUCKET) q.tm = shfl_max(fmaxf(el[0] >= 0 ? ex[0] : neg_inf(), el[1] >= 0 ? ex[1] : neg_inf()), 32);
+      if (BUCKET) q.tm = shfl_max(xmax, 32);
       const float tsh = shift_of(q.tm);
 #pragma unroll
-      for (int h = 0; h < 2; h++) {
+      for (int h = 0; h < kEnt; h++) {
         const float u = expf(et[h] - base);
         q.z += u;
         if (el[h] >= 0) {
@@ -552,11 +549,6 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     } else {
       __syncthreads();
     }
-    if (BUCKET) {  // clears this row's marks
-#pragma unroll
-      for (int h = 0; h < 2; h++)
-        if (el[h] >= 0) listed[turn][(el[h] / EPV * 8) >> 5] = 0;
-    }
     Part t = parts[turn][0];
     for (int i = 1; i < a.cluster; i++) {
       const Part p = parts[turn][i];
@@ -592,9 +584,12 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
       if (y >= 0) l += a.ce * (sh + logf(S1) - xy);
       a.loss[row] = w_now * l;
     }
-    if (!g) continue;
+    if (!g) {
+      if (w != 0.0f) fetch_ragged(at);
+      continue;
+    }
     // gradient = K1 2^((x - m) c) + K2 2^((x - m) log2 e), m the maximum of
-    // what the registers hold; the listed coordinates and the label after that
+    // what the buffer holds; the listed coordinates and the label after that
     const float A = has ? w_now * a.kd * a.tau : 0.0f, C1 = y >= 0 ? w_now * a.ce : 0.0f;
     float K1 = A * Q / S, K2 = C1 / S1;
     if (BUCKET) {
@@ -614,32 +609,36 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
       if (TWO) v = fma2(k2, ex2_2(fma2(x, l2, ml)), v);
       return v;
     };
-#pragma unroll
-    for (int u = 0; u < VECS; u++) {
-      if (u * NT >= here) break;
+#pragma unroll 2
+    for (int i = tid; i < here; i += NT) {
       float x[EPV];
-      E::unpack(r[u], x);
+      E::unpack(buf[i], x);
+      fetch(at, i);
 #pragma unroll
       for (int j = 0; j < EPV; j += 2) {
         const float2 f = unpair(grad_of(pair(x[j], x[j + 1])));
         x[j] = f.x;
         x[j + 1] = f.y;
       }
-      store(u, E::pack(x));
+      store(i, E::pack(x));
     }
-    const int64_t ly = y - e0;
+    if (w != 0.0f) fetch_ragged(at);
+    const int64_t ly = y - now.e0;
     const bool y_here = y >= 0 && ly >= 0 && ly < (int64_t)here * EPV;
-    const bool y_listed = __syncthreads_or(y_here && (el[0] == ly || el[1] == ly));
+    bool y_listed = false;
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
+    for (int h = 0; h < kEnt; h++) y_listed |= y_here && el[h] == ly;
+    y_listed = __syncthreads_or(y_listed);
+#pragma unroll
+    for (int h = 0; h < kEnt; h++) {
       if (el[h] < 0) continue;
       const float d = ex[h] - sh, u = has ? expf(et[h] - lt) : 0.0f;
       float v = A * ((Q + qr) * ex2(d * a.c) / S - u);
       if (y >= 0) v += C1 * ex2(d * kLog2e) / S1;
       if (y_here && el[h] == ly) v -= C1;
-      g[e0 + el[h]] = E::make(v);
+      g[el[h]] = E::make(v);
     }
-    if (y_here && !y_listed && tid == 0) g[y] = E::make(unpair(grad_of(pair(xy, xy))).x - C1);
+    if (y_here && !y_listed && tid == 0) g[ly] = E::make(unpair(grad_of(pair(xy, xy))).x - C1);
   }
   if (!met) cluster_wait();
 }
@@ -667,7 +666,7 @@ cudaError_t launch_parts(const DistillArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(clusters * a.cluster));
   cfg.blockDim = dim3(SH::NT);
-  cfg.dynamicSmemBytes = SH::PART * 16;
+  cfg.dynamicSmemBytes = (size_t)a.part_vecs * 16;
   cfg.stream = s;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
@@ -704,8 +703,7 @@ cudaError_t launch_distill(DistillArgs& a, cudaStream_t s) {
     while (a.cluster < 8 && a.rows * a.cluster * 2 <= num_sms() && nv > Narrow::NT * 2 * a.cluster)
       a.cluster *= 2;
     a.part_vecs = (int)((nv + a.cluster - 1) / a.cluster);
-    // a thread looks after two of the teacher's entries
-    const bool narrow = a.part_vecs <= Narrow::PART && a.k <= 2 * Narrow::NT;
+    const bool narrow = a.part_vecs <= Narrow::PART && a.k <= Narrow::NT * kEnt;
     e = narrow ? launch_sized<DT, Narrow>(a, s) : launch_sized<DT, Wide>(a, s);
   }
   const cudaError_t last = cudaGetLastError();
