@@ -230,18 +230,19 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
 
 constexpr int kMaxCluster = 16;
 
-// Threads of a CTA, CTAs of an SM, vectors of a row that a CTA holds at most,
-// for long and for short parts of a row.  Three CTAs share an SM's shared
-// memory (twelve of the short kind), and while one waits for its row the others
-// compute.
-template <int NT_, int MINB_, int PART_>
+// Threads of a CTA, vectors of a row that each of them has at most, CTAs of an
+// SM, teacher entries that a thread looks after: for long parts of a row, for
+// short ones, and for long ones with many entries.  Three CTAs share an SM's
+// shared memory, and while one waits for its row the others compute.
+template <int NT_, int VECS_, int MINB_, int ENT_>
 struct Shape {
-  static constexpr int NT = NT_, MINB = MINB_, PART = PART_;
+  static constexpr int NT = NT_, VECS = VECS_, MINB = MINB_, ENT = ENT_;
+  static constexpr int PART = NT_ * VECS_, MAXK = NT_ * ENT_;
 };
-using Wide = Shape<512, 3, 4096>;
-using Narrow = Shape<128, 12, 1024>;
-constexpr int kEnt = 2;  // teacher entries that a thread looks after
-static_assert(Wide::NT * kEnt == kMaxK, "every entry has a thread");
+using Wide = Shape<256, 16, 3, 1>;
+using Narrow = Shape<128, 8, 8, 2>;
+using Deep = Shape<512, 8, 2, 2>;
+static_assert(Deep::MAXK == kMaxK, "every entry has a thread");
 
 // What a row's statistics are made of.  A sum of exponentials is held relative
 // to a maximum: s = sum 2^((x - m) c), and s1 the same at temperature 1.
@@ -292,12 +293,19 @@ __device__ __forceinline__ void put_remote(const float* local, uint32_t rank, fl
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(v) : "memory");
 }
 
+// What one warp works out for all threads once a row's statistics are known.
+struct __align__(16) Row {
+  float m, K1, K2, rS;         // gradient = K1 2^((x - m) c) + K2 2^((x - m) log2 e) at unlisted
+  float M, A, C1, rS1;         // p = 2^((x - M) c) rS; softmax(x) = 2^((x - M) log2 e) rS1
+  float Qr, base, rz, unused;  // sum q + q_rest; q_i = exp(t_i - base) rz
+};
+
 // A cluster of CTAs (often just one) takes a row, each CTA a part of at most
 // PART vectors, and reads it once into shared memory; then the cluster takes
 // another row.  A thread works only on vectors that it copied itself, so that
 // it needs no barrier around them, and in its last pass over a row it starts
 // the copy of the next row's vector as soon as it has read the old one.  Each
-// thread looks after up to kEnt of the teacher's entries.  TWO: exponentials
+// thread looks after up to ENT of the teacher's entries.  TWO: exponentials
 // at both temperatures are needed (hard labels at temperature != 1).  BUCKET:
 // the coordinates not listed form a bucket; the listed ones are then set to
 // -inf in shared memory first and added to the sums by the threads that look
@@ -309,14 +317,19 @@ template <int DT, bool TWO, bool BUCKET, class SH>
 __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillArgs a) {
   using E = Elem<DT>;
   using T = typename E::T;
-  constexpr int EPV = E::kPerVec, NT = SH::NT, kWarps = NT / 32;
+  constexpr int EPV = E::kPerVec, NT = SH::NT, VECS = SH::VECS, ENT = SH::ENT;
+  constexpr int kWarps = NT / 32;
+  constexpr int BLK = 2;  // vectors that a thread handles at a time
   extern __shared__ __align__(16) uint4 buf[];  // the part of the row
   __shared__ Part warps[2][kWarps];
   __shared__ Part parts[2][kMaxCluster];
+  __shared__ Row rows[2];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const uint32_t rank = a.cluster > 1 ? cluster_rank() : 0;
   const int64_t step = gridDim.x / (unsigned)a.cluster;
-  const int64_t v0 = (int64_t)rank * a.part_vecs;
+  const int v0 = (int)rank * a.part_vecs;
+  const int V = (int)a.V;
+  const float inv_tau = 1.0f / a.tau;
   auto weight_of = [&](int64_t row) { return a.weight ? a.weight[row] : 1.0f; };
   // The part of a row: "here" vectors, whole ones [lo, hi); p is where its first
   // vector starts (outside the row if that is ragged), e0 that coordinate.
@@ -324,21 +337,31 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     const T* p;
     int e0, here, lo, hi;
   };
-  auto where = [&](int64_t row) {
-    const RowView<DT> view(a.x, row * a.stride, a.V);
-    const int V = (int)a.V, first = (int)v0 * EPV - view.shift;
+  auto where = [&](const T* row_start) {
     Where w;
-    w.e0 = first;
-    w.p = view.p + first;
-    w.here = max(0, min(a.part_vecs, (V - first + EPV - 1) / EPV));
-    w.lo = first < 0 ? 1 : 0;
-    w.hi = max(0, min(w.here, (V - first) / EPV));
+    w.e0 = v0 * EPV - (int)((reinterpret_cast<uintptr_t>(row_start) & 15u) / sizeof(T));
+    w.p = row_start + w.e0;
+    const int left = V - w.e0;  // elements from the part's start
+    w.here = max(0, min(a.part_vecs, (left + EPV - 1) / EPV));
+    w.lo = w.e0 < 0 ? 1 : 0;
+    w.hi = max(0, min(w.here, left / EPV));
     return w;
   };
-  // starts the copy of one whole vector
-  const uint32_t buf_at = (uint32_t)__cvta_generic_to_shared(buf);
-  auto fetch = [&](const Where& w, int i) {
-    if (i >= w.lo && i < w.hi) copy_async(buf_at + i * 16, w.p + i * EPV);
+  const uint32_t buf_at = (uint32_t)__cvta_generic_to_shared(buf) + tid * 16;
+  // starts the copies of the whole vectors among BLK of this thread's
+  auto fetch = [&](const Where& w, int u0) {
+    const T* p = w.p + (int64_t)(u0 * NT + tid) * EPV;
+    const uint32_t to = buf_at + u0 * NT * 16;
+    if (u0 * NT >= w.lo && (u0 + BLK) * NT <= w.hi) {
+#pragma unroll
+      for (int u = 0; u < BLK; u++) copy_async(to + u * NT * 16, p + u * NT * EPV);
+    } else {
+#pragma unroll
+      for (int u = 0; u < BLK; u++) {
+        const int i = (u0 + u) * NT + tid;
+        if (i >= w.lo && i < w.hi) copy_async(to + u * NT * 16, p + u * NT * EPV);
+      }
+    }
   };
   // ... and puts ragged ones together from single loads
   auto fetch_ragged = [&](const Where& w) {
@@ -347,21 +370,69 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
 #pragma unroll
       for (int j = 0; j < EPV; j++) {
         const int e = w.e0 + i * EPV + j;
-        f[j] = e >= 0 && e < (int)a.V ? E::load(w.p + i * EPV + j) : neg_inf();
+        f[j] = e >= 0 && e < V ? E::load(w.p + i * EPV + j) : neg_inf();
       }
       buf[i] = E::pack(f);
     };
     if (w.lo == 1 && w.here > 0 && tid == 0) one(0);
     if (w.here > w.hi && w.here > w.lo && (w.here - 1) % NT == tid) one(w.here - 1);
   };
+  // Side inputs of a row: what the arrays hold, loaded a row ahead, and what
+  // that and x make of it once the row is in shared memory.
+  int32_t raw_e[ENT];
+  float raw_v[ENT], raw_lse = 0.0f;
+  int64_t raw_y = -1;
+  auto load_side = [&](int64_t row) {
+#pragma unroll
+    for (int h = 0; h < ENT; h++) {
+      const int i = h * NT + tid;
+      raw_e[h] = -1;
+      raw_v[h] = 0.0f;
+      if (i < a.k) {
+        raw_e[h] = a.idx[row * a.k + i];
+        raw_v[h] = load_val(a.vals, a.vals_dtype, row * a.k + i);
+      }
+    }
+    if (a.labels) raw_y = a.labels[row];
+    if (BUCKET) raw_lse = a.tlse[row];
+  };
+  // the teacher's entries of this thread: local coordinate (-1: not of this
+  // part), t, x; the label and, for one thread, x there
+  int el[ENT], y = -1;
+  float et[ENT], ex[ENT], xy = 0.0f, tlse = 0.0f;
+  auto take_side = [&](const Where& w) {
+#pragma unroll
+    for (int h = 0; h < ENT; h++) {
+      const int32_t e = raw_e[h];
+      el[h] = -1;
+      et[h] = neg_inf();
+      ex[h] = 0.0f;
+      if (e >= V) {
+        if (a.bad && rank == 0) atomicAdd(a.bad, 1u);
+      } else if (e >= 0) {
+        et[h] = raw_v[h] * inv_tau;
+        const int l = e - w.e0;  // e < 2^20, e0 > -8
+        if (l >= 0 && l < w.here * EPV) {
+          el[h] = l;
+          ex[h] = E::load(reinterpret_cast<const T*>(buf) + l);
+        }
+      }
+    }
+    if (raw_y >= V && a.bad && tid == 0 && rank == 0) atomicAdd(a.bad, 1u);
+    y = raw_y < 0 || raw_y >= V ? -1 : (int)raw_y;
+    if (y >= 0 && tid == 0) xy = E::load(w.p + (y - w.e0));
+    tlse = raw_lse;
+  };
   if (a.cluster > 1) cluster_arrive();  // "this CTA runs": its shared memory may be written
   bool met = a.cluster == 1;
   int turn = 0;
   int64_t row = blockIdx.x / (unsigned)a.cluster;
+  const T* row_start = static_cast<const T*>(a.x) + row * a.stride;
   float w = row < a.rows ? weight_of(row) : 0.0f;
-  Where at = where(row < a.rows ? row : 0);
+  Where at = where(row_start);
   if (w != 0.0f) {
-    for (int i = tid; i < at.here; i += NT) fetch(at, i);
+    load_side(row);
+    for (int u0 = 0; u0 < VECS; u0 += BLK) fetch(at, u0);
     fetch_ragged(at);
   }
   for (; row < a.rows; row += step) {
@@ -369,79 +440,82 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     const float w_now = w;
     const Where now = at;
     const int here = now.here;
+    row_start += step * a.stride;
     w = row2 < a.rows ? weight_of(row2) : 0.0f;
-    at = where(row2 < a.rows ? row2 : row);
-    if (w == 0.0f) at.hi = 0;  // nothing to copy
+    at = where(row_start);
+    if (w == 0.0f) at.hi = at.here = 0;  // nothing to copy
     T* g = a.grad ? static_cast<T*>(a.grad) + row * a.gstride + now.e0 : nullptr;
-    // writes vector i of the part
     const bool same = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(now.p)) & 15u) == 0;
-    auto store = [&](int i, const uint4 v) {
-      if (same && i >= now.lo && i < now.hi) {
-        *reinterpret_cast<uint4*>(g + i * EPV) = v;
-      } else {
-        const T* t = reinterpret_cast<const T*>(&v);
+    // writes BLK vectors of this thread
+    auto store = [&](int u0, const uint4 (&v)[BLK]) {
+      T* p = g + (int64_t)(u0 * NT + tid) * EPV;
+      if (same && u0 * NT >= now.lo && (u0 + BLK) * NT <= now.hi) {
 #pragma unroll
-        for (int j = 0; j < EPV; j++) {
-          const int e = now.e0 + i * EPV + j;
-          if (e >= 0 && e < (int)a.V) g[i * EPV + j] = t[j];
+        for (int u = 0; u < BLK; u++) *reinterpret_cast<uint4*>(p + u * NT * EPV) = v[u];
+      } else {
+#pragma unroll
+        for (int u = 0; u < BLK; u++) {
+          const int i = (u0 + u) * NT + tid;
+          if (same && i >= now.lo && i < now.hi) {
+            *reinterpret_cast<uint4*>(p + u * NT * EPV) = v[u];
+          } else {
+            const T* t = reinterpret_cast<const T*>(&v[u]);
+#pragma unroll
+            for (int j = 0; j < EPV; j++) {
+              const int e = now.e0 + i * EPV + j;
+              if (i < here && e >= 0 && e < V) p[u * NT * EPV + j] = t[j];
+            }
+          }
         }
       }
     };
     if (w_now == 0.0f) {  // the whole cluster agrees
-      for (int i = tid; i < here; i += NT)
-        if (g) store(i, make_uint4(0, 0, 0, 0));
-      for (int i = tid; i < at.hi; i += NT) fetch(at, i);
-      if (w != 0.0f) fetch_ragged(at);
+      const uint4 zero[BLK] = {};
+      if (g)
+        for (int u0 = 0; u0 * NT < here; u0 += BLK) store(u0, zero);
       if (a.loss && tid == 0 && rank == 0) a.loss[row] = 0.0f;
+      if (w != 0.0f) {
+        load_side(row2);
+        for (int u0 = 0; u0 * NT < at.hi; u0 += BLK) fetch(at, u0);
+        fetch_ragged(at);
+      }
       continue;
     }
-    // the teacher's entries of this thread: local coordinate (-1: not of this
-    // part), t, x
-    int el[kEnt];
-    float et[kEnt], ex[kEnt];
-#pragma unroll
-    for (int h = 0; h < kEnt; h++) {
-      const int i = h * NT + tid;
-      el[h] = -1;
-      et[h] = neg_inf();
-      ex[h] = 0.0f;
-      if (i < a.k) {
-        const int32_t e = a.idx[row * a.k + i];
-        const float v = load_val(a.vals, a.vals_dtype, row * a.k + i);
-        if (e >= a.V) {
-          if (a.bad && rank == 0) atomicAdd(a.bad, 1u);
-        } else if (e >= 0) {
-          et[h] = v / a.tau;
-          const int64_t l = (int64_t)e - now.e0;
-          if (l >= 0 && l < (int64_t)here * EPV) {
-            el[h] = (int)l;
-            ex[h] = E::load(now.p + l);
-          }
-        }
-      }
-    }
-    int64_t y = a.labels ? a.labels[row] : -1;
-    if (y >= a.V) {
-      if (a.bad && tid == 0 && rank == 0) atomicAdd(a.bad, 1u);
-      y = -1;
-    }
-    const float xy = y >= 0 && tid == 0 ? E::load(now.p + ((int)y - now.e0)) : 0.0f;
-    const float tlse = a.tlse ? a.tlse[row] : 0.0f;
     copy_wait();
+    __syncthreads();
+    take_side(now);
+    if (w != 0.0f) load_side(row2);
     if (BUCKET) {
       __syncthreads();
 #pragma unroll
-      for (int h = 0; h < kEnt; h++)
+      for (int h = 0; h < ENT; h++)
         if (el[h] >= 0) reinterpret_cast<T*>(buf)[el[h]] = E::make(neg_inf());
       __syncthreads();
     }
+    // BLK vectors of this thread, -inf beyond the part
+    auto read = [&](int u0, uint4 (&r)[BLK]) {
+      const uint4* p = buf + u0 * NT + tid;
+      if ((u0 + BLK) * NT <= here) {
+#pragma unroll
+        for (int u = 0; u < BLK; u++) r[u] = p[u * NT];
+      } else {
+#pragma unroll
+        for (int u = 0; u < BLK; u++)
+          r[u] = (u0 + u) * NT + tid < here ? p[u * NT] : neg_inf_vec<DT>();
+      }
+    };
 
     // a thread's statistics, relative to its warp's maximum
     Part q;
     {
       uint4 mx = neg_inf_vec<DT>();
-#pragma unroll 4
-      for (int i = tid; i < here; i += NT) mx = max_vec<DT>(mx, buf[i]);
+#pragma unroll 1
+      for (int u0 = 0; u0 * NT < here; u0 += BLK) {
+        uint4 r[BLK];
+        read(u0, r);
+#pragma unroll
+        for (int u = 0; u < BLK; u++) mx = max_vec<DT>(mx, r[u]);
+      }
       float x[EPV];
       E::unpack(mx, x);
       q.m = x[0];
@@ -449,33 +523,37 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
       for (int j = 1; j < EPV; j++) q.m = fmaxf(q.m, x[j]);
       q.m = shfl_max(q.m, 32);
     }
+    const pair_t c2 = pair(a.c, a.c), l2 = pair(kLog2e, kLog2e);
     {
       const float sh = shift_of(q.m);
-      const uint64_t c2 = pair(a.c, a.c), mc = pair(-sh * a.c, -sh * a.c);
-      const uint64_t l2 = pair(kLog2e, kLog2e), ml = pair(-sh * kLog2e, -sh * kLog2e);
-      uint64_t s = 0, s1 = 0;
-#pragma unroll 4
-      for (int i = tid; i < here; i += NT) {
-        float x[EPV];
-        E::unpack(buf[i], x);
-        if (!g) fetch(at, i);
+      const pair_t mc = pair(-sh * a.c, -sh * a.c), ml = pair(-sh * kLog2e, -sh * kLog2e);
+      pair_t s = pair(0.0f, 0.0f), s1 = s;
+#pragma unroll 1
+      for (int u0 = 0; u0 * NT < here; u0 += BLK) {
+        uint4 r[BLK];
+        read(u0, r);
+        if (!g) fetch(at, u0);
 #pragma unroll
-        for (int j = 0; j < EPV; j += 2) {
-          const uint64_t xx = pair(x[j], x[j + 1]);
-          s = add2(s, ex2_2(fma2(xx, c2, mc)));
-          if (TWO) s1 = add2(s1, ex2_2(fma2(xx, l2, ml)));
+        for (int u = 0; u < BLK; u++) {
+          float x[EPV];
+          E::unpack(r[u], x);
+#pragma unroll
+          for (int j = 0; j < EPV; j += 2) {
+            const pair_t xx = pair(x[j], x[j + 1]);
+            s = add2(s, ex2_2(fma2(xx, c2, mc)));
+            if (TWO) s1 = add2(s1, ex2_2(fma2(xx, l2, ml)));
+          }
         }
       }
-      const float2 f = unpair(s), f1 = unpair(s1);
-      q.s = shfl_sum(f.x + f.y, 32);
-      q.s1 = TWO ? shfl_sum(f1.x + f1.y, 32) : q.s;
+      q.s = shfl_sum(s.x + s.y, 32);
+      q.s1 = TWO ? shfl_sum(s1.x + s1.y, 32) : q.s;
     }
     q.tm = q.base = neg_inf();
     q.ts = q.ts1 = q.z = q.zp = q.b = 0.0f;
     if (wid * 32 < a.k) {  // the teacher's entries of this warp
       float tmax = et[0], xmax = el[0] >= 0 ? ex[0] : neg_inf();
 #pragma unroll
-      for (int h = 1; h < kEnt; h++) {
+      for (int h = 1; h < ENT; h++) {
         tmax = fmaxf(tmax, et[h]);
         xmax = fmaxf(xmax, el[h] >= 0 ? ex[h] : neg_inf());
       }
@@ -484,12 +562,12 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
       if (BUCKET) q.tm = shfl_max(xmax, 32);
       const float tsh = shift_of(q.tm);
 #pragma unroll
-      for (int h = 0; h < kEnt; h++) {
+      for (int h = 0; h < ENT; h++) {
         const float u = expf(et[h] - base);
         q.z += u;
         if (el[h] >= 0) {
           q.zp += u;
-          if (u != 0.0f) q.b += u * ((et[h] - base) - ex[h] / a.tau);
+          if (u != 0.0f) q.b += u * ((et[h] - base) - ex[h] * inv_tau);
           if (BUCKET) {
             q.ts += ex2((ex[h] - tsh) * a.c);
             if (TWO) q.ts1 += ex2((ex[h] - tsh) * kLog2e);
@@ -506,139 +584,162 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     }
     if (lane == 0) warps[turn][wid] = q;
     __syncthreads();
-    if (wid == 0) {  // the CTA's
+    struct {
+      float sh, shr, S, S1, z, Q, qr;
+      bool has;
+      float odds, s, b;  // odds = p_listed / p_rest
+    } ls;
+    if (wid == 0) {
+      // the CTA's, then the cluster's: the partial statistics of n parts, one in
+      // each of the first n lanes
+      auto merge = [&](int n) {
+        const float m = shfl_max(q.m, n), d = q.m - shift_of(m);
+        q.s = shfl_sum(q.s * ex2(d * a.c), n);
+        q.s1 = TWO ? shfl_sum(q.s1 * ex2(d * kLog2e), n) : q.s;
+        q.m = m;
+        if (BUCKET) {
+          const float tm = shfl_max(q.tm, n), td = q.tm - shift_of(tm);
+          q.ts = shfl_sum(q.ts * ex2(td * a.c), n);
+          q.ts1 = TWO ? shfl_sum(q.ts1 * ex2(td * kLog2e), n) : q.ts;
+          q.tm = tm;
+        }
+      };
       if (lane < kWarps) q = warps[turn][lane];
+      merge(kWarps);
       const float base = shfl_max(q.base, kWarps);
-      const float m = shfl_max(q.m, kWarps), d = q.m - shift_of(m);
-      q.s = shfl_sum(q.s * ex2(d * a.c), kWarps);
-      q.s1 = TWO ? shfl_sum(q.s1 * ex2(d * kLog2e), kWarps) : q.s;
-      q.m = m;
-      if (BUCKET) {
-        const float tm = shfl_max(q.tm, kWarps), td = q.tm - shift_of(tm);
-        q.ts = shfl_sum(q.ts * ex2(td * a.c), kWarps);
-        q.ts1 = TWO ? shfl_sum(q.ts1 * ex2(td * kLog2e), kWarps) : q.ts;
-        q.tm = tm;
-        q.b = shfl_sum(q.b, kWarps);
-        q.z = shfl_sum(q.z, kWarps);
-      } else {
-        const float bd = shift_of(q.base) - shift_of(base);
-        const float f = expf(bd);
-        q.b = shfl_sum(q.z == 0.0f ? 0.0f : f * (q.b + bd * q.zp), kWarps);
-        q.z = shfl_sum(q.z == 0.0f ? 0.0f : f * q.z, kWarps);
+      if (!BUCKET) {  // relative to the CTA's base
+        const float bd = shift_of(q.base) - shift_of(base), f = expf(bd);
+        q.b = q.z == 0.0f ? 0.0f : f * (q.b + bd * q.zp);
+        q.z = q.z == 0.0f ? 0.0f : f * q.z;
       }
-      q.base = base;
-      if (lane == 0) {
-        parts[turn][rank] = q;
-        warps[turn][0] = q;
-      }
+      q.b = shfl_sum(q.b, kWarps);
+      const float z = shfl_sum(q.z, kWarps);
       if (a.cluster > 1) {
+        if (lane == 0) {
+          warps[turn][0] = q;
+          parts[turn][rank] = q;
+        }
         __syncwarp();
         if (!met) cluster_wait();
         const float* from = reinterpret_cast<const float*>(&warps[turn][0]);
         const float* to = reinterpret_cast<const float*>(&parts[turn][rank]);
         for (int i = lane; i < a.cluster * kShared; i += 32)
           if (i / kShared != (int)rank) put_remote(to + i % kShared, (uint32_t)(i / kShared), from[i % kShared]);
+        cluster_arrive();
+        cluster_wait();
+        if (lane < a.cluster) q = parts[turn][lane];
+        merge(a.cluster);
+        q.b = shfl_sum(q.b, a.cluster);
       }
-    } else if (!met) {
+      if (lane == 0) {
+        // the teacher: q_i = exp(t_i - base) / rz, Q = sum q_i
+        const bool has = base != neg_inf() || z != z;
+        const float Q = BUCKET ? z : has ? 1.0f : 0.0f;
+        // the whole row: all = rest and listed
+        float M = q.m, S = q.s, S1 = q.s1;
+        if (BUCKET) join(M, S, S1, q.tm, q.ts, q.ts1, a.c);
+        const float sh = shift_of(M), shr = shift_of(q.m), sht = shift_of(q.tm);
+        const bool bucket = BUCKET && has && q.s > 0.0f;
+        const float qr = bucket ? fmaxf(0.0f, 1.0f - Q) : 0.0f;
+        if (g) {
+          Row r;
+          r.M = sh;
+          r.m = shr;
+          r.rS = rcp(S);
+          r.rS1 = rcp(S1);
+          r.A = has ? w_now * a.kd * a.tau : 0.0f;
+          r.C1 = y >= 0 ? w_now * a.ce : 0.0f;
+          r.Qr = Q + qr;
+          r.base = BUCKET ? tlse : shift_of(base);
+          r.rz = !has ? 0.0f : BUCKET ? 1.0f : rcp(z);
+          r.unused = 0.0f;
+          r.K1 = r.A * Q * r.rS;
+          r.K2 = r.C1 * r.rS1;
+          if (BUCKET) {
+            // (Q + q_rest) p_rest - q_rest is Q - p_listed, as Q + q_rest = 1
+            const float f = ex2((shr - sh) * a.c), f1 = ex2((shr - sh) * kLog2e);
+            const float top = q.ts * ex2((sht - sh) * a.c) * r.rS;
+            r.K1 = q.s > 0.0f ? r.A * (qr > 0.0f ? (Q - top) / q.s : Q * f * r.rS) : 0.0f;
+            r.K2 = q.s1 > 0.0f ? r.C1 * f1 * r.rS1 : 0.0f;
+          }
+          if (!TWO) r.K1 += r.K2;
+          rows[turn] = r;
+        }
+        if (a.loss && rank == 0) {  // its logarithms are taken after the others have gone on
+          ls = {sh, shr, S, S1, z, Q, qr, has, q.ts / q.s * ex2((sht - shr) * a.c), q.s, q.b};
+        }
+      }
+    } else if (a.cluster > 1) {
+      if (!met) cluster_wait();
+      cluster_arrive();
       cluster_wait();
     }
     met = true;
-    if (a.cluster > 1) {
-      cluster_arrive();
-      cluster_wait();
-    } else {
-      __syncthreads();
-    }
-    Part t = parts[turn][0];
-    for (int i = 1; i < a.cluster; i++) {
-      const Part p = parts[turn][i];
-      join(t.m, t.s, t.s1, p.m, p.s, p.s1, a.c);
-      if (BUCKET) join(t.tm, t.ts, t.ts1, p.tm, p.ts, p.ts1, a.c);
-      t.b += p.b;
-    }
-    t.z = parts[turn][rank].z;
-    t.base = parts[turn][rank].base;
-    turn ^= 1;
-    // the teacher: q_i = exp(t_i - lt), Q = sum q_i
-    const bool has = t.base != neg_inf() || t.z != t.z;
-    const float lt = BUCKET ? tlse : shift_of(t.base) + logf(t.z);
-    const float Q = BUCKET ? t.z : has ? 1.0f : 0.0f;
-    // the whole row: all = rest and listed
-    float M = t.m, S = t.s, S1 = t.s1;
-    if (BUCKET) join(M, S, S1, t.tm, t.ts, t.ts1, a.c);
-    const float sh = shift_of(M), shr = shift_of(t.m);
-    const bool bucket = BUCKET && has && t.s > 0.0f;
-    const float qr = bucket ? fmaxf(0.0f, 1.0f - Q) : 0.0f;
+    if (g) __syncthreads();
     if (a.loss && tid == 0 && rank == 0) {
-      const float L = sh / a.tau + logf(S);
+      const float L = ls.sh * inv_tau + logf(ls.S);
       float l = 0.0f;
-      if (has) {  // sum q_i (t_i - lt - s_i) + L sum q_i
-        float kl = BUCKET ? t.b + Q * L : t.b / t.z + (L - logf(t.z));
-        if (qr > 0.0f) {  // log q_rest - log p_rest, both from what is listed
-          const float odds = t.ts / t.s * ex2((shift_of(t.tm) - shr) * a.c);
-          const float logp = odds < 1.0f ? log1pf(odds) : L - (shr / a.tau + logf(t.s));
-          kl += qr * (log1pf(-Q) + logp);
+      if (ls.has) {  // sum q_i (t_i - log z - base - s_i) + L sum q_i
+        float kl = BUCKET ? ls.b + ls.Q * L : ls.b / ls.z + (L - logf(ls.z));
+        if (ls.qr > 0.0f) {  // log q_rest - log p_rest, both from what is listed
+          const float logp = ls.odds < 1.0f ? log1pf(ls.odds) : L - (ls.shr * inv_tau + logf(ls.s));
+          kl += ls.qr * (log1pf(-ls.Q) + logp);
         }
         l = a.kd * a.tau * a.tau * kl;
       }
-      if (y >= 0) l += a.ce * (sh + logf(S1) - xy);
+      if (y >= 0) l += a.ce * (ls.sh + logf(ls.S1) - xy);
       a.loss[row] = w_now * l;
     }
-    if (!g) {
-      if (w != 0.0f) fetch_ragged(at);
-      continue;
-    }
-    // gradient = K1 2^((x - m) c) + K2 2^((x - m) log2 e), m the maximum of
-    // what the buffer holds; the listed coordinates and the label after that
-    const float A = has ? w_now * a.kd * a.tau : 0.0f, C1 = y >= 0 ? w_now * a.ce : 0.0f;
-    float K1 = A * Q / S, K2 = C1 / S1;
-    if (BUCKET) {
-      const float pr = t.s * ex2((shr - sh) * a.c) / S;
-      const float pr1 = t.s1 * ex2((shr - sh) * kLog2e) / S1;
-      const float ptop = t.ts * ex2((shift_of(t.tm) - sh) * a.c) / S;
-      const float d = qr > 0.0f ? Q - ptop : Q * pr;  // (Q + q_rest) p_rest - q_rest; Q + q_rest = 1
-      K1 = t.s > 0.0f ? A * d / t.s : 0.0f;
-      K2 = t.s1 > 0.0f ? C1 * pr1 / t.s1 : 0.0f;
-    }
-    if (!TWO) K1 += K2;
-    const uint64_t c2 = pair(a.c, a.c), mc = pair(-shr * a.c, -shr * a.c), k1 = pair(K1, K1);
-    const uint64_t l2 = pair(kLog2e, kLog2e), ml = pair(-shr * kLog2e, -shr * kLog2e);
-    const uint64_t k2 = pair(K2, K2);
-    auto grad_of = [&](uint64_t x) {
-      uint64_t v = mul2(k1, ex2_2(fma2(x, c2, mc)));
-      if (TWO) v = fma2(k2, ex2_2(fma2(x, l2, ml)), v);
-      return v;
-    };
-#pragma unroll 2
-    for (int i = tid; i < here; i += NT) {
-      float x[EPV];
-      E::unpack(buf[i], x);
-      fetch(at, i);
+    if (g) {
+      const Row t = rows[turn];
+      const pair_t mc = pair(-t.m * a.c, -t.m * a.c), ml = pair(-t.m * kLog2e, -t.m * kLog2e);
+      const pair_t k1 = pair(t.K1, t.K1), k2 = pair(t.K2, t.K2);
+      auto grad_of = [&](pair_t x) {
+        pair_t v = mul2(k1, ex2_2(fma2(x, c2, mc)));
+        if (TWO) v = fma2(k2, ex2_2(fma2(x, l2, ml)), v);
+        return v;
+      };
+#pragma unroll 1
+      for (int u0 = 0; u0 * NT < here; u0 += BLK) {
+        uint4 r[BLK];
+        read(u0, r);
+        fetch(at, u0);
 #pragma unroll
-      for (int j = 0; j < EPV; j += 2) {
-        const float2 f = unpair(grad_of(pair(x[j], x[j + 1])));
-        x[j] = f.x;
-        x[j + 1] = f.y;
+        for (int u = 0; u < BLK; u++) {
+          float x[EPV];
+          E::unpack(r[u], x);
+#pragma unroll
+          for (int j = 0; j < EPV; j += 2) {
+            const pair_t f = grad_of(pair(x[j], x[j + 1]));
+            x[j] = f.x;
+            x[j + 1] = f.y;
+          }
+          r[u] = E::pack(x);
+        }
+        store(u0, r);
       }
-      store(i, E::pack(x));
-    }
-    if (w != 0.0f) fetch_ragged(at);
-    const int64_t ly = y - now.e0;
-    const bool y_here = y >= 0 && ly >= 0 && ly < (int64_t)here * EPV;
-    bool y_listed = false;
+      const int ly = y - now.e0;
+      const bool y_here = y >= 0 && ly >= 0 && ly < here * EPV;
+      bool y_listed = false;
 #pragma unroll
-    for (int h = 0; h < kEnt; h++) y_listed |= y_here && el[h] == ly;
-    y_listed = __syncthreads_or(y_listed);
+      for (int h = 0; h < ENT; h++) y_listed |= y_here && el[h] == ly;
+      y_listed = __syncthreads_or(y_listed);
 #pragma unroll
-    for (int h = 0; h < kEnt; h++) {
-      if (el[h] < 0) continue;
-      const float d = ex[h] - sh, u = has ? expf(et[h] - lt) : 0.0f;
-      float v = A * ((Q + qr) * ex2(d * a.c) / S - u);
-      if (y >= 0) v += C1 * ex2(d * kLog2e) / S1;
-      if (y_here && el[h] == ly) v -= C1;
-      g[el[h]] = E::make(v);
+      for (int h = 0; h < ENT; h++) {
+        if (el[h] < 0) continue;
+        const float d = ex[h] - t.M;
+        float v = t.A * (t.Qr * ex2(d * a.c) * t.rS - expf(et[h] - t.base) * t.rz);
+        v += t.C1 * ex2(d * kLog2e) * t.rS1;
+        if (y_here && el[h] == ly) v -= t.C1;
+        g[el[h]] = E::make(v);
+      }
+      if (y_here && !y_listed && tid == 0) g[ly] = E::make(grad_of(pair(xy, xy)).x - t.C1);
     }
-    if (y_here && !y_listed && tid == 0) g[ly] = E::make(unpair(grad_of(pair(xy, xy))).x - C1);
+    // a part may be shorter in this row than in the next one (by where the rows
+    // start): what the pass above did not reach
+    for (int u0 = (here + BLK * NT - 1) / (BLK * NT) * BLK; u0 * NT < at.hi; u0 += BLK) fetch(at, u0);
+    fetch_ragged(at);
+    turn ^= 1;
   }
   if (!met) cluster_wait();
 }
@@ -703,8 +804,9 @@ cudaError_t launch_distill(DistillArgs& a, cudaStream_t s) {
     while (a.cluster < 8 && a.rows * a.cluster * 2 <= num_sms() && nv > Narrow::NT * 2 * a.cluster)
       a.cluster *= 2;
     a.part_vecs = (int)((nv + a.cluster - 1) / a.cluster);
-    const bool narrow = a.part_vecs <= Narrow::PART && a.k <= Narrow::NT * kEnt;
-    e = narrow ? launch_sized<DT, Narrow>(a, s) : launch_sized<DT, Wide>(a, s);
+    if (a.part_vecs <= Narrow::PART && a.k <= Narrow::MAXK) e = launch_sized<DT, Narrow>(a, s);
+    else if (a.k <= Wide::MAXK) e = launch_sized<DT, Wide>(a, s);
+    else e = launch_sized<DT, Deep>(a, s);
   }
   const cudaError_t last = cudaGetLastError();
   return e != cudaSuccess ? e : last;

@@ -34,36 +34,20 @@ __device__ __forceinline__ uint4 ld_row_u4(const void* p) {
   return r;
 }
 
-// Pairs of fp32 in one register pair: one instruction for two operations.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
+// 1 / x, off by at most one unit in the last place.
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t ex2_2(uint64_t v) {
-  const float2 f = unpair(v);
-  return pair(ex2(f.x), ex2(f.y));
-}
+
+// Two fp32 values: one instruction for two operations.
+using pair_t = float2;
+__device__ __forceinline__ pair_t pair(float a, float b) { return make_float2(a, b); }
+__device__ __forceinline__ pair_t fma2(pair_t a, pair_t b, pair_t c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ pair_t add2(pair_t a, pair_t b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ pair_t mul2(pair_t a, pair_t b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ pair_t ex2_2(pair_t v) { return pair(ex2(v.x), ex2(v.y)); }
 
 // Asynchronous 16-byte copy to shared memory.  A thread that reads back only
 // what it copied itself needs no barrier, only its own wait.
