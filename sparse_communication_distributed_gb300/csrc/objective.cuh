@@ -143,6 +143,38 @@ struct Elem<SCAPE_F32> {
   }
 };
 
+// Whether all elements of a vector are below a bound of the same type (NaN is
+// not; the bound comes in both halves of a word for 16-bit elements).
+template <int DT>
+__device__ __forceinline__ bool all_below(const uint4 v, uint32_t bound) {
+  if constexpr (DT == SCAPE_BF16) {
+    auto h = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
+    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(h(v.x), h(v.y)), __hmax2_nan(h(v.z), h(v.w)));
+    return __hblt2(m, h(bound));
+  } else if constexpr (DT == SCAPE_F16) {
+    auto h = [](uint32_t x) { return *reinterpret_cast<const __half2*>(&x); };
+    const __half2 m = __hmax2_nan(__hmax2_nan(h(v.x), h(v.y)), __hmax2_nan(h(v.z), h(v.w)));
+    return __hblt2(m, h(bound));
+  } else {
+    const float b = __uint_as_float(bound);
+    return __uint_as_float(v.x) < b && __uint_as_float(v.y) < b && __uint_as_float(v.z) < b &&
+           __uint_as_float(v.w) < b;
+  }
+}
+// The largest element not above f, as all_below() takes it.
+template <int DT>
+__device__ __forceinline__ uint32_t bound_of(float f) {
+  if constexpr (DT == SCAPE_BF16) {
+    const uint32_t h = __bfloat16_as_ushort(__float2bfloat16_rd(f));
+    return h << 16 | h;
+  } else if constexpr (DT == SCAPE_F16) {
+    const uint32_t h = __half_as_ushort(__float2half_rd(f));
+    return h << 16 | h;
+  } else {
+    return __float_as_uint(f);
+  }
+}
+
 // Element by element the larger one of two vectors (NaN loses).
 template <int DT>
 __device__ __forceinline__ uint4 max_vec(const uint4 a, const uint4 b) {
