@@ -2,14 +2,20 @@
 // choices every expert of every group of tokens got, the balance loss and the z
 // loss; and the gradient of the logits.
 //
-// Forward.  A token's logits lie across L lanes of a warp (L a power of two, 8
-// columns a lane, more for over 256 experts).  The tokens are cut into chunks,
-// one CTA each; within a chunk the CTA goes group by group and leaves, for every
-// group that the chunk touches, the sums of p and the counts over its tokens in
-// a slot of the workspace.  Chunk i and group g use slot i + g: along the
-// tokens either i or g moves on, so no two pairs share a slot and a group's
-// slots are adjacent.  A second kernel adds a group's slots up in order, so the
-// sums do not depend on the schedule.
+// Forward.  A token's logits lie across L lanes of a warp, so that a warp works
+// on 32 / L tokens at once (L = 8 for 33 to 256 experts).  The choice goes the
+// way of the top logits: of each of at least 32 groups of experts (or of each
+// expert) the largest logit is known, the k-th largest of those is a bound that
+// at least k experts reach, and only the few that do are put into a list and
+// ranked by comparing each with each.  Rows with too many of them (many equal
+// logits) are done one choice after the other.
+//
+// The tokens are cut into chunks, one CTA each; within a chunk the CTA goes group
+// by group and leaves, for every group that the chunk touches, the sums of p and
+// the counts over its tokens in a slot of the workspace.  Chunk i and group g
+// use slot i + g: along the tokens either i or g moves on, so no two pairs share
+// a slot and a group's slots are adjacent.  A second kernel adds a group's slots
+// up in order, so the sums do not depend on the schedule.
 //
 // Backward.  With d_e = dB / G' * E c_ge / (k T_g^2) of the token's group,
 //   d x_j = p_j (d_j - sum_e p_e d_e) + (2 dZ / T) lse p_j + (weights' part),
@@ -35,7 +41,8 @@ constexpr int kMaxExperts = 1024;
 struct RouteArgs {
   const void* x;
   int64_t T, stride;
-  int E, k, L, renorm;  // L: lanes of a token
+  int E, k, renorm;
+  bool vec, gvec;  // rows of the logits, of the gradient in whole 16-byte vectors
   const int32_t* cu;
   int64_t G;
   const uint8_t* valid;
@@ -49,6 +56,7 @@ struct RouteArgs {
   float* part_z;       // slots: sum of lse^2
   uint32_t* done;      // CTAs of the second kernel that have finished
   float* part_b;       // groups x column blocks of the second kernel
+  float* group_z;      // groups: sum of lse^2
   int32_t* counts;
   int32_t* live;
   float* losses;
@@ -80,62 +88,91 @@ __device__ __forceinline__ int64_t group_at(const RouteArgs& a, int64_t t) {
   return lo;
 }
 
-template <class F>
-__device__ __forceinline__ float lanes_reduce(float x, int L, F f) {
-  for (int o = L >> 1; o; o >>= 1) x = f(x, __shfl_xor_sync(kFull, x, o));
+template <int L>
+__device__ __forceinline__ float lanes_sum(float x) {
+#pragma unroll
+  for (int o = L >> 1; o; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
   return x;
 }
-__device__ __forceinline__ float lanes_sum(float x, int L) {
-  return lanes_reduce(x, L, [](float a, float b) { return a + b; });
-}
-__device__ __forceinline__ float lanes_max(float x, int L) {
-  return lanes_reduce(x, L, [](float a, float b) { return fmaxf(a, b); });
-}
-
-// The columns of a lane: column 8 (c L + sub) + j is its value 8 c + j.
-template <int VPL>
-__device__ __forceinline__ int col_of(int L, int sub, int j) {
-  return ((j >> 3) * L + sub) * 8 + (j & 7);
+template <int L>
+__device__ __forceinline__ float lanes_max(float x) {
+#pragma unroll
+  for (int o = L >> 1; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+  return x;
 }
 
-// A lane's logits of token t, -inf beyond the experts.
-template <int DT, int VPL, bool VEC>
-__device__ __forceinline__ void load_row(const void* base, int64_t t, int64_t stride, int Ex, int L,
-                                         int sub, bool in, float (&x)[VPL]) {
-  using E = Elem<DT>;
-  const typename E::T* p = static_cast<const typename E::T*>(base) + t * stride;
+// How a token's experts lie in a warp: L lanes, VPL values each, in vectors of
+// 16 bytes that follow each other over the lanes.  GPL groups of a lane's values
+// for the bound.
+template <int L_, int VPL_, int GPL_>
+struct Lanes {
+  static constexpr int L = L_, VPL = VPL_, GPL = GPL_, ROWS = 32 / L_;
+  static constexpr int CAP = L_ * VPL_ < 48 ? L_ * VPL_ : 48;  // list entries of a token
+};
+
+template <int DT, int L>
+__device__ __forceinline__ int col_of(int sub, int j) {
+  constexpr int N = Elem<DT>::kPerVec;
+  return (j / N * L + sub) * N + j % N;
+}
+
+// A lane's logits of one token as they lie in memory, -inf beyond the experts.
+// VEC: rows on 16-byte boundaries and whole vectors.
+template <int DT, class LN>
+struct RowRegs {
+  static constexpr int N = Elem<DT>::kPerVec, VECS = LN::VPL / N;
+  uint4 r[VECS];
+  __device__ __forceinline__ void load(const typename Elem<DT>::T* p, int E, int sub, bool in, bool vec) {
 #pragma unroll
-  for (int c = 0; c < VPL / 8; c++) {
-    const int col = (c * L + sub) * 8;
-    if (VEC) {
-      constexpr int N = 8 / E::kPerVec;
+    for (int v = 0; v < VECS; v++) {
+      const int col = (v * LN::L + sub) * N;
+      r[v] = neg_inf_vec<DT>();
+      if (!in || col >= E) continue;
+      if (vec) {
+        r[v] = ld_row_u4(p + col);
+      } else {
+        float f[N];
 #pragma unroll
-      for (int h = 0; h < N; h++) {
-        float f[E::kPerVec];
-        const uint4 ninf = make_uint4(E::kNegInf2, E::kNegInf2, E::kNegInf2, E::kNegInf2);
-        E::unpack(in && col < Ex ? ld_row_u4(p + col + h * E::kPerVec) : ninf, f);
-#pragma unroll
-        for (int j = 0; j < E::kPerVec; j++) x[c * 8 + h * E::kPerVec + j] = f[j];
+        for (int j = 0; j < N; j++) f[j] = col + j < E ? Elem<DT>::load(p + col + j) : neg_inf();
+        r[v] = Elem<DT>::pack(f);
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; j++) x[c * 8 + j] = in && col + j < Ex ? E::load(p + col + j) : neg_inf();
     }
   }
+  __device__ __forceinline__ void get(float (&x)[LN::VPL]) const {
+#pragma unroll
+    for (int v = 0; v < VECS; v++) {
+      float f[N];
+      Elem<DT>::unpack(r[v], f);
+#pragma unroll
+      for (int j = 0; j < N; j++) x[v * N + j] = f[j];
+    }
+  }
+};
+
+__device__ __forceinline__ float value_of_key(uint32_t k) {
+  return k == 0xFFFFFFFFu ? __uint_as_float(0x7FFFFFFFu)
+                          : __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
 
-template <int DT, int VPL, bool VEC>
-__global__ __launch_bounds__(kThreads) void route_chunks(const RouteArgs a) {
-  extern __shared__ unsigned char smem[];
-  const int L = a.L, per_warp = 32 / L;
-  float* sp = reinterpret_cast<float*>(smem);                   // kWarps x E
-  int32_t* sc = reinterpret_cast<int32_t*>(sp + kWarps * a.E);  // E
-  float* sw = reinterpret_cast<float*>(sc + a.E);               // tokens of a round x k
-  int32_t* si = reinterpret_cast<int32_t*>(sw + kWarps * per_warp * a.k);
+template <int DT, class LN>
+__global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
+  using E = Elem<DT>;
+  using T = typename E::T;
+  constexpr int L = LN::L, VPL = LN::VPL, GPL = LN::GPL, ROWS = LN::ROWS, CAP = LN::CAP;
+  extern __shared__ __align__(16) unsigned char smem[];
+  uint64_t* lists = reinterpret_cast<uint64_t*>(smem);  // kWarps x ROWS x CAP
+  uint64_t* ranks = lists + kWarps * ROWS * CAP;                      // kWarps x ROWS x k
+  int* n_cand = reinterpret_cast<int*>(ranks + kWarps * ROWS * a.k);  // kWarps x ROWS
+  float* sp = reinterpret_cast<float*>(n_cand + kWarps * ROWS);       // kWarps x E
+  int32_t* sc = reinterpret_cast<int32_t*>(sp + kWarps * a.E);        // E
   __shared__ float fbuf[32];
   __shared__ int32_t ibuf[32];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int sub = lane & (L - 1), slot = lane / L;
+  const unsigned seg = (L == 32 ? kFull : ((1u << L) - 1u) << (slot * L));  // this token's lanes
+  uint64_t* list = lists + (wid * ROWS + slot) * CAP;
+  uint64_t* sorted = ranks + (wid * ROWS + slot) * a.k;
+  int* n_mine = n_cand + wid * ROWS + slot;
   const int64_t t0 = (int64_t)blockIdx.x * a.chunk, t1 = min(t0 + a.chunk, a.T);
   if (blockIdx.x == 0 && tid == 0) *a.done = 0;
 
@@ -163,99 +200,149 @@ __global__ __launch_bounds__(kThreads) void route_chunks(const RouteArgs a) {
     int32_t nlive = 0;
     for (int i = tid; i < a.E; i += kThreads) sc[i] = 0;
     __syncthreads();
-    for (int64_t r = at; r < end; r += kWarps * per_warp) {
-      const int64_t t = r + wid * per_warp + slot;
+    RowRegs<DT, LN> next;
+    int64_t t = at + wid * ROWS + slot;
+    next.load(static_cast<const T*>(a.x) + t * a.stride, a.E, sub, t < end, a.vec);
+    for (int64_t r = at + wid * ROWS; r < end; r += kWarps * ROWS, t += kWarps * ROWS) {
       const bool in = t < end;
+      const T* p_row = static_cast<const T*>(a.x) + t * a.stride;
       float x[VPL];
-      load_row<DT, VPL, VEC>(a.x, t, a.stride, a.E, L, sub, in, x);
+      next.get(x);
+      next.load(p_row + kWarps * ROWS * a.stride, a.E, sub, t + kWarps * ROWS < end, a.vec);
       bool ok = in && inside && (!a.valid || a.valid[t] != 0);
-      float m = neg_inf();
-      bool nan = false;
+      float gm[GPL];
 #pragma unroll
-      for (int j = 0; j < VPL; j++) {
-        m = fmaxf(m, x[j]);
-        nan |= x[j] != x[j];
-      }
-      m = lanes_max(m, L);
-      nan = lanes_max(nan ? 1.0f : 0.0f, L) != 0.0f;
-      ok = ok && (m > neg_inf() || nan);
+      for (int j = 0; j < GPL; j++) gm[j] = x[j];
+#pragma unroll
+      for (int j = GPL; j < VPL; j++) gm[j % GPL] = fmaxf(gm[j % GPL], x[j]);
+      float m = gm[0];
+#pragma unroll
+      for (int j = 1; j < GPL; j++) m = fmaxf(m, gm[j]);
+      m = lanes_max<L>(m);
       const float sh = shift_of(m);
-      float p[VPL], s = 0.0f;
+
+      // the bound: the k-th largest of the groups' largest
+      float bound = neg_inf();
+      for (int i = 0; i < a.k; i++) {
+        float h = gm[0];
 #pragma unroll
-      for (int j = 0; j < VPL; j++) {
-        p[j] = ex2((x[j] - sh) * kLog2e);
-        s += p[j];
+        for (int j = 1; j < GPL; j++) h = fmaxf(h, gm[j]);
+        bound = lanes_max<L>(h);
+        // one of those that are equal to it is taken out
+        const unsigned who = __ballot_sync(kFull, h == bound) & seg;
+        bool mine = lane == __ffs(who) - 1;
+#pragma unroll
+        for (int j = 0; j < GPL; j++) {
+          const bool hit = mine && gm[j] == bound;
+          gm[j] = hit ? neg_inf() : gm[j];
+          mine = mine && !hit;
+        }
       }
-      s = lanes_sum(s, L);
-      const float lse = sh + logf(s), inv = 1.0f / s;
+      // the experts that reach it
+      uint32_t cand = 0;
+#pragma unroll
+      for (int j = 0; j < VPL; j++)
+        if (!(x[j] < bound)) cand |= 1u << j;
+
+      // p, and the sums
+      const pair_t c2 = pair(kLog2e, kLog2e), mc = pair(-sh * kLog2e, -sh * kLog2e);
+      pair_t s2 = pair(0.0f, 0.0f);
+#pragma unroll
+      for (int j = 0; j < VPL; j += 2) {
+        const pair_t e = ex2_2(fma2(pair(x[j], x[j + 1]), c2, mc));
+        s2 = add2(s2, e);
+        x[j] = e.x;
+        x[j + 1] = e.y;
+      }
+      const float s = lanes_sum<L>(s2.x + s2.y);
+      const float inv = 1.0f / s;
+      ok = ok && !(s == 0.0f);  // some logit above -inf
+      const float lse = sh + logf(s);
       if (ok) {
 #pragma unroll
-        for (int j = 0; j < VPL; j++) acc[j] += p[j] * inv;
+        for (int j = 0; j < VPL; j++) acc[j] = fmaf(x[j], inv, acc[j]);
         if (sub == 0) {
           zsum += lse * lse;
           nlive++;
         }
+      } else {
+        cand = 0;
       }
-      // the k best, one after the other
-      uint32_t key[VPL];
-#pragma unroll
-      for (int j = 0; j < VPL; j++)
-        key[j] = col_of<VPL>(L, sub, j) < a.E ? order_key(x[j]) : 0u;
-      const int base = (wid * per_warp + slot) * a.k;
-      float sel = 0.0f, top = 0.0f;
-      for (int i = 0; i < a.k; i++) {
-        uint64_t best = 0;
+
+      if (sub == 0) *n_mine = 0;
+      __syncwarp();
+      while (cand) {
+        const int j = __ffs(cand) - 1;
+        cand &= cand - 1;
+        const int col = col_of<DT, L>(sub, j);
+        if (col >= a.E) continue;
+        const int n = atomicAdd(n_mine, 1);
+        if (n < CAP) list[n] = (uint64_t)order_key(E::load(p_row + col)) << 32 | (uint32_t)~col;
+      }
+      __syncwarp();
+      const int n = *n_mine;
+      if (__any_sync(kFull, n > CAP)) {
+        // one choice after the other, all logits read again
+        uint32_t key[VPL];
+        const bool all = in && ok;
 #pragma unroll
         for (int j = 0; j < VPL; j++) {
-          const uint64_t v = (uint64_t)key[j] << 32 | (uint32_t)~col_of<VPL>(L, sub, j);
-          best = v > best && key[j] ? v : best;
+          const int col = col_of<DT, L>(sub, j);
+          key[j] = all && col < a.E ? order_key(E::load(p_row + col)) : 0u;
         }
-        for (int o = L >> 1; o; o >>= 1) {
-          const uint64_t other = __shfl_xor_sync(kFull, best, o);
-          best = other > best ? other : best;
-        }
-        const int col = (int)~(uint32_t)best;
-        const uint32_t kb = (uint32_t)(best >> 32);
-        const float v = kb == 0xFFFFFFFFu ? __uint_as_float(0x7FFFFFFFu)
-                        : __uint_as_float((kb & 0x80000000u) ? kb & 0x7FFFFFFFu : ~kb);
+        for (int i = 0; i < a.k; i++) {
+          uint64_t best = 0;
 #pragma unroll
-        for (int j = 0; j < VPL; j++)
-          if (col_of<VPL>(L, sub, j) == col) key[j] = 0;
-        if (i == 0) top = shift_of(v);
-        const float e = a.renorm ? ex2((v - top) * kLog2e) : ex2((v - sh) * kLog2e) * inv;
-        sel += e;
-        if (sub == 0) {
-          sw[base + i] = e;
-          si[base + i] = ok ? col : -1;
-          if (ok) atomicAdd(&sc[col], 1);
+          for (int j = 0; j < VPL; j++) {
+            const uint64_t v = (uint64_t)key[j] << 32 | (uint32_t)~col_of<DT, L>(sub, j);
+            best = v > best && key[j] ? v : best;
+          }
+#pragma unroll
+          for (int o = L >> 1; o; o >>= 1) {
+            const uint64_t other = __shfl_xor_sync(kFull, best, o);
+            best = other > best ? other : best;
+          }
+          const int col = (int)~(uint32_t)best;
+#pragma unroll
+          for (int j = 0; j < VPL; j++)
+            if (col_of<DT, L>(sub, j) == col) key[j] = 0;
+          if (sub == 0) sorted[i] = best;
+        }
+      } else {
+        // ranked: each entry counts those above it
+        for (int i = sub; i < n; i += L) {
+          const uint64_t v = list[i];
+          int above = 0;
+          for (int q = 0; q < n; q++) above += list[q] > v;
+          if (above < a.k) sorted[above] = v;
         }
       }
       __syncwarp();
-      const float scale = a.renorm ? 1.0f / sel : 1.0f;
-      const int64_t left = end - (r + wid * per_warp);
-      const int n = (int)(left < per_warp ? left : per_warp) * a.k;
-      // one value of the token's scale for each lane that writes it
-      for (int i = 0; i < per_warp * a.k; i += 32) {
-        const int q = i + lane, tok = q < per_warp * a.k ? q / a.k : 0;
-        const float sc_ = __shfl_sync(kFull, scale, tok * L);
-        if (q < n) {
-          const int32_t e = si[wid * per_warp * a.k + q];
-          const int64_t o = (r + wid * per_warp) * a.k + q;
-          a.idx[o] = e;
-          a.weights[o] = e < 0 ? 0.0f : sw[wid * per_warp * a.k + q] * sc_;
+      float chosen = 0.0f;
+      if (a.renorm && ok)
+        for (int i = sub; i < a.k; i += L)
+          chosen += ex2((value_of_key((uint32_t)(sorted[i] >> 32)) - sh) * kLog2e);
+      const float scale = a.renorm ? 1.0f / lanes_sum<L>(chosen) : inv;
+      if (in)
+        for (int i = sub; i < a.k; i += L) {
+          const uint64_t v = ok ? sorted[i] : 0;
+          const int col = (int)~(uint32_t)v;  // -1 for v = 0
+          a.idx[t * a.k + i] = col;
+          a.weights[t * a.k + i] = ok ? ex2((value_of_key((uint32_t)(v >> 32)) - sh) * kLog2e) * scale : 0.0f;
+          if (ok) atomicAdd(&sc[col], 1);
         }
-      }
       __syncwarp();
     }
     if (inside) {  // the slot of this chunk and group
 #pragma unroll
       for (int j = 0; j < VPL; j++) {
+#pragma unroll
         for (int o = L; o < 32; o <<= 1) acc[j] += __shfl_xor_sync(kFull, acc[j], o);
-        const int col = col_of<VPL>(L, sub, j);
+        const int col = col_of<DT, L>(sub, j);
         if (slot == 0 && col < a.E) sp[wid * a.E + col] = acc[j];
       }
       const float z = cta_sum(zsum, fbuf);
-      const int32_t n = cta_sum(nlive, ibuf);
+      const int32_t nl = cta_sum(nlive, ibuf);
       __syncthreads();
       const int64_t sl = blockIdx.x + g;
       for (int i = tid; i < a.E; i += kThreads) {
@@ -265,7 +352,7 @@ __global__ __launch_bounds__(kThreads) void route_chunks(const RouteArgs a) {
         a.part_c[sl * a.E + i] = sc[i];
       }
       if (tid == 0) {
-        a.part_n[sl] = n;
+        a.part_n[sl] = nl;
         a.part_z[sl] = z;
       }
     }
@@ -289,8 +376,13 @@ __global__ __launch_bounds__(kThreads) void route_finish(const RouteArgs a) {
   const int64_t lo = bound_of(a, g), hi = bound_of(a, g + 1);
   const int64_t s0 = lo / a.chunk + g, s1 = hi > lo ? (hi - 1) / a.chunk + g + 1 : s0;
   int32_t n = 0;
-  for (int64_t s = s0 + tid; s < s1; s += kThreads) n += a.part_n[s];
+  float zg = 0.0f;
+  for (int64_t s = s0 + tid; s < s1; s += kThreads) {
+    n += a.part_n[s];
+    zg += a.part_z[s];
+  }
   n = cta_sum(n, ibuf);
+  zg = cta_sum(zg, fbuf);
   const int col = blockIdx.y * kCols + (tid >> 3);
   float p = 0.0f;
   int32_t c = 0;
@@ -309,7 +401,10 @@ __global__ __launch_bounds__(kThreads) void route_finish(const RouteArgs a) {
   const float bal = cta_sum(b, fbuf) * ((float)a.E / ((float)a.k * tg)) / tg;
   if (tid == 0) {
     a.part_b[g * nb + blockIdx.y] = bal;
-    if (blockIdx.y == 0) a.live[g] = n;
+    if (blockIdx.y == 0) {
+      a.live[g] = n;
+      a.group_z[g] = zg;
+    }
     __threadfence();
     last = atomicAdd(a.done, 1u) == gridDim.x * gridDim.y - 1;
   }
@@ -323,9 +418,7 @@ __global__ __launch_bounds__(kThreads) void route_finish(const RouteArgs a) {
     const int32_t v = __ldcg(a.live + i);
     total += v;
     groups += v > 0;
-    const int64_t lo2 = bound_of(a, i), hi2 = bound_of(a, i + 1);
-    if (hi2 > lo2)
-      for (int64_t s = lo2 / a.chunk + i; s <= (hi2 - 1) / a.chunk + i; s++) z += a.part_z[s];
+    z += __ldcg(a.group_z + i);
   }
   sum = cta_sum(sum, fbuf);
   z = cta_sum(z, fbuf);
@@ -339,82 +432,106 @@ __global__ __launch_bounds__(kThreads) void route_finish(const RouteArgs a) {
   }
 }
 
-template <int DT, int VPL, bool VEC>
-__global__ __launch_bounds__(kThreads) void route_grad(const RouteArgs a) {
+template <int DT, class LN>
+__global__ __launch_bounds__(kThreads, 2) void route_grad(const RouteArgs a) {
   using E = Elem<DT>;
   using T = typename E::T;
-  const int L = a.L, per_warp = 32 / L;
+  constexpr int L = LN::L, VPL = LN::VPL, ROWS = LN::ROWS, N = E::kPerVec;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int sub = lane & (L - 1), slot = lane / L;
   const int64_t t0 = (int64_t)blockIdx.x * a.chunk, t1 = min(t0 + a.chunk, a.T);
   const float dB = a.dl ? a.dl[0] : 0.0f, dZ = a.dl ? a.dl[1] : 0.0f;
   const float zc = 2.0f * dZ / (float)max(a.blive[a.G], 1);
   const float bc = dB / (float)max(a.blive[a.G + 1], 1) * ((float)a.E / (float)a.k);
-  for (int64_t r = t0; r < t1; r += kWarps * per_warp) {
-    const int64_t t = r + wid * per_warp + slot;
+  int64_t t = t0 + wid * ROWS + slot;
+  RowRegs<DT, LN> next;
+  next.load(static_cast<const T*>(a.x) + t * a.stride, a.E, sub, t < t1, a.vec);
+  // this token's group: its end, and d of this lane's experts
+  int64_t g_end = t0;
+  const int32_t* gc = nullptr;
+  float coef = 0.0f, d[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; j++) d[j] = 0.0f;
+  for (int64_t r = t0 + wid * ROWS; r < t1; r += kWarps * ROWS, t += kWarps * ROWS) {
     const bool in = t < t1;
-    float x[VPL], y[VPL];
-    load_row<DT, VPL, VEC>(a.x, t, a.stride, a.E, L, sub, in, x);
+    const T* p_row = static_cast<const T*>(a.x) + t * a.stride;
+    float x[VPL];
+    next.get(x);
+    next.load(p_row + kWarps * ROWS * a.stride, a.E, sub, t + kWarps * ROWS < t1, a.vec);
+    // the first of the chosen tells whether the token is live
     const bool ok = in && a.bidx[t * a.k] >= 0;
-    const int64_t g = in ? group_at(a, t) : 0;
-    float m = neg_inf();
+    if (in && t >= g_end) {
+      const int64_t g = group_at(a, t);
+      g_end = g < a.G ? bound_of(a, g + 1) : a.T;
+      gc = g < a.G ? a.bcounts + g * a.E : nullptr;
+      const float tg = gc ? (float)max(a.blive[g], 1) : 1.0f;
+      coef = bc / tg / tg;
 #pragma unroll
-    for (int j = 0; j < VPL; j++) m = fmaxf(m, x[j]);
-    m = shift_of(lanes_max(m, L));
-    float s = 0.0f, pd = 0.0f;
-    float tg = 1.0f;
-    if (ok && g < a.G) tg = (float)max(a.blive[g], 1);
-    const float coef = bc / tg / tg;
-#pragma unroll
-    for (int j = 0; j < VPL; j++) {
-      const int col = col_of<VPL>(L, sub, j);
-      x[j] = ex2((x[j] - m) * kLog2e);
-      s += x[j];
-      y[j] = ok && g < a.G && col < a.E ? coef * (float)a.bcounts[g * a.E + col] : 0.0f;
-      pd += x[j] * y[j];
+      for (int j = 0; j < VPL; j++) {
+        const int col = col_of<DT, L>(sub, j);
+        d[j] = gc && col < a.E ? coef * (float)gc[col] : 0.0f;
+      }
     }
-    s = lanes_sum(s, L);
-    pd = lanes_sum(pd, L);
-    const float inv = 1.0f / s, lse = m + logf(s);
-    pd = pd * inv - zc * lse;
-    // the chosen experts: their weights, and what the weights' gradients give
-    float top = m, den = s, dot = 0.0f;
-    if (ok && a.dw) {
-      if (a.renorm) {
-        top = Elem<DT>::load(static_cast<const T*>(a.x) + t * a.stride + min(a.bidx[t * a.k], a.E - 1));
-        top = shift_of(top);
-        den = 0.0f;
-        for (int i = 0; i < a.k; i++) {
-          const int e = min(max(a.bidx[t * a.k + i], 0), a.E - 1);
-          den += ex2((Elem<DT>::load(static_cast<const T*>(a.x) + t * a.stride + e) - top) * kLog2e);
+    float m = x[0];
+#pragma unroll
+    for (int j = 1; j < VPL; j++) m = fmaxf(m, x[j]);
+    m = shift_of(lanes_max<L>(m));
+    const pair_t c2 = pair(kLog2e, kLog2e), mc = pair(-m * kLog2e, -m * kLog2e);
+    pair_t s2 = pair(0.0f, 0.0f), pd2 = s2;
+#pragma unroll
+    for (int j = 0; j < VPL; j += 2) {
+      const pair_t e = ex2_2(fma2(pair(x[j], x[j + 1]), c2, mc));
+      s2 = add2(s2, e);
+      pd2 = fma2(e, pair(d[j], d[j + 1]), pd2);
+      x[j] = e.x;
+      x[j + 1] = e.y;
+    }
+    const float s = lanes_sum<L>(s2.x + s2.y), inv = 1.0f / s, lse = m + logf(s);
+    float pd = lanes_sum<L>(pd2.x + pd2.y) * inv - zc * lse;
+    // the chosen experts, spread over the token's lanes: weights and what their
+    // gradients give
+    float den = s, dot = 0.0f;
+    if (a.dw) {
+      float e = 0.0f, ed = 0.0f;
+      if (ok)
+        for (int i = sub; i < a.k; i += L) {
+          const int col = min(max(a.bidx[t * a.k + i], 0), a.E - 1);
+          const float u = ex2((E::load(p_row + col) - m) * kLog2e);
+          e += u;
+          ed += u * a.dw[t * a.k + i];
         }
-      }
-      for (int i = 0; i < a.k; i++) {
-        const int e = min(max(a.bidx[t * a.k + i], 0), a.E - 1);
-        const float v = Elem<DT>::load(static_cast<const T*>(a.x) + t * a.stride + e);
-        dot += ex2((v - top) * kLog2e) / den * a.dw[t * a.k + i];
-      }
+      if (a.renorm) den = lanes_sum<L>(e);
+      dot = lanes_sum<L>(ed) / den;
     }
     if (!a.renorm) pd += dot;
+    if (in) {
+      T* gp = static_cast<T*>(a.grad) + t * a.gstride;
 #pragma unroll
-    for (int j = 0; j < VPL; j++) y[j] = x[j] * inv * (y[j] - pd);
-    if (ok && a.dw)
-      for (int i = 0; i < a.k; i++) {
-        const int e = a.bidx[t * a.k + i];
-        const float d = a.dw[t * a.k + i] - (a.renorm ? dot : 0.0f);
+      for (int v = 0; v < VPL / N; v++) {
+        float f[N];
+        const int col = col_of<DT, L>(sub, v * N);
 #pragma unroll
-        for (int j = 0; j < VPL; j++)
-          if (col_of<VPL>(L, sub, j) == e) {
-            const float v = Elem<DT>::load(static_cast<const T*>(a.x) + t * a.stride + e);
-            y[j] += ex2((v - top) * kLog2e) / den * d;
-          }
+        for (int j = 0; j < N; j++) f[j] = ok ? x[v * N + j] * inv * (d[v * N + j] - pd) : 0.0f;
+        if (a.gvec) {
+          if (col < a.E) *reinterpret_cast<uint4*>(gp + col) = E::pack(f);
+        } else {
+#pragma unroll
+          for (int j = 0; j < N; j++)
+            if (col + j < a.E) gp[col + j] = E::make(f[j]);
+        }
       }
-    if (!in) continue;
-    T* gp = static_cast<T*>(a.grad) + t * a.gstride;
-#pragma unroll
-    for (int j = 0; j < VPL; j++) {
-      const int col = col_of<VPL>(L, sub, j);
-      if (col < a.E) gp[col] = E::make(ok ? y[j] : 0.0f);
+    }
+    __syncwarp();
+    // their gradients, from fp32, over what was just written
+    if (ok && a.dw) {
+      T* gp = static_cast<T*>(a.grad) + t * a.gstride;
+      for (int i = sub; i < a.k; i += L) {
+        const int col = a.bidx[t * a.k + i];
+        if (col < 0 || col >= a.E) continue;
+        const float u = ex2((E::load(p_row + col) - m) * kLog2e), dwi = a.dw[t * a.k + i];
+        const float de = gc ? coef * (float)gc[col] : 0.0f;
+        gp[col] = E::make(u * inv * (de - pd) + u / den * (a.renorm ? dwi - dot : dwi));
+      }
     }
   }
 }
@@ -449,15 +566,22 @@ int check_route(const scape_route_args* q) {
   return SCAPE_OK;
 }
 
-// Tokens of a chunk: the chunks fill the GPU twice over, in whole rounds of a
-// CTA's tokens.
+// Lanes of a token for this many experts.
+int lanes_of(int experts) {
+  int L = 1;
+  while (L < 8 && L * 8 < experts) L *= 2;
+  return experts <= 256 ? L : experts <= 512 ? 16 : 32;
+}
+
+// Tokens of a chunk: two CTAs for each SM, in whole rounds of a CTA's warps.
 uint64_t chunk_of(const scape_route_args* q) {
-  const uint64_t want = (q->tokens + 303) / 304;
-  return (want + 255) / 256 * 256 ? (want + 255) / 256 * 256 : 256;
+  const uint64_t round = (uint64_t)kWarps * 32 / lanes_of(q->experts);
+  const uint64_t n = (q->tokens + 303) / 304;
+  return n == 0 ? round : (n + round - 1) / round * round;
 }
 
 struct Workspace {
-  uint64_t slots, nb, part_p, part_c, part_n, part_z, part_b, done, bytes;
+  uint64_t slots, nb, part_p, part_c, part_n, part_z, part_b, group_z, done, bytes;
 };
 
 Workspace workspace_of(const scape_route_args* q) {
@@ -475,6 +599,7 @@ Workspace workspace_of(const scape_route_args* q) {
   w.part_n = take(w.slots);
   w.part_z = take(w.slots);
   w.part_b = take(q->n_groups * w.nb);
+  w.group_z = take(q->n_groups);
   w.done = take(1);
   return w;
 }
@@ -490,44 +615,36 @@ void fill(const scape_route_args* q, RouteArgs& a) {
   a.G = (int64_t)q->n_groups;
   a.valid = q->valid;
   a.chunk = (int64_t)chunk_of(q);
-  const int vpl = q->experts <= 256 ? 8 : q->experts <= 512 ? 16 : 32;
-  a.L = 1;
-  while (a.L * vpl < q->experts) a.L <<= 1;
+  const uint64_t es = q->dtype == SCAPE_F32 ? 4 : 2;
+  a.vec = !misaligned(q->logits, 16) && q->row_stride * es % 16 == 0 && q->experts * es % 16 == 0;
 }
 
-template <int DT, int VPL, bool VEC>
+template <int DT, class LN>
 void launch(const RouteArgs& a, unsigned grid, bool back, cudaStream_t s) {
   if (back) {
-    route_grad<DT, VPL, VEC><<<grid, kThreads, 0, s>>>(a);
-  } else {
-    const size_t sm =  // under 48 KB at every size
-        (size_t)(kWarps + 1) * a.E * 4 + (size_t)kWarps * (32 / a.L) * a.k * 8;
-    route_chunks<DT, VPL, VEC><<<grid, kThreads, sm, s>>>(a);
+    route_grad<DT, LN><<<grid, kThreads, 0, s>>>(a);
+  } else {  // under 48 KB at every size
+    const size_t sm = (size_t)kWarps * LN::ROWS * (LN::CAP * 8 + a.k * 8 + 4) + (size_t)(kWarps + 1) * a.E * 4;
+    route_chunks<DT, LN><<<grid, kThreads, sm, s>>>(a);
   }
 }
 
 template <int DT>
-void launch_dt(const RouteArgs& a, bool vec, unsigned grid, bool back, cudaStream_t s) {
-  if (a.E <= 256) {
-    if (vec) launch<DT, 8, true>(a, grid, back, s);
-    else launch<DT, 8, false>(a, grid, back, s);
-  } else if (a.E <= 512) {
-    launch<DT, 16, false>(a, grid, back, s);
-  } else {
-    launch<DT, 32, false>(a, grid, back, s);
-  }
+void launch_dt(const RouteArgs& a, unsigned grid, bool back, cudaStream_t s) {
+  if (a.E <= 8) launch<DT, Lanes<1, 8, 8>>(a, grid, back, s);
+  else if (a.E <= 16) launch<DT, Lanes<2, 8, 8>>(a, grid, back, s);
+  else if (a.E <= 32) launch<DT, Lanes<4, 8, 8>>(a, grid, back, s);
+  else if (a.E <= 64) launch<DT, Lanes<8, 8, 4>>(a, grid, back, s);
+  else if (a.E <= 128) launch<DT, Lanes<8, 16, 4>>(a, grid, back, s);
+  else if (a.E <= 256) launch<DT, Lanes<8, 32, 4>>(a, grid, back, s);
+  else if (a.E <= 512) launch<DT, Lanes<16, 32, 2>>(a, grid, back, s);
+  else launch<DT, Lanes<32, 32, 1>>(a, grid, back, s);
 }
 
-void launch_any(int dtype, const RouteArgs& a, bool vec, unsigned grid, bool back, cudaStream_t s) {
-  if (dtype == SCAPE_BF16) launch_dt<SCAPE_BF16>(a, vec, grid, back, s);
-  else if (dtype == SCAPE_F16) launch_dt<SCAPE_F16>(a, vec, grid, back, s);
-  else launch_dt<SCAPE_F32>(a, vec, grid, back, s);
-}
-
-// 16-byte loads need every row on a 16-byte boundary and whole vectors of 8.
-bool vec_ok(const scape_route_args* q) {
-  const uint64_t es = q->dtype == SCAPE_F32 ? 4 : 2;
-  return !misaligned(q->logits, 16) && q->row_stride * es % 16 == 0 && q->experts % 8 == 0;
+void launch_any(int dtype, const RouteArgs& a, unsigned grid, bool back, cudaStream_t s) {
+  if (dtype == SCAPE_BF16) launch_dt<SCAPE_BF16>(a, grid, back, s);
+  else if (dtype == SCAPE_F16) launch_dt<SCAPE_F16>(a, grid, back, s);
+  else launch_dt<SCAPE_F32>(a, grid, back, s);
 }
 
 }  // namespace
@@ -580,10 +697,11 @@ SCAPE_API int scape_route(const scape_route_args* args, int32_t* idx, float* wei
   a.part_n = reinterpret_cast<int32_t*>(ws + w.part_n);
   a.part_z = reinterpret_cast<float*>(ws + w.part_z);
   a.part_b = reinterpret_cast<float*>(ws + w.part_b);
+  a.group_z = reinterpret_cast<float*>(ws + w.group_z);
   a.done = reinterpret_cast<uint32_t*>(ws + w.done);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const unsigned grid = (unsigned)((args->tokens + a.chunk - 1) / a.chunk);
-  launch_any(args->dtype, a, vec_ok(args), grid ? grid : 1u, false, s);
+  launch_any(args->dtype, a, grid ? grid : 1u, false, s);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "route_chunks: %s", cudaGetErrorString(e));
   route_finish<<<dim3((unsigned)args->n_groups, (unsigned)w.nb), kThreads, 0, s>>>(a);
@@ -617,8 +735,9 @@ SCAPE_API int scape_route_backward(const scape_route_args* args, const int32_t* 
   a.dl = d_losses;
   a.grad = grad;
   a.gstride = (int64_t)grad_stride;
+  a.gvec = !misaligned(grad, 16) && grad_stride * es % 16 == 0 && args->experts * es % 16 == 0;
   const unsigned grid = (unsigned)((args->tokens + a.chunk - 1) / a.chunk);
-  launch_any(args->dtype, a, vec_ok(args), grid, true, static_cast<cudaStream_t>(stream));
+  launch_any(args->dtype, a, grid, true, static_cast<cudaStream_t>(stream));
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SCAPE_OK : fail(SCAPE_ECUDA, "route_grad: %s", cudaGetErrorString(e));
 }
