@@ -108,6 +108,7 @@ template <int L_, int VPL_, int GPL_>
 struct Lanes {
   static constexpr int L = L_, VPL = VPL_, GPL = GPL_, ROWS = 32 / L_;
   static constexpr int CAP = L_ * VPL_ < 48 ? L_ * VPL_ : 48;  // list entries of a token
+  static_assert(CAP % 4 == 0, "the list is read in fours");
 };
 
 template <int DT, int L>
@@ -123,17 +124,21 @@ struct RowRegs {
   static constexpr int N = Elem<DT>::kPerVec, VECS = LN::VPL / N;
   uint4 r[VECS];
   __device__ __forceinline__ void load(const typename Elem<DT>::T* p, int E, int sub, bool in, bool vec) {
+    if (vec) {
+      p += sub * N;
+      E = in ? E - sub * N : 0;
 #pragma unroll
-    for (int v = 0; v < VECS; v++) {
-      const int col = (v * LN::L + sub) * N;
-      r[v] = neg_inf_vec<DT>();
-      if (!in || col >= E) continue;
-      if (vec) {
-        r[v] = ld_row_u4(p + col);
-      } else {
+      for (int v = 0; v < VECS; v++) {
+        r[v] = neg_inf_vec<DT>();
+        if (v * LN::L * N < E) r[v] = ld_row_u4(p + v * LN::L * N);
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < VECS; v++) {
+        const int col = (v * LN::L + sub) * N;
         float f[N];
 #pragma unroll
-        for (int j = 0; j < N; j++) f[j] = col + j < E ? Elem<DT>::load(p + col + j) : neg_inf();
+        for (int j = 0; j < N; j++) f[j] = in && col + j < E ? Elem<DT>::load(p + col + j) : neg_inf();
         r[v] = Elem<DT>::pack(f);
       }
     }
@@ -154,6 +159,56 @@ __device__ __forceinline__ float value_of_key(uint32_t k) {
                           : __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
 
+// A bound that at least k of a token's experts reach, from the largest logits of
+// its L x GPL groups.  If the k-th largest of the lanes' largest and the k/2-th
+// largest of their second largest are known, the larger one of the two will do:
+// k / 2 lanes have two groups each that reach the latter (13 of 256 experts
+// reach it on average for k = 8, where the exact k-th largest of the groups' is
+// reached by 9 but takes five times the instructions).  With k above L it is
+// that exact one.
+template <class LN>
+__device__ __forceinline__ float bound_for(float (&gm)[LN::GPL], int k, int lane, unsigned seg) {
+  constexpr int L = LN::L, GPL = LN::GPL;
+  if (k <= L) {
+    float top = neg_inf(), second = neg_inf();
+#pragma unroll
+    for (int j = 0; j < GPL; j++) {
+      second = fmaxf(second, fminf(top, gm[j]));
+      top = fmaxf(top, gm[j]);
+    }
+    // both in descending order over the lanes
+#pragma unroll
+    for (int size = 2; size <= L; size <<= 1)
+#pragma unroll
+      for (int d = size >> 1; d; d >>= 1) {
+        const bool keep_max = ((lane & d) == 0) == ((lane & size) == 0 || size == L);
+        const float t = __shfl_xor_sync(kFull, top, d), u = __shfl_xor_sync(kFull, second, d);
+        top = keep_max ? fmaxf(top, t) : fminf(top, t);
+        second = keep_max ? fmaxf(second, u) : fminf(second, u);
+      }
+    const float a = __shfl_sync(kFull, top, k - 1, L);
+    const float b = __shfl_sync(kFull, second, (k + 1) / 2 - 1, L);
+    return GPL > 1 ? fmaxf(a, b) : a;
+  }
+  float bound = neg_inf();
+  for (int i = 0; i < k; i++) {
+    float h = gm[0];
+#pragma unroll
+    for (int j = 1; j < GPL; j++) h = fmaxf(h, gm[j]);
+    bound = lanes_max<L>(h);
+    // one of those that are equal to it is taken out
+    const unsigned who = __ballot_sync(kFull, h == bound) & seg;
+    bool mine = lane == __ffs(who) - 1;
+#pragma unroll
+    for (int j = 0; j < GPL; j++) {
+      const bool hit = mine && gm[j] == bound;
+      gm[j] = hit ? neg_inf() : gm[j];
+      mine = mine && !hit;
+    }
+  }
+  return bound;
+}
+
 template <int DT, class LN>
 __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
   using E = Elem<DT>;
@@ -162,8 +217,7 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   uint64_t* lists = reinterpret_cast<uint64_t*>(smem);  // kWarps x ROWS x CAP
   uint64_t* ranks = lists + kWarps * ROWS * CAP;                      // kWarps x ROWS x k
-  int* n_cand = reinterpret_cast<int*>(ranks + kWarps * ROWS * a.k);  // kWarps x ROWS
-  float* sp = reinterpret_cast<float*>(n_cand + kWarps * ROWS);       // kWarps x E
+  float* sp = reinterpret_cast<float*>(ranks + kWarps * ROWS * a.k);  // kWarps x E
   int32_t* sc = reinterpret_cast<int32_t*>(sp + kWarps * a.E);        // E
   __shared__ float fbuf[32];
   __shared__ int32_t ibuf[32];
@@ -172,7 +226,10 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
   const unsigned seg = (L == 32 ? kFull : ((1u << L) - 1u) << (slot * L));  // this token's lanes
   uint64_t* list = lists + (wid * ROWS + slot) * CAP;
   uint64_t* sorted = ranks + (wid * ROWS + slot) * a.k;
-  int* n_mine = n_cand + wid * ROWS + slot;
+  uint32_t experts = 0;  // this lane's values that are experts
+#pragma unroll
+  for (int j = 0; j < VPL; j++)
+    if (col_of<DT, L>(sub, j) < a.E) experts |= 1u << j;
   const int64_t t0 = (int64_t)blockIdx.x * a.chunk, t1 = min(t0 + a.chunk, a.T);
   if (blockIdx.x == 0 && tid == 0) *a.done = 0;
 
@@ -193,9 +250,9 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
         continue;
       }
     }
-    float acc[VPL];
+    pair_t acc[VPL / 2];
 #pragma unroll
-    for (int j = 0; j < VPL; j++) acc[j] = 0.0f;
+    for (int j = 0; j < VPL / 2; j++) acc[j] = pair(0.0f, 0.0f);
     float zsum = 0.0f;
     int32_t nlive = 0;
     for (int i = tid; i < a.E; i += kThreads) sc[i] = 0;
@@ -221,28 +278,13 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
       m = lanes_max<L>(m);
       const float sh = shift_of(m);
 
-      // the bound: the k-th largest of the groups' largest
-      float bound = neg_inf();
-      for (int i = 0; i < a.k; i++) {
-        float h = gm[0];
-#pragma unroll
-        for (int j = 1; j < GPL; j++) h = fmaxf(h, gm[j]);
-        bound = lanes_max<L>(h);
-        // one of those that are equal to it is taken out
-        const unsigned who = __ballot_sync(kFull, h == bound) & seg;
-        bool mine = lane == __ffs(who) - 1;
-#pragma unroll
-        for (int j = 0; j < GPL; j++) {
-          const bool hit = mine && gm[j] == bound;
-          gm[j] = hit ? neg_inf() : gm[j];
-          mine = mine && !hit;
-        }
-      }
+      float bound = bound_for<LN>(gm, a.k, lane, seg);
       // the experts that reach it
       uint32_t cand = 0;
 #pragma unroll
       for (int j = 0; j < VPL; j++)
         if (!(x[j] < bound)) cand |= 1u << j;
+      cand &= experts;
 
       // p, and the sums
       const pair_t c2 = pair(kLog2e, kLog2e), mc = pair(-sh * kLog2e, -sh * kLog2e);
@@ -260,7 +302,8 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
       const float lse = sh + logf(s);
       if (ok) {
 #pragma unroll
-        for (int j = 0; j < VPL; j++) acc[j] = fmaf(x[j], inv, acc[j]);
+        for (int j = 0; j < VPL / 2; j++)
+          acc[j] = fma2(pair(x[2 * j], x[2 * j + 1]), pair(inv, inv), acc[j]);
         if (sub == 0) {
           zsum += lse * lse;
           nlive++;
@@ -269,18 +312,20 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
         cand = 0;
       }
 
-      if (sub == 0) *n_mine = 0;
-      __syncwarp();
-      while (cand) {
+      // listed: column first, then the composite
+      int incl = __popc(cand);
+#pragma unroll
+      for (int o = 1; o < L; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, incl, o, L);
+        if (sub >= o) incl += y;
+      }
+      const int n = __shfl_sync(kFull, incl, L - 1, L);
+      for (int at_ = incl - __popc(cand); cand; at_++) {
         const int j = __ffs(cand) - 1;
         cand &= cand - 1;
-        const int col = col_of<DT, L>(sub, j);
-        if (col >= a.E) continue;
-        const int n = atomicAdd(n_mine, 1);
-        if (n < CAP) list[n] = (uint64_t)order_key(E::load(p_row + col)) << 32 | (uint32_t)~col;
+        if (at_ < CAP) list[at_] = (uint64_t)col_of<DT, L>(sub, j);
       }
       __syncwarp();
-      const int n = *n_mine;
       if (__any_sync(kFull, n > CAP)) {
         // one choice after the other, all logits read again
         uint32_t key[VPL];
@@ -311,9 +356,21 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
       } else {
         // ranked: each entry counts those above it
         for (int i = sub; i < n; i += L) {
+          const uint32_t col = (uint32_t)list[i];
+          list[i] = (uint64_t)order_key(E::load(p_row + col)) << 32 | (uint32_t)~col;
+        }
+        const int n4 = (n + 3) & ~3;  // at most CAP, a multiple of 4
+        for (int i = n + sub; i < n4; i += L) list[i] = 0;
+        __syncwarp();
+        for (int i = sub; i < n; i += L) {
           const uint64_t v = list[i];
           int above = 0;
-          for (int q = 0; q < n; q++) above += list[q] > v;
+#pragma unroll 1
+          for (int q = 0; q < n; q += 4) {  // in fours: below the end come zeros
+            const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(list + q);
+            const ulonglong2 t2 = *reinterpret_cast<const ulonglong2*>(list + q + 2);
+            above += (u.x > v) + (u.y > v) + (t2.x > v) + (t2.y > v);
+          }
           if (above < a.k) sorted[above] = v;
         }
       }
@@ -336,10 +393,11 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
     if (inside) {  // the slot of this chunk and group
 #pragma unroll
       for (int j = 0; j < VPL; j++) {
+        float v = j % 2 ? acc[j / 2].y : acc[j / 2].x;
 #pragma unroll
-        for (int o = L; o < 32; o <<= 1) acc[j] += __shfl_xor_sync(kFull, acc[j], o);
+        for (int o = L; o < 32; o <<= 1) v += __shfl_xor_sync(kFull, v, o);
         const int col = col_of<DT, L>(sub, j);
-        if (slot == 0 && col < a.E) sp[wid * a.E + col] = acc[j];
+        if (slot == 0 && col < a.E) sp[wid * a.E + col] = v;
       }
       const float z = cta_sum(zsum, fbuf);
       const int32_t nl = cta_sum(nlive, ibuf);
@@ -360,21 +418,34 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
     if (g < a.G && bound_of(a, g + 1) <= end) g++;
     at = end;
   }
+  grid_launch_dependents();
 }
 
-// One CTA per group and block of kThreads / 8 columns; 8 threads share a
-// column's slots.  The last CTA to finish adds up what the groups contribute.
-constexpr int kCols = kThreads / 8;
+// One CTA per group and block of 8 columns (a sector of the slots); 32 threads
+// share a column's slots.  The last CTA to finish adds up what the groups
+// contribute.
+constexpr int kCols = 8;
 
 __global__ __launch_bounds__(kThreads) void route_finish(const RouteArgs a) {
-  __shared__ float fbuf[32];
-  __shared__ int32_t ibuf[32];
+  __shared__ float fbuf[32], sp[kWarps][kCols];
+  __shared__ int32_t ibuf[32], sc[kWarps][kCols];
   __shared__ bool last;
-  const int tid = threadIdx.x;
+  grid_dependency_wait();
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int64_t g = blockIdx.x;
   const int nb = gridDim.y;
   const int64_t lo = bound_of(a, g), hi = bound_of(a, g + 1);
   const int64_t s0 = lo / a.chunk + g, s1 = hi > lo ? (hi - 1) / a.chunk + g + 1 : s0;
+  const int col = blockIdx.y * kCols + (lane & 7);
+  float p = 0.0f;
+  int32_t c = 0;
+  if (col < a.E) {
+#pragma unroll 4
+    for (int64_t s = s0 + tid / kCols; s < s1; s += kThreads / kCols) {
+      p += a.part_p[s * a.E + col];
+      c += a.part_c[s * a.E + col];
+    }
+  }
   int32_t n = 0;
   float zg = 0.0f;
   for (int64_t s = s0 + tid; s < s1; s += kThreads) {
@@ -383,21 +454,29 @@ __global__ __launch_bounds__(kThreads) void route_finish(const RouteArgs a) {
   }
   n = cta_sum(n, ibuf);
   zg = cta_sum(zg, fbuf);
-  const int col = blockIdx.y * kCols + (tid >> 3);
-  float p = 0.0f;
-  int32_t c = 0;
-  if (col < a.E)
-    for (int64_t s = s0 + (tid & 7); s < s1; s += 8) {
-      p += a.part_p[s * a.E + col];
-      c += a.part_c[s * a.E + col];
-    }
-  for (int o = 4; o; o >>= 1) {
+#pragma unroll
+  for (int o = 16; o >= kCols; o >>= 1) {
     p += __shfl_xor_sync(kFull, p, o);
     c += __shfl_xor_sync(kFull, c, o);
   }
-  if (col < a.E && (tid & 7) == 0) a.counts[g * a.E + col] = c;
+  if (lane < kCols) {
+    sp[wid][lane] = p;
+    sc[wid][lane] = c;
+  }
+  __syncthreads();
+  float b = 0.0f;
+  if (tid < kCols && col < a.E) {
+    p = 0.0f;
+    c = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+      p += sp[w][tid];
+      c += sc[w][tid];
+    }
+    a.counts[g * a.E + col] = c;
+    b = p * (float)c;
+  }
   const float tg = (float)max(n, 1);
-  const float b = (tid & 7) == 0 && col < a.E ? p * (float)c : 0.0f;
   const float bal = cta_sum(b, fbuf) * ((float)a.E / ((float)a.k * tg)) / tg;
   if (tid == 0) {
     a.part_b[g * nb + blockIdx.y] = bal;
@@ -624,7 +703,7 @@ void launch(const RouteArgs& a, unsigned grid, bool back, cudaStream_t s) {
   if (back) {
     route_grad<DT, LN><<<grid, kThreads, 0, s>>>(a);
   } else {  // under 48 KB at every size
-    const size_t sm = (size_t)kWarps * LN::ROWS * (LN::CAP * 8 + a.k * 8 + 4) + (size_t)(kWarps + 1) * a.E * 4;
+    const size_t sm = (size_t)kWarps * LN::ROWS * (LN::CAP + a.k) * 8 + (size_t)(kWarps + 1) * a.E * 4;
     route_chunks<DT, LN><<<grid, kThreads, sm, s>>>(a);
   }
 }
@@ -704,8 +783,19 @@ SCAPE_API int scape_route(const scape_route_args* args, int32_t* idx, float* wei
   launch_any(args->dtype, a, grid ? grid : 1u, false, s);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "route_chunks: %s", cudaGetErrorString(e));
-  route_finish<<<dim3((unsigned)args->n_groups, (unsigned)w.nb), kThreads, 0, s>>>(a);
-  e = cudaGetLastError();
+  // launched behind the chunks: it waits for them on the GPU
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)args->n_groups, (unsigned)w.nb);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, route_finish, a);
+  const cudaError_t last = cudaGetLastError();
+  if (e == cudaSuccess) e = last;
   return e == cudaSuccess ? SCAPE_OK : fail(SCAPE_ECUDA, "route_finish: %s", cudaGetErrorString(e));
 }
 
