@@ -42,6 +42,7 @@ struct RouteArgs {
   const void* x;
   int64_t T, stride;
   int E, k, renorm;
+  bool single;     // one chunk and one group
   bool vec, gvec;  // rows of the logits, of the gradient in whole 16-byte vectors
   const int32_t* cu;
   int64_t G;
@@ -403,13 +404,28 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
       const int32_t nl = cta_sum(nlive, ibuf);
       __syncthreads();
       const int64_t sl = blockIdx.x + g;
+      float b = 0.0f;
       for (int i = tid; i < a.E; i += kThreads) {
         float p = 0.0f;
         for (int w = 0; w < kWarps; w++) p += sp[w * a.E + i];
-        a.part_p[sl * a.E + i] = p;
-        a.part_c[sl * a.E + i] = sc[i];
+        if (a.single) {
+          a.counts[i] = sc[i];
+          b += p * (float)sc[i];
+        } else {
+          a.part_p[sl * a.E + i] = p;
+          a.part_c[sl * a.E + i] = sc[i];
+        }
       }
-      if (tid == 0) {
+      if (a.single) {  // one CTA has it all: no second kernel
+        const float tg = (float)max(nl, 1);
+        b = cta_sum(b, fbuf) * ((float)a.E / ((float)a.k * tg)) / tg;
+        if (tid == 0) {
+          a.live[0] = a.live[1] = nl;
+          a.live[2] = nl > 0;
+          a.losses[0] = b;
+          a.losses[1] = z / tg;
+        }
+      } else if (tid == 0) {
         a.part_n[sl] = nl;
         a.part_z[sl] = z;
       }
@@ -694,6 +710,7 @@ void fill(const scape_route_args* q, RouteArgs& a) {
   a.G = (int64_t)q->n_groups;
   a.valid = q->valid;
   a.chunk = (int64_t)chunk_of(q);
+  a.single = q->tokens > 0 && q->tokens <= (uint64_t)a.chunk && !q->cu_tokens;
   const uint64_t es = q->dtype == SCAPE_F32 ? 4 : 2;
   a.vec = !misaligned(q->logits, 16) && q->row_stride * es % 16 == 0 && q->experts * es % 16 == 0;
 }
@@ -783,6 +800,7 @@ SCAPE_API int scape_route(const scape_route_args* args, int32_t* idx, float* wei
   launch_any(args->dtype, a, grid ? grid : 1u, false, s);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "route_chunks: %s", cudaGetErrorString(e));
+  if (a.single) return SCAPE_OK;
   // launched behind the chunks: it waits for them on the GPU
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)args->n_groups, (unsigned)w.nb);
