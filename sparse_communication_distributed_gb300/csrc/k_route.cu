@@ -78,13 +78,20 @@ __device__ __forceinline__ int64_t bound_of(const RouteArgs& a, int64_t g) {
   return v < 0 ? 0 : v > a.T ? a.T : v;
 }
 
-// First group whose end lies beyond token t (a.G if none).
+// First group whose end lies beyond token t (a.G if none), found by a whole
+// warp for one t: 32 probes at a time.
 __device__ __forceinline__ int64_t group_at(const RouteArgs& a, int64_t t) {
-  int64_t lo = 0, hi = a.G;
+  if (!a.cu) return t < a.T ? 0 : 1;
+  const int lane = threadIdx.x & 31;
+  int64_t lo = 0, hi = a.G;  // the answer is in [lo, hi]
   while (lo < hi) {
-    const int64_t mid = (lo + hi) / 2;
-    if (bound_of(a, mid + 1) > t) hi = mid;
-    else lo = mid + 1;
+    const int64_t step = (hi - lo + 31) / 32, probe = min(lo + (lane + 1) * step, hi) - 1;
+    const unsigned beyond = __ballot_sync(kFull, bound_of(a, probe + 1) > t);
+    if (!beyond) return hi;  // the last probe is hi - 1
+    const int first = __ffs(beyond) - 1;
+    hi = min(lo + (first + 1) * step, hi) - 1;
+    lo += first * step;
+    if (step == 1) return hi;
   }
   return lo;
 }
@@ -233,6 +240,7 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
     if (col_of<DT, L>(sub, j) < a.E) experts |= 1u << j;
   const int64_t t0 = (int64_t)blockIdx.x * a.chunk, t1 = min(t0 + a.chunk, a.T);
   if (blockIdx.x == 0 && tid == 0) *a.done = 0;
+  grid_launch_dependents();  // the second kernel waits for this one on its own
 
   // pieces of the chunk: each group it touches, and tokens outside all groups
   int64_t at = t0, g = group_at(a, t0);
@@ -434,7 +442,6 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
     if (g < a.G && bound_of(a, g + 1) <= end) g++;
     at = end;
   }
-  grid_launch_dependents();
 }
 
 // One CTA per group and block of 8 columns (a sector of the slots); 32 threads
@@ -446,12 +453,12 @@ __global__ __launch_bounds__(kThreads) void route_finish(const RouteArgs a) {
   __shared__ float fbuf[32], sp[kWarps][kCols];
   __shared__ int32_t ibuf[32], sc[kWarps][kCols];
   __shared__ bool last;
-  grid_dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int64_t g = blockIdx.x;
   const int nb = gridDim.y;
   const int64_t lo = bound_of(a, g), hi = bound_of(a, g + 1);
   const int64_t s0 = lo / a.chunk + g, s1 = hi > lo ? (hi - 1) / a.chunk + g + 1 : s0;
+  grid_dependency_wait();
   const int col = blockIdx.y * kCols + (lane & 7);
   float p = 0.0f;
   int32_t c = 0;
@@ -532,31 +539,65 @@ __global__ __launch_bounds__(kThreads, 2) void route_grad(const RouteArgs a) {
   using E = Elem<DT>;
   using T = typename E::T;
   constexpr int L = LN::L, VPL = LN::VPL, ROWS = LN::ROWS, N = E::kPerVec;
+  constexpr int KPL = 32 / L < 8 ? 32 / L : 8;  // choices of a lane: k <= 32, and k <= experts
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int sub = lane & (L - 1), slot = lane / L;
   const int64_t t0 = (int64_t)blockIdx.x * a.chunk, t1 = min(t0 + a.chunk, a.T);
+  constexpr int64_t kStep = kWarps * ROWS;
+  int64_t t = t0 + wid * ROWS + slot;
+  // a token's inputs: its logits and choices are loaded a round ahead, the
+  // logits at the choices at the end of the round before
+  RowRegs<DT, LN> next;
+  int32_t next_id[KPL], next_first = -1;
+  float next_dw[KPL], next_x[KPL];
+  auto fetch = [&](int64_t u) {
+    const bool in = u < t1;
+    next.load(static_cast<const T*>(a.x) + u * a.stride, a.E, sub, in, a.vec);
+    next_first = in ? a.bidx[u * a.k] : -1;  // tells whether the token is live
+#pragma unroll
+    for (int q = 0; q < KPL; q++) {
+      const int i = q * L + sub;
+      next_id[q] = -1;
+      next_dw[q] = 0.0f;
+      if (in && a.dw && i < a.k) {
+        next_id[q] = a.bidx[u * a.k + i];
+        next_dw[q] = a.dw[u * a.k + i];
+      }
+    }
+  };
+  auto fetch_chosen = [&](int64_t u) {
+#pragma unroll
+    for (int q = 0; q < KPL; q++) {
+      next_x[q] = neg_inf();
+      if (next_id[q] >= 0 && next_id[q] < a.E)
+        next_x[q] = E::load(static_cast<const T*>(a.x) + u * a.stride + next_id[q]);
+    }
+  };
+  fetch(t);
   const float dB = a.dl ? a.dl[0] : 0.0f, dZ = a.dl ? a.dl[1] : 0.0f;
   const float zc = 2.0f * dZ / (float)max(a.blive[a.G], 1);
   const float bc = dB / (float)max(a.blive[a.G + 1], 1) * ((float)a.E / (float)a.k);
-  int64_t t = t0 + wid * ROWS + slot;
-  RowRegs<DT, LN> next;
-  next.load(static_cast<const T*>(a.x) + t * a.stride, a.E, sub, t < t1, a.vec);
   // this token's group: its end, and d of this lane's experts
-  int64_t g_end = t0;
+  int64_t g = group_at(a, t0), g_end = t0;
   const int32_t* gc = nullptr;
   float coef = 0.0f, d[VPL];
 #pragma unroll
   for (int j = 0; j < VPL; j++) d[j] = 0.0f;
-  for (int64_t r = t0 + wid * ROWS; r < t1; r += kWarps * ROWS, t += kWarps * ROWS) {
-    const bool in = t < t1;
-    const T* p_row = static_cast<const T*>(a.x) + t * a.stride;
-    float x[VPL];
+  fetch_chosen(t);
+  for (int64_t r = t0 + wid * ROWS; r < t1; r += kStep, t += kStep) {
+    const bool in = t < t1, ok = in && next_first >= 0;
+    float x[VPL], xc[KPL], dwc[KPL];
+    int id[KPL];
     next.get(x);
-    next.load(p_row + kWarps * ROWS * a.stride, a.E, sub, t + kWarps * ROWS < t1, a.vec);
-    // the first of the chosen tells whether the token is live
-    const bool ok = in && a.bidx[t * a.k] >= 0;
+#pragma unroll
+    for (int q = 0; q < KPL; q++) {
+      id[q] = next_id[q];
+      dwc[q] = next_dw[q];
+      xc[q] = next_x[q];
+    }
+    fetch(t + kStep);
     if (in && t >= g_end) {
-      const int64_t g = group_at(a, t);
+      while (g < a.G && bound_of(a, g + 1) <= t) g++;
       g_end = g < a.G ? bound_of(a, g + 1) : a.T;
       gc = g < a.G ? a.bcounts + g * a.E : nullptr;
       const float tg = gc ? (float)max(a.blive[g], 1) : 1.0f;
@@ -567,6 +608,11 @@ __global__ __launch_bounds__(kThreads, 2) void route_grad(const RouteArgs a) {
         d[j] = gc && col < a.E ? coef * (float)gc[col] : 0.0f;
       }
     }
+    // d at the choices (needed late)
+    float dc[KPL];
+#pragma unroll
+    for (int q = 0; q < KPL; q++)
+      dc[q] = ok && gc && id[q] >= 0 && id[q] < a.E ? coef * (float)gc[id[q]] : 0.0f;
     float m = x[0];
 #pragma unroll
     for (int j = 1; j < VPL; j++) m = fmaxf(m, x[j]);
@@ -583,20 +629,18 @@ __global__ __launch_bounds__(kThreads, 2) void route_grad(const RouteArgs a) {
     }
     const float s = lanes_sum<L>(s2.x + s2.y), inv = 1.0f / s, lse = m + logf(s);
     float pd = lanes_sum<L>(pd2.x + pd2.y) * inv - zc * lse;
-    // the chosen experts, spread over the token's lanes: weights and what their
-    // gradients give
-    float den = s, dot = 0.0f;
+    // the choices: weights and what their gradients give
+    float inv_den = inv, dot = 0.0f;
     if (a.dw) {
       float e = 0.0f, ed = 0.0f;
-      if (ok)
-        for (int i = sub; i < a.k; i += L) {
-          const int col = min(max(a.bidx[t * a.k + i], 0), a.E - 1);
-          const float u = ex2((E::load(p_row + col) - m) * kLog2e);
-          e += u;
-          ed += u * a.dw[t * a.k + i];
-        }
-      if (a.renorm) den = lanes_sum<L>(e);
-      dot = lanes_sum<L>(ed) / den;
+#pragma unroll
+      for (int q = 0; q < KPL; q++) {
+        xc[q] = ex2((xc[q] - m) * kLog2e);
+        e += xc[q];
+        ed += xc[q] * dwc[q];
+      }
+      if (a.renorm) inv_den = 1.0f / lanes_sum<L>(e);
+      dot = lanes_sum<L>(ed) * inv_den;
     }
     if (!a.renorm) pd += dot;
     if (in) {
@@ -616,16 +660,15 @@ __global__ __launch_bounds__(kThreads, 2) void route_grad(const RouteArgs a) {
         }
       }
     }
+    fetch_chosen(t + kStep);
     __syncwarp();
     // their gradients, from fp32, over what was just written
     if (ok && a.dw) {
       T* gp = static_cast<T*>(a.grad) + t * a.gstride;
-      for (int i = sub; i < a.k; i += L) {
-        const int col = a.bidx[t * a.k + i];
-        if (col < 0 || col >= a.E) continue;
-        const float u = ex2((E::load(p_row + col) - m) * kLog2e), dwi = a.dw[t * a.k + i];
-        const float de = gc ? coef * (float)gc[col] : 0.0f;
-        gp[col] = E::make(u * inv * (de - pd) + u / den * (a.renorm ? dwi - dot : dwi));
+#pragma unroll
+      for (int q = 0; q < KPL; q++) {
+        if (id[q] < 0 || id[q] >= a.E) continue;
+        gp[id[q]] = E::make(xc[q] * inv * (dc[q] - pd) + xc[q] * inv_den * (a.renorm ? dwc[q] - dot : dwc[q]));
       }
     }
   }
