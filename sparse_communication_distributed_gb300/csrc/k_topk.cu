@@ -3,7 +3,7 @@
 //
 // Candidates are ranked by the unique composite key << 32 | ~index (order_key
 // of objective.cuh), so that equal logits go to the lower index.  A CTA takes a
-// row in tiles of up to 64 KB of shared memory; each thread works on vectors
+// row in tiles of up to 62 KB of shared memory; each thread works on vectors
 // that it copied itself.  One pass over a tile keeps, for each of G groups of
 // elements (a group is one place or a few of the vectors that a thread sees),
 // the group's largest element so far.  At least k elements reach the k-th
@@ -29,8 +29,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kVecs = 16;  // vectors a thread has of a tile
-constexpr int kTile = kThreads * kVecs;
+constexpr int kCtas = 3;   // CTAs that share an SM
+constexpr int kSmem = (228 / kCtas - 5) * 1024;  // of each one's: tile and list
 constexpr int kBlk = 2;    // vectors a thread handles at a time
 constexpr int kMaxK = 1024;
 constexpr int kBins = 256;
@@ -70,54 +70,96 @@ __device__ void sort_list(uint64_t* list, int n) {
   __syncthreads();
 }
 
+// Order of floats as signed whole numbers, and back (its own inverse).
+__device__ __forceinline__ int as_ordered(float f) {
+  const int i = __float_as_int(f);
+  return i ^ ((i >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float from_ordered(int i) {
+  return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF));
+}
+
 // GROUPS: groups of a thread (1, 2, 4 or 8 for 16-bit elements, up to 4 else).
 template <int DT, int GROUPS>
-__global__ __launch_bounds__(kThreads, 3) void topk_rows(const TopkArgs a) {
+__global__ __launch_bounds__(kThreads, kCtas) void topk_rows(const TopkArgs a) {
   using E = Elem<DT>;
   using T = typename E::T;
   constexpr int EPV = E::kPerVec;
-  extern __shared__ __align__(16) uint4 buf[];               // the tile
+  extern __shared__ __align__(16) uint4 buf[];                 // the tile
   uint64_t* list = reinterpret_cast<uint64_t*>(buf + a.tile);  // a.cap entries
-  __shared__ uint32_t hist[kBins];
+  __shared__ __align__(16) uint32_t hist[kBins];
+  __shared__ __align__(16) int range[2][kWarps];
   __shared__ uint32_t ubuf[32];
-  __shared__ float fbuf[2][kWarps];
   __shared__ uint16_t hits[kHits];  // vectors of the tile with something at the bound
   __shared__ uint32_t n_list, n_hits;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int V = (int)a.V;
   const uint32_t buf_at = (uint32_t)__cvta_generic_to_shared(buf) + tid * 16;
 
-  // starts the copy of vector t0 + i of a row
-  auto fetch = [&](const RowView<DT>& view, int64_t t0, int u) {
-    const int i = u * kThreads + tid;
-    if (i >= a.tile || t0 + i >= view.vectors()) return;
-    if (view.whole(t0 + i)) copy_async(buf_at + u * kThreads * 16, view.p + view.first_of(t0 + i));
-    else buf[i] = view.load(t0 + i);
+  // A tile of a row: its first vector starts at p, coordinate e0 (< 0 where the
+  // row starts inside it); "here" vectors, whole ones [lo, hi).
+  struct Where {
+    const T* p;
+    int e0, here, lo, hi;
   };
+  auto where = [&](const T* row_start, int t0) {
+    Where w;
+    w.e0 = t0 * EPV - (int)((reinterpret_cast<uintptr_t>(row_start) & 15u) / sizeof(T));
+    w.p = row_start + w.e0;
+    const unsigned left = (unsigned)V - (unsigned)w.e0;  // elements from the tile's start
+    w.here = (int)min((unsigned)a.tile, (left + EPV - 1) / EPV);
+    w.lo = w.e0 < 0 ? 1 : 0;
+    w.hi = (int)min((unsigned)w.here, left / EPV);
+    return w;
+  };
+  // starts the copies of the whole vectors among kBlk of this thread's
+  auto fetch = [&](const Where& w, int u0) {
+    const T* p = w.p + (int64_t)(u0 * kThreads + tid) * EPV;
+#pragma unroll
+    for (int u = 0; u < kBlk; u++) {
+      const int i = (u0 + u) * kThreads + tid;
+      if (i >= w.lo && i < w.hi) copy_async(buf_at + (u0 + u) * kThreads * 16, p + u * kThreads * EPV);
+    }
+  };
+  // one element by itself, -inf outside the row
+  auto element = [&](const Where& w, int l) {
+    const int e = w.e0 + l;
+    return e >= 0 && e < V ? E::load(w.p + l) : neg_inf();
+  };
+  // ... and puts ragged ones together
+  auto fetch_ragged = [&](const Where& w) {
+    auto one = [&](int i) {
+      float f[EPV];
+#pragma unroll
+      for (int j = 0; j < EPV; j++) f[j] = element(w, i * EPV + j);
+      buf[i] = E::pack(f);
+    };
+    if (w.lo && tid == 0) one(0);
+    if (w.here > w.hi && w.here > w.lo && (w.here - 1) % kThreads == tid) one(w.here - 1);
+  };
+
   int64_t row = blockIdx.x;
+  const T* row_start = static_cast<const T*>(a.x) + row * a.stride;
+  Where next = where(row_start, 0);
   if (row < a.rows) {
-    const RowView<DT> view(a.x, row * a.stride, a.V);
-    for (int u = 0; u < kVecs; u++) fetch(view, 0, u);
+    for (int u0 = 0; u0 * kThreads < next.hi; u0 += kBlk) fetch(next, u0);
+    fetch_ragged(next);
   }
   for (; row < a.rows; row += gridDim.x) {
-    const RowView<DT> view(a.x, row * a.stride, a.V);
-    const int64_t nv = view.vectors();
+    const T* const start = row_start;
+    row_start += (int64_t)gridDim.x * a.stride;
     uint64_t thr = 0;  // composites have to exceed it
     float m = neg_inf(), s = 0.0f;
     uint4 mx = neg_inf_vec<DT>();
     int n = 0;
     if (tid == 0) n_list = 0;
-    for (int64_t t0 = 0; t0 < nv; t0 += a.tile) {
-      const int here = (int)min((int64_t)a.tile, nv - t0);
-      // where the copies of the pass below go on: the next tile or row
-      const bool last = t0 + a.tile >= nv;
-      const int64_t row2 = last ? row + gridDim.x : row;
-      const RowView<DT> view2(a.x, (row2 < a.rows ? row2 : row) * a.stride, a.V);
-      const int64_t t2 = last ? 0 : t0 + a.tile;
-      const int64_t nv2 = row2 < a.rows ? view2.vectors() - t2 : 0;
-      const int here2 = (int)min((int64_t)a.tile, nv2);
-      const T* p2 = view2.p + view2.first_of(t2);
-      const int lo2 = t2 == 0 && view2.shift ? 1 : 0;
-      const int hi2 = here2 - (here2 > 0 && !view2.whole(t2 + here2 - 1) ? 1 : 0);
+    for (int t0 = 0;; t0 += a.tile) {
+      const Where now = next;
+      // where the copies of the listing pass go on: the next tile or row
+      const bool last = (unsigned)V - (unsigned)now.e0 <= (unsigned)(now.here * EPV);
+      next = where(last ? row_start : start, last ? 0 : t0 + a.tile);
+      if (last && row + gridDim.x >= a.rows) next.here = next.lo = next.hi = 0;
+      const int here = now.here;
 
       // the groups' largest, and with them the thread's
       for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
@@ -125,12 +167,11 @@ __global__ __launch_bounds__(kThreads, 3) void topk_rows(const TopkArgs a) {
       copy_wait();
 #pragma unroll 4
       for (int i = tid; i < here; i += kThreads) mx = max_vec<DT>(mx, buf[i]);
-      float gmax[EPV], m2;
+      float gmax[EPV];
       E::unpack(mx, gmax);
 #pragma unroll
       for (int g = GROUPS; g < EPV; g++) gmax[g % GROUPS] = fmaxf(gmax[g % GROUPS], gmax[g]);
-      m2 = gmax[0];
-      float low = gmax[0] > neg_inf() ? gmax[0] : INFINITY;
+      float m2 = gmax[0], low = gmax[0] > neg_inf() ? gmax[0] : INFINITY;
 #pragma unroll
       for (int g = 1; g < GROUPS; g++) {
         m2 = fmaxf(m2, gmax[g]);
@@ -139,22 +180,22 @@ __global__ __launch_bounds__(kThreads, 3) void topk_rows(const TopkArgs a) {
       s *= ex2((shift_of(m) - shift_of(m2)) * a.c);
       m = m2;
       // the range of the groups' largest: finite ones
-      float high = m < INFINITY ? m : 3.0e38f;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        low = fminf(low, __shfl_xor_sync(kFull, low, o));
-        high = fmaxf(high, __shfl_xor_sync(kFull, high, o));
-      }
+      int ihigh = __reduce_max_sync(kFull, as_ordered(fminf(m, 3.0e38f)));
+      int ilow = __reduce_min_sync(kFull, as_ordered(low));
       if (lane == 0) {
-        fbuf[0][wid] = low;
-        fbuf[1][wid] = high;
+        range[0][wid] = ilow;
+        range[1][wid] = ihigh;
       }
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < kWarps; i++) {
-        low = fminf(low, fbuf[0][i]);
-        high = fmaxf(high, fbuf[1][i]);
+      for (int i = 0; i < kWarps; i += 4) {
+        const int4 l = *reinterpret_cast<const int4*>(&range[0][i]);
+        const int4 h = *reinterpret_cast<const int4*>(&range[1][i]);
+        ilow = min(min(min(l.x, l.y), min(l.z, l.w)), ilow);
+        ihigh = max(max(max(h.x, h.y), max(h.z, h.w)), ihigh);
       }
+      low = from_ordered(ilow);
+      const float high = from_ordered(ihigh);
       const float scale = high > low ? (float)kBins * 0.999f / (high - low) : 0.0f;
 #pragma unroll
       for (int g = 0; g < GROUPS; g++)
@@ -163,16 +204,19 @@ __global__ __launch_bounds__(kThreads, 3) void topk_rows(const TopkArgs a) {
           atomicAdd(&hist[b], 1u);
         }
       __syncthreads();
-      // the last bin that has k of them in it and above (every warp for itself)
+      // the last bin that has k of them in it and above (every warp for itself);
+      // lane l has the bins from the top, l * per and on
       float bound = neg_inf();
       {
-        constexpr int per = kBins / 32;  // lane l: bins from the top, l * per and on
+        constexpr int per = kBins / 32;
         uint32_t h[per], sum = 0;
 #pragma unroll
-        for (int j = 0; j < per; j++) {
-          h[j] = hist[kBins - 1 - (lane * per + j)];
-          sum += h[j];
+        for (int j = 0; j < per; j += 4) {
+          const uint4 q = *reinterpret_cast<const uint4*>(&hist[kBins - (lane * per + j) - 4]);
+          h[j] = q.w; h[j + 1] = q.z; h[j + 2] = q.y; h[j + 3] = q.x;
         }
+#pragma unroll
+        for (int j = 0; j < per; j++) sum += h[j];
         const uint32_t inc = warp_incl_scan(sum, lane);
         const unsigned who = __ballot_sync(kFull, inc >= (uint32_t)a.k);
         if (who) {
@@ -205,33 +249,35 @@ __global__ __launch_bounds__(kThreads, 3) void topk_rows(const TopkArgs a) {
           if (at < (uint32_t)kHits) hits[at] = (uint16_t)i;
         }
       };
+      // whole blocks of vectors, then the rest one by one
+      int u0 = 0;
 #pragma unroll 1
-      for (int u0 = 0; u0 < kVecs; u0 += kBlk) {
-        if (u0 * kThreads >= here && u0 * kThreads >= here2) break;
+      for (; (u0 + kBlk) * kThreads <= here; u0 += kBlk) {
         uint4 r[kBlk];
 #pragma unroll
-        for (int u = 0; u < kBlk; u++) {
-          const int i = (u0 + u) * kThreads + tid;
-          r[u] = i < here ? buf[i] : neg_inf_vec<DT>();
-          if (i >= lo2 && i < hi2) copy_async(buf_at + (u0 + u) * kThreads * 16, p2 + (int64_t)i * EPV);
-        }
+        for (int u = 0; u < kBlk; u++) r[u] = buf[(u0 + u) * kThreads + tid];
+        fetch(next, u0);
 #pragma unroll
-        for (int u = 0; u < kBlk; u++)
-          if ((u0 + u) * kThreads + wid * 32 < here) take(r[u], (u0 + u) * kThreads + tid);
+        for (int u = 0; u < kBlk; u++) take(r[u], (u0 + u) * kThreads + tid);
       }
+#pragma unroll 1
+      for (int u = u0; u * kThreads + wid * 32 < here; u++) {
+        const int i = u * kThreads + tid;
+        take(i < here ? buf[i] : neg_inf_vec<DT>(), i);
+      }
+      for (; u0 * kThreads < next.hi; u0 += kBlk) fetch(next, u0);
       s += sum.x + sum.y;
-      // the ragged vectors of the next tile
-      if (lo2 && tid == 0 && here2 > 0) buf[0] = view2.load(t2);
-      if (hi2 < here2 && here2 > lo2 && (here2 - 1) % kThreads == tid) buf[here2 - 1] = view2.load(t2 + here2 - 1);
+      fetch_ragged(next);
       __syncthreads();
       // the elements of the vectors that have something at the bound, read again
       // (from L2) and spread over the threads
       const int n_hit = (int)n_hits;
-      if (n_hit <= kHits) {
+      bool done = n_hit <= kHits;
+      if (done) {
         for (int q = tid; q < n_hit * EPV; q += kThreads) {
-          const int64_t e = view.first_of(t0 + hits[q / EPV]) + q % EPV;
-          if (e < 0 || e >= view.n) continue;
-          const float x = E::load(view.p + e);
+          const int l = (int)hits[q / EPV] * EPV + q % EPV, e = now.e0 + l;
+          if (e < 0 || e >= V) continue;
+          const float x = E::load(now.p + l);
           const uint64_t v = (uint64_t)order_key(x) << 32 | (uint32_t)~(uint32_t)e;
           if (!(x < bound) && v > thr) {
             const uint32_t at = atomicAdd(&n_list, 1u);
@@ -239,59 +285,61 @@ __global__ __launch_bounds__(kThreads, 3) void topk_rows(const TopkArgs a) {
           }
         }
         __syncthreads();
-        if (n_list <= (uint32_t)a.cap) {
-          n = (int)n_list;
-          continue;
+        done = n_list <= (uint32_t)a.cap;
+        if (done) n = (int)n_list;
+      }
+      if (!done) {
+        // too many: cut the list to the k best of before, then take the tile's own
+        // k best above them, found bit by bit over further reads of it
+        sort_list(list, n);
+        if (n >= a.k) {
+          n = a.k;
+          thr = list[n - 1];
         }
-      }
-      // too many: cut the list to the k best of before, then take the tile's own
-      // k best above them, found bit by bit over a second read of it
-      sort_list(list, n);
-      if (n >= a.k) {
-        n = a.k;
-        thr = list[n - 1];
-      }
-      auto each = [&](auto f) {
+        auto each = [&](auto f) {
 #pragma unroll 1
-        for (int i = tid; i < here; i += kThreads) {
-          float x[EPV];
-          E::unpack(view.load(t0 + i), x);
-          const int64_t e0 = view.first_of(t0 + i);
-#pragma unroll
-          for (int j = 0; j < EPV; j++)
-            if (e0 + j >= 0 && e0 + j < view.n) {
-              const uint64_t v = (uint64_t)order_key(x[j]) << 32 | (uint32_t)~(uint32_t)(e0 + j);
-              if (v > thr) f(v);
-            }
+          for (int l = tid; l < here * EPV; l += kThreads) {
+            const int e = now.e0 + l;
+            if (e < 0 || e >= V) continue;
+            const uint64_t v = (uint64_t)order_key(E::load(now.p + l)) << 32 | (uint32_t)~(uint32_t)e;
+            if (v > thr) f(v);
+          }
+        };
+        uint64_t cut = 0;
+        for (int b = 63; b >= 0; b--) {
+          const uint64_t t = cut | (1ull << b);
+          uint32_t c = 0;
+          each([&](uint64_t v) { c += v >= t; });
+          c = cta_sum(c, ubuf);
+          if (c >= (uint32_t)a.k) {
+            cut = t;
+            if (n + (int)c <= a.cap) break;
+          }
         }
-      };
-      uint64_t cut = 0;
-      for (int b = 63; b >= 0; b--) {
-        const uint64_t t = cut | (1ull << b);
-        uint32_t c = 0;
-        each([&](uint64_t v) { c += v >= t; });
-        c = cta_sum(c, ubuf);
-        if (c >= (uint32_t)a.k) {
-          cut = t;
-          if (n + (int)c <= a.cap) break;
-        }
+        if (tid == 0) n_list = n;
+        __syncthreads();
+        each([&](uint64_t v) {
+          if (v >= cut) list[atomicAdd(&n_list, 1u)] = v;
+        });
+        __syncthreads();
+        n = (int)n_list;
       }
-      if (tid == 0) n_list = n;
-      __syncthreads();
-      each([&](uint64_t v) {
-        if (v >= cut) list[atomicAdd(&n_list, 1u)] = v;
-      });
-      __syncthreads();
-      n = (int)n_list;
+      if (last) break;
     }
     // in order
     if (n <= kCountSort) {
       uint64_t v = 0;
       int above = 0;
+      if (tid >= n && tid < ((n + 3) & ~3)) list[tid] = 0;
+      __syncthreads();
       if (tid < n) {
         v = list[tid];
-#pragma unroll 4
-        for (int i = 0; i < n; i++) above += list[i] > v;
+#pragma unroll 2
+        for (int i = 0; i < n; i += 4) {
+          const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(list + i);
+          const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(list + i + 2);
+          above += (p.x > v) + (p.y > v) + (q.x > v) + (q.y > v);
+        }
       }
       __syncthreads();
       if (tid < n) list[above] = v;
@@ -302,7 +350,7 @@ __global__ __launch_bounds__(kThreads, 3) void topk_rows(const TopkArgs a) {
     for (int i = tid; i < a.k; i += kThreads) {
       const int32_t e = (int32_t)~(uint32_t)list[i];
       a.idx[row * a.k + i] = e;
-      if (a.vals) static_cast<T*>(a.vals)[row * a.k + i] = view.p[e];
+      if (a.vals) static_cast<T*>(a.vals)[row * a.k + i] = start[e];
     }
     if (a.lse) {
       const float M = cta_max(m, reinterpret_cast<float*>(ubuf)), sh = shift_of(M);
@@ -322,18 +370,20 @@ cudaError_t launch(TopkArgs& a, cudaStream_t s) {
   const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
   if (!(configured.load() & bit)) {
     e = cudaFuncSetAttribute(topk_rows<DT, GROUPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kTile * 16 + 4 * kMaxK * 8);
+                             kSmem);
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
+  // tiles of one size that fit beside the list, the last one a little shorter
   constexpr int EPV = Elem<DT>::kPerVec;
-  // tiles of one size, the last one a little shorter
-  const int64_t nv = (a.V + 2 * EPV - 2) / EPV;
-  const int64_t tiles = (nv + kTile - 1) / kTile;
-  a.tile = (int)((nv + tiles - 1) / tiles);
   a.cap = 1024;
   while (a.cap < 3 * a.k) a.cap *= 2;
-  const int64_t slots = (int64_t)num_sms() * 3;
+  const bool whole = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && a.stride % EPV == 0;
+  const int64_t nv = (a.V + (whole ? 0 : EPV - 1) + EPV - 1) / EPV;
+  const int64_t most = (kSmem - a.cap * 8) / 16;
+  const int64_t tiles = (nv + most - 1) / most;
+  a.tile = (int)((nv + tiles - 1) / tiles);
+  const int64_t slots = (int64_t)num_sms() * kCtas;
   const int64_t rounds = (a.rows + slots - 1) / slots;
   const unsigned grid = (unsigned)((a.rows + rounds - 1) / rounds);
   topk_rows<DT, GROUPS><<<grid, kThreads, (size_t)a.tile * 16 + (size_t)a.cap * 8, s>>>(a);
