@@ -60,7 +60,7 @@ struct Lse {
   float m = neg_inf(), s = 0.0f;
   __device__ __forceinline__ void add(float x, float c) {
     if (x > m) {
-      s *= ex2((shift_of(m) - x) * c);
+      s *= ex2((m - x) * c);
       m = x;
     }
     s += ex2((x - shift_of(m)) * c);
@@ -161,13 +161,13 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
       }
     }
     const float Ms = shift_of(cta_max(all.m, fbuf));
-    const float L = Ms / a.tau + logf(cta_sum(all.s * ex2((shift_of(all.m) - Ms) * a.c), fbuf));
+    const float L = Ms / a.tau + logf(cta_sum(all.s * ex2((all.m - Ms) * a.c), fbuf));
     float L1 = 0.0f, Lr = neg_inf();
     if (y >= 0)
-      L1 = Ms + logf(cta_sum(one.s * ex2((shift_of(one.m) - Ms) * kLog2e), fbuf));
+      L1 = Ms + logf(cta_sum(one.s * ex2((one.m - Ms) * kLog2e), fbuf));
     if (tail_mode) {
       const float Mr = shift_of(cta_max(rest.m, fbuf));
-      Lr = Mr / a.tau + logf(cta_sum(rest.s * ex2((shift_of(rest.m) - Mr) * a.c), fbuf));
+      Lr = Mr / a.tau + logf(cta_sum(rest.s * ex2((rest.m - Mr) * a.c), fbuf));
     }
     const bool bucket = tail_mode && has && Lr > neg_inf();
     const float qr = bucket ? fmaxf(0.0f, 1.0f - Q) : 0.0f;
@@ -273,24 +273,6 @@ __device__ __forceinline__ void join(float& m, float& s, float& s1, float m2, fl
   s = s * f + s2 * f2;
   s1 = s1 * g + s12 * g2;
   m = M;
-}
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Writes to the same place of another CTA's shared memory in the cluster.
-__device__ __forceinline__ void put_remote(const float* local, uint32_t rank, float v) {
-  uint32_t at = (uint32_t)__cvta_generic_to_shared(local), there;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(v) : "memory");
 }
 
 // What one warp works out for all threads once a row's statistics are known.
@@ -638,7 +620,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
         // the whole row: all = rest and listed
         float M = q.m, S = q.s, S1 = q.s1;
         if (BUCKET) join(M, S, S1, q.tm, q.ts, q.ts1, a.c);
-        const float sh = shift_of(M), shr = shift_of(q.m), sht = shift_of(q.tm);
+        const float sh = shift_of(M), shr = shift_of(q.m);
         const bool bucket = BUCKET && has && q.s > 0.0f;
         const float qr = bucket ? fmaxf(0.0f, 1.0f - Q) : 0.0f;
         if (g) {
@@ -658,7 +640,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
           if (BUCKET) {
             // (Q + q_rest) p_rest - q_rest is Q - p_listed, as Q + q_rest = 1
             const float f = ex2((shr - sh) * a.c), f1 = ex2((shr - sh) * kLog2e);
-            const float top = q.ts * ex2((sht - sh) * a.c) * r.rS;
+            const float top = q.ts * ex2((q.tm - sh) * a.c) * r.rS;
             r.K1 = q.s > 0.0f ? r.A * (qr > 0.0f ? (Q - top) / q.s : Q * f * r.rS) : 0.0f;
             r.K2 = q.s1 > 0.0f ? r.C1 * f1 * r.rS1 : 0.0f;
           }
@@ -666,7 +648,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
           rows[turn] = r;
         }
         if (a.loss && rank == 0) {  // its logarithms are taken after the others have gone on
-          ls = {sh, shr, S, S1, z, Q, qr, has, q.ts / q.s * ex2((sht - shr) * a.c), q.s, q.b};
+          ls = {sh, shr, S, S1, z, Q, qr, has, q.ts / q.s * ex2((q.tm - shr) * a.c), q.s, q.b};
         }
       }
     } else if (a.cluster > 1) {

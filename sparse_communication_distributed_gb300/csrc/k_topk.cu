@@ -14,6 +14,10 @@
 // exponentials.  The list is sorted in the end.  Where too much reaches the
 // bound (many equal logits, few above -inf, adverse orders), the tile is read
 // again and its own k-th best composite is found bit by bit.
+//
+// Few rows: a cluster of CTAs takes a row, each a part of it; the parts' k best
+// go to the first CTA's shared memory and are sorted once more.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -34,6 +38,7 @@ constexpr int kSmem = (228 / kCtas - 5) * 1024;  // of each one's: tile and list
 constexpr int kBlk = 2;    // vectors a thread handles at a time
 constexpr int kMaxK = 1024;
 constexpr int kBins = 256;
+constexpr int kMaxCluster = 8;
 constexpr int kHits = 1024;
 constexpr int kCountSort = 256;  // lists up to this are sorted by counting
 
@@ -43,6 +48,9 @@ struct TopkArgs {
   int k;
   int cap;          // list entries; k of an earlier tile and k new ones always fit
   int tile;         // vectors of a tile
+  int list_at;      // where the list begins, in vectors
+  int cluster;      // CTAs of a row
+  int part;         // vectors of each one's part
   float tau, c;     // temperature, log2(e) / temperature
   int32_t* idx;
   void* vals;
@@ -70,6 +78,31 @@ __device__ void sort_list(uint64_t* list, int n) {
   __syncthreads();
 }
 
+// The same, for short lists by counting what is above each.
+__device__ void order_list(uint64_t* list, int n) {
+  if (n > kCountSort) {
+    sort_list(list, n);
+    return;
+  }
+  const int tid = threadIdx.x;
+  uint64_t v = 0;
+  int above = 0;
+  if (tid >= n && tid < ((n + 3) & ~3)) list[tid] = 0;
+  __syncthreads();
+  if (tid < n) {
+    v = list[tid];
+#pragma unroll 2
+    for (int i = 0; i < n; i += 4) {
+      const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(list + i);
+      const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(list + i + 2);
+      above += (p.x > v) + (p.y > v) + (q.x > v) + (q.y > v);
+    }
+  }
+  __syncthreads();
+  if (tid < n) list[above] = v;
+  __syncthreads();
+}
+
 // Order of floats as signed whole numbers, and back (its own inverse).
 __device__ __forceinline__ int as_ordered(float f) {
   const int i = __float_as_int(f);
@@ -86,14 +119,17 @@ __global__ __launch_bounds__(kThreads, kCtas) void topk_rows(const TopkArgs a) {
   using T = typename E::T;
   constexpr int EPV = E::kPerVec;
   extern __shared__ __align__(16) uint4 buf[];                 // the tile
-  uint64_t* list = reinterpret_cast<uint64_t*>(buf + a.tile);  // a.cap entries
+  uint64_t* list = reinterpret_cast<uint64_t*>(buf + a.list_at);  // a.cap entries
   __shared__ __align__(16) uint32_t hist[kBins];
   __shared__ __align__(16) int range[2][kWarps];
   __shared__ uint32_t ubuf[32];
   __shared__ uint16_t hits[kHits];  // vectors of the tile with something at the bound
+  __shared__ float parts[kMaxCluster][2];  // maximum and sum of each CTA of a row
   __shared__ uint32_t n_list, n_hits;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int V = (int)a.V;
+  const uint32_t rank = a.cluster > 1 ? cluster_rank() : 0;
+  const int first = (int)rank * a.part;  // vector of the row where this CTA starts
   const uint32_t buf_at = (uint32_t)__cvta_generic_to_shared(buf) + tid * 16;
 
   // A tile of a row: its first vector starts at p, coordinate e0 (< 0 where the
@@ -106,10 +142,12 @@ __global__ __launch_bounds__(kThreads, kCtas) void topk_rows(const TopkArgs a) {
     Where w;
     w.e0 = t0 * EPV - (int)((reinterpret_cast<uintptr_t>(row_start) & 15u) / sizeof(T));
     w.p = row_start + w.e0;
-    const unsigned left = (unsigned)V - (unsigned)w.e0;  // elements from the tile's start
-    w.here = (int)min((unsigned)a.tile, (left + EPV - 1) / EPV);
+    // elements from the tile's start; the last CTA of a row may have none
+    const unsigned left = (unsigned)max((int64_t)V - w.e0, (int64_t)0);
+    const unsigned most = (unsigned)min(a.tile, first + a.part - t0);
+    w.here = (int)min(most, (left + EPV - 1) / EPV);
     w.lo = w.e0 < 0 ? 1 : 0;
-    w.hi = (int)min((unsigned)w.here, left / EPV);
+    w.hi = (int)min(most, left / EPV);
     return w;
   };
   // starts the copies of the whole vectors among kBlk of this thread's
@@ -138,27 +176,28 @@ __global__ __launch_bounds__(kThreads, kCtas) void topk_rows(const TopkArgs a) {
     if (w.here > w.hi && w.here > w.lo && (w.here - 1) % kThreads == tid) one(w.here - 1);
   };
 
-  int64_t row = blockIdx.x;
+  const int64_t step = gridDim.x / (unsigned)a.cluster;
+  int64_t row = blockIdx.x / (unsigned)a.cluster;
   const T* row_start = static_cast<const T*>(a.x) + row * a.stride;
-  Where next = where(row_start, 0);
+  Where next = where(row_start, first);
   if (row < a.rows) {
     for (int u0 = 0; u0 * kThreads < next.hi; u0 += kBlk) fetch(next, u0);
     fetch_ragged(next);
   }
-  for (; row < a.rows; row += gridDim.x) {
+  for (; row < a.rows; row += step) {
     const T* const start = row_start;
-    row_start += (int64_t)gridDim.x * a.stride;
+    row_start += step * a.stride;
     uint64_t thr = 0;  // composites have to exceed it
     float m = neg_inf(), s = 0.0f;
     uint4 mx = neg_inf_vec<DT>();
     int n = 0;
     if (tid == 0) n_list = 0;
-    for (int t0 = 0;; t0 += a.tile) {
+    for (int t0 = first;; t0 += a.tile) {
       const Where now = next;
       // where the copies of the listing pass go on: the next tile or row
-      const bool last = (unsigned)V - (unsigned)now.e0 <= (unsigned)(now.here * EPV);
-      next = where(last ? row_start : start, last ? 0 : t0 + a.tile);
-      if (last && row + gridDim.x >= a.rows) next.here = next.lo = next.hi = 0;
+      const bool last = t0 + a.tile >= first + a.part || (int64_t)now.e0 + now.here * EPV >= V;
+      next = where(last ? row_start : start, last ? first : t0 + a.tile);
+      if (last && row + step >= a.rows) next.here = next.lo = next.hi = 0;
       const int here = now.here;
 
       // the groups' largest, and with them the thread's
@@ -177,7 +216,7 @@ __global__ __launch_bounds__(kThreads, kCtas) void topk_rows(const TopkArgs a) {
         m2 = fmaxf(m2, gmax[g]);
         low = fminf(low, gmax[g] > neg_inf() ? gmax[g] : INFINITY);
       }
-      s *= ex2((shift_of(m) - shift_of(m2)) * a.c);
+      s *= ex2((m - shift_of(m2)) * a.c);
       m = m2;
       // the range of the groups' largest: finite ones
       int ihigh = __reduce_max_sync(kFull, as_ordered(fminf(m, 3.0e38f)));
@@ -326,37 +365,35 @@ __global__ __launch_bounds__(kThreads, kCtas) void topk_rows(const TopkArgs a) {
       }
       if (last) break;
     }
-    // in order
-    if (n <= kCountSort) {
-      uint64_t v = 0;
-      int above = 0;
-      if (tid >= n && tid < ((n + 3) & ~3)) list[tid] = 0;
-      __syncthreads();
-      if (tid < n) {
-        v = list[tid];
-#pragma unroll 2
-        for (int i = 0; i < n; i += 4) {
-          const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(list + i);
-          const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(list + i + 2);
-          above += (p.x > v) + (p.y > v) + (q.x > v) + (q.y > v);
-        }
+    order_list(list, n);
+    float M = cta_max(m, reinterpret_cast<float*>(ubuf));
+    float S = cta_sum(s * ex2((m - shift_of(M)) * a.c), reinterpret_cast<float*>(ubuf));
+    if (a.cluster > 1) {  // (a single row for each cluster: the tile's space is free)
+      uint64_t* all = reinterpret_cast<uint64_t*>(buf);  // k entries of each CTA
+      cluster_arrive();
+      cluster_wait();
+      for (int i = tid; i < a.k; i += kThreads) put_remote(all + rank * a.k + i, 0, i < n ? list[i] : 0);
+      if (tid == 0) {
+        put_remote(&parts[rank][0], 0, M);
+        put_remote(&parts[rank][1], 0, S);
       }
-      __syncthreads();
-      if (tid < n) list[above] = v;
-      __syncthreads();
-    } else {
+      cluster_arrive();
+      cluster_wait();
+      if (rank != 0) return;
+      list = all;
+      n = a.cluster * a.k;
       sort_list(list, n);
+      for (int i = 0; i < a.cluster; i++) M = fmaxf(M, parts[i][0]);
+      S = 0.0f;
+      for (int i = 0; i < a.cluster; i++)
+        S += parts[i][1] * ex2((parts[i][0] - shift_of(M)) * a.c);
     }
     for (int i = tid; i < a.k; i += kThreads) {
       const int32_t e = (int32_t)~(uint32_t)list[i];
       a.idx[row * a.k + i] = e;
       if (a.vals) static_cast<T*>(a.vals)[row * a.k + i] = start[e];
     }
-    if (a.lse) {
-      const float M = cta_max(m, reinterpret_cast<float*>(ubuf)), sh = shift_of(M);
-      const float S = cta_sum(s * ex2((shift_of(m) - sh) * a.c), reinterpret_cast<float*>(ubuf));
-      if (tid == 0) a.lse[row] = sh / a.tau + logf(S);
-    }
+    if (a.lse && tid == 0) a.lse[row] = shift_of(M) / a.tau + logf(S);
     __syncthreads();
   }
 }
@@ -370,7 +407,7 @@ cudaError_t launch(TopkArgs& a, cudaStream_t s) {
   const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
   if (!(configured.load() & bit)) {
     e = cudaFuncSetAttribute(topk_rows<DT, GROUPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmem);
+                             kSmem + kMaxCluster * kMaxK * 8);
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
@@ -380,14 +417,38 @@ cudaError_t launch(TopkArgs& a, cudaStream_t s) {
   while (a.cap < 3 * a.k) a.cap *= 2;
   const bool whole = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && a.stride % EPV == 0;
   const int64_t nv = (a.V + (whole ? 0 : EPV - 1) + EPV - 1) / EPV;
+  a.cluster = 1;  // few rows: more CTAs for each, down to two vectors a thread
+  while (a.cluster < kMaxCluster && a.rows * a.cluster * 2 <= num_sms() && nv > 4 * kThreads * a.cluster)
+    a.cluster *= 2;
+  a.part = (int)((nv + a.cluster - 1) / a.cluster);
   const int64_t most = (kSmem - a.cap * 8) / 16;
-  const int64_t tiles = (nv + most - 1) / most;
-  a.tile = (int)((nv + tiles - 1) / tiles);
+  const int64_t tiles = (a.part + most - 1) / most;
+  a.tile = (int)((a.part + tiles - 1) / tiles);
+  size_t bytes = (size_t)a.tile * 16;
+  if (a.cluster > 1) {  // the parts' entries, and what their sort pads
+    size_t n = 1;
+    while (n < (size_t)a.cluster * a.k) n *= 2;
+    bytes = std::max(bytes, n * 8);
+  }
+  a.list_at = (int)(bytes + 15) / 16;
   const int64_t slots = (int64_t)num_sms() * kCtas;
-  const int64_t rounds = (a.rows + slots - 1) / slots;
-  const unsigned grid = (unsigned)((a.rows + rounds - 1) / rounds);
-  topk_rows<DT, GROUPS><<<grid, kThreads, (size_t)a.tile * 16 + (size_t)a.cap * 8, s>>>(a);
-  return cudaGetLastError();
+  const int64_t rounds = (a.rows * a.cluster + slots - 1) / slots;
+  const int64_t clusters = (a.rows + rounds - 1) / rounds;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(clusters * a.cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)a.list_at * 16 + (size_t)a.cap * 8;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)a.cluster;
+  at.val.clusterDim.y = 1;
+  at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, topk_rows<DT, GROUPS>, a);
+  const cudaError_t last = cudaGetLastError();
+  return e != cudaSuccess ? e : last;
 }
 
 // Groups: at least 4 k of them while a thread has that many places.

@@ -49,6 +49,33 @@ __device__ __forceinline__ pair_t add2(pair_t a, pair_t b) { return __fadd2_rn(a
 __device__ __forceinline__ pair_t mul2(pair_t a, pair_t b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ pair_t ex2_2(pair_t v) { return pair(ex2(v.x), ex2(v.y)); }
 
+// Thread-block clusters: this CTA's place, the barrier over all their threads
+// (it orders memory), and stores to another CTA's shared memory.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address in CTA "rank" of what lies at "local" in this one.
+__device__ __forceinline__ uint32_t remote_at(const void* local, uint32_t rank) {
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(local);
+  uint32_t there;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
+  return there;
+}
+__device__ __forceinline__ void put_remote(const float* local, uint32_t rank, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote_at(local, rank)), "f"(v) : "memory");
+}
+__device__ __forceinline__ void put_remote(const uint64_t* local, uint32_t rank, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(remote_at(local, rank)), "l"(v) : "memory");
+}
+
 // Asynchronous 16-byte copy to shared memory.  A thread that reads back only
 // what it copied itself needs no barrier, only its own wait.
 __device__ __forceinline__ void copy_async(uint32_t smem, const void* p) {

@@ -43,6 +43,10 @@ def logits(rng, R, V, kind="normal"):
         x[:, V // 2] = 0.5
     elif kind == "zeros":
         x = np.where(rng.random((R, V)) < 0.5, 0.0, -0.0)
+    elif kind == "low":  # far below zero, where exp() of a logit itself is 0
+        x -= 400.0
+    elif kind == "high":
+        x += 400.0
     elif kind == "spiked":
         x[np.arange(R), rng.integers(V, size=R)] += 60
     return x
@@ -118,6 +122,33 @@ def test_topk_past_32_bit_offsets():
     want[idx[5].long().cpu().numpy()] -= 1 / 9
     assert g.data_ptr() == x.data_ptr()
     assert np.abs(f64(x[5]) - want).max() < 2.0 ** -9 and not f64(x[0]).any()
+
+
+@pytest.mark.parametrize("R,V,dtype,kind", [(1, 9, "f32", "low"), (3, 700, "bf16", "low"), (2, 50257, "f32", "low"),
+                                            (1, 140000, "f16", "low"), (2, 33001, "bf16", "high"), (700, 300, "f32", "low")])
+def test_topk_far_from_zero(R, V, dtype, kind):
+    x = place(logits(np.random.default_rng(V), R, V, kind), dtype)
+    k = min(V, 40)
+    idx, _, lse = pkg.topk_logits(x, k, temperature=0.8)
+    h, got = f64(x), f64(lse)
+    for r in range(R):
+        assert np.array_equal(idx[r].cpu().numpy(), ref.topk(h[r], k))
+        L = ref.lse(h[r] / 0.8)
+        assert abs(got[r] - L) <= ref.lse_tol(V, L)
+
+
+@pytest.mark.parametrize("R,V,k,dtype", [(1, 40000, 1024, "bf16"), (2, 100000, 700, "f32"), (3, 70000, 64, "f16"), (5, 131072, 256, "f32"),
+                                         (19, 33000, 100, "bf16"), (1, 16400, 3, "f32"), (1, 50257, 64, "bf16")])
+@pytest.mark.parametrize("kind", ["normal", "equal", "masked"])
+def test_topk_few_long_rows(R, V, k, dtype, kind):
+    x = place(logits(np.random.default_rng(V + k), R, V, kind), dtype, 1, 2)
+    idx, vals, lse = pkg.topk_logits(x, k)
+    h, got = f64(x), f64(lse)
+    for r in range(R):
+        assert np.array_equal(idx[r].cpu().numpy(), ref.topk(h[r], k))
+        L = ref.lse(h[r])
+        assert abs(got[r] - L) <= ref.lse_tol(V, L)
+    assert torch.equal(vals, torch.gather(x, 1, idx.long()))
 
 
 # ---- distillation -------------------------------------------------------------------------------
@@ -199,6 +230,36 @@ def test_distill(R, V, k, dtype, kind, tail, ce, tau, offset, pad):
     pkg.distill_loss_grad(x, it, vals, **args, grad=x)
     assert torch.equal(x, grad)
     assert torch.equal(wide[:, :offset], before) and torch.equal(wide[:, offset + V:], after)
+
+
+@pytest.mark.parametrize("R,V,k,dtype", [(2, 9, 3, "f32"), (3, 700, 20, "bf16"), (2, 50257, 64, "f32"), (2, 600011, 31, "f32"),
+                                         (400, 300, 5, "f16"), (1, 1100003, 40, "bf16")])
+@pytest.mark.parametrize("kind", ["low", "high"])
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_far_from_zero(R, V, k, dtype, kind, tail):
+    rng = np.random.default_rng(V)
+    x = place(logits(rng, R, V, kind), dtype)
+    idx, vals, tl = teacher(rng, f64(x), k, 1.5, "f32")
+    tl = tl if tail else None
+    y = rng.integers(V, size=R)
+    args = dict(teacher_lse=None if tl is None else torch.from_numpy(tl).cuda(), labels=torch.from_numpy(y).cuda(),
+                temperature=1.5, kd_weight=0.7, ce_weight=0.4)
+    loss, grad = pkg.distill_loss_grad(x, torch.from_numpy(idx).cuda(), vals, **args)
+    check_distill(x, idx, vals, tl, y, None, 1.5, 0.7, 0.4, dtype, loss, grad)
+
+
+def test_distill_listed_words_masked_far_below_zero():
+    # a bucket whose listed words the student masks while the others are far below zero: p_listed is 0, not NaN
+    for V in (900, 300000):  # (the long row does not fit on chip)
+        x = np.full((1, V), -500.0)
+        x[0, :4] = -INF
+        xt = place(x, "f32")
+        idx = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+        vals = torch.tensor([[1.0, 0.5, -INF, -INF]], device="cuda")
+        tl = np.array([2.0], np.float32)
+        loss, grad = pkg.distill_loss_grad(xt, idx, vals, teacher_lse=torch.from_numpy(tl).cuda())
+        assert float(loss) == INF  # q > 0 where p = 0
+        check_distill(xt, idx.cpu().numpy(), vals, tl, None, None, 1.0, 1.0, 0.0, "f32", loss, grad)
 
 
 def test_distill_rows_of_weight_zero_are_not_read():
@@ -330,7 +391,10 @@ ROUTE = [  # tokens, experts, k, groups, dtype, kind, renorm, offset, pad
     (40, 512, 8, 1, "f16", "masked", True, 3, 1), (33, 1024, 32, 5, "f32", "masked", False, 0, 0),
     (2000, 16, 4, 40, "bf16", "masked", True, 8, 8), (64, 31, 31, 1, "f32", "equal", True, 0, 0),
     (0, 16, 2, 1, "bf16", "normal", True, 0, 0), (0, 16, 2, 3, "f32", "normal", True, 0, 0),
-    (5000, 128, 8, 7, "bf16", "normal", True, 0, 0),
+    (5000, 128, 8, 7, "bf16", "normal", True, 0, 0), (300, 48, 4, 2, "f32", "low", True, 0, 0),
+    (300, 200, 7, 1, "bf16", "high", False, 0, 0), (700, 64, 6, 300, "bf16", "normal", True, 0, 0),
+    (3000, 256, 8, 2, "bf16", "equal", True, 0, 0), (500, 100, 24, 3, "f32", "normal", True, 0, 0),
+    (20, 1000, 20, 2, "f16", "ties", False, 0, 0), (9000, 4, 1, 2, "bf16", "normal", False, 0, 0),
 ]
 
 
