@@ -15,6 +15,7 @@
 //
 // A CTA takes a row: one pass for the running maxima and sums, one for the
 // gradient.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -228,7 +229,7 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
 
 // ---- Rows held on chip -------------------------------------------------------
 
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 8;
 
 // Threads of a CTA, vectors of a row that each of them has at most, CTAs of an
 // SM, teacher entries that a thread looks after: for long parts of a row, for
@@ -238,6 +239,7 @@ template <int NT_, int VECS_, int MINB_, int ENT_>
 struct Shape {
   static constexpr int NT = NT_, VECS = VECS_, MINB = MINB_, ENT = ENT_;
   static constexpr int PART = NT_ * VECS_, MAXK = NT_ * ENT_;
+  static constexpr int MOST = 13824;  // vectors that fit at all (216 KB)
 };
 using Wide = Shape<256, 16, 3, 1>;
 using Narrow = Shape<128, 8, 8, 2>;
@@ -299,7 +301,7 @@ template <int DT, bool TWO, bool BUCKET, class SH>
 __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillArgs a) {
   using E = Elem<DT>;
   using T = typename E::T;
-  constexpr int EPV = E::kPerVec, NT = SH::NT, VECS = SH::VECS, ENT = SH::ENT;
+  constexpr int EPV = E::kPerVec, NT = SH::NT, ENT = SH::ENT;
   constexpr int kWarps = NT / 32;
   constexpr int BLK = 2;  // vectors that a thread handles at a time
   extern __shared__ __align__(16) uint4 buf[];  // the part of the row
@@ -414,7 +416,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
   Where at = where(row_start);
   if (w != 0.0f) {
     load_side(row);
-    for (int u0 = 0; u0 < VECS; u0 += BLK) fetch(at, u0);
+    for (int u0 = 0; u0 * NT < at.hi; u0 += BLK) fetch(at, u0);
     fetch_ragged(at);
   }
   for (; row < a.rows; row += step) {
@@ -735,15 +737,13 @@ cudaError_t launch_parts(const DistillArgs& a, cudaStream_t s) {
   const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
   if (!(configured.load() & bit)) {
     e = cudaFuncSetAttribute(distill_parts<DT, TWO, BUCKET, SH>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, SH::PART * 16);
-    if (e == cudaSuccess)  // clusters of 16
-      e = cudaFuncSetAttribute(distill_parts<DT, TWO, BUCKET, SH>,
-                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, SH::MOST * 16);
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
   // as many clusters as the GPU holds at once, evened out over the rounds
-  const int64_t slots = (int64_t)num_sms() * SH::MINB / a.cluster;
+  const int64_t ctas = std::min<int64_t>(SH::MINB, 224 * 1024 / (a.part_vecs * 16 + 4096));
+  const int64_t slots = std::max<int64_t>((int64_t)num_sms() * ctas / a.cluster, 1);
   const int64_t rounds = (a.rows + slots - 1) / slots;
   const int64_t clusters = (a.rows + rounds - 1) / rounds;
   cudaLaunchConfig_t cfg{};
@@ -775,15 +775,16 @@ cudaError_t launch_distill(DistillArgs& a, cudaStream_t s) {
   const bool whole = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && a.stride % EPV == 0;
   const int64_t nv = (a.V + (whole ? 0 : EPV - 1) + EPV - 1) / EPV;
   cudaError_t e;
-  if (nv > (int64_t)Wide::PART * kMaxCluster) {
+  if (nv > (int64_t)Wide::MOST * kMaxCluster) {
     const int64_t cap = (int64_t)num_sms() * 4;
     distill_rows<DT><<<(unsigned)(a.rows < cap ? a.rows : cap), kThreads, 0, s>>>(a);
     e = cudaSuccess;
   } else {
     a.cluster = 1;
-    while (nv > (int64_t)Wide::PART * a.cluster) a.cluster *= 2;
+    // parts that share an SM three at a time, larger ones only in clusters of 8
+    while (a.cluster < kMaxCluster && nv > (int64_t)Wide::PART * a.cluster) a.cluster *= 2;
     // few rows: more CTAs for each, down to a vector or two a thread
-    while (a.cluster < 8 && a.rows * a.cluster * 2 <= num_sms() && nv > Narrow::NT * 2 * a.cluster)
+    while (a.cluster < kMaxCluster && a.rows * a.cluster <= num_sms() && nv > Narrow::NT * 2 * a.cluster)
       a.cluster *= 2;
     a.part_vecs = (int)((nv + a.cluster - 1) / a.cluster);
     if (a.part_vecs <= Narrow::PART && a.k <= Narrow::MAXK) e = launch_sized<DT, Narrow>(a, s);

@@ -31,16 +31,20 @@
 namespace scape {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kCtas = 3;   // CTAs that share an SM
-constexpr int kSmem = (228 / kCtas - 5) * 1024;  // of each one's: tile and list
-constexpr int kBlk = 2;    // vectors a thread handles at a time
+// Threads of a CTA and CTAs of an SM, for long and for short rows.
+template <int NT_, int CTAS_>
+struct Shape {
+  static constexpr int NT = NT_, CTAS = CTAS_;
+  static constexpr int kSmem = (228 / CTAS_ - 5) * 1024;  // bytes of a CTA's tile and list
+};
+using Wide = Shape<256, 3>;
+using Narrow = Shape<128, 7>;
+constexpr int kNarrowVecs = 1024;  // rows up to this many vectors are short
+constexpr int kBlk = 2;            // vectors a thread handles at a time
 constexpr int kMaxK = 1024;
 constexpr int kBins = 256;
 constexpr int kMaxCluster = 8;
 constexpr int kHits = 1024;
-constexpr int kCountSort = 256;  // lists up to this are sorted by counting
 
 struct TopkArgs {
   const void* x;
@@ -58,6 +62,7 @@ struct TopkArgs {
 };
 
 // Sorts list[0..n) in descending order (bitonic, padded with 0).
+template <int kThreads>
 __device__ void sort_list(uint64_t* list, int n) {
   int P = 1;
   while (P < n) P <<= 1;
@@ -79,9 +84,10 @@ __device__ void sort_list(uint64_t* list, int n) {
 }
 
 // The same, for short lists by counting what is above each.
+template <int kThreads>
 __device__ void order_list(uint64_t* list, int n) {
-  if (n > kCountSort) {
-    sort_list(list, n);
+  if (n > kThreads) {
+    sort_list<kThreads>(list, n);
     return;
   }
   const int tid = threadIdx.x;
@@ -113,11 +119,11 @@ __device__ __forceinline__ float from_ordered(int i) {
 }
 
 // GROUPS: groups of a thread (1, 2, 4 or 8 for 16-bit elements, up to 4 else).
-template <int DT, int GROUPS>
-__global__ __launch_bounds__(kThreads, kCtas) void topk_rows(const TopkArgs a) {
+template <int DT, int GROUPS, class SH>
+__global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) {
   using E = Elem<DT>;
   using T = typename E::T;
-  constexpr int EPV = E::kPerVec;
+  constexpr int EPV = E::kPerVec, kThreads = SH::NT, kWarps = kThreads / 32;
   extern __shared__ __align__(16) uint4 buf[];                 // the tile
   uint64_t* list = reinterpret_cast<uint64_t*>(buf + a.list_at);  // a.cap entries
   __shared__ __align__(16) uint32_t hist[kBins];
@@ -330,7 +336,7 @@ __global__ __launch_bounds__(kThreads, kCtas) void topk_rows(const TopkArgs a) {
       if (!done) {
         // too many: cut the list to the k best of before, then take the tile's own
         // k best above them, found bit by bit over further reads of it
-        sort_list(list, n);
+        sort_list<kThreads>(list, n);
         if (n >= a.k) {
           n = a.k;
           thr = list[n - 1];
@@ -365,7 +371,7 @@ __global__ __launch_bounds__(kThreads, kCtas) void topk_rows(const TopkArgs a) {
       }
       if (last) break;
     }
-    order_list(list, n);
+    order_list<kThreads>(list, n);
     float M = cta_max(m, reinterpret_cast<float*>(ubuf));
     float S = cta_sum(s * ex2((m - shift_of(M)) * a.c), reinterpret_cast<float*>(ubuf));
     if (a.cluster > 1) {  // (a single row for each cluster: the tile's space is free)
@@ -382,7 +388,7 @@ __global__ __launch_bounds__(kThreads, kCtas) void topk_rows(const TopkArgs a) {
       if (rank != 0) return;
       list = all;
       n = a.cluster * a.k;
-      sort_list(list, n);
+      sort_list<kThreads>(list, n);
       for (int i = 0; i < a.cluster; i++) M = fmaxf(M, parts[i][0]);
       S = 0.0f;
       for (int i = 0; i < a.cluster; i++)
@@ -398,7 +404,7 @@ __global__ __launch_bounds__(kThreads, kCtas) void topk_rows(const TopkArgs a) {
   }
 }
 
-template <int DT, int GROUPS>
+template <int DT, int GROUPS, class SH>
 cudaError_t launch(TopkArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> configured{0};  // the shared-memory opt-in is per device
   int dev = 0;
@@ -406,8 +412,8 @@ cudaError_t launch(TopkArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
   if (!(configured.load() & bit)) {
-    e = cudaFuncSetAttribute(topk_rows<DT, GROUPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmem + kMaxCluster * kMaxK * 8);
+    e = cudaFuncSetAttribute(topk_rows<DT, GROUPS, SH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             SH::kSmem + kMaxCluster * kMaxK * 8);
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
@@ -418,10 +424,10 @@ cudaError_t launch(TopkArgs& a, cudaStream_t s) {
   const bool whole = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && a.stride % EPV == 0;
   const int64_t nv = (a.V + (whole ? 0 : EPV - 1) + EPV - 1) / EPV;
   a.cluster = 1;  // few rows: more CTAs for each, down to two vectors a thread
-  while (a.cluster < kMaxCluster && a.rows * a.cluster * 2 <= num_sms() && nv > 4 * kThreads * a.cluster)
+  while (a.cluster < kMaxCluster && a.rows * a.cluster <= num_sms() && nv > 4 * SH::NT * a.cluster)
     a.cluster *= 2;
   a.part = (int)((nv + a.cluster - 1) / a.cluster);
-  const int64_t most = (kSmem - a.cap * 8) / 16;
+  const int64_t most = (SH::kSmem - a.cap * 8) / 16;
   const int64_t tiles = (a.part + most - 1) / most;
   a.tile = (int)((a.part + tiles - 1) / tiles);
   size_t bytes = (size_t)a.tile * 16;
@@ -431,12 +437,12 @@ cudaError_t launch(TopkArgs& a, cudaStream_t s) {
     bytes = std::max(bytes, n * 8);
   }
   a.list_at = (int)(bytes + 15) / 16;
-  const int64_t slots = (int64_t)num_sms() * kCtas;
+  const int64_t slots = (int64_t)num_sms() * SH::CTAS;
   const int64_t rounds = (a.rows * a.cluster + slots - 1) / slots;
   const int64_t clusters = (a.rows + rounds - 1) / rounds;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(clusters * a.cluster));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(SH::NT);
   cfg.dynamicSmemBytes = (size_t)a.list_at * 16 + (size_t)a.cap * 8;
   cfg.stream = s;
   cudaLaunchAttribute at{};
@@ -446,18 +452,25 @@ cudaError_t launch(TopkArgs& a, cudaStream_t s) {
   at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = a.cluster > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, topk_rows<DT, GROUPS>, a);
+  e = cudaLaunchKernelEx(&cfg, topk_rows<DT, GROUPS, SH>, a);
   const cudaError_t last = cudaGetLastError();
   return e != cudaSuccess ? e : last;
 }
 
 // Groups: at least 4 k of them while a thread has that many places.
+template <int DT, class SH>
+cudaError_t launch_groups(TopkArgs& a, cudaStream_t s) {
+  if (4 * a.k <= SH::NT) return launch<DT, 1, SH>(a, s);
+  if (4 * a.k <= 2 * SH::NT) return launch<DT, 2, SH>(a, s);
+  if (DT == SCAPE_F32 || 4 * a.k <= 4 * SH::NT) return launch<DT, 4, SH>(a, s);
+  return launch<DT, Elem<DT>::kPerVec, SH>(a, s);
+}
+
 template <int DT>
 cudaError_t launch_dt(TopkArgs& a, cudaStream_t s) {
-  if (4 * a.k <= kThreads) return launch<DT, 1>(a, s);
-  if (4 * a.k <= 2 * kThreads) return launch<DT, 2>(a, s);
-  if (DT == SCAPE_F32 || 4 * a.k <= 4 * kThreads) return launch<DT, 4>(a, s);
-  return launch<DT, Elem<DT>::kPerVec>(a, s);
+  // (a narrow CTA's list holds 3 k entries beside its row for k up to this)
+  if (a.V <= (kNarrowVecs - 1) * Elem<DT>::kPerVec && a.k <= 256) return launch_groups<DT, Narrow>(a, s);
+  return launch_groups<DT, Wide>(a, s);
 }
 
 int fail(int code, const char* fmt, ...) {
