@@ -407,7 +407,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     if (y >= 0 && tid == 0) xy = E::load(w.p + (y - w.e0));
     tlse = raw_lse;
   };
-  if (a.cluster > 1) cluster_arrive();  // "this CTA runs": its shared memory may be written
+  if (a.cluster > 1) cluster_arrive_relaxed();  // "this CTA runs": its shared memory may be written
   bool met = a.cluster == 1;
   int turn = 0;
   int64_t row = blockIdx.x / (unsigned)a.cluster;
@@ -611,9 +611,13 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
           if (i / kShared != (int)rank) put_remote(to + i % kShared, (uint32_t)(i / kShared), from[i % kShared]);
         cluster_arrive();
         cluster_wait();
-        if (lane < a.cluster) q = parts[turn][lane];
-        merge(a.cluster);
-        q.b = shfl_sum(q.b, a.cluster);
+        q = parts[turn][min(lane, a.cluster - 1)];
+        if (lane >= a.cluster) {
+          q.m = q.tm = neg_inf();
+          q.s = q.s1 = q.ts = q.ts1 = q.b = 0.0f;
+        }
+        merge(kMaxCluster);
+        q.b = shfl_sum(q.b, kMaxCluster);
       }
       if (lane == 0) {
         // the teacher: q_i = exp(t_i - base) / rz, Q = sum q_i
@@ -655,7 +659,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
       }
     } else if (a.cluster > 1) {
       if (!met) cluster_wait();
-      cluster_arrive();
+      cluster_arrive_relaxed();
       cluster_wait();
     }
     met = true;
@@ -782,10 +786,10 @@ cudaError_t launch_distill(DistillArgs& a, cudaStream_t s) {
   } else {
     a.cluster = 1;
     // parts that share an SM three at a time, larger ones only in clusters of 8
-    while (a.cluster < kMaxCluster && nv > (int64_t)Wide::PART * a.cluster) a.cluster *= 2;
+    while (a.cluster < kMaxCluster && nv > (int64_t)Wide::PART * a.cluster) a.cluster++;
     // few rows: more CTAs for each, down to a vector or two a thread
     while (a.cluster < kMaxCluster && a.rows * a.cluster <= num_sms() && nv > Narrow::NT * 2 * a.cluster)
-      a.cluster *= 2;
+      a.cluster = std::min(2 * a.cluster, kMaxCluster);
     a.part_vecs = (int)((nv + a.cluster - 1) / a.cluster);
     if (a.part_vecs <= Narrow::PART && a.k <= Narrow::MAXK) e = launch_sized<DT, Narrow>(a, s);
     else if (a.k <= Wide::MAXK) e = launch_sized<DT, Wide>(a, s);
