@@ -337,7 +337,8 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     return w;
   };
   const uint32_t buf_at = (uint32_t)__cvta_generic_to_shared(buf) + tid * 16;
-  // starts the copies of the whole vectors among BLK of this thread's
+  // starts the copies of the whole vectors among BLK of this thread's (w.hi is 0
+  // for a row that is not read)
   auto fetch = [&](const Where& w, int u0) {
     const T* p = w.p + (int64_t)(u0 * NT + tid) * EPV;
     const uint32_t to = buf_at + u0 * NT * 16;
@@ -415,15 +416,15 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
   int64_t row = blockIdx.x / (unsigned)a.cluster;
   const T* row_start = static_cast<const T*>(a.x) + row * a.stride;
   Where at = where(row_start);  // this row, then the next one
+  float w = row < a.rows ? weight_of(row) : 0.0f;
   // starts the copies of the next row that the blocks of a pass did not reach
   auto fetch_rest = [&](int u0) {
     for (; u0 * NT < at.hi; u0 += BLK) fetch(at, u0);
-    fetch_ragged(at);
+    if (w != 0.0f) fetch_ragged(at);
   };
   if (a.cluster > 1) cluster_arrive_relaxed();  // "this CTA runs": its shared memory may be written
   bool met = a.cluster == 1;
   int turn = 0;
-  float w = row < a.rows ? weight_of(row) : 0.0f;
   if (w != 0.0f) {
     load_side(row);
     for (int u0 = 0; u0 * NT < at.hi; u0 += BLK) fetch(at, u0);
@@ -437,7 +438,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     row_start += step * a.stride;
     w = row2 < a.rows ? weight_of(row2) : 0.0f;
     at = where(row_start);
-    if (w == 0.0f) at.hi = at.here = 0;  // nothing to copy
+    if (w == 0.0f) at.hi = 0;  // not read
     T* g = a.grad ? static_cast<T*>(a.grad) + row * a.gstride + now.e0 : nullptr;
     const bool same = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(now.p)) & 15u) == 0;
     // writes vector u of this thread, to p
@@ -459,11 +460,8 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
       if (g)
         for (int u = 0; u * NT < here; u++) store(gt + (int64_t)u * NT * EPV, u, make_uint4(0, 0, 0, 0));
       if (a.loss && tid == 0 && rank == 0) a.loss[row] = 0.0f;
-      if (w != 0.0f) {
-        load_side(row2);
-        for (int u0 = 0; u0 * NT < at.hi; u0 += BLK) fetch(at, u0);
-        fetch_ragged(at);
-      }
+      if (w != 0.0f) load_side(row2);
+      fetch_rest(0);
       continue;
     }
     copy_wait();

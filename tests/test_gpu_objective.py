@@ -151,6 +151,23 @@ def test_topk_few_long_rows(R, V, k, dtype, kind):
     assert torch.equal(vals, torch.gather(x, 1, idx.long()))
 
 
+@pytest.mark.parametrize("R,V,k,dtype,kind", [(4000, 300, 7, "f32", "ties"), (2500, 1003, 64, "bf16", "normal"), (1300, 9001, 33, "bf16", "ties"),
+                                              (900, 33001, 200, "f16", "normal"), (1000, 50257, 64, "bf16", "normal"), (500, 131075, 256, "f32", "normal")])
+def test_topk_many_rows(R, V, k, dtype, kind):
+    # every CTA takes several rows
+    x = torch.randn(R, V, device="cuda", generator=torch.Generator("cuda").manual_seed(V)).mul_(3)
+    x = (x.mul(2).round().div(2) if kind == "ties" else x).to(DT[dtype])
+    idx, vals, lse = pkg.topk_logits(x, k)
+    # in descending order, ties by index, and nothing left out is larger than the last one (or equal, at a lower index)
+    v, i = vals.float(), idx.long()
+    assert torch.equal(vals, torch.gather(x, 1, i))
+    assert bool(((v[:, :-1] > v[:, 1:]) | ((v[:, :-1] == v[:, 1:]) & (i[:, :-1] < i[:, 1:]))).all())
+    last, at = v[:, -1:], i[:, -1:]
+    better = (x.float() > last) | ((x.float() == last) & (torch.arange(V, device="cuda") <= at))
+    assert bool((better.sum(1) == k).all())
+    assert float((lse.double() - torch.logsumexp(x.double(), 1)).abs().max()) <= ref.lse_tol(V, 20.0)
+
+
 # ---- distillation -------------------------------------------------------------------------------
 
 DISTILL = [  # rows, vocab, k, dtype, kind, tail, ce, tau, offset, pad
@@ -274,6 +291,37 @@ def test_distill_rows_of_weight_zero_are_not_read():
     assert not f64(grad)[[0, 1, 3]].any() and np.isfinite(f64(grad)).all()
 
 
+@pytest.mark.parametrize("R,V,k,dtype,tail", [(4000, 300, 7, "f32", True), (3001, 1003, 20, "bf16", False), (1300, 9001, 33, "bf16", True),
+                                              (900, 33001, 64, "f16", True), (530, 50257, 64, "bf16", False), (250, 131075, 300, "f32", True)])
+def test_distill_many_rows(R, V, k, dtype, tail):
+    # every CTA takes several rows, some of them of weight 0, in any order
+    rng = np.random.default_rng(V)
+    x = torch.randn(R, V, device="cuda", generator=torch.Generator("cuda").manual_seed(V)).mul_(3).to(DT[dtype])
+    z = x.float() * 0.9 + torch.randn(R, V, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    vals, idx = torch.topk(z, k, dim=1)
+    idx = idx.int()
+    tl = torch.logsumexp(z / 2.0, 1) if tail else None
+    y = rng.integers(V, size=R)
+    w = np.where(rng.random(R) < 0.3, 0.0, 0.5 + rng.random(R)).astype(np.float32)
+    w[-3:] = 0.0
+    for masked in (False, True):
+        wt = torch.from_numpy(w).cuda() if masked else None
+        args = dict(teacher_lse=tl, labels=torch.from_numpy(y).cuda(), row_weight=wt, temperature=2.0, kd_weight=0.7, ce_weight=0.4)
+        grad = torch.full_like(x, 7.0)
+        loss, _ = pkg.distill_loss_grad(x, idx, vals, **args, grad=grad)
+        assert torch.equal(pkg.distill_loss(x, idx, vals, **args), loss)
+        if masked:
+            off = wt == 0
+            assert not grad[off].any() and not loss[off].any()
+        some = np.unique(np.concatenate([rng.integers(R, size=10), [0, R - 4, R - 1]]))
+        st = torch.from_numpy(some).cuda()
+        check_distill(x[st], idx[st].cpu().numpy(), vals[st], None if tl is None else f64(tl)[some], y[some],
+                      w[some] if masked else None, 2.0, 0.7, 0.4, dtype, loss[st], grad[st])
+        # all rows: a row's gradient sums to 0
+        sums = grad.float().sum(1).abs() / grad.float().abs().sum(1).clamp(min=1e-20)
+        assert float(sums.max()) < 0.05
+
+
 def test_distill_rows_without_a_teacher():
     rng = np.random.default_rng(3)
     x = place(logits(rng, 3, 2000), "f32")
@@ -394,6 +442,8 @@ ROUTE = [  # tokens, experts, k, groups, dtype, kind, renorm, offset, pad
     (5000, 128, 8, 7, "bf16", "normal", True, 0, 0), (300, 48, 4, 2, "f32", "low", True, 0, 0),
     (300, 200, 7, 1, "bf16", "high", False, 0, 0), (700, 64, 6, 300, "bf16", "normal", True, 0, 0),
     (3000, 256, 8, 2, "bf16", "equal", True, 0, 0), (500, 100, 24, 3, "f32", "normal", True, 0, 0),
+    (40000, 64, 6, 9, "bf16", "normal", True, 0, 0), (90000, 8, 2, 3, "f32", "ties", True, 0, 0),
+    (20000, 256, 8, 1, "f32", "normal", False, 0, 0), (12000, 100, 3, 5, "bf16", "ties", True, 0, 0),
     (20, 1000, 20, 2, "f16", "ties", False, 0, 0), (9000, 4, 1, 2, "bf16", "normal", False, 0, 0),
 ]
 
