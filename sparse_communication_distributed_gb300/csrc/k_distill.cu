@@ -404,7 +404,9 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
         const int l = e - w.e0;  // e < 2^20, e0 > -8
         if (l >= 0 && l < w.here * EPV) {
           el[h] = l;
-          ex[h] = E::load(reinterpret_cast<const T*>(buf) + l);
+          // (from shared memory where a barrier comes before the copies of the
+          // next row that follow)
+          ex[h] = E::load((BUCKET || a.grad ? reinterpret_cast<const T*>(buf) : w.p) + l);
         }
       }
     }
@@ -413,61 +415,70 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     if (y >= 0 && tid == 0) xy = E::load(w.p + (y - w.e0));
     tlse = raw_lse;
   };
-  int64_t row = blockIdx.x / (unsigned)a.cluster;
-  const T* row_start = static_cast<const T*>(a.x) + row * a.stride;
-  Where at = where(row_start);  // this row, then the next one
-  float w = row < a.rows ? weight_of(row) : 0.0f;
-  // starts the copies of the next row that the blocks of a pass did not reach
-  auto fetch_rest = [&](int u0) {
-    for (; u0 * NT < at.hi; u0 += BLK) fetch(at, u0);
-    if (w != 0.0f) fetch_ragged(at);
+  auto row_at = [&](int64_t row) { return static_cast<const T*>(a.x) + row * a.stride; };
+  // writes vector i of a part of a gradient's row that starts at g
+  auto put = [&](T* g, const Where& w, bool same, int i, const uint4 v) {
+    T* p = g + i * EPV;
+    if (same && i >= w.lo && i < w.hi) {
+      *reinterpret_cast<uint4*>(p) = v;
+    } else if (i < w.here) {
+      const T* t = reinterpret_cast<const T*>(&v);
+#pragma unroll
+      for (int j = 0; j < EPV; j++) {
+        const int e = w.e0 + i * EPV + j;
+        if (e >= 0 && e < V) p[j] = t[j];
+      }
+    }
   };
+  auto grad_at = [&](int64_t row, const Where& w) {
+    return a.grad ? static_cast<T*>(a.grad) + row * a.gstride + w.e0 : nullptr;
+  };
+  auto alike = [](const T* g, const T* p) {  // in vectors at the same places
+    return ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(p)) & 15u) == 0;
+  };
+  // a row of weight 0
+  auto fill = [&](int64_t row) {
+    const Where w = where(row_at(row));
+    T* const g = grad_at(row, w);
+    const bool same = alike(g, w.p);
+    if (g)
+      for (int i = tid; i < w.here; i += NT) put(g, w, same, i, make_uint4(0, 0, 0, 0));
+    if (a.loss && tid == 0 && rank == 0) a.loss[row] = 0.0f;
+  };
+  auto weight_or_1 = [&](int64_t row) { return row < a.rows ? weight_of(row) : 1.0f; };
   if (a.cluster > 1) cluster_arrive_relaxed();  // "this CTA runs": its shared memory may be written
   bool met = a.cluster == 1;
   int turn = 0;
-  if (w != 0.0f) {
-    load_side(row);
-    for (int u0 = 0; u0 * NT < at.hi; u0 += BLK) fetch(at, u0);
-    fetch_ragged(at);
+  // (the whole cluster agrees on which rows are read)
+  int64_t row = blockIdx.x / (unsigned)a.cluster;
+  float w = weight_or_1(row);
+  while (w == 0.0f) {
+    fill(row);
+    row += step;
+    w = weight_or_1(row);
   }
-  for (; row < a.rows; row += step) {
-    const int64_t row2 = row + step;
+  bool more = row < a.rows;  // a row to copy: this one, then the next that is read
+  Where at = where(row_at(more ? row : 0));
+  // starts the copies of that row that the blocks of a pass did not reach
+  auto fetch_rest = [&](int u0) {
+    for (; u0 * NT < at.hi; u0 += BLK) fetch(at, u0);
+    if (more) fetch_ragged(at);
+  };
+  if (more) {
+    load_side(row);
+    fetch_rest(0);
+  }
+  while (row < a.rows) {
     const float w_now = w;
     const Where now = at;
     const int here = now.here;
-    row_start += step * a.stride;
-    w = row2 < a.rows ? weight_of(row2) : 0.0f;
-    at = where(row_start);
-    if (w == 0.0f) at.hi = 0;  // not read
-    T* g = a.grad ? static_cast<T*>(a.grad) + row * a.gstride + now.e0 : nullptr;
-    const bool same = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(now.p)) & 15u) == 0;
-    // writes vector u of this thread, to p
-    auto store = [&](T* p, int u, const uint4 v) {
-      const int i = u * NT + tid;
-      if (same && i >= now.lo && i < now.hi) {
-        *reinterpret_cast<uint4*>(p) = v;
-      } else if (i < here) {
-        const T* t = reinterpret_cast<const T*>(&v);
-#pragma unroll
-        for (int j = 0; j < EPV; j++) {
-          const int e = now.e0 + i * EPV + j;
-          if (e >= 0 && e < V) p[j] = t[j];
-        }
-      }
-    };
-    T* const gt = g + tid * EPV;
-    if (w_now == 0.0f) {  // the whole cluster agrees
-      if (g)
-        for (int u = 0; u * NT < here; u++) store(gt + (int64_t)u * NT * EPV, u, make_uint4(0, 0, 0, 0));
-      if (a.loss && tid == 0 && rank == 0) a.loss[row] = 0.0f;
-      if (w != 0.0f) load_side(row2);
-      fetch_rest(0);
-      continue;
-    }
+    int64_t row2 = row + step;
+    w = weight_or_1(row2);
+    T* const g = grad_at(row, now);
+    const bool same = alike(g, now.p);
     copy_wait();
     __syncthreads();
     take_side(now);
-    if (w != 0.0f) load_side(row2);
     if (BUCKET) {
       __syncthreads();
 #pragma unroll
@@ -509,6 +520,15 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
       for (int j = 1; j < EPV; j++) q.m = fmaxf(q.m, x[j]);
       q.m = shfl_max(q.m, 32);
     }
+    // the next row that is read
+    while (w == 0.0f) {
+      row2 += step;
+      w = weight_or_1(row2);
+    }
+    more = row2 < a.rows;
+    at = where(row_at(more ? row2 : row));
+    if (more) load_side(row2);
+    else at.hi = 0;
     const pair_t c2 = pair(a.c, a.c), l2 = pair(kLog2e, kLog2e);
     {
       const float sh = shift_of(q.m);
@@ -686,7 +706,6 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
         const pair_t v = mul2(k1, e);
         return EXPS == kTwo ? fma2(k2, ex2_2(fma2(x, l2, ml)), v) : v;
       };
-      T* p = gt;
       const int u0 = each([&](int u0) { fetch(at, u0); },
                           [&](const uint4 r, int u) {
         float x[EPV];
@@ -697,8 +716,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
           x[j] = f.x;
           x[j + 1] = f.y;
         }
-        store(p, u, E::pack(x));
-        p += NT * EPV;
+        put(g, now, same, u * NT + tid, E::pack(x));
       });
       fetch_rest(u0);
       const int ly = y - now.e0;
@@ -718,6 +736,8 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
       }
       if (y_here && !y_listed && tid == 0) g[ly] = E::make(grad_of(pair(xy, xy)).x - t.C1);
     }
+    for (row += step; row < min(row2, a.rows); row += step) fill(row);
+    row = row2;
     turn ^= 1;
   }
   if (!met) cluster_wait();
