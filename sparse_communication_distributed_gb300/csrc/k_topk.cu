@@ -8,12 +8,13 @@
 // elements (a group is one place or a few of the vectors that a thread sees),
 // the group's largest element so far.  At least k elements reach the k-th
 // largest of these G, so nothing below it is among the row's k best; a histogram
-// of the G over their range gives a bound just under it.  A second pass lists
-// what reaches the bound -- for logits in no special order k (1 + k / 2G)
-// elements of a first tile, a t-th part of that of the t-th tile -- and sums the
-// exponentials.  The list is sorted in the end.  Where too much reaches the
-// bound (many equal logits, few above -inf, adverse orders), the tile is read
-// again and its own k-th best composite is found bit by bit.
+// of the G over their range gives a bound just under it.  A second pass notes the
+// vectors that reach the bound -- for logits in no special order k (1 + k / 2G) of
+// a first tile, a t-th part of that of the t-th tile -- and sums the exponentials.
+// In the end the elements of the vectors noted that reach the last bound are
+// listed and sorted.  Where too much reaches the bound (many equal logits, few
+// above -inf, adverse orders), the tile is read again and its own k-th best
+// composite is found bit by bit.
 //
 // Few rows: a cluster of CTAs takes a row, each a part of it; the parts' k best
 // go to the first CTA's shared memory and are sorted once more.
@@ -35,7 +36,7 @@ namespace {
 template <int NT_, int CTAS_>
 struct Shape {
   static constexpr int NT = NT_, CTAS = CTAS_;
-  static constexpr int kSmem = (228 / CTAS_ - 5) * 1024;  // bytes of a CTA's tile and list
+  static constexpr int kSmem = (228 / CTAS_ - 3) * 1024;  // bytes of a CTA's tile, list and hits
 };
 using Wide = Shape<256, 3>;
 using Narrow = Shape<128, 7>;
@@ -44,7 +45,6 @@ constexpr int kBlk = 2;            // vectors a thread handles at a time
 constexpr int kMaxK = 1024;
 constexpr int kBins = 256;
 constexpr int kMaxCluster = 8;
-constexpr int kHits = 1024;
 
 struct TopkArgs {
   const void* x;
@@ -53,6 +53,7 @@ struct TopkArgs {
   int cap;          // list entries; k of an earlier tile and k new ones always fit
   int tile;         // vectors of a tile
   int list_at;      // where the list begins, in vectors
+  int hits;         // vectors that can be noted
   int cluster;      // CTAs of a row
   int part;         // vectors of each one's part
   float tau, c;     // temperature, log2(e) / temperature
@@ -126,10 +127,11 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
   constexpr int EPV = E::kPerVec, kThreads = SH::NT, kWarps = kThreads / 32;
   extern __shared__ __align__(16) uint4 buf[];                 // the tile
   uint64_t* list = reinterpret_cast<uint64_t*>(buf + a.list_at);  // a.cap entries
+  // vectors of the row with something at the bound: a.hits entries
+  uint32_t* const hits = reinterpret_cast<uint32_t*>(list + a.cap);
   __shared__ __align__(16) uint32_t hist[kBins];
   __shared__ __align__(16) int range[2][kWarps];
   __shared__ uint32_t ubuf[32];
-  __shared__ uint16_t hits[kHits];  // vectors of the tile with something at the bound
   __shared__ float parts[kMaxCluster][2];  // maximum and sum of each CTA of a row
   __shared__ uint32_t n_list, n_hits;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -192,12 +194,69 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
   }
   for (; row < a.rows; row += step) {
     const T* const start = row_start;
+    const int shift_e = (int)((reinterpret_cast<uintptr_t>(start) & 15u) / sizeof(T));
     row_start += step * a.stride;
     uint64_t thr = 0;  // composites have to exceed it
     float m = neg_inf(), s = 0.0f;
     uint4 mx = neg_inf_vec<DT>();
-    int n = 0;
-    if (tid == 0) n_list = 0;
+    int n = 0, before = 0;  // entries of the list, hits of the tiles before
+    if (tid == 0) n_list = n_hits = 0;
+    // an element's composite, if it is one of the row's
+    auto composite = [&](int e, float x) { return (uint64_t)order_key(x) << 32 | (uint32_t)~(uint32_t)e; };
+    // Takes the k best among what each(f) calls f for, and the list, into the
+    // list: it is cut to its k best, and those above the last of them are found
+    // bit by bit.
+    auto select = [&](auto each) {
+      sort_list<kThreads>(list, n);
+      if (n >= a.k) {
+        n = a.k;
+        thr = list[n - 1];
+      }
+      auto above = [&](auto f) {
+        each([&](int e) {
+          if (e < 0 || e >= V) return;
+          const uint64_t v = composite(e, E::load(start + e));
+          if (v > thr) f(v);
+        });
+      };
+      uint64_t cut = 0;
+      for (int b = 63; b >= 0; b--) {
+        const uint64_t t = cut | (1ull << b);
+        uint32_t c = 0;
+        above([&](uint64_t v) { c += v >= t; });
+        c = cta_sum(c, ubuf);
+        if (c >= (uint32_t)a.k) {
+          cut = t;
+          if (n + (int)c <= a.cap) break;
+        }
+      }
+      if (tid == 0) n_list = n;
+      __syncthreads();
+      above([&](uint64_t v) {
+        if (v >= cut) list[atomicAdd(&n_list, 1u)] = v;
+      });
+      __syncthreads();
+      n = (int)n_list;
+    };
+    // Lists the elements of the first h hits that reach the bound, read again (from
+    // L2 mostly) and spread over the threads.
+    auto flush = [&](int h, float bound) {
+      auto each = [&](auto f) {
+        for (int q = tid; q < h * EPV; q += kThreads) f((int)hits[q / EPV] * EPV + q % EPV - shift_e);
+      };
+      each([&](int e) {
+        if (e < 0 || e >= V) return;
+        const float x = E::load(start + e);
+        const uint64_t v = composite(e, x);
+        if (!(x < bound) && v > thr) {
+          const uint32_t at = atomicAdd(&n_list, 1u);
+          if (at < (uint32_t)a.cap) list[at] = v;
+        }
+      });
+      __syncthreads();
+      if (n_list <= (uint32_t)a.cap) n = (int)n_list;
+      else select(each);
+    };
     for (int t0 = first;; t0 += a.tile) {
       const Where now = next;
       // where the copies of the listing pass go on: the next tile or row
@@ -208,7 +267,6 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
 
       // the groups' largest, and with them the thread's
       for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
-      if (tid == 0) n_hits = 0;
       copy_wait();
 #pragma unroll 4
       for (int i = tid; i < here; i += kThreads) mx = max_vec<DT>(mx, buf[i]);
@@ -291,7 +349,7 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
         for (int j = 0; j < EPV; j += 2) sum = add2(sum, ex2_2(fma2(pair(x[j], x[j + 1]), c2, mc)));
         if (!all_below<DT>(r, bound2)) {
           const uint32_t at = atomicAdd(&n_hits, 1u);
-          if (at < (uint32_t)kHits) hits[at] = (uint16_t)i;
+          if (at < (uint32_t)a.hits) hits[at] = (uint32_t)(t0 + i);
         }
       };
       // whole blocks of vectors, then the rest one by one
@@ -313,63 +371,31 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
       for (; u0 * kThreads < next.hi; u0 += kBlk) fetch(next, u0);
       s += sum.x + sum.y;
       fetch_ragged(next);
-      __syncthreads();
-      // the elements of the vectors that have something at the bound, read again
-      // (from L2) and spread over the threads
-      const int n_hit = (int)n_hits;
-      bool done = n_hit <= kHits;
-      if (done) {
-        for (int q = tid; q < n_hit * EPV; q += kThreads) {
-          const int l = (int)hits[q / EPV] * EPV + q % EPV, e = now.e0 + l;
-          if (e < 0 || e >= V) continue;
-          const float x = E::load(now.p + l);
-          const uint64_t v = (uint64_t)order_key(x) << 32 | (uint32_t)~(uint32_t)e;
-          if (!(x < bound) && v > thr) {
-            const uint32_t at = atomicAdd(&n_list, 1u);
-            if (at < (uint32_t)a.cap) list[at] = v;
-          }
-        }
-        __syncthreads();
-        done = n_list <= (uint32_t)a.cap;
-        if (done) n = (int)n_list;
-      }
-      if (!done) {
-        // too many: cut the list to the k best of before, then take the tile's own
-        // k best above them, found bit by bit over further reads of it
-        sort_list<kThreads>(list, n);
-        if (n >= a.k) {
-          n = a.k;
-          thr = list[n - 1];
-        }
-        auto each = [&](auto f) {
+      auto all_of_tile = [&](auto f) {
 #pragma unroll 1
-          for (int l = tid; l < here * EPV; l += kThreads) {
-            const int e = now.e0 + l;
-            if (e < 0 || e >= V) continue;
-            const uint64_t v = (uint64_t)order_key(E::load(now.p + l)) << 32 | (uint32_t)~(uint32_t)e;
-            if (v > thr) f(v);
-          }
-        };
-        uint64_t cut = 0;
-        for (int b = 63; b >= 0; b--) {
-          const uint64_t t = cut | (1ull << b);
-          uint32_t c = 0;
-          each([&](uint64_t v) { c += v >= t; });
-          c = cta_sum(c, ubuf);
-          if (c >= (uint32_t)a.k) {
-            cut = t;
-            if (n + (int)c <= a.cap) break;
-          }
-        }
-        if (tid == 0) n_list = n;
+        for (int l = tid; l < here * EPV; l += kThreads) f(now.e0 + l);
+      };
+      __syncthreads();
+      const int noted = (int)n_hits;
+      if (noted > a.hits / 2 && !last) {
+        // room for the tiles to come; too many in this tile: it goes another way
+        flush(noted <= a.hits ? noted : before, bound);
+        if (noted > a.hits) select(all_of_tile);
         __syncthreads();
-        each([&](uint64_t v) {
-          if (v >= cut) list[atomicAdd(&n_list, 1u)] = v;
-        });
-        __syncthreads();
-        n = (int)n_list;
+        if (tid == 0) n_hits = 0;
+        before = 0;
+        continue;
       }
-      if (last) break;
+      if (noted > a.hits) {
+        flush(before, bound);
+        select(all_of_tile);
+        break;
+      }
+      before = noted;
+      if (last) {
+        flush(before, bound);
+        break;
+      }
     }
     order_list<kThreads>(list, n);
     float M = cta_max(m, reinterpret_cast<float*>(ubuf));
@@ -427,7 +453,8 @@ cudaError_t launch(TopkArgs& a, cudaStream_t s) {
   while (a.cluster < kMaxCluster && a.rows * a.cluster <= num_sms() && nv > 4 * SH::NT * a.cluster)
     a.cluster *= 2;
   a.part = (int)((nv + a.cluster - 1) / a.cluster);
-  const int64_t most = (SH::kSmem - a.cap * 8) / 16;
+  a.hits = std::max(1024, 6 * a.k);
+  const int64_t most = (SH::kSmem - a.cap * 8 - a.hits * 4) / 16;
   const int64_t tiles = (a.part + most - 1) / most;
   a.tile = (int)((a.part + tiles - 1) / tiles);
   size_t bytes = (size_t)a.tile * 16;
@@ -443,7 +470,7 @@ cudaError_t launch(TopkArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(clusters * a.cluster));
   cfg.blockDim = dim3(SH::NT);
-  cfg.dynamicSmemBytes = (size_t)a.list_at * 16 + (size_t)a.cap * 8;
+  cfg.dynamicSmemBytes = (size_t)a.list_at * 16 + (size_t)a.cap * 8 + (size_t)a.hits * 4;
   cfg.stream = s;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
