@@ -479,8 +479,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     copy_wait();
     __syncthreads();
     take_side(now);
-    if (BUCKET) {
-      __syncthreads();
+    if (BUCKET) {  // (each listed place is read and written by one thread)
 #pragma unroll
       for (int h = 0; h < ENT; h++)
         if (el[h] >= 0) reinterpret_cast<T*>(buf)[el[h]] = E::make(neg_inf());

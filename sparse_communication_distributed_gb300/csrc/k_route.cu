@@ -234,10 +234,10 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
   const unsigned seg = (L == 32 ? kFull : ((1u << L) - 1u) << (slot * L));  // this token's lanes
   uint64_t* list = lists + (wid * ROWS + slot) * CAP;
   uint64_t* sorted = ranks + (wid * ROWS + slot) * a.k;
-  uint32_t experts = 0;  // this lane's values that are experts
+  uint32_t experts = 0;  // this lane's values that are experts, value j at bit VPL - 1 - j
 #pragma unroll
   for (int j = 0; j < VPL; j++)
-    if (col_of<DT, L>(sub, j) < a.E) experts |= 1u << j;
+    if (col_of<DT, L>(sub, j) < a.E) experts |= 1u << (VPL - 1 - j);
   const int64_t t0 = (int64_t)blockIdx.x * a.chunk, t1 = min(t0 + a.chunk, a.T);
   if (blockIdx.x == 0 && tid == 0) *a.done = 0;
   grid_launch_dependents();  // the second kernel waits for this one on its own
@@ -288,12 +288,13 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
       const float sh = shift_of(m);
 
       float bound = bound_for<LN>(gm, a.k, lane, seg);
-      // the experts that reach it
+      if (bound == 0.0f) bound = -0.0f;  // -0 - (-0) = +0, as 0 - (-0)
+      // the experts that reach it, from the sign of the difference (positive or
+      // NaN where not below): value j at bit VPL - 1 - j
       uint32_t cand = 0;
 #pragma unroll
-      for (int j = 0; j < VPL; j++)
-        if (!(x[j] < bound)) cand |= 1u << j;
-      cand &= experts;
+      for (int j = 0; j < VPL; j++) cand = __funnelshift_l(__float_as_uint(x[j] - bound), cand, 1);
+      cand = ~cand & experts;
 
       // p, and the sums
       const pair_t c2 = pair(kLog2e, kLog2e), mc = pair(-sh * kLog2e, -sh * kLog2e);
@@ -330,7 +331,7 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
       }
       const int n = __shfl_sync(kFull, incl, L - 1, L);
       for (int at_ = incl - __popc(cand); cand; at_++) {
-        const int j = __ffs(cand) - 1;
+        const int j = VPL - __ffs(cand);
         cand &= cand - 1;
         if (at_ < CAP) list[at_] = (uint64_t)col_of<DT, L>(sub, j);
       }

@@ -62,15 +62,11 @@ def _arg(x, name: str, dtypes, shape, device) -> int | None:
     """Address of an optional contiguous input, checked."""
     if x is None:
         return None
-    if x.dtype not in dtypes:
-        raise ValueError(f"{name} must be of type {' or '.join(map(str, dtypes))}, not {x.dtype}")
-    if x.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(x.shape)}")
-    if x.device != device:
-        raise ValueError(f"{name} must be on {device}, not {x.device}")
-    if not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return x.data_ptr()
+    if x.dtype in dtypes and x.shape == shape and x.device == device and x.is_contiguous():
+        return x.data_ptr()
+    raise ValueError(f"{name} must be contiguous, of type {' or '.join(map(str, dtypes))} and shape "
+                     f"{shape} on {device}, not {x.dtype} {tuple(x.shape)} with strides "
+                     f"{x.stride()} on {x.device}")
 
 
 def _check(rc: int) -> None:

@@ -442,6 +442,7 @@ ROUTE = [  # tokens, experts, k, groups, dtype, kind, renorm, offset, pad
     (5000, 128, 8, 7, "bf16", "normal", True, 0, 0), (300, 48, 4, 2, "f32", "low", True, 0, 0),
     (300, 200, 7, 1, "bf16", "high", False, 0, 0), (700, 64, 6, 300, "bf16", "normal", True, 0, 0),
     (3000, 256, 8, 2, "bf16", "equal", True, 0, 0), (500, 100, 24, 3, "f32", "normal", True, 0, 0),
+    (400, 64, 6, 2, "bf16", "zeros", True, 0, 0), (400, 256, 8, 2, "f32", "zeros", False, 0, 0), (300, 16, 3, 1, "f16", "zeros", True, 0, 0),
     (40000, 64, 6, 9, "bf16", "normal", True, 0, 0), (90000, 8, 2, 3, "f32", "ties", True, 0, 0),
     (20000, 256, 8, 1, "f32", "normal", False, 0, 0), (12000, 100, 3, 5, "bf16", "ties", True, 0, 0),
     (20, 1000, 20, 2, "f16", "ties", False, 0, 0), (9000, 4, 1, 2, "bf16", "normal", False, 0, 0),
@@ -492,6 +493,27 @@ def test_route(T, E, k, G, dtype, kind, renorm, offset, pad):
         off = np.abs(grad - want) - ((4 * rel + 16 * ref.U) * size + np.abs(want) * ref.ROUND[dtype] + ref.TINY[dtype])
         assert off.max(initial=0.0) <= 0
     assert not f64(pkg.route_backward(x, idx, counts, live, renormalize=renorm, cu_tokens=cut)).any()
+
+
+@pytest.mark.parametrize("E,dtype", [(8, "f32"), (24, "bf16"), (64, "f32"), (128, "f16"), (256, "bf16"), (300, "f32"), (1000, "f32")])
+def test_route_nan_and_infinities(E, dtype):
+    # NaN ranks above +inf, an expert of -inf below all others; a token with one of the first two has NaN weights
+    rng = np.random.default_rng(E)
+    h = logits(rng, 40, E)
+    h[0, 3] = np.nan
+    h[1, 5] = INF
+    h[2, :] = -INF
+    h[2, [1, 6]] = [1.0, -2.0]
+    h[3, [7, 2]] = [-np.nan, np.nan]
+    x = place(h, dtype)
+    idx, w, counts, live, losses = pkg.route(x, 4)
+    i = idx.cpu().numpy()
+    assert i[0, 0] == 3 and i[1, 0] == 5 and i[3, :2].tolist() == [2, 7]
+    assert i[2].tolist() == [1, 6, 0, 2] and f64(w)[2, 2:].tolist() == [0.0, 0.0]
+    for t in range(40):
+        assert np.array_equal(i[t], ref.topk(f64(x[t]), 4)), t
+    assert live.tolist() == [40, 40, 1] and int(counts.sum()) == 160
+    assert np.isfinite(f64(w)[4:]).all() and np.isnan(f64(w)[[0, 1, 3]]).any(1).all()
 
 
 def test_route_gradient_against_differences():
