@@ -126,7 +126,9 @@ __device__ __forceinline__ int col_of(int sub, int j) {
 }
 
 // A lane's logits of one token as they lie in memory, -inf beyond the experts.
-// VEC: rows on 16-byte boundaries and whole vectors.
+// vec: rows on 16-byte boundaries and whole vectors.  The loads stay in L1, where
+// the few logits looked up by expert are found again (131072 x 256 fp32: 82 -> 73
+// us against loads that do not).
 template <int DT, class LN>
 struct RowRegs {
   static constexpr int N = Elem<DT>::kPerVec, VECS = LN::VPL / N;
@@ -138,7 +140,7 @@ struct RowRegs {
 #pragma unroll
       for (int v = 0; v < VECS; v++) {
         r[v] = neg_inf_vec<DT>();
-        if (v * LN::L * N < E) r[v] = ld_row_u4(p + v * LN::L * N);
+        if (v * LN::L * N < E) r[v] = *reinterpret_cast<const uint4*>(p + v * LN::L * N);
       }
     } else {
 #pragma unroll
