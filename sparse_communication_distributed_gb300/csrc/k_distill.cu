@@ -286,6 +286,16 @@ struct __align__(16) Row {
   float Qr, base, rz, unused;  // sum q + q_rest; q_i = exp(t_i - base) rz
 };
 
+// What a row's loss is worked out from.
+struct Loss {
+  float M, m, S, S1;   // as in Part and Row: the whole row's sums
+  float z, Q, qr;      // the teacher's
+  float top, s, b;     // p_listed on the scale of s; as in Part
+  float w, xy;
+  int64_t row;
+  bool has, hard;
+};
+
 // A cluster of CTAs (often just one) takes a row, each CTA a part of at most
 // PART vectors, and reads it once into shared memory; then the cluster takes
 // another row.  A thread works only on vectors that it copied itself, so that
@@ -313,6 +323,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
   __shared__ Part warps[2][kWarps];
   __shared__ Part parts[2][kMaxCluster];
   __shared__ Row rows[2];
+  __shared__ Loss pend[32];  // rows whose losses are still to be worked out, a lane each
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const uint32_t rank = a.cluster > 1 ? cluster_rank() : 0;
   const int64_t step = gridDim.x / (unsigned)a.cluster;
@@ -444,6 +455,30 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     if (g)
       for (int i = tid; i < w.here; i += NT) put(g, w, same, i, make_uint4(0, 0, 0, 0));
     if (a.loss && tid == 0 && rank == 0) a.loss[row] = 0.0f;
+  };
+  // The losses of up to 32 rows at once, by the first warp: their logarithms and
+  // quotients would hold up the CTA if one lane worked them out for each row.
+  int n_pend = 0;
+  auto write_losses = [&]() {
+    __syncwarp();
+    if (lane < n_pend) {
+      const Loss p = pend[lane];
+      const float L = p.M * inv_tau + logf(p.S);
+      float l = 0.0f;
+      if (p.has) {  // sum q_i (t_i - log z - base - s_i) + L sum q_i
+        float kl = BUCKET ? p.b + p.Q * L : p.b / p.z + (L - logf(p.z));
+        if (p.qr > 0.0f) {  // log q_rest - log p_rest, both from what is listed
+          const float odds = p.top / p.s;
+          const float logp = odds < 1.0f ? log1pf(odds) : L - (p.m * inv_tau + logf(p.s));
+          kl += p.qr * (log1pf(-p.Q) + logp);
+        }
+        l = a.kd * a.tau * a.tau * kl;
+      }
+      if (p.hard) l += a.ce * (p.M + logf(p.S1) - p.xy);
+      a.loss[p.row] = p.w * l;
+    }
+    __syncwarp();
+    n_pend = 0;
   };
   auto weight_or_1 = [&](int64_t row) { return row < a.rows ? weight_of(row) : 1.0f; };
   if (a.cluster > 1) cluster_arrive_relaxed();  // "this CTA runs": its shared memory may be written
@@ -585,11 +620,6 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     }
     if (lane == 0) warps[turn][wid] = q;
     __syncthreads();
-    struct {
-      float sh, shr, S, S1, z, Q, qr;
-      bool has;
-      float odds, s, b;  // odds = p_listed / p_rest
-    } ls;
     if (wid == 0) {
       // the CTA's, then the cluster's: the partial statistics of n parts, one in
       // each of the first n lanes
@@ -670,32 +700,19 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
           if (!TWO) r.K1 += r.K2;
           rows[turn] = r;
         }
-        if (a.loss && rank == 0) {  // its logarithms are taken after the others have gone on
-          ls = {sh, shr, S, S1, z, Q, qr, has, q.ts / q.s * ex2((q.tm - shr) * a.c), q.s, q.b};
-        }
+        if (a.loss && rank == 0)
+          pend[n_pend] = {sh, shr, S, S1, z, Q, qr, BUCKET ? q.ts * ex2((q.tm - shr) * a.c) : 0.0f,
+                          q.s, q.b, w_now, xy, row, has, y >= 0};
       }
+      if (a.loss && rank == 0 && ++n_pend == 32) write_losses();
     } else if (a.cluster > 1) {
       if (!met) cluster_wait();
       cluster_arrive_relaxed();
       cluster_wait();
     }
     met = true;
-    if (g) __syncthreads();
-    if (a.loss && tid == 0 && rank == 0) {
-      const float L = ls.sh * inv_tau + logf(ls.S);
-      float l = 0.0f;
-      if (ls.has) {  // sum q_i (t_i - log z - base - s_i) + L sum q_i
-        float kl = BUCKET ? ls.b + ls.Q * L : ls.b / ls.z + (L - logf(ls.z));
-        if (ls.qr > 0.0f) {  // log q_rest - log p_rest, both from what is listed
-          const float logp = ls.odds < 1.0f ? log1pf(ls.odds) : L - (ls.shr * inv_tau + logf(ls.s));
-          kl += ls.qr * (log1pf(-ls.Q) + logp);
-        }
-        l = a.kd * a.tau * a.tau * kl;
-      }
-      if (y >= 0) l += a.ce * (ls.sh + logf(ls.S1) - xy);
-      a.loss[row] = w_now * l;
-    }
     if (g) {
+      __syncthreads();
       const Row t = rows[turn];
       const pair_t mc = pair(-t.m * a.c, -t.m * a.c), ml = pair(-t.m * kLog2e, -t.m * kLog2e);
       const pair_t k1 = pair(t.K1, t.K1), k2 = pair(t.K2, t.K2);
@@ -739,6 +756,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     row = row2;
     turn ^= 1;
   }
+  if (wid == 0 && n_pend) write_losses();
   if (!met) cluster_wait();
 }
 

@@ -84,30 +84,16 @@ __device__ void sort_list(uint64_t* list, int n) {
   __syncthreads();
 }
 
-// The same, for short lists by counting what is above each.
-template <int kThreads>
-__device__ void order_list(uint64_t* list, int n) {
-  if (n > kThreads) {
-    sort_list<kThreads>(list, n);
-    return;
-  }
-  const int tid = threadIdx.x;
-  uint64_t v = 0;
+// Entries of list[0..n) above v; zeros follow up to a multiple of 4.
+__device__ __forceinline__ int count_above(const uint64_t* list, int n, uint64_t v) {
   int above = 0;
-  if (tid >= n && tid < ((n + 3) & ~3)) list[tid] = 0;
-  __syncthreads();
-  if (tid < n) {
-    v = list[tid];
 #pragma unroll 2
-    for (int i = 0; i < n; i += 4) {
-      const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(list + i);
-      const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(list + i + 2);
-      above += (p.x > v) + (p.y > v) + (q.x > v) + (q.y > v);
-    }
+  for (int i = 0; i < n; i += 4) {
+    const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(list + i);
+    const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(list + i + 2);
+    above += (p.x > v) + (p.y > v) + (q.x > v) + (q.y > v);
   }
-  __syncthreads();
-  if (tid < n) list[above] = v;
-  __syncthreads();
+  return above;
 }
 
 // Order of floats as signed whole numbers, and back (its own inverse).
@@ -132,7 +118,8 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
   __shared__ __align__(16) uint32_t hist[kBins];
   __shared__ __align__(16) int range[2][kWarps];
   __shared__ uint32_t ubuf[32];
-  __shared__ float parts[kMaxCluster][2];  // maximum and sum of each CTA of a row
+  // maximum and sum of each warp, and of each CTA of a row
+  __shared__ float wsum[2][kWarps], parts[2][kMaxCluster];
   __shared__ uint32_t n_list, n_hits;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int V = (int)a.V;
@@ -397,35 +384,66 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
         break;
       }
     }
-    order_list<kThreads>(list, n);
-    float M = cta_max(m, reinterpret_cast<float*>(ubuf));
-    float S = cta_sum(s * ex2((m - shift_of(M)) * a.c), reinterpret_cast<float*>(ubuf));
-    if (a.cluster > 1) {  // (a single row for each cluster: the tile's space is free)
-      uint64_t* all = reinterpret_cast<uint64_t*>(buf);  // k entries of each CTA
-      cluster_arrive();
-      cluster_wait();
-      for (int i = tid; i < a.k; i += kThreads) put_remote(all + rank * a.k + i, 0, i < n ? list[i] : 0);
-      if (tid == 0) {
-        put_remote(&parts[rank][0], 0, M);
-        put_remote(&parts[rank][1], 0, S);
+    // each warp's maximum and sum of exponentials
+    float M = m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    float S = s * ex2((m - shift_of(M)) * a.c);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) S += __shfl_xor_sync(kFull, S, o);
+    if (lane == 0) {
+      wsum[0][wid] = M;
+      wsum[1][wid] = S;
+    }
+    auto total = [&](const float* ms, const float* ss, int count) {  // of the first lanes' parts
+      const float pm = lane < count ? ms[lane] : neg_inf(), ps = lane < count ? ss[lane] : 0.0f;
+      M = pm;
+#pragma unroll
+      for (int o = 8; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+      S = ps * ex2((pm - shift_of(M)) * a.c);
+#pragma unroll
+      for (int o = 8; o; o >>= 1) S += __shfl_xor_sync(kFull, S, o);
+    };
+    auto write = [&](int at, uint64_t v) {
+      const int32_t e = (int32_t)~(uint32_t)v;
+      a.idx[row * a.k + at] = e;
+      if (a.vals) static_cast<T*>(a.vals)[row * a.k + at] = start[e];
+    };
+    auto write_lse = [&]() {
+      if (a.lse && tid == 0) a.lse[row] = shift_of(M) / a.tau + logf(S);
+    };
+    if (a.cluster == 1 && n <= kThreads) {  // by counting what is above each entry
+      for (int i = n + tid; i < ((n + 3) & ~3); i += kThreads) list[i] = 0;
+      __syncthreads();
+      if (tid < n) {
+        const uint64_t v = list[tid];
+        const int above = count_above(list, n, v);
+        if (above < a.k) write(above, v);
       }
-      cluster_arrive();
-      cluster_wait();
-      if (rank != 0) return;
-      list = all;
-      n = a.cluster * a.k;
+      if (wid == 0) total(wsum[0], wsum[1], kWarps);
+      write_lse();
+    } else {
       sort_list<kThreads>(list, n);
-      for (int i = 0; i < a.cluster; i++) M = fmaxf(M, parts[i][0]);
-      S = 0.0f;
-      for (int i = 0; i < a.cluster; i++)
-        S += parts[i][1] * ex2((parts[i][0] - shift_of(M)) * a.c);
+      if (wid == 0) total(wsum[0], wsum[1], kWarps);
+      if (a.cluster > 1) {  // (a single row for each cluster: the tile's space is free)
+        uint64_t* all = reinterpret_cast<uint64_t*>(buf);  // k entries of each CTA
+        cluster_arrive();
+        cluster_wait();
+        for (int i = tid; i < a.k; i += kThreads) put_remote(all + rank * a.k + i, 0, i < n ? list[i] : 0);
+        if (tid == 0) {
+          put_remote(&parts[0][rank], 0, M);
+          put_remote(&parts[1][rank], 0, S);
+        }
+        cluster_arrive();
+        cluster_wait();
+        if (rank != 0) return;
+        list = all;
+        sort_list<kThreads>(list, a.cluster * a.k);
+        if (wid == 0) total(parts[0], parts[1], a.cluster);
+      }
+      for (int i = tid; i < a.k; i += kThreads) write(i, list[i]);
+      write_lse();
     }
-    for (int i = tid; i < a.k; i += kThreads) {
-      const int32_t e = (int32_t)~(uint32_t)list[i];
-      a.idx[row * a.k + i] = e;
-      if (a.vals) static_cast<T*>(a.vals)[row * a.k + i] = start[e];
-    }
-    if (a.lse && tid == 0) a.lse[row] = shift_of(M) / a.tau + logf(S);
     __syncthreads();
   }
 }
