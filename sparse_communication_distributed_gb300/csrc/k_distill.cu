@@ -232,19 +232,21 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
 constexpr int kMaxCluster = 8;
 
 // Threads of a CTA, vectors of a row that each of them has at most, CTAs of an
-// SM, teacher entries that a thread looks after: for long parts of a row, for
-// short ones, and for long ones with many entries.  Three CTAs share an SM's
-// shared memory, and while one waits for its row the others compute.
+// SM, teacher entries that a thread looks after.  Three CTAs with parts of up to
+// 64 KB share an SM's shared memory, and while one waits for its row the others
+// compute; two with parts of 105 KB do better where that saves a cluster, eight
+// take short parts, and there is one shape for many entries.
 template <int NT_, int VECS_, int MINB_, int ENT_>
 struct Shape {
-  static constexpr int NT = NT_, VECS = VECS_, MINB = MINB_, ENT = ENT_;
+  static constexpr int NT = NT_, MINB = MINB_, ENT = ENT_;
   static constexpr int PART = NT_ * VECS_, MAXK = NT_ * ENT_;
   static constexpr int MOST = 13824;  // vectors that fit at all (216 KB)
 };
 using Wide = Shape<256, 16, 3, 1>;
+using Large = Shape<320, 21, 2, 1>;
 using Narrow = Shape<128, 8, 8, 2>;
-using Deep = Shape<512, 8, 2, 2>;
-static_assert(Deep::MAXK == kMaxK, "every entry has a thread");
+using Deep = Shape<320, 21, 2, 4>;
+static_assert(Deep::MAXK >= kMaxK, "every entry has a thread");
 
 // What a row's statistics are made of.  A sum of exponentials is held relative
 // to a maximum: s = sum 2^((x - m) c), and s1 the same at temperature 1.
@@ -317,7 +319,8 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
   using E = Elem<DT>;
   using T = typename E::T;
   constexpr int EPV = E::kPerVec, NT = SH::NT, ENT = SH::ENT;
-  constexpr int kWarps = NT / 32;
+  constexpr int kWarps = NT / 32, kMerge = kWarps <= 4 ? 4 : kWarps <= 8 ? 8 : 16;
+  static_assert(kWarps <= 16, "a warp merges the others' statistics");
   constexpr int BLK = 2;  // vectors that a thread handles at a time
   extern __shared__ __align__(16) uint4 buf[];  // the part of the row
   __shared__ Part warps[2][kWarps];
@@ -635,16 +638,17 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
           q.tm = tm;
         }
       };
-      if (lane < kWarps) q = warps[turn][lane];
-      merge(kWarps);
-      const float base = shfl_max(q.base, kWarps);
+      q = warps[turn][min(lane, kWarps - 1)];
+      if (lane >= kWarps) q = Part{neg_inf(), 0.0f, 0.0f, neg_inf(), 0.0f, 0.0f, 0.0f, neg_inf(), 0.0f, 0.0f};
+      merge(kMerge);
+      const float base = shfl_max(q.base, kMerge);
       if (!BUCKET) {  // relative to the CTA's base
         const float bd = shift_of(q.base) - shift_of(base), f = expf(bd);
         q.b = q.z == 0.0f ? 0.0f : f * (q.b + bd * q.zp);
         q.z = q.z == 0.0f ? 0.0f : f * q.z;
       }
-      q.b = shfl_sum(q.b, kWarps);
-      const float z = shfl_sum(q.z, kWarps);
+      q.b = shfl_sum(q.b, kMerge);
+      const float z = shfl_sum(q.z, kMerge);
       if (a.cluster > 1) {
         if (lane == 0) {
           warps[turn][0] = q;
@@ -815,15 +819,19 @@ cudaError_t launch_distill(DistillArgs& a, cudaStream_t s) {
     distill_rows<DT><<<(unsigned)(a.rows < cap ? a.rows : cap), kThreads, 0, s>>>(a);
     e = cudaSuccess;
   } else {
-    a.cluster = 1;
-    // parts that share an SM three at a time, larger ones only in clusters of 8
-    while (a.cluster < kMaxCluster && nv > (int64_t)Wide::PART * a.cluster) a.cluster++;
+    // large parts where one or two hold the row (4000 x 50257 bf16 gradient: 163 us
+    // against 210 with two wide ones, x 100000: 332 against 516 with four), wide
+    // ones for longer rows (1000 x 65536 fp32: four 127 us, three large ones 162)
+    const int wide = (int)((nv + Wide::PART - 1) / Wide::PART);
+    const int large = (int)((nv + Large::PART - 1) / Large::PART);
+    a.cluster = std::min(large <= 2 ? large : wide, kMaxCluster);
     // few rows: more CTAs for each, down to a vector or two a thread
     while (a.cluster < kMaxCluster && a.rows * a.cluster <= num_sms() && nv > Narrow::NT * 2 * a.cluster)
       a.cluster = std::min(2 * a.cluster, kMaxCluster);
     a.part_vecs = (int)((nv + a.cluster - 1) / a.cluster);
     if (a.part_vecs <= Narrow::PART && a.k <= Narrow::MAXK) e = launch_sized<DT, Narrow>(a, s);
-    else if (a.k <= Wide::MAXK) e = launch_sized<DT, Wide>(a, s);
+    else if (a.part_vecs <= Wide::PART && a.k <= Wide::MAXK) e = launch_sized<DT, Wide>(a, s);
+    else if (a.k <= Large::MAXK) e = launch_sized<DT, Large>(a, s);
     else e = launch_sized<DT, Deep>(a, s);
   }
   const cudaError_t last = cudaGetLastError();
