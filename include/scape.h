@@ -458,7 +458,8 @@ typedef struct {
 } scape_route_args;
 
 /* Bytes of device workspace that scape_route needs for these sizes (host call,
- * no device work; pointers in args are not looked at). */
+ * no device work; of the pointers in args only whether cu_tokens is NULL
+ * matters).  0 for a few tokens without groups: workspace may then be NULL. */
 int scape_route_workspace(const scape_route_args* args, uint64_t* bytes);
 
 /* Forward: idx and weights (tokens x k, contiguous; -1 and 0 for a token that

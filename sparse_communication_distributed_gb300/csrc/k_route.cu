@@ -241,7 +241,7 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
   for (int j = 0; j < VPL; j++)
     if (col_of<DT, L>(sub, j) < a.E) experts |= 1u << (VPL - 1 - j);
   const int64_t t0 = (int64_t)blockIdx.x * a.chunk, t1 = min(t0 + a.chunk, a.T);
-  if (blockIdx.x == 0 && tid == 0) *a.done = 0;
+  if (blockIdx.x == 0 && tid == 0 && !a.single) *a.done = 0;
   grid_launch_dependents();  // the second kernel waits for this one on its own
 
   // pieces of the chunk: each group it touches, and tokens outside all groups
@@ -721,12 +721,17 @@ uint64_t chunk_of(const scape_route_args* q) {
   return n == 0 ? round : (n + round - 1) / round * round;
 }
 
+bool single_chunk(const scape_route_args* q) {
+  return q->tokens > 0 && q->tokens <= chunk_of(q) && !q->cu_tokens && q->n_groups == 1;
+}
+
 struct Workspace {
   uint64_t slots, nb, part_p, part_c, part_n, part_z, part_b, group_z, done, bytes;
 };
 
 Workspace workspace_of(const scape_route_args* q) {
   Workspace w{};
+  if (single_chunk(q)) return w;  // one CTA, nothing to hand over
   const uint64_t ch = chunk_of(q);
   w.slots = (q->tokens + ch - 1) / ch + q->n_groups;
   w.nb = (q->experts + kCols - 1) / kCols;
@@ -756,7 +761,7 @@ void fill(const scape_route_args* q, RouteArgs& a) {
   a.G = (int64_t)q->n_groups;
   a.valid = q->valid;
   a.chunk = (int64_t)chunk_of(q);
-  a.single = q->tokens > 0 && q->tokens <= (uint64_t)a.chunk && !q->cu_tokens;
+  a.single = single_chunk(q);
   const uint64_t es = q->dtype == SCAPE_F32 ? 4 : 2;
   a.vec = !misaligned(q->logits, 16) && q->row_stride * es % 16 == 0 && q->experts * es % 16 == 0;
 }
@@ -823,7 +828,7 @@ SCAPE_API int scape_route(const scape_route_args* args, int32_t* idx, float* wei
       misaligned(losses, 4))
     return fail(SCAPE_EINVAL, "a buffer is not aligned to its element size");
   const Workspace w = workspace_of(args);
-  if (!workspace || misaligned(workspace, 16) || workspace_bytes < w.bytes)
+  if (w.bytes && (!workspace || misaligned(workspace, 16) || workspace_bytes < w.bytes))
     return fail(SCAPE_EINVAL, "workspace must be %llu bytes, 16-byte aligned",
                 (unsigned long long)w.bytes);
   RouteArgs a{};

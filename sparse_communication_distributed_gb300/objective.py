@@ -195,9 +195,10 @@ def route(logits, k: int, *, renormalize: bool = True, cu_tokens=None, valid=Non
     counts = empty((groups, experts), dtype=i32, device=dev)
     live = empty(groups + 2, dtype=i32, device=dev)
     losses = empty(2, dtype=f32, device=dev)
-    ws = empty(nbytes, dtype=torch.uint8, device=dev)
+    ws = empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     _check(_lib.scape_route(ref, idx.data_ptr(), weights.data_ptr(), counts.data_ptr(),
-                            live.data_ptr(), losses.data_ptr(), ws.data_ptr(), nbytes,
+                            live.data_ptr(), losses.data_ptr(),
+                            None if ws is None else ws.data_ptr(), nbytes,
                             torch._C._cuda_getCurrentRawStream(dev.index)))
     return idx, weights, counts, live, losses
 
