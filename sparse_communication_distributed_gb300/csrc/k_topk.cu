@@ -32,13 +32,16 @@
 namespace scape {
 namespace {
 
-// Threads of a CTA and CTAs of an SM, for long and for short rows.
+// Threads of a CTA and CTAs of an SM: for rows of up to four tiles, for longer
+// ones (1024 x 131072 fp32, k 256: 162 us against 180 with nine smaller tiles; at
+// three, 4000 x 32000 fp32, 144 against 130), and for short ones.
 template <int NT_, int CTAS_>
 struct Shape {
   static constexpr int NT = NT_, CTAS = CTAS_;
   static constexpr int kSmem = (228 / CTAS_ - 3) * 1024;  // bytes of a CTA's tile, list and hits
 };
 using Wide = Shape<256, 3>;
+using Large = Shape<384, 2>;
 using Narrow = Shape<128, 7>;
 constexpr int kNarrowVecs = 1024;  // rows up to this many vectors are short
 constexpr int kBlk = 2;            // vectors a thread handles at a time
@@ -515,7 +518,8 @@ template <int DT>
 cudaError_t launch_dt(TopkArgs& a, cudaStream_t s) {
   // (a narrow CTA's list holds 3 k entries beside its row for k up to this)
   if (a.V <= (kNarrowVecs - 1) * Elem<DT>::kPerVec && a.k <= 256) return launch_groups<DT, Narrow>(a, s);
-  return launch_groups<DT, Wide>(a, s);
+  const bool longer = a.V > 4 * (Wide::kSmem - 3 * 4096) / 16 * Elem<DT>::kPerVec;
+  return longer ? launch_groups<DT, Large>(a, s) : launch_groups<DT, Wide>(a, s);
 }
 
 int fail(int code, const char* fmt, ...) {
