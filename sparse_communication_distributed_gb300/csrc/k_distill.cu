@@ -777,13 +777,8 @@ cudaError_t launch_parts(const DistillArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
-  // as many clusters as the GPU holds at once, evened out over the rounds
-  const int64_t ctas = std::min<int64_t>(SH::MINB, 224 * 1024 / (a.part_vecs * 16 + 4096));
-  const int64_t slots = std::max<int64_t>((int64_t)num_sms() * ctas / a.cluster, 1);
-  const int64_t rounds = (a.rows + slots - 1) / slots;
-  const int64_t clusters = (a.rows + rounds - 1) / rounds;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(clusters * a.cluster));
+  cfg.gridDim = dim3((unsigned)(num_sms() * a.cluster));
   cfg.blockDim = dim3(SH::NT);
   cfg.dynamicSmemBytes = (size_t)a.part_vecs * 16;
   cfg.stream = s;
@@ -794,6 +789,19 @@ cudaError_t launch_parts(const DistillArgs& a, cudaStream_t s) {
   at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+  // as many clusters as the GPU holds at once, evened out over the rounds.  A
+  // cluster lies within a GPC, so that is less than the CTAs it holds divided by
+  // the cluster's (51 of 8, not 57), and one too many would run after all others.
+  int slots = 0;
+  if (a.cluster > 1) {
+    e = cudaOccupancyMaxActiveClusters(&slots, distill_parts<DT, EXPS, BUCKET, SH>, &cfg);
+    if (e != cudaSuccess) return e;
+  } else {
+    slots = num_sms() * std::min(SH::MINB, 224 * 1024 / (a.part_vecs * 16 + 4096));
+  }
+  slots = std::max(slots, 1);
+  const int64_t rounds = (a.rows + slots - 1) / slots;
+  cfg.gridDim.x = (unsigned)((a.rows + rounds - 1) / rounds * a.cluster);
   return cudaLaunchKernelEx(&cfg, distill_parts<DT, EXPS, BUCKET, SH>, a);
 }
 
@@ -819,9 +827,9 @@ cudaError_t launch_distill(DistillArgs& a, cudaStream_t s) {
     distill_rows<DT><<<(unsigned)(a.rows < cap ? a.rows : cap), kThreads, 0, s>>>(a);
     e = cudaSuccess;
   } else {
-    // large parts where one or two hold the row (4000 x 50257 bf16 gradient: 163 us
-    // against 210 with two wide ones, x 100000: 332 against 516 with four), wide
-    // ones for longer rows (1000 x 65536 fp32: four 127 us, three large ones 162)
+    // large parts where one or two hold the row (gradient of 1000 x 50257 bf16: 54
+    // us against 59 with two wide ones, x 100000: 98 against 109 with four), wide
+    // ones for longer rows (1000 x 65536 fp32: four 107 us, three large ones 119)
     const int wide = (int)((nv + Wide::PART - 1) / Wide::PART);
     const int large = (int)((nv + Large::PART - 1) / Large::PART);
     a.cluster = std::min(large <= 2 ? large : wide, kMaxCluster);
