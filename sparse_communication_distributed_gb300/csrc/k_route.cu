@@ -318,7 +318,7 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
         x[j + 1] = e.y;
       }
       const float s = lanes_sum<L>(s2.x + s2.y);
-      const float inv = 1.0f / s;
+      const float inv = rcp(s);
       ok = ok && !(s == 0.0f);  // some logit above -inf
       const float lse = sh + logf(s);
       if (ok) {
@@ -383,16 +383,19 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
         const int n4 = (n + 3) & ~3;  // at most CAP, a multiple of 4
         for (int i = n + sub; i < n4; i += L) list[i] = 0;
         __syncwarp();
-        for (int i = sub; i < n; i += L) {
-          const uint64_t v = list[i];
-          int above = 0;
+        for (int i = sub; i < n; i += 2 * L) {  // two of a lane at a time
+          const bool two = i + L < n;
+          const uint64_t v = list[i], w = two ? list[i + L] : 0;
+          int above = 0, above2 = 0;
 #pragma unroll 1
           for (int q = 0; q < n; q += 4) {  // in fours: below the end come zeros
             const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(list + q);
             const ulonglong2 t2 = *reinterpret_cast<const ulonglong2*>(list + q + 2);
             above += (u.x > v) + (u.y > v) + (t2.x > v) + (t2.y > v);
+            above2 += (u.x > w) + (u.y > w) + (t2.x > w) + (t2.y > w);
           }
           if (above < a.k) sorted[above] = v;
+          if (two && above2 < a.k) sorted[above2] = w;
         }
       }
       __syncwarp();
@@ -400,7 +403,7 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
       if (a.renorm && ok)
         for (int i = sub; i < a.k; i += L)
           chosen += ex2((value_of_key((uint32_t)(sorted[i] >> 32)) - sh) * kLog2e);
-      const float scale = a.renorm ? 1.0f / lanes_sum<L>(chosen) : inv;
+      const float scale = a.renorm ? rcp(lanes_sum<L>(chosen)) : inv;
       if (in)
         for (int i = sub; i < a.k; i += L) {
           const uint64_t v = ok ? sorted[i] : 0;
@@ -639,7 +642,7 @@ __global__ __launch_bounds__(kThreads, 2) void route_grad(const RouteArgs a) {
       x[j] = e.x;
       x[j + 1] = e.y;
     }
-    const float s = lanes_sum<L>(s2.x + s2.y), inv = 1.0f / s, lse = m + logf(s);
+    const float s = lanes_sum<L>(s2.x + s2.y), inv = rcp(s), lse = m + logf(s);
     float pd = lanes_sum<L>(pd2.x + pd2.y) * inv - zc * lse;
     // the choices: weights and what their gradients give
     float inv_den = inv, dot = 0.0f;
@@ -651,7 +654,7 @@ __global__ __launch_bounds__(kThreads, 2) void route_grad(const RouteArgs a) {
         e += xc[q];
         ed += xc[q] * dwc[q];
       }
-      if (a.renorm) inv_den = 1.0f / lanes_sum<L>(e);
+      if (a.renorm) inv_den = rcp(lanes_sum<L>(e));
       dot = lanes_sum<L>(ed) * inv_den;
     }
     if (!a.renorm) pd += dot;
