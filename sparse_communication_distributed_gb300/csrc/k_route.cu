@@ -554,7 +554,9 @@ __global__ __launch_bounds__(kThreads, 2) void route_grad(const RouteArgs a) {
   using E = Elem<DT>;
   using T = typename E::T;
   constexpr int L = LN::L, VPL = LN::VPL, ROWS = LN::ROWS, N = E::kPerVec;
-  constexpr int KPL = 32 / L < 8 ? 32 / L : 8;  // choices of a lane: k <= 32, and k <= experts
+  // choices of a lane at most (k <= 32, and k <= experts); loops over them end at k
+  // (524288 x 128 bf16, k 8: 89 -> 80 us)
+  constexpr int KPL = 32 / L < 8 ? 32 / L : 8;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int sub = lane & (L - 1), slot = lane / L;
   const int64_t t0 = (int64_t)blockIdx.x * a.chunk, t1 = min(t0 + a.chunk, a.T);
@@ -571,6 +573,7 @@ __global__ __launch_bounds__(kThreads, 2) void route_grad(const RouteArgs a) {
     next_first = in ? a.bidx[u * a.k] : -1;  // tells whether the token is live
 #pragma unroll
     for (int q = 0; q < KPL; q++) {
+      if (q * L >= a.k) break;
       const int i = q * L + sub;
       next_id[q] = -1;
       next_dw[q] = 0.0f;
@@ -583,6 +586,7 @@ __global__ __launch_bounds__(kThreads, 2) void route_grad(const RouteArgs a) {
   auto fetch_chosen = [&](int64_t u) {
 #pragma unroll
     for (int q = 0; q < KPL; q++) {
+      if (q * L >= a.k) break;
       next_x[q] = neg_inf();
       if (next_id[q] >= 0 && next_id[q] < a.E)
         next_x[q] = E::load(static_cast<const T*>(a.x) + u * a.stride + next_id[q]);
@@ -606,6 +610,7 @@ __global__ __launch_bounds__(kThreads, 2) void route_grad(const RouteArgs a) {
     next.get(x);
 #pragma unroll
     for (int q = 0; q < KPL; q++) {
+      if (q * L >= a.k) break;
       id[q] = next_id[q];
       dwc[q] = next_dw[q];
       xc[q] = next_x[q];
@@ -626,8 +631,10 @@ __global__ __launch_bounds__(kThreads, 2) void route_grad(const RouteArgs a) {
     // d at the choices (needed late)
     float dc[KPL];
 #pragma unroll
-    for (int q = 0; q < KPL; q++)
+    for (int q = 0; q < KPL; q++) {
+      if (q * L >= a.k) break;
       dc[q] = ok && gc && id[q] >= 0 && id[q] < a.E ? coef * (float)gc[id[q]] : 0.0f;
+    }
     float m = x[0];
 #pragma unroll
     for (int j = 1; j < VPL; j++) m = fmaxf(m, x[j]);
@@ -650,6 +657,7 @@ __global__ __launch_bounds__(kThreads, 2) void route_grad(const RouteArgs a) {
       float e = 0.0f, ed = 0.0f;
 #pragma unroll
       for (int q = 0; q < KPL; q++) {
+        if (q * L >= a.k) break;
         xc[q] = ex2((xc[q] - m) * kLog2e);
         e += xc[q];
         ed += xc[q] * dwc[q];
@@ -682,6 +690,7 @@ __global__ __launch_bounds__(kThreads, 2) void route_grad(const RouteArgs a) {
       T* gp = static_cast<T*>(a.grad) + t * a.gstride;
 #pragma unroll
       for (int q = 0; q < KPL; q++) {
+        if (q * L >= a.k) break;
         if (id[q] < 0 || id[q] >= a.E) continue;
         gp[id[q]] = E::make(xc[q] * inv * (dc[q] - pd) + xc[q] * inv_den * (a.renorm ? dwc[q] - dot : dwc[q]));
       }
