@@ -21,6 +21,15 @@
 //   d x_j = p_j (d_j - sum_e p_e d_e) + (2 dZ / T) lse p_j + (weights' part),
 // where the weights' part is w_i (dw_i - sum w dw) at the chosen experts if
 // renormalised, else p_j (dw_j [chosen] - sum w dw).
+//
+// Instructions are the bound, not bytes.  Forward, 131072 x 256 fp32 with k 8: 60
+// us in all, 35 % of the copy bandwidth.  A token of 256 experts costs 240 warp
+// instructions (three quarters for the bound, list, ranks and output of the four
+// tokens of a warp, whatever their width), and 16 warps an SM, as the logits, the
+// sums over the tokens and the next token's logits fill 128 registers, issue half
+// of the time.  Backward, 65536 x 128 bf16 with k 8 and 32 groups: 16 us, hardly
+// more than the call costs the host; 524288 tokens 80 us, 56 % of the copy
+// bandwidth.
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -163,11 +172,6 @@ struct RowRegs {
     }
   }
 };
-
-__device__ __forceinline__ float value_of_key(uint32_t k) {
-  return k == 0xFFFFFFFFu ? __uint_as_float(0x7FFFFFFFu)
-                          : __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
-}
 
 // A bound that at least k of a token's experts reach, from the largest logits of
 // its L x GPL groups: the k-th largest of the lanes' two largest of them, i from

@@ -18,6 +18,13 @@
 //
 // Few rows: a cluster of CTAs takes a row, each a part of it; the parts' k best
 // go to the first CTA's shared memory and are sorted once more.
+//
+// Each logit is read once from HBM, which alone would take 61 us for 4096 x
+// 50257 bf16; the kernel takes 116 us there (k 64, 52 % of the copy bandwidth) and
+// 162 us for 1024 x 131072 fp32 (k 256, 49 %).  Issue is active 55 % of the time
+// and DRAM busy 38 %: a row costs 20 thousand warp instructions, half of them in
+// the two passes, and its phases (maxima, histogram, sums, ranking) wait for one
+// another, which the other CTAs of the SM fill only in part.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -57,6 +64,7 @@ struct TopkArgs {
   int tile;         // vectors of a tile
   int list_at;      // where the list begins, in vectors
   int hits;         // vectors that can be noted
+  bool keep;        // whether they are kept, or read again
   int cluster;      // CTAs of a row
   int part;         // vectors of each one's part
   float tau, c;     // temperature, log2(e) / temperature
@@ -116,8 +124,9 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
   constexpr int EPV = E::kPerVec, kThreads = SH::NT, kWarps = kThreads / 32;
   extern __shared__ __align__(16) uint4 buf[];                 // the tile
   uint64_t* list = reinterpret_cast<uint64_t*>(buf + a.list_at);  // a.cap entries
-  // vectors of the row with something at the bound: a.hits entries
+  // vectors of the row with something at the bound: a.hits entries, and what they hold
   uint32_t* const hits = reinterpret_cast<uint32_t*>(list + a.cap);
+  uint4* const kept = reinterpret_cast<uint4*>(hits + a.hits);
   __shared__ __align__(16) uint32_t hist[kBins];
   __shared__ __align__(16) int range[2][kWarps];
   __shared__ uint32_t ubuf[32];
@@ -228,15 +237,15 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
       __syncthreads();
       n = (int)n_list;
     };
-    // Lists the elements of the first h hits that reach the bound, read again (from
-    // L2 mostly) and spread over the threads.
+    // Lists the elements of the first h hits that reach the bound, spread over the
+    // threads; if they are not kept, they are read again, from L2 mostly.
     auto flush = [&](int h, float bound) {
       auto each = [&](auto f) {
-        for (int q = tid; q < h * EPV; q += kThreads) f((int)hits[q / EPV] * EPV + q % EPV - shift_e);
+        for (int q = tid; q < h * EPV; q += kThreads) f((int)hits[q / EPV] * EPV + q % EPV - shift_e, q);
       };
-      each([&](int e) {
+      each([&](int e, int q) {
         if (e < 0 || e >= V) return;
-        const float x = E::load(start + e);
+        const float x = a.keep ? E::load(reinterpret_cast<const T*>(kept) + q) : E::load(start + e);
         const uint64_t v = composite(e, x);
         if (!(x < bound) && v > thr) {
           const uint32_t at = atomicAdd(&n_list, 1u);
@@ -245,7 +254,7 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
       });
       __syncthreads();
       if (n_list <= (uint32_t)a.cap) n = (int)n_list;
-      else select(each);
+      else select([&](auto f) { each([&](int e, int) { f(e); }); });
     };
     for (int t0 = first;; t0 += a.tile) {
       const Where now = next;
@@ -339,7 +348,10 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
         for (int j = 0; j < EPV; j += 2) sum = add2(sum, ex2_2(fma2(pair(x[j], x[j + 1]), c2, mc)));
         if (!all_below<DT>(r, bound2)) {
           const uint32_t at = atomicAdd(&n_hits, 1u);
-          if (at < (uint32_t)a.hits) hits[at] = (uint32_t)(t0 + i);
+          if (at < (uint32_t)a.hits) {
+            hits[at] = (uint32_t)(t0 + i);
+            if (a.keep) kept[at] = r;
+          }
         }
       };
       // whole blocks of vectors, then the rest one by one
@@ -410,7 +422,10 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
     auto write = [&](int at, uint64_t v) {
       const int32_t e = (int32_t)~(uint32_t)v;
       a.idx[row * a.k + at] = e;
-      if (a.vals) static_cast<T*>(a.vals)[row * a.k + at] = start[e];
+      if (a.vals) {  // only zeros and NaN have several logits to a key
+        const float x = value_of_key((uint32_t)(v >> 32));
+        static_cast<T*>(a.vals)[row * a.k + at] = x == 0.0f || x != x ? start[e] : E::make(x);
+      }
     };
     auto write_lse = [&]() {
       if (a.lse && tid == 0) a.lse[row] = shift_of(M) / a.tau + logf(S);
@@ -466,7 +481,7 @@ cudaError_t launch(TopkArgs& a, cudaStream_t s) {
   }
   // tiles of one size that fit beside the list, the last one a little shorter
   constexpr int EPV = Elem<DT>::kPerVec;
-  a.cap = 1024;
+  a.cap = 512;
   while (a.cap < 3 * a.k) a.cap *= 2;
   const bool whole = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && a.stride % EPV == 0;
   const int64_t nv = (a.V + (whole ? 0 : EPV - 1) + EPV - 1) / EPV;
@@ -474,8 +489,14 @@ cudaError_t launch(TopkArgs& a, cudaStream_t s) {
   while (a.cluster < kMaxCluster && a.rows * a.cluster <= num_sms() && nv > 4 * SH::NT * a.cluster)
     a.cluster *= 2;
   a.part = (int)((nv + a.cluster - 1) / a.cluster);
-  a.hits = std::max(1024, 6 * a.k);
-  const int64_t most = (SH::kSmem - a.cap * 8 - a.hits * 4) / 16;
+  // noted vectors are kept where a quarter of the memory holds them and the list
+  // (4096 x 50257 bf16, k 64: 120 us against 125; k 256 in large tiles, 1024 x
+  // 131072 fp32: 169 against 166)
+  a.hits = std::max(256, (4 * a.k + 3) & ~3);
+  a.keep = a.cap * 8 + a.hits * 20 <= SH::kSmem / 4;
+  if (!a.keep) a.hits = std::max(1024, 6 * a.k);
+  const int hit_bytes = a.hits * (a.keep ? 20 : 4);
+  const int64_t most = (SH::kSmem - a.cap * 8 - hit_bytes) / 16;
   const int64_t tiles = (a.part + most - 1) / most;
   a.tile = (int)((a.part + tiles - 1) / tiles);
   size_t bytes = (size_t)a.tile * 16;
@@ -491,7 +512,7 @@ cudaError_t launch(TopkArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(clusters * a.cluster));
   cfg.blockDim = dim3(SH::NT);
-  cfg.dynamicSmemBytes = (size_t)a.list_at * 16 + (size_t)a.cap * 8 + (size_t)a.hits * 4;
+  cfg.dynamicSmemBytes = (size_t)a.list_at * 16 + (size_t)a.cap * 8 + (size_t)hit_bytes;
   cfg.stream = s;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;

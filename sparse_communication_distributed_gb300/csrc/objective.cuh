@@ -12,7 +12,6 @@
 namespace scape {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
 
@@ -257,6 +256,12 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   if (x != x) return 0xFFFFFFFFu;
   const uint32_t u = __float_as_uint(x + 0.0f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// ... and the logit of a key (of zero +0, of NaN one of them).
+__device__ __forceinline__ float value_of_key(uint32_t k) {
+  return k == 0xFFFFFFFFu ? __uint_as_float(0x7FFFFFFFu)
+                          : __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
 
 // Sum / maximum over the CTA; every thread receives it.  "buf" is shared
