@@ -341,12 +341,12 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
       const float sh = shift_of(m);
       const pair_t c2 = pair(a.c, a.c), mc = pair(-sh * a.c, -sh * a.c);
       pair_t sum = pair(0.0f, 0.0f);
-      auto take = [&](const uint4 r, int i) {
+      auto take = [&](const uint4 r, int i, bool in) {
         float x[EPV];
         E::unpack(r, x);
 #pragma unroll
         for (int j = 0; j < EPV; j += 2) sum = add2(sum, ex2_2(fma2(pair(x[j], x[j + 1]), c2, mc)));
-        if (!all_below<DT>(r, bound2)) {
+        if (in && !all_below<DT>(r, bound2)) {
           const uint32_t at = atomicAdd(&n_hits, 1u);
           if (at < (uint32_t)a.hits) {
             hits[at] = (uint32_t)(t0 + i);
@@ -363,12 +363,14 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
         for (int u = 0; u < kBlk; u++) r[u] = buf[(u0 + u) * kThreads + tid];
         fetch(next, u0);
 #pragma unroll
-        for (int u = 0; u < kBlk; u++) take(r[u], (u0 + u) * kThreads + tid);
+        for (int u = 0; u < kBlk; u++) take(r[u], (u0 + u) * kThreads + tid, true);
       }
 #pragma unroll 1
       for (int u = u0; u * kThreads + wid * 32 < here; u++) {
         const int i = u * kThreads + tid;
-        take(i < here ? buf[i] : neg_inf_vec<DT>(), i);
+        // (what a lane has beyond the tile counts for the sums alone: the vector there
+        // is the next tile's or part's, and a bound of -inf would note it twice)
+        take(i < here ? buf[i] : neg_inf_vec<DT>(), i, i < here);
       }
       for (; u0 * kThreads < next.hi; u0 += kBlk) fetch(next, u0);
       s += sum.x + sum.y;

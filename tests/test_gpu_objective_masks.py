@@ -1,0 +1,57 @@
+"""The training-objective operators where a mask leaves little or nothing, where
+it is a large finite number instead of -inf, and where logits are infinite.
+
+References are objective_ref's on logits shifted by the row's largest, which
+changes neither a softmax nor a loss: a row masked at -1e30 throughout is then a
+row of zeros, and the bounds do not grow with the mask's size.  A word that is
+more than 1e6 below the row's largest has a probability of 0 in any arithmetic
+and stands as -inf."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import objective_ref as ref  # noqa: E402
+import sparse_communication_distributed_gb300 as pkg  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+INF = float("inf")
+
+
+def cuda(x, dtype="f32"):
+    return torch.from_numpy(np.ascontiguousarray(x)).to(DT[dtype]).cuda()
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+# ---- top logits: fewer words than k are left --------------------------------------------------------
+
+
+@pytest.mark.parametrize("R,V,k,dtype,left", [
+    (1, 32000, 256, "bf16", 200), (1, 40000, 1024, "bf16", 700), (40, 50257, 1024, "bf16", 300), (700, 50257, 1024, "f16", 1000),
+    (1000, 8100, 256, "bf16", 100), (1000, 8100, 200, "f16", 190), (3, 131075, 256, "f32", 255), (500, 4001, 250, "f32", 40),
+    (2, 33000, 64, "bf16", 30), (900, 20000, 64, "bf16", 1)])
+def test_topk_where_fewer_than_k_words_are_left(R, V, k, dtype, left):
+    rng = np.random.default_rng(V + k)
+    h = np.full((R, V), -INF, np.float32)
+    for r in range(R):
+        h[r, rng.choice(V, left, replace=False)] = rng.standard_normal(left) * 3
+    x = cuda(h, dtype)
+    idx, vals, lse = pkg.topk_logits(x, k)
+    i = idx.cpu().numpy()
+    assert all(np.unique(row).size == k for row in i)
+    h = f64(x)
+    for r in range(R):
+        words = np.flatnonzero(h[r] > -INF)
+        best = words[ref.topk(h[r, words], left)]
+        masked = np.setdiff1d(np.arange(k), words, assume_unique=True)  # (the first k hold enough of them)
+        masked = masked if masked.size >= k - left else np.setdiff1d(np.arange(2 * k), words)
+        assert np.array_equal(i[r], np.concatenate([best, masked[:k - left]])), r
+        L = ref.lse(h[r, words])
+        assert abs(float(lse[r]) - L) <= ref.lse_tol(V, L) if r < 50 else True
+    assert torch.equal(vals.cpu(), torch.gather(x.cpu(), 1, torch.from_numpy(i).long()))
