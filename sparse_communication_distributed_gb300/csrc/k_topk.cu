@@ -339,7 +339,8 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
       }
       const uint32_t bound2 = bound_of<DT>(bound);
       const float sh = shift_of(m);
-      const pair_t c2 = pair(a.c, a.c), mc = pair(-sh * a.c, -sh * a.c);
+      const Shift by(sh, a.c);  // (this thread's own maximum, far below the row's where all it has is masked)
+      const pair_t c2 = pair(by.c, by.c), mc = pair(-by.k, -by.k);
       pair_t sum = pair(0.0f, 0.0f);
       auto take = [&](const uint4 r, int i, bool in) {
         float x[EPV];
@@ -373,7 +374,7 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
         take(i < here ? buf[i] : neg_inf_vec<DT>(), i, i < here);
       }
       for (; u0 * kThreads < next.hi; u0 += kBlk) fetch(next, u0);
-      s += sum.x + sum.y;
+      s += (sum.x + sum.y) * by.fix(sh);
       fetch_ragged(next);
       auto all_of_tile = [&](auto f) {
 #pragma unroll 1

@@ -92,6 +92,25 @@ __device__ __forceinline__ void copy_wait() {
 // nothing but -inf is then exp2(-inf) = 0 and not NaN.
 __device__ __forceinline__ float shift_of(float m) { return m == neg_inf() ? 0.0f : m; }
 
+// The terms 2^((x - m) c) of such a sum at one FMA each, as 2^(x c' - k).  In
+// general c' = c and k = m c rounded: the FMA takes the exact product, so the
+// terms are all off by the same factor 2^(m c - k), which fix takes out of their
+// sum.  That holds while the factor is within 2^32, for m c below 2^30.  Beyond,
+// what is below m is so by 32 / c at least and its term is 0 in fp32; any c' shows
+// that, and with a power of two that puts m c' between 2^31 and 2^32 k is exact,
+// and finite down to the type's lowest value.  m is finite (+inf gives NaN).
+struct Shift {
+  float c, k;
+  __device__ __forceinline__ Shift(float m, float c_) : c(c_), k(m * c_) {
+    if (!(fabsf(k) < 0x1p30f)) {
+      const int biased = (__float_as_int(m) >> 23) & 0xFF;
+      c = __int_as_float(min(285 - biased, 254) << 23);
+      k = m * c;
+    }
+  }
+  __device__ __forceinline__ float fix(float m) const { return ex2(__fmaf_rn(-m, c, k)); }
+};
+
 template <int DT>
 struct Elem;
 

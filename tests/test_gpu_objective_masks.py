@@ -55,3 +55,52 @@ def test_topk_where_fewer_than_k_words_are_left(R, V, k, dtype, left):
         L = ref.lse(h[r, words])
         assert abs(float(lse[r]) - L) <= ref.lse_tol(V, L) if r < 50 else True
     assert torch.equal(vals.cpu(), torch.gather(x.cpu(), 1, torch.from_numpy(i).long()))
+
+
+# ---- masks that are large finite numbers ------------------------------------------------------------
+
+LOWEST = {"bf16": -3.3895313892515355e38, "f16": -65504.0, "f32": -3.4028234663852886e38}
+
+
+def masked(rng, R, V, dtype, where, value):
+    """Logits of which the last 8 words, all but 40 words, or every word hold the mask's value."""
+    h = (rng.standard_normal((R, V)) * 3).astype(np.float32)
+    keep = np.ones((R, V), bool)
+    if where == "tail":
+        keep[:, -8:] = False
+    elif where == "most":
+        keep[:] = False
+        for r in range(R):
+            keep[r, rng.choice(V, 40, replace=False)] = True
+    else:
+        keep[:] = False
+    low = LOWEST[dtype] if value == "lowest" else max(value, LOWEST[dtype])
+    return cuda(np.where(keep, h, np.float32(low)), dtype), keep
+
+
+def shifted(h):
+    d = h - h.max(1, keepdims=True)
+    return np.where(d < -1e6, -INF, d)
+
+
+SIZES = [(3, 300), (400, 700), (2, 50257), (1, 140000)]
+MASKS = ["lowest", -1e30, -1e10, -1e4]
+
+
+@pytest.mark.parametrize("R,V", SIZES)
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("where", ["tail", "most", "whole"])
+def test_topk_with_finite_masks(R, V, dtype, where):
+    rng = np.random.default_rng(V)
+    for value in MASKS:
+        x, _ = masked(rng, R, V, dtype, where, value)
+        h = f64(x)
+        for tau in (1.0, 2.0, 1.7):
+            idx, _, lse = pkg.topk_logits(x, 20, temperature=tau)
+            got = f64(lse)
+            for r in range(min(R, 5)):
+                assert np.array_equal(idx[r].cpu().numpy(), ref.topk(h[r], 20))
+                m = h[r].max()
+                L = m / tau + ref.lse((h[r] - m) / tau)
+                assert abs(got[r] - L) <= ref.lse_tol(V, L), (value, tau, r, got[r], L)
+            assert np.isfinite(got).all()
