@@ -656,7 +656,8 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
       const float base = shfl_max(q.base, kMerge);
       if (!BUCKET) {  // relative to the CTA's base
         const float bd = shift_of(q.base) - shift_of(base), f = expf(bd);
-        q.b = q.z == 0.0f ? 0.0f : f * (q.b + bd * q.zp);
+        // (f = 0: a warp of entries at the type's lowest value, whose q are 0 whatever its b)
+        q.b = f == 0.0f || q.z == 0.0f ? 0.0f : f * (q.b + bd * q.zp);
         q.z = q.z == 0.0f ? 0.0f : f * q.z;
       }
       q.b = shfl_sum(q.b, kMerge);

@@ -104,3 +104,41 @@ def test_topk_with_finite_masks(R, V, dtype, where):
                 L = m / tau + ref.lse((h[r] - m) / tau)
                 assert abs(got[r] - L) <= ref.lse_tol(V, L), (value, tau, r, got[r], L)
             assert np.isfinite(got).all()
+
+
+# ---- distillation -----------------------------------------------------------------------------------
+
+
+def check_distill(x, idx, vals, tl, y, tau, dtype, loss, grad, rows, kd=0.7, ce=0.4):
+    """Rows of x against the shifted reference; a loss or gradient that is None is not looked at."""
+    h, v = shifted(f64(x)), f64(vals)
+    for r in rows:
+        want, tol, wg, gtol = ref.distill(h[r], idx[r], v[r], None if tl is None else float(tl[r]), int(y[r]), 1.0, tau, kd, ce)
+        if loss is not None:
+            assert abs(float(loss[r]) - want) <= tol, (r, float(loss[r]), want, tol)
+        if grad is not None:
+            g = f64(grad[r])
+            off = np.abs(g - wg) - (gtol + (np.abs(wg) + gtol) * ref.ROUND[dtype] + ref.TINY[dtype])
+            assert off.max() <= 0, (r, int(off.argmax()), g[off.argmax()], wg[off.argmax()])
+
+
+@pytest.mark.parametrize("V,k,tau", [(300, 64, 1.0), (50257, 200, 2.0), (140001, 400, 1.5), (900001, 64, 2.0)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_with_teacher_entries_at_the_lowest_value(V, k, tau, dtype, tail):
+    # a teacher whose own mask left it 20 words: the others of its k hold the type's lowest value, and q = 0; so
+    # they do where the student's mask is -inf
+    rng = np.random.default_rng(V)
+    R = 3
+    x = rng.standard_normal((R, V)).astype(np.float32) * 3
+    idx = np.stack([rng.permutation(V)[:k] for _ in range(R)]).astype(np.int32)
+    x[2, idx[2, 20:]] = -INF
+    v = np.full((R, k), LOWEST[dtype], np.float32)
+    v[:, :20] = rng.standard_normal((R, 20)) * 2
+    vals, xt = cuda(v, dtype), cuda(x, dtype)
+    tl = np.array([ref.lse(r[:20] / tau) + 0.1 for r in f64(vals)], np.float32) if tail else None
+    y = np.full(R, -1)
+    loss, grad = pkg.distill_loss_grad(xt, torch.from_numpy(idx).cuda(), vals, teacher_lse=None if tl is None else cuda(tl),
+                                       temperature=tau, kd_weight=0.7)
+    vals[:, 20:] = -INF  # what they count as
+    check_distill(xt, idx, vals, tl, y, tau, dtype, loss, grad, range(R))
