@@ -173,15 +173,18 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
       }
     }
     const float Ms = shift_of(cta_max(all.m, fbuf));
-    const float L = Ms / a.tau + logf(cta_sum(all.s * ex2((all.m - Ms) * a.c), fbuf));
-    float L1 = 0.0f, Lr = neg_inf();
-    if (y >= 0)
-      L1 = Ms + logf(cta_sum(one.s * ex2((one.m - Ms) * kLog2e), fbuf));
-    if (tail_mode) {
-      const float Mr = shift_of(cta_max(rest.m, fbuf));
-      Lr = Mr / a.tau + logf(cta_sum(rest.s * ex2((rest.m - Mr) * a.c), fbuf));
+    const float S = cta_sum(all.s * ex2((all.m - Ms) * a.c), fbuf), L = Ms / a.tau + logf(S);
+    float L1 = 0.0f, S1 = 1.0f, Lr = neg_inf(), Mr = 0.0f, Sr = 0.0f;
+    if (y >= 0) {
+      S1 = cta_sum(one.s * ex2((one.m - Ms) * kLog2e), fbuf);
+      L1 = Ms + logf(S1);
     }
-    const bool bucket = tail_mode && has && Lr > neg_inf();
+    if (tail_mode) {
+      Mr = shift_of(cta_max(rest.m, fbuf));
+      Sr = cta_sum(rest.s * ex2((rest.m - Mr) * a.c), fbuf);
+      Lr = Mr / a.tau + logf(Sr);
+    }
+    const bool bucket = tail_mode && has && Sr > 0.0f;
     const float qr = bucket ? fmaxf(0.0f, 1.0f - Q) : 0.0f;
     float kl = 0.0f;
     for (int i = tid; i < a.k; i += kThreads) {
@@ -198,15 +201,16 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
     }
     if (!g) continue;
 
-    // the gradient: ref = L or L_rest, so that exp(s - ref) keeps the small
-    // probabilities of a bucket
+    // the gradient: p = exp(s - ref) / over with the maximum and the sum of the row, or
+    // of the bucket, whose small probabilities it keeps; from differences to the
+    // maximum, as a maximum may be the type's lowest value and p still 1 / vocab
     const float A = has ? w * a.kd * a.tau : 0.0f, C1 = y >= 0 ? w * a.ce : 0.0f;
-    const float ref = bucket ? Lr : L;
-    const float C = bucket ? A * ((Q + qr) * expf(Lr - L) - qr) : A * Q;
-    const float ref2 = ref * kLog2e, L12 = L1 * kLog2e;
+    const float ref = bucket ? Mr : Ms, over = bucket ? Sr : S;
+    const float C = (bucket ? A * ((Q + qr) * (Sr * ex2((Mr - Ms) * a.c) / S) - qr) : A * Q) / over;
+    const float C2 = C1 / S1;
     auto grad_of = [&](float x) {
-      float r = C * ex2(x * a.c - ref2);
-      if (y >= 0) r += C1 * ex2(x * kLog2e - L12);
+      float r = C * ex2((x - ref) * a.c);
+      if (y >= 0) r += C2 * ex2((x - Ms) * kLog2e);
       return r;
     };
     __syncthreads();  // sx is complete: the row may be overwritten
@@ -222,9 +226,9 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
     bool label_listed = false;
     for (int i = tid; i < a.k; i += kThreads) {
       if (sidx[i] < 0) continue;
-      float r = A * ((Q + qr) * expf(sx[i] / a.tau - L) - sq[i]);
+      float r = A * ((Q + qr) * (ex2((sx[i] - Ms) * a.c) / S) - sq[i]);
       if (y >= 0) {
-        r += C1 * expf(sx[i] - L1);
+        r += C2 * ex2((sx[i] - Ms) * kLog2e);
         if (sidx[i] == y) {
           r -= C1;
           label_listed = true;
@@ -294,7 +298,7 @@ enum { kOne, kTwo, kSquare };
 
 // What one warp works out for all threads once a row's statistics are known.
 struct __align__(16) Row {
-  float m, K1, K2, rS;         // gradient = K1 2^((x - m) c) + K2 2^((x - m) log2 e) at unlisted
+  float m, K1, K2, rS;         // gradient = K1 2^((x - m) c) + K2 2^((x - m) log2 e) at unlisted, by Shift's terms
   float M, A, C1, rS1;         // p = 2^((x - M) c) rS; softmax(x) = 2^((x - M) log2 e) rS1
   float Qr, base, rz, unused;  // sum q + q_rest; q_i = exp(t_i - base) rz
 };
@@ -578,10 +582,12 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     at = where(row_at(more ? row2 : row));
     if (more) load_side(row2);
     else at.hi = 0;
-    const pair_t c2 = pair(a.c, a.c), l2 = pair(kLog2e, kLog2e);
     {
+      // (this warp's own maximum, far below the row's where all it has is masked)
       const float sh = shift_of(q.m);
-      const pair_t mc = pair(-sh * a.c, -sh * a.c), ml = pair(-sh * kLog2e, -sh * kLog2e);
+      const Shift by(sh, a.c), by1(sh, kLog2e);
+      const pair_t c2 = pair(by.c, by.c), mc = pair(-by.k, -by.k);
+      const pair_t l2 = pair(by1.c, by1.c), ml = pair(-by1.k, -by1.k);
       pair_t s = pair(0.0f, 0.0f), s1 = s;
       const int u0 = each([&](int u0) { if (!g) fetch(at, u0); },
                           [&](const uint4 r, int) {
@@ -596,8 +602,9 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
         }
       });
       if (!g) fetch_rest(u0);
-      q.s = shfl_sum(s.x + s.y, 32);
-      q.s1 = TWO ? shfl_sum(s1.x + s1.y, 32) : q.s;
+      const float fix = by.fix(sh);
+      q.s = shfl_sum(s.x + s.y, 32) * fix;
+      q.s1 = TWO ? shfl_sum(s1.x + s1.y, 32) * (EXPS == kTwo ? by1.fix(sh) : fix * fix) : q.s;
     }
     q.tm = q.base = neg_inf();
     q.ts = q.ts1 = q.z = q.zp = q.b = 0.0f;
@@ -715,6 +722,9 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
             r.K2 = q.s1 > 0.0f ? r.C1 * f1 * r.rS1 : 0.0f;
           }
           if (!TWO) r.K1 += r.K2;
+          const float fix = Shift(shr, a.c).fix(shr);  // (the threads' terms are off by its inverse)
+          r.K1 *= fix;
+          if (TWO) r.K2 *= EXPS == kTwo ? Shift(shr, kLog2e).fix(shr) : fix * fix;
           rows[turn] = r;
         }
         if (a.loss && rank == 0)
@@ -731,7 +741,9 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     if (g) {
       __syncthreads();
       const Row t = rows[turn];
-      const pair_t mc = pair(-t.m * a.c, -t.m * a.c), ml = pair(-t.m * kLog2e, -t.m * kLog2e);
+      const Shift by(t.m, a.c), by1(t.m, kLog2e);
+      const pair_t c2 = pair(by.c, by.c), mc = pair(-by.k, -by.k);
+      const pair_t l2 = pair(by1.c, by1.c), ml = pair(-by1.k, -by1.k);
       const pair_t k1 = pair(t.K1, t.K1), k2 = pair(t.K2, t.K2);
       auto grad_of = [&](pair_t x) {
         const pair_t e = ex2_2(fma2(x, c2, mc));

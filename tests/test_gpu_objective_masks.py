@@ -142,3 +142,64 @@ def test_distill_with_teacher_entries_at_the_lowest_value(V, k, tau, dtype, tail
                                        temperature=tau, kd_weight=0.7)
     vals[:, 20:] = -INF  # what they count as
     check_distill(xt, idx, vals, tl, y, tau, dtype, loss, grad, range(R))
+
+
+def case_of(rng, x, keep, k, tau, tail):
+    """k words of each row that are not masked (any words where all are) for a teacher, and a label among them or not."""
+    R, V = x.shape
+    idx = np.empty((R, k), np.int32)
+    y = np.empty(R, np.int64)
+    for r in range(R):
+        words = np.flatnonzero(keep[r]) if keep[r].any() else np.arange(V)
+        idx[r] = rng.choice(words, k, replace=False)
+        y[r] = rng.choice(words)
+    vals = cuda(rng.standard_normal((R, k)) * 2)
+    tl = np.array([ref.lse(v / tau) + 0.3 for v in f64(vals)], np.float32) if tail else None
+    return idx, vals, tl, y
+
+
+def distill_masked(R, V, dtype, where, tail, labels):
+    rng = np.random.default_rng(V)
+    for value in MASKS:
+        x, keep = masked(rng, R, V, dtype, where, value)
+        for tau in (1.0, 2.0, 1.7):
+            idx, vals, tl, y = case_of(rng, x, keep, 8, tau, tail)
+            y = y if labels else np.full(R, -1)
+            loss, grad = pkg.distill_loss_grad(x, torch.from_numpy(idx).cuda(), vals, teacher_lse=None if tl is None else cuda(tl),
+                                               labels=torch.from_numpy(y).cuda(), temperature=tau, kd_weight=0.7, ce_weight=0.4)
+            yield x, idx, vals, tl, y, tau, loss, grad
+
+
+LONG = [(1, 900001, "bf16"), (1, 450001, "f32")]  # rows that do not fit on chip
+
+
+@pytest.mark.parametrize("R,V,dtype", [(R, V, d) for R, V in SIZES for d in ("bf16", "f16", "f32")] + LONG)
+@pytest.mark.parametrize("where", ["tail", "most", "whole"])
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_gradient_with_finite_masks(R, V, dtype, where, tail):
+    for labels in (True, False):
+        for x, idx, vals, tl, y, tau, loss, grad in distill_masked(R, V, dtype, where, tail, labels):
+            check_distill(x, idx, vals, tl, y, tau, dtype, None if where == "whole" else loss, grad, range(min(R, 4)))
+            assert bool(torch.isfinite(grad).all())
+
+
+@pytest.mark.parametrize("dtype,V", [("bf16", 700), ("f32", 50257), ("f32", 450001)])
+def test_distill_bucket_of_masked_words(dtype, V):
+    # every word that is not listed is masked: the bucket's mass is exp(value / tau), the loss q_rest times its
+    # distance, and the bucket's gradient - kd tau q_rest, spread evenly
+    rng = np.random.default_rng(5)
+    x = np.full((1, V), -1e10, np.float32)
+    idx = rng.permutation(V)[:8].astype(np.int32)[None]
+    x[0, idx[0]] = rng.standard_normal(8)
+    xt = cuda(x, dtype)
+    vals = cuda(rng.standard_normal((1, 8)))
+    tau, tl = 2.0, np.array([ref.lse(f64(vals)[0] / 2.0) + 0.3], np.float32)
+    loss, grad = pkg.distill_loss_grad(xt, torch.from_numpy(idx).cuda(), vals, teacher_lse=cuda(tl), temperature=tau)
+    low = f64(xt).min()
+    qr = 1 - np.exp(f64(vals)[0] / tau - float(tl[0])).sum()
+    want = tau ** 2 * qr * -low / tau
+    assert abs(float(loss) - want) < 1e-5 * want
+    rest = np.ones(V, bool)
+    rest[idx[0]] = False
+    g = f64(grad)[0][rest]
+    assert np.abs(g + tau * qr / (V - 8)).max() <= tau * qr / (V - 8) * (ref.ROUND[dtype] + 1e-5)
