@@ -131,20 +131,20 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
     const float xy = y >= 0 ? E::load(view.p + y) : 0.0f;
     const bool tail_mode = a.tlse != nullptr;
     bool has = __syncthreads_or(tm != neg_inf());
-    float lt = 0.0f;  // log of the teacher's normaliser
+    float base = 0.0f, lz = 0.0f;  // log q = (t - base) - lz
     if (has) {
       if (tail_mode) {
-        lt = a.tlse[row];
+        base = a.tlse[row];
       } else {
-        const float M = shift_of(cta_max(tm, fbuf));
+        base = shift_of(cta_max(tm, fbuf));
         float z = 0.0f;
-        for (int i = tid; i < a.k; i += kThreads) z += expf(sq[i] - M);
-        lt = M + logf(cta_sum(z, fbuf));
+        for (int i = tid; i < a.k; i += kThreads) z += expf(sq[i] - base);
+        lz = logf(cta_sum(z, fbuf));
       }
     }
     float qs = 0.0f;
     for (int i = tid; i < a.k; i += kThreads) {
-      const float logq = sq[i] - lt, q = has && sidx[i] >= 0 ? expf(logq) : 0.0f;
+      const float logq = sq[i] - base - lz, q = has && sidx[i] >= 0 ? expf(logq) : 0.0f;
       sq[i] = q;
       qs += q;
     }
@@ -173,16 +173,12 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
       }
     }
     const float Ms = shift_of(cta_max(all.m, fbuf));
-    const float S = cta_sum(all.s * ex2((all.m - Ms) * a.c), fbuf), L = Ms / a.tau + logf(S);
-    float L1 = 0.0f, S1 = 1.0f, Lr = neg_inf(), Mr = 0.0f, Sr = 0.0f;
-    if (y >= 0) {
-      S1 = cta_sum(one.s * ex2((one.m - Ms) * kLog2e), fbuf);
-      L1 = Ms + logf(S1);
-    }
+    const float S = cta_sum(all.s * ex2((all.m - Ms) * a.c), fbuf), ls = logf(S);
+    float S1 = 1.0f, Mr = 0.0f, Sr = 0.0f;
+    if (y >= 0) S1 = cta_sum(one.s * ex2((one.m - Ms) * kLog2e), fbuf);
     if (tail_mode) {
       Mr = shift_of(cta_max(rest.m, fbuf));
       Sr = cta_sum(rest.s * ex2((rest.m - Mr) * a.c), fbuf);
-      Lr = Mr / a.tau + logf(Sr);
     }
     const bool bucket = tail_mode && has && Sr > 0.0f;
     const float qr = bucket ? fmaxf(0.0f, 1.0f - Q) : 0.0f;
@@ -190,13 +186,13 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
     for (int i = tid; i < a.k; i += kThreads) {
       const float q = sq[i];
       if (q != 0.0f)
-        kl += q * ((load_val(a.vals, a.vals_dtype, row * a.k + i) / a.tau - lt) - (sx[i] / a.tau - L));
+        kl += q * ((load_val(a.vals, a.vals_dtype, row * a.k + i) / a.tau - base - lz) - ((sx[i] - Ms) / a.tau - ls));
     }
     kl = cta_sum(kl, fbuf);
-    if (qr > 0.0f) kl += qr * (logf(qr) - (Lr - L));
+    if (qr > 0.0f) kl += qr * (logf(qr) - ((Mr - Ms) / a.tau + logf(Sr) - ls));
     if (a.loss && tid == 0) {
       float l = has ? a.kd * a.tau * a.tau * kl : 0.0f;
-      if (y >= 0) l += a.ce * (L1 - xy);
+      if (y >= 0) l += a.ce * (Ms - xy + logf(S1));
       a.loss[row] = w * l;
     }
     if (!g) continue;
@@ -267,13 +263,14 @@ static_assert(Deep::MAXK >= kMaxK, "every entry has a thread");
 // to a maximum: s = sum 2^((x - m) c), and s1 the same at temperature 1.
 struct Part {
   float m, s, s1;     // coordinates held in registers (with a bucket: those not listed)
-  float tm, ts, ts1;  // listed coordinates (bucket only)
-  float b;            // over the listed coordinates of this part: sum u_i (t_i - base - s_i), u_i = exp(t_i - base)
+  float tm, ts, ts1;  // listed coordinates (the sums with a bucket only)
+  float b;            // over the listed coordinates of this part: sum u_i (t_i - base - (x_i - tm) / tau),
+                      // u_i = exp(t_i - base): no term holds a maximum, which may be the type's lowest value
+  float zp;           // sum u_i over those
   float base, z;      // over all listed coordinates: base = max t_i (u_i then is relative to
                       // teacher_lse with a bucket), z = sum u_i
-  float zp;           // sum u_i over those of this part
 };
-constexpr int kShared = 7;  // the leading members differ from part to part
+constexpr int kShared = 8;  // the leading members differ from part to part
 
 __device__ __forceinline__ float shfl_max(float x, int n) {
   for (int o = n >> 1; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
@@ -307,7 +304,7 @@ struct __align__(16) Row {
 struct Loss {
   float M, m, S, S1;   // as in Part and Row: the whole row's sums
   float z, Q, qr;      // the teacher's
-  float top, s, b;     // p_listed on the scale of s; as in Part
+  float top, s, b;     // p_listed on the scale of s; as in Part, relative to M
   float w, xy;
   int64_t row;
   bool has, hard;
@@ -482,18 +479,18 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     __syncwarp();
     if (lane < n_pend) {
       const Loss p = pend[lane];
-      const float L = p.M * inv_tau + logf(p.S);
+      const float ls = logf(p.S);
       float l = 0.0f;
-      if (p.has) {  // sum q_i (t_i - log z - base - s_i) + L sum q_i
-        float kl = BUCKET ? p.b + p.Q * L : p.b / p.z + (L - logf(p.z));
+      if (p.has) {  // sum q_i (t_i - log z - base - (x_i - M) / tau) + log S sum q_i
+        float kl = BUCKET ? p.b + p.Q * ls : p.b / p.z + (ls - logf(p.z));
         if (p.qr > 0.0f) {  // log q_rest - log p_rest, both from what is listed
           const float odds = p.top / p.s;
-          const float logp = odds < 1.0f ? log1pf(odds) : L - (p.m * inv_tau + logf(p.s));
+          const float logp = odds < 1.0f ? log1pf(odds) : (p.M - p.m) * inv_tau + (ls - logf(p.s));
           kl += p.qr * (log1pf(-p.Q) + logp);
         }
         l = a.kd * a.tau * a.tau * kl;
       }
-      if (p.hard) l += a.ce * (p.M + logf(p.S1) - p.xy);
+      if (p.hard) l += a.ce * (p.M - p.xy + logf(p.S1));
       a.loss[p.row] = p.w * l;
     }
     __syncwarp();
@@ -617,7 +614,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
       }
       q.base = shfl_max(tmax, 32);
       const float base = BUCKET ? tlse : shift_of(q.base);
-      if (BUCKET) q.tm = shfl_max(xmax, 32);
+      q.tm = shfl_max(xmax, 32);
       const float tsh = shift_of(q.tm);
 #pragma unroll
       for (int h = 0; h < ENT; h++) {
@@ -625,7 +622,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
         q.z += u;
         if (el[h] >= 0) {
           q.zp += u;
-          if (u != 0.0f) q.b += u * ((et[h] - base) - ex[h] * inv_tau);
+          if (u != 0.0f) q.b += u * ((et[h] - base) - (ex[h] - tsh) * inv_tau);
           if (BUCKET) {
             q.ts += ex2((ex[h] - tsh) * a.c);
             if (TWO) q.ts1 += ex2((ex[h] - tsh) * kLog2e);
@@ -634,7 +631,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
       }
       q.z = shfl_sum(q.z, 32);
       q.b = shfl_sum(q.b, 32);
-      if (!BUCKET) q.zp = shfl_sum(q.zp, 32);
+      q.zp = shfl_sum(q.zp, 32);
       if (BUCKET) {
         q.ts = shfl_sum(q.ts, 32);
         q.ts1 = TWO ? shfl_sum(q.ts1, 32) : q.ts;
@@ -643,6 +640,10 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     if (lane == 0) warps[turn][wid] = q;
     __syncthreads();
     if (wid == 0) {
+      // b relative to another logit instead of tm
+      auto raise = [&](float to) {
+        if (q.zp != 0.0f) q.b += q.zp * ((shift_of(to) - shift_of(q.tm)) * inv_tau);
+      };
       // the CTA's, then the cluster's: the partial statistics of n parts, one in
       // each of the first n lanes
       auto merge = [&](int n) {
@@ -650,24 +651,27 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
         q.s = shfl_sum(q.s * ex2(d * a.c), n);
         q.s1 = TWO ? shfl_sum(q.s1 * ex2(d * kLog2e), n) : q.s;
         q.m = m;
+        const float tm = shfl_max(q.tm, n), td = q.tm - shift_of(tm);
         if (BUCKET) {
-          const float tm = shfl_max(q.tm, n), td = q.tm - shift_of(tm);
           q.ts = shfl_sum(q.ts * ex2(td * a.c), n);
           q.ts1 = TWO ? shfl_sum(q.ts1 * ex2(td * kLog2e), n) : q.ts;
-          q.tm = tm;
         }
+        raise(tm);
+        q.tm = tm;
+        q.b = shfl_sum(q.b, n);
+        q.zp = shfl_sum(q.zp, n);
       };
       q = warps[turn][min(lane, kWarps - 1)];
-      if (lane >= kWarps) q = Part{neg_inf(), 0.0f, 0.0f, neg_inf(), 0.0f, 0.0f, 0.0f, neg_inf(), 0.0f, 0.0f};
-      merge(kMerge);
+      if (lane >= kWarps) q = Part{neg_inf(), 0.0f, 0.0f, neg_inf(), 0.0f, 0.0f, 0.0f, 0.0f, neg_inf(), 0.0f};
       const float base = shfl_max(q.base, kMerge);
       if (!BUCKET) {  // relative to the CTA's base
         const float bd = shift_of(q.base) - shift_of(base), f = expf(bd);
         // (f = 0: a warp of entries at the type's lowest value, whose q are 0 whatever its b)
         q.b = f == 0.0f || q.z == 0.0f ? 0.0f : f * (q.b + bd * q.zp);
         q.z = q.z == 0.0f ? 0.0f : f * q.z;
+        q.zp = q.zp == 0.0f ? 0.0f : f * q.zp;
       }
-      q.b = shfl_sum(q.b, kMerge);
+      merge(kMerge);
       const float z = shfl_sum(q.z, kMerge);
       if (a.cluster > 1) {
         if (lane == 0) {
@@ -685,10 +689,9 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
         q = parts[turn][min(lane, a.cluster - 1)];
         if (lane >= a.cluster) {
           q.m = q.tm = neg_inf();
-          q.s = q.s1 = q.ts = q.ts1 = q.b = 0.0f;
+          q.s = q.s1 = q.ts = q.ts1 = q.b = q.zp = 0.0f;
         }
         merge(kMaxCluster);
-        q.b = shfl_sum(q.b, kMaxCluster);
       }
       if (lane == 0) {
         // the teacher: q_i = exp(t_i - base) / rz, Q = sum q_i
@@ -727,9 +730,11 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
           if (TWO) r.K2 *= EXPS == kTwo ? Shift(shr, kLog2e).fix(shr) : fix * fix;
           rows[turn] = r;
         }
-        if (a.loss && rank == 0)
+        if (a.loss && rank == 0) {
+          raise(M);
           pend[n_pend] = {sh, shr, S, S1, z, Q, qr, BUCKET ? q.ts * ex2((q.tm - shr) * a.c) : 0.0f,
                           q.s, q.b, w_now, xy, row, has, y >= 0};
+        }
       }
       if (a.loss && rank == 0 && ++n_pend == 32) write_losses();
     } else if (a.cluster > 1) {

@@ -203,3 +203,30 @@ def test_distill_bucket_of_masked_words(dtype, V):
     rest[idx[0]] = False
     g = f64(grad)[0][rest]
     assert np.abs(g + tau * qr / (V - 8)).max() <= tau * qr / (V - 8) * (ref.ROUND[dtype] + 1e-5)
+
+
+@pytest.mark.parametrize("R,V,dtype", [(R, V, d) for R, V in SIZES for d in ("bf16", "f16", "f32")] + LONG)
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_loss_of_rows_masked_throughout(R, V, dtype, tail):
+    for labels in (True, False):
+        for x, idx, vals, tl, y, tau, loss, grad in distill_masked(R, V, dtype, "whole", tail, labels):
+            check_distill(x, idx, vals, tl, y, tau, dtype, loss, None, range(min(R, 4)))
+            alone = pkg.distill_loss(x, torch.from_numpy(idx).cuda(), vals, teacher_lse=None if tl is None else cuda(tl),
+                                     labels=torch.from_numpy(y).cuda(), temperature=tau, kd_weight=0.7, ce_weight=0.4)
+            assert torch.equal(alone, loss)
+
+
+@pytest.mark.parametrize("V", [300, 50257, 140000, 450001])
+@pytest.mark.parametrize("offset", [-2.0 ** 20, 2.0 ** 20])
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_does_not_depend_on_an_offset(V, offset, tail):
+    # logits on a grid of 1/8, so that the offset of 2^20 is exact: the loss is that of the logits without it
+    rng = np.random.default_rng(V)
+    h = np.round(rng.standard_normal((2, V)) * 24) / 8
+    x = cuda(h + offset)
+    assert np.array_equal(f64(x), h + offset)
+    for tau in (1.0, 2.0, 1.7):
+        idx, vals, tl, y = case_of(rng, x, np.ones((2, V), bool), 40, tau, tail)
+        loss, grad = pkg.distill_loss_grad(x, torch.from_numpy(idx).cuda(), vals, teacher_lse=None if tl is None else cuda(tl),
+                                           labels=torch.from_numpy(y).cuda(), temperature=tau, kd_weight=0.7, ce_weight=0.4)
+        check_distill(x, idx, vals, tl, y, tau, "f32", loss, grad, range(2))
