@@ -312,7 +312,8 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
       cand = ~cand & experts;
 
       // p, and the sums
-      const pair_t c2 = pair(kLog2e, kLog2e), mc = pair(-sh * kLog2e, -sh * kLog2e);
+      const Shift by(sh, kLog2e);  // (all logits may be the type's lowest value)
+      const pair_t c2 = pair(by.c, by.c), mc = pair(-by.k, -by.k);
       pair_t s2 = pair(0.0f, 0.0f);
 #pragma unroll
       for (int j = 0; j < VPL; j += 2) {
@@ -406,14 +407,14 @@ __global__ __launch_bounds__(kThreads, 2) void route_chunks(const RouteArgs a) {
       float chosen = 0.0f;
       if (a.renorm && ok)
         for (int i = sub; i < a.k; i += L)
-          chosen += ex2((value_of_key((uint32_t)(sorted[i] >> 32)) - sh) * kLog2e);
+          chosen += by.term(value_of_key((uint32_t)(sorted[i] >> 32)));
       const float scale = a.renorm ? rcp(lanes_sum<L>(chosen)) : inv;
       if (in)
         for (int i = sub; i < a.k; i += L) {
           const uint64_t v = ok ? sorted[i] : 0;
           const int col = (int)~(uint32_t)v;  // -1 for v = 0
           a.idx[t * a.k + i] = col;
-          a.weights[t * a.k + i] = ok ? ex2((value_of_key((uint32_t)(v >> 32)) - sh) * kLog2e) * scale : 0.0f;
+          a.weights[t * a.k + i] = ok ? by.term(value_of_key((uint32_t)(v >> 32))) * scale : 0.0f;
           if (ok) atomicAdd(&sc[col], 1);
         }
       __syncwarp();
@@ -643,11 +644,13 @@ __global__ __launch_bounds__(kThreads, 2) void route_grad(const RouteArgs a) {
 #pragma unroll
     for (int j = 1; j < VPL; j++) m = fmaxf(m, x[j]);
     m = shift_of(lanes_max<L>(m));
-    const pair_t c2 = pair(kLog2e, kLog2e), mc = pair(-m * kLog2e, -m * kLog2e);
+    // differences to m first, as all logits may be the type's lowest value (65536 x
+    // 256 bf16: 22.5 us, 22.6 with one FMA by Shift, which needs more registers)
+    const pair_t c2 = pair(kLog2e, kLog2e), m2 = pair(-m, -m);
     pair_t s2 = pair(0.0f, 0.0f), pd2 = s2;
 #pragma unroll
     for (int j = 0; j < VPL; j += 2) {
-      const pair_t e = ex2_2(fma2(pair(x[j], x[j + 1]), c2, mc));
+      const pair_t e = ex2_2(mul2(add2(pair(x[j], x[j + 1]), m2), c2));
       s2 = add2(s2, e);
       pd2 = fma2(e, pair(d[j], d[j + 1]), pd2);
       x[j] = e.x;

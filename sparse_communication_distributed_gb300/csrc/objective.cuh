@@ -108,6 +108,7 @@ struct Shift {
       k = m * c;
     }
   }
+  __device__ __forceinline__ float term(float x) const { return ex2(__fmaf_rn(x, c, -k)); }
   __device__ __forceinline__ float fix(float m) const { return ex2(__fmaf_rn(-m, c, k)); }
 };
 

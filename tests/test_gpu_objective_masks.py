@@ -230,3 +230,48 @@ def test_distill_does_not_depend_on_an_offset(V, offset, tail):
         loss, grad = pkg.distill_loss_grad(x, torch.from_numpy(idx).cuda(), vals, teacher_lse=None if tl is None else cuda(tl),
                                            labels=torch.from_numpy(y).cuda(), temperature=tau, kd_weight=0.7, ce_weight=0.4)
         check_distill(x, idx, vals, tl, y, tau, "f32", loss, grad, range(2))
+
+
+# ---- routing ----------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("T,E,k", [(40, 8, 2), (50, 64, 6), (3000, 256, 8), (60, 300, 12), (30, 1000, 20), (200, 16, 4)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_with_finite_masks(T, E, k, dtype, renorm):
+    # some tokens masked throughout, some but for a few experts: weights, counts, the balance loss and gradients are
+    # those of the shifted logits; z is the mean of lse^2, infinite where that is beyond fp32
+    rng = np.random.default_rng(T + E)
+    for value in MASKS:
+        low = np.float32(LOWEST[dtype] if value == "lowest" else max(value, LOWEST[dtype]))
+        h = (rng.standard_normal((T, E)) * 2).astype(np.float32)
+        h[3::5] = low
+        h[4::5, k // 2:] = low
+        x = cuda(h, dtype)
+        h = f64(x)
+        s = shifted(h)
+        cu = np.array([0, T // 3, T], np.int32)
+        cut = torch.from_numpy(cu).cuda()
+        idx, w, counts, live, losses = pkg.route(x, k, renormalize=renorm, cu_tokens=cut)
+        rl = np.array([cu[1], T - cu[1], T, 2])
+        assert np.array_equal(idx.cpu().numpy(), np.stack([ref.topk(t, k) for t in h]))
+        rel = ref.U * (E / 8 + 64 + 16 * 20)
+        many = ref.U * (T / 8 + 512)
+        by_logit = np.exp(np.take_along_axis(s, f64(idx).astype(int), 1)
+                          - np.array([ref.lse(t[i]) if renorm else ref.lse(t) for t, i in zip(s, f64(idx).astype(int))])[:, None])
+        assert np.abs(f64(w) - by_logit).max() <= rel
+        assert np.array_equal(live.cpu().numpy(), rl) and int(counts.sum()) == T * k
+        c = f64(counts)
+        p = np.exp(s - np.array([ref.lse(t) for t in s])[:, None])
+        want = np.mean([(E * c[g] / (k * rl[g]) * p[cu[g]:cu[g + 1]].sum(0) / rl[g]).sum() for g in range(2)])
+        assert abs(float(losses[0]) - want) <= (rel + many) * want
+        L = h.max(1) + np.array([ref.lse(t) for t in s])
+        z = np.mean(L ** 2)
+        assert abs(float(losses[1]) - z) <= 1e-4 * z if z < 1e38 else float(losses[1]) == INF
+
+        dw = rng.standard_normal((T, k)).astype(np.float32)
+        grad = f64(pkg.route_backward(x, idx, counts, live, d_weights=cuda(dw), d_losses=torch.tensor([0.7, 0.0], device="cuda"),
+                                      renormalize=renorm, cu_tokens=cut))
+        wg, size = ref.route_grad(s, f64(idx).astype(int), c, rl, cu, dw.astype(np.float64), np.array([0.7, 0.0]), renorm)
+        off = np.abs(grad - wg) - ((4 * rel + 16 * ref.U) * size + np.abs(wg) * ref.ROUND[dtype] + ref.TINY[dtype])
+        assert off.max() <= 0, value
