@@ -247,15 +247,17 @@ constexpr int kMaxCluster = 8;
 // 64 KB share an SM's shared memory, and while one waits for its row the others
 // compute; two with parts of 105 KB do better where that saves a cluster, eight
 // with parts of 16 KB share an SM where rows are short or few, and there is one shape for many entries.
-template <int NT_, int VECS_, int MINB_, int ENT_>
+template <int NT_, int VECS_, int MINB_, int ENT_, bool DIFF_ = false>
 struct Shape {
   static constexpr int NT = NT_, MINB = MINB_, ENT = ENT_;
+  static constexpr bool DIFF = DIFF_;  // Terms (gradient of 16384 x 1003 bf16 with labels and bucket: 82 us
+                                       // with differences, 87 without; of 8192 x 50257 319 and 312)
   static constexpr int PART = NT_ * VECS_, MAXK = NT_ * ENT_;
   static constexpr int MOST = 13824;  // vectors that fit at all (216 KB)
 };
 using Wide = Shape<256, 16, 3, 1>;
 using Large = Shape<320, 21, 2, 1>;
-using Narrow = Shape<128, 8, 8, 2>;
+using Narrow = Shape<128, 8, 8, 2, true>;
 using Deep = Shape<320, 21, 2, 4>;
 static_assert(Deep::MAXK >= kMaxK, "every entry has a thread");
 
@@ -295,7 +297,7 @@ enum { kOne, kTwo, kSquare };
 
 // What one warp works out for all threads once a row's statistics are known.
 struct __align__(16) Row {
-  float m, K1, K2, rS;         // gradient = K1 2^((x - m) c) + K2 2^((x - m) log2 e) at unlisted, by Shift's terms
+  float m, K1, K2, rS;         // gradient = K1 2^((x - m) c) + K2 2^((x - m) log2 e) at unlisted, by Terms
   float M, A, C1, rS1;         // p = 2^((x - M) c) rS; softmax(x) = 2^((x - M) log2 e) rS1
   float Qr, base, rz, unused;  // sum q + q_rest; q_i = exp(t_i - base) rz
 };
@@ -582,9 +584,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     {
       // (this warp's own maximum, far below the row's where all it has is masked)
       const float sh = shift_of(q.m);
-      const Shift by(sh, a.c), by1(sh, kLog2e);
-      const pair_t c2 = pair(by.c, by.c), mc = pair(-by.k, -by.k);
-      const pair_t l2 = pair(by1.c, by1.c), ml = pair(-by1.k, -by1.k);
+      const Terms<SH::DIFF> at_tau(sh, a.c), at_1(sh, kLog2e);
       pair_t s = pair(0.0f, 0.0f), s1 = s;
       const int u0 = each([&](int u0) { if (!g) fetch(at, u0); },
                           [&](const uint4 r, int) {
@@ -592,16 +592,15 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
         E::unpack(r, x);
 #pragma unroll
         for (int j = 0; j < EPV; j += 2) {
-          const pair_t xx = pair(x[j], x[j + 1]), e = ex2_2(fma2(xx, c2, mc));
+          const pair_t xx = pair(x[j], x[j + 1]), e = at_tau(xx);
           s = add2(s, e);
-          if (EXPS == kTwo) s1 = add2(s1, ex2_2(fma2(xx, l2, ml)));
+          if (EXPS == kTwo) s1 = add2(s1, at_1(xx));
           if (EXPS == kSquare) s1 = fma2(e, e, s1);
         }
       });
       if (!g) fetch_rest(u0);
-      const float fix = by.fix(sh);
-      q.s = shfl_sum(s.x + s.y, 32) * fix;
-      q.s1 = TWO ? shfl_sum(s1.x + s1.y, 32) * (EXPS == kTwo ? by1.fix(sh) : fix * fix) : q.s;
+      q.s = shfl_sum(s.x + s.y, 32) * at_tau.undo;
+      q.s1 = TWO ? shfl_sum(s1.x + s1.y, 32) * (EXPS == kTwo ? at_1.undo : at_tau.undo * at_tau.undo) : q.s;
     }
     q.tm = q.base = neg_inf();
     q.ts = q.ts1 = q.z = q.zp = q.b = 0.0f;
@@ -725,9 +724,9 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
             r.K2 = q.s1 > 0.0f ? r.C1 * f1 * r.rS1 : 0.0f;
           }
           if (!TWO) r.K1 += r.K2;
-          const float fix = Shift(shr, a.c).fix(shr);  // (the threads' terms are off by its inverse)
-          r.K1 *= fix;
-          if (TWO) r.K2 *= EXPS == kTwo ? Shift(shr, kLog2e).fix(shr) : fix * fix;
+          const float undo = Terms<SH::DIFF>(shr, a.c).undo;
+          r.K1 *= undo;
+          if (TWO) r.K2 *= EXPS == kTwo ? Terms<SH::DIFF>(shr, kLog2e).undo : undo * undo;
           rows[turn] = r;
         }
         if (a.loss && rank == 0) {
@@ -746,15 +745,13 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     if (g) {
       __syncthreads();
       const Row t = rows[turn];
-      const Shift by(t.m, a.c), by1(t.m, kLog2e);
-      const pair_t c2 = pair(by.c, by.c), mc = pair(-by.k, -by.k);
-      const pair_t l2 = pair(by1.c, by1.c), ml = pair(-by1.k, -by1.k);
+      const Terms<SH::DIFF> at_tau(t.m, a.c), at_1(t.m, kLog2e);
       const pair_t k1 = pair(t.K1, t.K1), k2 = pair(t.K2, t.K2);
       auto grad_of = [&](pair_t x) {
-        const pair_t e = ex2_2(fma2(x, c2, mc));
+        const pair_t e = at_tau(x);
         if (EXPS == kSquare) return mul2(e, fma2(k2, e, k1));
         const pair_t v = mul2(k1, e);
-        return EXPS == kTwo ? fma2(k2, ex2_2(fma2(x, l2, ml)), v) : v;
+        return EXPS == kTwo ? fma2(k2, at_1(x), v) : v;
       };
       const int u0 = each([&](int u0) { fetch(at, u0); },
                           [&](const uint4 r, int u) {

@@ -112,6 +112,25 @@ struct Shift {
   __device__ __forceinline__ float fix(float m) const { return ex2(__fmaf_rn(-m, c, k)); }
 };
 
+// 2^((x - m) c) for two logits: in one FMA by Shift, whose few instructions a row
+// pay off over many vectors, or as a difference and a product (DIFF), which is
+// the faster one where a thread has a vector or two.
+template <bool DIFF>
+struct Terms {
+  pair_t c, k;
+  float undo = 1.0f;  // Shift's fix()
+  __device__ __forceinline__ Terms(float m, float c_) : c(pair(c_, c_)), k(pair(-m, -m)) {
+    if (DIFF) return;
+    const Shift by(m, c_);
+    c = pair(by.c, by.c);
+    k = pair(-by.k, -by.k);
+    undo = by.fix(m);
+  }
+  __device__ __forceinline__ pair_t operator()(pair_t x) const {
+    return ex2_2(DIFF ? mul2(add2(x, k), c) : fma2(x, c, k));
+  }
+};
+
 template <int DT>
 struct Elem;
 
