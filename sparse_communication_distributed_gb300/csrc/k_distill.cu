@@ -202,7 +202,7 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
     // maximum, as a maximum may be the type's lowest value and p still 1 / vocab
     const float A = has ? w * a.kd * a.tau : 0.0f, C1 = y >= 0 ? w * a.ce : 0.0f;
     const float ref = bucket ? Mr : Ms, over = bucket ? Sr : S;
-    const float C = (bucket ? A * ((Q + qr) * (Sr * ex2((Mr - Ms) * a.c) / S) - qr) : A * Q) / over;
+    const float C = has ? (bucket ? A * ((Q + qr) * (Sr * ex2((Mr - Ms) * a.c) / S) - qr) : A * Q) / over : 0.0f;
     const float C2 = C1 / S1;
     auto grad_of = [&](float x) {
       float r = C * ex2((x - ref) * a.c);
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
     bool label_listed = false;
     for (int i = tid; i < a.k; i += kThreads) {
       if (sidx[i] < 0) continue;
-      float r = A * ((Q + qr) * (ex2((sx[i] - Ms) * a.c) / S) - sq[i]);
+      float r = has ? A * ((Q + qr) * (ex2((sx[i] - Ms) * a.c) / S) - sq[i]) : 0.0f;
       if (y >= 0) {
         r += C2 * ex2((sx[i] - Ms) * kLog2e);
         if (sidx[i] == y) {
@@ -706,8 +706,8 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
           Row r;
           r.M = sh;
           r.m = shr;
-          r.rS = rcp(S);
-          r.rS1 = rcp(S1);
+          r.rS = has ? rcp(S) : 0.0f;  // (infinite where the mask leaves no word: not for a term that is not there)
+          r.rS1 = y >= 0 ? rcp(S1) : 0.0f;
           r.A = has ? w_now * a.kd * a.tau : 0.0f;
           r.C1 = y >= 0 ? w_now * a.ce : 0.0f;
           r.Qr = Q + qr;

@@ -232,6 +232,19 @@ def test_distill_does_not_depend_on_an_offset(V, offset, tail):
         check_distill(x, idx, vals, tl, y, tau, "f32", loss, grad, range(2))
 
 
+@pytest.mark.parametrize("V,dtype", [(300, "bf16"), (50257, "f32"), (900001, "bf16")])
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_masked_row_without_a_term_has_no_gradient(V, dtype, tail):
+    # no word is left, the teacher no entry above -inf, and there is no label: the loss is 0, and so is its gradient
+    x = torch.full((2, V), -INF, dtype=DT[dtype], device="cuda")
+    idx = torch.tensor([[-1] * 4, [3, -1, 299, 7]], dtype=torch.int32, device="cuda")
+    tl = torch.zeros(2, device="cuda") if tail else None
+    for tau in (1.0, 2.0, 1.7):
+        loss, grad = pkg.distill_loss_grad(x, idx, torch.full((2, 4), -INF, device="cuda"), teacher_lse=tl, temperature=tau, ce_weight=0.5,
+                                           labels=torch.tensor([-100, -1], device="cuda"))
+        assert loss.tolist() == [0.0, 0.0] and not f64(grad).any()
+
+
 # ---- routing ----------------------------------------------------------------------------------------
 
 
