@@ -8,7 +8,8 @@
 //                = p_j (sum q + q_rest) - q_rest exp(s_j - L_rest) j not listed
 // where L_rest = log sum exp(s) over the coordinates not listed.  L_rest is
 // summed over just those, not taken as a difference, so that a student which is
-// sure of the listed words keeps its exact small p_rest.  Every coordinate is
+// sure of the listed words keeps its exact small p_rest, in the loss and in the
+// gradient (rest_of).  Every coordinate is
 // written by the formula of the unlisted ones and the k listed ones (and the
 // label) are then set one by one from fp32 values, so each gradient is rounded
 // once.
@@ -43,6 +44,15 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kMaxK = 1024;
 constexpr int kFilter = 32768;  // bits: coordinates that may be listed, modulo this
+
+// What all coordinates not listed get together, in units of kd tau:
+// (Q + q_rest) p_rest - q_rest, which is Q - p_listed as well where Q + q_rest = 1.
+// Of the two differences the one of the smaller numbers keeps more of a small
+// result: a student and a teacher both sure of the listed words have p_rest and
+// q_rest near 0, both unsure Q and p_listed.
+__device__ __forceinline__ float rest_of(float Q, float q_rest, float p_listed, float p_rest) {
+  return q_rest > 0.0f && p_rest > 0.5f ? Q - p_listed : (Q + q_rest) * p_rest - q_rest;
+}
 
 struct DistillArgs {
   const void* x;
@@ -182,13 +192,15 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
     }
     const bool bucket = tail_mode && has && Sr > 0.0f;
     const float qr = bucket ? fmaxf(0.0f, 1.0f - Q) : 0.0f;
-    float kl = 0.0f;
+    float kl = 0.0f, top = 0.0f;
     for (int i = tid; i < a.k; i += kThreads) {
       const float q = sq[i];
+      if (bucket && sidx[i] >= 0) top += ex2((sx[i] - Ms) * a.c);
       if (q != 0.0f)
         kl += q * ((load_val(a.vals, a.vals_dtype, row * a.k + i) / a.tau - base - lz) - ((sx[i] - Ms) / a.tau - ls));
     }
     kl = cta_sum(kl, fbuf);
+    if (bucket) top = cta_sum(top, fbuf) / S;
     if (qr > 0.0f) kl += qr * (logf(qr) - ((Mr - Ms) / a.tau + logf(Sr) - ls));
     if (a.loss && tid == 0) {
       float l = has ? a.kd * a.tau * a.tau * kl : 0.0f;
@@ -202,7 +214,7 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
     // maximum, as a maximum may be the type's lowest value and p still 1 / vocab
     const float A = has ? w * a.kd * a.tau : 0.0f, C1 = y >= 0 ? w * a.ce : 0.0f;
     const float ref = bucket ? Mr : Ms, over = bucket ? Sr : S;
-    const float C = has ? (bucket ? A * ((Q + qr) * (Sr * ex2((Mr - Ms) * a.c) / S) - qr) : A * Q) / over : 0.0f;
+    const float C = has ? A * (bucket ? rest_of(Q, qr, top, Sr * ex2((Mr - Ms) * a.c) / S) : Q) / over : 0.0f;
     const float C2 = C1 / S1;
     auto grad_of = [&](float x) {
       float r = C * ex2((x - ref) * a.c);
@@ -717,10 +729,9 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
           r.K1 = r.A * Q * r.rS;
           r.K2 = r.C1 * r.rS1;
           if (BUCKET) {
-            // (Q + q_rest) p_rest - q_rest is Q - p_listed, as Q + q_rest = 1
             const float f = ex2((shr - sh) * a.c), f1 = ex2((shr - sh) * kLog2e);
             const float top = q.ts * ex2((q.tm - sh) * a.c) * r.rS;
-            r.K1 = q.s > 0.0f ? r.A * (qr > 0.0f ? (Q - top) / q.s : Q * f * r.rS) : 0.0f;
+            r.K1 = q.s > 0.0f ? r.A * rest_of(Q, qr, top, q.s * f * r.rS) / q.s : 0.0f;
             r.K2 = q.s1 > 0.0f ? r.C1 * f1 * r.rS1 : 0.0f;
           }
           if (!TWO) r.K1 += r.K2;

@@ -245,6 +245,51 @@ def test_distill_masked_row_without_a_term_has_no_gradient(V, dtype, tail):
         assert loss.tolist() == [0.0, 0.0] and not f64(grad).any()
 
 
+def bucket_gradient(V, sure):
+    """(gradient of the unlisted words, their softmax among themselves, log p_rest, q_rest, x, teacher_lse) of 64 rows
+    with 64 listed words, one of them with an entry above -inf (0, so that q = exp(-teacher_lse))."""
+    R, k = 64, 64
+    rng = np.random.default_rng(V)
+    h = rng.standard_normal((R, V)) * (1.0 if sure else 0.1)
+    at = np.arange(k) * (V // k) + 3
+    if sure:
+        h[:, at] = np.log(V / k) + rng.uniform(13.0, 15.0, (R, 1)) + rng.uniform(-3, 0, (R, k))
+        tl = -np.log1p(-np.linspace(1, 40, R) * 2.0 ** -24)
+    else:
+        tl = -np.log(k / V * np.exp(rng.uniform(-0.1, 0.1, R)))
+    tl = tl.astype(np.float32)
+    x = cuda(h)
+    vals = torch.full((R, k), -INF, device="cuda")
+    vals[:, 5] = 0.0
+    idx = torch.from_numpy(np.tile(at, (R, 1)).astype(np.int32)).cuda()
+    _, grad = pkg.distill_loss_grad(x, idx, vals, teacher_lse=cuda(tl))
+    rest = np.ones(V, bool)
+    rest[at] = False
+    h = f64(x)
+    for r in range(R):
+        L, Lr, Lt = ref.lse(h[r]), ref.lse(h[r, rest]), ref.lse(h[r, at])
+        yield f64(grad[r])[rest], np.exp(h[r, rest] - Lr), np.exp(Lr - L), np.exp(Lt - L), float(tl[r]), ref.lse_tol(V, L)
+
+
+@pytest.mark.parametrize("V", [300, 50257, 450001])
+def test_distill_bucket_gradient_of_a_sure_student(V):
+    # p_rest and q_rest near 1e-6: an unlisted word's gradient is (p_rest - q_rest) softmax_rest_j.  q is one expf near
+    # 1, within 2 units of 2^-24, and 1 - q exact; p_rest is a sum of its own, off by a few 1e-6 of itself
+    for g, soft, p_rest, _, tl, es in bucket_gradient(V, True):
+        tol = 2 * 2.0 ** -24 + p_rest * 4 * es
+        want = (p_rest + np.expm1(-tl)) * soft
+        assert (np.abs(g - want) <= soft * tol + np.abs(want) * 4 * es + 1e-38).all(), (np.abs(g - want) / soft).max() / tol
+
+
+@pytest.mark.parametrize("V", [2000, 50257, 450001])
+def test_distill_bucket_gradient_of_an_unsure_student(V):
+    # p_rest and q_rest near 1: the same is (q - p_listed) softmax_rest_j, each of the two off by a few 1e-6 of itself
+    for g, soft, _, p_listed, tl, es in bucket_gradient(V, False):
+        q = np.exp(-tl)
+        tol = (q * 8 * 2.0 ** -24 + p_listed * 4 * es) + np.abs(q - p_listed) * 4 * es
+        assert (np.abs(g - (q - p_listed) * soft) <= soft * tol + 1e-38).all(), tol
+
+
 # ---- routing ----------------------------------------------------------------------------------------
 
 
