@@ -107,6 +107,10 @@ __device__ __forceinline__ int count_above(const uint64_t* list, int n, uint64_t
   return above;
 }
 
+// The shift of a row's sum: as shift_of, and 0 for a maximum of +inf, whose term
+// and log-sum-exp are then +inf and not NaN.
+__device__ __forceinline__ float sum_shift(float m) { return fabsf(m) < INFINITY ? m : 0.0f; }
+
 // Order of floats as signed whole numbers, and back (its own inverse).
 __device__ __forceinline__ int as_ordered(float f) {
   const int i = __float_as_int(f);
@@ -279,7 +283,7 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
         m2 = fmaxf(m2, gmax[g]);
         low = fminf(low, gmax[g] > neg_inf() ? gmax[g] : INFINITY);
       }
-      s *= ex2((m - shift_of(m2)) * a.c);
+      s *= ex2((m - sum_shift(m2)) * a.c);
       m = m2;
       // the range of the groups' largest: finite ones
       int ihigh = __reduce_max_sync(kFull, as_ordered(fminf(m, 3.0e38f)));
@@ -338,7 +342,7 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
         }
       }
       const uint32_t bound2 = bound_of<DT>(bound);
-      const float sh = shift_of(m);
+      const float sh = sum_shift(m);
       const Shift by(sh, a.c);  // (this thread's own maximum, far below the row's where all it has is masked)
       const pair_t c2 = pair(by.c, by.c), mc = pair(-by.k, -by.k);
       pair_t sum = pair(0.0f, 0.0f);
@@ -406,7 +410,7 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
     float M = m;
 #pragma unroll
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-    float S = s * ex2((m - shift_of(M)) * a.c);
+    float S = s * ex2((m - sum_shift(M)) * a.c);
 #pragma unroll
     for (int o = 16; o; o >>= 1) S += __shfl_xor_sync(kFull, S, o);
     if (lane == 0) {
@@ -418,7 +422,7 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
       M = pm;
 #pragma unroll
       for (int o = 8; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-      S = ps * ex2((pm - shift_of(M)) * a.c);
+      S = ps * ex2((pm - sum_shift(M)) * a.c);
 #pragma unroll
       for (int o = 8; o; o >>= 1) S += __shfl_xor_sync(kFull, S, o);
     };
@@ -431,7 +435,7 @@ __global__ __launch_bounds__(SH::NT, SH::CTAS) void topk_rows(const TopkArgs a) 
       }
     };
     auto write_lse = [&]() {
-      if (a.lse && tid == 0) a.lse[row] = shift_of(M) / a.tau + logf(S);
+      if (a.lse && tid == 0) a.lse[row] = sum_shift(M) / a.tau + logf(S);
     };
     if (a.cluster == 1 && n <= kThreads) {  // by counting what is above each entry
       for (int i = n + tid; i < ((n + 3) & ~3); i += kThreads) list[i] = 0;

@@ -333,3 +333,22 @@ def test_route_with_finite_masks(T, E, k, dtype, renorm):
         wg, size = ref.route_grad(s, f64(idx).astype(int), c, rl, cu, dw.astype(np.float64), np.array([0.7, 0.0]), renorm)
         off = np.abs(grad - wg) - ((4 * rel + 16 * ref.U) * size + np.abs(wg) * ref.ROUND[dtype] + ref.TINY[dtype])
         assert off.max() <= 0, value
+
+
+# ---- infinite logits --------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("R,V", [(3, 300), (3, 5000), (3, 50257), (3, 140000), (700, 3000)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_topk_of_an_infinite_logit(R, V, dtype):
+    rng = np.random.default_rng(V)
+    h = rng.standard_normal((R, V)).astype(np.float32)
+    h[0, V // 3] = INF
+    h[1, [1, V - 1]] = INF
+    h[2, V // 2], h[2, V // 5] = INF, np.nan
+    x = cuda(h, dtype)
+    idx, vals, lse = pkg.topk_logits(x, 3, temperature=2.0)
+    for r in range(3):
+        assert np.array_equal(idx[r].cpu().numpy(), ref.topk(f64(x)[r], 3))
+    assert float(lse[0]) == INF and float(lse[1]) == INF and np.isnan(float(lse[2]))
+    assert np.isfinite(f64(lse)[3:]).all()
