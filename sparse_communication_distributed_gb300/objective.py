@@ -69,6 +69,14 @@ def _arg(x, name: str, dtypes, shape, device) -> int | None:
                      f"{x.stride()} on {x.device}")
 
 
+def _count(k: int) -> int:
+    """Checks that k is what a C int holds (ctypes would cut it down); returns
+    the entries of a row that results have."""
+    if not -2 ** 31 <= k < 2 ** 31:
+        raise ValueError(f"k={k} does not fit 32 bits")
+    return max(k, 0)
+
+
 def _check(rc: int) -> None:
     if rc != SCAPE_OK:
         raise ScapeError(rc, _lib.scape_last_error(None).decode())
@@ -84,7 +92,7 @@ def topk_logits(logits, k: int, temperature: float = 1.0, stream=None):
             return topk_logits(logits, k, temperature)
     stride = _rows(logits)
     rows, vocab = logits.shape
-    dev, n = logits.device, max(k, 0)
+    dev, n = logits.device, _count(k)
     code = _code(logits, "logits")
     idx = torch.empty((rows, n), dtype=torch.int32, device=dev)
     vals = torch.empty((rows, n), dtype=logits.dtype, device=dev)
@@ -182,9 +190,10 @@ def route(logits, k: int, *, renormalize: bool = True, cu_tokens=None, valid=Non
     if stream is not None:
         with _stream_context(stream):
             return route(logits, k, renormalize=renormalize, cu_tokens=cu_tokens, valid=valid)
+    n = _count(k)
     args = _route_args(logits, k, renormalize, cu_tokens, valid)
     tokens, experts = logits.shape
-    n, groups, dev = max(k, 0), args.n_groups, logits.device
+    groups, dev = args.n_groups, logits.device
     need = ctypes.c_uint64()
     ref = ctypes.byref(args)
     _check(_lib.scape_route_workspace(ref, ctypes.byref(need)))

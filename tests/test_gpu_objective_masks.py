@@ -352,3 +352,12 @@ def test_topk_of_an_infinite_logit(R, V, dtype):
         assert np.array_equal(idx[r].cpu().numpy(), ref.topk(f64(x)[r], 3))
     assert float(lse[0]) == INF and float(lse[1]) == INF and np.isnan(float(lse[2]))
     assert np.isfinite(f64(lse)[3:]).all()
+
+
+def test_k_beyond_32_bits_is_refused():
+    x = torch.zeros(1, 100, device="cuda")
+    for k in (2 ** 32 + 3, -2 ** 32 + 3):
+        with pytest.raises(ValueError):
+            pkg.topk_logits(x, k)
+        with pytest.raises(ValueError):
+            pkg.route(x, k)
