@@ -290,6 +290,26 @@ def test_distill_bucket_gradient_of_an_unsure_student(V):
         assert (np.abs(g - (q - p_listed) * soft) <= soft * tol + 1e-38).all(), tol
 
 
+@pytest.mark.parametrize("R,V,k", [(700, 1003, 700), (400, 50257, 1000), (120, 131075, 400)])
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_many_entries_over_many_rows(R, V, k, tail):
+    # more entries than threads, and several rows for each CTA or cluster, some of weight 0
+    rng = np.random.default_rng(V)
+    x = cuda(rng.standard_normal((R, V)).astype(np.float32) * 3, "bf16")
+    z = f64(x) * 0.9 + rng.standard_normal((R, V))
+    idx = np.argpartition(-z, k, axis=1)[:, :k].astype(np.int32)
+    vals = cuda(np.take_along_axis(z, idx, 1))
+    tl = np.array([ref.lse(r / 1.7) for r in z], np.float32) if tail else None
+    y = rng.integers(V, size=R)
+    w = np.where(rng.random(R) < 0.2, 0.0, 1.0).astype(np.float32)
+    loss, grad = pkg.distill_loss_grad(x, torch.from_numpy(idx).cuda(), vals, teacher_lse=None if tl is None else cuda(tl),
+                                       labels=torch.from_numpy(y).cuda(), row_weight=cuda(w), temperature=1.7, kd_weight=0.7, ce_weight=0.4)
+    off = torch.from_numpy(w == 0).cuda()
+    assert not grad[off].any() and not loss[off].any()
+    some = [r for r in np.unique(np.concatenate([rng.integers(R, size=12), [0, R - 1]])) if w[r]]
+    check_distill(x, idx, vals, tl, y, 1.7, "bf16", loss, grad, some)
+
+
 # ---- routing ----------------------------------------------------------------------------------------
 
 
