@@ -742,10 +742,14 @@ int lanes_of(int experts) {
   return experts <= 256 ? L : experts <= 512 ? 16 : 32;
 }
 
-// Tokens of a chunk: two CTAs for each SM, in whole rounds of a CTA's warps.
+// Tokens of a chunk, in whole rounds of a CTA's warps: at most kChunks of them, two
+// CTAs for each of a GB300's 152 SMs.  A constant, as the workspace's size is asked
+// for without a device and the order of the sums follows the chunks.
+constexpr uint64_t kChunks = 304;
+
 uint64_t chunk_of(const scape_route_args* q) {
   const uint64_t round = (uint64_t)kWarps * 32 / lanes_of(q->experts);
-  const uint64_t n = (q->tokens + 303) / 304;
+  const uint64_t n = (q->tokens + kChunks - 1) / kChunks;
   return n == 0 ? round : (n + round - 1) / round * round;
 }
 

@@ -274,10 +274,6 @@ struct RowView {
     return (n + shift + E::kPerVec - 1) / E::kPerVec;
   }
   __device__ __forceinline__ int64_t first_of(int64_t v) const { return v * E::kPerVec - shift; }
-  __device__ __forceinline__ bool whole(int64_t v) const {
-    const int64_t e = first_of(v);
-    return e >= 0 && e + E::kPerVec <= n;
-  }
   __device__ __forceinline__ uint4 load(int64_t v) const {
     const int64_t e = first_of(v);
     if (e >= 0 && e + E::kPerVec <= n) return ld_row_u4(p + e);
