@@ -116,13 +116,13 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
     float tm = neg_inf();
     for (int i = tid; i < a.k; i += kThreads) {
       int32_t e = a.idx[row * a.k + i];
-      float t = neg_inf();
+      float v = neg_inf();
       if (e >= a.V) {
         if (a.bad) atomicAdd(a.bad, 1u);
         e = -1;
       }
       if (e >= 0) {
-        t = load_val(a.vals, a.vals_dtype, row * a.k + i) / a.tau;
+        v = load_val(a.vals, a.vals_dtype, row * a.k + i);
         sx[i] = E::load(view.p + e);
         atomicOr(&filter[e % kFilter / 32], 1u << (e & 31));
       } else {
@@ -130,8 +130,8 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
         sx[i] = 0.0f;
       }
       sidx[i] = e;
-      sq[i] = t;
-      if (!(t <= tm)) tm = t;  // NaN stays
+      sq[i] = v;
+      if (!(v <= tm)) tm = v;  // NaN stays
     }
     int64_t y = a.labels ? a.labels[row] : -1;
     if (y >= a.V) {
@@ -141,20 +141,21 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
     const float xy = y >= 0 ? E::load(view.p + y) : 0.0f;
     const bool tail_mode = a.tlse != nullptr;
     bool has = __syncthreads_or(tm != neg_inf());
-    float base = 0.0f, lz = 0.0f;  // log q = (t - base) - lz
+    // log q = (v - base) / tau - lz (v / tau alone may be beyond fp32)
+    float base = 0.0f, lz = 0.0f;
     if (has) {
       if (tail_mode) {
-        base = a.tlse[row];
+        lz = a.tlse[row];
       } else {
         base = shift_of(cta_max(tm, fbuf));
         float z = 0.0f;
-        for (int i = tid; i < a.k; i += kThreads) z += expf(sq[i] - base);
+        for (int i = tid; i < a.k; i += kThreads) z += expf((sq[i] - base) / a.tau);
         lz = logf(cta_sum(z, fbuf));
       }
     }
     float qs = 0.0f;
     for (int i = tid; i < a.k; i += kThreads) {
-      const float logq = sq[i] - base - lz, q = has && sidx[i] >= 0 ? expf(logq) : 0.0f;
+      const float logq = (sq[i] - base) / a.tau - lz, q = has && sidx[i] >= 0 ? expf(logq) : 0.0f;
       sq[i] = q;
       qs += q;
     }
@@ -197,7 +198,7 @@ __global__ __launch_bounds__(kThreads) void distill_rows(const DistillArgs a) {
       const float q = sq[i];
       if (bucket && sidx[i] >= 0) top += ex2((sx[i] - Ms) * a.c);
       if (q != 0.0f)
-        kl += q * ((load_val(a.vals, a.vals_dtype, row * a.k + i) / a.tau - base - lz) - ((sx[i] - Ms) / a.tau - ls));
+        kl += q * (((load_val(a.vals, a.vals_dtype, row * a.k + i) - base) / a.tau - lz) - ((sx[i] - Ms) / a.tau - ls));
     }
     kl = cta_sum(kl, fbuf);
     if (bucket) top = cta_sum(top, fbuf) / S;
@@ -278,11 +279,11 @@ static_assert(Deep::MAXK >= kMaxK, "every entry has a thread");
 struct Part {
   float m, s, s1;     // coordinates held in registers (with a bucket: those not listed)
   float tm, ts, ts1;  // listed coordinates (the sums with a bucket only)
-  float b;            // over the listed coordinates of this part: sum u_i (t_i - base - (x_i - tm) / tau),
-                      // u_i = exp(t_i - base): no term holds a maximum, which may be the type's lowest value
+  float b;            // over the listed coordinates of this part: sum u_i (log u_i - (x_i - tm) / tau): no
+                      // term holds a maximum, which may be the type's lowest value
   float zp;           // sum u_i over those
-  float base, z;      // over all listed coordinates: base = max t_i (u_i then is relative to
-                      // teacher_lse with a bucket), z = sum u_i
+  float base, z;      // over all listed coordinates: base = max vals_i and z = sum u_i, where log u_i =
+                      // (vals_i - base) / tau, or vals_i / tau - teacher_lse with a bucket
 };
 constexpr int kShared = 8;  // the leading members differ from part to part
 
@@ -311,7 +312,7 @@ enum { kOne, kTwo, kSquare };
 struct __align__(16) Row {
   float m, K1, K2, rS;         // gradient = K1 2^((x - m) c) + K2 2^((x - m) log2 e) at unlisted, by Terms
   float M, A, C1, rS1;         // p = 2^((x - M) c) rS; softmax(x) = 2^((x - M) log2 e) rS1
-  float Qr, base, rz, unused;  // sum q + q_rest; q_i = exp(t_i - base) rz
+  float Qr, base, rz, unused;  // sum q + q_rest; q_i = exp(log_u(vals_i, base)) rz
 };
 
 // What a row's loss is worked out from.
@@ -428,7 +429,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     if (BUCKET) raw_lse = a.tlse[row];
   };
   // the teacher's entries of this thread: local coordinate (-1: not of this
-  // part), t, x; the label and, for one thread, x there
+  // part), vals, x; the label and, for one thread, x there
   int el[ENT], y = -1;
   float et[ENT], ex[ENT], xy = 0.0f, tlse = 0.0f;
   auto take_side = [&](const Where& w) {
@@ -441,7 +442,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
       if (e >= V) {
         if (a.bad && rank == 0) atomicAdd(a.bad, 1u);
       } else if (e >= 0) {
-        et[h] = raw_v[h] * inv_tau;
+        et[h] = raw_v[h];
         const int l = e - w.e0;  // e < 2^20, e0 > -8
         if (l >= 0 && l < w.here * EPV) {
           el[h] = l;
@@ -456,6 +457,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
     if (y >= 0 && tid == 0) xy = E::load(w.p + (y - w.e0));
     tlse = raw_lse;
   };
+  auto log_u = [&](float v, float base) { return BUCKET ? v * inv_tau - base : (v - base) * inv_tau; };
   auto row_at = [&](int64_t row) { return static_cast<const T*>(a.x) + row * a.stride; };
   // writes vector i of a part of a gradient's row that starts at g
   auto put = [&](T* g, const Where& w, bool same, int i, const uint4 v) {
@@ -495,7 +497,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
       const Loss p = pend[lane];
       const float ls = logf(p.S);
       float l = 0.0f;
-      if (p.has) {  // sum q_i (t_i - log z - base - (x_i - M) / tau) + log S sum q_i
+      if (p.has) {  // sum q_i (log u_i - log z - (x_i - M) / tau) + log S sum q_i
         float kl = BUCKET ? p.b + p.Q * ls : p.b / p.z + (ls - logf(p.z));
         if (p.qr > 0.0f) {  // log q_rest - log p_rest, both from what is listed
           const float odds = p.top / p.s;
@@ -629,11 +631,11 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
       const float tsh = shift_of(q.tm);
 #pragma unroll
       for (int h = 0; h < ENT; h++) {
-        const float u = expf(et[h] - base);
+        const float lu = log_u(et[h], base), u = expf(lu);
         q.z += u;
         if (el[h] >= 0) {
           q.zp += u;
-          if (u != 0.0f) q.b += u * ((et[h] - base) - (ex[h] - tsh) * inv_tau);
+          if (u != 0.0f) q.b += u * (lu - (ex[h] - tsh) * inv_tau);
           if (BUCKET) {
             q.ts += ex2((ex[h] - tsh) * a.c);
             if (TWO) q.ts1 += ex2((ex[h] - tsh) * kLog2e);
@@ -676,7 +678,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
       if (lane >= kWarps) q = Part{neg_inf(), 0.0f, 0.0f, neg_inf(), 0.0f, 0.0f, 0.0f, 0.0f, neg_inf(), 0.0f};
       const float base = shfl_max(q.base, kMerge);
       if (!BUCKET) {  // relative to the CTA's base
-        const float bd = shift_of(q.base) - shift_of(base), f = expf(bd);
+        const float bd = (shift_of(q.base) - shift_of(base)) * inv_tau, f = expf(bd);
         // (f = 0: a warp of entries at the type's lowest value, whose q are 0 whatever its b)
         q.b = f == 0.0f || q.z == 0.0f ? 0.0f : f * (q.b + bd * q.zp);
         q.z = q.z == 0.0f ? 0.0f : f * q.z;
@@ -705,7 +707,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
         merge(kMaxCluster);
       }
       if (lane == 0) {
-        // the teacher: q_i = exp(t_i - base) / rz, Q = sum q_i
+        // the teacher: q_i = u_i / z (u_i with a bucket), Q = sum q_i
         const bool has = base != neg_inf() || z != z;
         const float Q = BUCKET ? z : has ? 1.0f : 0.0f;
         // the whole row: all = rest and listed
@@ -787,7 +789,7 @@ __global__ __launch_bounds__(SH::NT, SH::MINB) void distill_parts(const DistillA
       for (int h = 0; h < ENT; h++) {
         if (el[h] < 0) continue;
         const float d = ex[h] - t.M;
-        float v = t.A * (t.Qr * ex2(d * a.c) * t.rS - expf(et[h] - t.base) * t.rz);
+        float v = t.A * (t.Qr * ex2(d * a.c) * t.rS - expf(log_u(et[h], t.base)) * t.rz);
         v += t.C1 * ex2(d * kLog2e) * t.rS1;
         if (y_here && el[h] == ly) v -= t.C1;
         g[el[h]] = E::make(v);

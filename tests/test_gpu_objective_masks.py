@@ -144,6 +144,22 @@ def test_distill_with_teacher_entries_at_the_lowest_value(V, k, tau, dtype, tail
     check_distill(xt, idx, vals, tl, y, tau, dtype, loss, grad, range(R))
 
 
+@pytest.mark.parametrize("V,k,tau", [(300, 40, 0.7), (50257, 200, 0.9), (140001, 400, 0.8), (900001, 64, 0.7)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("value", ["lowest", 2.0 ** 20])
+def test_distill_with_teacher_entries_far_from_zero(V, k, tau, dtype, value):
+    # entries that all hold the type's lowest value are equal (their quotient by a temperature below 1 is beyond fp32);
+    # entries at 2^20 and a few eighths are those few eighths
+    rng = np.random.default_rng(V)
+    R = 2
+    xt = cuda(rng.standard_normal((R, V)).astype(np.float32) * 3, dtype)
+    idx = np.stack([rng.permutation(V)[:k] for _ in range(R)]).astype(np.int32)
+    near = np.zeros((R, k)) if value == "lowest" else np.round(rng.standard_normal((R, k)) * 16) / 8
+    vals = cuda(np.full((R, k), LOWEST[dtype]), dtype) if value == "lowest" else cuda(near + value)
+    loss, grad = pkg.distill_loss_grad(xt, torch.from_numpy(idx).cuda(), vals, temperature=tau, kd_weight=0.7)
+    check_distill(xt, idx, cuda(near), None, np.full(R, -1), tau, dtype, loss, grad, range(R))
+
+
 def case_of(rng, x, keep, k, tau, tail):
     """k words of each row that are not masked (any words where all are) for a teacher, and a label among them or not."""
     R, V = x.shape
