@@ -357,10 +357,11 @@ int scape_step_noalloc(const scape_step_buffers* buffers, const void* const* gra
                        void* stream);
 
 /* ---- Training objective ------------------------------------------------------
- * What the gradients of scape_step come from, where the trained model is a
- * student of a larger one or a mixture of experts: the top logits that a
- * teacher leaves behind, the loss of a student against them with its gradient,
- * and an expert router with its balance loss and gradients.  All calls are
+ * Where the trained model is a student of a larger one or a mixture of experts:
+ * the top logits that a teacher leaves behind, the loss of a student against them
+ * with its gradient, and an expert router with its balance loss and gradients.
+ * The gradients are those of the logits; the model's own backward pass leads from
+ * them to the parameters' gradients, which scape_step takes.  All calls are
  * stateless: pointers are DEVICE pointers owned by the caller unless said
  * otherwise, nothing is allocated, the work is enqueued on "stream" and the
  * call returns.  Argument errors give SCAPE_EINVAL and launch errors
@@ -370,8 +371,10 @@ int scape_step_noalloc(const scape_step_buffers* buffers, const void* const* gra
  *
  * Logits are rows of bf16, fp16 or fp32 elements, each row contiguous, rows
  * row_stride elements apart (row_stride >= the row's length; any alignment of
- * the element's own size).  -inf marks an element that is out of the running.
- * Arithmetic is fp32: softmax statistics, sums and losses are held in fp32,
+ * the element's own size).  -inf marks an element that is out of the running; a
+ * large finite number in its place, down to the type's lowest value, is a logit
+ * like others, whose probability is 0 beside larger ones and 1 / n in a row of n
+ * such.  Arithmetic is fp32: softmax statistics, sums and losses are held in fp32,
  * gradients are rounded once to the logits' type. */
 enum { SCAPE_BF16 = 0, SCAPE_F16 = 1, SCAPE_F32 = 2 };
 
@@ -379,6 +382,8 @@ enum { SCAPE_BF16 = 0, SCAPE_F16 = 1, SCAPE_F32 = 2 };
  * ascending index (+0 and -0 are equal; NaN ranks above +inf), and the row's
  * log-sum-exp at a temperature:
  *   idx[r][i], vals[r][i] (logits' type, unchanged), lse[r] = log sum_j exp(x[r][j] / temperature)
+ * (+inf for a row with +inf, NaN for one with NaN, -inf for one of -inf or where
+ * the value is below fp32's range).
  * idx and vals are rows x k, contiguous; vals and lse may be NULL.
  * 1 <= k <= min(vocab, 1024); 1 <= vocab < 2^31; rows = 0 is a no-op. */
 int scape_topk_logits(const void* logits, int dtype, uint64_t rows, uint64_t vocab,

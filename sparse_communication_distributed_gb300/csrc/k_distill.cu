@@ -20,13 +20,18 @@
 // gradient (distill_rows).
 //
 // The bound is HBM where a row is short enough for three CTAs an SM: 8192 x 32000
-// bf16 with the gradient take 186 us, 5.6 TB/s, 83 % of the copy bandwidth (DRAM
+// bf16 with the gradient take 187 us, 5.6 TB/s, 83 % of the copy bandwidth (DRAM
 // busy 64 % and issue active 59 % on 4096 rows, which fit the caches in part).
-// Rows of 50257 take two CTAs of 105 KB: 311 us for 8192 with bucket and labels
-// (78 %), 84 us for the loss alone of 4096 (72 %), where the exponentials at two
-// temperatures and the chain of phases leave the memory idle in between.  Rows of
+// Rows of 50257 take two CTAs of 105 KB: 313 us for 8192 with bucket and labels
+// (78 %), 84 us for the loss alone of 4096 (72 %).  There neither limit is reached
+// (issue 58 %, DRAM 56 %, 29 % of the warps; the instructions alone are 45 us): 20
+// warps an SM do not cover the chain of copy, maximum, sums and merge.  Rows of
 // 131072 fp32 words take eight CTAs, whose exchange costs a cluster barrier a row:
-// 156 us for 768 (76 %).
+// 156 us for 768 (76 %).  Rows of a vector or two a thread are bound by that chain
+// too (16384 x 1003 bf16 80 us, barriers first among the stalls); Narrow's 64
+// registers spill 168 to 192 bytes a thread, outside the loops over vectors.
+// Rows that do not fit the chip are read twice and written an element at a time:
+// 64 x 1000003 bf16 take 1.03 ms, 4 % of the copy bandwidth.
 #include <algorithm>
 #include <atomic>
 #include <cmath>

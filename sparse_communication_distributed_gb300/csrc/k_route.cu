@@ -23,13 +23,17 @@
 // renormalised, else p_j (dw_j [chosen] - sum w dw).
 //
 // Instructions are the bound, not bytes.  Forward, 131072 x 256 fp32 with k 8: 60
-// us in all, 35 % of the copy bandwidth.  A token of 256 experts costs 240 warp
-// instructions (three quarters for the bound, list, ranks and output of the four
-// tokens of a warp, whatever their width), and 16 warps an SM, as the logits, the
-// sums over the tokens and the next token's logits fill 128 registers, issue half
-// of the time.  Backward, 65536 x 128 bf16 with k 8 and 32 groups: 16 us, hardly
-// more than the call costs the host; 524288 tokens 80 us, 56 % of the copy
-// bandwidth.
+// us in all, 35 % of the copy bandwidth, bf16 60 us (18 %).  A token of 256 experts
+// costs 235 warp instructions (three quarters for the bound, list, ranks and output
+// of the four tokens of a warp, whatever their width), and 16 warps an SM, as the
+// logits, the sums over the tokens and the next token's logits fill 128 registers,
+// issue half of the time.  They do not all fit: above 128 experts the forward spills
+// up to 8 bytes a thread in fp32 and 76 to 108 in 16 bits, the backward 8 to 180 in 16 bits
+// and 124 to 392 in fp32.  A ragged batch of 16384 x 64 is bound by latency: 15.5 us
+// in a graph, two rounds of tokens and a second kernel's chain of sums.  Backward,
+// 65536 x 128 bf16 with k 8 and 32 groups: 16 us, hardly more than the call costs the
+// host; 524288 tokens 82 us, 55 % of the copy bandwidth; 65536 x 256 bf16 23 us, fp32
+// 41 us (49 %).
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -560,7 +564,7 @@ __global__ __launch_bounds__(kThreads, 2) void route_grad(const RouteArgs a) {
   using T = typename E::T;
   constexpr int L = LN::L, VPL = LN::VPL, ROWS = LN::ROWS, N = E::kPerVec;
   // choices of a lane at most (k <= 32, and k <= experts); loops over them end at k
-  // (524288 x 128 bf16, k 8: 89 -> 80 us)
+  // (524288 x 128 bf16, k 8: 82 us, 91 without)
   constexpr int KPL = 32 / L < 8 ? 32 / L : 8;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int sub = lane & (L - 1), slot = lane / L;

@@ -3,8 +3,8 @@
 //
 // Candidates are ranked by the unique composite key << 32 | ~index (order_key
 // of objective.cuh), so that equal logits go to the lower index.  A CTA takes a
-// row in tiles of up to 62 KB of shared memory; each thread works on vectors
-// that it copied itself.  One pass over a tile keeps, for each of G groups of
+// row in tiles of up to 64 KB of shared memory (97 KB in the shape for long rows);
+// each thread works on vectors that it copied itself.  One pass over a tile keeps, for each of G groups of
 // elements (a group is one place or a few of the vectors that a thread sees),
 // the group's largest element so far.  At least k elements reach the k-th
 // largest of these G, so nothing below it is among the row's k best; a histogram
@@ -12,7 +12,8 @@
 // vectors that reach the bound -- for logits in no special order k (1 + k / 2G) of
 // a first tile, a t-th part of that of the t-th tile -- and sums the exponentials.
 // In the end the elements of the vectors noted that reach the last bound are
-// listed and sorted.  Where too much reaches the bound (many equal logits, few
+// listed, and ranked by counting what is above each; a list longer than the CTA
+// has threads, or a part of a row, is sorted.  Where too much reaches the bound (many equal logits, few
 // above -inf, adverse orders), the tile is read again and its own k-th best
 // composite is found bit by bit.
 //
@@ -21,10 +22,13 @@
 //
 // Each logit is read once from HBM, which alone would take 61 us for 4096 x
 // 50257 bf16; the kernel takes 116 us there (k 64, 52 % of the copy bandwidth) and
-// 162 us for 1024 x 131072 fp32 (k 256, 49 %).  Issue is active 55 % of the time
-// and DRAM busy 38 %: a row costs 20 thousand warp instructions, half of them in
-// the two passes, and its phases (maxima, histogram, sums, ranking) wait for one
-// another, which the other CTAs of the SM fill only in part.
+// 163 us for 1024 x 131072 fp32 (k 256, 49 %).  Issue is active 58 % of the time
+// and DRAM busy 39 % (2048 rows): a row costs 21 thousand warp instructions, 74 us
+// for 4096 rows at the full issue rate, so the instructions bound it before the
+// bytes.  Half of them are in the two passes, the others in the phases of a tile and
+// the ranking, which compares each entry of the list with each other; the phases
+// (maxima, histogram, sums, ranking) wait for one another, which the other CTAs of
+// the SM fill only in part.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -40,7 +44,7 @@ namespace scape {
 namespace {
 
 // Threads of a CTA and CTAs of an SM: for rows of up to four tiles, for longer
-// ones (1024 x 131072 fp32, k 256: 162 us against 180 with nine smaller tiles; at
+// ones (1024 x 131072 fp32, k 256: 163 us against 180 with nine smaller tiles; at
 // three, 4000 x 32000 fp32, 144 against 130), and for short ones.
 template <int NT_, int CTAS_>
 struct Shape {

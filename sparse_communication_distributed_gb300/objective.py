@@ -8,6 +8,10 @@ runs on (``stream``: None for the current one, a torch stream or a raw handle),
 unless ``grad`` says where the gradient goes.  Inputs are borrowed until the
 work enqueued on that stream has finished.  A wrong type, shape or device
 raises ``ValueError``; an error of the library raises ``ScapeError``.
+
+The calls build no autograd graph: results of inputs that require a gradient
+do not.  ``distill_loss_grad`` and ``route_backward`` are the gradients, and
+``examples/distill_moe.py`` wraps them in two ``torch.autograd.Function``s.
 """
 from __future__ import annotations
 
