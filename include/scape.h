@@ -221,7 +221,7 @@ int scape_read_sparse(scape_handle* h, int w, uint32_t* idx, float* vals, uint64
  * on the handle.  h == NULL gives the message of the last failure, on this
  * thread, of a call that has no handle: scape_create, scape_create_ex,
  * scape_unpack, scape_dense_adams_step, scape_step_noalloc and the calls of
- * the training objective. */
+ * the training objective, of the experts' rows and of the gradients' norms. */
 const char* scape_last_error(const scape_handle* h);
 
 /* enable != 0: every later step records CUDA events around each kernel phase
@@ -485,6 +485,99 @@ int scape_route(const scape_route_args* args, int32_t* idx, float* weights, int3
 int scape_route_backward(const scape_route_args* args, const int32_t* idx, const int32_t* counts,
                          const int32_t* live, const float* d_weights, const float* d_losses,
                          void* grad, uint64_t grad_stride, void* stream);
+
+/* ---- Experts' rows -------------------------------------------------------------
+ * What lies between scape_route and the experts' matrix products: the tokens'
+ * rows sorted by expert, and the experts' rows summed back.  A choice is one
+ * (token, j) of the router's idx (tokens x k); the plan gives every choice a row
+ * (its slot) so that an expert's rows follow one another in ascending order of
+ * their choices.  Conventions as for the training objective: stateless, nothing
+ * allocated, the same inputs give the same bits.  Rows are bf16, fp16 or fp32 of
+ * any length; those of 16-byte multiples at 16-byte addresses move fastest. */
+
+/* Rows that a plan has room for, tokens * k + min(experts, tokens * k) * (align - 1)
+ * (< 2^31), and the bytes of device workspace that scape_expert_plan needs (may be
+ * 0).  Host call.  1 <= experts <= 1024, 1 <= k <= 32, 1 <= align <= 65536. */
+int scape_expert_plan_sizes(uint64_t tokens, int k, int experts, int align, uint64_t* capacity,
+                            uint64_t* workspace_bytes);
+
+/* idx: tokens x k experts; a negative one is no choice, one >= experts neither and
+ * is counted into *bad_count (a counter added to, may be NULL).  The same expert
+ * twice in a token gets two rows.
+ *   offsets (experts + 1)  expert e has the rows [offsets[e], offsets[e+1]), its
+ *                          choices first, filled up to a multiple of align
+ *   slots (tokens x k)     the row of every choice, -1 for none
+ *   source (capacity)      the choice (token * k + j) of every row, -1 for a row
+ *                          that fills up a segment or lies behind the last one
+ * The workspace (16-byte aligned) needs no initial value. */
+int scape_expert_plan(const int32_t* idx, uint64_t tokens, int k, int experts, int align,
+                      int32_t* offsets, int32_t* slots, int32_t* source, uint32_t* bad_count,
+                      void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* out[slots[t][j]] = x[t] for every choice, and 0 in every row without one
+ * (source < 0).  x: tokens x dim, row_stride elements apart; out: rows x dim,
+ * contiguous, not overlapping x (rows: the plan's capacity).  A token without a
+ * choice is not read.  Its gradient is scape_expert_combine of the rows' gradient
+ * without weights.  Here and below a slot outside [0, rows) is no choice. */
+int scape_expert_dispatch(const void* x, int dtype, uint64_t tokens, uint64_t dim,
+                          uint64_t row_stride, int k, const int32_t* slots, const int32_t* source,
+                          uint64_t rows, void* out, void* stream);
+
+/* out[t] = sum over j of weights[t][j] * y[slots[t][j]], in this order in fp32,
+ * rounded once; 0 for a token without a choice.  weights: tokens x k, or NULL
+ * (all 1).  y: rows x dim and out: tokens x dim, contiguous, not overlapping. */
+int scape_expert_combine(const void* y, int dtype, uint64_t rows, uint64_t dim,
+                         const int32_t* slots, const float* weights, uint64_t tokens, int k,
+                         void* out, void* stream);
+
+/* The gradients of scape_expert_combine with weights:
+ *   d_y[slots[t][j]] = weights[t][j] * d_out[t], 0 in rows without a choice
+ *   d_weights[t][j]  = <d_out[t], y[slots[t][j]]>, 0 for no choice (may be NULL)
+ * d_out: tokens x dim; y and d_y: rows x dim; all contiguous, d_y overlapping
+ * neither of the others. */
+int scape_expert_combine_backward(const void* d_out, const void* y, int dtype, uint64_t rows,
+                                  uint64_t dim, const int32_t* slots, const int32_t* source,
+                                  const float* weights, uint64_t tokens, int k, void* d_y,
+                                  float* d_weights, void* stream);
+
+/* ---- Gradients' norms ----------------------------------------------------------
+ * What lies between the backward pass and scape_step: the norm of each worker's
+ * gradients over all of its tensors, and the gradients scaled so that it is at most
+ * max_norm, in place or into the bf16 buffers that the step takes.
+ *   norm_g = sqrt(sum of x^2 over the tensors of group g)
+ *   out    = x * (norm_g > max_norm ? max_norm / norm_g : 1)
+ * Squares are added up in fp32 over 64 elements and in 64 bits from there on, and
+ * whatever would leave fp32's range in 64 bits from the start; each product is
+ * formed in fp32 and rounded to the result's type.  A group whose norm is infinite or NaN is not scaled (the caller
+ * sees the norm); so is one of norm 0.  The same inputs give the same bits. */
+typedef struct {
+  const void* const* grads; /* HOST array of n_tensors DEVICE pointers, each to numel[i] contiguous
+                               elements at any multiple of the element's size */
+  const uint64_t* numel;    /* HOST, each < 2^40; 0 is fine */
+  const uint8_t* dtypes;    /* HOST: SCAPE_BF16, SCAPE_F16 or SCAPE_F32 of every tensor */
+  uint32_t n_tensors;       /* < 2^20 */
+  uint32_t n_groups;        /* workers, 1 to 64 */
+  const uint64_t* first_tensor; /* HOST, n_groups + 1 ascending: group g has the tensors
+                                   [first_tensor[g], first_tensor[g+1]); NULL: one group */
+} scape_grads;
+
+/* Bytes of device workspace for these sizes (host call; numel, n_tensors and the
+ * groups matter). */
+int scape_grad_workspace(const scape_grads* grads, uint64_t* bytes);
+
+/* norms: DEVICE, n_groups.  The workspace (16-byte aligned) needs no initial value
+ * and may be used again by later work of the same stream.  Here a tensor may be
+ * listed twice or overlap another one. */
+int scape_grad_norm(const scape_grads* grads, float* norms, void* workspace,
+                    uint64_t workspace_bytes, void* stream);
+
+/* The same norms (those before clipping), and the scaled gradients.  out: HOST array
+ * of n_tensors DEVICE pointers and out_dtypes their types, or NULL for in place.  A
+ * result may be its own tensor (same address and type) and overlaps no other tensor
+ * or result.  max_norm > 0 (inf: never scaled). */
+int scape_clip_grads(const scape_grads* grads, float max_norm, void* const* out,
+                     const uint8_t* out_dtypes, float* norms, void* workspace,
+                     uint64_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,631 @@
+// Tokens sorted by expert and back (scape_expert_plan, _dispatch, _combine,
+// _combine_backward).
+//
+// The plan is a stable counting sort of the tokens x k choices: place_counts counts
+// the experts of every chunk of choices, place_scan turns the counts into each
+// chunk's first place in every expert's segment, place_choices ranks the choices
+// inside a chunk (a warp's 32 at a time, equal experts found with match.any) and
+// writes both directions of the permutation.  Up to one chunk of choices all of it
+// is one kernel of one CTA.
+//
+// Rows move in 16-byte vectors where their length and addresses allow, else in
+// units of 4 or 2 bytes.  A token's row is read once and stored to its k places
+// (dispatch), or its k rows are summed in registers (combine): HBM sees each row
+// once.
+#include <algorithm>
+#include <cstdarg>
+#include <cstdio>
+
+#include "objective.cuh"
+#include "scape_kernels.cuh"
+
+#define SCAPE_API extern "C" __attribute__((visibility("default")))
+
+namespace scape {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kRounds = 8;                          // choices of a thread
+constexpr int kChunk = kThreads * kRounds;          // choices of a CTA
+constexpr int kMaxExperts = 1024, kMaxChoices = 32;
+
+struct PlanArgs {
+  const int32_t* idx;
+  int64_t n;  // choices
+  int E;
+  int align;
+  int64_t chunks, capacity;
+  int32_t* offsets;
+  int32_t* slots;
+  int32_t* source;
+  uint32_t* bad;
+  int32_t* counts;  // chunks x E: choices; after place_scan their exclusive sums over the chunks
+  int32_t* totals;  // E
+};
+
+// The expert of a choice, -1 for none.
+__device__ __forceinline__ int expert_of(const PlanArgs& a, int64_t i) {
+  if (i >= a.n) return -1;
+  const int e = a.idx[i];
+  return e < a.E ? e : -1;
+}
+
+__global__ __launch_bounds__(kThreads) void place_counts(const PlanArgs a) {
+  __shared__ int32_t h[kMaxExperts];
+  for (int e = threadIdx.x; e < a.E; e += kThreads) h[e] = 0;
+  __syncthreads();
+  const int64_t base = (int64_t)blockIdx.x * kChunk;
+#pragma unroll
+  for (int r = 0; r < kRounds; r++) {
+    const int e = expert_of(a, base + r * kThreads + threadIdx.x);
+    if (e >= 0) atomicAdd(&h[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += kThreads) a.counts[(int64_t)blockIdx.x * a.E + e] = h[e];
+  grid_launch_dependents();
+}
+
+// 32 experts a CTA, the chunks in 32 slices.
+__global__ __launch_bounds__(1024) void place_scan(const PlanArgs a) {
+  __shared__ int32_t sums[32][33];
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int e = blockIdx.x * 32 + lane;
+  const int64_t per = (a.chunks + 31) / 32;
+  const int64_t b0 = min(a.chunks, slice * per), b1 = min(a.chunks, b0 + per);
+  int32_t s = 0;
+  if (e < a.E) {
+#pragma unroll 8
+    for (int64_t b = b0; b < b1; b++) s += a.counts[b * a.E + e];
+  }
+  sums[slice][lane] = s;
+  __syncthreads();
+  const int32_t mine = sums[lane][slice];  // (expert "slice", slice "lane")
+  const int32_t incl = (int32_t)warp_incl_scan((uint32_t)mine, lane);
+  __syncthreads();
+  sums[lane][slice] = incl - mine;
+  if (lane == 31 && blockIdx.x * 32 + slice < a.E) a.totals[blockIdx.x * 32 + slice] = incl;
+  __syncthreads();
+  if (e < a.E) {
+    int32_t run = sums[slice][lane];
+#pragma unroll 8
+    for (int64_t b = b0; b < b1; b++) {
+      const int32_t c = a.counts[b * a.E + e];
+      a.counts[b * a.E + e] = run;
+      run += c;
+    }
+  }
+  grid_launch_dependents();
+}
+
+// SINGLE: one chunk, whose own counts are the totals.
+template <bool SINGLE>
+__global__ __launch_bounds__(kThreads) void place_choices(const PlanArgs a) {
+  __shared__ uint16_t hist[kWarps][kMaxExperts];  // a warp's choices of each expert, then those of the warps before it
+  __shared__ int32_t base[kMaxExperts];           // place of the chunk's first choice of each expert
+  __shared__ int32_t start[kMaxExperts + 1];      // segments
+  __shared__ int32_t total[kMaxExperts];
+  __shared__ uint32_t scan[kWarps + 1];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  for (int i = tid; i < kWarps * kMaxExperts / 2; i += kThreads) reinterpret_cast<uint32_t*>(hist)[i] = 0;
+  __syncthreads();
+  // a warp's choices follow one another: 32 a round
+  const int64_t first = (int64_t)blockIdx.x * kChunk + wid * (32 * kRounds) + lane;
+  int ex[kRounds];
+  uint32_t rank[kRounds];
+  uint32_t n_bad = 0;
+#pragma unroll
+  for (int r = 0; r < kRounds; r++) {
+    const int64_t i = first + r * 32;
+    ex[r] = -1;
+    if (i < a.n) {
+      const int e = a.idx[i];
+      n_bad += e >= a.E;
+      ex[r] = e >= 0 && e < a.E ? e : -1;
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRounds; r++) {
+    const uint32_t same = __match_any_sync(kFull, ex[r]);
+    const int leader = __ffs(same) - 1;
+    rank[r] = 0;
+    if (ex[r] >= 0) rank[r] = hist[wid][ex[r]] + __popc(same & ((1u << lane) - 1));
+    __syncwarp();
+    if (ex[r] >= 0 && lane == leader) hist[wid][ex[r]] += (uint16_t)__popc(same);
+    __syncwarp();
+  }
+  if (a.bad) {
+    n_bad = __reduce_add_sync(kFull, n_bad);
+    if (lane == 0 && n_bad) atomicAdd(a.bad, n_bad);
+  }
+  __syncthreads();
+  if (!SINGLE) grid_dependency_wait();
+  // segments: each thread has a run of experts
+  const int per = (a.E + kThreads - 1) / kThreads;
+  uint32_t room = 0;
+  for (int j = 0; j < per; j++) {
+    const int e = tid * per + j;
+    if (e < a.E) {
+      uint32_t own = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; w++) {
+        const uint32_t c = hist[w][e];
+        hist[w][e] = (uint16_t)own;
+        own += c;
+      }
+      total[e] = SINGLE ? (int32_t)own : a.totals[e];
+      base[e] = SINGLE ? 0 : a.counts[(int64_t)blockIdx.x * a.E + e];
+      room += (uint32_t)((total[e] + a.align - 1) / a.align * a.align);
+    }
+  }
+  uint32_t all;
+  uint32_t at = block_incl_scan<kThreads>(room, scan, &all) - room;
+  for (int j = 0; j < per; j++) {
+    const int e = tid * per + j;
+    if (e < a.E) {
+      start[e] = (int32_t)at;
+      base[e] += (int32_t)at;
+      at += (uint32_t)((total[e] + a.align - 1) / a.align * a.align);
+    }
+  }
+  if (tid == 0) start[a.E] = (int32_t)all;
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kRounds; r++) {
+    const int64_t i = first + r * 32;
+    if (i >= a.n) break;
+    int32_t slot = -1;
+    if (ex[r] >= 0) {
+      slot = base[ex[r]] + hist[wid][ex[r]] + (int32_t)rank[r];
+      a.source[slot] = (int32_t)i;
+    }
+    a.slots[i] = slot;
+  }
+  if (blockIdx.x == 0)
+    for (int e = tid; e <= a.E; e += kThreads) a.offsets[e] = start[e];
+  // rows without a choice: a segment's end, and what is behind the last one
+  if (a.align > 1)
+    for (int e = blockIdx.x * kWarps + wid; e < a.E; e += gridDim.x * kWarps)
+      for (int32_t r = start[e] + total[e] + lane; r < start[e + 1]; r += 32) a.source[r] = -1;
+  for (int64_t r = start[a.E] + (int64_t)blockIdx.x * kThreads + tid; r < a.capacity; r += (int64_t)gridDim.x * kThreads)
+    a.source[r] = -1;
+}
+
+// ---- rows -----------------------------------------------------------------------
+
+template <int BYTES> struct Unit;
+template <> struct Unit<16> { using T = uint4; };
+template <> struct Unit<4> { using T = uint32_t; };
+template <> struct Unit<2> { using T = uint16_t; };
+
+// The elements of a unit.
+template <int DT, int BYTES>
+struct Packed {
+  using E = Elem<DT>;
+  using U = typename Unit<BYTES>::T;
+  static constexpr int N = BYTES / (int)sizeof(typename E::T);
+  static __device__ __forceinline__ void unpack(const U u, float (&f)[N]) {
+    if constexpr (BYTES == 16) E::unpack(u, f);
+    else if constexpr (DT == SCAPE_F32) f[0] = __uint_as_float(u);
+    else if constexpr (BYTES == 2) f[0] = E::load(&u);
+    else {
+      const uint16_t lo = (uint16_t)u, hi = (uint16_t)(u >> 16);
+      f[0] = E::load(&lo);
+      f[1] = E::load(&hi);
+    }
+  }
+  static __device__ __forceinline__ U pack(const float (&f)[N]) {
+    if constexpr (BYTES == 16) return E::pack(f);
+    else if constexpr (DT == SCAPE_F32) return __float_as_uint(f[0]);
+    else if constexpr (BYTES == 2) return E::make(f[0]);
+    else return E::pack2(f[0], f[1]);
+  }
+};
+
+template <int BYTES>
+__device__ __forceinline__ typename Unit<BYTES>::T zero_unit() {
+  if constexpr (BYTES == 16) return make_uint4(0, 0, 0, 0);
+  else return 0;
+}
+
+struct RowArgs {
+  const char* x;  // dispatch: tokens; combine, backward: rows by expert
+  char* out;      // dispatch, backward: rows by expert; combine: tokens
+  const char* d_out;
+  int64_t stride;   // of a token's row, in bytes (dispatch)
+  int64_t bytes;    // of a row
+  int64_t tokens, rows;
+  int k;
+  int slices;       // parts of a row that are worked on apart
+  const int32_t* slots;
+  const int32_t* source;
+  const float* weights;
+  float* d_weights;
+  int64_t row_warps;  // dispatch, backward: warps for the tokens; the others look for empty rows
+};
+
+constexpr int kEmptyRows = 4;  // rows that such a warp looks at
+
+template <int BYTES>
+__device__ void clear_empty_rows(const RowArgs& a, int64_t item, int lane) {
+  using U = typename Unit<BYTES>::T;
+  const int64_t units = a.bytes / BYTES;
+  for (int64_t r = item * kEmptyRows; r < min(a.rows, (item + 1) * kEmptyRows); r++) {
+    if (a.source[r] >= 0) continue;
+    U* out = reinterpret_cast<U*>(a.out + r * a.bytes);
+    for (int64_t u = lane; u < units; u += 32) out[u] = zero_unit<BYTES>();
+  }
+}
+
+// A warp takes R units a lane of a token's row, and stores them k times.
+template <int BYTES, int R>
+__global__ __launch_bounds__(kThreads) void dispatch_rows(const RowArgs a) {
+  using U = typename Unit<BYTES>::T;
+  const int lane = threadIdx.x & 31;
+  const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (item >= a.row_warps) {
+    clear_empty_rows<BYTES>(a, item - a.row_warps, lane);
+    return;
+  }
+  const int64_t t = item / a.slices, u0 = (item % a.slices) * (32 * R) + lane, units = a.bytes / BYTES;
+  int slot = lane < a.k ? a.slots[t * a.k + lane] : -1;
+  if (slot >= a.rows) slot = -1;
+  if (!__any_sync(kFull, slot >= 0)) return;  // (a token of no expert is not read)
+  const U* x = reinterpret_cast<const U*>(a.x + t * a.stride);
+  U v[R];
+#pragma unroll
+  for (int i = 0; i < R; i++) v[i] = u0 + i * 32 < units ? x[u0 + i * 32] : zero_unit<BYTES>();
+  for (int j = 0; j < a.k; j++) {
+    const int s = __shfl_sync(kFull, slot, j);
+    if (s < 0) continue;
+    U* out = reinterpret_cast<U*>(a.out + s * a.bytes);
+#pragma unroll
+    for (int i = 0; i < R; i++)
+      if (u0 + i * 32 < units) out[u0 + i * 32] = v[i];
+  }
+}
+
+// out[t] = sum over j of w_tj y[slot_tj], in this order, rounded once.
+template <int DT, int BYTES, int R>
+__global__ __launch_bounds__(kThreads) void combine_rows(const RowArgs a) {
+  using P = Packed<DT, BYTES>;
+  using U = typename P::U;
+  const int lane = threadIdx.x & 31;
+  const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (item >= a.row_warps) return;
+  const int64_t t = item / a.slices, u0 = (item % a.slices) * (32 * R) + lane, units = a.bytes / BYTES;
+  int slot = -1;
+  float w = 1.0f;
+  if (lane < a.k) {
+    slot = a.slots[t * a.k + lane];
+    if (slot >= a.rows) slot = -1;
+    if (a.weights) w = a.weights[t * a.k + lane];
+  }
+  float acc[R][P::N];
+#pragma unroll
+  for (int i = 0; i < R; i++)
+#pragma unroll
+    for (int e = 0; e < P::N; e++) acc[i][e] = 0.0f;
+#pragma unroll 2
+  for (int j = 0; j < a.k; j++) {
+    const int s = __shfl_sync(kFull, slot, j);
+    const float wj = __shfl_sync(kFull, w, j);
+    if (s < 0) continue;
+    const U* y = reinterpret_cast<const U*>(a.x + s * a.bytes);
+    U v[R];
+#pragma unroll
+    for (int i = 0; i < R; i++) v[i] = u0 + i * 32 < units ? y[u0 + i * 32] : zero_unit<BYTES>();
+#pragma unroll
+    for (int i = 0; i < R; i++) {
+      float f[P::N];
+      P::unpack(v[i], f);
+#pragma unroll
+      for (int e = 0; e < P::N; e++) acc[i][e] = __fmaf_rn(wj, f[e], acc[i][e]);
+    }
+  }
+  U* out = reinterpret_cast<U*>(a.out + t * a.bytes);
+#pragma unroll
+  for (int i = 0; i < R; i++)
+    if (u0 + i * 32 < units) out[u0 + i * 32] = P::pack(acc[i]);
+}
+
+// A warp has one choice: dy[slot] = w dout[t], dw = <dout[t], y[slot]>.  The token's
+// row comes from L1 for all but the first of its choices.
+template <int DT, int BYTES, int R>
+__global__ __launch_bounds__(kThreads) void combine_grad(const RowArgs a) {
+  using P = Packed<DT, BYTES>;
+  using U = typename P::U;
+  const int lane = threadIdx.x & 31;
+  const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (item >= a.row_warps) {
+    clear_empty_rows<BYTES>(a, item - a.row_warps, lane);
+    return;
+  }
+  const int64_t t = item / a.k, units = a.bytes / BYTES;
+  int s = a.slots[item];
+  if (s >= a.rows) s = -1;
+  float dot = 0.0f;
+  if (s >= 0) {
+    const float w = a.weights[item];
+    const U* g = reinterpret_cast<const U*>(a.d_out + t * a.bytes);
+    const U* y = reinterpret_cast<const U*>(a.x + s * a.bytes);
+    U* dy = reinterpret_cast<U*>(a.out + s * a.bytes);
+    for (int64_t u0 = lane; u0 < units; u0 += 32 * R) {
+      U vy[R], vg[R];
+#pragma unroll
+      for (int i = 0; i < R; i++) {
+        const bool in = u0 + i * 32 < units;
+        vy[i] = in ? y[u0 + i * 32] : zero_unit<BYTES>();
+        vg[i] = in ? g[u0 + i * 32] : zero_unit<BYTES>();
+      }
+#pragma unroll
+      for (int i = 0; i < R; i++) {
+        float fy[P::N], fg[P::N];
+        P::unpack(vy[i], fy);
+        P::unpack(vg[i], fg);
+#pragma unroll
+        for (int e = 0; e < P::N; e++) {
+          dot = __fmaf_rn(fg[e], fy[e], dot);
+          fg[e] *= w;
+        }
+        if (u0 + i * 32 < units) dy[u0 + i * 32] = P::pack(fg);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+  }
+  if (lane == 0 && a.d_weights) a.d_weights[item] = dot;
+}
+
+int fail(int code, const char* fmt, ...) {
+  char buf[256];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  set_thread_error(buf);
+  return code;
+}
+
+bool misaligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
+uint64_t size_of(int dtype) { return dtype == SCAPE_F32 ? 4 : 2; }
+
+template <class K, class... A>
+cudaError_t launch_behind(K kernel, unsigned grid, unsigned block, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  const cudaError_t last = cudaGetLastError();
+  return e != cudaSuccess ? e : last;
+}
+
+int check_plan(uint64_t tokens, int k, int experts, int align, uint64_t& capacity, uint64_t& bytes) {
+  if (experts < 1 || experts > kMaxExperts)
+    return fail(SCAPE_EINVAL, "experts=%d must be in [1, %d]", experts, kMaxExperts);
+  if (k < 1 || k > kMaxChoices) return fail(SCAPE_EINVAL, "k=%d outside [1, %d]", k, kMaxChoices);
+  if (align < 1 || align > 65536) return fail(SCAPE_EINVAL, "align=%d must be in [1, 65536]", align);
+  if (tokens >= (1ull << 31)) return fail(SCAPE_EINVAL, "tokens must be < 2^31");
+  const uint64_t n = tokens * (uint64_t)k;
+  capacity = n + std::min<uint64_t>((uint64_t)experts, n) * (uint64_t)(align - 1);
+  if (capacity >= (1ull << 31)) return fail(SCAPE_EINVAL, "the plan must have < 2^31 rows");
+  const uint64_t chunks = (n + kChunk - 1) / kChunk;
+  bytes = chunks > 1 ? (chunks + 1) * (uint64_t)experts * 4 : 0;
+  return SCAPE_OK;
+}
+
+// The widest unit that a row's length and all addresses are multiples of.
+int unit_of(int dtype, uint64_t bytes, std::initializer_list<uintptr_t> at) {
+  uintptr_t all = bytes;
+  for (uintptr_t p : at) all |= p;
+  return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : (int)size_of(dtype);
+}
+
+constexpr int kUnits16 = 4, kUnitsSmall = 8;  // units a lane has in flight
+
+int check_rows(int dtype, uint64_t tokens, int k, uint64_t rows, uint64_t dim) {
+  if (dtype < SCAPE_BF16 || dtype > SCAPE_F32) return fail(SCAPE_EINVAL, "unknown dtype %d", dtype);
+  if (k < 1 || k > kMaxChoices) return fail(SCAPE_EINVAL, "k=%d outside [1, %d]", k, kMaxChoices);
+  if (tokens >= (1ull << 31) || rows >= (1ull << 31) || tokens * (uint64_t)k >= (1ull << 31))
+    return fail(SCAPE_EINVAL, "tokens x k and rows must be < 2^31");
+  if (dim < 1 || dim >= (1ull << 24)) return fail(SCAPE_EINVAL, "dim=%llu must be in [1, 2^24)", (unsigned long long)dim);
+  return SCAPE_OK;
+}
+
+void fill(RowArgs& a, int dtype, uint64_t tokens, int k, uint64_t rows, uint64_t dim, int unit) {
+  a.bytes = (int64_t)(dim * size_of(dtype));
+  a.tokens = (int64_t)tokens;
+  a.rows = (int64_t)rows;
+  a.k = k;
+  const int64_t part = 32 * (int64_t)unit * (unit == 16 ? kUnits16 : kUnitsSmall);
+  a.slices = (int)((a.bytes + part - 1) / part);
+}
+
+bool grid_of(int64_t warps, unsigned& grid) {
+  const int64_t g = (warps + kWarps - 1) / kWarps;
+  grid = (unsigned)g;
+  return g < (1ll << 31);
+}
+
+bool ranges_meet(const void* p, uint64_t n, const void* q, uint64_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + m && b < a + n;
+}
+
+}  // namespace
+}  // namespace scape
+
+SCAPE_API int scape_expert_plan_sizes(uint64_t tokens, int k, int experts, int align, uint64_t* capacity,
+                                      uint64_t* workspace_bytes) {
+  using namespace scape;
+  if (!capacity || !workspace_bytes) return fail(SCAPE_EINVAL, "capacity and workspace_bytes are required");
+  *capacity = *workspace_bytes = 0;
+  uint64_t c, b;
+  if (int rc = check_plan(tokens, k, experts, align, c, b)) return rc;
+  *capacity = c;
+  *workspace_bytes = b;
+  return SCAPE_OK;
+}
+
+SCAPE_API int scape_expert_plan(const int32_t* idx, uint64_t tokens, int k, int experts, int align,
+                                int32_t* offsets, int32_t* slots, int32_t* source, uint32_t* bad_count,
+                                void* workspace, uint64_t workspace_bytes, void* stream) {
+  using namespace scape;
+  uint64_t capacity, need;
+  if (int rc = check_plan(tokens, k, experts, align, capacity, need)) return rc;
+  if (!offsets || (tokens > 0 && (!idx || !slots || !source)))
+    return fail(SCAPE_EINVAL, "idx, offsets, slots and source are required");
+  if (misaligned(idx, 4) || misaligned(offsets, 4) || misaligned(slots, 4) || misaligned(source, 4) ||
+      misaligned(bad_count, 4))
+    return fail(SCAPE_EINVAL, "a buffer is not aligned to its element size");
+  if (need && (!workspace || misaligned(workspace, 16) || workspace_bytes < need))
+    return fail(SCAPE_EINVAL, "workspace must be %llu bytes, 16-byte aligned", (unsigned long long)need);
+  PlanArgs a{};
+  a.idx = idx;
+  a.n = (int64_t)(tokens * (uint64_t)k);
+  a.E = experts;
+  a.align = align;
+  a.chunks = (a.n + kChunk - 1) / kChunk;
+  a.capacity = (int64_t)capacity;
+  a.offsets = offsets;
+  a.slots = slots;
+  a.source = source;
+  a.bad = bad_count;
+  a.totals = static_cast<int32_t*>(workspace);
+  a.counts = a.totals + experts;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a.chunks <= 1) {
+    place_choices<true><<<1, kThreads, 0, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? SCAPE_OK : fail(SCAPE_ECUDA, "place_choices: %s", cudaGetErrorString(e));
+  }
+  place_counts<<<(unsigned)a.chunks, kThreads, 0, s>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(SCAPE_ECUDA, "place_counts: %s", cudaGetErrorString(e));
+  e = launch_behind(place_scan, (unsigned)((experts + 31) / 32), 1024, s, a);
+  if (e != cudaSuccess) return fail(SCAPE_ECUDA, "place_scan: %s", cudaGetErrorString(e));
+  e = launch_behind(place_choices<false>, (unsigned)a.chunks, kThreads, s, a);
+  return e == cudaSuccess ? SCAPE_OK : fail(SCAPE_ECUDA, "place_choices: %s", cudaGetErrorString(e));
+}
+
+SCAPE_API int scape_expert_dispatch(const void* x, int dtype, uint64_t tokens, uint64_t dim,
+                                    uint64_t row_stride, int k, const int32_t* slots,
+                                    const int32_t* source, uint64_t rows, void* out, void* stream) {
+  using namespace scape;
+  if (int rc = check_rows(dtype, tokens, k, rows, dim)) return rc;
+  if (row_stride < dim || row_stride >= (1ull << 32)) return fail(SCAPE_EINVAL, "row_stride must be >= dim and < 2^32");
+  if (rows == 0) return SCAPE_OK;
+  if ((tokens > 0 && (!x || !slots)) || !source || !out)
+    return fail(SCAPE_EINVAL, "x, slots, source and out are required");
+  const uint64_t es = size_of(dtype);
+  if (misaligned(x, es) || misaligned(out, es) || misaligned(slots, 4) || misaligned(source, 4))
+    return fail(SCAPE_EINVAL, "a buffer is not aligned to its element size");
+  if (tokens && ranges_meet(x, ((tokens - 1) * row_stride + dim) * es, out, rows * dim * es))
+    return fail(SCAPE_EINVAL, "out must not overlap x");
+  RowArgs a{};
+  const int unit = unit_of(dtype, dim * es, {row_stride * es, reinterpret_cast<uintptr_t>(x), reinterpret_cast<uintptr_t>(out)});
+  fill(a, dtype, tokens, k, rows, dim, unit);
+  a.x = static_cast<const char*>(x);
+  a.out = static_cast<char*>(out);
+  a.stride = (int64_t)(row_stride * es);
+  a.slots = slots;
+  a.source = source;
+  a.row_warps = a.tokens * a.slices;
+  unsigned grid;
+  if (!grid_of(a.row_warps + (a.rows + kEmptyRows - 1) / kEmptyRows, grid)) return fail(SCAPE_EINVAL, "too many rows");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (unit == 16) dispatch_rows<16, kUnits16><<<grid, kThreads, 0, s>>>(a);
+  else if (unit == 4) dispatch_rows<4, kUnitsSmall><<<grid, kThreads, 0, s>>>(a);
+  else dispatch_rows<2, kUnitsSmall><<<grid, kThreads, 0, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? SCAPE_OK : fail(SCAPE_ECUDA, "dispatch_rows: %s", cudaGetErrorString(e));
+}
+
+namespace scape {
+namespace {
+template <int DT>
+void launch_combine(const RowArgs& a, int unit, unsigned grid, bool back, cudaStream_t s) {
+  if (unit == 16) {
+    if (back) combine_grad<DT, 16, kUnits16><<<grid, kThreads, 0, s>>>(a);
+    else combine_rows<DT, 16, kUnits16><<<grid, kThreads, 0, s>>>(a);
+  } else if (unit == 4) {
+    if (back) combine_grad<DT, 4, kUnitsSmall><<<grid, kThreads, 0, s>>>(a);
+    else combine_rows<DT, 4, kUnitsSmall><<<grid, kThreads, 0, s>>>(a);
+  } else if constexpr (DT != SCAPE_F32) {
+    if (back) combine_grad<DT, 2, kUnitsSmall><<<grid, kThreads, 0, s>>>(a);
+    else combine_rows<DT, 2, kUnitsSmall><<<grid, kThreads, 0, s>>>(a);
+  }
+}
+void launch_combine_any(int dtype, const RowArgs& a, int unit, unsigned grid, bool back, cudaStream_t s) {
+  if (dtype == SCAPE_BF16) launch_combine<SCAPE_BF16>(a, unit, grid, back, s);
+  else if (dtype == SCAPE_F16) launch_combine<SCAPE_F16>(a, unit, grid, back, s);
+  else launch_combine<SCAPE_F32>(a, unit, grid, back, s);
+}
+}  // namespace
+}  // namespace scape
+
+SCAPE_API int scape_expert_combine(const void* y, int dtype, uint64_t rows, uint64_t dim,
+                                   const int32_t* slots, const float* weights, uint64_t tokens, int k,
+                                   void* out, void* stream) {
+  using namespace scape;
+  if (int rc = check_rows(dtype, tokens, k, rows, dim)) return rc;
+  if (tokens == 0) return SCAPE_OK;
+  if ((rows > 0 && !y) || !slots || !out) return fail(SCAPE_EINVAL, "y, slots and out are required");
+  const uint64_t es = size_of(dtype);
+  if (misaligned(y, es) || misaligned(out, es) || misaligned(slots, 4) || misaligned(weights, 4))
+    return fail(SCAPE_EINVAL, "a buffer is not aligned to its element size");
+  if (ranges_meet(y, rows * dim * es, out, tokens * dim * es)) return fail(SCAPE_EINVAL, "out must not overlap y");
+  RowArgs a{};
+  const int unit = unit_of(dtype, dim * es, {reinterpret_cast<uintptr_t>(y), reinterpret_cast<uintptr_t>(out)});
+  fill(a, dtype, tokens, k, rows, dim, unit);
+  a.x = static_cast<const char*>(y);
+  a.out = static_cast<char*>(out);
+  a.slots = slots;
+  a.weights = weights;
+  a.row_warps = a.tokens * a.slices;
+  unsigned grid;
+  if (!grid_of(a.row_warps, grid)) return fail(SCAPE_EINVAL, "too many rows");
+  launch_combine_any(dtype, a, unit, grid, false, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? SCAPE_OK : fail(SCAPE_ECUDA, "combine_rows: %s", cudaGetErrorString(e));
+}
+
+SCAPE_API int scape_expert_combine_backward(const void* d_out, const void* y, int dtype, uint64_t rows,
+                                            uint64_t dim, const int32_t* slots, const int32_t* source,
+                                            const float* weights, uint64_t tokens, int k, void* d_y,
+                                            float* d_weights, void* stream) {
+  using namespace scape;
+  if (int rc = check_rows(dtype, tokens, k, rows, dim)) return rc;
+  if (rows == 0 && tokens == 0) return SCAPE_OK;
+  if ((tokens > 0 && (!d_out || !slots || !weights)) || (rows > 0 && (!y || !source || !d_y)))
+    return fail(SCAPE_EINVAL, "d_out, y, slots, source, weights and d_y are required");
+  const uint64_t es = size_of(dtype);
+  if (misaligned(d_out, es) || misaligned(y, es) || misaligned(d_y, es) || misaligned(slots, 4) ||
+      misaligned(source, 4) || misaligned(weights, 4) || misaligned(d_weights, 4))
+    return fail(SCAPE_EINVAL, "a buffer is not aligned to its element size");
+  if (ranges_meet(d_y, rows * dim * es, d_out, tokens * dim * es) || ranges_meet(d_y, rows * dim * es, y, rows * dim * es))
+    return fail(SCAPE_EINVAL, "d_y must not overlap d_out or y");
+  RowArgs a{};
+  const int unit = unit_of(dtype, dim * es, {reinterpret_cast<uintptr_t>(y), reinterpret_cast<uintptr_t>(d_out),
+                                             reinterpret_cast<uintptr_t>(d_y)});
+  fill(a, dtype, tokens, k, rows, dim, unit);
+  a.x = static_cast<const char*>(y);
+  a.d_out = static_cast<const char*>(d_out);
+  a.out = static_cast<char*>(d_y);
+  a.slots = slots;
+  a.source = source;
+  a.weights = weights;
+  a.d_weights = d_weights;
+  a.row_warps = a.tokens * a.k;
+  unsigned grid;
+  if (!grid_of(a.row_warps + (a.rows + kEmptyRows - 1) / kEmptyRows, grid)) return fail(SCAPE_EINVAL, "too many rows");
+  launch_combine_any(dtype, a, unit, grid, true, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? SCAPE_OK : fail(SCAPE_ECUDA, "combine_grad: %s", cudaGetErrorString(e));
+}

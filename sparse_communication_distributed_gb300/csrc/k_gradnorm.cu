@@ -1,0 +1,495 @@
+// Norms of the workers' gradients over many tensors, and their clipping
+// (scape_grad_norm, scape_clip_grads).
+//
+// A worker's tensors are cut into chunks.  norm_chunks adds up the squares of a
+// chunk (fp32 over 64 elements of a thread, 64 bits from there on) and leaves one
+// partial sum a chunk; norm_finish adds up a worker's partials in a fixed order;
+// clip_chunks multiplies.  The scale is known only after the last element, so a
+// clipped gradient is read twice: the floor is one reading, and what the second
+// one finds in L2 is what can be saved of it.  clip_chunks therefore goes from the
+// last chunk to the first.
+//
+// The table of tensors travels in the kernels' parameters (at most 32764 bytes), so
+// there is nothing to copy to the device and a captured graph keeps its own.
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <vector>
+
+#include "objective.cuh"
+#include "scape_kernels.cuh"
+
+#define SCAPE_API extern "C" __attribute__((visibility("default")))
+
+namespace scape {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 8;  // vectors that a thread has in flight
+constexpr uint64_t kMinChunk = 4096, kMaxChunkElems = 65536;
+constexpr int kMaxGroups = kMaxW;
+
+struct Tensor {
+  const void* src;
+  void* dst;
+  uint64_t n;
+  uint32_t chunk0;  // its first chunk, counted over all tensors
+  uint32_t meta;    // type | type of dst << 2 | group << 8
+};
+
+template <int CAP>
+struct Table {
+  Tensor t[CAP];
+  int n;
+  uint32_t end;         // chunk behind the last one
+  uint32_t chunk_elems;
+};
+
+// The tensor of chunk c: the last one that starts at or before it.
+template <int CAP>
+__device__ __forceinline__ int tensor_of(const Table<CAP>& tb, uint32_t c) {
+  int lo = 0, hi = tb.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tb.t[mid].chunk0 <= c) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Sum of squares of a thread's batch.  In fp32 it is right to 2^-18 as long as it
+// is neither beyond fp32's range nor so small that squares were lost below it;
+// otherwise the batch is added up again in 64 bits.
+template <int DT>
+__device__ __forceinline__ double squares(const uint4 (&v)[kBatch]) {
+  using E = Elem<DT>;
+  float s[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < kBatch; i++) {
+    float f[E::kPerVec];
+    E::unpack(v[i], f);
+#pragma unroll
+    for (int j = 0; j < E::kPerVec; j++) s[j & 1] = __fmaf_rn(f[j], f[j], s[j & 1]);
+  }
+  const float sum = s[0] + s[1];
+  if (sum > 0x1p-80f && sum < 0x1p120f) return (double)sum;
+  double d = 0.0;
+#pragma unroll
+  for (int i = 0; i < kBatch; i++) {
+    if ((v[i].x | v[i].y | v[i].z | v[i].w) == 0u) continue;
+    float f[E::kPerVec];
+    E::unpack(v[i], f);
+#pragma unroll
+    for (int j = 0; j < E::kPerVec; j++) d += (double)f[j] * (double)f[j];
+  }
+  return d;
+}
+
+template <int DT>
+__device__ double chunk_squares(const void* base, uint64_t first, uint32_t n) {
+  using E = Elem<DT>;
+  using T = typename E::T;
+  const T* p = static_cast<const T*>(base) + first;
+  const int tid = threadIdx.x;
+  // elements in front of the first 16-byte boundary, whole vectors, the rest
+  const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T);
+  const uint32_t head = min(n, off ? (uint32_t)E::kPerVec - off : 0u);
+  const uint32_t nv = (n - head) / E::kPerVec;
+  const uint32_t done = head + nv * E::kPerVec;
+  double d = 0.0;
+  if (tid < head) {
+    const float x = E::load(p + tid);
+    d = (double)x * x;
+  }
+  if (done + tid < n) {  // fewer than a vector
+    const float x = E::load(p + done + tid);
+    d += (double)x * x;
+  }
+  const uint4* q = reinterpret_cast<const uint4*>(p + head);
+  for (uint32_t v0 = tid; v0 < nv; v0 += kThreads * kBatch) {
+    uint4 v[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; i++) {
+      const uint32_t at = v0 + i * kThreads;
+      v[i] = at < nv ? ld_row_u4(q + at) : make_uint4(0, 0, 0, 0);
+    }
+    d += squares<DT>(v);
+  }
+  return d;
+}
+
+template <int CAP>
+__global__ __launch_bounds__(kThreads) void norm_chunks(const __grid_constant__ Table<CAP> tb,
+                                                        double* __restrict__ part) {
+  __shared__ double buf[32];
+  for (uint32_t c = tb.t[0].chunk0 + blockIdx.x; c < tb.end; c += gridDim.x) {
+    const Tensor& t = tb.t[tensor_of(tb, c)];
+    const uint64_t first = (uint64_t)(c - t.chunk0) * tb.chunk_elems;
+    const uint32_t n = (uint32_t)min((uint64_t)tb.chunk_elems, t.n - first);
+    const int dt = t.meta & 3;
+    double d = dt == SCAPE_BF16  ? chunk_squares<SCAPE_BF16>(t.src, first, n)
+               : dt == SCAPE_F16 ? chunk_squares<SCAPE_F16>(t.src, first, n)
+                                 : chunk_squares<SCAPE_F32>(t.src, first, n);
+    d = cta_sum(d, buf);
+    if (threadIdx.x == 0) part[c] = d;
+  }
+  grid_launch_dependents();
+}
+
+struct Groups {
+  uint32_t chunk0[kMaxGroups + 1];
+};
+
+// One CTA a group.
+__global__ __launch_bounds__(1024) void norm_finish(const __grid_constant__ Groups g,
+                                                    const double* __restrict__ part, float max_norm,
+                                                    float* __restrict__ norms,
+                                                    float* __restrict__ scales) {
+  __shared__ double buf[32];
+  grid_dependency_wait();
+  double d = 0.0;
+  for (uint32_t c = g.chunk0[blockIdx.x] + threadIdx.x; c < g.chunk0[blockIdx.x + 1]; c += 1024)
+    d += part[c];
+  d = cta_sum(d, buf);
+  if (threadIdx.x == 0) {
+    const double norm = sqrt(d);
+    norms[blockIdx.x] = (float)norm;
+    // (an infinite norm and NaN are not clipped: the caller sees them)
+    if (scales)
+      scales[blockIdx.x] = norm > (double)max_norm && norm < INFINITY ? (float)((double)max_norm / norm) : 1.0f;
+  }
+  grid_launch_dependents();
+}
+
+// Eight elements as 32-bit values.
+template <int DT>
+__device__ __forceinline__ void load8(const void* base, uint64_t at, bool vec, float (&f)[8]) {
+  using E = Elem<DT>;
+  const typename E::T* p = static_cast<const typename E::T*>(base) + at;
+  if (!vec) {
+#pragma unroll
+    for (int j = 0; j < 8; j++) f[j] = E::load(p + j);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8 / E::kPerVec; i++) {
+      float g[E::kPerVec];
+      E::unpack(ld_row_u4(p + i * E::kPerVec), g);
+#pragma unroll
+      for (int j = 0; j < E::kPerVec; j++) f[i * E::kPerVec + j] = g[j];
+    }
+  }
+}
+template <int DT>
+__device__ __forceinline__ void store8(void* base, uint64_t at, const float (&f)[8]) {
+  using E = Elem<DT>;
+  typename E::T* p = static_cast<typename E::T*>(base) + at;
+#pragma unroll
+  for (int i = 0; i < 8 / E::kPerVec; i++) {
+    float g[E::kPerVec];
+#pragma unroll
+    for (int j = 0; j < E::kPerVec; j++) g[j] = f[i * E::kPerVec + j];
+    reinterpret_cast<uint4*>(p)[i] = E::pack(g);
+  }
+}
+
+// dst = src * scale, each product rounded once.  Whole stores of 16 bytes from the
+// first boundary of dst on; loads of 16 bytes where src has its boundary there too.
+template <int SDT, int DDT>
+__device__ void scale_chunk(const Tensor& t, uint64_t first, uint32_t n, float scale) {
+  using S = Elem<SDT>;
+  using D = Elem<DDT>;
+  const typename S::T* src = static_cast<const typename S::T*>(t.src) + first;
+  typename D::T* dst = static_cast<typename D::T*>(t.dst) + first;
+  const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(dst) & 15u) / sizeof(typename D::T);
+  const uint32_t head = min(n, off ? (uint32_t)D::kPerVec - off : 0u);
+  const uint32_t n8 = (n - head) / 8, done = head + n8 * 8;
+  const bool vec = (reinterpret_cast<uintptr_t>(src + head) & 15u) == 0;
+  constexpr int U = 4;
+  const uint32_t tid = threadIdx.x;
+  if (tid < head) dst[tid] = D::make(S::load(src + tid) * scale);
+  if (done + tid < n) dst[done + tid] = D::make(S::load(src + done + tid) * scale);
+  for (uint32_t v0 = tid; v0 < n8; v0 += kThreads * U) {
+    float f[U][8];
+#pragma unroll
+    for (int i = 0; i < U; i++)
+      if (v0 + i * kThreads < n8) load8<SDT>(src, head + (uint64_t)(v0 + i * kThreads) * 8, vec, f[i]);
+#pragma unroll
+    for (int i = 0; i < U; i++)
+      if (v0 + i * kThreads < n8) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) f[i][j] *= scale;
+        store8<DDT>(dst, head + (uint64_t)(v0 + i * kThreads) * 8, f[i]);
+      }
+  }
+}
+
+template <int SDT>
+__device__ void scale_from(const Tensor& t, uint64_t first, uint32_t n, float scale) {
+  const int dt = (t.meta >> 2) & 3;
+  if (dt == SCAPE_BF16) scale_chunk<SDT, SCAPE_BF16>(t, first, n, scale);
+  else if (dt == SCAPE_F16) scale_chunk<SDT, SCAPE_F16>(t, first, n, scale);
+  else scale_chunk<SDT, SCAPE_F32>(t, first, n, scale);
+}
+
+template <int CAP>
+__global__ __launch_bounds__(kThreads) void clip_chunks(const __grid_constant__ Table<CAP> tb,
+                                                        const float* __restrict__ scales) {
+  grid_dependency_wait();
+  const uint32_t begin = tb.t[0].chunk0;
+  for (uint32_t i = begin + blockIdx.x; i < tb.end; i += gridDim.x) {
+    const uint32_t c = begin + (tb.end - 1 - i);  // what was read last comes first
+    const Tensor& t = tb.t[tensor_of(tb, c)];
+    const float scale = scales[t.meta >> 8];
+    const uint64_t first = (uint64_t)(c - t.chunk0) * tb.chunk_elems;
+    const uint32_t n = (uint32_t)min((uint64_t)tb.chunk_elems, t.n - first);
+    const int dt = t.meta & 3;
+    if (scale == 1.0f && t.src == t.dst) continue;  // in place: nothing to change
+    if (dt == SCAPE_BF16) scale_from<SCAPE_BF16>(t, first, n, scale);
+    else if (dt == SCAPE_F16) scale_from<SCAPE_F16>(t, first, n, scale);
+    else scale_from<SCAPE_F32>(t, first, n, scale);
+  }
+}
+
+int fail(int code, const char* fmt, ...) {
+  char buf[256];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  set_thread_error(buf);
+  return code;
+}
+
+uint64_t size_of(int dtype) { return dtype == SCAPE_F32 ? 4 : 2; }
+bool known(int dtype) { return dtype >= SCAPE_BF16 && dtype <= SCAPE_F32; }
+
+// How the tensors are cut, by their sizes alone.
+struct Cut {
+  uint64_t chunk_elems = kMinChunk, chunks = 0;
+};
+
+int check_sizes(const scape_grads* g, Cut& cut) {
+  if (!g) return fail(SCAPE_EINVAL, "grads is NULL");
+  if (g->n_groups < 1 || g->n_groups > (uint32_t)kMaxGroups)
+    return fail(SCAPE_EINVAL, "n_groups=%u must be in [1, %d]", g->n_groups, kMaxGroups);
+  if (g->n_tensors >= (1u << 20)) return fail(SCAPE_EINVAL, "n_tensors must be < 2^20");
+  if (g->n_tensors && !g->numel) return fail(SCAPE_EINVAL, "numel is NULL");
+  if (g->first_tensor) {
+    if (g->first_tensor[0] != 0 || g->first_tensor[g->n_groups] != g->n_tensors)
+      return fail(SCAPE_EINVAL, "first_tensor must begin with 0 and end with n_tensors");
+    for (uint32_t i = 0; i < g->n_groups; i++)
+      if (g->first_tensor[i] > g->first_tensor[i + 1])
+        return fail(SCAPE_EINVAL, "first_tensor must ascend");
+  } else if (g->n_groups != 1) {
+    return fail(SCAPE_EINVAL, "n_groups > 1 needs first_tensor");
+  }
+  uint64_t total = 0;
+  for (uint32_t i = 0; i < g->n_tensors; i++) {
+    if (g->numel[i] >= (1ull << 40)) return fail(SCAPE_EINVAL, "tensor %u: numel must be < 2^40", i);
+    total += g->numel[i];
+  }
+  if (total >= (1ull << 44)) return fail(SCAPE_EINVAL, "the gradients must have < 2^44 elements");
+  // chunks large enough that few partials are left, and two a resident CTA where there is enough for that
+  const uint64_t want = 2ull * 8 * (uint64_t)num_sms();
+  while (cut.chunk_elems < kMaxChunkElems && total / (2 * cut.chunk_elems) >= want) cut.chunk_elems *= 2;
+  for (uint32_t i = 0; i < g->n_tensors; i++)
+    cut.chunks += (g->numel[i] + cut.chunk_elems - 1) / cut.chunk_elems;
+  if (cut.chunks >= (1ull << 31)) return fail(SCAPE_EINVAL, "too many elements or tensors");
+  return SCAPE_OK;
+}
+
+int check_tensors(const scape_grads* g) {
+  if (g->n_tensors && (!g->grads || !g->dtypes)) return fail(SCAPE_EINVAL, "grads and dtypes are required");
+  for (uint32_t i = 0; i < g->n_tensors; i++) {
+    if (!known(g->dtypes[i])) return fail(SCAPE_EINVAL, "tensor %u: unknown dtype %d", i, g->dtypes[i]);
+    if (g->numel[i] && !g->grads[i]) return fail(SCAPE_EINVAL, "tensor %u is NULL", i);
+    if (reinterpret_cast<uintptr_t>(g->grads[i]) % size_of(g->dtypes[i]))
+      return fail(SCAPE_EINVAL, "tensor %u is not aligned to its element size", i);
+  }
+  return SCAPE_OK;
+}
+
+// No element is written twice, nor read after another tensor's was written over it.
+int check_overlap(const scape_grads* g, void* const* out, const uint8_t* odt) {
+  struct Span {
+    uintptr_t a, b;
+    uint32_t i;
+  };
+  std::vector<Span> w;
+  w.reserve(g->n_tensors);
+  for (uint32_t i = 0; i < g->n_tensors; i++)
+    if (g->numel[i]) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(out[i]);
+      w.push_back({a, a + g->numel[i] * size_of(odt[i]), i});
+    }
+  if (!std::is_sorted(w.begin(), w.end(), [](const Span& x, const Span& y) { return x.a < y.a; }))
+    std::sort(w.begin(), w.end(), [](const Span& x, const Span& y) { return x.a < y.a; });
+  for (size_t j = 1; j < w.size(); j++)
+    if (w[j].a < w[j - 1].b)
+      return fail(SCAPE_EINVAL, "the results of tensors %u and %u overlap", w[j - 1].i, w[j].i);
+  for (uint32_t i = 0; i < g->n_tensors; i++) {
+    if (!g->numel[i]) continue;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(g->grads[i]), b = a + g->numel[i] * size_of(g->dtypes[i]);
+    size_t lo = 0, hi = w.size();  // the first span that ends behind a
+    while (lo < hi) {
+      const size_t mid = (lo + hi) / 2;
+      if (w[mid].b > a) hi = mid;
+      else lo = mid + 1;
+    }
+    if (lo < w.size() && w[lo].a < b &&
+        !(w[lo].i == i && w[lo].a == a && odt[i] == g->dtypes[i]))
+      return fail(SCAPE_EINVAL, "the result of tensor %u overlaps tensor %u", w[lo].i, i);
+  }
+  return SCAPE_OK;
+}
+
+template <class K, class... A>
+cudaError_t launch_behind(K kernel, unsigned grid, unsigned block, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  const cudaError_t last = cudaGetLastError();
+  return e != cudaSuccess ? e : last;
+}
+
+// Tensors [i0, i1) into a table, and its launch.
+template <int CAP>
+cudaError_t launch_table(const scape_grads* g, const Cut& cut, void* const* out, const uint8_t* odt,
+                         const uint32_t* group, uint32_t i0, uint32_t i1, uint32_t chunk0, double* part,
+                         const float* scales, bool behind, cudaStream_t s) {
+  Table<CAP> tb;
+  tb.n = 0;
+  tb.chunk_elems = (uint32_t)cut.chunk_elems;
+  uint32_t c = chunk0;
+  for (uint32_t i = i0; i < i1; i++) {
+    if (!g->numel[i]) continue;
+    Tensor& t = tb.t[tb.n++];
+    t.src = g->grads[i];
+    t.dst = out ? out[i] : nullptr;
+    t.n = g->numel[i];
+    t.chunk0 = c;
+    t.meta = g->dtypes[i] | (odt ? odt[i] : 0u) << 2 | group[i] << 8;
+    c += (uint32_t)((g->numel[i] + cut.chunk_elems - 1) / cut.chunk_elems);
+  }
+  tb.end = c;
+  if (!tb.n) return cudaSuccess;
+  const unsigned grid = std::min<unsigned>(c - chunk0, 8u * (unsigned)num_sms());
+  if (out) {
+    return behind ? launch_behind(clip_chunks<CAP>, grid, kThreads, s, tb, scales)
+                  : (clip_chunks<CAP><<<grid, kThreads, 0, s>>>(tb, scales), cudaGetLastError());
+  }
+  norm_chunks<CAP><<<grid, kThreads, 0, s>>>(tb, part);
+  return cudaGetLastError();
+}
+
+// All tensors, as many tables as they need: small calls take small parameters.
+constexpr int kSmallTable = 16, kLargeTable = 640;
+cudaError_t launch_all(const scape_grads* g, const Cut& cut, void* const* out, const uint8_t* odt,
+                       const uint32_t* group, double* part, const float* scales, cudaStream_t s) {
+  uint32_t chunk0 = 0;
+  for (uint32_t i0 = 0; i0 < g->n_tensors;) {
+    const uint32_t i1 = std::min(g->n_tensors, i0 + (uint32_t)kLargeTable);
+    const bool behind = i0 == 0;  // (only the first follows norm_finish directly)
+    const cudaError_t e =
+        i1 - i0 <= (uint32_t)kSmallTable
+            ? launch_table<kSmallTable>(g, cut, out, odt, group, i0, i1, chunk0, part, scales, behind, s)
+            : launch_table<kLargeTable>(g, cut, out, odt, group, i0, i1, chunk0, part, scales, behind, s);
+    if (e != cudaSuccess) return e;
+    for (; i0 < i1; i0++) chunk0 += (uint32_t)((g->numel[i0] + cut.chunk_elems - 1) / cut.chunk_elems);
+  }
+  return cudaSuccess;
+}
+
+uint64_t bytes_of(const Cut& cut) { return cut.chunks * 8 + kMaxGroups * 4; }
+
+int norm_and_clip(const scape_grads* g, bool clip, float max_norm, void* const* out, const uint8_t* odt,
+                  float* norms, void* workspace, uint64_t workspace_bytes, void* stream) {
+  Cut cut;
+  if (int rc = check_sizes(g, cut)) return rc;
+  if (int rc = check_tensors(g)) return rc;
+  if (clip) {
+    if (!(max_norm > 0.0f)) return fail(SCAPE_EINVAL, "max_norm must be > 0");
+    if (!out) {
+      out = const_cast<void* const*>(reinterpret_cast<const void* const*>(g->grads));
+      odt = g->dtypes;
+    } else {
+      if (g->n_tensors && !odt) return fail(SCAPE_EINVAL, "out_dtypes is NULL");
+      for (uint32_t i = 0; i < g->n_tensors; i++) {
+        if (!known(odt[i])) return fail(SCAPE_EINVAL, "out %u: unknown dtype %d", i, odt[i]);
+        if (g->numel[i] && !out[i]) return fail(SCAPE_EINVAL, "out %u is NULL", i);
+        if (reinterpret_cast<uintptr_t>(out[i]) % size_of(odt[i]))
+          return fail(SCAPE_EINVAL, "out %u is not aligned to its element size", i);
+      }
+    }
+    if (int rc = check_overlap(g, out, odt)) return rc;
+  }
+  if (!norms || reinterpret_cast<uintptr_t>(norms) % 4)
+    return fail(SCAPE_EINVAL, "norms is required, aligned to its element size");
+  const uint64_t need = bytes_of(cut);
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 || workspace_bytes < need)
+    return fail(SCAPE_EINVAL, "workspace must be %llu bytes, 16-byte aligned", (unsigned long long)need);
+
+  std::vector<uint32_t> group(g->n_tensors, 0u);
+  Groups gr{};
+  uint32_t at = 0;
+  for (uint32_t w = 0, i = 0; w < g->n_groups; w++) {
+    gr.chunk0[w] = at;
+    const uint32_t end = g->first_tensor ? (uint32_t)g->first_tensor[w + 1] : g->n_tensors;
+    for (; i < end; i++) {
+      group[i] = w;
+      at += (uint32_t)((g->numel[i] + cut.chunk_elems - 1) / cut.chunk_elems);
+    }
+    gr.chunk0[w + 1] = at;
+  }
+  double* part = static_cast<double*>(workspace);
+  float* scales = reinterpret_cast<float*>(part + cut.chunks);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_all(g, cut, nullptr, nullptr, group.data(), part, nullptr, s);
+  if (e != cudaSuccess) return fail(SCAPE_ECUDA, "norm_chunks: %s", cudaGetErrorString(e));
+  e = launch_behind(norm_finish, g->n_groups, 1024, s, gr, (const double*)part, max_norm, norms,
+                    clip ? scales : (float*)nullptr);
+  if (e != cudaSuccess) return fail(SCAPE_ECUDA, "norm_finish: %s", cudaGetErrorString(e));
+  if (!clip) return SCAPE_OK;
+  e = launch_all(g, cut, out, odt, group.data(), part, scales, s);
+  return e == cudaSuccess ? SCAPE_OK : fail(SCAPE_ECUDA, "clip_chunks: %s", cudaGetErrorString(e));
+}
+
+}  // namespace
+}  // namespace scape
+
+SCAPE_API int scape_grad_workspace(const scape_grads* grads, uint64_t* bytes) {
+  using namespace scape;
+  if (!bytes) return fail(SCAPE_EINVAL, "bytes is NULL");
+  *bytes = 0;
+  Cut cut;
+  if (int rc = check_sizes(grads, cut)) return rc;
+  *bytes = bytes_of(cut);
+  return SCAPE_OK;
+}
+
+SCAPE_API int scape_grad_norm(const scape_grads* grads, float* norms, void* workspace,
+                              uint64_t workspace_bytes, void* stream) {
+  try {
+    return scape::norm_and_clip(grads, false, 0.0f, nullptr, nullptr, norms, workspace, workspace_bytes, stream);
+  } catch (...) {
+    return scape::fail(SCAPE_ENOMEM, "host allocation failed");
+  }
+}
+
+SCAPE_API int scape_clip_grads(const scape_grads* grads, float max_norm, void* const* out,
+                               const uint8_t* out_dtypes, float* norms, void* workspace,
+                               uint64_t workspace_bytes, void* stream) {
+  try {
+    return scape::norm_and_clip(grads, true, max_norm, out, out_dtypes, norms, workspace, workspace_bytes, stream);
+  } catch (...) {
+    return scape::fail(SCAPE_ENOMEM, "host allocation failed");
+  }
+}

@@ -27,7 +27,10 @@ EXPORTS = ("scape_create", "scape_create_ex", "scape_step", "scape_step_host", "
            "scape_info", "scape_read_state", "scape_load_state", "scape_read_sparse",
            "scape_last_error", "scape_profile", "scape_profile_read", "scape_step_noalloc",
            "scape_dense_adams_step", "scape_mask_stats", "scape_unpack", "scape_topk_logits",
-           "scape_distill_loss", "scape_route_workspace", "scape_route", "scape_route_backward")
+           "scape_distill_loss", "scape_route_workspace", "scape_route", "scape_route_backward",
+           "scape_expert_plan_sizes", "scape_expert_plan", "scape_expert_dispatch",
+           "scape_expert_combine", "scape_expert_combine_backward", "scape_grad_workspace",
+           "scape_grad_norm", "scape_clip_grads")
 
 
 class ScapeError(RuntimeError):
@@ -86,6 +89,13 @@ class RouteArgs(ctypes.Structure):
                 ("valid", ctypes.c_void_p)]
 
 
+class GradsArgs(ctypes.Structure):
+    """scape_grads: the tensors of scape_grad_norm and scape_clip_grads."""
+    _fields_ = [("grads", ctypes.c_void_p), ("numel", ctypes.c_void_p), ("dtypes", ctypes.c_void_p),
+                ("n_tensors", ctypes.c_uint32), ("n_groups", ctypes.c_uint32),
+                ("first_tensor", ctypes.c_void_p)]
+
+
 _lib = None
 _libs: dict = {}
 
@@ -135,6 +145,17 @@ def load_library(path: str = LIB_PATH):
     lib.scape_route_workspace.argtypes = [rp, ctypes.POINTER(u64)]
     lib.scape_route.argtypes = [rp, vp, vp, vp, vp, vp, vp, u64, vp]
     lib.scape_route_backward.argtypes = [rp, vp, vp, vp, vp, vp, vp, u64, vp]
+    pu64 = ctypes.POINTER(u64)
+    lib.scape_expert_plan_sizes.argtypes = [u64, i32, i32, i32, pu64, pu64]
+    lib.scape_expert_plan.argtypes = [vp, u64, i32, i32, i32, vp, vp, vp, vp, vp, u64, vp]
+    lib.scape_expert_dispatch.argtypes = [vp, i32, u64, u64, u64, i32, vp, vp, u64, vp, vp]
+    lib.scape_expert_combine.argtypes = [vp, i32, u64, u64, vp, vp, u64, i32, vp, vp]
+    lib.scape_expert_combine_backward.argtypes = [vp, vp, i32, u64, u64, vp, vp, vp, u64, i32, vp,
+                                                  vp, vp]
+    gp = ctypes.POINTER(GradsArgs)
+    lib.scape_grad_workspace.argtypes = [gp, pu64]
+    lib.scape_grad_norm.argtypes = [gp, vp, vp, u64, vp]
+    lib.scape_clip_grads.argtypes = [gp, f32, vp, vp, vp, vp, u64, vp]
     _libs[path] = lib
     if path == LIB_PATH:
         _lib = lib
