@@ -486,6 +486,56 @@ int scape_route_backward(const scape_route_args* args, const int32_t* idx, const
                          const int32_t* live, const float* d_weights, const float* d_losses,
                          void* grad, uint64_t grad_stride, void* stream);
 
+/* Cross entropy of hidden states through an output matrix, for a model without a
+ * teacher: the logits l = hidden weight^T (rows x vocab) are worked out in tiles and
+ * never stored.  For a row with a label y in [0, vocab) and a weight w != 0
+ *   loss = w (log sum_v exp(l_v) - l_y)
+ * and, where d_hidden and d_weight are given, with G = w (softmax(l) - [v = y])
+ *   d_hidden = G weight   (of the row),   d_weight = sum over the rows of G^T hidden.
+ * A row with a label < 0 (by custom -100) or of weight 0 is not read: its loss and
+ * gradient are 0 whatever it holds.  A label >= vocab is treated as < 0 and counted
+ * into *bad_count (weight 0: not counted).  row_weight carries what comes from above
+ * (a mean's 1/rows, padding, a loss scale).
+ *
+ * hidden and weight have one type, bf16 or fp16, and so have their gradients.
+ * Products are of 16-bit operands added up in fp32; statistics and losses are fp32.
+ * G is rounded to the operands' type (for fp16 after scaling the weights by a power
+ * of two, so that its entries keep their precision down to 2^-28 of the largest
+ * weight), each gradient once more.  dim is a multiple of 8, matrices are 16-byte
+ * aligned with strides of a multiple of 8 elements.  The kernels' waits are bounded:
+ * one that ran out (which says that the GPU or the library is at fault) makes all
+ * losses NaN. */
+typedef struct {
+  const void* hidden; /* rows x dim, hidden_stride elements apart */
+  const void* weight; /* vocab x dim, weight_stride elements apart */
+  int dtype;          /* SCAPE_BF16 or SCAPE_F16 */
+  uint64_t rows;      /* < 2^24 */
+  uint64_t vocab;     /* 1 to 2^24 - 1 */
+  uint64_t dim;       /* a multiple of 8, 8 to 65536 */
+  uint64_t hidden_stride;
+  uint64_t weight_stride;
+  const int64_t* labels;   /* rows */
+  const float* row_weight; /* rows, or NULL (all 1) */
+  float* loss;             /* rows */
+  void* d_hidden;          /* rows x dim, or NULL (loss alone) */
+  uint64_t d_hidden_stride;
+  void* d_weight;          /* vocab x dim, or NULL with d_hidden */
+  uint64_t d_weight_stride;
+  uint32_t* bad_count;     /* one counter, added to, or NULL */
+} scape_linear_ce_args;
+
+/* Bytes of device workspace for these sizes (host call; of the pointers only whether
+ * d_hidden and d_weight are NULL matters): 4 bytes for every 64 logits and a copy
+ * of the hidden states, for the gradients up to 512 MB (or 512 bytes a row) for a
+ * piece of G and, where the vocabulary has several pieces or the rows are few, fp32
+ * sums of d_hidden. */
+int scape_linear_ce_workspace(const scape_linear_ce_args* args, uint64_t* bytes);
+
+/* The workspace (256-byte aligned) needs no initial value and may be used again by
+ * later work of the same stream. */
+int scape_linear_ce(const scape_linear_ce_args* args, void* workspace, uint64_t workspace_bytes,
+                    void* stream);
+
 /* ---- Experts' rows -------------------------------------------------------------
  * What lies between scape_route and the experts' matrix products: the tokens'
  * rows sorted by expert, and the experts' rows summed back.  A choice is one

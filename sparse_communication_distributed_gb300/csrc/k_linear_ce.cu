@@ -1,0 +1,847 @@
+// Softmax cross entropy of hidden states through an output matrix, without the
+// logits in memory (scape_linear_ce).
+//
+//   l_tv = h_t . W_v;  loss_t = w_t (log sum_v exp l_tv - l_{t, y_t})
+//   G_tv = w_t (exp(l_tv - lse_t) - [v = y_t]);  dH = G W;  dW = G^T H
+//
+// Four products on the tensor cores (16-bit operands, fp32 accumulators in tensor
+// memory), one kernel with four epilogues:
+//   LOSS  H W^T: the maximum and the sum of exponentials of every row of a tile, and
+//         the label's logit
+//   GRAD  the same product again, for a piece of the vocabulary: G of that piece
+//   DH    G W, added up over the pieces in fp32
+//   DW    G^T H, complete for the piece's words
+// A gradient thus costs 8 T D V operations and not 6: keeping the logits would cost
+// 2 T V bytes, keeping them exact enough for the exponential 4 T V.
+//
+// Rows without a term (no label, weight 0) are left out: the others are copied
+// together first, so that neither time nor the gradients depend on what they hold.
+//
+// G is rounded to the operands' type: its entries carry half a step of it, as the
+// results do.  Row weights are first multiplied by a power of two (2^k, by the
+// largest of them) that keeps fp16 entries clear of both ends of their range, and
+// the results by 2^-k.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+#include "objective.cuh"
+#include "scape_kernels.cuh"
+#include "tc.cuh"
+
+#define SCAPE_API extern "C" __attribute__((visibility("default")))
+
+namespace scape {
+namespace {
+
+using namespace tc;
+
+enum Job { LOSS, GRAD, DH, DW };
+
+constexpr int kM = 128, kN = 256, kK = 64;  // tile; 64 elements are one swizzled row
+constexpr int kStages = 4;
+constexpr uint32_t kBytesA = kM * kK * 2, kBytesB = kN * kK * 2;
+constexpr uint32_t kStageBytes = kBytesA + kBytesB;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpiWarps;  // copies, products, allocation, one idle; epilogue
+constexpr uint32_t kSmem = kStages * kStageBytes + 1024;
+constexpr int kGroup = 16;  // tiles of rows that walk along the other dimension together
+
+struct CeArgs {
+  // rows with a term, together
+  const int32_t* map;      // rows of the caller's: [0, live) with a term, then those without
+  const int32_t* label;
+  const float* weight;
+  float* label_logit;
+  float2* parts;           // (2 tiles of words) x cap: maximum, sum of exponentials
+  float2* stats;           // cap: maximum, log2 of the sum
+  int32_t* live;
+  float* scale;            // 2^k, 2^-k
+  uint32_t* status;        // 0, or a wait ran out
+  float* loss;             // caller's
+  int64_t rows, cap;       // caller's rows; rounded up to a multiple of 256
+  int D, V;
+  // the piece of the vocabulary
+  int v0, vn;
+  void* g;                 // cap x ldg
+  int64_t ldg;
+  // DH
+  float* acc;              // splits x cap x D
+  int splits, first, last;
+  void* d_hidden;
+  int64_t dh_stride;
+  // DW
+  void* d_weight;
+  int64_t dw_stride;
+};
+
+struct Tile {
+  int m, n, k0, k1;
+};
+
+// The order of the tiles: kGroup rows of tiles at a time, down first.
+struct Tiles {
+  int mt, nt, kb, splits;
+  __device__ __forceinline__ int count() const { return mt * nt * splits; }
+  __device__ __forceinline__ Tile at(int i) const {
+    const int s = i / (mt * nt);
+    i -= s * mt * nt;
+    const int g = i / (kGroup * nt), in = i - g * kGroup * nt;
+    const int rows = min(kGroup, mt - g * kGroup);
+    Tile t;
+    t.n = in / rows;
+    t.m = g * kGroup + in - t.n * rows;
+    t.k0 = (int)((int64_t)kb * s / splits);
+    t.k1 = (int)((int64_t)kb * (s + 1) / splits);
+    return t;
+  }
+};
+
+template <int JOB>
+__device__ __forceinline__ Tiles tiles_of(const CeArgs& a, int live) {
+  auto up = [](int x, int y) { return (x + y - 1) / y; };
+  if (JOB == LOSS || JOB == GRAD) return {up(live, kM), up(a.vn, kN), up(a.D, kK), 1};
+  if (JOB == DH) return {up(live, kM), up(a.D, kN), up(a.vn, kK), a.splits};
+  return {up(a.vn, kM), up(a.D, kN), up(live, kK), 1};
+}
+
+// 32 results of a row, columns [c, c + 32) of which those below n exist (n a multiple of 8).
+template <int DT>
+__device__ __forceinline__ void store32(void* row, int c, int n, const float (&f)[32]) {
+  using E = Elem<DT>;
+  typename E::T* p = static_cast<typename E::T*>(row) + c;
+#pragma unroll
+  for (int j = 0; j < 4; j++)
+    if (c + 8 * j < n) {
+      float g[8];
+#pragma unroll
+      for (int i = 0; i < 8; i++) g[i] = f[8 * j + i];
+      reinterpret_cast<uint4*>(p)[j] = E::pack(g);
+    }
+}
+
+// What a thread of the epilogue does with its row of a tile: 128 columns in tensor
+// memory at "tmem" ("empty": there were no products, all is 0).
+template <int JOB, int DT>
+__device__ __forceinline__ void epilogue(const CeArgs& a, const Tile& t, int live, int half, int lane_row,
+                                         uint32_t tmem, bool empty, int split) {
+  const int r = t.m * kM + lane_row;
+  const int c0 = t.n * kN + half * 128;
+  float f[32];
+  auto fetch = [&](int c) {
+    if (empty) {
+#pragma unroll
+      for (int i = 0; i < 32; i++) f[i] = 0.0f;
+    } else {
+      tmem_load32(tmem + (uint32_t)(32 * c), f);
+    }
+  };
+  if constexpr (JOB == LOSS) {
+    const int label = r < live ? a.label[r] : -1;
+    float m = neg_inf(), s = 0.0f, y = 0.0f;
+    bool mine = false;
+    for (int c = 0; c < 4; c++) {
+      fetch(c);
+      const int w0 = a.v0 + c0 + 32 * c;
+      if (w0 + 32 > a.V) {
+#pragma unroll
+        for (int i = 0; i < 32; i++)
+          if (w0 + i >= a.V) f[i] = neg_inf();
+      }
+      if ((uint32_t)(label - w0) < 32u) {
+        mine = true;
+#pragma unroll
+        for (int i = 0; i < 32; i++)
+          if (label == w0 + i) y = f[i];
+      }
+      float top = f[0];
+#pragma unroll
+      for (int i = 1; i < 32; i++) top = fmaxf(top, f[i]);
+      const float m2 = fmaxf(m, top), by = shift_of(m2);
+      s *= ex2((m - by) * kLog2e);
+      pair_t sum = pair(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2)
+        sum = add2(sum, ex2_2(mul2(add2(pair(f[i], f[i + 1]), pair(-by, -by)), pair(kLog2e, kLog2e))));
+      s += sum.x + sum.y;
+      m = m2;
+    }
+    if (r < live) {
+      a.parts[(int64_t)(t.n * 2 + half) * a.cap + r] = make_float2(m, s);
+      if (mine) a.label_logit[r] = y;
+    }
+  } else if constexpr (JOB == GRAD) {
+    const bool on = r < live;
+    const int label = on ? a.label[r] : -1;
+    const float2 st = on ? a.stats[r] : make_float2(0.0f, 0.0f);
+    const float w = on ? a.weight[r] * a.scale[0] : 0.0f;
+    for (int c = 0; c < 4; c++) {
+      fetch(c);
+      const int w0 = a.v0 + c0 + 32 * c;
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const pair_t x = add2(pair(f[i], f[i + 1]), pair(-st.x, -st.x));
+        const pair_t p = ex2_2(fma2(x, pair(kLog2e, kLog2e), pair(-st.y, -st.y)));
+        f[i] = p.x;
+        f[i + 1] = p.y;
+      }
+      if ((uint32_t)(label - w0) < 32u) {
+#pragma unroll
+        for (int i = 0; i < 32; i++)
+          if (label == w0 + i) f[i] -= 1.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; i++) f[i] *= w;
+      if (!on || w0 + 32 > a.V) {
+#pragma unroll
+        for (int i = 0; i < 32; i++)
+          if (!on || w0 + i >= a.V) f[i] = 0.0f;
+      }
+      store32<DT>(static_cast<char*>(a.g) + (int64_t)r * a.ldg * 2, c0 + 32 * c, (int)a.ldg, f);
+    }
+  } else if constexpr (JOB == DH) {
+    const float un = a.scale[1];
+    const bool on = r < live;
+    float* acc = a.acc + ((int64_t)split * a.cap + r) * a.D;
+    char* out = on && a.last ? static_cast<char*>(a.d_hidden) + (int64_t)a.map[r] * a.dh_stride * 2 : nullptr;
+    for (int c = 0; c < 4; c++) {
+      fetch(c);
+      const int d0 = c0 + 32 * c;
+      if (!on) continue;
+#pragma unroll
+      for (int j = 0; j < 32; j += 4)
+        if (d0 + j < a.D) {
+          float4* q = reinterpret_cast<float4*>(acc + d0 + j);
+          if (!a.first) {
+            const float4 o = *q;
+            f[j] += o.x; f[j + 1] += o.y; f[j + 2] += o.z; f[j + 3] += o.w;
+          }
+          if (!a.last) *q = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+        }
+      if (a.last) {
+#pragma unroll
+        for (int i = 0; i < 32; i++) f[i] *= un;
+        store32<DT>(out, d0, a.D, f);
+      }
+    }
+  } else {
+    const float un = a.scale[1];
+    const int v = a.v0 + r;
+    char* out = static_cast<char*>(a.d_weight) + (int64_t)v * a.dw_stride * 2;
+    for (int c = 0; c < 4; c++) {
+      fetch(c);
+#pragma unroll
+      for (int i = 0; i < 32; i++) f[i] *= un;
+      if (v < a.V) store32<DT>(out, c0 + 32 * c, a.D, f);
+    }
+  }
+}
+
+template <int JOB, int DT>
+__global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ CUtensorMap map_a,
+                                                       const __grid_constant__ CUtensorMap map_b,
+                                                       const CeArgs a) {
+  constexpr bool kAcrossA = JOB == DW, kAcrossB = JOB == DH || JOB == DW;
+  extern __shared__ uint8_t raw[];
+  __shared__ uint64_t bars[2 * kStages + 4];
+  __shared__ uint32_t tmem_at;
+  __shared__ volatile uint32_t gone;
+  const uint32_t buf = (smem_at(raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto full = [&](int s) { return smem_at(&bars[s]); };
+  auto free_ = [&](int s) { return smem_at(&bars[kStages + s]); };
+  auto ready = [&](int s) { return smem_at(&bars[2 * kStages + s]); };
+  auto taken = [&](int s) { return smem_at(&bars[2 * kStages + 2 + s]); };
+  if (warp == 0 && lane == 0) {
+    prefetch_map(&map_a);
+    prefetch_map(&map_b);
+    gone = 0u;
+    for (int s = 0; s < kStages; s++) {
+      bar_init(full(s), 1);
+      bar_init(free_(s), 1);
+    }
+    for (int s = 0; s < 2; s++) {
+      bar_init(ready(s), 1);
+      bar_init(taken(s), kEpiWarps);
+    }
+    bar_init_fence();
+  }
+  if (warp == 2) tmem_alloc(smem_at(&tmem_at), 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_at;
+  const int live = *a.live;
+  const Tiles tiles = tiles_of<JOB>(a, live);
+  const int n_tiles = tiles.count();
+
+  if (warp == 0 && lane == 0) {
+    int s = 0;
+    uint32_t ph = 0;
+    int issued = 0;  // copies that may still be on their way, oldest first
+    bool ok = true;
+    for (int i = blockIdx.x; ok && i < n_tiles; i += gridDim.x) {
+      const Tile t = tiles.at(i);
+      for (int k = t.k0; k < t.k1; k++) {
+        if (!(ok = bar_wait(free_(s), ph ^ 1u, &gone))) break;
+        const uint32_t sa = buf + s * kStageBytes, sb = sa + kBytesA, bar = full(s);
+        bar_expect(bar, kStageBytes);
+        if (!kAcrossA) {
+          load_box(sa, &map_a, k * kK, t.m * kM, bar);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kM / 64; j++) load_box(sa + j * 8192, &map_a, t.m * kM + 64 * j, k * kK, bar);
+        }
+        if (!kAcrossB) {
+          load_box(sb, &map_b, k * kK, a.v0 + t.n * kN, bar);
+        } else {
+          const int y = (JOB == DH ? a.v0 : 0) + k * kK;
+#pragma unroll
+          for (int j = 0; j < kN / 64; j++) load_box(sb + j * 8192, &map_b, t.n * kN + 64 * j, y, bar);
+        }
+        issued++;
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    if (!ok) {  // wait for what is still being copied here, each for a while
+      for (int j = min(issued, kStages); j > 0; j--) {
+        int q = s - j;
+        uint32_t p = ph;
+        if (q < 0) {
+          q += kStages;
+          p ^= 1u;
+        }
+        const uint64_t began = now_ns();
+        while (!bar_try(full(q), p) && now_ns() - began < kWaitNs / 100) {
+        }
+      }
+    }
+  } else if (warp == 1 && lane == 0) {
+    constexpr uint32_t kind = product_of(DT == SCAPE_BF16, kAcrossA, kAcrossB, kM, kN);
+    int s = 0, n = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; ok && i < n_tiles; i += gridDim.x, n++) {
+      const Tile t = tiles.at(i);
+      if (t.k0 >= t.k1) {
+        n--;  // nothing to multiply: no accumulator
+        continue;
+      }
+      const int acc = n & 1;
+      if (!(ok = bar_wait(taken(acc), ((n >> 1) & 1) ^ 1, &gone))) break;
+      fence_after();
+      const uint32_t d = tmem + acc * kN;
+      for (int k = t.k0; k < t.k1; k++) {
+        if (!(ok = bar_wait(full(s), ph, &gone))) break;
+        fence_after();
+        const uint32_t sa = buf + s * kStageBytes, sb = sa + kBytesA;
+        // 16 elements of K: 32 bytes along a row, or 16 rows of 128 bytes
+        const uint64_t oa = kAcrossA ? operand(sa, 8192, 1024) : operand(sa, 16, 1024);
+        const uint64_t ob = kAcrossB ? operand(sb, 8192, 1024) : operand(sb, 16, 1024);
+#pragma unroll
+        for (int j = 0; j < kK / 16; j++)
+          mma(d, oa + j * (kAcrossA ? 128 : 2), ob + j * (kAcrossB ? 128 : 2), kind, k > t.k0 || j > 0);
+        commit(free_(s));
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      if (ok) commit(ready(acc));
+    }
+  } else if (warp >= 4) {
+    const int half = (warp - 4) >> 2, quarter = warp & 3;
+    int n = 0;
+    for (int i = blockIdx.x; i < n_tiles; i += gridDim.x) {
+      const Tile t = tiles.at(i);
+      const bool empty = t.k0 >= t.k1;
+      const int acc = n & 1;
+      if (!empty) {
+        if (!bar_wait(ready(acc), (n >> 1) & 1, &gone)) break;
+        fence_after();
+      }
+      __syncwarp();
+      epilogue<JOB, DT>(a, t, live, half, quarter * 32 + lane,
+                        tmem + acc * kN + half * 128 + ((uint32_t)(quarter * 32) << 16), empty,
+                        JOB == DH ? i / (tiles.mt * tiles.nt) : 0);
+      if (!empty) {
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(taken(acc));
+        n++;
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (gone) {  // (never in a correct run) the losses say so
+    if (threadIdx.x == 0) *a.status = 1u;
+    for (int64_t i = threadIdx.x; i < a.rows; i += kThreads) a.loss[i] = __uint_as_float(0x7FFFFFFFu);
+  }
+  __syncwarp();
+  if (warp == 2) tmem_free(tmem, 512);
+}
+
+// ---- rows -------------------------------------------------------------------------
+
+struct RowsArgs {
+  const int64_t* labels;
+  const float* row_weight;
+  int64_t rows;
+  int V;
+  int32_t* map;
+  int32_t* label;
+  float* weight;
+  int32_t* live;
+  float* scale;
+  uint32_t* status;
+  float* loss;
+  uint32_t* bad;
+  float target;  // the largest weight is scaled to between target and 2 target
+};
+
+// The rows with a term in front, in their order; the others behind them, from the end.
+constexpr int kRowsPer = 8;
+__global__ __launch_bounds__(1024) void rows_with_loss(const RowsArgs a) {
+  __shared__ uint32_t scan[33];
+  __shared__ float fbuf[32];
+  const int tid = threadIdx.x;
+  int64_t n_live = 0;
+  float top = 0.0f;
+  uint32_t n_bad = 0;
+  for (int64_t base = 0; base < a.rows; base += 1024 * kRowsPer) {
+    const int64_t r0 = base + (int64_t)tid * kRowsPer;
+    int32_t y[kRowsPer];
+    float w[kRowsPer];
+    uint32_t mine = 0;
+#pragma unroll
+    for (int j = 0; j < kRowsPer; j++) {
+      y[j] = -1;
+      w[j] = 0.0f;
+      if (r0 + j < a.rows) {
+        const int64_t l = a.labels[r0 + j];
+        w[j] = a.row_weight ? a.row_weight[r0 + j] : 1.0f;
+        n_bad += l >= a.V && w[j] != 0.0f;
+        if (l >= 0 && l < a.V && w[j] != 0.0f) {
+          y[j] = (int32_t)l;
+          mine++;
+          if (fabsf(w[j]) < INFINITY) top = fmaxf(top, fabsf(w[j]));
+        }
+      }
+    }
+    uint32_t all;
+    int64_t at = n_live + block_incl_scan<1024>(mine, scan, &all) - mine;
+#pragma unroll
+    for (int j = 0; j < kRowsPer; j++) {
+      if (r0 + j >= a.rows) break;
+      if (y[j] >= 0) {
+        a.map[at] = (int32_t)(r0 + j);
+        a.label[at] = y[j];
+        a.weight[at] = w[j];
+        at++;
+      } else {
+        a.map[a.rows - 1 - (r0 + j - at)] = (int32_t)(r0 + j);  // (r0 + j - at rows without a term before it)
+        a.loss[r0 + j] = 0.0f;
+      }
+    }
+    n_live += all;
+  }
+  top = cta_max(top, fbuf);
+  __syncthreads();
+  n_bad = cta_sum(n_bad, scan);
+  if (tid == 0) {
+    *a.live = (int32_t)n_live;
+    *a.status = 0u;
+    float s = 1.0f;
+    const int e = (int)((__float_as_uint(top) >> 23) & 0xFF);  // (0: no weight or a denormal one)
+    if (e > 0) s = a.target * __uint_as_float((uint32_t)min(max(254 - e, 30), 224) << 23);
+    a.scale[0] = s;
+    a.scale[1] = 1.0f / s;
+    if (a.bad && n_bad) atomicAdd(a.bad, n_bad);
+  }
+}
+
+struct GatherArgs {
+  const char* hidden;
+  int64_t stride, bytes;  // of a row, in bytes
+  char* rows;             // cap x D
+  char* d_hidden;         // or NULL
+  int64_t dh_stride;      // bytes
+  const int32_t* map;
+  const int32_t* live;
+  int64_t n, cap;
+};
+
+// A warp a row: copies it, fills up with rows of 0, or clears the gradient of a row
+// without a term.
+__global__ __launch_bounds__(256) void gather_rows(const GatherArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (i >= a.cap) return;
+  const int64_t live = *a.live, vecs = a.bytes / 16;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4* to = reinterpret_cast<uint4*>(a.rows + i * a.bytes);
+  if (i < live) {
+    const uint4* from = reinterpret_cast<const uint4*>(a.hidden + (int64_t)a.map[i] * a.stride);
+#pragma unroll 4
+    for (int64_t v = lane; v < vecs; v += 32) to[v] = ld_row_u4(from + v);
+    return;
+  }
+  if (i < (live + 255) / 256 * 256)
+    for (int64_t v = lane; v < vecs; v += 32) to[v] = zero;
+  if (a.d_hidden && i < a.n) {
+    uint4* g = reinterpret_cast<uint4*>(a.d_hidden + (int64_t)a.map[i] * a.dh_stride);
+    for (int64_t v = lane; v < vecs; v += 32) g[v] = zero;
+  }
+}
+
+// 32 rows a CTA, their parts in 32 slices: maximum and sum of the row, and its loss.
+__global__ __launch_bounds__(1024) void row_losses(const CeArgs a, int n_parts) {
+  __shared__ float2 part[32][33];
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int live = *a.live;
+  if (blockIdx.x * 32 >= live) return;
+  const int r = blockIdx.x * 32 + lane;
+  auto join = [](float2 p, float2 q) {
+    const float m = fmaxf(p.x, q.x), by = shift_of(m);
+    return make_float2(m, p.y * ex2((p.x - by) * kLog2e) + q.y * ex2((q.x - by) * kLog2e));
+  };
+  float2 p = make_float2(neg_inf(), 0.0f);
+  if (r < live) {
+#pragma unroll 4
+    for (int i = slice; i < n_parts; i += 32) p = join(p, a.parts[(int64_t)i * a.cap + r]);
+  }
+  part[slice][lane] = p;
+  __syncthreads();
+  // a warp joins the slices of one row
+  p = part[lane][slice];
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+    p = join(p, make_float2(__shfl_xor_sync(kFull, p.x, o), __shfl_xor_sync(kFull, p.y, o)));
+  const int row = blockIdx.x * 32 + slice;
+  if (lane == 0 && row < live) {
+    a.stats[row] = make_float2(p.x, log2f(p.y));
+    const float loss = a.weight[row] * ((p.x - a.label_logit[row]) + logf(p.y));
+    a.loss[a.map[row]] = *a.status ? __uint_as_float(0x7FFFFFFFu) : loss;
+  }
+}
+
+// d_hidden of few rows, whose product was split along the vocabulary: the splits in order.
+template <int DT>
+__global__ __launch_bounds__(256) void sum_splits(const CeArgs a) {
+  const int live = *a.live, per = a.D / 8;
+  const float un = a.scale[1];
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)live * per; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / per;
+    const int d = (int)(i - r * per) * 8;
+    float f[8] = {};
+    for (int s = 0; s < a.splits; s++) {
+      const float4* q = reinterpret_cast<const float4*>(a.acc + ((int64_t)s * a.cap + r) * a.D + d);
+      const float4 x = q[0], y = q[1];
+      f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
+      f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) f[j] *= un;
+    typename Elem<DT>::T* out = static_cast<typename Elem<DT>::T*>(a.d_hidden) + (int64_t)a.map[r] * a.dh_stride + d;
+    *reinterpret_cast<uint4*>(out) = Elem<DT>::pack(f);
+  }
+}
+
+// ---- host -------------------------------------------------------------------------
+
+int fail(int code, const char* fmt, ...) {
+  char buf[256];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  set_thread_error(buf);
+  return code;
+}
+
+bool misaligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+  static std::atomic<EncodeFn> cache{nullptr};
+  EncodeFn fn = cache.load(std::memory_order_acquire);
+  if (fn) return fn;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult st{};
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &st) != cudaSuccess ||
+      st != cudaDriverEntryPointSuccess)
+    return nullptr;
+  fn = reinterpret_cast<EncodeFn>(p);
+  cache.store(fn, std::memory_order_release);
+  return fn;
+}
+
+// Rows of "cols" 16-bit elements, "ld" apart; boxes of 64 columns and "box" rows.
+bool encode(CUtensorMap* map, int dtype, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box) {
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld * 2};
+  const cuuint32_t boxes[2] = {64, box}, steps[2] = {1, 1};
+  const EncodeFn fn = encoder();
+  return fn && fn(map, dtype == SCAPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                  const_cast<void*>(base), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+uint64_t up(uint64_t x, uint64_t y) { return (x + y - 1) / y * y; }
+
+// How a call is cut, by its sizes alone.
+struct Cut {
+  uint64_t cap = 0;      // rows, rounded up
+  uint64_t piece = 0;    // words of a piece
+  uint64_t pieces = 0;
+  int splits = 1;        // of the vocabulary in DH
+  uint64_t n_parts = 0;
+};
+
+// G of a piece is kept to this size, so that a gradient needs little memory beside its
+// results.
+constexpr uint64_t kPieceBytes = 512ull << 20;
+
+Cut cut_of(const scape_linear_ce_args* q, bool grad) {
+  Cut c;
+  c.cap = std::max<uint64_t>(up(q->rows, 256), 256);
+  c.n_parts = 2 * ((q->vocab + kN - 1) / kN);
+  if (!grad) return c;
+  const uint64_t tiles = (q->vocab + kN - 1) / kN;
+  const uint64_t fit = std::max<uint64_t>(kPieceBytes / (c.cap * 2 * kN), 1);
+  c.pieces = (tiles + fit - 1) / fit;
+  c.piece = (tiles + c.pieces - 1) / c.pieces * kN;
+  c.pieces = (tiles * kN + c.piece - 1) / c.piece;
+  // few rows have few tiles of d_hidden, with a long sum each: the sum is split
+  const uint64_t dh = ((q->rows + kM - 1) / kM) * ((q->dim + kN - 1) / kN);
+  const uint64_t sms = (uint64_t)num_sms();
+  if (c.pieces == 1 && dh > 0 && 2 * dh <= sms)
+    c.splits = (int)std::min<uint64_t>(sms / dh, std::max<uint64_t>(1, c.piece / kK / 8));
+  return c;
+}
+
+struct Layout {
+  uint64_t map, label, weight, logit, parts, stats, head, rows, g, acc, bytes;
+};
+
+Layout layout_of(const scape_linear_ce_args* q, const Cut& c, bool grad) {
+  Layout l{};
+  uint64_t at = 0;
+  auto take = [&](uint64_t bytes) {
+    const uint64_t p = at;
+    at += up(bytes, 256);
+    return p;
+  };
+  l.head = take(64);
+  l.map = take(c.cap * 4);
+  l.label = take(c.cap * 4);
+  l.weight = take(c.cap * 4);
+  l.logit = take(c.cap * 4);
+  l.stats = take(c.cap * 8);
+  l.parts = take(c.n_parts * c.cap * 8);
+  l.rows = take(c.cap * q->dim * 2);
+  if (grad) {
+    l.g = take(c.cap * c.piece * 2);
+    if (c.pieces > 1 || c.splits > 1) l.acc = take((uint64_t)c.splits * c.cap * q->dim * 4);
+  }
+  l.bytes = at;
+  return l;
+}
+
+int check_sizes(const scape_linear_ce_args* q) {
+  if (!q) return fail(SCAPE_EINVAL, "args is NULL");
+  if (q->dtype != SCAPE_BF16 && q->dtype != SCAPE_F16)
+    return fail(SCAPE_EINVAL, "dtype=%d: hidden states and weights are bf16 or fp16", q->dtype);
+  if (q->rows >= (1ull << 24)) return fail(SCAPE_EINVAL, "rows must be < 2^24");
+  if (q->vocab < 1 || q->vocab >= (1ull << 24))
+    return fail(SCAPE_EINVAL, "vocab=%llu must be in [1, 2^24)", (unsigned long long)q->vocab);
+  if (q->dim < 8 || q->dim % 8 || q->dim > 65536)
+    return fail(SCAPE_EINVAL, "dim=%llu must be a multiple of 8 in [8, 65536]", (unsigned long long)q->dim);
+  if (!q->d_hidden != !q->d_weight) return fail(SCAPE_EINVAL, "d_hidden and d_weight come together");
+  return SCAPE_OK;
+}
+
+int check_matrix(const void* p, uint64_t stride, uint64_t dim, const char* name) {
+  if (stride < dim || stride % 8 || stride >= (1ull << 32))
+    return fail(SCAPE_EINVAL, "%s: the row stride must be a multiple of 8, >= dim and < 2^32", name);
+  if (misaligned(p, 16)) return fail(SCAPE_EINVAL, "%s must be 16-byte aligned", name);
+  return SCAPE_OK;
+}
+
+bool ranges_meet(const void* p, uint64_t n, const void* q, uint64_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && n && m && a < b + m && b < a + n;
+}
+
+template <int JOB, int DT>
+cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const CeArgs& a, uint64_t tiles,
+                           cudaStream_t s) {
+  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    e = cudaFuncSetAttribute(product<JOB, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  const unsigned grid = (unsigned)std::min<uint64_t>(std::max<uint64_t>(tiles, 1), (uint64_t)num_sms());
+  product<JOB, DT><<<grid, kThreads, kSmem, s>>>(ma, mb, a);
+  return cudaGetLastError();
+}
+
+template <int DT>
+int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, cudaStream_t s) {
+  const bool grad = q->d_hidden != nullptr;
+  auto tiles = [](uint64_t x, int t) { return (x + t - 1) / t; };
+  CeArgs a{};
+  a.map = reinterpret_cast<int32_t*>(ws + l.map);
+  a.label = reinterpret_cast<int32_t*>(ws + l.label);
+  a.weight = reinterpret_cast<float*>(ws + l.weight);
+  a.label_logit = reinterpret_cast<float*>(ws + l.logit);
+  a.parts = reinterpret_cast<float2*>(ws + l.parts);
+  a.stats = reinterpret_cast<float2*>(ws + l.stats);
+  a.live = reinterpret_cast<int32_t*>(ws + l.head);
+  a.scale = reinterpret_cast<float*>(ws + l.head + 8);
+  a.status = reinterpret_cast<uint32_t*>(ws + l.head + 16);
+  a.loss = q->loss;
+  a.rows = (int64_t)q->rows;
+  a.cap = (int64_t)c.cap;
+  a.D = (int)q->dim;
+  a.V = (int)q->vocab;
+  char* rows = ws + l.rows;
+
+  RowsArgs ra{};
+  ra.labels = q->labels;
+  ra.row_weight = q->row_weight;
+  ra.rows = a.rows;
+  ra.V = a.V;
+  ra.map = const_cast<int32_t*>(a.map);
+  ra.label = const_cast<int32_t*>(a.label);
+  ra.weight = const_cast<float*>(a.weight);
+  ra.live = a.live;
+  ra.scale = a.scale;
+  ra.status = a.status;
+  ra.loss = q->loss;
+  ra.bad = q->bad_count;
+  ra.target = DT == SCAPE_F16 ? 16384.0f : 1.0f;
+  rows_with_loss<<<1, 1024, 0, s>>>(ra);
+  GatherArgs ga{};
+  ga.hidden = static_cast<const char*>(q->hidden);
+  ga.stride = (int64_t)q->hidden_stride * 2;
+  ga.bytes = (int64_t)q->dim * 2;
+  ga.rows = rows;
+  ga.d_hidden = static_cast<char*>(q->d_hidden);
+  ga.dh_stride = (int64_t)q->d_hidden_stride * 2;
+  ga.map = a.map;
+  ga.live = a.live;
+  ga.n = a.rows;
+  ga.cap = a.cap;
+  gather_rows<<<(unsigned)(c.cap / 8), 256, 0, s>>>(ga);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(SCAPE_ECUDA, "gather_rows: %s", cudaGetErrorString(e));
+
+  CUtensorMap along_h, along_w, across_h, across_w, along_g, across_g;
+  bool ok = encode(&along_h, q->dtype, rows, c.cap, q->dim, q->dim, kM) &&
+            encode(&along_w, q->dtype, q->weight, q->vocab, q->dim, q->weight_stride, kN);
+  if (ok && grad)
+    ok = encode(&across_h, q->dtype, rows, c.cap, q->dim, q->dim, kK) &&
+         encode(&across_w, q->dtype, q->weight, q->vocab, q->dim, q->weight_stride, kK) &&
+         encode(&along_g, q->dtype, ws + l.g, c.cap, c.piece, c.piece, kM) &&
+         encode(&across_g, q->dtype, ws + l.g, c.cap, c.piece, c.piece, kK);
+  if (!ok) return fail(SCAPE_ECUDA, "cuTensorMapEncodeTiled failed or is missing in the driver");
+
+  a.v0 = 0;
+  a.vn = a.V;
+  e = launch_product<LOSS, DT>(along_h, along_w, a, tiles(q->rows, kM) * tiles(q->vocab, kN), s);
+  if (e != cudaSuccess) return fail(SCAPE_ECUDA, "product (loss): %s", cudaGetErrorString(e));
+  row_losses<<<(unsigned)(c.cap / 32), 1024, 0, s>>>(a, (int)c.n_parts);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(SCAPE_ECUDA, "row_losses: %s", cudaGetErrorString(e));
+  if (!grad) return SCAPE_OK;
+
+  a.g = ws + l.g;
+  a.ldg = (int64_t)c.piece;
+  a.acc = reinterpret_cast<float*>(ws + l.acc);
+  a.splits = c.splits;
+  a.d_hidden = q->d_hidden;
+  a.dh_stride = (int64_t)q->d_hidden_stride;
+  a.d_weight = q->d_weight;
+  a.dw_stride = (int64_t)q->d_weight_stride;
+  for (uint64_t p = 0; p < c.pieces; p++) {
+    a.v0 = (int)(p * c.piece);
+    a.vn = (int)std::min<uint64_t>(c.piece, q->vocab - p * c.piece);
+    a.first = p == 0;
+    a.last = p + 1 == c.pieces && c.splits == 1;
+    e = launch_product<GRAD, DT>(along_h, along_w, a, tiles(q->rows, kM) * tiles(a.vn, kN), s);
+    if (e == cudaSuccess)
+      e = launch_product<DH, DT>(along_g, across_w, a, tiles(q->rows, kM) * tiles(q->dim, kN) * c.splits, s);
+    if (e == cudaSuccess)
+      e = launch_product<DW, DT>(across_g, across_h, a, tiles(a.vn, kM) * tiles(q->dim, kN), s);
+    if (e != cudaSuccess) return fail(SCAPE_ECUDA, "product (gradient): %s", cudaGetErrorString(e));
+  }
+  if (c.splits > 1) {
+    const uint64_t n = q->rows * (q->dim / 8);
+    sum_splits<DT><<<(unsigned)std::min<uint64_t>((n + 255) / 256, 8ull * num_sms()), 256, 0, s>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(SCAPE_ECUDA, "sum_splits: %s", cudaGetErrorString(e));
+  }
+  return SCAPE_OK;
+}
+
+}  // namespace
+}  // namespace scape
+
+SCAPE_API int scape_linear_ce_workspace(const scape_linear_ce_args* args, uint64_t* bytes) {
+  using namespace scape;
+  if (!bytes) return fail(SCAPE_EINVAL, "bytes is NULL");
+  *bytes = 0;
+  if (int rc = check_sizes(args)) return rc;
+  const bool grad = args->d_hidden != nullptr;
+  *bytes = layout_of(args, cut_of(args, grad), grad).bytes;
+  return SCAPE_OK;
+}
+
+SCAPE_API int scape_linear_ce(const scape_linear_ce_args* args, void* workspace, uint64_t workspace_bytes,
+                              void* stream) {
+  using namespace scape;
+  if (int rc = check_sizes(args)) return rc;
+  const bool grad = args->d_hidden != nullptr;
+  if (int rc = check_matrix(args->hidden, args->hidden_stride, args->dim, "hidden")) return rc;
+  if (int rc = check_matrix(args->weight, args->weight_stride, args->dim, "weight")) return rc;
+  if (!args->weight || (args->rows > 0 && (!args->hidden || !args->labels || !args->loss)))
+    return fail(SCAPE_EINVAL, "hidden, weight, labels and loss are required");
+  if (misaligned(args->labels, 8) || misaligned(args->row_weight, 4) || misaligned(args->loss, 4) ||
+      misaligned(args->bad_count, 4))
+    return fail(SCAPE_EINVAL, "a buffer is not aligned to its element size");
+  if (grad) {
+    if (int rc = check_matrix(args->d_hidden, args->d_hidden_stride, args->dim, "d_hidden")) return rc;
+    if (int rc = check_matrix(args->d_weight, args->d_weight_stride, args->dim, "d_weight")) return rc;
+    auto bytes = [&](uint64_t rows, uint64_t stride) { return rows ? ((rows - 1) * stride + args->dim) * 2 : 0; };
+    const uint64_t h = bytes(args->rows, args->hidden_stride), w = bytes(args->vocab, args->weight_stride);
+    const uint64_t dh = bytes(args->rows, args->d_hidden_stride), dw = bytes(args->vocab, args->d_weight_stride);
+    if (ranges_meet(args->d_hidden, dh, args->hidden, h) || ranges_meet(args->d_hidden, dh, args->weight, w) ||
+        ranges_meet(args->d_weight, dw, args->hidden, h) || ranges_meet(args->d_weight, dw, args->weight, w) ||
+        ranges_meet(args->d_hidden, dh, args->d_weight, dw))
+      return fail(SCAPE_EINVAL, "the gradients overlap each other or an input");
+  }
+  const Cut c = cut_of(args, grad);
+  const Layout l = layout_of(args, c, grad);
+  if (!workspace || misaligned(workspace, 256) || workspace_bytes < l.bytes)
+    return fail(SCAPE_EINVAL, "workspace must be %llu bytes, 256-byte aligned", (unsigned long long)l.bytes);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  return args->dtype == SCAPE_BF16 ? run<SCAPE_BF16>(args, c, l, ws, s) : run<SCAPE_F16>(args, c, l, ws, s);
+}

@@ -10,14 +10,15 @@ work enqueued on that stream has finished.  A wrong type, shape or device
 raises ``ValueError``; an error of the library raises ``ScapeError``.
 
 The calls build no autograd graph: results of inputs that require a gradient
-do not.  ``distill_loss_grad`` and ``route_backward`` are the gradients, and
+do not.  ``distill_loss_grad``, ``linear_ce_grad`` and ``route_backward`` are the gradients, and
 ``examples/distill_moe.py`` wraps them in two ``torch.autograd.Function``s.
 """
 from __future__ import annotations
 
 import ctypes
 
-from .scape import SCAPE_OK, DistillArgs, RouteArgs, ScapeError, load_library
+from .scape import (SCAPE_OK, DistillArgs, LinearCeArgs, RouteArgs, ScapeError,
+                    load_library)
 
 BF16, F16, F32 = 0, 1, 2
 
@@ -168,6 +169,59 @@ def distill_loss_grad(logits, idx, vals, *, teacher_lse=None, labels=None, row_w
     gradient of each row's loss)."""
     return _distill(logits, idx, vals, teacher_lse, labels, row_weight, temperature, kd_weight,
                     ce_weight, bad_count, True, grad, stream)
+
+
+def _linear_ce(hidden, weight, labels, row_weight, bad_count, with_grad, stream):
+    if _lib is None:
+        _load()
+    if stream is not None:
+        with _stream_context(stream):
+            return _linear_ce(hidden, weight, labels, row_weight, bad_count, with_grad, None)
+    h_stride, w_stride = _rows(hidden, "hidden"), _rows(weight, "weight")
+    (rows, dim), (vocab, wdim) = hidden.shape, weight.shape
+    dev = hidden.device
+    if wdim != dim or weight.dtype != hidden.dtype:
+        raise ValueError(f"weight must be of {hidden.dtype} with {dim} columns, not {weight.dtype} of shape "
+                         f"{tuple(weight.shape)}")
+    code = _code(hidden, "hidden")
+    if labels is None:
+        raise ValueError("labels are required")
+    f32 = (torch.float32,)
+    p_lab = _arg(labels, "labels", (torch.int64,), (rows,), dev)
+    p_w = _arg(row_weight, "row_weight", f32, (rows,), dev)
+    p_bad = _arg(bad_count, "bad_count", (torch.int32,), (1,), dev)
+    loss = torch.empty(rows, dtype=torch.float32, device=dev)
+    d_hidden = d_weight = None
+    args = LinearCeArgs(hidden.data_ptr(), weight.data_ptr(), code, rows, vocab, dim,
+                        dim if rows == 1 else h_stride, dim if vocab == 1 else w_stride, p_lab, p_w,
+                        loss.data_ptr(), None, dim, None, dim, p_bad)
+    if with_grad:
+        d_hidden = torch.empty((rows, dim), dtype=hidden.dtype, device=dev)
+        d_weight = torch.empty((vocab, dim), dtype=hidden.dtype, device=dev)
+        # (a tensor of no rows has no address)
+        args.d_hidden, args.d_weight = d_hidden.data_ptr() or d_weight.data_ptr(), d_weight.data_ptr()
+    ref = ctypes.byref(args)
+    need = ctypes.c_uint64()
+    _check(_lib.scape_linear_ce_workspace(ref, ctypes.byref(need)))
+    ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    _check(_lib.scape_linear_ce(ref, ws.data_ptr(), need.value,
+                                torch._C._cuda_getCurrentRawStream(dev.index)))
+    return loss, d_hidden, d_weight
+
+
+def linear_ce(hidden, weight, labels, *, row_weight=None, bad_count=None, stream=None):
+    """scape_linear_ce without gradients: the cross entropy (float32 [rows]) of
+    the logits ``hidden @ weight.T``, which are not stored.  ``hidden`` [rows,
+    dim] and ``weight`` [vocab, dim] are bf16 or fp16, ``labels`` int64 [rows]
+    (negative: no loss)."""
+    return _linear_ce(hidden, weight, labels, row_weight, bad_count, False, stream)[0]
+
+
+def linear_ce_grad(hidden, weight, labels, *, row_weight=None, bad_count=None, stream=None):
+    """scape_linear_ce: (loss [rows], gradients of ``hidden`` and ``weight`` in
+    their type).  ``row_weight`` carries what comes from above (a mean's 1/rows,
+    padding, a loss scale)."""
+    return _linear_ce(hidden, weight, labels, row_weight, bad_count, True, stream)
 
 
 def _route_args(logits, k, renormalize, cu_tokens, valid):

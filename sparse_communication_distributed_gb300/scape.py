@@ -28,7 +28,7 @@ EXPORTS = ("scape_create", "scape_create_ex", "scape_step", "scape_step_host", "
            "scape_last_error", "scape_profile", "scape_profile_read", "scape_step_noalloc",
            "scape_dense_adams_step", "scape_mask_stats", "scape_unpack", "scape_topk_logits",
            "scape_distill_loss", "scape_route_workspace", "scape_route", "scape_route_backward",
-           "scape_expert_plan_sizes", "scape_expert_plan", "scape_expert_dispatch",
+           "scape_linear_ce_workspace", "scape_linear_ce", "scape_expert_plan_sizes", "scape_expert_plan", "scape_expert_dispatch",
            "scape_expert_combine", "scape_expert_combine_backward", "scape_grad_workspace",
            "scape_grad_norm", "scape_clip_grads")
 
@@ -89,6 +89,17 @@ class RouteArgs(ctypes.Structure):
                 ("valid", ctypes.c_void_p)]
 
 
+class LinearCeArgs(ctypes.Structure):
+    """scape_linear_ce_args: arguments of scape_linear_ce."""
+    _fields_ = [("hidden", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("rows", ctypes.c_uint64), ("vocab", ctypes.c_uint64), ("dim", ctypes.c_uint64),
+                ("hidden_stride", ctypes.c_uint64), ("weight_stride", ctypes.c_uint64),
+                ("labels", ctypes.c_void_p), ("row_weight", ctypes.c_void_p),
+                ("loss", ctypes.c_void_p), ("d_hidden", ctypes.c_void_p),
+                ("d_hidden_stride", ctypes.c_uint64), ("d_weight", ctypes.c_void_p),
+                ("d_weight_stride", ctypes.c_uint64), ("bad_count", ctypes.c_void_p)]
+
+
 class GradsArgs(ctypes.Structure):
     """scape_grads: the tensors of scape_grad_norm and scape_clip_grads."""
     _fields_ = [("grads", ctypes.c_void_p), ("numel", ctypes.c_void_p), ("dtypes", ctypes.c_void_p),
@@ -146,6 +157,9 @@ def load_library(path: str = LIB_PATH):
     lib.scape_route.argtypes = [rp, vp, vp, vp, vp, vp, vp, u64, vp]
     lib.scape_route_backward.argtypes = [rp, vp, vp, vp, vp, vp, vp, u64, vp]
     pu64 = ctypes.POINTER(u64)
+    cp = ctypes.POINTER(LinearCeArgs)
+    lib.scape_linear_ce_workspace.argtypes = [cp, pu64]
+    lib.scape_linear_ce.argtypes = [cp, vp, u64, vp]
     lib.scape_expert_plan_sizes.argtypes = [u64, i32, i32, i32, pu64, pu64]
     lib.scape_expert_plan.argtypes = [vp, u64, i32, i32, i32, vp, vp, vp, vp, vp, u64, vp]
     lib.scape_expert_dispatch.argtypes = [vp, i32, u64, u64, u64, i32, vp, vp, u64, vp, vp]
