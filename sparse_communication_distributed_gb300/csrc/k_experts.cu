@@ -285,9 +285,12 @@ __global__ __launch_bounds__(kThreads) void dispatch_rows(const RowArgs a) {
   }
 }
 
-// out[t] = sum over j of w_tj y[slot_tj], in this order, rounded once.
+// out[t] = sum over j of w_tj y[slot_tj], in this order, rounded once.  The loads of
+// kAhead choices are under way together: with those of one alone (64 bytes a lane) 605 MB
+// took 138 us.
+constexpr int kAhead = 4;
 template <int DT, int BYTES, int R>
-__global__ __launch_bounds__(kThreads) void combine_rows(const RowArgs a) {
+__global__ __launch_bounds__(kThreads, 4) void combine_rows(const RowArgs a) {
   using P = Packed<DT, BYTES>;
   using U = typename P::U;
   const int lane = threadIdx.x & 31;
@@ -295,32 +298,37 @@ __global__ __launch_bounds__(kThreads) void combine_rows(const RowArgs a) {
   if (item >= a.row_warps) return;
   const int64_t t = item / a.slices, u0 = (item % a.slices) * (32 * R) + lane, units = a.bytes / BYTES;
   int slot = -1;
-  float w = 1.0f;
+  float w = 0.0f;
   if (lane < a.k) {
     slot = a.slots[t * a.k + lane];
     if (slot >= a.rows) slot = -1;
-    if (a.weights) w = a.weights[t * a.k + lane];
+    if (slot >= 0) w = a.weights ? a.weights[t * a.k + lane] : 1.0f;
   }
   float acc[R][P::N];
 #pragma unroll
   for (int i = 0; i < R; i++)
 #pragma unroll
     for (int e = 0; e < P::N; e++) acc[i][e] = 0.0f;
-#pragma unroll 2
-  for (int j = 0; j < a.k; j++) {
-    const int s = __shfl_sync(kFull, slot, j);
-    const float wj = __shfl_sync(kFull, w, j);
-    if (s < 0) continue;
-    const U* y = reinterpret_cast<const U*>(a.x + s * a.bytes);
-    U v[R];
+  for (int j0 = 0; j0 < a.k; j0 += kAhead) {
+    U v[kAhead][R];
 #pragma unroll
-    for (int i = 0; i < R; i++) v[i] = u0 + i * 32 < units ? y[u0 + i * 32] : zero_unit<BYTES>();
+    for (int j = 0; j < kAhead; j++) {
+      const int s = __shfl_sync(kFull, slot, (j0 + j) & 31);
+      const bool on = s >= 0 && j0 + j < a.k;
+      const U* y = reinterpret_cast<const U*>(a.x + (on ? s : 0) * a.bytes);
 #pragma unroll
-    for (int i = 0; i < R; i++) {
-      float f[P::N];
-      P::unpack(v[i], f);
+      for (int i = 0; i < R; i++) v[j][i] = on && u0 + i * 32 < units ? y[u0 + i * 32] : zero_unit<BYTES>();
+    }
 #pragma unroll
-      for (int e = 0; e < P::N; e++) acc[i][e] = __fmaf_rn(wj, f[e], acc[i][e]);
+    for (int j = 0; j < kAhead; j++) {
+      const float wj = __shfl_sync(kFull, w, (j0 + j) & 31);  // (no choice: 0 times 0)
+#pragma unroll
+      for (int i = 0; i < R; i++) {
+        float f[P::N];
+        P::unpack(v[j][i], f);
+#pragma unroll
+        for (int e = 0; e < P::N; e++) acc[i][e] = __fmaf_rn(wj, f[e], acc[i][e]);
+      }
     }
   }
   U* out = reinterpret_cast<U*>(a.out + t * a.bytes);
@@ -427,7 +435,8 @@ int unit_of(int dtype, uint64_t bytes, std::initializer_list<uintptr_t> at) {
   return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : (int)size_of(dtype);
 }
 
-constexpr int kUnits16 = 4, kUnitsSmall = 8;  // units a lane has in flight
+constexpr int kUnits16 = 4, kUnitsSmall = 8;       // units of a row that a lane has in flight
+constexpr int kCombine16 = 2, kCombineSmall = 4;  // ... of each choice, where several are
 
 int check_rows(int dtype, uint64_t tokens, int k, uint64_t rows, uint64_t dim) {
   if (dtype < SCAPE_BF16 || dtype > SCAPE_F32) return fail(SCAPE_EINVAL, "unknown dtype %d", dtype);
@@ -438,12 +447,12 @@ int check_rows(int dtype, uint64_t tokens, int k, uint64_t rows, uint64_t dim) {
   return SCAPE_OK;
 }
 
-void fill(RowArgs& a, int dtype, uint64_t tokens, int k, uint64_t rows, uint64_t dim, int unit) {
+void fill(RowArgs& a, int dtype, uint64_t tokens, int k, uint64_t rows, uint64_t dim, int unit, int units) {
   a.bytes = (int64_t)(dim * size_of(dtype));
   a.tokens = (int64_t)tokens;
   a.rows = (int64_t)rows;
   a.k = k;
-  const int64_t part = 32 * (int64_t)unit * (unit == 16 ? kUnits16 : kUnitsSmall);
+  const int64_t part = 32 * (int64_t)unit * units;
   a.slices = (int)((a.bytes + part - 1) / part);
 }
 
@@ -530,7 +539,7 @@ SCAPE_API int scape_expert_dispatch(const void* x, int dtype, uint64_t tokens, u
     return fail(SCAPE_EINVAL, "out must not overlap x");
   RowArgs a{};
   const int unit = unit_of(dtype, dim * es, {row_stride * es, reinterpret_cast<uintptr_t>(x), reinterpret_cast<uintptr_t>(out)});
-  fill(a, dtype, tokens, k, rows, dim, unit);
+  fill(a, dtype, tokens, k, rows, dim, unit, unit == 16 ? kUnits16 : kUnitsSmall);
   a.x = static_cast<const char*>(x);
   a.out = static_cast<char*>(out);
   a.stride = (int64_t)(row_stride * es);
@@ -553,13 +562,13 @@ template <int DT>
 void launch_combine(const RowArgs& a, int unit, unsigned grid, bool back, cudaStream_t s) {
   if (unit == 16) {
     if (back) combine_grad<DT, 16, kUnits16><<<grid, kThreads, 0, s>>>(a);
-    else combine_rows<DT, 16, kUnits16><<<grid, kThreads, 0, s>>>(a);
+    else combine_rows<DT, 16, kCombine16><<<grid, kThreads, 0, s>>>(a);
   } else if (unit == 4) {
     if (back) combine_grad<DT, 4, kUnitsSmall><<<grid, kThreads, 0, s>>>(a);
-    else combine_rows<DT, 4, kUnitsSmall><<<grid, kThreads, 0, s>>>(a);
+    else combine_rows<DT, 4, kCombineSmall><<<grid, kThreads, 0, s>>>(a);
   } else if constexpr (DT != SCAPE_F32) {
     if (back) combine_grad<DT, 2, kUnitsSmall><<<grid, kThreads, 0, s>>>(a);
-    else combine_rows<DT, 2, kUnitsSmall><<<grid, kThreads, 0, s>>>(a);
+    else combine_rows<DT, 2, kCombineSmall><<<grid, kThreads, 0, s>>>(a);
   }
 }
 void launch_combine_any(int dtype, const RowArgs& a, int unit, unsigned grid, bool back, cudaStream_t s) {
@@ -583,7 +592,7 @@ SCAPE_API int scape_expert_combine(const void* y, int dtype, uint64_t rows, uint
   if (ranges_meet(y, rows * dim * es, out, tokens * dim * es)) return fail(SCAPE_EINVAL, "out must not overlap y");
   RowArgs a{};
   const int unit = unit_of(dtype, dim * es, {reinterpret_cast<uintptr_t>(y), reinterpret_cast<uintptr_t>(out)});
-  fill(a, dtype, tokens, k, rows, dim, unit);
+  fill(a, dtype, tokens, k, rows, dim, unit, unit == 16 ? kCombine16 : kCombineSmall);
   a.x = static_cast<const char*>(y);
   a.out = static_cast<char*>(out);
   a.slots = slots;
@@ -614,7 +623,7 @@ SCAPE_API int scape_expert_combine_backward(const void* d_out, const void* y, in
   RowArgs a{};
   const int unit = unit_of(dtype, dim * es, {reinterpret_cast<uintptr_t>(y), reinterpret_cast<uintptr_t>(d_out),
                                              reinterpret_cast<uintptr_t>(d_y)});
-  fill(a, dtype, tokens, k, rows, dim, unit);
+  fill(a, dtype, tokens, k, rows, dim, unit, unit == 16 ? kUnits16 : kUnitsSmall);
   a.x = static_cast<const char*>(y);
   a.d_out = static_cast<const char*>(d_out);
   a.out = static_cast<char*>(d_y);

@@ -26,7 +26,8 @@ namespace scape {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 8;  // vectors that a thread has in flight
+constexpr int kResident = 4;  // CTAs of an SM: 64 registers a thread, 128 KB of loads in flight
+constexpr int kBatch = 8;     // vectors that a thread has in flight
 constexpr uint64_t kMinChunk = 4096, kMaxChunkElems = 65536;
 constexpr int kMaxGroups = kMaxW;
 
@@ -34,15 +35,17 @@ struct Tensor {
   const void* src;
   void* dst;
   uint64_t n;
-  uint32_t chunk0;  // its first chunk, counted over all tensors
-  uint32_t meta;    // type | type of dst << 2 | group << 8
+  uint32_t chunk0;  // its first chunk of this table
+  uint32_t part0;   // ... of all
+  uint32_t group;
 };
 
+// Tensors of one type (and one type of results).
 template <int CAP>
 struct Table {
   Tensor t[CAP];
   int n;
-  uint32_t end;         // chunk behind the last one
+  uint32_t chunks;
   uint32_t chunk_elems;
 };
 
@@ -56,6 +59,18 @@ __device__ __forceinline__ int tensor_of(const Table<CAP>& tb, uint32_t c) {
     else hi = mid - 1;
   }
   return lo;
+}
+
+// ... of a vector, in 64 bits.  (A call, so that the loop keeps its registers.)
+template <int DT>
+__device__ __noinline__ double squares64(const uint4 v) {
+  using E = Elem<DT>;
+  float f[E::kPerVec];
+  E::unpack(v, f);
+  double d = 0.0;
+#pragma unroll
+  for (int j = 0; j < E::kPerVec; j++) d += (double)f[j] * (double)f[j];
+  return d;
 }
 
 // Sum of squares of a thread's batch.  In fp32 it is right to 2^-18 as long as it
@@ -76,13 +91,8 @@ __device__ __forceinline__ double squares(const uint4 (&v)[kBatch]) {
   if (sum > 0x1p-80f && sum < 0x1p120f) return (double)sum;
   double d = 0.0;
 #pragma unroll
-  for (int i = 0; i < kBatch; i++) {
-    if ((v[i].x | v[i].y | v[i].z | v[i].w) == 0u) continue;
-    float f[E::kPerVec];
-    E::unpack(v[i], f);
-#pragma unroll
-    for (int j = 0; j < E::kPerVec; j++) d += (double)f[j] * (double)f[j];
-  }
+  for (int i = 0; i < kBatch; i++)
+    if (v[i].x | v[i].y | v[i].z | v[i].w) d += squares64<DT>(v[i]);
   return d;
 }
 
@@ -119,20 +129,16 @@ __device__ double chunk_squares(const void* base, uint64_t first, uint32_t n) {
   return d;
 }
 
-template <int CAP>
-__global__ __launch_bounds__(kThreads) void norm_chunks(const __grid_constant__ Table<CAP> tb,
-                                                        double* __restrict__ part) {
+template <int CAP, int DT>
+__global__ __launch_bounds__(kThreads, kResident) void norm_chunks(const __grid_constant__ Table<CAP> tb,
+                                                                   double* __restrict__ part) {
   __shared__ double buf[32];
-  for (uint32_t c = tb.t[0].chunk0 + blockIdx.x; c < tb.end; c += gridDim.x) {
+  for (uint32_t c = blockIdx.x; c < tb.chunks; c += gridDim.x) {
     const Tensor& t = tb.t[tensor_of(tb, c)];
     const uint64_t first = (uint64_t)(c - t.chunk0) * tb.chunk_elems;
     const uint32_t n = (uint32_t)min((uint64_t)tb.chunk_elems, t.n - first);
-    const int dt = t.meta & 3;
-    double d = dt == SCAPE_BF16  ? chunk_squares<SCAPE_BF16>(t.src, first, n)
-               : dt == SCAPE_F16 ? chunk_squares<SCAPE_F16>(t.src, first, n)
-                                 : chunk_squares<SCAPE_F32>(t.src, first, n);
-    d = cta_sum(d, buf);
-    if (threadIdx.x == 0) part[c] = d;
+    const double d = cta_sum(chunk_squares<DT>(t.src, first, n), buf);
+    if (threadIdx.x == 0) part[t.part0 + (c - t.chunk0)] = d;
   }
   grid_launch_dependents();
 }
@@ -149,6 +155,7 @@ __global__ __launch_bounds__(1024) void norm_finish(const __grid_constant__ Grou
   __shared__ double buf[32];
   grid_dependency_wait();
   double d = 0.0;
+#pragma unroll 8
   for (uint32_t c = g.chunk0[blockIdx.x] + threadIdx.x; c < g.chunk0[blockIdx.x + 1]; c += 1024)
     d += part[c];
   d = cta_sum(d, buf);
@@ -162,92 +169,98 @@ __global__ __launch_bounds__(1024) void norm_finish(const __grid_constant__ Grou
   grid_launch_dependents();
 }
 
-// Eight elements as 32-bit values.
-template <int DT>
-__device__ __forceinline__ void load8(const void* base, uint64_t at, bool vec, float (&f)[8]) {
-  using E = Elem<DT>;
-  const typename E::T* p = static_cast<const typename E::T*>(base) + at;
-  if (!vec) {
-#pragma unroll
-    for (int j = 0; j < 8; j++) f[j] = E::load(p + j);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8 / E::kPerVec; i++) {
-      float g[E::kPerVec];
-      E::unpack(ld_row_u4(p + i * E::kPerVec), g);
-#pragma unroll
-      for (int j = 0; j < E::kPerVec; j++) f[i * E::kPerVec + j] = g[j];
-    }
-  }
+// A streaming store of 16 bytes: it does not push what is still to be read out of L2.
+__device__ __forceinline__ void st_stream_u4(void* p, const uint4 v) {
+  asm volatile("st.global.cs.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
 }
+
+// Eight products, stored.
 template <int DT>
-__device__ __forceinline__ void store8(void* base, uint64_t at, const float (&f)[8]) {
+__device__ __forceinline__ void store8(typename Elem<DT>::T* p, const float (&f)[8], float scale) {
   using E = Elem<DT>;
-  typename E::T* p = static_cast<typename E::T*>(base) + at;
 #pragma unroll
   for (int i = 0; i < 8 / E::kPerVec; i++) {
     float g[E::kPerVec];
 #pragma unroll
-    for (int j = 0; j < E::kPerVec; j++) g[j] = f[i * E::kPerVec + j];
-    reinterpret_cast<uint4*>(p)[i] = E::pack(g);
+    for (int j = 0; j < E::kPerVec; j++) g[j] = f[i * E::kPerVec + j] * scale;
+    st_stream_u4(p + i * E::kPerVec, E::pack(g));
   }
 }
 
-// dst = src * scale, each product rounded once.  Whole stores of 16 bytes from the
-// first boundary of dst on; loads of 16 bytes where src has its boundary there too.
+// dst = src * scale.  Whole stores of 16 bytes from the first boundary of dst on;
+// loads of 16 bytes where src has its boundary there too.
 template <int SDT, int DDT>
-__device__ void scale_chunk(const Tensor& t, uint64_t first, uint32_t n, float scale) {
+__device__ __forceinline__ void scale_chunk(const void* from, void* to, uint32_t n, float scale) {
   using S = Elem<SDT>;
   using D = Elem<DDT>;
-  const typename S::T* src = static_cast<const typename S::T*>(t.src) + first;
-  typename D::T* dst = static_cast<typename D::T*>(t.dst) + first;
+  const typename S::T* src = static_cast<const typename S::T*>(from);
+  typename D::T* dst = static_cast<typename D::T*>(to);
   const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(dst) & 15u) / sizeof(typename D::T);
   const uint32_t head = min(n, off ? (uint32_t)D::kPerVec - off : 0u);
   const uint32_t n8 = (n - head) / 8, done = head + n8 * 8;
-  const bool vec = (reinterpret_cast<uintptr_t>(src + head) & 15u) == 0;
-  constexpr int U = 4;
   const uint32_t tid = threadIdx.x;
   if (tid < head) dst[tid] = D::make(S::load(src + tid) * scale);
   if (done + tid < n) dst[done + tid] = D::make(S::load(src + done + tid) * scale);
-  for (uint32_t v0 = tid; v0 < n8; v0 += kThreads * U) {
-    float f[U][8];
+  src += head;
+  dst += head;
+  if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
+    constexpr int V = 8 / S::kPerVec, U = 4 / V * 2;  // 128 bytes of a thread in flight
+#pragma unroll 1
+    for (uint32_t v0 = tid; v0 < n8; v0 += kThreads * U) {
+      uint4 raw[U][V];
 #pragma unroll
-    for (int i = 0; i < U; i++)
-      if (v0 + i * kThreads < n8) load8<SDT>(src, head + (uint64_t)(v0 + i * kThreads) * 8, vec, f[i]);
+      for (int i = 0; i < U; i++)
+        if (v0 + i * kThreads < n8) {
 #pragma unroll
-    for (int i = 0; i < U; i++)
-      if (v0 + i * kThreads < n8) {
+          for (int j = 0; j < V; j++)
+            raw[i][j] = ld_row_u4(src + (size_t)(v0 + i * kThreads) * 8 + j * S::kPerVec);
+        }
 #pragma unroll
-        for (int j = 0; j < 8; j++) f[i][j] *= scale;
-        store8<DDT>(dst, head + (uint64_t)(v0 + i * kThreads) * 8, f[i]);
-      }
+      for (int i = 0; i < U; i++)
+        if (v0 + i * kThreads < n8) {
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < V; j++) {
+            float g[S::kPerVec];
+            S::unpack(raw[i][j], g);
+#pragma unroll
+            for (int e = 0; e < S::kPerVec; e++) f[j * S::kPerVec + e] = g[e];
+          }
+          store8<DDT>(dst + (size_t)(v0 + i * kThreads) * 8, f, scale);
+        }
+    }
+  } else {
+#pragma unroll 1
+    for (uint32_t v0 = tid; v0 < n8; v0 += kThreads * 2) {
+      float f[2][8];
+#pragma unroll
+      for (int i = 0; i < 2; i++)
+        if (v0 + i * kThreads < n8) {
+#pragma unroll
+          for (int e = 0; e < 8; e++) f[i][e] = S::load(src + (size_t)(v0 + i * kThreads) * 8 + e);
+        }
+#pragma unroll
+      for (int i = 0; i < 2; i++)
+        if (v0 + i * kThreads < n8) store8<DDT>(dst + (size_t)(v0 + i * kThreads) * 8, f[i], scale);
+    }
   }
 }
 
-template <int SDT>
-__device__ void scale_from(const Tensor& t, uint64_t first, uint32_t n, float scale) {
-  const int dt = (t.meta >> 2) & 3;
-  if (dt == SCAPE_BF16) scale_chunk<SDT, SCAPE_BF16>(t, first, n, scale);
-  else if (dt == SCAPE_F16) scale_chunk<SDT, SCAPE_F16>(t, first, n, scale);
-  else scale_chunk<SDT, SCAPE_F32>(t, first, n, scale);
-}
-
-template <int CAP>
-__global__ __launch_bounds__(kThreads) void clip_chunks(const __grid_constant__ Table<CAP> tb,
-                                                        const float* __restrict__ scales) {
+// A kernel for each pair of types: all of them in one take 255 registers, one CTA an SM.
+template <int CAP, int SDT, int DDT>
+__global__ __launch_bounds__(kThreads, kResident) void clip_chunks(const __grid_constant__ Table<CAP> tb,
+                                                                   const float* __restrict__ scales) {
   grid_dependency_wait();
-  const uint32_t begin = tb.t[0].chunk0;
-  for (uint32_t i = begin + blockIdx.x; i < tb.end; i += gridDim.x) {
-    const uint32_t c = begin + (tb.end - 1 - i);  // what was read last comes first
+  for (uint32_t i = blockIdx.x; i < tb.chunks; i += gridDim.x) {
+    const uint32_t c = tb.chunks - 1 - i;  // what was read last comes first
     const Tensor& t = tb.t[tensor_of(tb, c)];
-    const float scale = scales[t.meta >> 8];
+    const float scale = scales[t.group];
+    if (scale == 1.0f && t.src == t.dst) continue;  // in place: nothing to change
     const uint64_t first = (uint64_t)(c - t.chunk0) * tb.chunk_elems;
     const uint32_t n = (uint32_t)min((uint64_t)tb.chunk_elems, t.n - first);
-    const int dt = t.meta & 3;
-    if (scale == 1.0f && t.src == t.dst) continue;  // in place: nothing to change
-    if (dt == SCAPE_BF16) scale_from<SCAPE_BF16>(t, first, n, scale);
-    else if (dt == SCAPE_F16) scale_from<SCAPE_F16>(t, first, n, scale);
-    else scale_from<SCAPE_F32>(t, first, n, scale);
+    scale_chunk<SDT, DDT>(static_cast<const typename Elem<SDT>::T*>(t.src) + first,
+                          static_cast<typename Elem<DDT>::T*>(t.dst) + first, n, scale);
   }
 }
 
@@ -290,8 +303,8 @@ int check_sizes(const scape_grads* g, Cut& cut) {
     total += g->numel[i];
   }
   if (total >= (1ull << 44)) return fail(SCAPE_EINVAL, "the gradients must have < 2^44 elements");
-  // chunks large enough that few partials are left, and two a resident CTA where there is enough for that
-  const uint64_t want = 2ull * 8 * (uint64_t)num_sms();
+  // chunks large enough that few partials are left, and two of them for every SM where there is enough for that
+  const uint64_t want = 2ull * (uint64_t)num_sms();
   while (cut.chunk_elems < kMaxChunkElems && total / (2 * cut.chunk_elems) >= want) cut.chunk_elems *= 2;
   for (uint32_t i = 0; i < g->n_tensors; i++)
     cut.chunks += (g->numel[i] + cut.chunk_elems - 1) / cut.chunk_elems;
@@ -360,52 +373,74 @@ cudaError_t launch_behind(K kernel, unsigned grid, unsigned block, cudaStream_t 
   return e != cudaSuccess ? e : last;
 }
 
-// Tensors [i0, i1) into a table, and its launch.
-template <int CAP>
-cudaError_t launch_table(const scape_grads* g, const Cut& cut, void* const* out, const uint8_t* odt,
-                         const uint32_t* group, uint32_t i0, uint32_t i1, uint32_t chunk0, double* part,
-                         const float* scales, bool behind, cudaStream_t s) {
+// What launch_tables goes through: the tensors, and where the results go (clipping).
+struct Todo {
+  const scape_grads* g;
+  uint32_t chunk_elems;
+  const uint32_t* part0;  // of every tensor
+  const uint32_t* group;
+  void* const* out;
+  const uint8_t* out_dtypes;
+  double* part;
+  const float* scales;
+  uint32_t chunks_of(uint32_t i) const { return (uint32_t)((g->numel[i] + chunk_elems - 1) / chunk_elems); }
+};
+
+// The tensors that "list" names into one table, and its launch.
+template <int CAP, int SDT, int DDT>
+cudaError_t launch_table(const Todo& q, const std::vector<uint32_t>& list, size_t i0, size_t i1, bool behind,
+                         cudaStream_t s) {
   Table<CAP> tb;
-  tb.n = 0;
-  tb.chunk_elems = (uint32_t)cut.chunk_elems;
-  uint32_t c = chunk0;
-  for (uint32_t i = i0; i < i1; i++) {
-    if (!g->numel[i]) continue;
-    Tensor& t = tb.t[tb.n++];
-    t.src = g->grads[i];
-    t.dst = out ? out[i] : nullptr;
-    t.n = g->numel[i];
-    t.chunk0 = c;
-    t.meta = g->dtypes[i] | (odt ? odt[i] : 0u) << 2 | group[i] << 8;
-    c += (uint32_t)((g->numel[i] + cut.chunk_elems - 1) / cut.chunk_elems);
+  tb.n = (int)(i1 - i0);
+  tb.chunk_elems = q.chunk_elems;
+  tb.chunks = 0;
+  for (size_t j = i0; j < i1; j++) {
+    const uint32_t i = list[j];
+    tb.t[j - i0] = {q.g->grads[i], q.out ? q.out[i] : nullptr, q.g->numel[i], tb.chunks, q.part0[i], q.group[i]};
+    tb.chunks += q.chunks_of(i);
   }
-  tb.end = c;
-  if (!tb.n) return cudaSuccess;
-  const unsigned grid = std::min<unsigned>(c - chunk0, 8u * (unsigned)num_sms());
-  if (out) {
-    return behind ? launch_behind(clip_chunks<CAP>, grid, kThreads, s, tb, scales)
-                  : (clip_chunks<CAP><<<grid, kThreads, 0, s>>>(tb, scales), cudaGetLastError());
+  const unsigned grid = std::min<unsigned>(tb.chunks, (unsigned)(kResident * num_sms()));
+  if (!q.out) {
+    if constexpr (DDT == SCAPE_BF16) norm_chunks<CAP, SDT><<<grid, kThreads, 0, s>>>(tb, q.part);
+  } else if (behind) {
+    return launch_behind(clip_chunks<CAP, SDT, DDT>, grid, kThreads, s, tb, q.scales);
+  } else {
+    clip_chunks<CAP, SDT, DDT><<<grid, kThreads, 0, s>>>(tb, q.scales);
   }
-  norm_chunks<CAP><<<grid, kThreads, 0, s>>>(tb, part);
   return cudaGetLastError();
 }
 
-// All tensors, as many tables as they need: small calls take small parameters.
-constexpr int kSmallTable = 16, kLargeTable = 640;
-cudaError_t launch_all(const scape_grads* g, const Cut& cut, void* const* out, const uint8_t* odt,
-                       const uint32_t* group, double* part, const float* scales, cudaStream_t s) {
-  uint32_t chunk0 = 0;
-  for (uint32_t i0 = 0; i0 < g->n_tensors;) {
-    const uint32_t i1 = std::min(g->n_tensors, i0 + (uint32_t)kLargeTable);
-    const bool behind = i0 == 0;  // (only the first follows norm_finish directly)
-    const cudaError_t e =
-        i1 - i0 <= (uint32_t)kSmallTable
-            ? launch_table<kSmallTable>(g, cut, out, odt, group, i0, i1, chunk0, part, scales, behind, s)
-            : launch_table<kLargeTable>(g, cut, out, odt, group, i0, i1, chunk0, part, scales, behind, s);
+// All tensors of one type (and one type of results): as many tables as they need, small
+// parameters for small calls.
+constexpr int kSmallTable = 16, kLargeTable = 600;
+template <int SDT, int DDT>
+cudaError_t launch_tables(const Todo& q, bool& behind, cudaStream_t s) {
+  std::vector<uint32_t> list;
+  for (uint32_t i = 0; i < q.g->n_tensors; i++)
+    if (q.g->numel[i] && q.g->dtypes[i] == SDT && (!q.out || q.out_dtypes[i] == DDT)) list.push_back(i);
+  for (size_t i0 = 0; i0 < list.size(); i0 += kLargeTable) {
+    const size_t i1 = std::min(list.size(), i0 + kLargeTable);
+    const cudaError_t e = i1 - i0 <= (size_t)kSmallTable ? launch_table<kSmallTable, SDT, DDT>(q, list, i0, i1, behind, s)
+                                                         : launch_table<kLargeTable, SDT, DDT>(q, list, i0, i1, behind, s);
     if (e != cudaSuccess) return e;
-    for (; i0 < i1; i0++) chunk0 += (uint32_t)((g->numel[i0] + cut.chunk_elems - 1) / cut.chunk_elems);
+    behind = false;  // (only the first follows norm_finish directly)
   }
   return cudaSuccess;
+}
+
+template <int SDT>
+cudaError_t launch_from(const Todo& q, bool& behind, cudaStream_t s) {
+  cudaError_t e = launch_tables<SDT, SCAPE_BF16>(q, behind, s);
+  if (e == cudaSuccess && q.out) e = launch_tables<SDT, SCAPE_F16>(q, behind, s);
+  if (e == cudaSuccess && q.out) e = launch_tables<SDT, SCAPE_F32>(q, behind, s);
+  return e;
+}
+cudaError_t launch_all(const Todo& q, cudaStream_t s) {
+  bool behind = true;
+  cudaError_t e = launch_from<SCAPE_BF16>(q, behind, s);
+  if (e == cudaSuccess) e = launch_from<SCAPE_F16>(q, behind, s);
+  if (e == cudaSuccess) e = launch_from<SCAPE_F32>(q, behind, s);
+  return e;
 }
 
 uint64_t bytes_of(const Cut& cut) { return cut.chunks * 8 + kMaxGroups * 4; }
@@ -437,7 +472,10 @@ int norm_and_clip(const scape_grads* g, bool clip, float max_norm, void* const* 
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 || workspace_bytes < need)
     return fail(SCAPE_EINVAL, "workspace must be %llu bytes, 16-byte aligned", (unsigned long long)need);
 
-  std::vector<uint32_t> group(g->n_tensors, 0u);
+  double* part = static_cast<double*>(workspace);
+  float* scales = reinterpret_cast<float*>(part + cut.chunks);
+  std::vector<uint32_t> group(g->n_tensors), part0(g->n_tensors);
+  Todo q{g, (uint32_t)cut.chunk_elems, part0.data(), group.data(), nullptr, nullptr, part, scales};
   Groups gr{};
   uint32_t at = 0;
   for (uint32_t w = 0, i = 0; w < g->n_groups; w++) {
@@ -445,20 +483,21 @@ int norm_and_clip(const scape_grads* g, bool clip, float max_norm, void* const* 
     const uint32_t end = g->first_tensor ? (uint32_t)g->first_tensor[w + 1] : g->n_tensors;
     for (; i < end; i++) {
       group[i] = w;
-      at += (uint32_t)((g->numel[i] + cut.chunk_elems - 1) / cut.chunk_elems);
+      part0[i] = at;
+      at += q.chunks_of(i);
     }
     gr.chunk0[w + 1] = at;
   }
-  double* part = static_cast<double*>(workspace);
-  float* scales = reinterpret_cast<float*>(part + cut.chunks);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_all(g, cut, nullptr, nullptr, group.data(), part, nullptr, s);
+  cudaError_t e = launch_all(q, s);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "norm_chunks: %s", cudaGetErrorString(e));
   e = launch_behind(norm_finish, g->n_groups, 1024, s, gr, (const double*)part, max_norm, norms,
                     clip ? scales : (float*)nullptr);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "norm_finish: %s", cudaGetErrorString(e));
   if (!clip) return SCAPE_OK;
-  e = launch_all(g, cut, out, odt, group.data(), part, scales, s);
+  q.out = out;
+  q.out_dtypes = odt;
+  e = launch_all(q, s);
   return e == cudaSuccess ? SCAPE_OK : fail(SCAPE_ECUDA, "clip_chunks: %s", cudaGetErrorString(e));
 }
 

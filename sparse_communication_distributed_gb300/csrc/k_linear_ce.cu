@@ -48,12 +48,14 @@ constexpr uint32_t kBytesA = kM * kK * 2, kBytesB = kN * kK * 2;
 constexpr uint32_t kStageBytes = kBytesA + kBytesB;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;  // copies, products, allocation, one idle; epilogue
-constexpr uint32_t kSmem = kStages * kStageBytes + 1024;
-constexpr int kGroup = 16;  // tiles of rows that walk along the other dimension together
+constexpr uint32_t kOutBytes = 4096;            // a warp's results on their way out: 32 rows of 128 bytes
+constexpr uint32_t kSmem = kStages * kStageBytes + kEpiWarps * kOutBytes + 1024;
+constexpr int kGroup = 16;                      // tiles of rows that walk along the other dimension together
+constexpr uint64_t kTileFloats = (uint64_t)kM * kN;
 
 struct CeArgs {
   // rows with a term, together
-  const int32_t* map;      // rows of the caller's: [0, live) with a term, then those without
+  const int32_t* map;      // their places among the caller's
   const int32_t* label;
   const float* weight;
   float* label_logit;
@@ -65,48 +67,89 @@ struct CeArgs {
   float* loss;             // caller's
   int64_t rows, cap;       // caller's rows; rounded up to a multiple of 256
   int D, V;
+  int bn;                  // words of a tile (LOSS, GRAD)
   // the piece of the vocabulary
   int v0, vn;
-  void* g;                 // cap x ldg
-  int64_t ldg;
-  // DH
-  float* acc;              // splits x cap x D
-  int splits, first, last;
+  // sums of tiles in fp32, a float4 of a row's columns 4 j to 4 j + 3 at [j][row]
+  float* acc;              // DH, over the pieces: all tiles
+  float* tail;             // DH, DW: the parts of split tiles
+  int grid;                // CTAs of DH and DW
+  int first, last;
   void* d_hidden;
   int64_t dh_stride;
-  // DW
   void* d_weight;
   int64_t dw_stride;
 };
 
-struct Tile {
+// A unit of work: a tile, or a part of its sum.
+struct Unit {
   int m, n, k0, k1;
+  int tile, part;  // part: its place among the parts, -1 for a whole tile
 };
 
-// The order of the tiles: kGroup rows of tiles at a time, down first.
-struct Tiles {
-  int mt, nt, kb, splits;
-  __device__ __forceinline__ int count() const { return mt * nt * splits; }
-  __device__ __forceinline__ Tile at(int i) const {
-    const int s = i / (mt * nt);
-    i -= s * mt * nt;
-    const int g = i / (kGroup * nt), in = i - g * kGroup * nt;
+// The order of the tiles: kGroup rows of tiles at a time, down first.  The tiles that
+// fill the last round of CTAs only in part are split along the sum, so that the round
+// is short; their parts are added up by join_parts.
+constexpr int kMaxParts = 3;  // parts, per CTA
+struct Units {
+  int mt, nt, kb;
+  int whole, split;  // tiles in front that are not split; parts of each of the others
+  __device__ __forceinline__ int count() const { return whole + (mt * nt - whole) * split; }
+  __device__ __forceinline__ void divide(int grid) {
+    const int rest = (mt * nt) % grid;
+    whole = mt * nt;
+    split = 1;
+    if (rest == 0) return;
+    float best = 0.95f;  // of a round; the parts cost a little, too
+    for (int s = 2; s <= 32 && s * rest <= kMaxParts * grid && s * 8 <= kb; s++) {
+      const float rounds = (float)((s * rest + grid - 1) / grid) / (float)s + 0.01f * s;
+      if (rounds < best) {
+        best = rounds;
+        split = s;
+      }
+    }
+    if (split > 1) whole -= rest;
+  }
+  __device__ __forceinline__ void place(int tile, Unit& u) const {
+    const int g = tile / (kGroup * nt), in = tile - g * kGroup * nt;
     const int rows = min(kGroup, mt - g * kGroup);
-    Tile t;
-    t.n = in / rows;
-    t.m = g * kGroup + in - t.n * rows;
-    t.k0 = (int)((int64_t)kb * s / splits);
-    t.k1 = (int)((int64_t)kb * (s + 1) / splits);
-    return t;
+    u.tile = tile;
+    u.n = in / rows;
+    u.m = g * kGroup + in - u.n * rows;
+  }
+  __device__ __forceinline__ Unit at(int i) const {
+    Unit u;
+    if (i < whole) {
+      place(i, u);
+      u.k0 = 0;
+      u.k1 = kb;
+      u.part = -1;
+    } else {
+      const int rest = mt * nt - whole, s = (i - whole) / rest;
+      place(whole + (i - whole) - s * rest, u);
+      u.k0 = (int)((int64_t)kb * s / split);
+      u.k1 = (int)((int64_t)kb * (s + 1) / split);
+      u.part = i - whole;
+    }
+    return u;
   }
 };
 
 template <int JOB>
-__device__ __forceinline__ Tiles tiles_of(const CeArgs& a, int live) {
+__device__ __forceinline__ Units units_of(const CeArgs& a, int live) {
   auto up = [](int x, int y) { return (x + y - 1) / y; };
-  if (JOB == LOSS || JOB == GRAD) return {up(live, kM), up(a.vn, kN), up(a.D, kK), 1};
-  if (JOB == DH) return {up(live, kM), up(a.D, kN), up(a.vn, kK), a.splits};
-  return {up(a.vn, kM), up(a.D, kN), up(live, kK), 1};
+  Units u;
+  if (JOB == LOSS || JOB == GRAD) {
+    u.mt = up(live, kM); u.nt = up(a.vn, a.bn); u.kb = up(a.D, kK);
+  } else if (JOB == DH) {
+    u.mt = up(live, kM); u.nt = up(a.D, kN); u.kb = up(a.vn, kK);
+  } else {
+    u.mt = up(a.vn, kM); u.nt = up(a.D, kN); u.kb = up(live, kK);
+  }
+  u.whole = u.mt * u.nt;
+  u.split = 1;
+  if (JOB == DH || JOB == DW) u.divide(a.grid);
+  return u;
 }
 
 // 32 results of a row, columns [c, c + 32) of which those below n exist (n a multiple of 8).
@@ -124,13 +167,25 @@ __device__ __forceinline__ void store32(void* row, int c, int n, const float (&f
     }
 }
 
-// What a thread of the epilogue does with its row of a tile: 128 columns in tensor
+// 32 results of a row into the warp's buffer, whose rows hold 64 of them in swizzled
+// vectors (as the copy engine expects them); "side" is the half.
+template <int DT>
+__device__ __forceinline__ void stage32(uint32_t out, int lane, int side, const float (&f)[32]) {
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    float g[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) g[i] = f[8 * j + i];
+    put_smem(out + lane * 128 + (uint32_t)(((side * 4 + j) ^ (lane & 7)) * 16), Elem<DT>::pack(g));
+  }
+}
+
+// What a warp of the epilogue does with its 32 rows and 128 columns of a unit, in tensor
 // memory at "tmem" ("empty": there were no products, all is 0).
 template <int JOB, int DT>
-__device__ __forceinline__ void epilogue(const CeArgs& a, const Tile& t, int live, int half, int lane_row,
-                                         uint32_t tmem, bool empty, int split) {
-  const int r = t.m * kM + lane_row;
-  const int c0 = t.n * kN + half * 128;
+__device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map_out, const Unit& u, int live, int half,
+                                         int quarter, int lane, uint32_t tmem, bool empty, uint32_t out) {
+  const int r0 = u.m * kM + quarter * 32, r = r0 + lane;
   float f[32];
   auto fetch = [&](int c) {
     if (empty) {
@@ -140,17 +195,29 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const Tile& t, int liv
       tmem_load32(tmem + (uint32_t)(32 * c), f);
     }
   };
+  // (both halves of a row are in the buffer: 64 columns go out from column x)
+  auto send = [&](int x, int y) {
+    store_fence();
+    __syncwarp();
+    if (lane == 0) store_box(map_out, x, y, out);
+  };
+  auto reuse = [&]() {
+    if (lane == 0) store_read();
+    __syncwarp();
+  };
   if constexpr (JOB == LOSS) {
     const int label = r < live ? a.label[r] : -1;
+    const int end = min(a.V, (u.n + 1) * a.bn);
     float m = neg_inf(), s = 0.0f, y = 0.0f;
     bool mine = false;
     for (int c = 0; c < 4; c++) {
+      const int w0 = u.n * a.bn + half * 128 + 32 * c;
+      if (w0 >= end) break;
       fetch(c);
-      const int w0 = a.v0 + c0 + 32 * c;
-      if (w0 + 32 > a.V) {
+      if (w0 + 32 > end) {
 #pragma unroll
         for (int i = 0; i < 32; i++)
-          if (w0 + i >= a.V) f[i] = neg_inf();
+          if (w0 + i >= end) f[i] = neg_inf();
       }
       if ((uint32_t)(label - w0) < 32u) {
         mine = true;
@@ -171,7 +238,7 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const Tile& t, int liv
       m = m2;
     }
     if (r < live) {
-      a.parts[(int64_t)(t.n * 2 + half) * a.cap + r] = make_float2(m, s);
+      a.parts[(int64_t)(u.n * 2 + half) * a.cap + r] = make_float2(m, s);
       if (mine) a.label_logit[r] = y;
     }
   } else if constexpr (JOB == GRAD) {
@@ -180,8 +247,8 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const Tile& t, int liv
     const float2 st = on ? a.stats[r] : make_float2(0.0f, 0.0f);
     const float w = on ? a.weight[r] * a.scale[0] : 0.0f;
     for (int c = 0; c < 4; c++) {
+      const int c0 = u.n * kN + half * 128 + 32 * c, w0 = a.v0 + c0;
       fetch(c);
-      const int w0 = a.v0 + c0 + 32 * c;
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
         const pair_t x = add2(pair(f[i], f[i + 1]), pair(-st.x, -st.x));
@@ -201,42 +268,49 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const Tile& t, int liv
         for (int i = 0; i < 32; i++)
           if (!on || w0 + i >= a.V) f[i] = 0.0f;
       }
-      store32<DT>(static_cast<char*>(a.g) + (int64_t)r * a.ldg * 2, c0 + 32 * c, (int)a.ldg, f);
-    }
-  } else if constexpr (JOB == DH) {
-    const float un = a.scale[1];
-    const bool on = r < live;
-    float* acc = a.acc + ((int64_t)split * a.cap + r) * a.D;
-    char* out = on && a.last ? static_cast<char*>(a.d_hidden) + (int64_t)a.map[r] * a.dh_stride * 2 : nullptr;
-    for (int c = 0; c < 4; c++) {
-      fetch(c);
-      const int d0 = c0 + 32 * c;
-      if (!on) continue;
-#pragma unroll
-      for (int j = 0; j < 32; j += 4)
-        if (d0 + j < a.D) {
-          float4* q = reinterpret_cast<float4*>(acc + d0 + j);
-          if (!a.first) {
-            const float4 o = *q;
-            f[j] += o.x; f[j + 1] += o.y; f[j + 2] += o.z; f[j + 3] += o.w;
-          }
-          if (!a.last) *q = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
-        }
-      if (a.last) {
-#pragma unroll
-        for (int i = 0; i < 32; i++) f[i] *= un;
-        store32<DT>(out, d0, a.D, f);
-      }
+      if (!(c & 1)) reuse();
+      stage32<DT>(out, lane, c & 1, f);
+      if (c & 1) send(c0 - 32, r0);
     }
   } else {
     const float un = a.scale[1];
-    const int v = a.v0 + r;
-    char* out = static_cast<char*>(a.d_weight) + (int64_t)v * a.dw_stride * 2;
+    const bool on = JOB == DH ? r < live : true;
+    // columns of the unit in fp32: a part's own place, or the sums over the pieces
+    float4* sums = reinterpret_cast<float4*>(u.part >= 0 ? a.tail + u.part * kTileFloats : a.acc + u.tile * kTileFloats) +
+                   half * 32 * kM + quarter * 32 + lane;
     for (int c = 0; c < 4; c++) {
       fetch(c);
+      const int d0 = u.n * kN + half * 128 + 32 * c;
+      if (u.part >= 0) {
 #pragma unroll
-      for (int i = 0; i < 32; i++) f[i] *= un;
-      if (v < a.V) store32<DT>(out, c0 + 32 * c, a.D, f);
+        for (int j = 0; j < 8; j++)
+          sums[(c * 8 + j) * kM] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+        continue;
+      }
+      if constexpr (JOB == DH) {
+        if (!a.first) {
+#pragma unroll
+          for (int j = 0; j < 8; j++) {
+            const float4 o = sums[(c * 8 + j) * kM];
+            f[4 * j] += o.x; f[4 * j + 1] += o.y; f[4 * j + 2] += o.z; f[4 * j + 3] += o.w;
+          }
+        }
+        if (!a.last) {
+#pragma unroll
+          for (int j = 0; j < 8; j++)
+            sums[(c * 8 + j) * kM] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+        } else if (on) {
+#pragma unroll
+          for (int i = 0; i < 32; i++) f[i] *= un;
+          store32<DT>(static_cast<char*>(a.d_hidden) + (int64_t)a.map[r] * a.dh_stride * 2, d0, a.D, f);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; i++) f[i] *= un;
+        if (!(c & 1)) reuse();
+        stage32<DT>(out, lane, c & 1, f);
+        if (c & 1) send(d0 - 32, a.v0 + r0);
+      }
     }
   }
 }
@@ -244,6 +318,7 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const Tile& t, int liv
 template <int JOB, int DT>
 __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ CUtensorMap map_a,
                                                        const __grid_constant__ CUtensorMap map_b,
+                                                       const __grid_constant__ CUtensorMap map_out,
                                                        const CeArgs a) {
   constexpr bool kAcrossA = JOB == DW, kAcrossB = JOB == DH || JOB == DW;
   extern __shared__ uint8_t raw[];
@@ -275,21 +350,24 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_at;
+  grid_launch_dependents();
+  grid_dependency_wait();
   const int live = *a.live;
-  const Tiles tiles = tiles_of<JOB>(a, live);
-  const int n_tiles = tiles.count();
+  const Units units = units_of<JOB>(a, live);
+  const int n_units = units.count();
+  const uint32_t stage_bytes = kBytesA + (JOB == LOSS || JOB == GRAD ? a.bn : kN) * kK * 2;
 
   if (warp == 0 && lane == 0) {
     int s = 0;
     uint32_t ph = 0;
     int issued = 0;  // copies that may still be on their way, oldest first
     bool ok = true;
-    for (int i = blockIdx.x; ok && i < n_tiles; i += gridDim.x) {
-      const Tile t = tiles.at(i);
+    for (int i = blockIdx.x; ok && i < n_units; i += gridDim.x) {
+      const Unit t = units.at(i);
       for (int k = t.k0; k < t.k1; k++) {
         if (!(ok = bar_wait(free_(s), ph ^ 1u, &gone))) break;
         const uint32_t sa = buf + s * kStageBytes, sb = sa + kBytesA, bar = full(s);
-        bar_expect(bar, kStageBytes);
+        bar_expect(bar, stage_bytes);
         if (!kAcrossA) {
           load_box(sa, &map_a, k * kK, t.m * kM, bar);
         } else {
@@ -297,7 +375,7 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
           for (int j = 0; j < kM / 64; j++) load_box(sa + j * 8192, &map_a, t.m * kM + 64 * j, k * kK, bar);
         }
         if (!kAcrossB) {
-          load_box(sb, &map_b, k * kK, a.v0 + t.n * kN, bar);
+          load_box(sb, &map_b, k * kK, a.v0 + t.n * a.bn, bar);
         } else {
           const int y = (JOB == DH ? a.v0 : 0) + k * kK;
 #pragma unroll
@@ -324,12 +402,12 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
       }
     }
   } else if (warp == 1 && lane == 0) {
-    constexpr uint32_t kind = product_of(DT == SCAPE_BF16, kAcrossA, kAcrossB, kM, kN);
+    const uint32_t kind = product_of(DT == SCAPE_BF16, kAcrossA, kAcrossB, kM, JOB == LOSS || JOB == GRAD ? a.bn : kN);
     int s = 0, n = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int i = blockIdx.x; ok && i < n_tiles; i += gridDim.x, n++) {
-      const Tile t = tiles.at(i);
+    for (int i = blockIdx.x; ok && i < n_units; i += gridDim.x, n++) {
+      const Unit t = units.at(i);
       if (t.k0 >= t.k1) {
         n--;  // nothing to multiply: no accumulator
         continue;
@@ -359,8 +437,9 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
   } else if (warp >= 4) {
     const int half = (warp - 4) >> 2, quarter = warp & 3;
     int n = 0;
-    for (int i = blockIdx.x; i < n_tiles; i += gridDim.x) {
-      const Tile t = tiles.at(i);
+    const uint32_t out = buf + kStages * kStageBytes + (warp - 4) * kOutBytes;
+    for (int i = blockIdx.x; i < n_units; i += gridDim.x) {
+      const Unit t = units.at(i);
       const bool empty = t.k0 >= t.k1;
       const int acc = n & 1;
       if (!empty) {
@@ -368,9 +447,8 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
         fence_after();
       }
       __syncwarp();
-      epilogue<JOB, DT>(a, t, live, half, quarter * 32 + lane,
-                        tmem + acc * kN + half * 128 + ((uint32_t)(quarter * 32) << 16), empty,
-                        JOB == DH ? i / (tiles.mt * tiles.nt) : 0);
+      epilogue<JOB, DT>(a, &map_out, t, live, half, quarter, lane,
+                        tmem + acc * kN + half * 128 + ((uint32_t)(quarter * 32) << 16), empty, out);
       if (!empty) {
         fence_before();
         __syncwarp();
@@ -378,6 +456,7 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
         n++;
       }
     }
+    if (lane == 0) store_done();
   }
   fence_before();
   __syncthreads();
@@ -395,11 +474,16 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
 struct RowsArgs {
   const int64_t* labels;
   const float* row_weight;
-  int64_t rows;
+  int64_t rows, chunk;  // chunk: rows of a CTA
   int V;
+  const char* hidden;
+  int64_t stride, bytes;  // of a row, in bytes
+  char* d_hidden;         // or NULL
+  int64_t dh_stride;      // bytes
   int32_t* map;
   int32_t* label;
   float* weight;
+  char* together;         // cap x D
   int32_t* live;
   float* scale;
   uint32_t* status;
@@ -408,98 +492,82 @@ struct RowsArgs {
   float target;  // the largest weight is scaled to between target and 2 target
 };
 
-// The rows with a term in front, in their order; the others behind them, from the end.
-constexpr int kRowsPer = 8;
-__global__ __launch_bounds__(1024) void rows_with_loss(const RowsArgs a) {
-  __shared__ uint32_t scan[33];
+// The rows with a term, together and in their order.  Each CTA takes a chunk of the
+// rows and counts those in front of it by itself: at most 512 CTAs read all labels,
+// which costs less than a second kernel.  The rows without a term get their loss and
+// gradient of 0.
+constexpr int kRowThreads = 512, kRowWarps = kRowThreads / 32, kMaxRowCtas = 512;
+__global__ __launch_bounds__(kRowThreads) void take_rows(const RowsArgs a) {
+  __shared__ uint32_t scan[kRowWarps + 1];
+  __shared__ uint32_t ubuf[32];
   __shared__ float fbuf[32];
-  const int tid = threadIdx.x;
-  int64_t n_live = 0;
+  __shared__ int64_t place[kRowThreads];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int64_t begin = blockIdx.x * a.chunk, end = min(a.rows, begin + a.chunk);
   float top = 0.0f;
-  uint32_t n_bad = 0;
-  for (int64_t base = 0; base < a.rows; base += 1024 * kRowsPer) {
-    const int64_t r0 = base + (int64_t)tid * kRowsPer;
-    int32_t y[kRowsPer];
-    float w[kRowsPer];
-    uint32_t mine = 0;
-#pragma unroll
-    for (int j = 0; j < kRowsPer; j++) {
-      y[j] = -1;
-      w[j] = 0.0f;
-      if (r0 + j < a.rows) {
-        const int64_t l = a.labels[r0 + j];
-        w[j] = a.row_weight ? a.row_weight[r0 + j] : 1.0f;
-        n_bad += l >= a.V && w[j] != 0.0f;
-        if (l >= 0 && l < a.V && w[j] != 0.0f) {
-          y[j] = (int32_t)l;
-          mine++;
-          if (fabsf(w[j]) < INFINITY) top = fmaxf(top, fabsf(w[j]));
-        }
-      }
-    }
+  auto look = [&](int64_t r, int64_t& y, float& w) {
+    y = a.labels[r];
+    w = a.row_weight ? a.row_weight[r] : 1.0f;
+    const bool on = y >= 0 && y < a.V && w != 0.0f;
+    if (on && fabsf(w) < INFINITY) top = fmaxf(top, fabsf(w));
+    return on;
+  };
+  uint32_t before = 0, n_bad = 0;
+  int64_t y;
+  float w;
+#pragma unroll 8
+  for (int64_t r = tid; r < begin; r += kRowThreads) before += look(r, y, w);
+  int64_t at = cta_sum(before, ubuf);  // (rows < 2^24)
+  grid_launch_dependents();
+  const int64_t vecs = a.bytes / 16;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int64_t r0 = begin; r0 < end; r0 += kRowThreads) {
+    const int64_t r = r0 + tid;
+    const bool in = r < end, on = in && look(r, y, w);
     uint32_t all;
-    int64_t at = n_live + block_incl_scan<1024>(mine, scan, &all) - mine;
-#pragma unroll
-    for (int j = 0; j < kRowsPer; j++) {
-      if (r0 + j >= a.rows) break;
-      if (y[j] >= 0) {
-        a.map[at] = (int32_t)(r0 + j);
-        a.label[at] = y[j];
-        a.weight[at] = w[j];
-        at++;
-      } else {
-        a.map[a.rows - 1 - (r0 + j - at)] = (int32_t)(r0 + j);  // (r0 + j - at rows without a term before it)
-        a.loss[r0 + j] = 0.0f;
+    const uint32_t rank = block_incl_scan<kRowThreads>(on, scan, &all) - on;
+    if (on) {
+      a.map[at + rank] = (int32_t)r;
+      a.label[at + rank] = (int32_t)y;
+      a.weight[at + rank] = w;
+    } else if (in) {
+      a.loss[r] = 0.0f;
+      n_bad += y >= a.V && w != 0.0f;
+    }
+    place[tid] = on ? at + rank : -1;
+    __syncthreads();
+    const int n = (int)min((int64_t)kRowThreads, end - r0);
+    for (int i = wid; i < n; i += kRowWarps) {
+      const int64_t p = place[i];
+      if (p >= 0) {
+        const uint4* from = reinterpret_cast<const uint4*>(a.hidden + (r0 + i) * a.stride);
+        uint4* to = reinterpret_cast<uint4*>(a.together + p * a.bytes);
+#pragma unroll 4
+        for (int64_t v = lane; v < vecs; v += 32) to[v] = ld_row_u4(from + v);
+      } else if (a.d_hidden) {
+        uint4* g = reinterpret_cast<uint4*>(a.d_hidden + (r0 + i) * a.dh_stride);
+        for (int64_t v = lane; v < vecs; v += 32) g[v] = zero;
       }
     }
-    n_live += all;
+    __syncthreads();
+    at += all;
   }
+  n_bad = cta_sum(n_bad, ubuf);
+  if (tid == 0 && a.bad && n_bad) atomicAdd(a.bad, n_bad);
+  if (blockIdx.x + 1 < gridDim.x) return;
+  // the last CTA has seen every row.  Rows of 0 behind the last one, to a multiple of 64:
+  // DW adds them up, too
+  for (int64_t i = at * vecs + tid; i < (at + 63) / 64 * 64 * vecs; i += kRowThreads)
+    reinterpret_cast<uint4*>(a.together)[i] = zero;
   top = cta_max(top, fbuf);
-  __syncthreads();
-  n_bad = cta_sum(n_bad, scan);
   if (tid == 0) {
-    *a.live = (int32_t)n_live;
+    *a.live = (int32_t)at;
     *a.status = 0u;
     float s = 1.0f;
     const int e = (int)((__float_as_uint(top) >> 23) & 0xFF);  // (0: no weight or a denormal one)
     if (e > 0) s = a.target * __uint_as_float((uint32_t)min(max(254 - e, 30), 224) << 23);
     a.scale[0] = s;
     a.scale[1] = 1.0f / s;
-    if (a.bad && n_bad) atomicAdd(a.bad, n_bad);
-  }
-}
-
-struct GatherArgs {
-  const char* hidden;
-  int64_t stride, bytes;  // of a row, in bytes
-  char* rows;             // cap x D
-  char* d_hidden;         // or NULL
-  int64_t dh_stride;      // bytes
-  const int32_t* map;
-  const int32_t* live;
-  int64_t n, cap;
-};
-
-// A warp a row: copies it, fills up with rows of 0, or clears the gradient of a row
-// without a term.
-__global__ __launch_bounds__(256) void gather_rows(const GatherArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (i >= a.cap) return;
-  const int64_t live = *a.live, vecs = a.bytes / 16;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  uint4* to = reinterpret_cast<uint4*>(a.rows + i * a.bytes);
-  if (i < live) {
-    const uint4* from = reinterpret_cast<const uint4*>(a.hidden + (int64_t)a.map[i] * a.stride);
-#pragma unroll 4
-    for (int64_t v = lane; v < vecs; v += 32) to[v] = ld_row_u4(from + v);
-    return;
-  }
-  if (i < (live + 255) / 256 * 256)
-    for (int64_t v = lane; v < vecs; v += 32) to[v] = zero;
-  if (a.d_hidden && i < a.n) {
-    uint4* g = reinterpret_cast<uint4*>(a.d_hidden + (int64_t)a.map[i] * a.dh_stride);
-    for (int64_t v = lane; v < vecs; v += 32) g[v] = zero;
   }
 }
 
@@ -507,6 +575,8 @@ __global__ __launch_bounds__(256) void gather_rows(const GatherArgs a) {
 __global__ __launch_bounds__(1024) void row_losses(const CeArgs a, int n_parts) {
   __shared__ float2 part[32][33];
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  grid_launch_dependents();
+  grid_dependency_wait();
   const int live = *a.live;
   if (blockIdx.x * 32 >= live) return;
   const int r = blockIdx.x * 32 + lane;
@@ -534,24 +604,46 @@ __global__ __launch_bounds__(1024) void row_losses(const CeArgs a, int n_parts) 
   }
 }
 
-// d_hidden of few rows, whose product was split along the vocabulary: the splits in order.
-template <int DT>
-__global__ __launch_bounds__(256) void sum_splits(const CeArgs a) {
-  const int live = *a.live, per = a.D / 8;
+// The parts of the split tiles of DH or DW, added up in order: a thread has eight
+// columns of a row.
+template <int JOB, int DT>
+__global__ __launch_bounds__(256) void join_parts(const CeArgs a) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int live = *a.live;
+  const Units units = units_of<JOB>(a, live);
+  const int rest = units.mt * units.nt - units.whole;
   const float un = a.scale[1];
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)live * per; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / per;
-    const int d = (int)(i - r * per) * 8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)rest * kM * (kN / 8);
+       i += (int64_t)gridDim.x * 256) {
+    const int row = (int)(i % kM), j = (int)(i / kM % (kN / 8)), t = (int)(i / (kM * (kN / 8)));
+    Unit u;
+    units.place(units.whole + t, u);
+    const int r = u.m * kM + row, d = u.n * kN + 8 * j;
     float f[8] = {};
-    for (int s = 0; s < a.splits; s++) {
-      const float4* q = reinterpret_cast<const float4*>(a.acc + ((int64_t)s * a.cap + r) * a.D + d);
-      const float4 x = q[0], y = q[1];
+    auto add = [&](const float* tile) {
+      const float4* q = reinterpret_cast<const float4*>(tile) + 2 * j * kM + row;
+      const float4 x = q[0], y = q[kM];
       f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
       f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+    };
+    for (int s = 0; s < units.split; s++) add(a.tail + (uint64_t)(s * rest + t) * kTileFloats);
+    if (JOB == DH) {
+      float* acc = a.acc + u.tile * kTileFloats;
+      if (!a.first) add(acc);
+      if (!a.last) {
+        float4* q = reinterpret_cast<float4*>(acc) + 2 * j * kM + row;
+        q[0] = make_float4(f[0], f[1], f[2], f[3]);
+        q[kM] = make_float4(f[4], f[5], f[6], f[7]);
+        continue;
+      }
     }
+    if (d >= a.D || (JOB == DH ? r >= live : a.v0 + r >= a.V)) continue;
 #pragma unroll
-    for (int j = 0; j < 8; j++) f[j] *= un;
-    typename Elem<DT>::T* out = static_cast<typename Elem<DT>::T*>(a.d_hidden) + (int64_t)a.map[r] * a.dh_stride + d;
+    for (int e = 0; e < 8; e++) f[e] *= un;
+    typename Elem<DT>::T* out =
+        JOB == DH ? static_cast<typename Elem<DT>::T*>(a.d_hidden) + (int64_t)a.map[r] * a.dh_stride + d
+                  : static_cast<typename Elem<DT>::T*>(a.d_weight) + (int64_t)(a.v0 + r) * a.dw_stride + d;
     *reinterpret_cast<uint4*>(out) = Elem<DT>::pack(f);
   }
 }
@@ -603,10 +695,10 @@ uint64_t up(uint64_t x, uint64_t y) { return (x + y - 1) / y * y; }
 
 // How a call is cut, by its sizes alone.
 struct Cut {
-  uint64_t cap = 0;      // rows, rounded up
-  uint64_t piece = 0;    // words of a piece
+  uint64_t cap = 0;     // rows, rounded up
+  uint64_t bn = kN;     // words of a tile of LOSS
+  uint64_t piece = 0;   // words of a piece
   uint64_t pieces = 0;
-  int splits = 1;        // of the vocabulary in DH
   uint64_t n_parts = 0;
 };
 
@@ -614,26 +706,36 @@ struct Cut {
 // results.
 constexpr uint64_t kPieceBytes = 512ull << 20;
 
+uint64_t ceil_div(uint64_t x, uint64_t y) { return (x + y - 1) / y; }
+
 Cut cut_of(const scape_linear_ce_args* q, bool grad) {
   Cut c;
   c.cap = std::max<uint64_t>(up(q->rows, 256), 256);
-  c.n_parts = 2 * ((q->vocab + kN - 1) / kN);
+  // Few rows: the weights' way to the CTAs is what takes time, and tiles of 256 words leave
+  // CTAs without any.  The width that needs the fewest words a CTA, all rounds together
+  // (32 for a tile's other costs).
+  if (q->rows <= kM) {
+    const uint64_t sms = (uint64_t)num_sms();
+    uint64_t best = ~0ull;
+    for (uint64_t n = kN; n >= 32; n -= 32) {
+      const uint64_t words = ceil_div(ceil_div(q->vocab, n), sms) * (n + 32);
+      if (words < best) {
+        best = words;
+        c.bn = n;
+      }
+    }
+  }
+  c.n_parts = 2 * ceil_div(q->vocab, c.bn);
   if (!grad) return c;
-  const uint64_t tiles = (q->vocab + kN - 1) / kN;
+  const uint64_t tiles = ceil_div(q->vocab, kN);
   const uint64_t fit = std::max<uint64_t>(kPieceBytes / (c.cap * 2 * kN), 1);
-  c.pieces = (tiles + fit - 1) / fit;
-  c.piece = (tiles + c.pieces - 1) / c.pieces * kN;
-  c.pieces = (tiles * kN + c.piece - 1) / c.piece;
-  // few rows have few tiles of d_hidden, with a long sum each: the sum is split
-  const uint64_t dh = ((q->rows + kM - 1) / kM) * ((q->dim + kN - 1) / kN);
-  const uint64_t sms = (uint64_t)num_sms();
-  if (c.pieces == 1 && dh > 0 && 2 * dh <= sms)
-    c.splits = (int)std::min<uint64_t>(sms / dh, std::max<uint64_t>(1, c.piece / kK / 8));
+  c.piece = ceil_div(tiles, ceil_div(tiles, fit)) * kN;
+  c.pieces = ceil_div(tiles * kN, c.piece);
   return c;
 }
 
 struct Layout {
-  uint64_t map, label, weight, logit, parts, stats, head, rows, g, acc, bytes;
+  uint64_t map, label, weight, logit, parts, stats, head, rows, g, acc, tail, bytes;
 };
 
 Layout layout_of(const scape_linear_ce_args* q, const Cut& c, bool grad) {
@@ -654,7 +756,8 @@ Layout layout_of(const scape_linear_ce_args* q, const Cut& c, bool grad) {
   l.rows = take(c.cap * q->dim * 2);
   if (grad) {
     l.g = take(c.cap * c.piece * 2);
-    if (c.pieces > 1 || c.splits > 1) l.acc = take((uint64_t)c.splits * c.cap * q->dim * 4);
+    if (c.pieces > 1) l.acc = take(c.cap / kM * ceil_div(q->dim, kN) * kTileFloats * 4);
+    l.tail = take(kMaxParts * (uint64_t)num_sms() * kTileFloats * 4);
   }
   l.bytes = at;
   return l;
@@ -685,9 +788,27 @@ bool ranges_meet(const void* p, uint64_t n, const void* q, uint64_t m) {
   return p && q && n && m && a < b + m && b < a + n;
 }
 
+// Launches behind the kernel in front of it, which it waits for on the GPU.
+template <class K, class... A>
+cudaError_t launch_behind(K kernel, unsigned grid, unsigned block, uint32_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  const cudaError_t last = cudaGetLastError();
+  return e != cudaSuccess ? e : last;
+}
+
 template <int JOB, int DT>
-cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const CeArgs& a, uint64_t tiles,
-                           cudaStream_t s) {
+cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const CeArgs& a,
+                           uint64_t tiles, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -697,15 +818,14 @@ cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const C
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
   }
-  const unsigned grid = (unsigned)std::min<uint64_t>(std::max<uint64_t>(tiles, 1), (uint64_t)num_sms());
-  product<JOB, DT><<<grid, kThreads, kSmem, s>>>(ma, mb, a);
-  return cudaGetLastError();
+  unsigned grid = (unsigned)a.grid;  // (DH and DW divide their sums by it)
+  if (JOB == LOSS || JOB == GRAD) grid = (unsigned)std::min<uint64_t>(std::max<uint64_t>(tiles, 1), grid);
+  return launch_behind(product<JOB, DT>, grid, kThreads, kSmem, s, ma, mb, mo, a);
 }
 
 template <int DT>
 int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, cudaStream_t s) {
   const bool grad = q->d_hidden != nullptr;
-  auto tiles = [](uint64_t x, int t) { return (x + t - 1) / t; };
   CeArgs a{};
   a.map = reinterpret_cast<int32_t*>(ws + l.map);
   a.label = reinterpret_cast<int32_t*>(ws + l.label);
@@ -721,82 +841,76 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
   a.cap = (int64_t)c.cap;
   a.D = (int)q->dim;
   a.V = (int)q->vocab;
+  a.grid = num_sms();
   char* rows = ws + l.rows;
+
+  CUtensorMap along_h, along_w, across_h, across_w, along_g, across_g, piece_w, out_g, out_w;
+  bool ok = encode(&along_h, q->dtype, rows, c.cap, q->dim, q->dim, kM) &&
+            encode(&along_w, q->dtype, q->weight, q->vocab, q->dim, q->weight_stride, (uint32_t)c.bn);
+  if (ok && grad)
+    ok = encode(&piece_w, q->dtype, q->weight, q->vocab, q->dim, q->weight_stride, kN) &&
+         encode(&across_h, q->dtype, rows, c.cap, q->dim, q->dim, kK) &&
+         encode(&across_w, q->dtype, q->weight, q->vocab, q->dim, q->weight_stride, kK) &&
+         encode(&along_g, q->dtype, ws + l.g, c.cap, c.piece, c.piece, kM) &&
+         encode(&across_g, q->dtype, ws + l.g, c.cap, c.piece, c.piece, kK) &&
+         encode(&out_g, q->dtype, ws + l.g, c.cap, c.piece, c.piece, 32) &&
+         encode(&out_w, q->dtype, q->d_weight, q->vocab, q->dim, q->d_weight_stride, 32);
+  if (!ok) return fail(SCAPE_ECUDA, "cuTensorMapEncodeTiled failed or is missing in the driver");
 
   RowsArgs ra{};
   ra.labels = q->labels;
   ra.row_weight = q->row_weight;
   ra.rows = a.rows;
+  const uint64_t row_ctas = std::min<uint64_t>(std::max<uint64_t>(ceil_div(q->rows, 32), 1), kMaxRowCtas);
+  ra.chunk = (int64_t)std::max<uint64_t>(ceil_div(q->rows, row_ctas), 1);
   ra.V = a.V;
+  ra.hidden = static_cast<const char*>(q->hidden);
+  ra.stride = (int64_t)q->hidden_stride * 2;
+  ra.bytes = (int64_t)q->dim * 2;
+  ra.d_hidden = static_cast<char*>(q->d_hidden);
+  ra.dh_stride = (int64_t)q->d_hidden_stride * 2;
   ra.map = const_cast<int32_t*>(a.map);
   ra.label = const_cast<int32_t*>(a.label);
   ra.weight = const_cast<float*>(a.weight);
+  ra.together = rows;
   ra.live = a.live;
   ra.scale = a.scale;
   ra.status = a.status;
   ra.loss = q->loss;
   ra.bad = q->bad_count;
   ra.target = DT == SCAPE_F16 ? 16384.0f : 1.0f;
-  rows_with_loss<<<1, 1024, 0, s>>>(ra);
-  GatherArgs ga{};
-  ga.hidden = static_cast<const char*>(q->hidden);
-  ga.stride = (int64_t)q->hidden_stride * 2;
-  ga.bytes = (int64_t)q->dim * 2;
-  ga.rows = rows;
-  ga.d_hidden = static_cast<char*>(q->d_hidden);
-  ga.dh_stride = (int64_t)q->d_hidden_stride * 2;
-  ga.map = a.map;
-  ga.live = a.live;
-  ga.n = a.rows;
-  ga.cap = a.cap;
-  gather_rows<<<(unsigned)(c.cap / 8), 256, 0, s>>>(ga);
+  take_rows<<<(unsigned)std::max<uint64_t>(ceil_div(q->rows, (uint64_t)ra.chunk), 1), kRowThreads, 0, s>>>(ra);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(SCAPE_ECUDA, "gather_rows: %s", cudaGetErrorString(e));
-
-  CUtensorMap along_h, along_w, across_h, across_w, along_g, across_g;
-  bool ok = encode(&along_h, q->dtype, rows, c.cap, q->dim, q->dim, kM) &&
-            encode(&along_w, q->dtype, q->weight, q->vocab, q->dim, q->weight_stride, kN);
-  if (ok && grad)
-    ok = encode(&across_h, q->dtype, rows, c.cap, q->dim, q->dim, kK) &&
-         encode(&across_w, q->dtype, q->weight, q->vocab, q->dim, q->weight_stride, kK) &&
-         encode(&along_g, q->dtype, ws + l.g, c.cap, c.piece, c.piece, kM) &&
-         encode(&across_g, q->dtype, ws + l.g, c.cap, c.piece, c.piece, kK);
-  if (!ok) return fail(SCAPE_ECUDA, "cuTensorMapEncodeTiled failed or is missing in the driver");
+  if (e != cudaSuccess) return fail(SCAPE_ECUDA, "take_rows: %s", cudaGetErrorString(e));
 
   a.v0 = 0;
   a.vn = a.V;
-  e = launch_product<LOSS, DT>(along_h, along_w, a, tiles(q->rows, kM) * tiles(q->vocab, kN), s);
+  a.bn = (int)c.bn;
+  e = launch_product<LOSS, DT>(along_h, along_w, along_w, a, ceil_div(q->rows, kM) * ceil_div(q->vocab, c.bn), s);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "product (loss): %s", cudaGetErrorString(e));
-  row_losses<<<(unsigned)(c.cap / 32), 1024, 0, s>>>(a, (int)c.n_parts);
-  e = cudaGetLastError();
+  e = launch_behind(row_losses, (unsigned)(c.cap / 32), 1024, 0, s, a, (int)c.n_parts);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "row_losses: %s", cudaGetErrorString(e));
   if (!grad) return SCAPE_OK;
 
-  a.g = ws + l.g;
-  a.ldg = (int64_t)c.piece;
+  a.bn = kN;
   a.acc = reinterpret_cast<float*>(ws + l.acc);
-  a.splits = c.splits;
+  a.tail = reinterpret_cast<float*>(ws + l.tail);
   a.d_hidden = q->d_hidden;
   a.dh_stride = (int64_t)q->d_hidden_stride;
   a.d_weight = q->d_weight;
   a.dw_stride = (int64_t)q->d_weight_stride;
+  const unsigned join = 4u * (unsigned)a.grid;
   for (uint64_t p = 0; p < c.pieces; p++) {
     a.v0 = (int)(p * c.piece);
     a.vn = (int)std::min<uint64_t>(c.piece, q->vocab - p * c.piece);
     a.first = p == 0;
-    a.last = p + 1 == c.pieces && c.splits == 1;
-    e = launch_product<GRAD, DT>(along_h, along_w, a, tiles(q->rows, kM) * tiles(a.vn, kN), s);
-    if (e == cudaSuccess)
-      e = launch_product<DH, DT>(along_g, across_w, a, tiles(q->rows, kM) * tiles(q->dim, kN) * c.splits, s);
-    if (e == cudaSuccess)
-      e = launch_product<DW, DT>(across_g, across_h, a, tiles(a.vn, kM) * tiles(q->dim, kN), s);
+    a.last = p + 1 == c.pieces;
+    e = launch_product<GRAD, DT>(along_h, piece_w, out_g, a, ceil_div(q->rows, kM) * ceil_div(a.vn, kN), s);
+    if (e == cudaSuccess) e = launch_product<DH, DT>(along_g, across_w, out_g, a, 0, s);
+    if (e == cudaSuccess) e = launch_behind(join_parts<DH, DT>, join, 256, 0, s, a);
+    if (e == cudaSuccess) e = launch_product<DW, DT>(across_g, across_h, out_w, a, 0, s);
+    if (e == cudaSuccess) e = launch_behind(join_parts<DW, DT>, join, 256, 0, s, a);
     if (e != cudaSuccess) return fail(SCAPE_ECUDA, "product (gradient): %s", cudaGetErrorString(e));
-  }
-  if (c.splits > 1) {
-    const uint64_t n = q->rows * (q->dim / 8);
-    sum_splits<DT><<<(unsigned)std::min<uint64_t>((n + 255) / 256, 8ull * num_sms()), 256, 0, s>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return fail(SCAPE_ECUDA, "sum_splits: %s", cudaGetErrorString(e));
   }
   return SCAPE_OK;
 }

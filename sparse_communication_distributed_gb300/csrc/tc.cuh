@@ -75,6 +75,29 @@ __device__ __forceinline__ void load_box(uint32_t smem, const CUtensorMap* map, 
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
+// A box from shared memory to a 2-D tensor: what lies outside is left out.  The writes
+// of the threads to shared memory come first (store_fence, then a barrier).
+__device__ __forceinline__ void store_fence() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void store_box(const CUtensorMap* map, int x, int y, uint32_t smem) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n"
+      " cp.async.bulk.commit_group;" ::"l"(map),
+      "r"(x), "r"(y), "r"(smem)
+      : "memory");
+}
+// The thread's stores have read shared memory; ... are done.
+__device__ __forceinline__ void store_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void store_done() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+__device__ __forceinline__ void put_smem(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
