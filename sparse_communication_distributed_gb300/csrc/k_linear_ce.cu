@@ -42,14 +42,21 @@ using namespace tc;
 
 enum Job { LOSS, GRAD, DH, DW };
 
-constexpr int kM = 128, kN = 256, kK = 64;  // tile; 64 elements are one swizzled row
-constexpr int kStages = 4;
-constexpr uint32_t kBytesA = kM * kK * 2, kBytesB = kN * kK * 2;
-constexpr uint32_t kStageBytes = kBytesA + kBytesB;
+constexpr int kM = 128, kN = 256, kK = 64;  // a CTA's tile; 64 elements are one swizzled row
+// A pair of CTAs has a tile of 256 x 256: each copies its own 128 rows of A and half of
+// the columns of B, a third less than alone.
+template <int CG>
+struct Shape {
+  static constexpr int kRows = kM * CG, kCols = kN / CG;  // rows of a tile; columns of B that a CTA copies
+  static constexpr int kStages = CG == 2 ? 6 : 4;
+  static constexpr uint32_t kBytesA = kM * kK * 2, kBytesB = kCols * kK * 2, kStageBytes = kBytesA + kBytesB;
+};
+constexpr uint32_t kRing = 196608;  // all stages
+static_assert(Shape<1>::kStages * Shape<1>::kStageBytes == kRing && Shape<2>::kStages * Shape<2>::kStageBytes == kRing, "");
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;  // copies, products, allocation, one idle; epilogue
 constexpr uint32_t kOutBytes = 4096;            // a warp's results on their way out: 32 rows of 128 bytes
-constexpr uint32_t kSmem = kStages * kStageBytes + kEpiWarps * kOutBytes + 1024;
+constexpr uint32_t kSmem = kRing + kEpiWarps * kOutBytes + 1024;
 constexpr int kGroup = 16;                      // tiles of rows that walk along the other dimension together
 constexpr uint64_t kTileFloats = (uint64_t)kM * kN;
 
@@ -73,7 +80,7 @@ struct CeArgs {
   // sums of tiles in fp32, a float4 of a row's columns 4 j to 4 j + 3 at [j][row]
   float* acc;              // DH, over the pieces: all tiles
   float* tail;             // DH, DW: the parts of split tiles
-  int grid;                // CTAs of DH and DW
+  int grid;                // CTAs, or pairs of them, of DH and DW
   int first, last;
   void* d_hidden;
   int64_t dh_stride;
@@ -135,16 +142,17 @@ struct Units {
   }
 };
 
-template <int JOB>
+template <int JOB, int CG>
 __device__ __forceinline__ Units units_of(const CeArgs& a, int live) {
+  constexpr int kRows = Shape<CG>::kRows;
   auto up = [](int x, int y) { return (x + y - 1) / y; };
   Units u;
   if (JOB == LOSS || JOB == GRAD) {
-    u.mt = up(live, kM); u.nt = up(a.vn, a.bn); u.kb = up(a.D, kK);
+    u.mt = up(live, kRows); u.nt = up(a.vn, a.bn); u.kb = up(a.D, kK);
   } else if (JOB == DH) {
-    u.mt = up(live, kM); u.nt = up(a.D, kN); u.kb = up(a.vn, kK);
+    u.mt = up(live, kRows); u.nt = up(a.D, kN); u.kb = up(a.vn, kK);
   } else {
-    u.mt = up(a.vn, kM); u.nt = up(a.D, kN); u.kb = up(live, kK);
+    u.mt = up(a.vn, kRows); u.nt = up(a.D, kN); u.kb = up(live, kK);
   }
   u.whole = u.mt * u.nt;
   u.split = 1;
@@ -182,10 +190,10 @@ __device__ __forceinline__ void stage32(uint32_t out, int lane, int side, const 
 
 // What a warp of the epilogue does with its 32 rows and 128 columns of a unit, in tensor
 // memory at "tmem" ("empty": there were no products, all is 0).
-template <int JOB, int DT>
-__device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map_out, const Unit& u, int live, int half,
-                                         int quarter, int lane, uint32_t tmem, bool empty, uint32_t out) {
-  const int r0 = u.m * kM + quarter * 32, r = r0 + lane;
+template <int JOB, int DT, int CG>
+__device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map_out, const Unit& u, int live, int rank,
+                                         int half, int quarter, int lane, uint32_t tmem, bool empty, uint32_t out) {
+  const int r0 = u.m * Shape<CG>::kRows + rank * kM + quarter * 32, r = r0 + lane;
   float f[32];
   auto fetch = [&](int c) {
     if (empty) {
@@ -276,7 +284,8 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
     const float un = a.scale[1];
     const bool on = JOB == DH ? r < live : true;
     // columns of the unit in fp32: a part's own place, or the sums over the pieces
-    float4* sums = reinterpret_cast<float4*>(u.part >= 0 ? a.tail + u.part * kTileFloats : a.acc + u.tile * kTileFloats) +
+    float4* sums = reinterpret_cast<float4*>(u.part >= 0 ? a.tail + (u.part * CG + rank) * kTileFloats
+                                                         : a.acc + (u.tile * CG + rank) * kTileFloats) +
                    half * 32 * kM + quarter * 32 + lane;
     for (int c = 0; c < 4; c++) {
       fetch(c);
@@ -315,11 +324,16 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
   }
 }
 
-template <int JOB, int DT>
+// Warp 0 copies tiles to shared memory, warp 1 (of a pair's first CTA) issues the products,
+// warp 2 allocates tensor memory, warps 4 to 11 are the epilogue: two accumulators let it
+// work on one tile during the products of the next.
+template <int JOB, int DT, int CG>
 __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ CUtensorMap map_a,
                                                        const __grid_constant__ CUtensorMap map_b,
                                                        const __grid_constant__ CUtensorMap map_out,
                                                        const CeArgs a) {
+  using S = Shape<CG>;
+  constexpr int kStages = S::kStages;
   constexpr bool kAcrossA = JOB == DW, kAcrossB = JOB == DH || JOB == DW;
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t bars[2 * kStages + 4];
@@ -327,10 +341,22 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
   __shared__ volatile uint32_t gone;
   const uint32_t buf = (smem_at(raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto full = [&](int s) { return smem_at(&bars[s]); };
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+  const int first = blockIdx.x / CG, step = gridDim.x / CG;
+  auto full = [&](int s) { return smem_at(&bars[s]); };  // (of a pair: the first CTA's counts for both)
   auto free_ = [&](int s) { return smem_at(&bars[kStages + s]); };
   auto ready = [&](int s) { return smem_at(&bars[2 * kStages + s]); };
-  auto taken = [&](int s) { return smem_at(&bars[2 * kStages + 2 + s]); };
+  auto taken = [&](int s) { return smem_at(&bars[2 * kStages + 2 + s]); };  // (the same)
+  auto meet = [&]() {
+    fence_before();
+    if constexpr (CG == 2) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+    fence_after();
+  };
   if (warp == 0 && lane == 0) {
     prefetch_map(&map_a);
     prefetch_map(&map_b);
@@ -341,104 +367,94 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
     }
     for (int s = 0; s < 2; s++) {
       bar_init(ready(s), 1);
-      bar_init(taken(s), kEpiWarps);
+      bar_init(taken(s), kEpiWarps * CG);
     }
     bar_init_fence();
   }
-  if (warp == 2) tmem_alloc(smem_at(&tmem_at), 512);
-  fence_before();
-  __syncthreads();
-  fence_after();
+  __syncwarp();
+  if (warp == 2) tmem_alloc<CG>(smem_at(&tmem_at), 512);
+  meet();
   const uint32_t tmem = tmem_at;
   grid_launch_dependents();
   grid_dependency_wait();
   const int live = *a.live;
-  const Units units = units_of<JOB>(a, live);
+  const Units units = units_of<JOB, CG>(a, live);
   const int n_units = units.count();
-  const uint32_t stage_bytes = kBytesA + (JOB == LOSS || JOB == GRAD ? a.bn : kN) * kK * 2;
+  const int cols = JOB == LOSS || JOB == GRAD ? a.bn : kN;  // of a tile
 
   if (warp == 0 && lane == 0) {
+    const uint32_t bytes = (S::kBytesA + cols / CG * kK * 2) * CG;
     int s = 0;
     uint32_t ph = 0;
-    int issued = 0;  // copies that may still be on their way, oldest first
     bool ok = true;
-    for (int i = blockIdx.x; ok && i < n_units; i += gridDim.x) {
+    for (int i = first; ok && i < n_units; i += step) {
       const Unit t = units.at(i);
+      const int m0 = t.m * S::kRows + rank * kM, n0 = t.n * cols + rank * (cols / CG);
       for (int k = t.k0; k < t.k1; k++) {
         if (!(ok = bar_wait(free_(s), ph ^ 1u, &gone))) break;
-        const uint32_t sa = buf + s * kStageBytes, sb = sa + kBytesA, bar = full(s);
-        bar_expect(bar, stage_bytes);
+        const uint32_t sa = buf + s * S::kStageBytes, sb = sa + S::kBytesA;
+        const uint32_t bar = CG == 2 ? bar_of(full(s), 0) : full(s);
+        if (rank == 0) bar_expect(full(s), bytes);
         if (!kAcrossA) {
-          load_box(sa, &map_a, k * kK, t.m * kM, bar);
+          load_box<CG>(sa, &map_a, k * kK, m0, bar);
         } else {
 #pragma unroll
-          for (int j = 0; j < kM / 64; j++) load_box(sa + j * 8192, &map_a, t.m * kM + 64 * j, k * kK, bar);
+          for (int j = 0; j < kM / 64; j++) load_box<CG>(sa + j * 8192, &map_a, m0 + 64 * j, k * kK, bar);
         }
         if (!kAcrossB) {
-          load_box(sb, &map_b, k * kK, a.v0 + t.n * a.bn, bar);
+          load_box<CG>(sb, &map_b, k * kK, a.v0 + n0, bar);
         } else {
           const int y = (JOB == DH ? a.v0 : 0) + k * kK;
 #pragma unroll
-          for (int j = 0; j < kN / 64; j++) load_box(sb + j * 8192, &map_b, t.n * kN + 64 * j, y, bar);
+          for (int j = 0; j < S::kCols / 64; j++) load_box<CG>(sb + j * 8192, &map_b, n0 + 64 * j, y, bar);
         }
-        issued++;
         if (++s == kStages) {
           s = 0;
           ph ^= 1u;
         }
       }
     }
-    if (!ok) {  // wait for what is still being copied here, each for a while
-      for (int j = min(issued, kStages); j > 0; j--) {
-        int q = s - j;
-        uint32_t p = ph;
-        if (q < 0) {
-          q += kStages;
-          p ^= 1u;
-        }
-        const uint64_t began = now_ns();
-        while (!bar_try(full(q), p) && now_ns() - began < kWaitNs / 100) {
-        }
+    if (!ok) {  // what is still being copied arrives meanwhile
+      const uint64_t began = now_ns();
+      while (now_ns() - began < kWaitNs / 100) {
       }
     }
-  } else if (warp == 1 && lane == 0) {
-    const uint32_t kind = product_of(DT == SCAPE_BF16, kAcrossA, kAcrossB, kM, JOB == LOSS || JOB == GRAD ? a.bn : kN);
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    const uint32_t kind = product_of(DT == SCAPE_BF16, kAcrossA, kAcrossB, S::kRows, cols);
     int s = 0, n = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int i = blockIdx.x; ok && i < n_units; i += gridDim.x, n++) {
+    for (int i = first; ok && i < n_units; i += step) {
       const Unit t = units.at(i);
-      if (t.k0 >= t.k1) {
-        n--;  // nothing to multiply: no accumulator
-        continue;
-      }
+      if (t.k0 >= t.k1) continue;  // nothing to multiply: no accumulator
       const int acc = n & 1;
       if (!(ok = bar_wait(taken(acc), ((n >> 1) & 1) ^ 1, &gone))) break;
+      n++;
       fence_after();
       const uint32_t d = tmem + acc * kN;
       for (int k = t.k0; k < t.k1; k++) {
         if (!(ok = bar_wait(full(s), ph, &gone))) break;
         fence_after();
-        const uint32_t sa = buf + s * kStageBytes, sb = sa + kBytesA;
+        const uint32_t sa = buf + s * S::kStageBytes, sb = sa + S::kBytesA;
         // 16 elements of K: 32 bytes along a row, or 16 rows of 128 bytes
         const uint64_t oa = kAcrossA ? operand(sa, 8192, 1024) : operand(sa, 16, 1024);
         const uint64_t ob = kAcrossB ? operand(sb, 8192, 1024) : operand(sb, 16, 1024);
 #pragma unroll
         for (int j = 0; j < kK / 16; j++)
-          mma(d, oa + j * (kAcrossA ? 128 : 2), ob + j * (kAcrossB ? 128 : 2), kind, k > t.k0 || j > 0);
-        commit(free_(s));
+          mma<CG>(d, oa + j * (kAcrossA ? 128 : 2), ob + j * (kAcrossB ? 128 : 2), kind, k > t.k0 || j > 0);
+        commit<CG>(free_(s));
         if (++s == kStages) {
           s = 0;
           ph ^= 1u;
         }
       }
-      if (ok) commit(ready(acc));
+      if (ok) commit<CG>(ready(acc));
     }
   } else if (warp >= 4) {
     const int half = (warp - 4) >> 2, quarter = warp & 3;
     int n = 0;
-    const uint32_t out = buf + kStages * kStageBytes + (warp - 4) * kOutBytes;
-    for (int i = blockIdx.x; i < n_units; i += gridDim.x) {
+    const uint32_t out = buf + kRing + (warp - 4) * kOutBytes;
+    for (int i = first; i < n_units; i += step) {
       const Unit t = units.at(i);
       const bool empty = t.k0 >= t.k1;
       const int acc = n & 1;
@@ -447,26 +463,28 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
         fence_after();
       }
       __syncwarp();
-      epilogue<JOB, DT>(a, &map_out, t, live, half, quarter, lane,
-                        tmem + acc * kN + half * 128 + ((uint32_t)(quarter * 32) << 16), empty, out);
+      epilogue<JOB, DT, CG>(a, &map_out, t, live, (int)rank, half, quarter, lane,
+                            tmem + acc * kN + half * 128 + ((uint32_t)(quarter * 32) << 16), empty, out);
       if (!empty) {
         fence_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(taken(acc));
+        if (lane == 0) {
+          if (CG == 2) bar_arrive_at(bar_of(taken(acc), 0));
+          else bar_arrive(taken(acc));
+        }
         n++;
       }
     }
     if (lane == 0) store_done();
   }
-  fence_before();
-  __syncthreads();
-  fence_after();
+  __syncwarp();
+  meet();  // (neither CTA of a pair leaves while the other one's products and arrivals may still reach it)
   if (gone) {  // (never in a correct run) the losses say so
     if (threadIdx.x == 0) *a.status = 1u;
     for (int64_t i = threadIdx.x; i < a.rows; i += kThreads) a.loss[i] = __uint_as_float(0x7FFFFFFFu);
   }
   __syncwarp();
-  if (warp == 2) tmem_free(tmem, 512);
+  if (warp == 2) tmem_free<CG>(tmem, 512);
 }
 
 // ---- rows -------------------------------------------------------------------------
@@ -606,20 +624,22 @@ __global__ __launch_bounds__(1024) void row_losses(const CeArgs a, int n_parts) 
 
 // The parts of the split tiles of DH or DW, added up in order: a thread has eight
 // columns of a row.
-template <int JOB, int DT>
+template <int JOB, int DT, int CG>
 __global__ __launch_bounds__(256) void join_parts(const CeArgs a) {
+  constexpr int kRows = Shape<CG>::kRows;
   grid_launch_dependents();
   grid_dependency_wait();
   const int live = *a.live;
-  const Units units = units_of<JOB>(a, live);
+  const Units units = units_of<JOB, CG>(a, live);
   const int rest = units.mt * units.nt - units.whole;
   const float un = a.scale[1];
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)rest * kM * (kN / 8);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)rest * kRows * (kN / 8);
        i += (int64_t)gridDim.x * 256) {
-    const int row = (int)(i % kM), j = (int)(i / kM % (kN / 8)), t = (int)(i / (kM * (kN / 8)));
+    const int row = (int)(i % kM), j = (int)(i / kM % (kN / 8)), both = (int)(i / (kM * (kN / 8)));
+    const int t = both / CG, rank = both % CG;
     Unit u;
     units.place(units.whole + t, u);
-    const int r = u.m * kM + row, d = u.n * kN + 8 * j;
+    const int r = u.m * kRows + rank * kM + row, d = u.n * kN + 8 * j;
     float f[8] = {};
     auto add = [&](const float* tile) {
       const float4* q = reinterpret_cast<const float4*>(tile) + 2 * j * kM + row;
@@ -627,9 +647,9 @@ __global__ __launch_bounds__(256) void join_parts(const CeArgs a) {
       f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
       f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
     };
-    for (int s = 0; s < units.split; s++) add(a.tail + (uint64_t)(s * rest + t) * kTileFloats);
+    for (int s = 0; s < units.split; s++) add(a.tail + (uint64_t)((s * rest + t) * CG + rank) * kTileFloats);
     if (JOB == DH) {
-      float* acc = a.acc + u.tile * kTileFloats;
+      float* acc = a.acc + (u.tile * CG + rank) * kTileFloats;
       if (!a.first) add(acc);
       if (!a.last) {
         float4* q = reinterpret_cast<float4*>(acc) + 2 * j * kM + row;
@@ -788,25 +808,29 @@ bool ranges_meet(const void* p, uint64_t n, const void* q, uint64_t m) {
   return p && q && n && m && a < b + m && b < a + n;
 }
 
-// Launches behind the kernel in front of it, which it waits for on the GPU.
+// Launches behind the kernel in front of it, which it waits for on the GPU; in clusters.
 template <class K, class... A>
-cudaError_t launch_behind(K kernel, unsigned grid, unsigned block, uint32_t smem, cudaStream_t s, const A&... args) {
+cudaError_t launch_behind(K kernel, unsigned grid, unsigned block, uint32_t smem, int cluster, cudaStream_t s,
+                          const A&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   const cudaError_t last = cudaGetLastError();
   return e != cudaSuccess ? e : last;
 }
 
-template <int JOB, int DT>
+template <int JOB, int DT, int CG>
 cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const CeArgs& a,
                            uint64_t tiles, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
@@ -814,16 +838,16 @@ cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const C
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
-    e = cudaFuncSetAttribute(product<JOB, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    e = cudaFuncSetAttribute(product<JOB, DT, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
   }
   unsigned grid = (unsigned)a.grid;  // (DH and DW divide their sums by it)
   if (JOB == LOSS || JOB == GRAD) grid = (unsigned)std::min<uint64_t>(std::max<uint64_t>(tiles, 1), grid);
-  return launch_behind(product<JOB, DT>, grid, kThreads, kSmem, s, ma, mb, mo, a);
+  return launch_behind(product<JOB, DT, CG>, grid * CG, kThreads, kSmem, CG, s, ma, mb, mo, a);
 }
 
-template <int DT>
+template <int DT, int CG>
 int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, cudaStream_t s) {
   const bool grad = q->d_hidden != nullptr;
   CeArgs a{};
@@ -841,14 +865,15 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
   a.cap = (int64_t)c.cap;
   a.D = (int)q->dim;
   a.V = (int)q->vocab;
-  a.grid = num_sms();
+  constexpr int kRows = Shape<CG>::kRows;
+  a.grid = num_sms() / CG;
   char* rows = ws + l.rows;
 
   CUtensorMap along_h, along_w, across_h, across_w, along_g, across_g, piece_w, out_g, out_w;
   bool ok = encode(&along_h, q->dtype, rows, c.cap, q->dim, q->dim, kM) &&
-            encode(&along_w, q->dtype, q->weight, q->vocab, q->dim, q->weight_stride, (uint32_t)c.bn);
+            encode(&along_w, q->dtype, q->weight, q->vocab, q->dim, q->weight_stride, (uint32_t)c.bn / CG);
   if (ok && grad)
-    ok = encode(&piece_w, q->dtype, q->weight, q->vocab, q->dim, q->weight_stride, kN) &&
+    ok = encode(&piece_w, q->dtype, q->weight, q->vocab, q->dim, q->weight_stride, Shape<CG>::kCols) &&
          encode(&across_h, q->dtype, rows, c.cap, q->dim, q->dim, kK) &&
          encode(&across_w, q->dtype, q->weight, q->vocab, q->dim, q->weight_stride, kK) &&
          encode(&along_g, q->dtype, ws + l.g, c.cap, c.piece, c.piece, kM) &&
@@ -886,9 +911,9 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
   a.v0 = 0;
   a.vn = a.V;
   a.bn = (int)c.bn;
-  e = launch_product<LOSS, DT>(along_h, along_w, along_w, a, ceil_div(q->rows, kM) * ceil_div(q->vocab, c.bn), s);
+  e = launch_product<LOSS, DT, CG>(along_h, along_w, along_w, a, ceil_div(q->rows, kRows) * ceil_div(q->vocab, c.bn), s);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "product (loss): %s", cudaGetErrorString(e));
-  e = launch_behind(row_losses, (unsigned)(c.cap / 32), 1024, 0, s, a, (int)c.n_parts);
+  e = launch_behind(row_losses, (unsigned)(c.cap / 32), 1024, 0, 1, s, a, (int)c.n_parts);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "row_losses: %s", cudaGetErrorString(e));
   if (!grad) return SCAPE_OK;
 
@@ -899,17 +924,17 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
   a.dh_stride = (int64_t)q->d_hidden_stride;
   a.d_weight = q->d_weight;
   a.dw_stride = (int64_t)q->d_weight_stride;
-  const unsigned join = 4u * (unsigned)a.grid;
+  const unsigned join = 4u * (unsigned)num_sms();
   for (uint64_t p = 0; p < c.pieces; p++) {
     a.v0 = (int)(p * c.piece);
     a.vn = (int)std::min<uint64_t>(c.piece, q->vocab - p * c.piece);
     a.first = p == 0;
     a.last = p + 1 == c.pieces;
-    e = launch_product<GRAD, DT>(along_h, piece_w, out_g, a, ceil_div(q->rows, kM) * ceil_div(a.vn, kN), s);
-    if (e == cudaSuccess) e = launch_product<DH, DT>(along_g, across_w, out_g, a, 0, s);
-    if (e == cudaSuccess) e = launch_behind(join_parts<DH, DT>, join, 256, 0, s, a);
-    if (e == cudaSuccess) e = launch_product<DW, DT>(across_g, across_h, out_w, a, 0, s);
-    if (e == cudaSuccess) e = launch_behind(join_parts<DW, DT>, join, 256, 0, s, a);
+    e = launch_product<GRAD, DT, CG>(along_h, piece_w, out_g, a, ceil_div(q->rows, kRows) * ceil_div(a.vn, kN), s);
+    if (e == cudaSuccess) e = launch_product<DH, DT, CG>(along_g, across_w, out_g, a, 0, s);
+    if (e == cudaSuccess) e = launch_behind(join_parts<DH, DT, CG>, join, 256, 0, 1, s, a);
+    if (e == cudaSuccess) e = launch_product<DW, DT, CG>(across_g, across_h, out_w, a, 0, s);
+    if (e == cudaSuccess) e = launch_behind(join_parts<DW, DT, CG>, join, 256, 0, 1, s, a);
     if (e != cudaSuccess) return fail(SCAPE_ECUDA, "product (gradient): %s", cudaGetErrorString(e));
   }
   return SCAPE_OK;
@@ -957,5 +982,8 @@ SCAPE_API int scape_linear_ce(const scape_linear_ce_args* args, void* workspace,
     return fail(SCAPE_EINVAL, "workspace must be %llu bytes, 256-byte aligned", (unsigned long long)l.bytes);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
-  return args->dtype == SCAPE_BF16 ? run<SCAPE_BF16>(args, c, l, ws, s) : run<SCAPE_F16>(args, c, l, ws, s);
+  // pairs of CTAs, unless the rows of one are enough
+  if (args->rows <= (uint64_t)kM)
+    return args->dtype == SCAPE_BF16 ? run<SCAPE_BF16, 1>(args, c, l, ws, s) : run<SCAPE_F16, 1>(args, c, l, ws, s);
+  return args->dtype == SCAPE_BF16 ? run<SCAPE_BF16, 2>(args, c, l, ws, s) : run<SCAPE_F16, 2>(args, c, l, ws, s);
 }
