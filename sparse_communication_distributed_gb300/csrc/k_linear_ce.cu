@@ -7,12 +7,18 @@
 // Four products on the tensor cores (16-bit operands, fp32 accumulators in tensor
 // memory), one kernel with four epilogues:
 //   LOSS  H W^T: the maximum and the sum of exponentials of every row of a tile, and
-//         the label's logit
-//   GRAD  the same product again, for a piece of the vocabulary: G of that piece
+//         the label's logit; for a gradient also the exponentials themselves, for as
+//         many words as there is room for
+//   GRAD  the same product again, for a piece of the vocabulary without such room: G of
+//         that piece
 //   DH    G W, added up over the pieces in fp32
 //   DW    G^T H, complete for the piece's words
-// A gradient thus costs 8 T D V operations and not 6: keeping the logits would cost
-// 2 T V bytes, keeping them exact enough for the exponential 4 T V.
+// With GRAD a gradient costs 8 T D V operations, without it 6.  What LOSS keeps of a
+// bf16 problem are exponentials against the maximum of their 128 words, in fp16 times
+// 2^15: their rounding (half a step is 2^-11) does not count beside that of G (2^-8),
+// and G takes their place (grad_kept).  Logits in 16 bits would not do: exp() makes an
+// error of 2^-8 |l| of them.  For fp16, whose G is rounded to 2^-11 itself, nothing is
+// kept.
 //
 // Rows without a term (no label, weight 0) are left out: the others are copied
 // together first, so that neither time nor the gradients depend on what they hold.
@@ -75,13 +81,19 @@ struct CeArgs {
   int64_t rows, cap;       // caller's rows; rounded up to a multiple of 256
   int D, V;
   int bn;                  // words of a tile (LOSS, GRAD)
+  int bm;                  // rows of a CTA's tile that are copied (LOSS, GRAD, DH)
+  int keep;                // words below this are kept (LOSS)
   // the piece of the vocabulary
   int v0, vn;
+  int piece;               // words of a piece, all but the last one
+  int64_t g0;              // its first row in the buffer of G
+  void* g;
   // sums of tiles in fp32, a float4 of a row's columns 4 j to 4 j + 3 at [j][row]
   float* acc;              // DH, over the pieces: all tiles
   float* tail;             // DH, DW: the parts of split tiles
   int grid;                // CTAs, or pairs of them, of DH and DW
   int first, last;
+  int early;               // LOSS: no more than one row of tiles
   void* d_hidden;
   int64_t dh_stride;
   void* d_weight;
@@ -190,7 +202,9 @@ __device__ __forceinline__ void stage32(uint32_t out, int lane, int side, const 
 
 // What a warp of the epilogue does with its 32 rows and 128 columns of a unit, in tensor
 // memory at "tmem" ("empty": there were no products, all is 0).
-template <int JOB, int DT, int CG>
+constexpr float kKept = 32768.0f;
+
+template <int JOB, int DT, int CG, bool KEEP>
 __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map_out, const Unit& u, int live, int rank,
                                          int half, int quarter, int lane, uint32_t tmem, bool empty, uint32_t out) {
   const int r0 = u.m * Shape<CG>::kRows + rank * kM + quarter * 32, r = r0 + lane;
@@ -216,35 +230,60 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
   if constexpr (JOB == LOSS) {
     const int label = r < live ? a.label[r] : -1;
     const int end = min(a.V, (u.n + 1) * a.bn);
-    float m = neg_inf(), s = 0.0f, y = 0.0f;
+    const int first = u.n * a.bn + half * 128;
+    float m = neg_inf(), y = 0.0f;
     bool mine = false;
-    for (int c = 0; c < 4; c++) {
-      const int w0 = u.n * a.bn + half * 128 + 32 * c;
-      if (w0 >= end) break;
+    auto logits = [&](int c) {  // 32 of them; words that there are not are out of the running
+      const int w0 = first + 32 * c;
       fetch(c);
       if (w0 + 32 > end) {
 #pragma unroll
         for (int i = 0; i < 32; i++)
           if (w0 + i >= end) f[i] = neg_inf();
       }
+    };
+    for (int c = 0; c < 4 && first + 32 * c < end; c++) {
+      logits(c);
+      const int w0 = first + 32 * c;
       if ((uint32_t)(label - w0) < 32u) {
         mine = true;
 #pragma unroll
         for (int i = 0; i < 32; i++)
           if (label == w0 + i) y = f[i];
       }
-      float top = f[0];
 #pragma unroll
-      for (int i = 1; i < 32; i++) top = fmaxf(top, f[i]);
-      const float m2 = fmaxf(m, top), by = shift_of(m2);
-      s *= ex2((m - by) * kLog2e);
-      pair_t sum = pair(0.0f, 0.0f);
-#pragma unroll
-      for (int i = 0; i < 32; i += 2)
-        sum = add2(sum, ex2_2(mul2(add2(pair(f[i], f[i + 1]), pair(-by, -by)), pair(kLog2e, kLog2e))));
-      s += sum.x + sum.y;
-      m = m2;
+      for (int i = 0; i < 32; i++) m = fmaxf(m, f[i]);
     }
+    // (tensor memory is read a second time: that costs less than adjusting sums and what
+    // is kept to a maximum that grows)
+    const float by = shift_of(m);
+    const bool keep = KEEP && first < a.keep;
+    const int p = keep ? first / a.piece : 0;
+    pair_t sum = pair(0.0f, 0.0f);
+    for (int c = 0; c < 4 && first + 32 * c < end; c++) {
+      logits(c);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const pair_t e = ex2_2(mul2(add2(pair(f[i], f[i + 1]), pair(-by, -by)), pair(kLog2e, kLog2e)));
+        sum = add2(sum, e);
+        f[i] = e.x;
+        f[i + 1] = e.y;
+      }
+      if constexpr (KEEP) {
+        if (!keep) continue;
+#pragma unroll
+        for (int i = 0; i < 32; i++) f[i] *= kKept;
+        const int x = first + 32 * c - p * a.piece;
+        if constexpr (CG == 1) {  // (few rows, and tiles that need not be a multiple of 64 words wide)
+          if (r < live) store32<SCAPE_F16>(static_cast<char*>(a.g) + ((int64_t)p * a.cap + r) * a.piece * 2, x, a.piece, f);
+        } else {
+          if (!(c & 1)) reuse();
+          stage32<SCAPE_F16>(out, lane, c & 1, f);
+          if ((c & 1) || first + 32 * (c + 1) >= end) send(x & ~63, (int)(p * a.cap) + r0);
+        }
+      }
+    }
+    const float s = sum.x + sum.y;
     if (r < live) {
       a.parts[(int64_t)(u.n * 2 + half) * a.cap + r] = make_float2(m, s);
       if (mine) a.label_logit[r] = y;
@@ -278,7 +317,7 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
       }
       if (!(c & 1)) reuse();
       stage32<DT>(out, lane, c & 1, f);
-      if (c & 1) send(c0 - 32, r0);
+      if (c & 1) send(c0 - 32, (int)a.g0 + r0);
     }
   } else {
     const float un = a.scale[1];
@@ -327,7 +366,7 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
 // Warp 0 copies tiles to shared memory, warp 1 (of a pair's first CTA) issues the products,
 // warp 2 allocates tensor memory, warps 4 to 11 are the epilogue: two accumulators let it
 // work on one tile during the products of the next.
-template <int JOB, int DT, int CG>
+template <int JOB, int DT, int CG, bool KEEP>
 __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ CUtensorMap map_a,
                                                        const __grid_constant__ CUtensorMap map_b,
                                                        const __grid_constant__ CUtensorMap map_out,
@@ -376,14 +415,27 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
   meet();
   const uint32_t tmem = tmem_at;
   grid_launch_dependents();
+  const int cols = JOB == LOSS || JOB == GRAD ? a.bn : kN;  // of a tile
+  const uint32_t bytes = ((kAcrossA ? kM : a.bm) + cols / CG) * kK * 2 * CG;  // of a stage
+  // Few rows: the first weights are on their way while the rows are still being taken
+  // (with at most one row of tiles, unit i is tile i).
+  int early = 0;
+  if (JOB == LOSS && CG == 1 && warp == 0 && lane == 0 && a.early && blockIdx.x * cols < a.V)
+    for (; early < min(kStages, (a.D + kK - 1) / kK); early++) {
+      bar_expect(full(early), bytes);
+      load_box<CG>(buf + early * S::kStageBytes + S::kBytesA, &map_b, early * kK, blockIdx.x * cols, full(early));
+    }
   grid_dependency_wait();
   const int live = *a.live;
   const Units units = units_of<JOB, CG>(a, live);
   const int n_units = units.count();
-  const int cols = JOB == LOSS || JOB == GRAD ? a.bn : kN;  // of a tile
 
   if (warp == 0 && lane == 0) {
-    const uint32_t bytes = (S::kBytesA + cols / CG * kK * 2) * CG;
+    if (n_units == 0)  // no row after all: the stages are completed and left
+      for (int s = 0; s < early; s++) {
+        load_box<CG>(buf + s * S::kStageBytes, &map_a, 0, 0, full(s));
+        bar_wait(full(s), 0, &gone);
+      }
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
@@ -391,17 +443,20 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
       const Unit t = units.at(i);
       const int m0 = t.m * S::kRows + rank * kM, n0 = t.n * cols + rank * (cols / CG);
       for (int k = t.k0; k < t.k1; k++) {
-        if (!(ok = bar_wait(free_(s), ph ^ 1u, &gone))) break;
+        const bool begun = early > 0;
+        if (!begun && !(ok = bar_wait(free_(s), ph ^ 1u, &gone))) break;
         const uint32_t sa = buf + s * S::kStageBytes, sb = sa + S::kBytesA;
         const uint32_t bar = CG == 2 ? bar_of(full(s), 0) : full(s);
-        if (rank == 0) bar_expect(full(s), bytes);
+        if (rank == 0 && !begun) bar_expect(full(s), bytes);
         if (!kAcrossA) {
-          load_box<CG>(sa, &map_a, k * kK, m0, bar);
+          load_box<CG>(sa, &map_a, k * kK, (JOB == DH ? (int)a.g0 : 0) + m0, bar);
         } else {
 #pragma unroll
-          for (int j = 0; j < kM / 64; j++) load_box<CG>(sa + j * 8192, &map_a, m0 + 64 * j, k * kK, bar);
+          for (int j = 0; j < kM / 64; j++) load_box<CG>(sa + j * 8192, &map_a, m0 + 64 * j, (int)a.g0 + k * kK, bar);
         }
-        if (!kAcrossB) {
+        if (begun) {
+          early--;
+        } else if (!kAcrossB) {
           load_box<CG>(sb, &map_b, k * kK, a.v0 + n0, bar);
         } else {
           const int y = (JOB == DH ? a.v0 : 0) + k * kK;
@@ -463,7 +518,7 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
         fence_after();
       }
       __syncwarp();
-      epilogue<JOB, DT, CG>(a, &map_out, t, live, (int)rank, half, quarter, lane,
+      epilogue<JOB, DT, CG, KEEP>(a, &map_out, t, live, (int)rank, half, quarter, lane,
                             tmem + acc * kN + half * 128 + ((uint32_t)(quarter * 32) << 16), empty, out);
       if (!empty) {
         fence_before();
@@ -520,7 +575,7 @@ __global__ __launch_bounds__(kRowThreads) void take_rows(const RowsArgs a) {
   __shared__ uint32_t ubuf[32];
   __shared__ float fbuf[32];
   __shared__ int64_t place[kRowThreads];
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int tid = threadIdx.x;
   const int64_t begin = blockIdx.x * a.chunk, end = min(a.rows, begin + a.chunk);
   float top = 0.0f;
   auto look = [&](int64_t r, int64_t& y, float& w) {
@@ -537,7 +592,7 @@ __global__ __launch_bounds__(kRowThreads) void take_rows(const RowsArgs a) {
   for (int64_t r = tid; r < begin; r += kRowThreads) before += look(r, y, w);
   int64_t at = cta_sum(before, ubuf);  // (rows < 2^24)
   grid_launch_dependents();
-  const int64_t vecs = a.bytes / 16;
+  const uint32_t vecs = (uint32_t)(a.bytes / 16);  // (up to 8192, of 512 rows)
   const uint4 zero = make_uint4(0, 0, 0, 0);
   for (int64_t r0 = begin; r0 < end; r0 += kRowThreads) {
     const int64_t r = r0 + tid;
@@ -555,17 +610,15 @@ __global__ __launch_bounds__(kRowThreads) void take_rows(const RowsArgs a) {
     place[tid] = on ? at + rank : -1;
     __syncthreads();
     const int n = (int)min((int64_t)kRowThreads, end - r0);
-    for (int i = wid; i < n; i += kRowWarps) {
-      const int64_t p = place[i];
-      if (p >= 0) {
-        const uint4* from = reinterpret_cast<const uint4*>(a.hidden + (r0 + i) * a.stride);
-        uint4* to = reinterpret_cast<uint4*>(a.together + p * a.bytes);
 #pragma unroll 4
-        for (int64_t v = lane; v < vecs; v += 32) to[v] = ld_row_u4(from + v);
-      } else if (a.d_hidden) {
-        uint4* g = reinterpret_cast<uint4*>(a.d_hidden + (r0 + i) * a.dh_stride);
-        for (int64_t v = lane; v < vecs; v += 32) g[v] = zero;
-      }
+    for (uint32_t x = tid; x < (uint32_t)n * vecs; x += kRowThreads) {
+      const uint32_t i = x / vecs, v = x - i * vecs;
+      const int64_t p = place[i];
+      if (p >= 0)
+        reinterpret_cast<uint4*>(a.together + p * a.bytes)[v] =
+            ld_row_u4(reinterpret_cast<const uint4*>(a.hidden + (r0 + i) * a.stride) + v);
+      else if (a.d_hidden)
+        reinterpret_cast<uint4*>(a.d_hidden + (r0 + i) * a.dh_stride)[v] = zero;
     }
     __syncthreads();
     at += all;
@@ -575,8 +628,9 @@ __global__ __launch_bounds__(kRowThreads) void take_rows(const RowsArgs a) {
   if (blockIdx.x + 1 < gridDim.x) return;
   // the last CTA has seen every row.  Rows of 0 behind the last one, to a multiple of 64:
   // DW adds them up, too
-  for (int64_t i = at * vecs + tid; i < (at + 63) / 64 * 64 * vecs; i += kRowThreads)
-    reinterpret_cast<uint4*>(a.together)[i] = zero;
+  if (a.d_hidden)
+    for (int64_t i = at * vecs + tid; i < (at + 63) / 64 * 64 * vecs; i += kRowThreads)
+      reinterpret_cast<uint4*>(a.together)[i] = zero;
   top = cta_max(top, fbuf);
   if (tid == 0) {
     *a.live = (int32_t)at;
@@ -619,6 +673,65 @@ __global__ __launch_bounds__(1024) void row_losses(const CeArgs a, int n_parts) 
     a.stats[row] = make_float2(p.x, log2f(p.y));
     const float loss = a.weight[row] * ((p.x - a.label_logit[row]) + logf(p.y));
     a.loss[a.map[row]] = *a.status ? __uint_as_float(0x7FFFFFFFu) : loss;
+  }
+}
+
+// G of a piece in the place of its kept exponentials e:
+//   p = e 2^((m_part - m) log2e - log2 sum - 15),  G = w 2^k (p - [label])
+// A warp has eight vectors of a row at a time.
+__global__ __launch_bounds__(256) void grad_kept(const CeArgs a) {
+  using E = Elem<SCAPE_BF16>;
+  constexpr int kVecs = 8;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int live = *a.live, lane = threadIdx.x & 31;
+  const int64_t rows = min((int64_t)(live + 255) / 256 * 256, a.cap);  // (as many as DH and DW read)
+  const int vecs = (a.vn + 7) / 8, runs = (vecs + 32 * kVecs - 1) / (32 * kVecs);
+  const int tail = a.piece / 8;  // vectors of a row, those behind the last word included
+  for (int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); item < rows * runs; item += (int64_t)gridDim.x * 8) {
+    const int r = (int)(item / runs), v0 = (int)(item - (int64_t)r * runs) * 32 * kVecs + lane;
+    const bool on = r < live, last = v0 - lane + 32 * kVecs >= vecs;
+    uint4* row = reinterpret_cast<uint4*>(static_cast<char*>(a.g) + (a.g0 + r) * a.piece * 2);
+    uint4 e[kVecs];
+    float f[kVecs];
+    if (on) {
+      const float2 st = a.stats[r];
+      const float w = a.weight[r] * a.scale[0];
+#pragma unroll
+      for (int i = 0; i < kVecs; i++) {
+        const int v = v0 + 32 * i;
+        if (v < vecs) {
+          e[i] = row[v];
+          const int word = a.v0 + 8 * v, tile = word / a.bn, part = 2 * tile + (word - tile * a.bn >= 128);
+          const float m = a.parts[(int64_t)part * a.cap + r].x;
+          f[i] = w * ex2(__fmaf_rn(m - st.x, kLog2e, -st.y) - 15.0f);
+        }
+      }
+      const int label = a.label[r] - a.v0;
+#pragma unroll
+      for (int i = 0; i < kVecs; i++) {
+        const int v = v0 + 32 * i;
+        if (v >= vecs) continue;
+        float x[8];
+        Elem<SCAPE_F16>::unpack(e[i], x);
+#pragma unroll
+        for (int j = 0; j < 8; j++) x[j] = a.v0 + 8 * v + j < a.V ? x[j] * f[i] : 0.0f;
+        if ((uint32_t)(label - 8 * v) < 8u) {
+          const float g = w * (ex2(__fmaf_rn(a.label_logit[r] - st.x, kLog2e, -st.y)) - 1.0f);
+#pragma unroll
+          for (int j = 0; j < 8; j++)
+            if (label == 8 * v + j) x[j] = g;
+        }
+        row[v] = E::pack(x);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVecs; i++)
+        if (v0 + 32 * i < vecs) row[v0 + 32 * i] = make_uint4(0, 0, 0, 0);
+    }
+    // what a tile of DH or DW reads beside the last word
+    if (last)
+      for (int v = vecs + lane; v < tail; v += 32) row[v] = make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -719,12 +832,14 @@ struct Cut {
   uint64_t bn = kN;     // words of a tile of LOSS
   uint64_t piece = 0;   // words of a piece
   uint64_t pieces = 0;
+  uint64_t kept = 0;    // pieces that LOSS keeps
   uint64_t n_parts = 0;
 };
 
-// G of a piece is kept to this size, so that a gradient needs little memory beside its
-// results.
-constexpr uint64_t kPieceBytes = 512ull << 20;
+// G takes at most this much, so that a gradient needs little memory beside its results:
+// of a piece, and of all pieces that are there at once (kept ones; the others come one
+// after the other).
+constexpr uint64_t kPieceBytes = 512ull << 20, kAllBytes = 1024ull << 20;
 
 uint64_t ceil_div(uint64_t x, uint64_t y) { return (x + y - 1) / y; }
 
@@ -751,6 +866,9 @@ Cut cut_of(const scape_linear_ce_args* q, bool grad) {
   const uint64_t fit = std::max<uint64_t>(kPieceBytes / (c.cap * 2 * kN), 1);
   c.piece = ceil_div(tiles, ceil_div(tiles, fit)) * kN;
   c.pieces = ceil_div(tiles * kN, c.piece);
+  // (fp16: not kept; a tile of another width may lie in two pieces)
+  if (q->dtype == SCAPE_BF16 && (c.pieces == 1 || c.bn == (uint64_t)kN))
+    c.kept = std::min(c.pieces, std::max<uint64_t>(kAllBytes / (c.cap * c.piece * 2), 1));
   return c;
 }
 
@@ -775,7 +893,7 @@ Layout layout_of(const scape_linear_ce_args* q, const Cut& c, bool grad) {
   l.parts = take(c.n_parts * c.cap * 8);
   l.rows = take(c.cap * q->dim * 2);
   if (grad) {
-    l.g = take(c.cap * c.piece * 2);
+    l.g = take(std::max<uint64_t>(c.kept, 1) * c.cap * c.piece * 2);
     if (c.pieces > 1) l.acc = take(c.cap / kM * ceil_div(q->dim, kN) * kTileFloats * 4);
     l.tail = take(kMaxParts * (uint64_t)num_sms() * kTileFloats * 4);
   }
@@ -830,7 +948,7 @@ cudaError_t launch_behind(K kernel, unsigned grid, unsigned block, uint32_t smem
   return e != cudaSuccess ? e : last;
 }
 
-template <int JOB, int DT, int CG>
+template <int JOB, int DT, int CG, bool KEEP = false>
 cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const CeArgs& a,
                            uint64_t tiles, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
@@ -838,13 +956,13 @@ cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const C
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
-    e = cudaFuncSetAttribute(product<JOB, DT, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    e = cudaFuncSetAttribute(product<JOB, DT, CG, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
   }
   unsigned grid = (unsigned)a.grid;  // (DH and DW divide their sums by it)
   if (JOB == LOSS || JOB == GRAD) grid = (unsigned)std::min<uint64_t>(std::max<uint64_t>(tiles, 1), grid);
-  return launch_behind(product<JOB, DT, CG>, grid * CG, kThreads, kSmem, CG, s, ma, mb, mo, a);
+  return launch_behind(product<JOB, DT, CG, KEEP>, grid * CG, kThreads, kSmem, CG, s, ma, mb, mo, a);
 }
 
 template <int DT, int CG>
@@ -869,16 +987,20 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
   a.grid = num_sms() / CG;
   char* rows = ws + l.rows;
 
+  const uint64_t g_rows = std::max<uint64_t>(c.kept, 1) * c.cap;
   CUtensorMap along_h, along_w, across_h, across_w, along_g, across_g, piece_w, out_g, out_w;
-  bool ok = encode(&along_h, q->dtype, rows, c.cap, q->dim, q->dim, kM) &&
+  // (what is not copied of a tile's rows are rows that nobody reads)
+  a.bm = CG == 1 ? (int)up(std::max<uint64_t>(q->rows, 1), 8) : kM;
+  a.early = CG == 1;
+  bool ok = encode(&along_h, q->dtype, rows, c.cap, q->dim, q->dim, (uint32_t)a.bm) &&
             encode(&along_w, q->dtype, q->weight, q->vocab, q->dim, q->weight_stride, (uint32_t)c.bn / CG);
   if (ok && grad)
     ok = encode(&piece_w, q->dtype, q->weight, q->vocab, q->dim, q->weight_stride, Shape<CG>::kCols) &&
          encode(&across_h, q->dtype, rows, c.cap, q->dim, q->dim, kK) &&
          encode(&across_w, q->dtype, q->weight, q->vocab, q->dim, q->weight_stride, kK) &&
-         encode(&along_g, q->dtype, ws + l.g, c.cap, c.piece, c.piece, kM) &&
-         encode(&across_g, q->dtype, ws + l.g, c.cap, c.piece, c.piece, kK) &&
-         encode(&out_g, q->dtype, ws + l.g, c.cap, c.piece, c.piece, 32) &&
+         encode(&along_g, q->dtype, ws + l.g, g_rows, c.piece, c.piece, (uint32_t)a.bm) &&
+         encode(&across_g, q->dtype, ws + l.g, g_rows, c.piece, c.piece, kK) &&
+         encode(&out_g, q->dtype, ws + l.g, g_rows, c.piece, c.piece, 32) &&
          encode(&out_w, q->dtype, q->d_weight, q->vocab, q->dim, q->d_weight_stride, 32);
   if (!ok) return fail(SCAPE_ECUDA, "cuTensorMapEncodeTiled failed or is missing in the driver");
 
@@ -886,7 +1008,7 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
   ra.labels = q->labels;
   ra.row_weight = q->row_weight;
   ra.rows = a.rows;
-  const uint64_t row_ctas = std::min<uint64_t>(std::max<uint64_t>(ceil_div(q->rows, 32), 1), kMaxRowCtas);
+  const uint64_t row_ctas = std::min<uint64_t>(std::max<uint64_t>(ceil_div(q->rows, 4), 1), kMaxRowCtas);
   ra.chunk = (int64_t)std::max<uint64_t>(ceil_div(q->rows, row_ctas), 1);
   ra.V = a.V;
   ra.hidden = static_cast<const char*>(q->hidden);
@@ -911,13 +1033,20 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
   a.v0 = 0;
   a.vn = a.V;
   a.bn = (int)c.bn;
-  e = launch_product<LOSS, DT, CG>(along_h, along_w, along_w, a, ceil_div(q->rows, kRows) * ceil_div(q->vocab, c.bn), s);
+  a.g = ws + l.g;
+  a.piece = (int)c.piece;
+  a.keep = (int)std::min<uint64_t>(c.kept * c.piece, q->vocab);
+  const uint64_t loss_tiles = ceil_div(q->rows, kRows) * ceil_div(q->vocab, c.bn);
+  if constexpr (DT == SCAPE_BF16)
+    e = c.kept ? launch_product<LOSS, DT, CG, true>(along_h, along_w, out_g, a, loss_tiles, s)
+               : launch_product<LOSS, DT, CG>(along_h, along_w, along_w, a, loss_tiles, s);
+  else
+    e = launch_product<LOSS, DT, CG>(along_h, along_w, along_w, a, loss_tiles, s);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "product (loss): %s", cudaGetErrorString(e));
   e = launch_behind(row_losses, (unsigned)(c.cap / 32), 1024, 0, 1, s, a, (int)c.n_parts);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "row_losses: %s", cudaGetErrorString(e));
   if (!grad) return SCAPE_OK;
 
-  a.bn = kN;
   a.acc = reinterpret_cast<float*>(ws + l.acc);
   a.tail = reinterpret_cast<float*>(ws + l.tail);
   a.d_hidden = q->d_hidden;
@@ -930,7 +1059,15 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
     a.vn = (int)std::min<uint64_t>(c.piece, q->vocab - p * c.piece);
     a.first = p == 0;
     a.last = p + 1 == c.pieces;
-    e = launch_product<GRAD, DT, CG>(along_h, piece_w, out_g, a, ceil_div(q->rows, kRows) * ceil_div(a.vn, kN), s);
+    if (p < c.kept) {
+      a.g0 = (int64_t)(p * c.cap);
+      a.bn = (int)c.bn;
+      e = launch_behind(grad_kept, 8u * (unsigned)num_sms(), 256, 0, 1, s, a);
+    } else {  // (the kept ones are done with)
+      a.g0 = 0;
+      a.bn = kN;
+      e = launch_product<GRAD, DT, CG>(along_h, piece_w, out_g, a, ceil_div(q->rows, kRows) * ceil_div(a.vn, kN), s);
+    }
     if (e == cudaSuccess) e = launch_product<DH, DT, CG>(along_g, across_w, out_g, a, 0, s);
     if (e == cudaSuccess) e = launch_behind(join_parts<DH, DT, CG>, join, 256, 0, 1, s, a);
     if (e == cudaSuccess) e = launch_product<DW, DT, CG>(across_g, across_h, out_w, a, 0, s);
