@@ -72,7 +72,8 @@ struct CeArgs {
   const int32_t* label;
   const float* weight;
   float* label_logit;
-  float2* parts;           // (2 tiles of words) x cap: maximum, sum of exponentials
+  float2* parts;           // cap x n_parts (two for a tile of words): maximum, sum of exponentials
+  int n_parts;
   float2* stats;           // cap: maximum, log2 of the sum
   int32_t* live;
   float* scale;            // 2^k, 2^-k
@@ -285,7 +286,7 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
     }
     const float s = sum.x + sum.y;
     if (r < live) {
-      a.parts[(int64_t)(u.n * 2 + half) * a.cap + r] = make_float2(m, s);
+      a.parts[(int64_t)r * a.n_parts + u.n * 2 + half] = make_float2(m, s);
       if (mine) a.label_logit[r] = y;
     }
   } else if constexpr (JOB == GRAD) {
@@ -643,95 +644,92 @@ __global__ __launch_bounds__(kRowThreads) void take_rows(const RowsArgs a) {
   }
 }
 
-// 32 rows a CTA, their parts in 32 slices: maximum and sum of the row, and its loss.
-__global__ __launch_bounds__(1024) void row_losses(const CeArgs a, int n_parts) {
-  __shared__ float2 part[32][33];
-  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+// A warp a row: maximum and sum of its parts, and its loss.
+__global__ __launch_bounds__(256) void row_losses(const CeArgs a) {
   grid_launch_dependents();
   grid_dependency_wait();
-  const int live = *a.live;
-  if (blockIdx.x * 32 >= live) return;
-  const int r = blockIdx.x * 32 + lane;
+  const int lane = threadIdx.x & 31, r = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (r >= *a.live) return;
   auto join = [](float2 p, float2 q) {
     const float m = fmaxf(p.x, q.x), by = shift_of(m);
     return make_float2(m, p.y * ex2((p.x - by) * kLog2e) + q.y * ex2((q.x - by) * kLog2e));
   };
   float2 p = make_float2(neg_inf(), 0.0f);
-  if (r < live) {
-#pragma unroll 4
-    for (int i = slice; i < n_parts; i += 32) p = join(p, a.parts[(int64_t)i * a.cap + r]);
-  }
-  part[slice][lane] = p;
-  __syncthreads();
-  // a warp joins the slices of one row
-  p = part[lane][slice];
+#pragma unroll 8
+  for (int i = lane; i < a.n_parts; i += 32) p = join(p, a.parts[(int64_t)r * a.n_parts + i]);
 #pragma unroll
   for (int o = 16; o; o >>= 1)
     p = join(p, make_float2(__shfl_xor_sync(kFull, p.x, o), __shfl_xor_sync(kFull, p.y, o)));
-  const int row = blockIdx.x * 32 + slice;
-  if (lane == 0 && row < live) {
-    a.stats[row] = make_float2(p.x, log2f(p.y));
-    const float loss = a.weight[row] * ((p.x - a.label_logit[row]) + logf(p.y));
-    a.loss[a.map[row]] = *a.status ? __uint_as_float(0x7FFFFFFFu) : loss;
+  if (lane == 0) {
+    a.stats[r] = make_float2(p.x, log2f(p.y));
+    const float loss = a.weight[r] * ((p.x - a.label_logit[r]) + logf(p.y));
+    a.loss[a.map[r]] = *a.status ? __uint_as_float(0x7FFFFFFFu) : loss;
   }
 }
 
 // G of a piece in the place of its kept exponentials e:
 //   p = e 2^((m_part - m) log2e - log2 sum - 15),  G = w 2^k (p - [label])
-// A warp has eight vectors of a row at a time.
-__global__ __launch_bounds__(256) void grad_kept(const CeArgs a) {
+// A warp has a run of a row, four vectors a lane.
+__global__ __launch_bounds__(256, 6) void grad_kept(const CeArgs a) {
   using E = Elem<SCAPE_BF16>;
-  constexpr int kVecs = 8;
+  constexpr int kVecs = 4, kRun = 32 * kVecs;
   grid_launch_dependents();
   grid_dependency_wait();
   const int live = *a.live, lane = threadIdx.x & 31;
   const int64_t rows = min((int64_t)(live + 255) / 256 * 256, a.cap);  // (as many as DH and DW read)
-  const int vecs = (a.vn + 7) / 8, runs = (vecs + 32 * kVecs - 1) / (32 * kVecs);
-  const int tail = a.piece / 8;  // vectors of a row, those behind the last word included
+  const int vecs = a.piece / 8, runs = (vecs + kRun - 1) / kRun;       // (beside the last word, too)
+  const float scale = a.scale[0];
   for (int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); item < rows * runs; item += (int64_t)gridDim.x * 8) {
-    const int r = (int)(item / runs), v0 = (int)(item - (int64_t)r * runs) * 32 * kVecs + lane;
-    const bool on = r < live, last = v0 - lane + 32 * kVecs >= vecs;
+    const int r = (int)(item / runs), v0 = (int)(item - (int64_t)r * runs) * kRun + lane;
     uint4* row = reinterpret_cast<uint4*>(static_cast<char*>(a.g) + (a.g0 + r) * a.piece * 2);
+    if (r >= live) {
+#pragma unroll
+      for (int i = 0; i < kVecs; i++)
+        if (v0 + 32 * i < vecs) row[v0 + 32 * i] = make_uint4(0, 0, 0, 0);
+      continue;
+    }
     uint4 e[kVecs];
-    float f[kVecs];
-    if (on) {
-      const float2 st = a.stats[r];
-      const float w = a.weight[r] * a.scale[0];
+    float m[kVecs];
 #pragma unroll
-      for (int i = 0; i < kVecs; i++) {
-        const int v = v0 + 32 * i;
-        if (v < vecs) {
-          e[i] = row[v];
-          const int word = a.v0 + 8 * v, tile = word / a.bn, part = 2 * tile + (word - tile * a.bn >= 128);
-          const float m = a.parts[(int64_t)part * a.cap + r].x;
-          f[i] = w * ex2(__fmaf_rn(m - st.x, kLog2e, -st.y) - 15.0f);
-        }
+    for (int i = 0; i < kVecs; i++) {
+      const int v = v0 + 32 * i, word = a.v0 + 8 * v;
+      m[i] = neg_inf();
+      if (v < vecs && word < a.V) {
+        e[i] = ld_row_u4(row + v);
+        const int tile = word / a.bn;
+        m[i] = a.parts[(int64_t)r * a.n_parts + 2 * tile + (word - tile * a.bn >= 128)].x;
       }
-      const int label = a.label[r] - a.v0;
+    }
+    const float2 st = a.stats[r];
+    const float w = a.weight[r] * scale;
+    const int label = a.label[r] - a.v0;
 #pragma unroll
-      for (int i = 0; i < kVecs; i++) {
-        const int v = v0 + 32 * i;
-        if (v >= vecs) continue;
-        float x[8];
+    for (int i = 0; i < kVecs; i++) {
+      const int v = v0 + 32 * i, left = a.V - (a.v0 + 8 * v);  // words from here on
+      if (v >= vecs) break;
+      float x[8];
+      if (left > 0) {
+        const float f = w * ex2(__fmaf_rn(m[i] - st.x, kLog2e, -st.y) - 15.0f);
         Elem<SCAPE_F16>::unpack(e[i], x);
 #pragma unroll
-        for (int j = 0; j < 8; j++) x[j] = a.v0 + 8 * v + j < a.V ? x[j] * f[i] : 0.0f;
+        for (int j = 0; j < 8; j++) x[j] *= f;
+        if (left < 8) {
+#pragma unroll
+          for (int j = 0; j < 8; j++)
+            if (j >= left) x[j] = 0.0f;
+        }
         if ((uint32_t)(label - 8 * v) < 8u) {
           const float g = w * (ex2(__fmaf_rn(a.label_logit[r] - st.x, kLog2e, -st.y)) - 1.0f);
 #pragma unroll
           for (int j = 0; j < 8; j++)
             if (label == 8 * v + j) x[j] = g;
         }
-        row[v] = E::pack(x);
-      }
-    } else {
+      } else {
 #pragma unroll
-      for (int i = 0; i < kVecs; i++)
-        if (v0 + 32 * i < vecs) row[v0 + 32 * i] = make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < 8; j++) x[j] = 0.0f;
+      }
+      row[v] = E::pack(x);
     }
-    // what a tile of DH or DW reads beside the last word
-    if (last)
-      for (int v = vecs + lane; v < tail; v += 32) row[v] = make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -985,6 +983,7 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
   a.V = (int)q->vocab;
   constexpr int kRows = Shape<CG>::kRows;
   a.grid = num_sms() / CG;
+  a.n_parts = (int)c.n_parts;
   char* rows = ws + l.rows;
 
   const uint64_t g_rows = std::max<uint64_t>(c.kept, 1) * c.cap;
@@ -1043,7 +1042,7 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
   else
     e = launch_product<LOSS, DT, CG>(along_h, along_w, along_w, a, loss_tiles, s);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "product (loss): %s", cudaGetErrorString(e));
-  e = launch_behind(row_losses, (unsigned)(c.cap / 32), 1024, 0, 1, s, a, (int)c.n_parts);
+  e = launch_behind(row_losses, (unsigned)ceil_div(std::max<uint64_t>(q->rows, 1), 8), 256, 0, 1, s, a);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "row_losses: %s", cudaGetErrorString(e));
   if (!grad) return SCAPE_OK;
 
@@ -1062,7 +1061,7 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
     if (p < c.kept) {
       a.g0 = (int64_t)(p * c.cap);
       a.bn = (int)c.bn;
-      e = launch_behind(grad_kept, 8u * (unsigned)num_sms(), 256, 0, 1, s, a);
+      e = launch_behind(grad_kept, 6u * (unsigned)num_sms(), 256, 0, 1, s, a);
     } else {  // (the kept ones are done with)
       a.g0 = 0;
       a.bn = kN;

@@ -9,6 +9,7 @@ fp16 or fp32, of any size.
 from __future__ import annotations
 
 import ctypes
+from array import array
 
 from . import objective as _o
 from .scape import GradsArgs
@@ -31,23 +32,29 @@ def _flat(grads, name: str):
 
 
 def _describe(flat, name: str, dev):
-    """Arrays of the tensors' addresses, sizes and types, checked."""
-    t = _o.torch.Tensor
-    codes, n = _o._codes, len(flat)
-    for x in flat:
-        if not isinstance(x, t):
-            raise ValueError(f"{name} must hold tensors, not {type(x).__name__}")
-    if not all(map(t.is_contiguous, flat)):
+    """Arrays of the tensors' addresses, sizes and types, checked.  (Lists have
+    hundreds of tensors: each is gone through by calls that stay in C.)"""
+    t, codes = _o.torch.Tensor, _o._codes
+    try:
+        contiguous = all(map(t.is_contiguous, flat))
+    except TypeError:
+        bad = next(x for x in flat if not isinstance(x, t))
+        raise ValueError(f"{name} must hold tensors, not {type(bad).__name__}") from None
+    if not contiguous:
         raise ValueError(f"{name} must hold contiguous tensors")
     where = set(map(t.get_device, flat))
     if where - {dev}:
         raise ValueError(f"{name} must be on the current CUDA device ({dev}), not on {sorted(where)} (-1: CPU)")
+    dtypes = [x.dtype for x in flat]
     try:
-        types = bytes([codes[x.dtype] for x in flat])
+        types = {d: codes[d] for d in set(dtypes)}
     except KeyError as e:
         raise ValueError(f"{name} must hold bfloat16, float16 or float32, not {e.args[0]}") from None
-    numel = list(map(t.numel, flat))
-    return (ctypes.c_uint64 * n)(*map(t.data_ptr, flat)), numel, (ctypes.c_uint64 * n)(*numel), types
+    if len(types) == 1:
+        types = bytes(types.values()) * len(flat)
+    else:
+        types = bytes([types[d] for d in dtypes])
+    return array("Q", map(t.data_ptr, flat)), array("Q", map(t.numel, flat)), types
 
 
 def _run(grads, max_norm, out, clip: bool, stream):
@@ -59,11 +66,11 @@ def _run(grads, max_norm, out, clip: bool, stream):
     torch, lib = _o.torch, _o._lib
     dev = torch.cuda.current_device()
     flat, first = _flat(grads, "grads")
-    ptrs, sizes, numel, types = _describe(flat, "grads", dev)
+    ptrs, numel, types = _describe(flat, "grads", dev)
+    first = array("Q", first)
     groups = len(first) - 1
-    first = (ctypes.c_uint64 * (groups + 1))(*first)
-    args = GradsArgs(ctypes.addressof(ptrs), ctypes.addressof(numel), ctypes.cast(types, ctypes.c_void_p),
-                     len(flat), groups, ctypes.addressof(first))
+    args = GradsArgs(ptrs.buffer_info()[0], numel.buffer_info()[0], ctypes.cast(types, ctypes.c_void_p),
+                     len(flat), groups, first.buffer_info()[0])
     need = ctypes.c_uint64()
     _o._check(lib.scape_grad_workspace(ctypes.byref(args), ctypes.byref(need)))
     norms = torch.empty(groups, dtype=torch.float32, device=dev)
@@ -75,11 +82,11 @@ def _run(grads, max_norm, out, clip: bool, stream):
     optrs = otypes = None
     if out is not None:
         oflat, _ = _flat(out, "out")
-        optrs, osizes, _, otypes = _describe(oflat, "out", dev)
-        if osizes != sizes:
+        optrs, onumel, otypes = _describe(oflat, "out", dev)
+        if onumel != numel:
             raise ValueError("out must hold one tensor of the same size for each of grads")
     _o._check(lib.scape_clip_grads(ctypes.byref(args), max_norm,
-                                   None if optrs is None else ctypes.addressof(optrs), otypes,
+                                   None if optrs is None else optrs.buffer_info()[0], otypes,
                                    norms.data_ptr(), ws.data_ptr(), need.value, raw))
     return norms
 
