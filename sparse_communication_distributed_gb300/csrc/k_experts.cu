@@ -6,7 +6,8 @@
 // chunk's first place in every expert's segment, place_choices ranks the choices
 // inside a chunk (a warp's 32 at a time, equal experts found with match.any) and
 // writes both directions of the permutation.  Up to one chunk of choices all of it
-// is one kernel of one CTA.
+// is one kernel of one CTA; up to kFewChunks chunks place_choices adds up the counts
+// itself, which is sooner done than another kernel started.
 //
 // Rows move in 16-byte vectors where their length and addresses allow, else in
 // units of 4 or 2 bytes.  A token's row is read once and stored to its k places
@@ -28,6 +29,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kRounds = 8;                          // choices of a thread
 constexpr int kChunk = kThreads * kRounds;          // choices of a CTA
 constexpr int kMaxExperts = 1024, kMaxChoices = 32;
+constexpr int kFewChunks = 64;
 
 struct PlanArgs {
   const int32_t* idx;
@@ -54,6 +56,8 @@ __global__ __launch_bounds__(kThreads) void place_counts(const PlanArgs a) {
   __shared__ int32_t h[kMaxExperts];
   for (int e = threadIdx.x; e < a.E; e += kThreads) h[e] = 0;
   __syncthreads();
+  grid_dependency_wait();
+  grid_launch_dependents();  // (not before: place_choices reads idx ahead of its own wait)
   const int64_t base = (int64_t)blockIdx.x * kChunk;
 #pragma unroll
   for (int r = 0; r < kRounds; r++) {
@@ -62,12 +66,12 @@ __global__ __launch_bounds__(kThreads) void place_counts(const PlanArgs a) {
   }
   __syncthreads();
   for (int e = threadIdx.x; e < a.E; e += kThreads) a.counts[(int64_t)blockIdx.x * a.E + e] = h[e];
-  grid_launch_dependents();
 }
 
 // 32 experts a CTA, the chunks in 32 slices.
 __global__ __launch_bounds__(1024) void place_scan(const PlanArgs a) {
   __shared__ int32_t sums[32][33];
+  grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int e = blockIdx.x * 32 + lane;
@@ -95,11 +99,12 @@ __global__ __launch_bounds__(1024) void place_scan(const PlanArgs a) {
       run += c;
     }
   }
-  grid_launch_dependents();
 }
 
-// SINGLE: one chunk, whose own counts are the totals.
-template <bool SINGLE>
+// ONE: one chunk, whose own counts are the totals.  FEW: the counts are as place_counts
+// left them.  MANY: after place_scan.
+enum Chunks { ONE, FEW, MANY };
+template <Chunks C>
 __global__ __launch_bounds__(kThreads) void place_choices(const PlanArgs a) {
   __shared__ uint16_t hist[kWarps][kMaxExperts];  // a warp's choices of each expert, then those of the warps before it
   __shared__ int32_t base[kMaxExperts];           // place of the chunk's first choice of each expert
@@ -107,8 +112,13 @@ __global__ __launch_bounds__(kThreads) void place_choices(const PlanArgs a) {
   __shared__ int32_t total[kMaxExperts];
   __shared__ uint32_t scan[kWarps + 1];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  grid_launch_dependents();
   for (int i = tid; i < kWarps * kMaxExperts / 2; i += kThreads) reinterpret_cast<uint32_t*>(hist)[i] = 0;
+  if (C == FEW)
+    for (int e = tid; e < a.E; e += kThreads) base[e] = total[e] = 0;
   __syncthreads();
+  // (idx was complete before place_counts let this kernel start)
+  if (C == ONE) grid_dependency_wait();
   // a warp's choices follow one another: 32 a round
   const int64_t first = (int64_t)blockIdx.x * kChunk + wid * (32 * kRounds) + lane;
   int ex[kRounds];
@@ -139,7 +149,22 @@ __global__ __launch_bounds__(kThreads) void place_choices(const PlanArgs a) {
     if (lane == 0 && n_bad) atomicAdd(a.bad, n_bad);
   }
   __syncthreads();
-  if (!SINGLE) grid_dependency_wait();
+  if (C != ONE) grid_dependency_wait();
+  if (C == FEW) {  // threads side by side have experts side by side; as many slices of chunks as there are threads for
+    const int wide = min(kThreads, (a.E + 31) / 32 * 32), slices = kThreads / wide;
+    for (int e = tid % wide; e < a.E && tid / wide < slices; e += wide) {
+      int32_t before = 0, all = 0;
+#pragma unroll 8
+      for (int b = tid / wide; b < (int)a.chunks; b += slices) {
+        const int32_t c = a.counts[(int64_t)b * a.E + e];
+        all += c;
+        if (b < (int)blockIdx.x) before += c;
+      }
+      atomicAdd(&total[e], all);
+      atomicAdd(&base[e], before);
+    }
+    __syncthreads();
+  }
   // segments: each thread has a run of experts
   const int per = (a.E + kThreads - 1) / kThreads;
   uint32_t room = 0;
@@ -153,8 +178,10 @@ __global__ __launch_bounds__(kThreads) void place_choices(const PlanArgs a) {
         hist[w][e] = (uint16_t)own;
         own += c;
       }
-      total[e] = SINGLE ? (int32_t)own : a.totals[e];
-      base[e] = SINGLE ? 0 : a.counts[(int64_t)blockIdx.x * a.E + e];
+      if (C != FEW) {
+        total[e] = C == ONE ? (int32_t)own : a.totals[e];
+        base[e] = C == ONE ? 0 : a.counts[(int64_t)blockIdx.x * a.E + e];
+      }
       room += (uint32_t)((total[e] + a.align - 1) / a.align * a.align);
     }
   }
@@ -261,6 +288,8 @@ __device__ void clear_empty_rows(const RowArgs& a, int64_t item, int lane) {
 template <int BYTES, int R>
 __global__ __launch_bounds__(kThreads) void dispatch_rows(const RowArgs a) {
   using U = typename Unit<BYTES>::T;
+  grid_launch_dependents();
+  grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (item >= a.row_warps) {
@@ -293,6 +322,8 @@ template <int DT, int BYTES, int R>
 __global__ __launch_bounds__(kThreads, 4) void combine_rows(const RowArgs a) {
   using P = Packed<DT, BYTES>;
   using U = typename P::U;
+  grid_launch_dependents();
+  grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (item >= a.row_warps) return;
@@ -343,6 +374,8 @@ template <int DT, int BYTES, int R>
 __global__ __launch_bounds__(kThreads) void combine_grad(const RowArgs a) {
   using P = Packed<DT, BYTES>;
   using U = typename P::U;
+  grid_launch_dependents();
+  grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (item >= a.row_warps) {
@@ -509,17 +542,20 @@ SCAPE_API int scape_expert_plan(const int32_t* idx, uint64_t tokens, int k, int 
   a.totals = static_cast<int32_t*>(workspace);
   a.counts = a.totals + experts;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
   if (a.chunks <= 1) {
-    place_choices<true><<<1, kThreads, 0, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? SCAPE_OK : fail(SCAPE_ECUDA, "place_choices: %s", cudaGetErrorString(e));
+    e = launch_behind(place_choices<ONE>, 1, kThreads, s, a);
+  } else {
+    e = launch_behind(place_counts, (unsigned)a.chunks, kThreads, s, a);
+    if (e != cudaSuccess) return fail(SCAPE_ECUDA, "place_counts: %s", cudaGetErrorString(e));
+    if (a.chunks <= kFewChunks) {
+      e = launch_behind(place_choices<FEW>, (unsigned)a.chunks, kThreads, s, a);
+    } else {
+      e = launch_behind(place_scan, (unsigned)((experts + 31) / 32), 1024, s, a);
+      if (e != cudaSuccess) return fail(SCAPE_ECUDA, "place_scan: %s", cudaGetErrorString(e));
+      e = launch_behind(place_choices<MANY>, (unsigned)a.chunks, kThreads, s, a);
+    }
   }
-  place_counts<<<(unsigned)a.chunks, kThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(SCAPE_ECUDA, "place_counts: %s", cudaGetErrorString(e));
-  e = launch_behind(place_scan, (unsigned)((experts + 31) / 32), 1024, s, a);
-  if (e != cudaSuccess) return fail(SCAPE_ECUDA, "place_scan: %s", cudaGetErrorString(e));
-  e = launch_behind(place_choices<false>, (unsigned)a.chunks, kThreads, s, a);
   return e == cudaSuccess ? SCAPE_OK : fail(SCAPE_ECUDA, "place_choices: %s", cudaGetErrorString(e));
 }
 
@@ -549,32 +585,34 @@ SCAPE_API int scape_expert_dispatch(const void* x, int dtype, uint64_t tokens, u
   unsigned grid;
   if (!grid_of(a.row_warps + (a.rows + kEmptyRows - 1) / kEmptyRows, grid)) return fail(SCAPE_EINVAL, "too many rows");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (unit == 16) dispatch_rows<16, kUnits16><<<grid, kThreads, 0, s>>>(a);
-  else if (unit == 4) dispatch_rows<4, kUnitsSmall><<<grid, kThreads, 0, s>>>(a);
-  else dispatch_rows<2, kUnitsSmall><<<grid, kThreads, 0, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if (unit == 16) e = launch_behind(dispatch_rows<16, kUnits16>, grid, kThreads, s, a);
+  else if (unit == 4) e = launch_behind(dispatch_rows<4, kUnitsSmall>, grid, kThreads, s, a);
+  else e = launch_behind(dispatch_rows<2, kUnitsSmall>, grid, kThreads, s, a);
   return e == cudaSuccess ? SCAPE_OK : fail(SCAPE_ECUDA, "dispatch_rows: %s", cudaGetErrorString(e));
 }
 
 namespace scape {
 namespace {
 template <int DT>
-void launch_combine(const RowArgs& a, int unit, unsigned grid, bool back, cudaStream_t s) {
+cudaError_t launch_combine(const RowArgs& a, int unit, unsigned grid, bool back, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
   if (unit == 16) {
-    if (back) combine_grad<DT, 16, kUnits16><<<grid, kThreads, 0, s>>>(a);
-    else combine_rows<DT, 16, kCombine16><<<grid, kThreads, 0, s>>>(a);
+    if (back) e = launch_behind(combine_grad<DT, 16, kUnits16>, grid, kThreads, s, a);
+    else e = launch_behind(combine_rows<DT, 16, kCombine16>, grid, kThreads, s, a);
   } else if (unit == 4) {
-    if (back) combine_grad<DT, 4, kUnitsSmall><<<grid, kThreads, 0, s>>>(a);
-    else combine_rows<DT, 4, kCombineSmall><<<grid, kThreads, 0, s>>>(a);
+    if (back) e = launch_behind(combine_grad<DT, 4, kUnitsSmall>, grid, kThreads, s, a);
+    else e = launch_behind(combine_rows<DT, 4, kCombineSmall>, grid, kThreads, s, a);
   } else if constexpr (DT != SCAPE_F32) {
-    if (back) combine_grad<DT, 2, kUnitsSmall><<<grid, kThreads, 0, s>>>(a);
-    else combine_rows<DT, 2, kCombineSmall><<<grid, kThreads, 0, s>>>(a);
+    if (back) e = launch_behind(combine_grad<DT, 2, kUnitsSmall>, grid, kThreads, s, a);
+    else e = launch_behind(combine_rows<DT, 2, kCombineSmall>, grid, kThreads, s, a);
   }
+  return e;
 }
-void launch_combine_any(int dtype, const RowArgs& a, int unit, unsigned grid, bool back, cudaStream_t s) {
-  if (dtype == SCAPE_BF16) launch_combine<SCAPE_BF16>(a, unit, grid, back, s);
-  else if (dtype == SCAPE_F16) launch_combine<SCAPE_F16>(a, unit, grid, back, s);
-  else launch_combine<SCAPE_F32>(a, unit, grid, back, s);
+cudaError_t launch_combine_any(int dtype, const RowArgs& a, int unit, unsigned grid, bool back, cudaStream_t s) {
+  if (dtype == SCAPE_BF16) return launch_combine<SCAPE_BF16>(a, unit, grid, back, s);
+  if (dtype == SCAPE_F16) return launch_combine<SCAPE_F16>(a, unit, grid, back, s);
+  return launch_combine<SCAPE_F32>(a, unit, grid, back, s);
 }
 }  // namespace
 }  // namespace scape
@@ -600,8 +638,7 @@ SCAPE_API int scape_expert_combine(const void* y, int dtype, uint64_t rows, uint
   a.row_warps = a.tokens * a.slices;
   unsigned grid;
   if (!grid_of(a.row_warps, grid)) return fail(SCAPE_EINVAL, "too many rows");
-  launch_combine_any(dtype, a, unit, grid, false, static_cast<cudaStream_t>(stream));
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_combine_any(dtype, a, unit, grid, false, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SCAPE_OK : fail(SCAPE_ECUDA, "combine_rows: %s", cudaGetErrorString(e));
 }
 
@@ -634,7 +671,6 @@ SCAPE_API int scape_expert_combine_backward(const void* d_out, const void* y, in
   a.row_warps = a.tokens * a.k;
   unsigned grid;
   if (!grid_of(a.row_warps + (a.rows + kEmptyRows - 1) / kEmptyRows, grid)) return fail(SCAPE_EINVAL, "too many rows");
-  launch_combine_any(dtype, a, unit, grid, true, static_cast<cudaStream_t>(stream));
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_combine_any(dtype, a, unit, grid, true, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SCAPE_OK : fail(SCAPE_ECUDA, "combine_grad: %s", cudaGetErrorString(e));
 }

@@ -133,6 +133,8 @@ template <int CAP, int DT>
 __global__ __launch_bounds__(kThreads, kResident) void norm_chunks(const __grid_constant__ Table<CAP> tb,
                                                                    double* __restrict__ part) {
   __shared__ double buf[32];
+  grid_launch_dependents();
+  grid_dependency_wait();
   for (uint32_t c = blockIdx.x; c < tb.chunks; c += gridDim.x) {
     const Tensor& t = tb.t[tensor_of(tb, c)];
     const uint64_t first = (uint64_t)(c - t.chunk0) * tb.chunk_elems;
@@ -140,7 +142,6 @@ __global__ __launch_bounds__(kThreads, kResident) void norm_chunks(const __grid_
     const double d = cta_sum(chunk_squares<DT>(t.src, first, n), buf);
     if (threadIdx.x == 0) part[t.part0 + (c - t.chunk0)] = d;
   }
-  grid_launch_dependents();
 }
 
 struct Groups {
@@ -153,6 +154,7 @@ __global__ __launch_bounds__(1024) void norm_finish(const __grid_constant__ Grou
                                                     float* __restrict__ norms,
                                                     float* __restrict__ scales) {
   __shared__ double buf[32];
+  grid_launch_dependents();
   grid_dependency_wait();
   double d = 0.0;
 #pragma unroll 8
@@ -166,7 +168,6 @@ __global__ __launch_bounds__(1024) void norm_finish(const __grid_constant__ Grou
     if (scales)
       scales[blockIdx.x] = norm > (double)max_norm && norm < INFINITY ? (float)((double)max_norm / norm) : 1.0f;
   }
-  grid_launch_dependents();
 }
 
 // A streaming store of 16 bytes: it does not push what is still to be read out of L2.
@@ -251,6 +252,7 @@ __device__ __forceinline__ void scale_chunk(const void* from, void* to, uint32_t
 template <int CAP, int SDT, int DDT>
 __global__ __launch_bounds__(kThreads, kResident) void clip_chunks(const __grid_constant__ Table<CAP> tb,
                                                                    const float* __restrict__ scales) {
+  grid_launch_dependents();
   grid_dependency_wait();
   for (uint32_t i = blockIdx.x; i < tb.chunks; i += gridDim.x) {
     const uint32_t c = tb.chunks - 1 - i;  // what was read last comes first
@@ -388,7 +390,7 @@ struct Todo {
 
 // The tensors that "list" names into one table, and its launch.
 template <int CAP, int SDT, int DDT>
-cudaError_t launch_table(const Todo& q, const std::vector<uint32_t>& list, size_t i0, size_t i1, bool behind,
+cudaError_t launch_table(const Todo& q, const std::vector<uint32_t>& list, size_t i0, size_t i1,
                          cudaStream_t s) {
   Table<CAP> tb;
   tb.n = (int)(i1 - i0);
@@ -400,46 +402,39 @@ cudaError_t launch_table(const Todo& q, const std::vector<uint32_t>& list, size_
     tb.chunks += q.chunks_of(i);
   }
   const unsigned grid = std::min<unsigned>(tb.chunks, (unsigned)(kResident * num_sms()));
-  if (!q.out) {
-    if constexpr (DDT == SCAPE_BF16) norm_chunks<CAP, SDT><<<grid, kThreads, 0, s>>>(tb, q.part);
-  } else if (behind) {
-    return launch_behind(clip_chunks<CAP, SDT, DDT>, grid, kThreads, s, tb, q.scales);
-  } else {
-    clip_chunks<CAP, SDT, DDT><<<grid, kThreads, 0, s>>>(tb, q.scales);
-  }
-  return cudaGetLastError();
+  if (q.out) return launch_behind(clip_chunks<CAP, SDT, DDT>, grid, kThreads, s, tb, q.scales);
+  if constexpr (DDT == SCAPE_BF16) return launch_behind(norm_chunks<CAP, SDT>, grid, kThreads, s, tb, q.part);
+  return cudaSuccess;
 }
 
 // All tensors of one type (and one type of results): as many tables as they need, small
 // parameters for small calls.
 constexpr int kSmallTable = 16, kLargeTable = 600;
 template <int SDT, int DDT>
-cudaError_t launch_tables(const Todo& q, bool& behind, cudaStream_t s) {
+cudaError_t launch_tables(const Todo& q, cudaStream_t s) {
   std::vector<uint32_t> list;
   for (uint32_t i = 0; i < q.g->n_tensors; i++)
     if (q.g->numel[i] && q.g->dtypes[i] == SDT && (!q.out || q.out_dtypes[i] == DDT)) list.push_back(i);
   for (size_t i0 = 0; i0 < list.size(); i0 += kLargeTable) {
     const size_t i1 = std::min(list.size(), i0 + kLargeTable);
-    const cudaError_t e = i1 - i0 <= (size_t)kSmallTable ? launch_table<kSmallTable, SDT, DDT>(q, list, i0, i1, behind, s)
-                                                         : launch_table<kLargeTable, SDT, DDT>(q, list, i0, i1, behind, s);
+    const cudaError_t e = i1 - i0 <= (size_t)kSmallTable ? launch_table<kSmallTable, SDT, DDT>(q, list, i0, i1, s)
+                                                         : launch_table<kLargeTable, SDT, DDT>(q, list, i0, i1, s);
     if (e != cudaSuccess) return e;
-    behind = false;  // (only the first follows norm_finish directly)
   }
   return cudaSuccess;
 }
 
 template <int SDT>
-cudaError_t launch_from(const Todo& q, bool& behind, cudaStream_t s) {
-  cudaError_t e = launch_tables<SDT, SCAPE_BF16>(q, behind, s);
-  if (e == cudaSuccess && q.out) e = launch_tables<SDT, SCAPE_F16>(q, behind, s);
-  if (e == cudaSuccess && q.out) e = launch_tables<SDT, SCAPE_F32>(q, behind, s);
+cudaError_t launch_from(const Todo& q, cudaStream_t s) {
+  cudaError_t e = launch_tables<SDT, SCAPE_BF16>(q, s);
+  if (e == cudaSuccess && q.out) e = launch_tables<SDT, SCAPE_F16>(q, s);
+  if (e == cudaSuccess && q.out) e = launch_tables<SDT, SCAPE_F32>(q, s);
   return e;
 }
 cudaError_t launch_all(const Todo& q, cudaStream_t s) {
-  bool behind = true;
-  cudaError_t e = launch_from<SCAPE_BF16>(q, behind, s);
-  if (e == cudaSuccess) e = launch_from<SCAPE_F16>(q, behind, s);
-  if (e == cudaSuccess) e = launch_from<SCAPE_F32>(q, behind, s);
+  cudaError_t e = launch_from<SCAPE_BF16>(q, s);
+  if (e == cudaSuccess) e = launch_from<SCAPE_F16>(q, s);
+  if (e == cudaSuccess) e = launch_from<SCAPE_F32>(q, s);
   return e;
 }
 

@@ -589,10 +589,11 @@ __global__ __launch_bounds__(kRowThreads) void take_rows(const RowsArgs a) {
   uint32_t before = 0, n_bad = 0;
   int64_t y;
   float w;
+  grid_dependency_wait();
 #pragma unroll 8
   for (int64_t r = tid; r < begin; r += kRowThreads) before += look(r, y, w);
   int64_t at = cta_sum(before, ubuf);  // (rows < 2^24)
-  grid_launch_dependents();
+  grid_launch_dependents();  // (not ahead of the wait: LOSS loads weights ahead of its own)
   const uint32_t vecs = (uint32_t)(a.bytes / 16);  // (up to 8192, of 512 rows)
   const uint4 zero = make_uint4(0, 0, 0, 0);
   for (int64_t r0 = begin; r0 < end; r0 += kRowThreads) {
@@ -670,7 +671,7 @@ __global__ __launch_bounds__(256) void row_losses(const CeArgs a) {
 // G of a piece in the place of its kept exponentials e:
 //   p = e 2^((m_part - m) log2e - log2 sum - 15),  G = w 2^k (p - [label])
 // A warp has a run of a row, four vectors a lane.
-__global__ __launch_bounds__(256, 6) void grad_kept(const CeArgs a) {
+__global__ __launch_bounds__(256, 5) void grad_kept(const CeArgs a) {
   using E = Elem<SCAPE_BF16>;
   constexpr int kVecs = 4, kRun = 32 * kVecs;
   grid_launch_dependents();
@@ -1025,8 +1026,8 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
   ra.loss = q->loss;
   ra.bad = q->bad_count;
   ra.target = DT == SCAPE_F16 ? 16384.0f : 1.0f;
-  take_rows<<<(unsigned)std::max<uint64_t>(ceil_div(q->rows, (uint64_t)ra.chunk), 1), kRowThreads, 0, s>>>(ra);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_behind(take_rows, (unsigned)std::max<uint64_t>(ceil_div(q->rows, (uint64_t)ra.chunk), 1),
+                                kRowThreads, 0, 1, s, ra);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "take_rows: %s", cudaGetErrorString(e));
 
   a.v0 = 0;
@@ -1061,7 +1062,7 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
     if (p < c.kept) {
       a.g0 = (int64_t)(p * c.cap);
       a.bn = (int)c.bn;
-      e = launch_behind(grad_kept, 6u * (unsigned)num_sms(), 256, 0, 1, s, a);
+      e = launch_behind(grad_kept, 5u * (unsigned)num_sms(), 256, 0, 1, s, a);
     } else {  // (the kept ones are done with)
       a.g0 = 0;
       a.bn = kN;
