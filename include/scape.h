@@ -499,9 +499,9 @@ int scape_route_backward(const scape_route_args* args, const int32_t* idx, const
  *
  * hidden and weight have one type, bf16 or fp16, and so have their gradients.
  * Products are of 16-bit operands added up in fp32; statistics and losses are fp32.
- * G is rounded to the operands' type (for fp16 after scaling the weights by a power
- * of two, so that its entries keep their precision down to 2^-28 of the largest
- * weight), each gradient once more.  dim is a multiple of 8, matrices are 16-byte
+ * G is rounded to the operands' type (after dividing the weights by the largest of
+ * them; for fp16 its entries then keep their precision down to 2^-28), each gradient
+ * once more.  dim is a multiple of 8, matrices are 16-byte
  * aligned with strides of a multiple of 8 elements.  The kernels' waits are bounded:
  * one that ran out (which says that the GPU or the library is at fault) makes all
  * losses NaN. */

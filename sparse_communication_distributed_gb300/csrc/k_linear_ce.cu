@@ -24,9 +24,11 @@
 // together first, so that neither time nor the gradients depend on what they hold.
 //
 // G is rounded to the operands' type: its entries carry half a step of it, as the
-// results do.  Row weights are first multiplied by a power of two (2^k, by the
-// largest of them) that keeps fp16 entries clear of both ends of their range, and
-// the results by 2^-k.
+// results do.  Row weights are first divided by the largest of them, and the results
+// multiplied by it: where all weights are the same, as those of a mean, the labels'
+// entries, w (p - 1), are then next to -1 and not all rounded the same way (of bf16
+// results 4.5e-3 instead of 1.8e-3 off).  For fp16 they are multiplied by 2^14, too,
+// which keeps small entries clear of the end of its range.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -72,11 +74,14 @@ struct CeArgs {
   const int32_t* label;
   const float* weight;
   float* label_logit;
+  float* left;             // what rounding took from the label's entry of G
+  const void* w;           // vocab x D
+  int64_t w_stride;
   float2* parts;           // cap x n_parts (two for a tile of words): maximum, sum of exponentials
   int n_parts;
   float2* stats;           // cap: maximum, log2 of the sum
   int32_t* live;
-  float* scale;            // 2^k, 2^-k
+  float* scale;            // of the weights, and its reciprocal
   uint32_t* status;        // 0, or a wait ran out
   float* loss;             // caller's
   int64_t rows, cap;       // caller's rows; rounded up to a multiple of 256
@@ -186,6 +191,27 @@ __device__ __forceinline__ void store32(void* row, int c, int n, const float (&f
       for (int i = 0; i < 8; i++) g[i] = f[8 * j + i];
       reinterpret_cast<uint4*>(p)[j] = E::pack(g);
     }
+}
+
+// A number as the operands' type holds it.
+template <int DT>
+__device__ __forceinline__ float rounded(float x) {
+  const typename Elem<DT>::T t = Elem<DT>::make(x);
+  return Elem<DT>::load(&t);
+}
+
+// Eight columns of a row of dH, from d on, with the part of the label's entry that its
+// rounding in G took away.  That entry is the largest of most rows, next to -w, and
+// without this its rounding would be most of the error of dH.
+template <int DT>
+__device__ __forceinline__ void add_left(const CeArgs& a, int r, int d, float (&f)[8]) {
+  using E = Elem<DT>;
+  const typename E::T* w = static_cast<const typename E::T*>(a.w) + (int64_t)a.label[r] * a.w_stride + d;
+  float x[8];
+  E::unpack(ld_row_u4(w), x);
+  const float left = a.left[r];
+#pragma unroll
+  for (int j = 0; j < 8; j++) f[j] = __fmaf_rn(left, x[j], f[j]);
 }
 
 // 32 results of a row into the warp's buffer, whose rows hold 64 of them in swizzled
@@ -304,13 +330,15 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
         f[i] = p.x;
         f[i + 1] = p.y;
       }
-      if ((uint32_t)(label - w0) < 32u) {
-#pragma unroll
-        for (int i = 0; i < 32; i++)
-          if (label == w0 + i) f[i] -= 1.0f;
-      }
 #pragma unroll
       for (int i = 0; i < 32; i++) f[i] *= w;
+      if ((uint32_t)(label - w0) < 32u) {
+        float g = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; i++)
+          if (label == w0 + i) g = f[i] -= w;
+        a.left[r] = g - rounded<DT>(g);
+      }
       if (!on || w0 + 32 > a.V) {
 #pragma unroll
         for (int i = 0; i < 32; i++)
@@ -349,9 +377,18 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
           for (int j = 0; j < 8; j++)
             sums[(c * 8 + j) * kM] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
         } else if (on) {
+          typename Elem<DT>::T* to = static_cast<typename Elem<DT>::T*>(a.d_hidden) + (int64_t)a.map[r] * a.dh_stride + d0;
 #pragma unroll
-          for (int i = 0; i < 32; i++) f[i] *= un;
-          store32<DT>(static_cast<char*>(a.d_hidden) + (int64_t)a.map[r] * a.dh_stride * 2, d0, a.D, f);
+          for (int j = 0; j < 4; j++)
+            if (d0 + 8 * j < a.D) {
+              float g[8];
+#pragma unroll
+              for (int i = 0; i < 8; i++) g[i] = f[8 * j + i];
+              add_left<DT>(a, r, d0 + 8 * j, g);
+#pragma unroll
+              for (int i = 0; i < 8; i++) g[i] *= un;
+              reinterpret_cast<uint4*>(to)[j] = Elem<DT>::pack(g);
+            }
         }
       } else {
 #pragma unroll
@@ -563,7 +600,7 @@ struct RowsArgs {
   uint32_t* status;
   float* loss;
   uint32_t* bad;
-  float target;  // the largest weight is scaled to between target and 2 target
+  float target;  // what the largest weight becomes
 };
 
 // The rows with a term, together and in their order.  Each CTA takes a chunk of the
@@ -638,8 +675,9 @@ __global__ __launch_bounds__(kRowThreads) void take_rows(const RowsArgs a) {
     *a.live = (int32_t)at;
     *a.status = 0u;
     float s = 1.0f;
-    const int e = (int)((__float_as_uint(top) >> 23) & 0xFF);  // (0: no weight or a denormal one)
-    if (e > 0) s = a.target * __uint_as_float((uint32_t)min(max(254 - e, 30), 224) << 23);
+    const int e = (int)((__float_as_uint(top) >> 23) & 0xFF);
+    if (e >= 30 && e <= 224) s = a.target / top;
+    else if (e > 0) s = a.target * (e < 30 ? 0x1p97f : 0x1p-97f);  // (0: no weight or a denormal one)
     a.scale[0] = s;
     a.scale[1] = 1.0f / s;
   }
@@ -669,7 +707,7 @@ __global__ __launch_bounds__(256) void row_losses(const CeArgs a) {
 }
 
 // G of a piece in the place of its kept exponentials e:
-//   p = e 2^((m_part - m) log2e - log2 sum - 15),  G = w 2^k (p - [label])
+//   p = e 2^((m_part - m) log2e - log2 sum - 15),  G = w (p - [label]), w scaled
 // A warp has a run of a row, four vectors a lane.
 __global__ __launch_bounds__(256, 5) void grad_kept(const CeArgs a) {
   using E = Elem<SCAPE_BF16>;
@@ -721,6 +759,7 @@ __global__ __launch_bounds__(256, 5) void grad_kept(const CeArgs a) {
         }
         if ((uint32_t)(label - 8 * v) < 8u) {
           const float g = w * (ex2(__fmaf_rn(a.label_logit[r] - st.x, kLog2e, -st.y)) - 1.0f);
+          a.left[r] = g - rounded<SCAPE_BF16>(g);
 #pragma unroll
           for (int j = 0; j < 8; j++)
             if (label == 8 * v + j) x[j] = g;
@@ -771,6 +810,7 @@ __global__ __launch_bounds__(256) void join_parts(const CeArgs a) {
       }
     }
     if (d >= a.D || (JOB == DH ? r >= live : a.v0 + r >= a.V)) continue;
+    if (JOB == DH) add_left<DT>(a, r, d, f);
 #pragma unroll
     for (int e = 0; e < 8; e++) f[e] *= un;
     typename Elem<DT>::T* out =
@@ -872,7 +912,7 @@ Cut cut_of(const scape_linear_ce_args* q, bool grad) {
 }
 
 struct Layout {
-  uint64_t map, label, weight, logit, parts, stats, head, rows, g, acc, tail, bytes;
+  uint64_t map, label, weight, logit, left, parts, stats, head, rows, g, acc, tail, bytes;
 };
 
 Layout layout_of(const scape_linear_ce_args* q, const Cut& c, bool grad) {
@@ -888,6 +928,7 @@ Layout layout_of(const scape_linear_ce_args* q, const Cut& c, bool grad) {
   l.label = take(c.cap * 4);
   l.weight = take(c.cap * 4);
   l.logit = take(c.cap * 4);
+  l.left = take(c.cap * 4);
   l.stats = take(c.cap * 8);
   l.parts = take(c.n_parts * c.cap * 8);
   l.rows = take(c.cap * q->dim * 2);
@@ -972,6 +1013,9 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
   a.label = reinterpret_cast<int32_t*>(ws + l.label);
   a.weight = reinterpret_cast<float*>(ws + l.weight);
   a.label_logit = reinterpret_cast<float*>(ws + l.logit);
+  a.left = reinterpret_cast<float*>(ws + l.left);
+  a.w = q->weight;
+  a.w_stride = (int64_t)q->weight_stride;
   a.parts = reinterpret_cast<float2*>(ws + l.parts);
   a.stats = reinterpret_cast<float2*>(ws + l.stats);
   a.live = reinterpret_cast<int32_t*>(ws + l.head);
