@@ -13,12 +13,11 @@
 //         that piece
 //   DH    G W, added up over the pieces in fp32
 //   DW    G^T H, complete for the piece's words
-// With GRAD a gradient costs 8 T D V operations, without it 6.  What LOSS keeps of a
-// bf16 problem are exponentials against the maximum of their 128 words, in fp16 times
-// 2^15: their rounding (half a step is 2^-11) does not count beside that of G (2^-8),
-// and G takes their place (grad_kept).  Logits in 16 bits would not do: exp() makes an
-// error of 2^-8 |l| of them.  For fp16, whose G is rounded to 2^-11 itself, nothing is
-// kept.
+// With GRAD a gradient costs 8 T D V operations, without it 6.  What LOSS keeps are
+// exponentials against the maximum of their 128 words, in fp16 times 2^15: their
+// rounding (half a step is 2^-11) does not count beside that of a bf16 G (2^-8) and is
+// as large as that of an fp16 one, and G takes their place (grad_kept).  Logits in 16
+// bits would not do: exp() makes an error of 2^-8 |l| of them.
 //
 // Rows without a term (no label, weight 0) are left out: the others are copied
 // together first, so that neither time nor the gradients depend on what they hold.
@@ -178,7 +177,7 @@ __device__ __forceinline__ Units units_of(const CeArgs& a, int live) {
   return u;
 }
 
-// 32 results of a row, columns [c, c + 32) of which those below n exist (n a multiple of 8).
+// 32 numbers of a row, columns [c, c + 32) of which those below n exist (n a multiple of 8).
 template <int DT>
 __device__ __forceinline__ void store32(void* row, int c, int n, const float (&f)[32]) {
   using E = Elem<DT>;
@@ -709,8 +708,9 @@ __global__ __launch_bounds__(256) void row_losses(const CeArgs a) {
 // G of a piece in the place of its kept exponentials e:
 //   p = e 2^((m_part - m) log2e - log2 sum - 15),  G = w (p - [label]), w scaled
 // A warp has a run of a row, four vectors a lane.
-__global__ __launch_bounds__(256, 5) void grad_kept(const CeArgs a) {
-  using E = Elem<SCAPE_BF16>;
+template <int DT>
+__global__ __launch_bounds__(256, 4) void grad_kept(const CeArgs a) {
+  using E = Elem<DT>;
   constexpr int kVecs = 4, kRun = 32 * kVecs;
   grid_launch_dependents();
   grid_dependency_wait();
@@ -759,7 +759,7 @@ __global__ __launch_bounds__(256, 5) void grad_kept(const CeArgs a) {
         }
         if ((uint32_t)(label - 8 * v) < 8u) {
           const float g = w * (ex2(__fmaf_rn(a.label_logit[r] - st.x, kLog2e, -st.y)) - 1.0f);
-          a.left[r] = g - rounded<SCAPE_BF16>(g);
+          a.left[r] = g - rounded<DT>(g);
 #pragma unroll
           for (int j = 0; j < 8; j++)
             if (label == 8 * v + j) x[j] = g;
@@ -905,8 +905,8 @@ Cut cut_of(const scape_linear_ce_args* q, bool grad) {
   const uint64_t fit = std::max<uint64_t>(kPieceBytes / (c.cap * 2 * kN), 1);
   c.piece = ceil_div(tiles, ceil_div(tiles, fit)) * kN;
   c.pieces = ceil_div(tiles * kN, c.piece);
-  // (fp16: not kept; a tile of another width may lie in two pieces)
-  if (q->dtype == SCAPE_BF16 && (c.pieces == 1 || c.bn == (uint64_t)kN))
+  // (a tile of another width may lie in two pieces)
+  if (c.pieces == 1 || c.bn == (uint64_t)kN)
     c.kept = std::min(c.pieces, std::max<uint64_t>(kAllBytes / (c.cap * c.piece * 2), 1));
   return c;
 }
@@ -1081,11 +1081,8 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
   a.piece = (int)c.piece;
   a.keep = (int)std::min<uint64_t>(c.kept * c.piece, q->vocab);
   const uint64_t loss_tiles = ceil_div(q->rows, kRows) * ceil_div(q->vocab, c.bn);
-  if constexpr (DT == SCAPE_BF16)
-    e = c.kept ? launch_product<LOSS, DT, CG, true>(along_h, along_w, out_g, a, loss_tiles, s)
-               : launch_product<LOSS, DT, CG>(along_h, along_w, along_w, a, loss_tiles, s);
-  else
-    e = launch_product<LOSS, DT, CG>(along_h, along_w, along_w, a, loss_tiles, s);
+  e = c.kept ? launch_product<LOSS, DT, CG, true>(along_h, along_w, out_g, a, loss_tiles, s)
+             : launch_product<LOSS, DT, CG>(along_h, along_w, along_w, a, loss_tiles, s);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "product (loss): %s", cudaGetErrorString(e));
   e = launch_behind(row_losses, (unsigned)ceil_div(std::max<uint64_t>(q->rows, 1), 8), 256, 0, 1, s, a);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "row_losses: %s", cudaGetErrorString(e));
@@ -1106,7 +1103,7 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
     if (p < c.kept) {
       a.g0 = (int64_t)(p * c.cap);
       a.bn = (int)c.bn;
-      e = launch_behind(grad_kept, 5u * (unsigned)num_sms(), 256, 0, 1, s, a);
+      e = launch_behind(grad_kept<DT>, 4u * (unsigned)num_sms(), 256, 0, 1, s, a);
     } else {  // (the kept ones are done with)
       a.g0 = 0;
       a.bn = kN;

@@ -8,9 +8,9 @@ add them up in fp32, at least eight at a time, each such addition off by at most
 a loss by w (2 dl + the bound of a log-sum-exp + roundings of its logits), a
 probability by the factor 2 dl + that bound, an entry of G by p times this, its
 rounding (half a step) and, for fp16, half the least step at the scale 2^14 of the
-largest weight.  For bf16 the exponentials are rounded to fp16 first, times 2^15 and
-against the largest of their 128 words, so p carries half a step of that type and half
-its least step, 2^-25, times 2^-15 of the largest p.  A gradient of n terms carries the terms' errors, n / 8 additions
+largest weight.  The exponentials are rounded to fp16 first, times 2^15 and against
+the largest of their 128 words, so p carries half a step of that type and half its
+least step, 2^-25, times 2^-15 of the largest p.  A gradient of n terms carries the terms' errors, n / 8 additions
 and its own rounding.  These bounds hold whatever the signs; roundings of random
 sign give a far smaller norm of the error, which is held to 2 half steps besides
 (one of G, one of the result; equal parts of random sign would be sqrt(2 / 3))."""
@@ -84,7 +84,7 @@ def check(H, W, y, w, dtype, grad=True, norms=True):
     G *= k
     top = float(k.abs().max()) if at.numel() else 1.0
     eG = k.abs() * p * (2 * dl + tol_l + 8 * U) if at.numel() else G
-    if dtype == "bf16" and at.numel():
+    if at.numel():
         eG = eG + k.abs() * (ROUND["f16"] * p + 2.0 ** -40 * p.amax(1, keepdim=True))
     eG = eG + ROUND[dtype] * G.abs() + (top * 2.0 ** -14 * 2.0 ** -25 if dtype == "f16" else 0.0)
     assert dh[~on].eq(0).all()
