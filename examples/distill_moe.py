@@ -11,10 +11,15 @@ products.  libscape does the rest of a step:
   log-sum-exp of the row, which is all that is kept of the teacher;
 - ``route`` sends every token to 2 of 8 experts and gives the balance and z
   losses of each sequence, ``route_backward`` the router's gradient;
+- ``expert_plan`` and ``expert_dispatch`` sort the tokens' rows by expert,
+  ``expert_combine`` sums the experts' rows back with the router's weights, and
+  ``expert_combine_backward`` gives the gradients of both;
 - ``distill_loss_grad`` gives the loss against the teacher's words (the others as
   one bucket) mixed with the hard labels, and overwrites the logits by their
   gradient;
-- ``Scape.step`` takes the workers' bf16 gradients and updates the parameters.
+- ``clip_grads`` scales a worker's gradient to a largest norm and writes it into
+  the worker's bf16 buffer;
+- ``Scape.step`` takes these buffers and updates the parameters.
 """
 from __future__ import annotations
 
@@ -28,7 +33,7 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import sparse_communication_distributed_gb300 as scape  # noqa: E402
 
 VOCAB, DIM, FF, EXPERTS, TOP = 1003, 64, 128, 8, 2
-TAU, KD, CE, BALANCE, Z = 2.0, 0.7, 0.3, 0.01, 0.001
+TAU, KD, CE, BALANCE, Z, CLIP = 2.0, 0.7, 0.3, 0.01, 0.001, 5.0
 SHAPES = {"emb": (VOCAB, DIM), "router": (DIM, EXPERTS), "w1": (EXPERTS, DIM, FF), "w2": (EXPERTS, FF, DIM),
           "head": (DIM, VOCAB)}
 
@@ -48,6 +53,33 @@ class Route(torch.autograd.Function):
         logits, idx, counts, live, cu_tokens = ctx.saved_tensors
         return scape.route_backward(logits, idx, counts, live, d_weights=d_weights.contiguous(),
                                     d_losses=d_losses.contiguous(), cu_tokens=cu_tokens), None
+
+
+class Dispatch(torch.autograd.Function):
+    """The tokens' rows sorted by expert."""
+
+    @staticmethod
+    def forward(ctx, x, slots, source):
+        ctx.save_for_backward(slots)
+        return scape.expert_dispatch(x, slots, source)
+
+    @staticmethod
+    def backward(ctx, d_rows):
+        return scape.expert_combine(d_rows.contiguous(), ctx.saved_tensors[0]), None, None
+
+
+class Combine(torch.autograd.Function):
+    """The experts' rows summed back, with the router's weights."""
+
+    @staticmethod
+    def forward(ctx, rows, weights, slots, source):
+        ctx.save_for_backward(rows, weights, slots, source)
+        return scape.expert_combine(rows, slots, weights)
+
+    @staticmethod
+    def backward(ctx, d_out):
+        rows, weights, slots, source = ctx.saved_tensors
+        return *scape.expert_combine_backward(d_out.contiguous(), rows, slots, source, weights), None, None
 
 
 class Distill(torch.autograd.Function):
@@ -71,11 +103,10 @@ def student(p, tokens, cu_tokens):
     """Logits, tokens of each expert, balance and z losses."""
     h = p["emb"][tokens]
     idx, weights, counts, losses = Route.apply(h @ p["router"], cu_tokens)
-    y = torch.zeros_like(h)
-    for e in range(EXPERTS):
-        at, slot = torch.nonzero(idx == e, as_tuple=True)
-        out = torch.nn.functional.gelu(h[at] @ p["w1"][e]) @ p["w2"][e]
-        y = y.index_add(0, at, out * weights[at, slot, None])
+    offsets, slots, source = scape.expert_plan(idx, EXPERTS)
+    rows = Dispatch.apply(h, slots, source).split(offsets.diff().tolist())  # (no token is left out)
+    out = [torch.nn.functional.gelu(rows[e] @ p["w1"][e]) @ p["w2"][e] for e in range(EXPERTS)]
+    y = Combine.apply(torch.cat(out), weights, slots, source)
     return (h + y) @ p["head"], counts, losses
 
 
@@ -106,7 +137,7 @@ def train(steps: int, workers: int, tokens: int = 512, seed: int = 0, log=print)
             logits, counts, aux = student(p, x, cu)
             loss = Distill.apply(logits, idx, vals, lse, labels)
             (loss + BALANCE * aux[0] + Z * aux[1]).backward()
-            grads[w].copy_(leaf.grad)
+            scape.clip_grads([leaf.grad], CLIP, out=[grads[w]])
             total += float(loss.detach()) / workers
         opt.step(grads)
         history.append(total)
