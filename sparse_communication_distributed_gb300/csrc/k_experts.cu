@@ -468,8 +468,16 @@ int unit_of(int dtype, uint64_t bytes, std::initializer_list<uintptr_t> at) {
   return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : (int)size_of(dtype);
 }
 
-constexpr int kUnits16 = 4, kUnitsSmall = 8;       // units of a row that a lane has in flight
-constexpr int kCombine16 = 2, kCombineSmall = 4;  // ... of each choice, where several are
+// Units of a row that a lane has in flight, of 16 bytes at most and of fewer; of each
+// choice, where several are.
+constexpr int kUnits16 = 4, kUnitsSmall = 8, kCombine16 = 2, kCombineSmall = 4;
+
+// As many 16-byte units a lane as divide a row of "bytes" into equal rounds (1280 bf16
+// elements: 3 and 2 of them, not 4 and 1).
+int units16_of(uint64_t bytes) {
+  const int all = (int)((bytes / 16 + 31) / 32), rounds = (all + kUnits16 - 1) / kUnits16;
+  return (all + rounds - 1) / rounds;
+}
 
 int check_rows(int dtype, uint64_t tokens, int k, uint64_t rows, uint64_t dim) {
   if (dtype < SCAPE_BF16 || dtype > SCAPE_F32) return fail(SCAPE_EINVAL, "unknown dtype %d", dtype);
@@ -575,7 +583,7 @@ SCAPE_API int scape_expert_dispatch(const void* x, int dtype, uint64_t tokens, u
     return fail(SCAPE_EINVAL, "out must not overlap x");
   RowArgs a{};
   const int unit = unit_of(dtype, dim * es, {row_stride * es, reinterpret_cast<uintptr_t>(x), reinterpret_cast<uintptr_t>(out)});
-  fill(a, dtype, tokens, k, rows, dim, unit, unit == 16 ? kUnits16 : kUnitsSmall);
+  fill(a, dtype, tokens, k, rows, dim, unit, unit == 16 ? units16_of(dim * es) : kUnitsSmall);
   a.x = static_cast<const char*>(x);
   a.out = static_cast<char*>(out);
   a.stride = (int64_t)(row_stride * es);
@@ -586,7 +594,12 @@ SCAPE_API int scape_expert_dispatch(const void* x, int dtype, uint64_t tokens, u
   if (!grid_of(a.row_warps + (a.rows + kEmptyRows - 1) / kEmptyRows, grid)) return fail(SCAPE_EINVAL, "too many rows");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (unit == 16) e = launch_behind(dispatch_rows<16, kUnits16>, grid, kThreads, s, a);
+  const int units = units16_of(dim * es);
+  if (unit == 16)
+    e = units == 1   ? launch_behind(dispatch_rows<16, 1>, grid, kThreads, s, a)
+        : units == 2 ? launch_behind(dispatch_rows<16, 2>, grid, kThreads, s, a)
+        : units == 3 ? launch_behind(dispatch_rows<16, 3>, grid, kThreads, s, a)
+                     : launch_behind(dispatch_rows<16, kUnits16>, grid, kThreads, s, a);
   else if (unit == 4) e = launch_behind(dispatch_rows<4, kUnitsSmall>, grid, kThreads, s, a);
   else e = launch_behind(dispatch_rows<2, kUnitsSmall>, grid, kThreads, s, a);
   return e == cudaSuccess ? SCAPE_OK : fail(SCAPE_ECUDA, "dispatch_rows: %s", cudaGetErrorString(e));
@@ -598,7 +611,12 @@ template <int DT>
 cudaError_t launch_combine(const RowArgs& a, int unit, unsigned grid, bool back, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (unit == 16) {
-    if (back) e = launch_behind(combine_grad<DT, 16, kUnits16>, grid, kThreads, s, a);
+    const int units = units16_of((uint64_t)a.bytes);
+    if (back)
+      e = units == 1   ? launch_behind(combine_grad<DT, 16, 1>, grid, kThreads, s, a)
+          : units == 2 ? launch_behind(combine_grad<DT, 16, 2>, grid, kThreads, s, a)
+          : units == 3 ? launch_behind(combine_grad<DT, 16, 3>, grid, kThreads, s, a)
+                       : launch_behind(combine_grad<DT, 16, kUnits16>, grid, kThreads, s, a);
     else e = launch_behind(combine_rows<DT, 16, kCombine16>, grid, kThreads, s, a);
   } else if (unit == 4) {
     if (back) e = launch_behind(combine_grad<DT, 4, kUnitsSmall>, grid, kThreads, s, a);
@@ -660,7 +678,7 @@ SCAPE_API int scape_expert_combine_backward(const void* d_out, const void* y, in
   RowArgs a{};
   const int unit = unit_of(dtype, dim * es, {reinterpret_cast<uintptr_t>(y), reinterpret_cast<uintptr_t>(d_out),
                                              reinterpret_cast<uintptr_t>(d_y)});
-  fill(a, dtype, tokens, k, rows, dim, unit, unit == 16 ? kUnits16 : kUnitsSmall);
+  fill(a, dtype, tokens, k, rows, dim, unit, unit == 16 ? units16_of(dim * es) : kUnitsSmall);
   a.x = static_cast<const char*>(y);
   a.d_out = static_cast<const char*>(d_out);
   a.out = static_cast<char*>(d_y);

@@ -51,15 +51,14 @@ enum Job { LOSS, GRAD, DH, DW };
 
 constexpr int kM = 128, kN = 256, kK = 64;  // a CTA's tile; 64 elements are one swizzled row
 // A pair of CTAs has a tile of 256 x 256: each copies its own 128 rows of A and half of
-// the columns of B, a third less than alone.
+// the columns of B, a third less than alone.  The tiles of K on their way fill the same
+// memory either way; where rows or words are few, more of them.
 template <int CG>
 struct Shape {
   static constexpr int kRows = kM * CG, kCols = kN / CG;  // rows of a tile; columns of B that a CTA copies
-  static constexpr int kStages = CG == 2 ? 6 : 4;
-  static constexpr uint32_t kBytesA = kM * kK * 2, kBytesB = kCols * kK * 2, kStageBytes = kBytesA + kBytesB;
+  static constexpr int kMaxStages = CG == 2 ? 6 : 16;
 };
-constexpr uint32_t kRing = 196608;  // all stages
-static_assert(Shape<1>::kStages * Shape<1>::kStageBytes == kRing && Shape<2>::kStages * Shape<2>::kStageBytes == kRing, "");
+constexpr uint32_t kRing = 196608;  // all stages: 6 of a pair's (32 KB), 4 of a CTA's alone (48 KB)
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;  // copies, products, allocation, one idle; epilogue
 constexpr uint32_t kOutBytes = 4096;            // a warp's results on their way out: 32 rows of 128 bytes
@@ -177,7 +176,7 @@ __device__ __forceinline__ Units units_of(const CeArgs& a, int live) {
   return u;
 }
 
-// 32 numbers of a row, columns [c, c + 32) of which those below n exist (n a multiple of 8).
+// 32 numbers of a row, columns [c, c + 32), in vectors of 8 that begin below n.
 template <int DT>
 __device__ __forceinline__ void store32(void* row, int c, int n, const float (&f)[32]) {
   using E = Elem<DT>;
@@ -300,8 +299,9 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
 #pragma unroll
         for (int i = 0; i < 32; i++) f[i] *= kKept;
         const int x = first + 32 * c - p * a.piece;
-        if constexpr (CG == 1) {  // (few rows, and tiles that need not be a multiple of 64 words wide)
-          if (r < live) store32<SCAPE_F16>(static_cast<char*>(a.g) + ((int64_t)p * a.cap + r) * a.piece * 2, x, a.piece, f);
+        if constexpr (CG == 1) {  // (few rows, and tiles of any multiple of 16 words)
+          if (r < live)
+            store32<SCAPE_F16>(static_cast<char*>(a.g) + ((int64_t)p * a.cap + r) * a.piece * 2, x, end - p * a.piece, f);
         } else {
           if (!(c & 1)) reuse();
           stage32<SCAPE_F16>(out, lane, c & 1, f);
@@ -409,10 +409,10 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
                                                        const __grid_constant__ CUtensorMap map_out,
                                                        const CeArgs a) {
   using S = Shape<CG>;
-  constexpr int kStages = S::kStages;
+  constexpr int kMax = S::kMaxStages;
   constexpr bool kAcrossA = JOB == DW, kAcrossB = JOB == DH || JOB == DW;
   extern __shared__ uint8_t raw[];
-  __shared__ uint64_t bars[2 * kStages + 4];
+  __shared__ uint64_t bars[2 * kMax + 4];
   __shared__ uint32_t tmem_at;
   __shared__ volatile uint32_t gone;
   const uint32_t buf = (smem_at(raw) + 1023u) & ~1023u;
@@ -420,9 +420,9 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
   auto full = [&](int s) { return smem_at(&bars[s]); };  // (of a pair: the first CTA's counts for both)
-  auto free_ = [&](int s) { return smem_at(&bars[kStages + s]); };
-  auto ready = [&](int s) { return smem_at(&bars[2 * kStages + s]); };
-  auto taken = [&](int s) { return smem_at(&bars[2 * kStages + 2 + s]); };  // (the same)
+  auto free_ = [&](int s) { return smem_at(&bars[kMax + s]); };
+  auto ready = [&](int s) { return smem_at(&bars[2 * kMax + s]); };
+  auto taken = [&](int s) { return smem_at(&bars[2 * kMax + 2 + s]); };  // (the same)
   auto meet = [&]() {
     fence_before();
     if constexpr (CG == 2) {
@@ -437,7 +437,7 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
     prefetch_map(&map_a);
     prefetch_map(&map_b);
     gone = 0u;
-    for (int s = 0; s < kStages; s++) {
+    for (int s = 0; s < kMax; s++) {
       bar_init(full(s), 1);
       bar_init(free_(s), 1);
     }
@@ -453,14 +453,15 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
   const uint32_t tmem = tmem_at;
   grid_launch_dependents();
   const int cols = JOB == LOSS || JOB == GRAD ? a.bn : kN;  // of a tile
-  const uint32_t bytes = ((kAcrossA ? kM : a.bm) + cols / CG) * kK * 2 * CG;  // of a stage
+  const uint32_t bytes_a = (kAcrossA ? kM : a.bm) * kK * 2, stage = bytes_a + cols / CG * kK * 2;
+  const int stages = min(kMax, (int)(kRing / stage));
   // Few rows: the first weights are on their way while the rows are still being taken
   // (with at most one row of tiles, unit i is tile i).
   int early = 0;
   if (JOB == LOSS && CG == 1 && warp == 0 && lane == 0 && a.early && blockIdx.x * cols < a.V)
-    for (; early < min(kStages, (a.D + kK - 1) / kK); early++) {
-      bar_expect(full(early), bytes);
-      load_box<CG>(buf + early * S::kStageBytes + S::kBytesA, &map_b, early * kK, blockIdx.x * cols, full(early));
+    for (; early < min(stages, (a.D + kK - 1) / kK); early++) {
+      bar_expect(full(early), stage);
+      load_box<CG>(buf + early * stage + bytes_a, &map_b, early * kK, blockIdx.x * cols, full(early));
     }
   grid_dependency_wait();
   const int live = *a.live;
@@ -470,7 +471,7 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
   if (warp == 0 && lane == 0) {
     if (n_units == 0)  // no row after all: the stages are completed and left
       for (int s = 0; s < early; s++) {
-        load_box<CG>(buf + s * S::kStageBytes, &map_a, 0, 0, full(s));
+        load_box<CG>(buf + s * stage, &map_a, 0, 0, full(s));
         bar_wait(full(s), 0, &gone);
       }
     int s = 0;
@@ -482,9 +483,9 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
       for (int k = t.k0; k < t.k1; k++) {
         const bool begun = early > 0;
         if (!begun && !(ok = bar_wait(free_(s), ph ^ 1u, &gone))) break;
-        const uint32_t sa = buf + s * S::kStageBytes, sb = sa + S::kBytesA;
+        const uint32_t sa = buf + s * stage, sb = sa + bytes_a;
         const uint32_t bar = CG == 2 ? bar_of(full(s), 0) : full(s);
-        if (rank == 0 && !begun) bar_expect(full(s), bytes);
+        if (rank == 0 && !begun) bar_expect(full(s), stage * CG);
         if (!kAcrossA) {
           load_box<CG>(sa, &map_a, k * kK, (JOB == DH ? (int)a.g0 : 0) + m0, bar);
         } else {
@@ -500,7 +501,7 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
 #pragma unroll
           for (int j = 0; j < S::kCols / 64; j++) load_box<CG>(sb + j * 8192, &map_b, n0 + 64 * j, y, bar);
         }
-        if (++s == kStages) {
+        if (++s == stages) {
           s = 0;
           ph ^= 1u;
         }
@@ -527,7 +528,7 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
       for (int k = t.k0; k < t.k1; k++) {
         if (!(ok = bar_wait(full(s), ph, &gone))) break;
         fence_after();
-        const uint32_t sa = buf + s * S::kStageBytes, sb = sa + S::kBytesA;
+        const uint32_t sa = buf + s * stage, sb = sa + bytes_a;
         // 16 elements of K: 32 bytes along a row, or 16 rows of 128 bytes
         const uint64_t oa = kAcrossA ? operand(sa, 8192, 1024) : operand(sa, 16, 1024);
         const uint64_t ob = kAcrossB ? operand(sb, 8192, 1024) : operand(sb, 16, 1024);
@@ -535,7 +536,7 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
         for (int j = 0; j < kK / 16; j++)
           mma<CG>(d, oa + j * (kAcrossA ? 128 : 2), ob + j * (kAcrossB ? 128 : 2), kind, k > t.k0 || j > 0);
         commit<CG>(free_(s));
-        if (++s == kStages) {
+        if (++s == stages) {
           s = 0;
           ph ^= 1u;
         }

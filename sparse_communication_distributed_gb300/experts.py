@@ -14,14 +14,11 @@ import ctypes
 from . import objective as _o
 
 
-def _int32(x, name: str, dim: int):
-    t = _o.torch
-    if x.dtype != t.int32 or x.dim() != dim or not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous, int32 and {dim}-D, not {x.dtype} of shape "
-                         f"{tuple(x.shape)} with strides {x.stride()}")
-    if not x.is_cuda or x.get_device() != t.cuda.current_device():
-        raise ValueError(f"{name} must be on the current CUDA device, not {x.device}")
-    return x.data_ptr()
+def _int32(x, name: str, dim: int, dev):
+    if x.dtype is _o.torch.int32 and x.dim() == dim and x.is_contiguous() and x.device == dev:
+        return x.data_ptr()
+    raise ValueError(f"{name} must be contiguous, int32 and {dim}-D on {dev}, not {x.dtype} of shape "
+                     f"{tuple(x.shape)} with strides {x.stride()} on {x.device}")
 
 
 def _contiguous(x, name: str):
@@ -44,9 +41,9 @@ def expert_plan(idx, experts: int, *, align: int = 1, bad_count=None, stream=Non
         with _o._stream_context(stream):
             return expert_plan(idx, experts, align=align, bad_count=bad_count)
     t, lib = _o.torch, _o._lib
-    p_idx = _int32(idx, "idx", 2)
-    tokens, k = idx.shape
-    dev = idx.device
+    _o._rows(idx, "idx")
+    (tokens, k), dev = idx.shape, idx.device
+    p_idx = _int32(idx, "idx", 2, dev)
     p_bad = _o._arg(bad_count, "bad_count", (t.int32,), (1,), dev)
     _o._count(experts)
     _o._count(align)
@@ -73,11 +70,11 @@ def expert_dispatch(x, slots, source, *, stream=None):
             return expert_dispatch(x, slots, source)
     stride = _o._rows(x, "x")
     code = _o._code(x, "x")
-    p_slots, p_source = _int32(slots, "slots", 2), _int32(source, "source", 1)
-    tokens, dim = x.shape
+    (tokens, dim), dev = x.shape, x.device
+    p_slots, p_source = _int32(slots, "slots", 2, dev), _int32(source, "source", 1, dev)
     if slots.shape[0] != tokens:
         raise ValueError(f"slots must have {tokens} rows, not {slots.shape[0]}")
-    rows, dev = source.shape[0], x.device
+    rows = source.shape[0]
     out = _o.torch.empty((rows, dim), dtype=x.dtype, device=dev)
     _o._check(_o._lib.scape_expert_dispatch(x.data_ptr(), code, tokens, dim, stride, slots.shape[1],
                                             p_slots, p_source, rows, out.data_ptr(), _raw(dev)))
@@ -95,9 +92,9 @@ def expert_combine(y, slots, weights=None, *, stream=None):
             return expert_combine(y, slots, weights)
     p_y = _contiguous(y, "y")
     code = _o._code(y, "y")
-    p_slots = _int32(slots, "slots", 2)
-    tokens, k = slots.shape
     (rows, dim), dev = y.shape, y.device
+    p_slots = _int32(slots, "slots", 2, dev)
+    tokens, k = slots.shape
     p_w = _o._arg(weights, "weights", (_o.torch.float32,), (tokens, k), dev)
     out = _o.torch.empty((tokens, dim), dtype=y.dtype, device=dev)
     _o._check(_o._lib.scape_expert_combine(p_y, code, rows, dim, p_slots, p_w, tokens, k,
@@ -116,9 +113,9 @@ def expert_combine_backward(d_out, y, slots, source, weights, *, stream=None):
     t = _o.torch
     p_y = _contiguous(y, "y")
     code = _o._code(y, "y")
-    p_slots, p_source = _int32(slots, "slots", 2), _int32(source, "source", 1)
-    tokens, k = slots.shape
     (rows, dim), dev = y.shape, y.device
+    p_slots, p_source = _int32(slots, "slots", 2, dev), _int32(source, "source", 1, dev)
+    tokens, k = slots.shape
     if source.shape[0] != rows:
         raise ValueError(f"source must have {rows} entries, not {source.shape[0]}")
     if weights is None or d_out is None:
