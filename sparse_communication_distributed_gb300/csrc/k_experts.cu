@@ -220,22 +220,27 @@ __global__ __launch_bounds__(kThreads) void place_choices(const PlanArgs a) {
 
 // ---- rows -----------------------------------------------------------------------
 
+// A unit of a row, and as a register holds it.  (16-bit units in 32-bit registers: with
+// uint16_t combine of 16384 x 1001 bf16, k 8, took 227 us and not 68.)
 template <int BYTES> struct Unit;
-template <> struct Unit<16> { using T = uint4; };
-template <> struct Unit<4> { using T = uint32_t; };
-template <> struct Unit<2> { using T = uint16_t; };
+template <> struct Unit<16> { using T = uint4; using Reg = uint4; };
+template <> struct Unit<4> { using T = uint32_t; using Reg = uint32_t; };
+template <> struct Unit<2> { using T = uint16_t; using Reg = uint32_t; };
 
 // The elements of a unit.
 template <int DT, int BYTES>
 struct Packed {
   using E = Elem<DT>;
   using U = typename Unit<BYTES>::T;
+  using Reg = typename Unit<BYTES>::Reg;
   static constexpr int N = BYTES / (int)sizeof(typename E::T);
-  static __device__ __forceinline__ void unpack(const U u, float (&f)[N]) {
+  static __device__ __forceinline__ void unpack(const Reg u, float (&f)[N]) {
     if constexpr (BYTES == 16) E::unpack(u, f);
     else if constexpr (DT == SCAPE_F32) f[0] = __uint_as_float(u);
-    else if constexpr (BYTES == 2) f[0] = E::load(&u);
-    else {
+    else if constexpr (BYTES == 2) {
+      const uint16_t h = (uint16_t)u;
+      f[0] = E::load(&h);
+    } else {
       const uint16_t lo = (uint16_t)u, hi = (uint16_t)(u >> 16);
       f[0] = E::load(&lo);
       f[1] = E::load(&hi);
@@ -250,9 +255,23 @@ struct Packed {
 };
 
 template <int BYTES>
-__device__ __forceinline__ typename Unit<BYTES>::T zero_unit() {
+__device__ __forceinline__ typename Unit<BYTES>::Reg zero_unit() {
   if constexpr (BYTES == 16) return make_uint4(0, 0, 0, 0);
   else return 0;
+}
+// Unit u of a row, 0 where there is none.
+template <int BYTES>
+__device__ __forceinline__ typename Unit<BYTES>::Reg unit_at(const typename Unit<BYTES>::T* row, int64_t u, bool there) {
+  if constexpr (BYTES == 2) {
+    uint32_t r = 0;
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n @p ld.global.u16 %0, [%1];\n}"
+                 : "+r"(r)
+                 : "l"(row + u), "r"((uint32_t)there)
+                 : "memory");
+    return r;
+  } else {
+    return there ? row[u] : zero_unit<BYTES>();
+  }
 }
 
 struct RowArgs {
@@ -280,7 +299,7 @@ __device__ void clear_empty_rows(const RowArgs& a, int64_t item, int lane) {
   for (int64_t r = item * kEmptyRows; r < min(a.rows, (item + 1) * kEmptyRows); r++) {
     if (a.source[r] >= 0) continue;
     U* out = reinterpret_cast<U*>(a.out + r * a.bytes);
-    for (int64_t u = lane; u < units; u += 32) out[u] = zero_unit<BYTES>();
+    for (int64_t u = lane; u < units; u += 32) out[u] = (U)zero_unit<BYTES>();
   }
 }
 
@@ -301,24 +320,23 @@ __global__ __launch_bounds__(kThreads) void dispatch_rows(const RowArgs a) {
   if (slot >= a.rows) slot = -1;
   if (!__any_sync(kFull, slot >= 0)) return;  // (a token of no expert is not read)
   const U* x = reinterpret_cast<const U*>(a.x + t * a.stride);
-  U v[R];
+  typename Unit<BYTES>::Reg v[R];
 #pragma unroll
-  for (int i = 0; i < R; i++) v[i] = u0 + i * 32 < units ? x[u0 + i * 32] : zero_unit<BYTES>();
+  for (int i = 0; i < R; i++) v[i] = unit_at<BYTES>(x, u0 + i * 32, u0 + i * 32 < units);
   for (int j = 0; j < a.k; j++) {
     const int s = __shfl_sync(kFull, slot, j);
     if (s < 0) continue;
     U* out = reinterpret_cast<U*>(a.out + s * a.bytes);
 #pragma unroll
     for (int i = 0; i < R; i++)
-      if (u0 + i * 32 < units) out[u0 + i * 32] = v[i];
+      if (u0 + i * 32 < units) out[u0 + i * 32] = (U)v[i];
   }
 }
 
 // out[t] = sum over j of w_tj y[slot_tj], in this order, rounded once.  The loads of
-// kAhead choices are under way together: with those of one alone (64 bytes a lane) 605 MB
-// took 138 us.
-constexpr int kAhead = 4;
-template <int DT, int BYTES, int R>
+// AHEAD choices are under way together: with those of one alone (64 bytes a lane) 605 MB
+// took 138 us, with 128 bytes of four 90.
+template <int DT, int BYTES, int R, int AHEAD>
 __global__ __launch_bounds__(kThreads, 4) void combine_rows(const RowArgs a) {
   using P = Packed<DT, BYTES>;
   using U = typename P::U;
@@ -340,18 +358,18 @@ __global__ __launch_bounds__(kThreads, 4) void combine_rows(const RowArgs a) {
   for (int i = 0; i < R; i++)
 #pragma unroll
     for (int e = 0; e < P::N; e++) acc[i][e] = 0.0f;
-  for (int j0 = 0; j0 < a.k; j0 += kAhead) {
-    U v[kAhead][R];
+  for (int j0 = 0; j0 < a.k; j0 += AHEAD) {
+    typename P::Reg v[AHEAD][R];
 #pragma unroll
-    for (int j = 0; j < kAhead; j++) {
+    for (int j = 0; j < AHEAD; j++) {
       const int s = __shfl_sync(kFull, slot, (j0 + j) & 31);
       const bool on = s >= 0 && j0 + j < a.k;
       const U* y = reinterpret_cast<const U*>(a.x + (on ? s : 0) * a.bytes);
 #pragma unroll
-      for (int i = 0; i < R; i++) v[j][i] = on && u0 + i * 32 < units ? y[u0 + i * 32] : zero_unit<BYTES>();
+      for (int i = 0; i < R; i++) v[j][i] = unit_at<BYTES>(y, u0 + i * 32, on && u0 + i * 32 < units);
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; j++) {
+    for (int j = 0; j < AHEAD; j++) {
       const float wj = __shfl_sync(kFull, w, (j0 + j) & 31);  // (no choice: 0 times 0)
 #pragma unroll
       for (int i = 0; i < R; i++) {
@@ -368,10 +386,12 @@ __global__ __launch_bounds__(kThreads, 4) void combine_rows(const RowArgs a) {
     if (u0 + i * 32 < units) out[u0 + i * 32] = P::pack(acc[i]);
 }
 
-// A warp has one choice: dy[slot] = w dout[t], dw = <dout[t], y[slot]>.  The token's
-// row comes from L1 for all but the first of its choices.
+// dy[slot] = w dout[t], dw = <dout[t], y[slot]>.  A warp has two choices of a token, whose
+// row it loads once for both; the warps of the token's other choices find it in L1.
+// (With one choice a warp, and half of the loads under way: 128 us for 696 MB.)
+constexpr int kPair = 2;
 template <int DT, int BYTES, int R>
-__global__ __launch_bounds__(kThreads) void combine_grad(const RowArgs a) {
+__global__ __launch_bounds__(kThreads, 4) void combine_grad(const RowArgs a) {
   using P = Packed<DT, BYTES>;
   using U = typename P::U;
   grid_launch_dependents();
@@ -382,40 +402,61 @@ __global__ __launch_bounds__(kThreads) void combine_grad(const RowArgs a) {
     clear_empty_rows<BYTES>(a, item - a.row_warps, lane);
     return;
   }
-  const int64_t t = item / a.k, units = a.bytes / BYTES;
-  int s = a.slots[item];
-  if (s >= a.rows) s = -1;
-  float dot = 0.0f;
-  if (s >= 0) {
-    const float w = a.weights[item];
+  const int pairs = (a.k + kPair - 1) / kPair;
+  const int64_t t = item / pairs, units = a.bytes / BYTES;
+  const int j0 = (int)(item - t * pairs) * kPair;
+  bool on[kPair];
+  float w[kPair], dot[kPair];
+  const U* y[kPair];
+  U* dy[kPair];
+#pragma unroll
+  for (int c = 0; c < kPair; c++) {
+    const int s = j0 + c < a.k ? a.slots[t * a.k + j0 + c] : -1;
+    on[c] = s >= 0 && s < a.rows;
+    w[c] = on[c] ? a.weights[t * a.k + j0 + c] : 0.0f;
+    y[c] = reinterpret_cast<const U*>(a.x + (on[c] ? s : 0) * a.bytes);
+    dy[c] = reinterpret_cast<U*>(a.out + (on[c] ? s : 0) * a.bytes);
+    dot[c] = 0.0f;
+  }
+  bool any = false;
+#pragma unroll
+  for (int c = 0; c < kPair; c++) any |= on[c];
+  if (any) {  // (a token without a choice is not read)
     const U* g = reinterpret_cast<const U*>(a.d_out + t * a.bytes);
-    const U* y = reinterpret_cast<const U*>(a.x + s * a.bytes);
-    U* dy = reinterpret_cast<U*>(a.out + s * a.bytes);
     for (int64_t u0 = lane; u0 < units; u0 += 32 * R) {
-      U vy[R], vg[R];
+      typename P::Reg vy[kPair][R], vg[R];
 #pragma unroll
       for (int i = 0; i < R; i++) {
         const bool in = u0 + i * 32 < units;
-        vy[i] = in ? y[u0 + i * 32] : zero_unit<BYTES>();
-        vg[i] = in ? g[u0 + i * 32] : zero_unit<BYTES>();
+        vg[i] = unit_at<BYTES>(g, u0 + i * 32, in);
+#pragma unroll
+        for (int c = 0; c < kPair; c++) vy[c][i] = unit_at<BYTES>(y[c], u0 + i * 32, in && on[c]);
       }
 #pragma unroll
       for (int i = 0; i < R; i++) {
-        float fy[P::N], fg[P::N];
-        P::unpack(vy[i], fy);
+        float fg[P::N];
         P::unpack(vg[i], fg);
 #pragma unroll
-        for (int e = 0; e < P::N; e++) {
-          dot = __fmaf_rn(fg[e], fy[e], dot);
-          fg[e] *= w;
+        for (int c = 0; c < kPair; c++) {
+          float fy[P::N], d[P::N];
+          P::unpack(vy[c][i], fy);
+#pragma unroll
+          for (int e = 0; e < P::N; e++) {
+            dot[c] = __fmaf_rn(fg[e], fy[e], dot[c]);
+            d[e] = fg[e] * w[c];
+          }
+          if (on[c] && u0 + i * 32 < units) dy[c][u0 + i * 32] = P::pack(d);
         }
-        if (u0 + i * 32 < units) dy[u0 + i * 32] = P::pack(fg);
       }
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
   }
-  if (lane == 0 && a.d_weights) a.d_weights[item] = dot;
+#pragma unroll
+  for (int c = 0; c < kPair; c++) {
+    float d = dot[c];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(kFull, d, o);
+    if (lane == 0 && a.d_weights && j0 + c < a.k) a.d_weights[t * a.k + j0 + c] = on[c] ? d : 0.0f;
+  }
 }
 
 int fail(int code, const char* fmt, ...) {
@@ -468,14 +509,16 @@ int unit_of(int dtype, uint64_t bytes, std::initializer_list<uintptr_t> at) {
   return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : (int)size_of(dtype);
 }
 
-// Units of a row that a lane has in flight, of 16 bytes at most and of fewer; of each
-// choice, where several are.
-constexpr int kUnits16 = 4, kUnitsSmall = 8, kCombine16 = 2, kCombineSmall = 4;
+// Units of a row that a lane has in flight, of 16 bytes and of fewer: dispatch; combine,
+// of each choice; its backward pass, of each choice and the token's row.
+constexpr int kUnits16 = 4, kUnitsSmall = 8, kBack16 = 3, kBack4 = 4, kBack2 = 8;
+// (two choices leave room for more of each)
+int combine_units(int unit, int k) { return unit == 16 ? (k <= 2 ? 4 : 2) : unit == 4 ? 4 : 8; }
 
-// As many 16-byte units a lane as divide a row of "bytes" into equal rounds (1280 bf16
-// elements: 3 and 2 of them, not 4 and 1).
-int units16_of(uint64_t bytes) {
-  const int all = (int)((bytes / 16 + 31) / 32), rounds = (all + kUnits16 - 1) / kUnits16;
+// As many 16-byte units a lane, up to "most", as divide a row of "bytes" into equal rounds
+// (1280 bf16 elements: 3 and 2 of them, not 4 and 1).
+int units16_of(uint64_t bytes, int most) {
+  const int all = (int)((bytes / 16 + 31) / 32), rounds = (all + most - 1) / most;
   return (all + rounds - 1) / rounds;
 }
 
@@ -583,7 +626,7 @@ SCAPE_API int scape_expert_dispatch(const void* x, int dtype, uint64_t tokens, u
     return fail(SCAPE_EINVAL, "out must not overlap x");
   RowArgs a{};
   const int unit = unit_of(dtype, dim * es, {row_stride * es, reinterpret_cast<uintptr_t>(x), reinterpret_cast<uintptr_t>(out)});
-  fill(a, dtype, tokens, k, rows, dim, unit, unit == 16 ? units16_of(dim * es) : kUnitsSmall);
+  fill(a, dtype, tokens, k, rows, dim, unit, unit == 16 ? units16_of(dim * es, kUnits16) : kUnitsSmall);
   a.x = static_cast<const char*>(x);
   a.out = static_cast<char*>(out);
   a.stride = (int64_t)(row_stride * es);
@@ -594,7 +637,7 @@ SCAPE_API int scape_expert_dispatch(const void* x, int dtype, uint64_t tokens, u
   if (!grid_of(a.row_warps + (a.rows + kEmptyRows - 1) / kEmptyRows, grid)) return fail(SCAPE_EINVAL, "too many rows");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  const int units = units16_of(dim * es);
+  const int units = units16_of(dim * es, kUnits16);
   if (unit == 16)
     e = units == 1   ? launch_behind(dispatch_rows<16, 1>, grid, kThreads, s, a)
         : units == 2 ? launch_behind(dispatch_rows<16, 2>, grid, kThreads, s, a)
@@ -611,19 +654,20 @@ template <int DT>
 cudaError_t launch_combine(const RowArgs& a, int unit, unsigned grid, bool back, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (unit == 16) {
-    const int units = units16_of((uint64_t)a.bytes);
+    const int units = units16_of((uint64_t)a.bytes, kBack16);
     if (back)
       e = units == 1   ? launch_behind(combine_grad<DT, 16, 1>, grid, kThreads, s, a)
           : units == 2 ? launch_behind(combine_grad<DT, 16, 2>, grid, kThreads, s, a)
-          : units == 3 ? launch_behind(combine_grad<DT, 16, 3>, grid, kThreads, s, a)
-                       : launch_behind(combine_grad<DT, 16, kUnits16>, grid, kThreads, s, a);
-    else e = launch_behind(combine_rows<DT, 16, kCombine16>, grid, kThreads, s, a);
+                       : launch_behind(combine_grad<DT, 16, kBack16>, grid, kThreads, s, a);
+    else
+      e = a.k <= 2 ? launch_behind(combine_rows<DT, 16, 4, 2>, grid, kThreads, s, a)
+                   : launch_behind(combine_rows<DT, 16, 2, 4>, grid, kThreads, s, a);
   } else if (unit == 4) {
-    if (back) e = launch_behind(combine_grad<DT, 4, kUnitsSmall>, grid, kThreads, s, a);
-    else e = launch_behind(combine_rows<DT, 4, kCombineSmall>, grid, kThreads, s, a);
+    if (back) e = launch_behind(combine_grad<DT, 4, kBack4>, grid, kThreads, s, a);
+    else e = launch_behind(combine_rows<DT, 4, 4, 4>, grid, kThreads, s, a);
   } else if constexpr (DT != SCAPE_F32) {
-    if (back) e = launch_behind(combine_grad<DT, 2, kUnitsSmall>, grid, kThreads, s, a);
-    else e = launch_behind(combine_rows<DT, 2, kCombineSmall>, grid, kThreads, s, a);
+    if (back) e = launch_behind(combine_grad<DT, 2, kBack2>, grid, kThreads, s, a);
+    else e = launch_behind(combine_rows<DT, 2, 8, 4>, grid, kThreads, s, a);
   }
   return e;
 }
@@ -648,7 +692,7 @@ SCAPE_API int scape_expert_combine(const void* y, int dtype, uint64_t rows, uint
   if (ranges_meet(y, rows * dim * es, out, tokens * dim * es)) return fail(SCAPE_EINVAL, "out must not overlap y");
   RowArgs a{};
   const int unit = unit_of(dtype, dim * es, {reinterpret_cast<uintptr_t>(y), reinterpret_cast<uintptr_t>(out)});
-  fill(a, dtype, tokens, k, rows, dim, unit, unit == 16 ? kCombine16 : kCombineSmall);
+  fill(a, dtype, tokens, k, rows, dim, unit, combine_units(unit, k));
   a.x = static_cast<const char*>(y);
   a.out = static_cast<char*>(out);
   a.slots = slots;
@@ -678,7 +722,7 @@ SCAPE_API int scape_expert_combine_backward(const void* d_out, const void* y, in
   RowArgs a{};
   const int unit = unit_of(dtype, dim * es, {reinterpret_cast<uintptr_t>(y), reinterpret_cast<uintptr_t>(d_out),
                                              reinterpret_cast<uintptr_t>(d_y)});
-  fill(a, dtype, tokens, k, rows, dim, unit, unit == 16 ? units16_of(dim * es) : kUnitsSmall);
+  fill(a, dtype, tokens, k, rows, dim, unit, unit == 16 ? units16_of(dim * es, kUnits16) : kUnitsSmall);
   a.x = static_cast<const char*>(y);
   a.d_out = static_cast<const char*>(d_out);
   a.out = static_cast<char*>(d_y);
@@ -686,7 +730,7 @@ SCAPE_API int scape_expert_combine_backward(const void* d_out, const void* y, in
   a.source = source;
   a.weights = weights;
   a.d_weights = d_weights;
-  a.row_warps = a.tokens * a.k;
+  a.row_warps = a.tokens * ((a.k + kPair - 1) / kPair);
   unsigned grid;
   if (!grid_of(a.row_warps + (a.rows + kEmptyRows - 1) / kEmptyRows, grid)) return fail(SCAPE_EINVAL, "too many rows");
   const cudaError_t e = launch_combine_any(dtype, a, unit, grid, true, static_cast<cudaStream_t>(stream));
