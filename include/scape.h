@@ -527,7 +527,7 @@ typedef struct {
 /* Bytes of device workspace for these sizes (host call; of the pointers only whether
  * d_hidden and d_weight are NULL matters): 4 bytes for every 64 logits and a copy
  * of the hidden states, for the gradients up to 1 GB (or 512 bytes a row) for G or
- * the pieces of it that are there at once, 60 MB for sums in parts and, where the
+ * the pieces of it that are there at once, 80 MB for sums in parts and, where the
  * vocabulary has several pieces, fp32 sums of d_hidden. */
 int scape_linear_ce_workspace(const scape_linear_ce_args* args, uint64_t* bytes);
 

@@ -5,14 +5,14 @@
 //   G_tv = w_t (exp(l_tv - lse_t) - [v = y_t]);  dH = G W;  dW = G^T H
 //
 // Four products on the tensor cores (16-bit operands, fp32 accumulators in tensor
-// memory), one kernel with four epilogues:
+// memory), one kernel for all:
 //   LOSS  H W^T: the maximum and the sum of exponentials of every row of a tile, and
 //         the label's logit; for a gradient also the exponentials themselves, for as
 //         many words as there is room for
 //   GRAD  the same product again, for a piece of the vocabulary without such room: G of
 //         that piece
-//   DH    G W, added up over the pieces in fp32
-//   DW    G^T H, complete for the piece's words
+//   BACK  G W, added up over the pieces in fp32, and G^T H, complete for the piece's
+//         words: the tiles of both in one launch
 // With GRAD a gradient costs 8 T D V operations, without it 6.  What LOSS keeps are
 // exponentials against the maximum of their 128 words, in fp16 times 2^15: their
 // rounding (half a step is 2^-11) does not count beside that of a bf16 G (2^-8) and is
@@ -47,7 +47,7 @@ namespace {
 
 using namespace tc;
 
-enum Job { LOSS, GRAD, DH, DW };
+enum Job { LOSS, GRAD, BACK };
 
 constexpr int kM = 128, kN = 256, kK = 64;  // a CTA's tile; 64 elements are one swizzled row
 // A pair of CTAs has a tile of 256 x 256: each copies its own 128 rows of A and half of
@@ -85,7 +85,7 @@ struct CeArgs {
   int64_t rows, cap;       // caller's rows; rounded up to a multiple of 256
   int D, V;
   int bn;                  // words of a tile (LOSS, GRAD)
-  int bm;                  // rows of a CTA's tile that are copied (LOSS, GRAD, DH)
+  int bm;                  // rows of a CTA's tile of H or G that are copied
   int keep;                // words below this are kept (LOSS)
   // the piece of the vocabulary
   int v0, vn;
@@ -93,9 +93,9 @@ struct CeArgs {
   int64_t g0;              // its first row in the buffer of G
   void* g;
   // sums of tiles in fp32, a float4 of a row's columns 4 j to 4 j + 3 at [j][row]
-  float* acc;              // DH, over the pieces: all tiles
-  float* tail;             // DH, DW: the parts of split tiles
-  int grid;                // CTAs, or pairs of them, of DH and DW
+  float* acc;              // dH, over the pieces: all tiles
+  float* tail;             // the parts of split tiles, of dH and behind them of dW
+  int grid;                // CTAs, or pairs of them, of BACK
   int first, last;
   int early;               // LOSS: no more than one row of tiles
   void* d_hidden;
@@ -104,77 +104,142 @@ struct CeArgs {
   int64_t dw_stride;
 };
 
+// Tiles of a product, in the order in which they are worked on: kGroup rows of tiles at a
+// time, down first.
+struct Tiles {
+  int mt, nt, kb;  // kb: blocks of the sum
+  __device__ __forceinline__ int count() const { return mt * nt; }
+  __device__ __forceinline__ void place(int tile, int& m, int& n) const {
+    const int g = tile / (kGroup * nt), in = tile - g * kGroup * nt;
+    const int rows = min(kGroup, mt - g * kGroup);
+    n = in / rows;
+    m = g * kGroup + in - n * rows;
+  }
+};
+
 // A unit of work: a tile, or a part of its sum.
 struct Unit {
   int m, n, k0, k1;
-  int tile, part;  // part: its place among the parts, -1 for a whole tile
+  int tile;
+  int part;  // its place among the parts of its product, -1 for a whole tile
+  bool dw;   // BACK: of dW
 };
 
-// The order of the tiles: kGroup rows of tiles at a time, down first.  The tiles that
-// fill the last round of CTAs only in part are split along the sum, so that the round
-// is short; their parts are added up by join_parts.
-constexpr int kMaxParts = 3;  // parts, per CTA
-struct Units {
-  int mt, nt, kb;
-  int whole, split;  // tiles in front that are not split; parts of each of the others
-  __device__ __forceinline__ int count() const { return whole + (mt * nt - whole) * split; }
-  __device__ __forceinline__ void divide(int grid) {
-    const int rest = (mt * nt) % grid;
-    whole = mt * nt;
-    split = 1;
-    if (rest == 0) return;
-    float best = 0.95f;  // of a round; the parts cost a little, too
-    for (int s = 2; s <= 32 && s * rest <= kMaxParts * grid && s * 8 <= kb; s++) {
-      const float rounds = (float)((s * rest + grid - 1) / grid) / (float)s + 0.01f * s;
-      if (rounds < best) {
-        best = rounds;
-        split = s;
+__device__ __forceinline__ int up_div(int x, int y) { return (x + y - 1) / y; }
+
+// The units of a CTA (or pair), one after the other.
+template <int JOB, int CG>
+struct Work {
+  Tiles t;
+  __device__ __forceinline__ Work(const CeArgs& a, int live)
+      : t{up_div(live, Shape<CG>::kRows), up_div(a.vn, a.bn), up_div(a.D, kK)} {}
+  __device__ __forceinline__ bool get(int me, int all, int j, Unit& u) const {
+    u.tile = me + j * all;
+    if (u.tile >= t.count()) return false;
+    t.place(u.tile, u.m, u.n);
+    u.k0 = 0;
+    u.k1 = t.kb;
+    u.part = -1;
+    u.dw = false;
+    return true;
+  }
+};
+
+// BACK: first the tiles of dH, whose sums are long, then those of dW.  Where the tiles of
+// dH do not go evenly into the CTAs, those that have one less begin with as many tiles of
+// dW as that one takes.  So the CTAs end together, which two launches do not let them:
+// with 55 tiles of dH for 76 pairs of CTAs and 625 of dW (2723 rows, 32000 x 1280) a whole
+// gradient took 555 us in two and takes 533 in one.  Split, and added up by join_parts, are the tiles of dH where they are
+// too few and too long for that, and those of dW that would be a last round by themselves.
+constexpr int kMaxParts = 2;         // of each product, per CTA
+constexpr float kUnitCost = 6.0f;    // what a unit costs beside its blocks, in blocks
+constexpr float kPartCost = 0.14f;   // what writing and adding up a CTA's part costs, on all CTAs
+template <int CG>
+struct Work<BACK, CG> {
+  Tiles h, w;
+  int split_h;          // parts of every tile of dH
+  int each, more;       // units of dH of every CTA; CTAs with one more
+  int early;            // tiles of dW that the others begin with
+  int whole, split_w;   // tiles of dW that are not split; parts of the others
+  __device__ __forceinline__ Work(const CeArgs& a, int live) {
+    constexpr int kRows = Shape<CG>::kRows;
+    const int all = a.grid;
+    h = {up_div(live, kRows), up_div(a.D, kN), up_div(a.vn, kK)};
+    w = {up_div(a.vn, kRows), up_div(a.D, kN), up_div(live, kK)};
+    const float cost_w = (float)w.kb + kUnitCost;
+    split_h = 1;
+    float best = 0.0f;
+    for (int s = 1; s <= 32 && (s == 1 || (s * h.count() <= kMaxParts * all && 8 * s <= h.kb)); s++) {
+      const int n = s * h.count();
+      const float unit = (float)h.kb / (float)s + kUnitCost;
+      const float even = ((float)n * unit + (float)w.count() * cost_w) / (float)all;
+      const float last = (float)up_div(n, all) * unit;
+      const float cost = fmaxf(even, last) + (s > 1 ? kPartCost * (float)(n * CG) : 0.0f);
+      if (s == 1 || cost < best) {
+        best = cost;
+        split_h = s;
+      }
+      if (h.count() >= all) break;
+    }
+    const int n = split_h * h.count();
+    each = n / all;
+    more = n - each * all;
+    const float unit = (float)h.kb / (float)split_h + kUnitCost;
+    early = more ? min((int)(unit / cost_w + 0.5f), w.count() / (all - more)) : 0;
+    const int left = w.count() - early * (all - more), rest = left % all;
+    whole = w.count();
+    split_w = 1;
+    float round = 0.9f;  // the last one, of a whole one
+    for (int s = 2; s <= 16 && rest && s * rest <= kMaxParts * all && 8 * s <= w.kb; s++) {
+      const float cost = (float)up_div(s * rest, all) / (float)s + kPartCost * (float)(s * rest * CG) / cost_w;
+      if (cost < round) {
+        round = cost;
+        split_w = s;
       }
     }
-    if (split > 1) whole -= rest;
+    if (split_w > 1) whole -= rest;
   }
-  __device__ __forceinline__ void place(int tile, Unit& u) const {
-    const int g = tile / (kGroup * nt), in = tile - g * kGroup * nt;
-    const int rows = min(kGroup, mt - g * kGroup);
-    u.tile = tile;
-    u.n = in / rows;
-    u.m = g * kGroup + in - u.n * rows;
-  }
-  __device__ __forceinline__ Unit at(int i) const {
-    Unit u;
+  __device__ __forceinline__ int rest() const { return w.count() - whole; }
+  __device__ __forceinline__ bool get(int me, int all, int j, Unit& u) const {
+    const bool has_more = me < more;
+    const int own = each + has_more;
+    u.dw = j >= own;
+    if (!u.dw) {
+      const int i = me + j * all, s = i / h.count();
+      u.tile = i - s * h.count();
+      h.place(u.tile, u.m, u.n);
+      u.k0 = (int)((int64_t)h.kb * s / split_h);
+      u.k1 = (int)((int64_t)h.kb * (s + 1) / split_h);
+      u.part = split_h > 1 ? i : -1;
+      return true;
+    }
+    j -= own;
+    const int others = all - more, first = early * others;
+    int i;
+    if (has_more) i = first + j * all + me;
+    else if (j < early) i = j * others + me - more;
+    else i = first + (j - early) * all + me;
     if (i < whole) {
-      place(i, u);
+      u.tile = i;
       u.k0 = 0;
-      u.k1 = kb;
+      u.k1 = w.kb;
       u.part = -1;
     } else {
-      const int rest = mt * nt - whole, s = (i - whole) / rest;
-      place(whole + (i - whole) - s * rest, u);
-      u.k0 = (int)((int64_t)kb * s / split);
-      u.k1 = (int)((int64_t)kb * (s + 1) / split);
-      u.part = i - whole;
+      if (i >= whole + rest() * split_w) return false;
+      const int p = i - whole, s = p / rest();
+      u.tile = whole + p - s * rest();
+      u.k0 = (int)((int64_t)w.kb * s / split_w);
+      u.k1 = (int)((int64_t)w.kb * (s + 1) / split_w);
+      u.part = p;
     }
-    return u;
+    w.place(u.tile, u.m, u.n);
+    return true;
+  }
+  // Where the parts of a CTA's half of a unit are.
+  static __device__ __forceinline__ float* part_at(const CeArgs& a, bool dw, int part, int rank) {
+    return a.tail + ((int64_t)((dw ? kMaxParts * a.grid : 0) + part) * CG + rank) * (int64_t)kTileFloats;
   }
 };
-
-template <int JOB, int CG>
-__device__ __forceinline__ Units units_of(const CeArgs& a, int live) {
-  constexpr int kRows = Shape<CG>::kRows;
-  auto up = [](int x, int y) { return (x + y - 1) / y; };
-  Units u;
-  if (JOB == LOSS || JOB == GRAD) {
-    u.mt = up(live, kRows); u.nt = up(a.vn, a.bn); u.kb = up(a.D, kK);
-  } else if (JOB == DH) {
-    u.mt = up(live, kRows); u.nt = up(a.D, kN); u.kb = up(a.vn, kK);
-  } else {
-    u.mt = up(a.vn, kRows); u.nt = up(a.D, kN); u.kb = up(live, kK);
-  }
-  u.whole = u.mt * u.nt;
-  u.split = 1;
-  if (JOB == DH || JOB == DW) u.divide(a.grid);
-  return u;
-}
 
 // 32 numbers of a row, columns [c, c + 32), in vectors of 8 that begin below n.
 template <int DT>
@@ -349,21 +414,21 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
     }
   } else {
     const float un = a.scale[1];
-    const bool on = JOB == DH ? r < live : true;
-    // columns of the unit in fp32: a part's own place, or the sums over the pieces
-    float4* sums = reinterpret_cast<float4*>(u.part >= 0 ? a.tail + (u.part * CG + rank) * kTileFloats
-                                                         : a.acc + (u.tile * CG + rank) * kTileFloats) +
-                   half * 32 * kM + quarter * 32 + lane;
-    for (int c = 0; c < 4; c++) {
-      fetch(c);
-      const int d0 = u.n * kN + half * 128 + 32 * c;
-      if (u.part >= 0) {
+    const int at = half * 32 * kM + quarter * 32 + lane;  // of the row's first columns in a tile's sums
+    if (u.part >= 0) {
+      float4* part = reinterpret_cast<float4*>(Work<BACK, CG>::part_at(a, u.dw, u.part, rank)) + at;
+      for (int c = 0; c < 4; c++) {
+        fetch(c);
 #pragma unroll
         for (int j = 0; j < 8; j++)
-          sums[(c * 8 + j) * kM] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
-        continue;
+          part[(c * 8 + j) * kM] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
       }
-      if constexpr (JOB == DH) {
+    } else if (!u.dw) {
+      const bool on = r < live;
+      float4* sums = reinterpret_cast<float4*>(a.acc + ((int64_t)u.tile * CG + rank) * (int64_t)kTileFloats) + at;
+      for (int c = 0; c < 4; c++) {
+        fetch(c);
+        const int d0 = u.n * kN + half * 128 + 32 * c;
         if (!a.first) {
 #pragma unroll
           for (int j = 0; j < 8; j++) {
@@ -389,12 +454,15 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
               reinterpret_cast<uint4*>(to)[j] = Elem<DT>::pack(g);
             }
         }
-      } else {
+      }
+    } else {
+      for (int c = 0; c < 4; c++) {
+        fetch(c);
 #pragma unroll
         for (int i = 0; i < 32; i++) f[i] *= un;
         if (!(c & 1)) reuse();
         stage32<DT>(out, lane, c & 1, f);
-        if (c & 1) send(d0 - 32, a.v0 + r0);
+        if (c & 1) send(u.n * kN + half * 128 + 32 * (c - 1), a.v0 + r0);
       }
     }
   }
@@ -406,11 +474,12 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
 template <int JOB, int DT, int CG, bool KEEP>
 __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ CUtensorMap map_a,
                                                        const __grid_constant__ CUtensorMap map_b,
+                                                       const __grid_constant__ CUtensorMap map_wa,  // dW's operands
+                                                       const __grid_constant__ CUtensorMap map_wb,
                                                        const __grid_constant__ CUtensorMap map_out,
                                                        const CeArgs a) {
   using S = Shape<CG>;
   constexpr int kMax = S::kMaxStages;
-  constexpr bool kAcrossA = JOB == DW, kAcrossB = JOB == DH || JOB == DW;
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t bars[2 * kMax + 4];
   __shared__ uint32_t tmem_at;
@@ -436,6 +505,10 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
   if (warp == 0 && lane == 0) {
     prefetch_map(&map_a);
     prefetch_map(&map_b);
+    if (JOB == BACK) {
+      prefetch_map(&map_wa);
+      prefetch_map(&map_wb);
+    }
     gone = 0u;
     for (int s = 0; s < kMax; s++) {
       bar_init(full(s), 1);
@@ -452,8 +525,8 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
   meet();
   const uint32_t tmem = tmem_at;
   grid_launch_dependents();
-  const int cols = JOB == LOSS || JOB == GRAD ? a.bn : kN;  // of a tile
-  const uint32_t bytes_a = (kAcrossA ? kM : a.bm) * kK * 2, stage = bytes_a + cols / CG * kK * 2;
+  const int cols = JOB == BACK ? kN : a.bn;  // of a tile
+  const uint32_t bytes_a = (JOB == BACK ? kM : a.bm) * kK * 2, bytes_b = cols / CG * kK * 2, stage = bytes_a + bytes_b;
   const int stages = min(kMax, (int)(kRing / stage));
   // Few rows: the first weights are on their way while the rows are still being taken
   // (with at most one row of tiles, unit i is tile i).
@@ -465,11 +538,11 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
     }
   grid_dependency_wait();
   const int live = *a.live;
-  const Units units = units_of<JOB, CG>(a, live);
-  const int n_units = units.count();
+  const Work<JOB, CG> work(a, live);
+  Unit t;
 
   if (warp == 0 && lane == 0) {
-    if (n_units == 0)  // no row after all: the stages are completed and left
+    if (live == 0)  // no row after all: the stages are completed and left
       for (int s = 0; s < early; s++) {
         load_box<CG>(buf + s * stage, &map_a, 0, 0, full(s));
         bar_wait(full(s), 0, &gone);
@@ -477,29 +550,27 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int i = first; ok && i < n_units; i += step) {
-      const Unit t = units.at(i);
+    for (int j = 0; ok && work.get(first, step, j, t); j++) {
       const int m0 = t.m * S::kRows + rank * kM, n0 = t.n * cols + rank * (cols / CG);
       for (int k = t.k0; k < t.k1; k++) {
         const bool begun = early > 0;
         if (!begun && !(ok = bar_wait(free_(s), ph ^ 1u, &gone))) break;
         const uint32_t sa = buf + s * stage, sb = sa + bytes_a;
         const uint32_t bar = CG == 2 ? bar_of(full(s), 0) : full(s);
-        if (rank == 0 && !begun) bar_expect(full(s), stage * CG);
-        if (!kAcrossA) {
-          load_box<CG>(sa, &map_a, k * kK, (JOB == DH ? (int)a.g0 : 0) + m0, bar);
+        if (rank == 0 && !begun) bar_expect(full(s), ((t.dw ? kM : a.bm) * kK * 2 + bytes_b) * CG);
+        if (JOB != BACK) {
+          load_box<CG>(sa, &map_a, k * kK, m0, bar);
+          if (begun) early--;
+          else load_box<CG>(sb, &map_b, k * kK, a.v0 + n0, bar);
+        } else if (!t.dw) {
+          load_box<CG>(sa, &map_a, k * kK, (int)a.g0 + m0, bar);
+#pragma unroll
+          for (int i = 0; i < S::kCols / 64; i++) load_box<CG>(sb + i * 8192, &map_b, n0 + 64 * i, a.v0 + k * kK, bar);
         } else {
 #pragma unroll
-          for (int j = 0; j < kM / 64; j++) load_box<CG>(sa + j * 8192, &map_a, m0 + 64 * j, (int)a.g0 + k * kK, bar);
-        }
-        if (begun) {
-          early--;
-        } else if (!kAcrossB) {
-          load_box<CG>(sb, &map_b, k * kK, a.v0 + n0, bar);
-        } else {
-          const int y = (JOB == DH ? a.v0 : 0) + k * kK;
+          for (int i = 0; i < kM / 64; i++) load_box<CG>(sa + i * 8192, &map_wa, m0 + 64 * i, (int)a.g0 + k * kK, bar);
 #pragma unroll
-          for (int j = 0; j < S::kCols / 64; j++) load_box<CG>(sb + j * 8192, &map_b, n0 + 64 * j, y, bar);
+          for (int i = 0; i < S::kCols / 64; i++) load_box<CG>(sb + i * 8192, &map_wb, n0 + 64 * i, k * kK, bar);
         }
         if (++s == stages) {
           s = 0;
@@ -513,28 +584,28 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
       }
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
-    const uint32_t kind = product_of(DT == SCAPE_BF16, kAcrossA, kAcrossB, S::kRows, cols);
     int s = 0, n = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int i = first; ok && i < n_units; i += step) {
-      const Unit t = units.at(i);
+    for (int j = 0; ok && work.get(first, step, j, t); j++) {
       if (t.k0 >= t.k1) continue;  // nothing to multiply: no accumulator
       const int acc = n & 1;
       if (!(ok = bar_wait(taken(acc), ((n >> 1) & 1) ^ 1, &gone))) break;
       n++;
       fence_after();
       const uint32_t d = tmem + acc * kN;
+      const bool across_a = JOB == BACK && t.dw;
+      const uint32_t kind = product_of(DT == SCAPE_BF16, across_a, JOB == BACK, S::kRows, cols);
       for (int k = t.k0; k < t.k1; k++) {
         if (!(ok = bar_wait(full(s), ph, &gone))) break;
         fence_after();
         const uint32_t sa = buf + s * stage, sb = sa + bytes_a;
         // 16 elements of K: 32 bytes along a row, or 16 rows of 128 bytes
-        const uint64_t oa = kAcrossA ? operand(sa, 8192, 1024) : operand(sa, 16, 1024);
-        const uint64_t ob = kAcrossB ? operand(sb, 8192, 1024) : operand(sb, 16, 1024);
+        const uint64_t oa = across_a ? operand(sa, 8192, 1024) : operand(sa, 16, 1024);
+        const uint64_t ob = JOB == BACK ? operand(sb, 8192, 1024) : operand(sb, 16, 1024);
 #pragma unroll
-        for (int j = 0; j < kK / 16; j++)
-          mma<CG>(d, oa + j * (kAcrossA ? 128 : 2), ob + j * (kAcrossB ? 128 : 2), kind, k > t.k0 || j > 0);
+        for (int i = 0; i < kK / 16; i++)
+          mma<CG>(d, oa + i * (across_a ? 128 : 2), ob + i * (JOB == BACK ? 128 : 2), kind, k > t.k0 || i > 0);
         commit<CG>(free_(s));
         if (++s == stages) {
           s = 0;
@@ -547,8 +618,7 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
     const int half = (warp - 4) >> 2, quarter = warp & 3;
     int n = 0;
     const uint32_t out = buf + kRing + (warp - 4) * kOutBytes;
-    for (int i = first; i < n_units; i += step) {
-      const Unit t = units.at(i);
+    for (int j = 0; work.get(first, step, j, t); j++) {
       const bool empty = t.k0 >= t.k1;
       const int acc = n & 1;
       if (!empty) {
@@ -666,7 +736,7 @@ __global__ __launch_bounds__(kRowThreads) void take_rows(const RowsArgs a) {
   if (tid == 0 && a.bad && n_bad) atomicAdd(a.bad, n_bad);
   if (blockIdx.x + 1 < gridDim.x) return;
   // the last CTA has seen every row.  Rows of 0 behind the last one, to a multiple of 64:
-  // DW adds them up, too
+  // the product of dW adds them up, too
   if (a.d_hidden)
     for (int64_t i = at * vecs + tid; i < (at + 63) / 64 * 64 * vecs; i += kRowThreads)
       reinterpret_cast<uint4*>(a.together)[i] = zero;
@@ -716,7 +786,7 @@ __global__ __launch_bounds__(256, 4) void grad_kept(const CeArgs a) {
   grid_launch_dependents();
   grid_dependency_wait();
   const int live = *a.live, lane = threadIdx.x & 31;
-  const int64_t rows = min((int64_t)(live + 255) / 256 * 256, a.cap);  // (as many as DH and DW read)
+  const int64_t rows = min((int64_t)(live + 255) / 256 * 256, a.cap);  // (as many as BACK reads)
   const int vecs = a.piece / 8, runs = (vecs + kRun - 1) / kRun;       // (beside the last word, too)
   const float scale = a.scale[0];
   for (int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); item < rows * runs; item += (int64_t)gridDim.x * 8) {
@@ -774,34 +844,38 @@ __global__ __launch_bounds__(256, 4) void grad_kept(const CeArgs a) {
   }
 }
 
-// The parts of the split tiles of DH or DW, added up in order: a thread has eight
-// columns of a row.
-template <int JOB, int DT, int CG>
+// The parts of the split tiles, added up in order: a thread has eight columns of a row.
+template <int DT, int CG>
 __global__ __launch_bounds__(256) void join_parts(const CeArgs a) {
   constexpr int kRows = Shape<CG>::kRows;
   grid_launch_dependents();
   grid_dependency_wait();
   const int live = *a.live;
-  const Units units = units_of<JOB, CG>(a, live);
-  const int rest = units.mt * units.nt - units.whole;
+  const Work<BACK, CG> work(a, live);
   const float un = a.scale[1];
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)rest * kRows * (kN / 8);
+  const int of_h = work.split_h > 1 ? work.h.count() : 0, tiles = of_h + work.rest();
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)tiles * kRows * (kN / 8);
        i += (int64_t)gridDim.x * 256) {
     const int row = (int)(i % kM), j = (int)(i / kM % (kN / 8)), both = (int)(i / (kM * (kN / 8)));
-    const int t = both / CG, rank = both % CG;
-    Unit u;
-    units.place(units.whole + t, u);
-    const int r = u.m * kRows + rank * kM + row, d = u.n * kN + 8 * j;
+    const int rank = both % CG;
+    int t = both / CG;
+    const bool dw = t >= of_h;
+    if (dw) t -= of_h;
+    const Tiles& all = dw ? work.w : work.h;
+    const int tile = dw ? work.whole + t : t, step = dw ? work.rest() : of_h, parts = dw ? work.split_w : work.split_h;
+    int m, n;
+    all.place(tile, m, n);
+    const int r = m * kRows + rank * kM + row, d = n * kN + 8 * j;
     float f[8] = {};
-    auto add = [&](const float* tile) {
-      const float4* q = reinterpret_cast<const float4*>(tile) + 2 * j * kM + row;
+    auto add = [&](const float* sums) {
+      const float4* q = reinterpret_cast<const float4*>(sums) + 2 * j * kM + row;
       const float4 x = q[0], y = q[kM];
       f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
       f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
     };
-    for (int s = 0; s < units.split; s++) add(a.tail + (uint64_t)((s * rest + t) * CG + rank) * kTileFloats);
-    if (JOB == DH) {
-      float* acc = a.acc + (u.tile * CG + rank) * kTileFloats;
+    for (int s = 0; s < parts; s++) add(Work<BACK, CG>::part_at(a, dw, s * step + t, rank));
+    if (!dw) {
+      float* acc = a.acc + ((int64_t)tile * CG + rank) * (int64_t)kTileFloats;
       if (!a.first) add(acc);
       if (!a.last) {
         float4* q = reinterpret_cast<float4*>(acc) + 2 * j * kM + row;
@@ -810,13 +884,13 @@ __global__ __launch_bounds__(256) void join_parts(const CeArgs a) {
         continue;
       }
     }
-    if (d >= a.D || (JOB == DH ? r >= live : a.v0 + r >= a.V)) continue;
-    if (JOB == DH) add_left<DT>(a, r, d, f);
+    if (d >= a.D || (dw ? a.v0 + r >= a.V : r >= live)) continue;
+    if (!dw) add_left<DT>(a, r, d, f);
 #pragma unroll
     for (int e = 0; e < 8; e++) f[e] *= un;
     typename Elem<DT>::T* out =
-        JOB == DH ? static_cast<typename Elem<DT>::T*>(a.d_hidden) + (int64_t)a.map[r] * a.dh_stride + d
-                  : static_cast<typename Elem<DT>::T*>(a.d_weight) + (int64_t)(a.v0 + r) * a.dw_stride + d;
+        dw ? static_cast<typename Elem<DT>::T*>(a.d_weight) + (int64_t)(a.v0 + r) * a.dw_stride + d
+           : static_cast<typename Elem<DT>::T*>(a.d_hidden) + (int64_t)a.map[r] * a.dh_stride + d;
     *reinterpret_cast<uint4*>(out) = Elem<DT>::pack(f);
   }
 }
@@ -936,7 +1010,7 @@ Layout layout_of(const scape_linear_ce_args* q, const Cut& c, bool grad) {
   if (grad) {
     l.g = take(std::max<uint64_t>(c.kept, 1) * c.cap * c.piece * 2);
     if (c.pieces > 1) l.acc = take(c.cap / kM * ceil_div(q->dim, kN) * kTileFloats * 4);
-    l.tail = take(kMaxParts * (uint64_t)num_sms() * kTileFloats * 4);
+    l.tail = take(2 * kMaxParts * (uint64_t)num_sms() * kTileFloats * 4);
   }
   l.bytes = at;
   return l;
@@ -990,8 +1064,8 @@ cudaError_t launch_behind(K kernel, unsigned grid, unsigned block, uint32_t smem
 }
 
 template <int JOB, int DT, int CG, bool KEEP = false>
-cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const CeArgs& a,
-                           uint64_t tiles, cudaStream_t s) {
+cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mwa, const CUtensorMap& mwb,
+                           const CUtensorMap& mo, const CeArgs& a, uint64_t tiles, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1001,9 +1075,9 @@ cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const C
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
   }
-  unsigned grid = (unsigned)a.grid;  // (DH and DW divide their sums by it)
-  if (JOB == LOSS || JOB == GRAD) grid = (unsigned)std::min<uint64_t>(std::max<uint64_t>(tiles, 1), grid);
-  return launch_behind(product<JOB, DT, CG, KEEP>, grid * CG, kThreads, kSmem, CG, s, ma, mb, mo, a);
+  unsigned grid = (unsigned)a.grid;  // (BACK divides its work by it)
+  if (JOB != BACK) grid = (unsigned)std::min<uint64_t>(std::max<uint64_t>(tiles, 1), grid);
+  return launch_behind(product<JOB, DT, CG, KEEP>, grid * CG, kThreads, kSmem, CG, s, ma, mb, mwa, mwb, mo, a);
 }
 
 template <int DT, int CG>
@@ -1082,8 +1156,8 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
   a.piece = (int)c.piece;
   a.keep = (int)std::min<uint64_t>(c.kept * c.piece, q->vocab);
   const uint64_t loss_tiles = ceil_div(q->rows, kRows) * ceil_div(q->vocab, c.bn);
-  e = c.kept ? launch_product<LOSS, DT, CG, true>(along_h, along_w, out_g, a, loss_tiles, s)
-             : launch_product<LOSS, DT, CG>(along_h, along_w, along_w, a, loss_tiles, s);
+  e = c.kept ? launch_product<LOSS, DT, CG, true>(along_h, along_w, along_h, along_w, out_g, a, loss_tiles, s)
+             : launch_product<LOSS, DT, CG>(along_h, along_w, along_h, along_w, along_w, a, loss_tiles, s);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "product (loss): %s", cudaGetErrorString(e));
   e = launch_behind(row_losses, (unsigned)ceil_div(std::max<uint64_t>(q->rows, 1), 8), 256, 0, 1, s, a);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "row_losses: %s", cudaGetErrorString(e));
@@ -1095,7 +1169,6 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
   a.dh_stride = (int64_t)q->d_hidden_stride;
   a.d_weight = q->d_weight;
   a.dw_stride = (int64_t)q->d_weight_stride;
-  const unsigned join = 4u * (unsigned)num_sms();
   for (uint64_t p = 0; p < c.pieces; p++) {
     a.v0 = (int)(p * c.piece);
     a.vn = (int)std::min<uint64_t>(c.piece, q->vocab - p * c.piece);
@@ -1108,12 +1181,11 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
     } else {  // (the kept ones are done with)
       a.g0 = 0;
       a.bn = kN;
-      e = launch_product<GRAD, DT, CG>(along_h, piece_w, out_g, a, ceil_div(q->rows, kRows) * ceil_div(a.vn, kN), s);
+      e = launch_product<GRAD, DT, CG>(along_h, piece_w, along_h, piece_w, out_g, a, ceil_div(q->rows, kRows) * ceil_div(a.vn, kN), s);
     }
-    if (e == cudaSuccess) e = launch_product<DH, DT, CG>(along_g, across_w, out_g, a, 0, s);
-    if (e == cudaSuccess) e = launch_behind(join_parts<DH, DT, CG>, join, 256, 0, 1, s, a);
-    if (e == cudaSuccess) e = launch_product<DW, DT, CG>(across_g, across_h, out_w, a, 0, s);
-    if (e == cudaSuccess) e = launch_behind(join_parts<DW, DT, CG>, join, 256, 0, 1, s, a);
+    if (e == cudaSuccess)
+      e = launch_product<BACK, DT, CG>(along_g, across_w, across_g, across_h, out_w, a, 0, s);
+    if (e == cudaSuccess) e = launch_behind(join_parts<DT, CG>, 4u * (unsigned)num_sms(), 256, 0, 1, s, a);
     if (e != cudaSuccess) return fail(SCAPE_ECUDA, "product (gradient): %s", cudaGetErrorString(e));
   }
   return SCAPE_OK;
