@@ -104,16 +104,19 @@ struct CeArgs {
   int64_t dw_stride;
 };
 
-// Tiles of a product, in the order in which they are worked on: kGroup rows of tiles at a
-// time, down first.
+__device__ __forceinline__ int up_div(int x, int y) { return (x + y - 1) / y; }
+
+// Tiles of a product, in the order in which they are worked on: up to kGroup rows of tiles
+// at a time, down first, in groups of equal height.
 struct Tiles {
   int mt, nt, kb;  // kb: blocks of the sum
   __device__ __forceinline__ int count() const { return mt * nt; }
   __device__ __forceinline__ void place(int tile, int& m, int& n) const {
-    const int g = tile / (kGroup * nt), in = tile - g * kGroup * nt;
-    const int rows = min(kGroup, mt - g * kGroup);
+    const int groups = up_div(mt, kGroup), high = up_div(mt, groups);
+    const int g = tile / (high * nt), in = tile - g * high * nt;
+    const int rows = min(high, mt - g * high);
     n = in / rows;
-    m = g * kGroup + in - n * rows;
+    m = g * high + in - n * rows;
   }
 };
 
@@ -124,8 +127,6 @@ struct Unit {
   int part;  // its place among the parts of its product, -1 for a whole tile
   bool dw;   // BACK: of dW
 };
-
-__device__ __forceinline__ int up_div(int x, int y) { return (x + y - 1) / y; }
 
 // The units of a CTA (or pair), one after the other.
 template <int JOB, int CG>
