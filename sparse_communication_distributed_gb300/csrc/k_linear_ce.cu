@@ -305,7 +305,7 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
 #pragma unroll
       for (int i = 0; i < 32; i++) f[i] = 0.0f;
     } else {
-      tmem_load32(tmem + (uint32_t)(32 * c), f);
+      tmem_load(tmem + (uint32_t)(32 * c), f);
     }
   };
   // (both halves of a row are in the buffer: 64 columns go out from column x)
@@ -324,26 +324,27 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
     const int first = u.n * a.bn + half * 128;
     float m = neg_inf(), y = 0.0f;
     bool mine = false;
-    auto logits = [&](int c) {  // 32 of them; words that there are not are out of the running
-      const int w0 = first + 32 * c;
-      fetch(c);
-      if (w0 + 32 > end) {
+    float l[64];
+    auto logits = [&](int c) {  // 64 of them; words that there are not are out of the running
+      const int w0 = first + 64 * c;
+      tmem_load(tmem + (uint32_t)(64 * c), l);
+      if (w0 + 64 > end) {
 #pragma unroll
-        for (int i = 0; i < 32; i++)
-          if (w0 + i >= end) f[i] = neg_inf();
+        for (int i = 0; i < 64; i++)
+          if (w0 + i >= end) l[i] = neg_inf();
       }
     };
-    for (int c = 0; c < 4 && first + 32 * c < end; c++) {
+    for (int c = 0; c < 2 && first + 64 * c < end; c++) {
       logits(c);
-      const int w0 = first + 32 * c;
-      if ((uint32_t)(label - w0) < 32u) {
+      const int w0 = first + 64 * c;
+      if (label >= w0 && label < min(w0 + 64, end)) {
         mine = true;
 #pragma unroll
-        for (int i = 0; i < 32; i++)
-          if (label == w0 + i) y = f[i];
+        for (int i = 0; i < 64; i++)
+          if (label == w0 + i) y = l[i];
       }
 #pragma unroll
-      for (int i = 0; i < 32; i++) m = fmaxf(m, f[i]);
+      for (int i = 0; i < 64; i++) m = fmaxf(m, l[i]);
     }
     // (tensor memory is read a second time: that costs less than adjusting sums and what
     // is kept to a maximum that grows)
@@ -351,28 +352,31 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
     const bool keep = KEEP && first < a.keep;
     const int p = keep ? first / a.piece : 0;
     pair_t sum = pair(0.0f, 0.0f);
-    for (int c = 0; c < 4 && first + 32 * c < end; c++) {
+    for (int c = 0; c < 2 && first + 64 * c < end; c++) {
       logits(c);
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const pair_t e = ex2_2(mul2(add2(pair(f[i], f[i + 1]), pair(-by, -by)), pair(kLog2e, kLog2e)));
+      for (int i = 0; i < 64; i += 2) {
+        const pair_t e = ex2_2(mul2(add2(pair(l[i], l[i + 1]), pair(-by, -by)), pair(kLog2e, kLog2e)));
         sum = add2(sum, e);
-        f[i] = e.x;
-        f[i + 1] = e.y;
+        l[i] = e.x;
+        l[i + 1] = e.y;
       }
       if constexpr (KEEP) {
         if (!keep) continue;
+        const int x = first + 64 * c - p * a.piece;
+        if (CG == 2) reuse();
 #pragma unroll
-        for (int i = 0; i < 32; i++) f[i] *= kKept;
-        const int x = first + 32 * c - p * a.piece;
-        if constexpr (CG == 1) {  // (few rows, and tiles of any multiple of 16 words)
-          if (r < live)
-            store32<SCAPE_F16>(static_cast<char*>(a.g) + ((int64_t)p * a.cap + r) * a.piece * 2, x, end - p * a.piece, f);
-        } else {
-          if (!(c & 1)) reuse();
-          stage32<SCAPE_F16>(out, lane, c & 1, f);
-          if ((c & 1) || first + 32 * (c + 1) >= end) send(x & ~63, (int)(p * a.cap) + r0);
+        for (int side = 0; side < 2; side++) {
+#pragma unroll
+          for (int i = 0; i < 32; i++) f[i] = l[32 * side + i] * kKept;
+          if constexpr (CG == 2) {
+            stage32<SCAPE_F16>(out, lane, side, f);
+          } else if (r < live) {  // (few rows, and tiles of any multiple of 16 words)
+            store32<SCAPE_F16>(static_cast<char*>(a.g) + ((int64_t)p * a.cap + r) * a.piece * 2, x + 32 * side,
+                               end - p * a.piece, f);
+          }
         }
+        if (CG == 2) send(x, (int)(p * a.cap) + r0);
       }
     }
     const float s = sum.x + sum.y;
