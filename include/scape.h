@@ -599,7 +599,7 @@ int scape_expert_combine_backward(const void* d_out, const void* y, int dtype, u
  * Squares are added up in fp32 over 64 elements and in 64 bits from there on, and
  * whatever would leave fp32's range in 64 bits from the start; each product is
  * formed in fp32 and rounded to the result's type.  A group whose norm is infinite or NaN is not scaled (the caller
- * sees the norm); so is one of norm 0.  The same inputs give the same bits. */
+ * sees the norm), nor is one of norm 0.  The same inputs give the same bits. */
 typedef struct {
   const void* const* grads; /* HOST array of n_tensors DEVICE pointers, each to numel[i] contiguous
                                elements at any multiple of the element's size */

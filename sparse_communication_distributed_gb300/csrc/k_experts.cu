@@ -303,7 +303,8 @@ __device__ void clear_empty_rows(const RowArgs& a, int64_t item, int lane) {
   }
 }
 
-// A warp takes R units a lane of a token's row, and stores them k times.
+// A warp takes R units a lane of a token's row, and stores them k times.  Bound by HBM: 16384 x
+// 2048 bf16 to 8 experts in 93 us (6.5 TB/s), stores for the most part.
 template <int BYTES, int R>
 __global__ __launch_bounds__(kThreads) void dispatch_rows(const RowArgs a) {
   using U = typename Unit<BYTES>::T;
@@ -335,7 +336,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_rows(const RowArgs a) {
 
 // out[t] = sum over j of w_tj y[slot_tj], in this order, rounded once.  The loads of
 // AHEAD choices are under way together: with those of one alone (64 bytes a lane) 605 MB
-// took 138 us, with 128 bytes of four 90.
+// took 138 us, with 128 bytes of four 90 (6.7 TB/s).
 template <int DT, int BYTES, int R, int AHEAD>
 __global__ __launch_bounds__(kThreads, 4) void combine_rows(const RowArgs a) {
   using P = Packed<DT, BYTES>;
@@ -388,7 +389,7 @@ __global__ __launch_bounds__(kThreads, 4) void combine_rows(const RowArgs a) {
 
 // dy[slot] = w dout[t], dw = <dout[t], y[slot]>.  A warp has two choices of a token, whose
 // row it loads once for both; the warps of the token's other choices find it in L1.
-// (With one choice a warp, and half of the loads under way: 128 us for 696 MB.)
+// (With one choice a warp, and half of the loads under way: 128 us for 696 MB; so, 114.)
 constexpr int kPair = 2;
 template <int DT, int BYTES, int R>
 __global__ __launch_bounds__(kThreads, 4) void combine_grad(const RowArgs a) {

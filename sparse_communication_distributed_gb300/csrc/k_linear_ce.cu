@@ -475,7 +475,12 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
 
 // Warp 0 copies tiles to shared memory, warp 1 (of a pair's first CTA) issues the products,
 // warp 2 allocates tensor memory, warps 4 to 11 are the epilogue: two accumulators let it
-// work on one tile during the products of the next.
+// work on one tile during the products of the next.  The products follow one another
+// without a pause (4864 x 32000 x 4096: 1.027 M cycles of 1.024 M at the full rate), so
+// that the time of large calls is the clock's, which the power limit sets: 16384 x 32000 x
+// 2048 in 1.09 ms (1.97 PFLOP/s) alone, 4.07 ms for loss and gradient, one call behind the
+// other.  Tiles of one CTA alone took 10 % more.  The epilogue is hidden from a dim of 768
+// on; at 512 it takes as long as the products.
 template <int JOB, int DT, int CG, bool KEEP>
 __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ CUtensorMap map_a,
                                                        const __grid_constant__ CUtensorMap map_b,
@@ -681,7 +686,8 @@ struct RowsArgs {
 // The rows with a term, together and in their order.  Each CTA takes a chunk of the
 // rows and counts those in front of it by itself: at most 512 CTAs read all labels,
 // which costs less than a second kernel.  The rows without a term get their loss and
-// gradient of 0.
+// gradient of 0.  (One CTA that numbers the rows took 33 us for 16384 of them, and a second
+// kernel 20 us to copy them; this one copies them in 31 us, 4096 rows in 9.)
 constexpr int kRowThreads = 512, kRowWarps = kRowThreads / 32, kMaxRowCtas = 512;
 __global__ __launch_bounds__(kRowThreads) void take_rows(const RowsArgs a) {
   __shared__ uint32_t scan[kRowWarps + 1];
@@ -783,7 +789,7 @@ __global__ __launch_bounds__(256) void row_losses(const CeArgs a) {
 
 // G of a piece in the place of its kept exponentials e:
 //   p = e 2^((m_part - m) log2e - log2 sum - 15),  G = w (p - [label]), w scaled
-// A warp has a run of a row, four vectors a lane.
+// A warp has a run of a row, four vectors a lane.  Bound by HBM: 4096 x 50257 at 5.4 TB/s.
 template <int DT>
 __global__ __launch_bounds__(256, 4) void grad_kept(const CeArgs a) {
   using E = Elem<DT>;

@@ -124,6 +124,48 @@ def test_several_pieces_of_the_vocabulary():
     check(H, W, y, w, "bf16")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_pieces_that_are_worked_out_again(dtype):
+    # more logits than exponentials are kept of (1 GB): three pieces, the last one recomputed
+    H, W, y, w = inputs(20000, 64, 30001, dtype, masked=0.05)
+    check(H, W, y, w * (8192.0 if dtype == "f16" else 1.0), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T", [3, 128])
+def test_a_few_rows_of_a_million_words(T, dtype):
+    # two pieces, and narrow tiles of words that lie in both: nothing is kept
+    H, W, y, w = inputs(T, 8, 1100003, dtype, weights=False)
+    y[0], y[1], y[2] = 1100002, 550143, 550144
+    check(H, W, y, w, dtype)
+
+
+def test_many_rows():
+    H, W, y, w = inputs(300001, 64, 1000, "bf16", masked=0.3)
+    check(H, W, y, w, "bf16")
+
+
+def test_the_widest_rows():
+    H, W, y, w = inputs(150, 65536, 300, "bf16", masked=0.1)
+    check(H, W, y, w, "bf16")
+
+
+@pytest.mark.parametrize("T", [127, 128, 129, 255, 256, 257])
+def test_around_the_tiles_of_rows(T):
+    for V in (255, 256, 257, 513):
+        H, W, y, w = inputs(T, 64, V, "bf16", seed=V, weights=False)
+        y[-1], y[0] = V - 1, 0
+        check(H, W, y, w, "bf16")
+
+
+def test_labels_beyond_32_bits_are_counted():
+    H, W, y, w = inputs(50, 64, 100, "bf16")
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y[3], y[4], y[5] = 2 ** 32 + 5, 2 ** 62, -2 ** 40
+    loss = pkg.linear_ce(H, W, y, row_weight=w, bad_count=bad)
+    assert int(bad) == 2 and loss[3:6].eq(0).all() and (loss[6:] > 0).all()
+
+
 def test_many_tiles_of_every_product():
     H, W, y, w = inputs(5000, 1288, 9001, "bf16", masked=0.05)
     check(H, W, y, w, "bf16")
