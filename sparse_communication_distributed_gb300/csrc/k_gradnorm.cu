@@ -155,7 +155,7 @@ struct Groups {
 __global__ __launch_bounds__(1024) void norm_finish(const __grid_constant__ Groups g,
                                                     const double* __restrict__ part, float max_norm,
                                                     float* __restrict__ norms,
-                                                    float* __restrict__ scales) {
+                                                    float2* __restrict__ scales) {
   __shared__ double buf[32];
   grid_launch_dependents();
   grid_dependency_wait();
@@ -168,8 +168,10 @@ __global__ __launch_bounds__(1024) void norm_finish(const __grid_constant__ Grou
     const double norm = sqrt(d);
     norms[blockIdx.x] = (float)norm;
     // (an infinite norm and NaN are not clipped: the caller sees them)
+    const double scale = norm > (double)max_norm && norm < INFINITY ? (double)max_norm / norm : 1.0;
+    // two factors: the scale itself may be below fp32's range where the products are not
     if (scales)
-      scales[blockIdx.x] = norm > (double)max_norm && norm < INFINITY ? (float)((double)max_norm / norm) : 1.0f;
+      scales[blockIdx.x] = scale < 0x1p-100 ? make_float2((float)(scale * 0x1p100), 0x1p-100f) : make_float2((float)scale, 1.0f);
   }
 }
 
@@ -181,13 +183,13 @@ __device__ __forceinline__ void st_stream_u4(void* p, const uint4 v) {
 
 // Eight products, stored.
 template <int DT>
-__device__ __forceinline__ void store8(typename Elem<DT>::T* p, const float (&f)[8], float scale) {
+__device__ __forceinline__ void store8(typename Elem<DT>::T* p, const float (&f)[8], float2 scale) {
   using E = Elem<DT>;
 #pragma unroll
   for (int i = 0; i < 8 / E::kPerVec; i++) {
     float g[E::kPerVec];
 #pragma unroll
-    for (int j = 0; j < E::kPerVec; j++) g[j] = f[i * E::kPerVec + j] * scale;
+    for (int j = 0; j < E::kPerVec; j++) g[j] = f[i * E::kPerVec + j] * scale.x * scale.y;
     st_stream_u4(p + i * E::kPerVec, E::pack(g));
   }
 }
@@ -195,7 +197,7 @@ __device__ __forceinline__ void store8(typename Elem<DT>::T* p, const float (&f)
 // dst = src * scale.  Whole stores of 16 bytes from the first boundary of dst on;
 // loads of 16 bytes where src has its boundary there too.
 template <int SDT, int DDT>
-__device__ __forceinline__ void scale_chunk(const void* from, void* to, uint32_t n, float scale) {
+__device__ __forceinline__ void scale_chunk(const void* from, void* to, uint32_t n, float2 scale) {
   using S = Elem<SDT>;
   using D = Elem<DDT>;
   const typename S::T* src = static_cast<const typename S::T*>(from);
@@ -204,8 +206,8 @@ __device__ __forceinline__ void scale_chunk(const void* from, void* to, uint32_t
   const uint32_t head = min(n, off ? (uint32_t)D::kPerVec - off : 0u);
   const uint32_t n8 = (n - head) / 8, done = head + n8 * 8;
   const uint32_t tid = threadIdx.x;
-  if (tid < head) dst[tid] = D::make(S::load(src + tid) * scale);
-  if (done + tid < n) dst[done + tid] = D::make(S::load(src + done + tid) * scale);
+  if (tid < head) dst[tid] = D::make(S::load(src + tid) * scale.x * scale.y);
+  if (done + tid < n) dst[done + tid] = D::make(S::load(src + done + tid) * scale.x * scale.y);
   src += head;
   dst += head;
   if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
@@ -254,14 +256,14 @@ __device__ __forceinline__ void scale_chunk(const void* from, void* to, uint32_t
 // A kernel for each pair of types: all of them in one take 255 registers, one CTA an SM.
 template <int CAP, int SDT, int DDT>
 __global__ __launch_bounds__(kThreads, kResident) void clip_chunks(const __grid_constant__ Table<CAP> tb,
-                                                                   const float* __restrict__ scales) {
+                                                                   const float2* __restrict__ scales) {
   grid_launch_dependents();
   grid_dependency_wait();
   for (uint32_t i = blockIdx.x; i < tb.chunks; i += gridDim.x) {
     const uint32_t c = tb.chunks - 1 - i;  // what was read last comes first
     const Tensor& t = tb.t[tensor_of(tb, c)];
-    const float scale = scales[t.group];
-    if (scale == 1.0f && t.src == t.dst) continue;  // in place: nothing to change
+    const float2 scale = scales[t.group];
+    if (scale.x == 1.0f && scale.y == 1.0f && t.src == t.dst) continue;  // in place: nothing to change
     const uint64_t first = (uint64_t)(c - t.chunk0) * tb.chunk_elems;
     const uint32_t n = (uint32_t)min((uint64_t)tb.chunk_elems, t.n - first);
     scale_chunk<SDT, DDT>(static_cast<const typename Elem<SDT>::T*>(t.src) + first,
@@ -387,7 +389,7 @@ struct Todo {
   void* const* out;
   const uint8_t* out_dtypes;
   double* part;
-  const float* scales;
+  const float2* scales;
   uint32_t chunks_of(uint32_t i) const { return (uint32_t)((g->numel[i] + chunk_elems - 1) / chunk_elems); }
 };
 
@@ -441,7 +443,7 @@ cudaError_t launch_all(const Todo& q, cudaStream_t s) {
   return e;
 }
 
-uint64_t bytes_of(const Cut& cut) { return cut.chunks * 8 + kMaxGroups * 4; }
+uint64_t bytes_of(const Cut& cut) { return cut.chunks * 8 + kMaxGroups * 8; }
 
 int norm_and_clip(const scape_grads* g, bool clip, float max_norm, void* const* out, const uint8_t* odt,
                   float* norms, void* workspace, uint64_t workspace_bytes, void* stream) {
@@ -471,7 +473,7 @@ int norm_and_clip(const scape_grads* g, bool clip, float max_norm, void* const* 
     return fail(SCAPE_EINVAL, "workspace must be %llu bytes, 16-byte aligned", (unsigned long long)need);
 
   double* part = static_cast<double*>(workspace);
-  float* scales = reinterpret_cast<float*>(part + cut.chunks);
+  float2* scales = reinterpret_cast<float2*>(part + cut.chunks);
   std::vector<uint32_t> group(g->n_tensors), part0(g->n_tensors);
   Todo q{g, (uint32_t)cut.chunk_elems, part0.data(), group.data(), nullptr, nullptr, part, scales};
   Groups gr{};
@@ -490,7 +492,7 @@ int norm_and_clip(const scape_grads* g, bool clip, float max_norm, void* const* 
   cudaError_t e = launch_all(q, s);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "norm_chunks: %s", cudaGetErrorString(e));
   e = launch_behind(norm_finish, g->n_groups, 1024, s, gr, (const double*)part, max_norm, norms,
-                    clip ? scales : (float*)nullptr);
+                    clip ? scales : (float2*)nullptr);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "norm_finish: %s", cudaGetErrorString(e));
   if (!clip) return SCAPE_OK;
   q.out = out;

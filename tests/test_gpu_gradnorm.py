@@ -127,6 +127,18 @@ def test_squares_beyond_32_bits(dtype, scale):
         assert ((o.double() - ref).abs() <= 20 * U * ref.abs() + 2.0 ** -149).all()
 
 
+def test_a_scale_below_32_bits():
+    # 1e-25 / 4e37 is no number of 32 bits, what it gives is
+    t = torch.tensor([3e37, -2e37, 1e30, 1.0], device="cuda")
+    out = torch.empty(4, device="cuda")
+    n = float(pkg.clip_grads([t], 1e-25, out=[out]))
+    want = t.double() * (np.float32(1e-25).item() / norm64([t]))
+    assert abs(n - norm64([t])) <= 18 * U * n
+    assert ((out.double() - want).abs() <= 20 * U * want.abs() + 2.0 ** -149).all() and float(out[0]) > 0
+    pkg.clip_grads([t], 1e-25)
+    assert torch.equal(t, out)
+
+
 def test_one_huge_element_among_small_ones():
     t = torch.full((100000,), 1e-20, device="cuda")
     t[54321] = 3e25
