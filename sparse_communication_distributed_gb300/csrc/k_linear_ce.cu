@@ -153,7 +153,8 @@ struct Work {
 // gradient took 555 us in two and takes 533 in one.  Split, and added up by join_parts, are the tiles of dH where they are
 // too few and too long for that, and those of dW that would be a last round by themselves.
 constexpr int kMaxParts = 2;         // of each product, per CTA
-constexpr float kUnitCost = 6.0f;    // what a unit costs beside its blocks, in blocks
+constexpr float kUnitCost = 4.0f;    // what a unit costs beside its blocks, in blocks, of pairs
+constexpr float kUnitCostOne = 1.5f; // ... of CTAs alone, whose blocks wait for HBM (16 rows: 108 us; with 6: 124)
 constexpr float kPartCost = 0.14f;   // what writing and adding up a CTA's part costs, on all CTAs
 template <int CG>
 struct Work<BACK, CG> {
@@ -167,12 +168,13 @@ struct Work<BACK, CG> {
     const int all = a.grid;
     h = {up_div(live, kRows), up_div(a.D, kN), up_div(a.vn, kK)};
     w = {up_div(a.vn, kRows), up_div(a.D, kN), up_div(live, kK)};
-    const float cost_w = (float)w.kb + kUnitCost;
+    constexpr float kUnit = CG == 2 ? kUnitCost : kUnitCostOne;
+    const float cost_w = (float)w.kb + kUnit;
     split_h = 1;
     float best = 0.0f;
     for (int s = 1; s <= 32 && (s == 1 || (s * h.count() <= kMaxParts * all && 8 * s <= h.kb)); s++) {
       const int n = s * h.count();
-      const float unit = (float)h.kb / (float)s + kUnitCost;
+      const float unit = (float)h.kb / (float)s + kUnit;
       const float even = ((float)n * unit + (float)w.count() * cost_w) / (float)all;
       const float last = (float)up_div(n, all) * unit;
       const float cost = fmaxf(even, last) + (s > 1 ? kPartCost * (float)(n * CG) : 0.0f);
@@ -185,7 +187,7 @@ struct Work<BACK, CG> {
     const int n = split_h * h.count();
     each = n / all;
     more = n - each * all;
-    const float unit = (float)h.kb / (float)split_h + kUnitCost;
+    const float unit = (float)h.kb / (float)split_h + kUnit;
     early = more ? min((int)(unit / cost_w + 0.5f), w.count() / (all - more)) : 0;
     const int left = w.count() - early * (all - more), rest = left % all;
     whole = w.count();
@@ -422,11 +424,12 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
     const int at = half * 32 * kM + quarter * 32 + lane;  // of the row's first columns in a tile's sums
     if (u.part >= 0) {
       float4* part = reinterpret_cast<float4*>(Work<BACK, CG>::part_at(a, u.dw, u.part, rank)) + at;
+      const bool on = u.dw || r < live;
       for (int c = 0; c < 4; c++) {
         fetch(c);
 #pragma unroll
         for (int j = 0; j < 8; j++)
-          part[(c * 8 + j) * kM] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+          if (on) part[(c * 8 + j) * kM] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
       }
     } else if (!u.dw) {
       const bool on = r < live;
@@ -877,6 +880,7 @@ __global__ __launch_bounds__(256) void join_parts(const CeArgs a) {
     int m, n;
     all.place(tile, m, n);
     const int r = m * kRows + rank * kM + row, d = n * kN + 8 * j;
+    if (d >= a.D || (dw ? a.v0 + r >= a.V : r >= live)) continue;
     float f[8] = {};
     auto add = [&](const float* sums) {
       const float4* q = reinterpret_cast<const float4*>(sums) + 2 * j * kM + row;
@@ -895,7 +899,6 @@ __global__ __launch_bounds__(256) void join_parts(const CeArgs a) {
         continue;
       }
     }
-    if (d >= a.D || (dw ? a.v0 + r >= a.V : r >= live)) continue;
     if (!dw) add_left<DT>(a, r, d, f);
 #pragma unroll
     for (int e = 0; e < 8; e++) f[e] *= un;
