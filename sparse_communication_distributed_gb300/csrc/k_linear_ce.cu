@@ -150,12 +150,14 @@ struct Work {
 // dH do not go evenly into the CTAs, those that have one less begin with as many tiles of
 // dW as that one takes.  So the CTAs end together, which two launches do not let them:
 // with 55 tiles of dH for 76 pairs of CTAs and 625 of dW (2723 rows, 32000 x 1280) a whole
-// gradient took 555 us in two and takes 533 in one.  Split, and added up by join_parts, are the tiles of dH where they are
-// too few and too long for that, and those of dW that would be a last round by themselves.
+// gradient took 555 us in two and takes 530 in one.  Split, and added up by join_parts, are
+// the tiles of dH where they are too few and too long for that, and those of dW that
+// would be a last round by themselves.
 constexpr int kMaxParts = 2;         // of each product, per CTA
-constexpr float kUnitCost = 4.0f;    // what a unit costs beside its blocks, in blocks, of pairs
-constexpr float kUnitCostOne = 1.5f; // ... of CTAs alone, whose blocks wait for HBM (16 rows: 108 us; with 6: 124)
-constexpr float kPartCost = 0.14f;   // what writing and adding up a CTA's part costs, on all CTAs
+// What a unit costs beside its blocks, in blocks: of pairs (512 rows: 175 us, with 6 181, with
+// 8 184), of CTAs alone, whose blocks wait for HBM (16 rows: 108 us, with 0.5 116, with 3
+// 115, with 6 124); and what writing and adding up a CTA's part costs, on all CTAs.
+constexpr float kUnitCost = 4.0f, kUnitCostOne = 1.5f, kPartCost = 0.14f;
 template <int CG>
 struct Work<BACK, CG> {
   Tiles h, w;
