@@ -6,8 +6,9 @@
 // chunk's first place in every expert's segment, place_choices ranks the choices
 // inside a chunk (a warp's 32 at a time, equal experts found with match.any) and
 // writes both directions of the permutation.  Up to one chunk of choices all of it
-// is one kernel of one CTA; up to kFewChunks chunks place_choices adds up the counts
-// itself, which is sooner done than another kernel started.
+// is one kernel of one CTA.  (A place_choices that adds up the counts itself saves a
+// kernel and gains nothing: 7.4 us either way for 48 chunks, 12.1 instead of 7.8 for 64 and
+// 256 experts.)
 //
 // Rows move in 16-byte vectors where their length and addresses allow, else in
 // units of 4 or 2 bytes.  A token's row is read once and stored to its k places
@@ -29,7 +30,6 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kRounds = 8;                          // choices of a thread
 constexpr int kChunk = kThreads * kRounds;          // choices of a CTA
 constexpr int kMaxExperts = 1024, kMaxChoices = 32;
-constexpr int kFewChunks = 64;
 
 struct PlanArgs {
   const int32_t* idx;
@@ -101,10 +101,8 @@ __global__ __launch_bounds__(1024) void place_scan(const PlanArgs a) {
   }
 }
 
-// ONE: one chunk, whose own counts are the totals.  FEW: the counts are as place_counts
-// left them.  MANY: after place_scan.
-enum Chunks { ONE, FEW, MANY };
-template <Chunks C>
+// SINGLE: one chunk, whose own counts are the totals.
+template <bool SINGLE>
 __global__ __launch_bounds__(kThreads) void place_choices(const PlanArgs a) {
   __shared__ uint16_t hist[kWarps][kMaxExperts];  // a warp's choices of each expert, then those of the warps before it
   __shared__ int32_t base[kMaxExperts];           // place of the chunk's first choice of each expert
@@ -114,11 +112,9 @@ __global__ __launch_bounds__(kThreads) void place_choices(const PlanArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   grid_launch_dependents();
   for (int i = tid; i < kWarps * kMaxExperts / 2; i += kThreads) reinterpret_cast<uint32_t*>(hist)[i] = 0;
-  if (C == FEW)
-    for (int e = tid; e < a.E; e += kThreads) base[e] = total[e] = 0;
   __syncthreads();
   // (idx was complete before place_counts let this kernel start)
-  if (C == ONE) grid_dependency_wait();
+  if (SINGLE) grid_dependency_wait();
   // a warp's choices follow one another: 32 a round
   const int64_t first = (int64_t)blockIdx.x * kChunk + wid * (32 * kRounds) + lane;
   int ex[kRounds];
@@ -149,22 +145,7 @@ __global__ __launch_bounds__(kThreads) void place_choices(const PlanArgs a) {
     if (lane == 0 && n_bad) atomicAdd(a.bad, n_bad);
   }
   __syncthreads();
-  if (C != ONE) grid_dependency_wait();
-  if (C == FEW) {  // threads side by side have experts side by side; as many slices of chunks as there are threads for
-    const int wide = min(kThreads, (a.E + 31) / 32 * 32), slices = kThreads / wide;
-    for (int e = tid % wide; e < a.E && tid / wide < slices; e += wide) {
-      int32_t before = 0, all = 0;
-#pragma unroll 8
-      for (int b = tid / wide; b < (int)a.chunks; b += slices) {
-        const int32_t c = a.counts[(int64_t)b * a.E + e];
-        all += c;
-        if (b < (int)blockIdx.x) before += c;
-      }
-      atomicAdd(&total[e], all);
-      atomicAdd(&base[e], before);
-    }
-    __syncthreads();
-  }
+  if (!SINGLE) grid_dependency_wait();
   // segments: each thread has a run of experts
   const int per = (a.E + kThreads - 1) / kThreads;
   uint32_t room = 0;
@@ -178,10 +159,8 @@ __global__ __launch_bounds__(kThreads) void place_choices(const PlanArgs a) {
         hist[w][e] = (uint16_t)own;
         own += c;
       }
-      if (C != FEW) {
-        total[e] = C == ONE ? (int32_t)own : a.totals[e];
-        base[e] = C == ONE ? 0 : a.counts[(int64_t)blockIdx.x * a.E + e];
-      }
+      total[e] = SINGLE ? (int32_t)own : a.totals[e];
+      base[e] = SINGLE ? 0 : a.counts[(int64_t)blockIdx.x * a.E + e];
       room += (uint32_t)((total[e] + a.align - 1) / a.align * a.align);
     }
   }
@@ -596,17 +575,13 @@ SCAPE_API int scape_expert_plan(const int32_t* idx, uint64_t tokens, int k, int 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (a.chunks <= 1) {
-    e = launch_behind(place_choices<ONE>, 1, kThreads, s, a);
+    e = launch_behind(place_choices<true>, 1, kThreads, s, a);
   } else {
     e = launch_behind(place_counts, (unsigned)a.chunks, kThreads, s, a);
     if (e != cudaSuccess) return fail(SCAPE_ECUDA, "place_counts: %s", cudaGetErrorString(e));
-    if (a.chunks <= kFewChunks) {
-      e = launch_behind(place_choices<FEW>, (unsigned)a.chunks, kThreads, s, a);
-    } else {
-      e = launch_behind(place_scan, (unsigned)((experts + 31) / 32), 1024, s, a);
-      if (e != cudaSuccess) return fail(SCAPE_ECUDA, "place_scan: %s", cudaGetErrorString(e));
-      e = launch_behind(place_choices<MANY>, (unsigned)a.chunks, kThreads, s, a);
-    }
+    e = launch_behind(place_scan, (unsigned)((experts + 31) / 32), 1024, s, a);
+    if (e != cudaSuccess) return fail(SCAPE_ECUDA, "place_scan: %s", cudaGetErrorString(e));
+    e = launch_behind(place_choices<false>, (unsigned)a.chunks, kThreads, s, a);
   }
   return e == cudaSuccess ? SCAPE_OK : fail(SCAPE_ECUDA, "place_choices: %s", cudaGetErrorString(e));
 }

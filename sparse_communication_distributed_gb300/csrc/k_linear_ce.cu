@@ -968,7 +968,8 @@ struct Cut {
 
 // G takes at most this much, so that a gradient needs little memory beside its results:
 // of a piece, and of all pieces that are there at once (kept ones; the others come one
-// after the other).
+// after the other).  Pieces of half and of twice the size: 16384 x 32000 in 4.50 and 4.44 ms
+// instead of 4.40.
 constexpr uint64_t kPieceBytes = 512ull << 20, kAllBytes = 1024ull << 20;
 
 uint64_t ceil_div(uint64_t x, uint64_t y) { return (x + y - 1) / y; }
@@ -978,7 +979,7 @@ Cut cut_of(const scape_linear_ce_args* q, bool grad) {
   c.cap = std::max<uint64_t>(up(q->rows, 256), 256);
   // Few rows: the weights' way to the CTAs is what takes time, and tiles of 256 words leave
   // CTAs without any.  The width that needs the fewest words a CTA, all rounds together
-  // (32 for a tile's other costs).
+  // (32 for a tile's other costs).  16 rows, 32000 words: 224 a tile 30.7 us, 256 32.4, 112 35.2, 64 52.
   if (q->rows <= kM) {
     const uint64_t sms = (uint64_t)num_sms();
     uint64_t best = ~0ull;
@@ -1249,7 +1250,8 @@ SCAPE_API int scape_linear_ce(const scape_linear_ce_args* args, void* workspace,
     return fail(SCAPE_EINVAL, "workspace must be %llu bytes, 256-byte aligned", (unsigned long long)l.bytes);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
-  // pairs of CTAs, unless the rows of one are enough
+  // Pairs of CTAs, unless the rows of one are enough (dim 2048, 32000 words: 128 rows 34 us and 115 with gradients, in
+  // pairs 38 and 121; 200 rows in pairs 38 and 131, in CTAs alone 42 and 140).
   if (args->rows <= (uint64_t)kM)
     return args->dtype == SCAPE_BF16 ? run<SCAPE_BF16, 1>(args, c, l, ws, s) : run<SCAPE_F16, 1>(args, c, l, ws, s);
   return args->dtype == SCAPE_BF16 ? run<SCAPE_BF16, 2>(args, c, l, ws, s) : run<SCAPE_F16, 2>(args, c, l, ws, s);
