@@ -501,7 +501,10 @@ int scape_route_backward(const scape_route_args* args, const int32_t* idx, const
  * Products are of 16-bit operands added up in fp32; statistics and losses are fp32.
  * G is rounded to the operands' type (after dividing the weights by the largest of
  * them; for fp16 its entries then keep their precision down to 2^-28), each gradient
- * once more.  dim is a multiple of 8, matrices are 16-byte
+ * once more.  Where the logits are kept between the loss and the gradient, the
+ * probabilities are right to 2^-11 (bf16; 2^-9 for words 2^48 or more below the
+ * likeliest of the 128 around them; fp16: 2^-13, below 2^12 2^-11) as far down as G's
+ * type goes.  dim is a multiple of 8, matrices are 16-byte
  * aligned with strides of a multiple of 8 elements.  The kernels' waits are bounded:
  * one that ran out (which says that the GPU or the library is at fault) makes all
  * losses NaN. */

@@ -7,17 +7,15 @@
 // Four products on the tensor cores (16-bit operands, fp32 accumulators in tensor
 // memory), one kernel for all:
 //   LOSS  H W^T: the maximum and the sum of exponentials of every row of a tile, and
-//         the label's logit; for a gradient also the exponentials themselves, for as
-//         many words as there is room for
+//         the label's logit; for a gradient also the logits themselves, as distances
+//         from that maximum, for as many words as there is room for
 //   GRAD  the same product again, for a piece of the vocabulary without such room: G of
 //         that piece
 //   BACK  G W, added up over the pieces in fp32, and G^T H, complete for the piece's
 //         words: the tiles of both in one launch
-// With GRAD a gradient costs 8 T D V operations, without it 6.  What LOSS keeps are
-// exponentials against the maximum of their 128 words, in fp16 times 2^15: their
-// rounding (half a step is 2^-11) does not count beside that of a bf16 G (2^-8) and is
-// as large as that of an fp16 one, and G takes their place (grad_kept).  Logits in 16
-// bits would not do: exp() makes an error of 2^-8 |l| of them.
+// With GRAD a gradient costs 8 T D V operations, without it 6.  What LOSS keeps of a
+// logit is its distance from the maximum of its 128 words, in 16 bits (Kept), and G
+// takes its place (grad_kept).
 //
 // Rows without a term (no label, weight 0) are left out: the others are copied
 // together first, so that neither time nor the gradients depend on what they hold.
@@ -246,21 +244,6 @@ struct Work<BACK, CG> {
   }
 };
 
-// 32 numbers of a row, columns [c, c + 32), in vectors of 8 that begin below n.
-template <int DT>
-__device__ __forceinline__ void store32(void* row, int c, int n, const float (&f)[32]) {
-  using E = Elem<DT>;
-  typename E::T* p = static_cast<typename E::T*>(row) + c;
-#pragma unroll
-  for (int j = 0; j < 4; j++)
-    if (c + 8 * j < n) {
-      float g[8];
-#pragma unroll
-      for (int i = 0; i < 8; i++) g[i] = f[8 * j + i];
-      reinterpret_cast<uint4*>(p)[j] = E::pack(g);
-    }
-}
-
 // A number as the operands' type holds it.
 template <int DT>
 __device__ __forceinline__ float rounded(float x) {
@@ -282,8 +265,12 @@ __device__ __forceinline__ void add_left(const CeArgs& a, int r, int d, float (&
   for (int j = 0; j < 8; j++) f[j] = __fmaf_rn(left, x[j], f[j]);
 }
 
-// 32 results of a row into the warp's buffer, whose rows hold 64 of them in swizzled
-// vectors (as the copy engine expects them); "side" is the half.
+// Vector v of the lane's row in the warp's buffer, whose rows hold 64 results in eight
+// swizzled vectors (as the copy engine expects them).
+__device__ __forceinline__ uint32_t staged(uint32_t out, int lane, int v) {
+  return out + lane * 128 + (uint32_t)((v ^ (lane & 7)) * 16);
+}
+// 32 results of a row into the buffer; "side" is the half.
 template <int DT>
 __device__ __forceinline__ void stage32(uint32_t out, int lane, int side, const float (&f)[32]) {
 #pragma unroll
@@ -291,14 +278,57 @@ __device__ __forceinline__ void stage32(uint32_t out, int lane, int side, const 
     float g[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) g[i] = f[8 * j + i];
-    put_smem(out + lane * 128 + (uint32_t)(((side * 4 + j) ^ (lane & 7)) * 16), Elem<DT>::pack(g));
+    put_smem(staged(out, lane, side * 4 + j), Elem<DT>::pack(g));
+  }
+}
+
+// What is kept of a logit: its distance s <= 0 from the maximum of its 128 words, in units of
+// ln 2, as a code of 16 bits that is linear in s, with finer steps from the knee up to 0 than
+// from there down to where G holds no more of 2^s (code 0).  A step of s is that step times
+// ln 2 of the exponential, wherever it is; half of one is
+//   bf16  2^-11.5 down to s = -48, 2^-9.2 down to -128   (G: 2^-8)
+//   fp16  2^-13.1 down to s = -12, 2^-11.5 down to -40   (G: 2^-11, of its own least step below -28)
+// (Exponentials in fp16 lost their bits from s = -29 on and all of them from -40, and their
+// rounding was as large as that of an fp16 G: the gradients of 2000 words that are no label,
+// 300 rows, were 2.93e-4 off and are 2.63e-4.)
+template <int DT> struct Kept;
+template <> struct Kept<SCAPE_BF16> {  // codes of the two lines at s = 0, codes a unit
+  static constexpr float kHigh = 1024.0f, kLow = 204.75f, kLow0 = 26211.0f;
+};
+template <> struct Kept<SCAPE_F16> {
+  static constexpr float kHigh = 3072.0f, kLow = 1024.0f, kLow0 = 40959.0f;
+};
+constexpr float kHigh0 = 65535.0f;
+constexpr float kInt = 8388608.0f;  // 2^23: a sum with it is rounded to a whole number, its low bits
+
+// Two codes as the low 16 bits of two floats (the larger one of the two lines, at least 0).
+template <int DT>
+__device__ __forceinline__ uint32_t keep2(pair_t s) {
+  using K = Kept<DT>;
+  const pair_t hi = fma2(s, pair(K::kHigh, K::kHigh), pair(kInt + kHigh0, kInt + kHigh0));
+  const pair_t lo = fma2(s, pair(K::kLow, K::kLow), pair(kInt + K::kLow0, kInt + K::kLow0));
+  const float a = fmaxf(fmaxf(hi.x, lo.x), kInt), b = fmaxf(fmaxf(hi.y, lo.y), kInt);
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
+}
+// Eight exponentials 2^(s + by) of a vector of codes.
+template <int DT>
+__device__ __forceinline__ void kept8(const uint4 v, float by, float (&f)[8]) {
+  using K = Kept<DT>;
+  const float hi0 = by - kHigh0 / K::kHigh, lo0 = by - K::kLow0 / K::kLow;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const pair_t c = add2(pair(__uint_as_float(__byte_perm(w[i], 0x4B000000u, 0x7610)),
+                               __uint_as_float(__byte_perm(w[i], 0x4B000000u, 0x7632))), pair(-kInt, -kInt));
+    const pair_t hi = fma2(c, pair(1.0f / K::kHigh, 1.0f / K::kHigh), pair(hi0, hi0));
+    const pair_t lo = fma2(c, pair(1.0f / K::kLow, 1.0f / K::kLow), pair(lo0, lo0));
+    f[2 * i] = ex2(fminf(hi.x, lo.x));
+    f[2 * i + 1] = ex2(fminf(hi.y, lo.y));
   }
 }
 
 // What a warp of the epilogue does with its 32 rows and 128 columns of a unit, in tensor
 // memory at "tmem" ("empty": there were no products, all is 0).
-constexpr float kKept = 32768.0f;
-
 template <int JOB, int DT, int CG, bool KEEP>
 __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map_out, const Unit& u, int live, int rank,
                                          int half, int quarter, int lane, uint32_t tmem, bool empty, uint32_t out) {
@@ -358,30 +388,28 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
     pair_t sum = pair(0.0f, 0.0f);
     for (int c = 0; c < 2 && first + 64 * c < end; c++) {
       logits(c);
+      const int x = first + 64 * c - p * a.piece;
+      if (KEEP && CG == 2 && keep) reuse();
 #pragma unroll
-      for (int i = 0; i < 64; i += 2) {
-        const pair_t e = ex2_2(mul2(add2(pair(l[i], l[i + 1]), pair(-by, -by)), pair(kLog2e, kLog2e)));
-        sum = add2(sum, e);
-        l[i] = e.x;
-        l[i + 1] = e.y;
-      }
-      if constexpr (KEEP) {
-        if (!keep) continue;
-        const int x = first + 64 * c - p * a.piece;
-        if (CG == 2) reuse();
+      for (int v = 0; v < 8; v++) {
+        uint32_t code[4];
 #pragma unroll
-        for (int side = 0; side < 2; side++) {
-#pragma unroll
-          for (int i = 0; i < 32; i++) f[i] = l[32 * side + i] * kKept;
+        for (int i = 0; i < 4; i++) {
+          const pair_t s = mul2(add2(pair(l[8 * v + 2 * i], l[8 * v + 2 * i + 1]), pair(-by, -by)), pair(kLog2e, kLog2e));
+          sum = add2(sum, ex2_2(s));
+          if constexpr (KEEP) code[i] = keep2<DT>(s);
+        }
+        if constexpr (KEEP) {
+          if (!keep) continue;
+          const uint4 codes = make_uint4(code[0], code[1], code[2], code[3]);
           if constexpr (CG == 2) {
-            stage32<SCAPE_F16>(out, lane, side, f);
-          } else if (r < live) {  // (few rows, and tiles of any multiple of 16 words)
-            store32<SCAPE_F16>(static_cast<char*>(a.g) + ((int64_t)p * a.cap + r) * a.piece * 2, x + 32 * side,
-                               end - p * a.piece, f);
+            put_smem(staged(out, lane, v), codes);
+          } else if (r < live && x + 8 * v < end - p * a.piece) {  // (few rows, and tiles of any multiple of 32 words)
+            reinterpret_cast<uint4*>(static_cast<char*>(a.g) + (((int64_t)p * a.cap + r) * a.piece + x) * 2)[v] = codes;
           }
         }
-        if (CG == 2) send(x, (int)(p * a.cap) + r0);
       }
+      if (KEEP && CG == 2 && keep) send(x, (int)(p * a.cap) + r0);
     }
     const float s = sum.x + sum.y;
     if (r < live) {
@@ -792,8 +820,8 @@ __global__ __launch_bounds__(256) void row_losses(const CeArgs a) {
   }
 }
 
-// G of a piece in the place of its kept exponentials e:
-//   p = e 2^((m_part - m) log2e - log2 sum - 15),  G = w (p - [label]), w scaled
+// G of a piece in the place of what was kept of its logits, s:
+//   p = 2^(s + (m_part - m) log2e - log2 sum),  G = w (p - [label]), w scaled
 // A warp has a run of a row, four vectors a lane.  Bound by HBM: 4096 x 50257 at 5.4 TB/s.
 template <int DT>
 __global__ __launch_bounds__(256, 4) void grad_kept(const CeArgs a) {
@@ -835,10 +863,9 @@ __global__ __launch_bounds__(256, 4) void grad_kept(const CeArgs a) {
       if (v >= vecs) break;
       float x[8];
       if (left > 0) {
-        const float f = w * ex2(__fmaf_rn(m[i] - st.x, kLog2e, -st.y) - 15.0f);
-        Elem<SCAPE_F16>::unpack(e[i], x);
+        kept8<DT>(e[i], __fmaf_rn(m[i] - st.x, kLog2e, -st.y), x);
 #pragma unroll
-        for (int j = 0; j < 8; j++) x[j] *= f;
+        for (int j = 0; j < 8; j++) x[j] *= w;
         if (left < 8) {
 #pragma unroll
           for (int j = 0; j < 8; j++)
