@@ -126,6 +126,17 @@ struct Unit {
   bool dw;   // BACK: of dW
 };
 
+// The tensor cores cut off what an addition to an accumulator loses, always towards 0, so the
+// sums over the vocabulary and over the rows are taken in chains of at most so many blocks
+// (8192 terms, 512 additions), added up in fp32 by the epilogue, which has the time.  In one
+// chain the fp16 d_hidden of 32000 words with a common direction was 2.99e-4 off and is
+// 2.30e-4 (2.08e-4: its own rounding), d_weight of 8 M rows 3.1e-3 and is 2.0e-4.
+constexpr int kChain = 128;
+template <int JOB>
+__device__ __forceinline__ int chains_of(const Unit& u) {
+  return JOB == BACK ? max(1, up_div(u.k1 - u.k0, kChain)) : 1;
+}
+
 // The units of a CTA (or pair), one after the other.
 template <int JOB, int CG>
 struct Work {
@@ -152,6 +163,8 @@ struct Work {
 // the tiles of dH where they are too few and too long for that, and those of dW that
 // would be a last round by themselves.
 constexpr int kMaxParts = 2;         // of each product, per CTA
+// (Where rows make several chains of a tile of dW, the second half of the places for parts of dH
+// holds the CTAs' sums of chains; where dH is not split, it is free anyway.)
 // What a unit costs beside its blocks, in blocks: of pairs (512 rows: 175 us, with 6 181, with
 // 8 184), of CTAs alone, whose blocks wait for HBM (16 rows: 108 us, with 0.5 116, with 3
 // 115, with 6 124); and what writing and adding up a CTA's part costs, on all CTAs.
@@ -172,7 +185,8 @@ struct Work<BACK, CG> {
     const float cost_w = (float)w.kb + kUnit;
     split_h = 1;
     float best = 0.0f;
-    for (int s = 1; s <= 32 && (s == 1 || (s * h.count() <= kMaxParts * all && 8 * s <= h.kb)); s++) {
+    const int most = w.kb > kChain ? all : kMaxParts * all;
+    for (int s = 1; s <= 32 && (s == 1 || (s * h.count() <= most && 8 * s <= h.kb)); s++) {
       const int n = s * h.count();
       const float unit = (float)h.kb / (float)s + kUnit;
       const float even = ((float)n * unit + (float)w.count() * cost_w) / (float)all;
@@ -237,6 +251,10 @@ struct Work<BACK, CG> {
     }
     w.place(u.tile, u.m, u.n);
     return true;
+  }
+  // Where a CTA adds up the chains of a whole tile.
+  static __device__ __forceinline__ float* chains_at(const CeArgs& a, int me, int rank) {
+    return part_at(a, false, a.grid + me, rank);
   }
   // Where the parts of a CTA's half of a unit are.
   static __device__ __forceinline__ float* part_at(const CeArgs& a, bool dw, int part, int rank) {
@@ -328,10 +346,12 @@ __device__ __forceinline__ void kept8(const uint4 v, float by, float (&f)[8]) {
 }
 
 // What a warp of the epilogue does with its 32 rows and 128 columns of a unit, in tensor
-// memory at "tmem" ("empty": there were no products, all is 0).
+// memory at "tmem" ("empty": there were no products, all is 0).  BACK: begin, end: of the
+// unit's chains this is the first, the last; me: the CTA (or pair).
 template <int JOB, int DT, int CG, bool KEEP>
-__device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map_out, const Unit& u, int live, int rank,
-                                         int half, int quarter, int lane, uint32_t tmem, bool empty, uint32_t out) {
+__device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map_out, const Unit& u, int live, int me,
+                                         int rank, int half, int quarter, int lane, uint32_t tmem, bool empty, bool begin,
+                                         bool end, uint32_t out) {
   const int r0 = u.m * Shape<CG>::kRows + rank * kM + quarter * 32, r = r0 + lane;
   float f[32];
   auto fetch = [&](int c) {
@@ -452,20 +472,31 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
   } else {
     const float un = a.scale[1];
     const int at = half * 32 * kM + quarter * 32 + lane;  // of the row's first columns in a tile's sums
-    if (u.part >= 0) {
-      float4* part = reinterpret_cast<float4*>(Work<BACK, CG>::part_at(a, u.dw, u.part, rank)) + at;
+    float4* const chains = reinterpret_cast<float4*>(u.part >= 0 ? Work<BACK, CG>::part_at(a, u.dw, u.part, rank)
+                                                                 : Work<BACK, CG>::chains_at(a, me, rank)) + at;
+    auto fetch_sum = [&](int c) {  // of all chains so far
+      fetch(c);
+      if (!begin) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+          const float4 o = chains[(c * 8 + j) * kM];
+          f[4 * j] += o.x; f[4 * j + 1] += o.y; f[4 * j + 2] += o.z; f[4 * j + 3] += o.w;
+        }
+      }
+    };
+    if (u.part >= 0 || !end) {
       const bool on = u.dw || r < live;
       for (int c = 0; c < 4; c++) {
-        fetch(c);
+        fetch_sum(c);
 #pragma unroll
         for (int j = 0; j < 8; j++)
-          if (on) part[(c * 8 + j) * kM] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+          if (on) chains[(c * 8 + j) * kM] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
       }
     } else if (!u.dw) {
       const bool on = r < live;
       float4* sums = reinterpret_cast<float4*>(a.acc + ((int64_t)u.tile * CG + rank) * (int64_t)kTileFloats) + at;
       for (int c = 0; c < 4; c++) {
-        fetch(c);
+        fetch_sum(c);
         const int d0 = u.n * kN + half * 128 + 32 * c;
         if (!a.first) {
 #pragma unroll
@@ -494,14 +525,19 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
         }
       }
     } else {
-      for (int c = 0; c < 4; c++) {
-        fetch(c);
+      auto finish = [&](auto get) {
+        for (int c = 0; c < 4; c++) {
+          get(c);
 #pragma unroll
-        for (int i = 0; i < 32; i++) f[i] *= un;
-        if (!(c & 1)) reuse();
-        stage32<DT>(out, lane, c & 1, f);
-        if (c & 1) send(u.n * kN + half * 128 + 32 * (c - 1), a.v0 + r0);
-      }
+          for (int i = 0; i < 32; i++) f[i] *= un;
+          if (!(c & 1)) reuse();
+          stage32<DT>(out, lane, c & 1, f);
+          if (c & 1) send(u.n * kN + half * 128 + 32 * (c - 1), a.v0 + r0);
+        }
+      };
+      // (in one loop the tiles of few rows, which are epilogue for the most part, took 4 % longer)
+      if (begin) finish(fetch);
+      else finish(fetch_sum);
     }
   }
 }
@@ -632,53 +668,62 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
     bool ok = true;
     for (int j = 0; ok && work.get(first, step, j, t); j++) {
       if (t.k0 >= t.k1) continue;  // nothing to multiply: no accumulator
-      const int acc = n & 1;
-      if (!(ok = bar_wait(taken(acc), ((n >> 1) & 1) ^ 1, &gone))) break;
-      n++;
-      fence_after();
-      const uint32_t d = tmem + acc * kN;
       const bool across_a = JOB == BACK && t.dw;
       const uint32_t kind = product_of(DT == SCAPE_BF16, across_a, JOB == BACK, S::kRows, cols);
-      for (int k = t.k0; k < t.k1; k++) {
-        if (!(ok = bar_wait(full(s), ph, &gone))) break;
+      const int chains = chains_of<JOB>(t), length = chains == 1 ? t.k1 - t.k0 : up_div(t.k1 - t.k0, chains);
+      for (int c = 0; ok && c < chains; c++) {
+        const int acc = n & 1;
+        if (!(ok = bar_wait(taken(acc), ((n >> 1) & 1) ^ 1, &gone))) break;
+        n++;
         fence_after();
-        const uint32_t sa = buf + s * stage, sb = sa + bytes_a;
-        // 16 elements of K: 32 bytes along a row, or 16 rows of 128 bytes
-        const uint64_t oa = across_a ? operand(sa, 8192, 1024) : operand(sa, 16, 1024);
-        const uint64_t ob = JOB == BACK ? operand(sb, 8192, 1024) : operand(sb, 16, 1024);
+        const uint32_t d = tmem + acc * kN;
+        const int k0 = t.k0 + c * length, k1 = min(t.k1, k0 + length);
+        for (int k = k0; k < k1; k++) {
+          if (!(ok = bar_wait(full(s), ph, &gone))) break;
+          fence_after();
+          const uint32_t sa = buf + s * stage, sb = sa + bytes_a;
+          // 16 elements of K: 32 bytes along a row, or 16 rows of 128 bytes
+          const uint64_t oa = across_a ? operand(sa, 8192, 1024) : operand(sa, 16, 1024);
+          const uint64_t ob = JOB == BACK ? operand(sb, 8192, 1024) : operand(sb, 16, 1024);
 #pragma unroll
-        for (int i = 0; i < kK / 16; i++)
-          mma<CG>(d, oa + i * (across_a ? 128 : 2), ob + i * (JOB == BACK ? 128 : 2), kind, k > t.k0 || i > 0);
-        commit<CG>(free_(s));
-        if (++s == stages) {
-          s = 0;
-          ph ^= 1u;
+          for (int i = 0; i < kK / 16; i++)
+            mma<CG>(d, oa + i * (across_a ? 128 : 2), ob + i * (JOB == BACK ? 128 : 2), kind, k > k0 || i > 0);
+          commit<CG>(free_(s));
+          if (++s == stages) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
+        if (ok) commit<CG>(ready(acc));
       }
-      if (ok) commit<CG>(ready(acc));
     }
   } else if (warp >= 4) {
     const int half = (warp - 4) >> 2, quarter = warp & 3;
     int n = 0;
     const uint32_t out = buf + kRing + (warp - 4) * kOutBytes;
-    for (int j = 0; work.get(first, step, j, t); j++) {
+    bool ok = true;
+    for (int j = 0; ok && work.get(first, step, j, t); j++) {
       const bool empty = t.k0 >= t.k1;
-      const int acc = n & 1;
-      if (!empty) {
-        if (!bar_wait(ready(acc), (n >> 1) & 1, &gone)) break;
-        fence_after();
-      }
-      __syncwarp();
-      epilogue<JOB, DT, CG, KEEP>(a, &map_out, t, live, (int)rank, half, quarter, lane,
-                            tmem + acc * kN + half * 128 + ((uint32_t)(quarter * 32) << 16), empty, out);
-      if (!empty) {
-        fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (CG == 2) bar_arrive_at(bar_of(taken(acc), 0));
-          else bar_arrive(taken(acc));
+      const int chains = chains_of<JOB>(t);
+      for (int c = 0; c < chains; c++) {
+        const int acc = n & 1;
+        if (!empty) {
+          if (!(ok = bar_wait(ready(acc), (n >> 1) & 1, &gone))) break;
+          fence_after();
         }
-        n++;
+        __syncwarp();
+        epilogue<JOB, DT, CG, KEEP>(a, &map_out, t, live, first, (int)rank, half, quarter, lane,
+                                    tmem + acc * kN + half * 128 + ((uint32_t)(quarter * 32) << 16), empty, c == 0,
+                                    c + 1 == chains, out);
+        if (!empty) {
+          fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (CG == 2) bar_arrive_at(bar_of(taken(acc), 0));
+            else bar_arrive(taken(acc));
+          }
+          n++;
+        }
       }
     }
     if (lane == 0) store_done();

@@ -102,3 +102,109 @@ def test_what_is_kept_adds_little_to_the_rounding_of_g(T, dtype):
     expect = ((step(p, scale) ** 2 / 12 + kept ** 2 / 3).T @ h ** 2 + step(want, 1.0) ** 2 / 12).sum()
     got = (dw[64:].double() - want).square().sum()
     assert float(got) <= 1.1 * float(expect), float(got / expect)
+
+
+def counted(x, bits, least, scale=1.0):
+    """Squares that roundings to "bits" bits behind the leading one add, on average."""
+    step = 2.0 ** torch.floor(torch.log2(x.abs() * scale)).clamp(min=least + bits).sub(bits) / scale
+    return step.nan_to_num(0.0) ** 2 / 12
+
+
+def test_sums_over_a_large_vocabulary():
+    # Words with a common direction: a row's sum over the words before its label comes is as large as the result and what
+    # follows is added to it, 2000 additions one behind the other.  Cut off at 512 of them, and 2^-24 each on average, they may add
+    # a tenth to the roundings that are counted from the exact numbers: G's (not the label's, which is given back) and the result's
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    T, D, V = 4096, 1280, 32000
+    u = torch.nn.functional.normalize(torch.randn(D, generator=gen, device="cuda"), dim=0)
+    W = torch.randn(V, D, generator=gen, device="cuda") * 0.02
+    W -= torch.log1p(torch.arange(V, device="cuda"))[torch.randperm(V, generator=gen, device="cuda")][:, None] / 8 * u
+    H, W = (torch.randn(T, D, generator=gen, device="cuda") + 8 * u).half(), W.half()
+    y = torch.randint(V, (T,), generator=gen, device="cuda")
+    _, dh, _ = pkg.linear_ce_grad(H, W, y)
+    w = W.double()
+    got = expect = 0.0
+    for r in range(0, T, 1024):
+        p = torch.softmax(H[r:r + 1024].double() @ w.T, 1)
+        at = y[r:r + 1024, None]
+        off = (counted(p, 10, -24, 2.0 ** 14) + (2.0 ** -13 * p) ** 2 / 3).scatter(1, at, 0.0)
+        p.scatter_add_(1, at, torch.full(at.shape, -1.0, dtype=p.dtype, device="cuda"))
+        want = p @ w
+        got += float((dh[r:r + 1024].double() - want).square().sum())
+        expect += float((off @ w ** 2).sum() + counted(want, 10, -24).sum())
+    assert got <= 1.21 * expect, got / expect
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_sums_over_many_rows(dtype):
+    # Rows sorted by label: a word's sum is as large as all its labels together when the other rows come, 12500 additions.
+    # 512 of them, cut off by 2^-23 at most, make 2^-14 of the sum of magnitudes.  The probabilities of a word are nearly
+    # the same in all rows here, and equal numbers are rounded alike: the errors of G add up, by half a step of each at
+    # most, and not by their squares
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    T, D, V = 200000, 64, 1000
+    H = (torch.randn(T, D, generator=gen, device="cuda") + 4).to(DT[dtype])
+    W = (torch.randn(V, D, generator=gen, device="cuda") * 0.02).to(DT[dtype])
+    y = torch.randint(V, (T,), generator=gen, device="cuda").sort().values
+    weight = torch.full((T,), 2.0 ** -8, device="cuda")
+    _, _, dw = pkg.linear_ce_grad(H, W, y, row_weight=weight)
+    bits, least, scale = (7, -133, 1.0) if dtype == "bf16" else (10, -24, 2.0 ** 14)
+    want, size, off = (torch.zeros(V, D, dtype=torch.float64, device="cuda") for _ in range(3))
+    for r in range(0, T, 20000):
+        h = H[r:r + 20000].double()
+        G = torch.softmax(h @ W.double().T, 1)
+        kept = (2.0 ** -11 if dtype == "bf16" else 2.0 ** -13) * G
+        G.scatter_add_(1, y[r:r + 20000, None], torch.full((h.shape[0], 1), -1.0, dtype=G.dtype, device="cuda"))
+        off += ((3 * counted(G, bits, least, scale)).sqrt() + kept).T @ h.abs()
+        want += G.T @ h
+        size += G.abs().T @ h.abs()
+    want, size, off = want / 256, size / 256, off / 256
+    err = (dw.double() - want).norm()
+    assert float(err) <= float((off + (3 * counted(want, bits, least)).sqrt()).norm() + 2.0 ** -14 * size.norm())
+
+
+def test_sums_over_millions_of_rows():
+    # 250000 additions one behind the other.  Against the sum of G as it is rounded, in 64 bits: what is kept of the
+    # probabilities adds 2^-13 of them, chains of 512 additions 2^-14 of the magnitudes, the result's rounding 2^-11
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    T, D, V = 4000000, 16, 256
+    H = (torch.randn(T, D, generator=gen, device="cuda") + 4).half()
+    W = (torch.randn(V, D, generator=gen, device="cuda") * 0.3).half()
+    y = torch.randint(V, (T,), generator=gen, device="cuda")
+    _, _, dw = pkg.linear_ce_grad(H, W, y, row_weight=torch.full((T,), 2.0 ** -12, device="cuda"))
+    want, size, kept = (torch.zeros(V, D, dtype=torch.float64, device="cuda") for _ in range(3))
+    for r in range(0, T, 100000):
+        h = H[r:r + 100000].double()
+        p = torch.softmax(h @ W.double().T, 1)
+        kept += p.T @ h.abs()
+        G = p.scatter_add_(1, y[r:r + 100000, None], torch.full((h.shape[0], 1), -1.0, dtype=p.dtype, device="cuda"))
+        G = (G * 2 ** 14).half().double() / 2 ** 26
+        want += G.T @ h
+        size += G.abs().T @ h.abs()
+    err = (dw.double() - want).norm()
+    bound = 2.0 ** -11 * want.norm() + 2.0 ** -14 * size.norm() + 2.0 ** -13 * kept.norm() / 4096
+    assert float(err) <= float(bound), (float(err), float(bound), float(want.norm()))
+
+
+@pytest.mark.parametrize("T,D,V", [(300, 8, 600003), (64, 16, 600003), (9000, 256, 3000), (8193, 520, 9001), (20000, 264, 20001)])
+def test_chains_in_parts_and_in_whole_tiles(T, D, V):
+    # parts of a sum that are chains themselves, rows just above a chain, both products in chains: against 64 bits, bf16
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    H = torch.randn(T, D, generator=gen, device="cuda").bfloat16()
+    W = (torch.randn(V, D, generator=gen, device="cuda") / math.sqrt(D)).bfloat16()
+    y = torch.randint(V, (T,), generator=gen, device="cuda")
+    y[::7] = -100
+    _, dh, dw = pkg.linear_ce_grad(H, W, y)
+    w, rh, rw = W.double(), [], torch.zeros(V, D, dtype=torch.float64, device="cuda")
+    step = max(1, (1 << 28) // V)
+    for r in range(0, T, step):
+        h, at = H[r:r + step].double(), y[r:r + step]
+        G = torch.softmax(h @ w.T, 1)
+        G.scatter_add_(1, at.clamp(min=0)[:, None], torch.full((h.shape[0], 1), -1.0, dtype=G.dtype, device="cuda"))
+        G[at < 0] = 0.0
+        rh.append(G @ w)
+        rw += G.T @ h
+    for got, want in ((dh, torch.cat(rh)), (dw, rw)):
+        assert float((got.double() - want).norm() / want.norm()) <= 2 * ROUND["bf16"]
+    again = pkg.linear_ce_grad(H, W, y)
+    assert bool(torch.equal(again[1], dh)) and bool(torch.equal(again[2], dw))
