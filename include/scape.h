@@ -508,7 +508,7 @@ int scape_route_backward(const scape_route_args* args, const int32_t* idx, const
  * type goes.  dim is a multiple of 8, matrices are 16-byte
  * aligned with strides of a multiple of 8 elements.  The kernels' waits are bounded:
  * one that ran out (which says that the GPU or the library is at fault) makes all
- * losses NaN. */
+ * losses and gradients NaN. */
 typedef struct {
   const void* hidden; /* rows x dim, hidden_stride elements apart */
   const void* weight; /* vocab x dim, weight_stride elements apart */

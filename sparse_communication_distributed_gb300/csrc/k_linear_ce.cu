@@ -33,6 +33,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 
 #include "objective.cuh"
 #include "scape_kernels.cuh"
@@ -96,6 +97,9 @@ struct CeArgs {
   int grid;                // CTAs, or pairs of them, of BACK
   int first, last;
   int early;               // LOSS: no more than one row of tiles
+#ifdef SCAPE_DEBUG_CHECKS
+  int lost;                // test hook: in this job (1 + Job) the first products wait for what nobody sends
+#endif
   void* d_hidden;
   int64_t dh_stride;
   void* d_weight;
@@ -560,7 +564,7 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
   using S = Shape<CG>;
   constexpr int kMax = S::kMaxStages;
   extern __shared__ uint8_t raw[];
-  __shared__ uint64_t bars[2 * kMax + 4];
+  __shared__ uint64_t bars[2 * kMax + 5];
   __shared__ uint32_t tmem_at;
   __shared__ volatile uint32_t gone;
   const uint32_t buf = (smem_at(raw) + 1023u) & ~1023u;
@@ -597,6 +601,9 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
       bar_init(ready(s), 1);
       bar_init(taken(s), kEpiWarps * CG);
     }
+#ifdef SCAPE_DEBUG_CHECKS
+    bar_init(smem_at(&bars[2 * kMax + 4]), 1);
+#endif
     bar_init_fence();
   }
   __syncwarp();
@@ -657,11 +664,6 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
         }
       }
     }
-    if (!ok) {  // what is still being copied arrives meanwhile
-      const uint64_t began = now_ns();
-      while (now_ns() - began < kWaitNs / 100) {
-      }
-    }
   } else if (warp == 1 && lane == 0 && rank == 0) {
     int s = 0, n = 0;
     uint32_t ph = 0;
@@ -679,6 +681,9 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
         const uint32_t d = tmem + acc * kN;
         const int k0 = t.k0 + c * length, k1 = min(t.k1, k0 + length);
         for (int k = k0; k < k1; k++) {
+#ifdef SCAPE_DEBUG_CHECKS
+          if (a.lost == 1 + JOB && blockIdx.x == 0 && !(ok = bar_wait(smem_at(&bars[2 * kMax + 4]), 0, &gone))) break;
+#endif
           if (!(ok = bar_wait(full(s), ph, &gone))) break;
           fence_after();
           const uint32_t sa = buf + s * stage, sb = sa + bytes_a;
@@ -728,9 +733,20 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
     }
     if (lane == 0) store_done();
   }
+  // A wait ran out (never in a correct run): what is still being copied or multiplied ends
+  // meanwhile.  All roles have ended, so nothing is started any more; a CTA whose own waits all
+  // came true has nothing under way (its epilogue saw all of its products), and what its peer
+  // has, the peer waits for.
+  __syncwarp();
+  __syncthreads();
+  if (gone && threadIdx.x == 0) {
+    const uint64_t began = now_ns();
+    while (now_ns() - began < kDrainNs) {
+    }
+  }
   __syncwarp();
   meet();  // (neither CTA of a pair leaves while the other one's products and arrivals may still reach it)
-  if (gone) {  // (never in a correct run) the losses say so
+  if (gone) {  // the losses say so, and the gradients (join_parts)
     if (threadIdx.x == 0) *a.status = 1u;
     for (int64_t i = threadIdx.x; i < a.rows; i += kThreads) a.loss[i] = __uint_as_float(0x7FFFFFFFu);
   }
@@ -933,11 +949,23 @@ __global__ __launch_bounds__(256, 4) void grad_kept(const CeArgs a) {
 }
 
 // The parts of the split tiles, added up in order: a thread has eight columns of a row.
+// Where a wait ran out, behind the last piece, all gradients become NaN.
 template <int DT, int CG>
 __global__ __launch_bounds__(256) void join_parts(const CeArgs a) {
   constexpr int kRows = Shape<CG>::kRows;
   grid_launch_dependents();
   grid_dependency_wait();
+  if (*a.status) {
+    if (!a.last) return;
+    const int64_t vecs = a.D / 8;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (a.rows + a.V) * vecs; i += (int64_t)gridDim.x * 256) {
+      const int64_t row = i / vecs;
+      char* to = row < a.rows ? static_cast<char*>(a.d_hidden) + row * a.dh_stride * 2
+                              : static_cast<char*>(a.d_weight) + (row - a.rows) * a.dw_stride * 2;
+      reinterpret_cast<uint4*>(to)[i - row * vecs] = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
+    }
+    return;
+  }
   const int live = *a.live;
   const Work<BACK, CG> work(a, live);
   const float un = a.scale[1];
@@ -1192,6 +1220,10 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
   a.V = (int)q->vocab;
   constexpr int kRows = Shape<CG>::kRows;
   a.grid = num_sms() / CG;
+#ifdef SCAPE_DEBUG_CHECKS
+  const char* lost = std::getenv("SCAPE_TEST_LOST_WAIT");
+  a.lost = lost ? std::atoi(lost) : 0;
+#endif
   a.n_parts = (int)c.n_parts;
   char* rows = ws + l.rows;
 

@@ -59,8 +59,15 @@ __device__ __forceinline__ uint64_t now_ns() {
 
 // Waits for a phase, at most kWaitNs or until another wait of the CTA has run out.
 // No correct run comes near the limit; a wait that does marks the CTA, whose other
-// waits then end too, so that the kernel returns.
+// waits then end too, so that the kernel returns.  (Debug builds have a test that lets a
+// wait run out.)
+#ifdef SCAPE_DEBUG_CHECKS
+constexpr uint64_t kWaitNs = 200000000ull;
+#else
 constexpr uint64_t kWaitNs = 2000000000ull;
+#endif
+// Copies and products that are under way take microseconds.
+constexpr uint64_t kDrainNs = 20000000ull;
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gone) {
   if (bar_try(bar, parity)) return true;
   const uint64_t began = now_ns();
