@@ -603,8 +603,10 @@ int scape_expert_combine_backward(const void* d_out, const void* y, int dtype, u
  *   out    = x * (norm_g > max_norm ? max_norm / norm_g : 1)
  * Squares are added up in fp32 over 64 elements and in 64 bits from there on, and
  * whatever would leave fp32's range in 64 bits from the start; each product is
- * formed in fp32 and rounded to the result's type.  A group whose norm is infinite or NaN is not scaled (the caller
- * sees the norm), nor is one of norm 0.  The same inputs give the same bits. */
+ * formed in fp32 and rounded to the result's type.  A group whose norm is infinite or NaN
+ * as fp32 (one of finite elements beyond fp32's range, too) is not scaled: the caller
+ * sees the norm.  Nor is one of norm 0.  The same inputs at addresses of the same
+ * alignment give the same bits. */
 typedef struct {
   const void* const* grads; /* HOST array of n_tensors DEVICE pointers, each to numel[i] contiguous
                                elements at any multiple of the element's size */

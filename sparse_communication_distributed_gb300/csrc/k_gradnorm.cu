@@ -166,9 +166,10 @@ __global__ __launch_bounds__(1024) void norm_finish(const __grid_constant__ Grou
   d = cta_sum(d, buf);
   if (threadIdx.x == 0) {
     const double norm = sqrt(d);
-    norms[blockIdx.x] = (float)norm;
-    // (an infinite norm and NaN are not clipped: the caller sees them)
-    const double scale = norm > (double)max_norm && norm < INFINITY ? (double)max_norm / norm : 1.0;
+    const float seen = (float)norm;
+    norms[blockIdx.x] = seen;
+    // (a norm that the caller sees as infinite or NaN is not applied, be it finite in 64 bits)
+    const double scale = norm > (double)max_norm && seen < INFINITY ? (double)max_norm / norm : 1.0;
     // two factors: the scale itself may be below fp32's range where the products are not
     if (scales)
       scales[blockIdx.x] = scale < 0x1p-100 ? make_float2((float)(scale * 0x1p100), 0x1p-100f) : make_float2((float)scale, 1.0f);
