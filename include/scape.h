@@ -601,8 +601,8 @@ int scape_expert_combine_backward(const void* d_out, const void* y, int dtype, u
  * max_norm, in place or into the bf16 buffers that the step takes.
  *   norm_g = sqrt(sum of x^2 over the tensors of group g)
  *   out    = x * (norm_g > max_norm ? max_norm / norm_g : 1)
- * Squares are added up in fp32 over 64 elements and in 64 bits from there on, and
- * whatever would leave fp32's range in 64 bits from the start; each product is
+ * Squares are added up in fp32 over 64 elements (scaled by a power of two where they would
+ * leave its range) and in 64 bits from there on; each product is
  * formed in fp32 and rounded to the result's type.  A group whose norm is infinite or NaN
  * as fp32 (one of finite elements beyond fp32's range, too) is not scaled: the caller
  * sees the norm.  Nor is one of norm 0.  The same inputs at addresses of the same
