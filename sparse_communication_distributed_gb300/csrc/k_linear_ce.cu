@@ -851,8 +851,8 @@ __global__ __launch_bounds__(kRowThreads) void take_rows(const RowsArgs a) {
     *a.status = 0u;
     float s = 1.0f;
     const int e = (int)((__float_as_uint(top) >> 23) & 0xFF);
-    if (e >= 30 && e <= 224) s = a.target / top;
-    else if (e > 0) s = a.target * (e < 30 ? 0x1p97f : 0x1p-97f);  // (0: no weight or a denormal one)
+    if (e >= 30) s = fmaxf(a.target / top, 0x1p-126f);  // (its reciprocal is finite; a bf16 weight becomes 4 at most)
+    else if (e > 0) s = a.target * 0x1p97f;             // (0: no weight or a denormal one)
     a.scale[0] = s;
     a.scale[1] = 1.0f / s;
   }

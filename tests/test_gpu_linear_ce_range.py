@@ -208,3 +208,25 @@ def test_chains_in_parts_and_in_whole_tiles(T, D, V):
         assert float((got.double() - want).norm() / want.norm()) <= 2 * ROUND["bf16"]
     again = pkg.linear_ce_grad(H, W, y)
     assert bool(torch.equal(again[1], dh)) and bool(torch.equal(again[2], dw))
+
+
+@pytest.mark.parametrize("exponent", [90, 97, 98, 100, 120, 127])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_row_weights_near_the_end_of_32_bits(exponent, dtype):
+    # what is exactly 0 stays 0, and nothing becomes NaN: the gradient itself may be beyond the type
+    gen = torch.Generator(device="cuda").manual_seed(exponent)
+    T, D, V = 130, 64, 500
+    H, W = (torch.randn(n, D, generator=gen, device="cuda").to(DT[dtype]) for n in (T, V))
+    H[:, 5], W[:, 9] = 0.0, 0.0
+    y = torch.randint(V, (T,), generator=gen, device="cuda")
+    w = torch.full((T,), 2.0 ** exponent, device="cuda")
+    _, dh, dw = pkg.linear_ce_grad(H, W, y, row_weight=w)
+    assert not dh.isnan().any() and not dw.isnan().any()
+    assert dh[:, 9].eq(0).all() and dw[:, 5].eq(0).all()
+    if dtype == "bf16":
+        # the gradients scale by the power of two, exactly, as far as they are within the type
+        _, eh, ew = pkg.linear_ce_grad(H, W, y)
+        for a, b in ((dh, eh), (dw, ew)):
+            want = b.double() * 2.0 ** exponent
+            ok = (want.abs() < 3e38) & (b.abs() > 2.0 ** -100)
+            assert torch.equal(a.double()[ok], want[ok])
