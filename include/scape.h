@@ -529,11 +529,11 @@ typedef struct {
 } scape_linear_ce_args;
 
 /* Bytes of device workspace for these sizes (host call; of the pointers only whether
- * d_hidden and d_weight are NULL matters): 4 bytes for every 64 logits (of up to 128
- * rows for every 8 or more) and a copy of the hidden states; for the gradients up to
- * 1 GB (or 512 bytes a row) for G or the pieces of it that are there at once, 80 MB
- * for sums in parts and, where the vocabulary has several pieces, fp32 sums of
- * d_hidden. */
+ * d_hidden and d_weight are NULL matters).  With the rows rounded up to a multiple of 64
+ * (more than 128 rows: of 256): 4 bytes for every 64 logits (up to 128 rows: for every 8 or
+ * more) and a copy of the hidden states; for the gradients up to 1 GB (or 512 bytes a row) for
+ * G or the pieces of it that are there at once, 80 MB for sums in parts and, where the
+ * vocabulary has several pieces, fp32 sums of d_hidden. */
 int scape_linear_ce_workspace(const scape_linear_ce_args* args, uint64_t* bytes);
 
 /* The workspace (256-byte aligned) needs no initial value and may be used again by

@@ -81,7 +81,7 @@ struct CeArgs {
   float* scale;            // of the weights, and its reciprocal
   uint32_t* status;        // 0, or a wait ran out
   float* loss;             // caller's
-  int64_t rows, cap;       // caller's rows; rounded up to a multiple of 256
+  int64_t rows, cap;       // caller's rows; rounded up (Cut)
   int D, V;
   int bn;                  // words of a tile (LOSS, GRAD)
   int bm;                  // rows of a CTA's tile of H or G that are copied
@@ -891,7 +891,7 @@ __global__ __launch_bounds__(256, 4) void grad_kept(const CeArgs a) {
   grid_launch_dependents();
   grid_dependency_wait();
   const int live = *a.live, lane = threadIdx.x & 31;
-  const int64_t rows = min((int64_t)(live + 255) / 256 * 256, a.cap);  // (as many as BACK reads)
+  const int64_t rows = up_div(live, kK) * kK;                          // (as many as the sums of dW take; dH's own rows of tiles are not read)
   const int vecs = a.piece / 8, runs = (vecs + kRun - 1) / kRun;       // (beside the last word, too)
   const float scale = a.scale[0];
   for (int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); item < rows * runs; item += (int64_t)gridDim.x * 8) {
@@ -1076,7 +1076,8 @@ uint64_t ceil_div(uint64_t x, uint64_t y) { return (x + y - 1) / y; }
 
 Cut cut_of(const scape_linear_ce_args* q, bool grad) {
   Cut c;
-  c.cap = std::max<uint64_t>(up(q->rows, 256), 256);
+  // (whole tiles; of few rows as many as the sums over them take at a time)
+  c.cap = q->rows <= kM ? up(std::max<uint64_t>(q->rows, 1), kK) : up(q->rows, Shape<2>::kRows);
   // Few rows: the weights' way to the CTAs is what takes time, and tiles of 256 words leave
   // CTAs without any.  The width that needs the fewest words a CTA, all rounds together
   // (32 for a tile's other costs).  16 rows, 32000 words: 224 a tile 30.7 us, 256 32.4, 112 35.2, 64 52.
@@ -1126,7 +1127,7 @@ Layout layout_of(const scape_linear_ce_args* q, const Cut& c, bool grad) {
   l.rows = take(c.cap * q->dim * 2);
   if (grad) {
     l.g = take(std::max<uint64_t>(c.kept, 1) * c.cap * c.piece * 2);
-    if (c.pieces > 1) l.acc = take(c.cap / kM * ceil_div(q->dim, kN) * kTileFloats * 4);
+    if (c.pieces > 1) l.acc = take(ceil_div(c.cap, kM) * ceil_div(q->dim, kN) * kTileFloats * 4);
     l.tail = take(2 * kMaxParts * (uint64_t)num_sms() * kTileFloats * 4);
   }
   l.bytes = at;

@@ -56,3 +56,20 @@ def test_linear_ce_workspace(lib):
     # the hidden states' copy, 4 bytes for 64 logits, row scalars; for gradients a piece of G, sums in parts and those of d_hidden
     assert loss_alone < 8192 * 4096 * 2 + logits / 32 + 8192 * 64
     assert need.value < loss_alone + (1 << 30) + (80 << 20) + 8192 * 4096 * 4 + 4096
+
+
+@pytest.mark.parametrize("rows,taken", [(0, 64), (1, 64), (16, 64), (64, 64), (65, 128), (128, 128), (129, 256), (256, 256), (257, 512)])
+@pytest.mark.parametrize("vocab", [1000, 32000, 1000003])
+def test_linear_ce_workspace_of_few_rows(lib, rows, taken, vocab):
+    # the bound that the header gives: rows rounded up to 64 (more than 128: to 256), 4 bytes for every 64 logits (up to
+    # 128 rows: for every 8) and the last tile's, the hidden states, 28 bytes a row, some of every buffer for its alignment
+    need = ctypes.c_uint64()
+    a = scape.LinearCeArgs(dtype=0, rows=rows, vocab=vocab, dim=2048)
+    assert lib.scape_linear_ce_workspace(ctypes.byref(a), ctypes.byref(need)) == 0
+    words = vocab + 256
+    loss_alone = taken * (words // (16 if rows > 128 else 2) + 2048 * 2 + 28) + 9 * 256
+    assert need.value <= loss_alone
+    a.d_hidden = a.d_weight = P
+    assert lib.scape_linear_ce_workspace(ctypes.byref(a), ctypes.byref(need)) == 0
+    sums = max(taken, 128) * 2048 * 4 if taken * words * 2 > 512 << 20 else 0  # (several pieces)
+    assert need.value <= loss_alone + taken * words * 2 + (80 << 20) + sums + 1024
