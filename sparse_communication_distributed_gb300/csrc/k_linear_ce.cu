@@ -137,8 +137,8 @@ struct Unit {
 // 2.30e-4 (2.08e-4: its own rounding), d_weight of 8 M rows 3.1e-3 and is 2.0e-4.
 constexpr int kChain = 128;
 template <int JOB>
-__device__ __forceinline__ int chains_of(const Unit& u) {
-  return JOB == BACK ? max(1, up_div(u.k1 - u.k0, kChain)) : 1;
+__device__ __forceinline__ int chain_end(const Unit& u, int k) {  // ... of the chain that begins at k
+  return JOB == BACK ? min(u.k1, k + kChain) : u.k1;
 }
 
 // The units of a CTA (or pair), one after the other.
@@ -672,15 +672,14 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
       if (t.k0 >= t.k1) continue;  // nothing to multiply: no accumulator
       const bool across_a = JOB == BACK && t.dw;
       const uint32_t kind = product_of(DT == SCAPE_BF16, across_a, JOB == BACK, S::kRows, cols);
-      const int chains = chains_of<JOB>(t), length = chains == 1 ? t.k1 - t.k0 : up_div(t.k1 - t.k0, chains);
-      for (int c = 0; ok && c < chains; c++) {
+      for (int k = t.k0; ok && k < t.k1;) {
         const int acc = n & 1;
         if (!(ok = bar_wait(taken(acc), ((n >> 1) & 1) ^ 1, &gone))) break;
         n++;
         fence_after();
         const uint32_t d = tmem + acc * kN;
-        const int k0 = t.k0 + c * length, k1 = min(t.k1, k0 + length);
-        for (int k = k0; k < k1; k++) {
+        const int k0 = k, k1 = chain_end<JOB>(t, k);
+        for (; k < k1; k++) {
 #ifdef SCAPE_DEBUG_CHECKS
           if (a.lost == 1 + JOB && blockIdx.x == 0 && !(ok = bar_wait(smem_at(&bars[2 * kMax + 4]), 0, &gone))) break;
 #endif
@@ -709,8 +708,8 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
     bool ok = true;
     for (int j = 0; ok && work.get(first, step, j, t); j++) {
       const bool empty = t.k0 >= t.k1;
-      const int chains = chains_of<JOB>(t);
-      for (int c = 0; c < chains; c++) {
+      for (int k = t.k0, k1;; k = k1) {
+        k1 = chain_end<JOB>(t, k);
         const int acc = n & 1;
         if (!empty) {
           if (!(ok = bar_wait(ready(acc), (n >> 1) & 1, &gone))) break;
@@ -718,8 +717,8 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
         }
         __syncwarp();
         epilogue<JOB, DT, CG, KEEP>(a, &map_out, t, live, first, (int)rank, half, quarter, lane,
-                                    tmem + acc * kN + half * 128 + ((uint32_t)(quarter * 32) << 16), empty, c == 0,
-                                    c + 1 == chains, out);
+                                    tmem + acc * kN + half * 128 + ((uint32_t)(quarter * 32) << 16), empty, k == t.k0,
+                                    k1 == t.k1, out);
         if (!empty) {
           fence_before();
           __syncwarp();
@@ -729,6 +728,7 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
           }
           n++;
         }
+        if (k1 == t.k1) break;
       }
     }
     if (lane == 0) store_done();
