@@ -11,10 +11,9 @@
 // 16-byte loads and stores each of theta, m and v.  HBM traffic per
 // coordinate: 2W + 24 bytes, all compulsory.
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 
 #include "../../include/scape.h"
+#include "host.cuh"
 #include "scape_device.cuh"
 #include "scape_kernels.cuh"
 
@@ -81,16 +80,6 @@ __global__ __launch_bounds__(256) void dense_adams(const DenseArgs p) {
       }
     }
   }
-}
-
-int fail(int code, const char* fmt, ...) {
-  char buf[256];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  set_thread_error(buf);
-  return code;
 }
 
 bool aligned16(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; }

@@ -35,9 +35,8 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 
+#include "host.cuh"
 #include "objective.cuh"
 #include "scape_kernels.cuh"
 
@@ -890,19 +889,6 @@ cudaError_t launch_distill(DistillArgs& a, cudaStream_t s) {
   const cudaError_t last = cudaGetLastError();
   return e != cudaSuccess ? e : last;
 }
-
-int fail(int code, const char* fmt, ...) {
-  char buf[256];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  set_thread_error(buf);
-  return code;
-}
-
-bool known(int dtype) { return dtype >= SCAPE_BF16 && dtype <= SCAPE_F32; }
-bool misaligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
 }  // namespace
 }  // namespace scape

@@ -15,9 +15,8 @@
 // (dispatch), or its k rows are summed in registers (combine): HBM sees each row
 // once.
 #include <algorithm>
-#include <cstdarg>
-#include <cstdio>
 
+#include "host.cuh"
 #include "objective.cuh"
 #include "scape_kernels.cuh"
 
@@ -439,35 +438,6 @@ __global__ __launch_bounds__(kThreads, 4) void combine_grad(const RowArgs a) {
   }
 }
 
-int fail(int code, const char* fmt, ...) {
-  char buf[256];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  set_thread_error(buf);
-  return code;
-}
-
-bool misaligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
-uint64_t size_of(int dtype) { return dtype == SCAPE_F32 ? 4 : 2; }
-
-template <class K, class... A>
-cudaError_t launch_behind(K kernel, unsigned grid, unsigned block, cudaStream_t s, const A&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  const cudaError_t last = cudaGetLastError();
-  return e != cudaSuccess ? e : last;
-}
-
 int check_plan(uint64_t tokens, int k, int experts, int align, uint64_t& capacity, uint64_t& bytes) {
   if (experts < 1 || experts > kMaxExperts)
     return fail(SCAPE_EINVAL, "experts=%d must be in [1, %d]", experts, kMaxExperts);
@@ -524,11 +494,6 @@ bool grid_of(int64_t warps, unsigned& grid) {
   const int64_t g = (warps + kWarps - 1) / kWarps;
   grid = (unsigned)g;
   return g < (1ll << 31);
-}
-
-bool ranges_meet(const void* p, uint64_t n, const void* q, uint64_t m) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a < b + m && b < a + n;
 }
 
 }  // namespace

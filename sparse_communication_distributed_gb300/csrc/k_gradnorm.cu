@@ -16,10 +16,9 @@
 // there is nothing to copy to the device and a captured graph keeps its own.
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <vector>
 
+#include "host.cuh"
 #include "objective.cuh"
 #include "scape_kernels.cuh"
 
@@ -277,19 +276,6 @@ __global__ __launch_bounds__(kThreads, kResident) void clip_chunks(const __grid_
   }
 }
 
-int fail(int code, const char* fmt, ...) {
-  char buf[256];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  set_thread_error(buf);
-  return code;
-}
-
-uint64_t size_of(int dtype) { return dtype == SCAPE_F32 ? 4 : 2; }
-bool known(int dtype) { return dtype >= SCAPE_BF16 && dtype <= SCAPE_F32; }
-
 // How the tensors are cut, by their sizes alone.
 struct Cut {
   uint64_t chunk_elems = kMinChunk, chunks = 0;
@@ -369,22 +355,6 @@ int check_overlap(const scape_grads* g, void* const* out, const uint8_t* odt) {
       return fail(SCAPE_EINVAL, "the result of tensor %u overlaps tensor %u", w[lo].i, i);
   }
   return SCAPE_OK;
-}
-
-template <class K, class... A>
-cudaError_t launch_behind(K kernel, unsigned grid, unsigned block, cudaStream_t s, const A&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  const cudaError_t last = cudaGetLastError();
-  return e != cudaSuccess ? e : last;
 }
 
 // What launch_tables goes through: the tensors, and where the results go (clipping).

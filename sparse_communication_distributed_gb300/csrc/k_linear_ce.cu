@@ -31,10 +31,9 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <cstdlib>
 
+#include "host.cuh"
 #include "objective.cuh"
 #include "scape_kernels.cuh"
 #include "tc.cuh"
@@ -1013,18 +1012,6 @@ __global__ __launch_bounds__(256) void join_parts(const CeArgs a) {
 
 // ---- host -------------------------------------------------------------------------
 
-int fail(int code, const char* fmt, ...) {
-  char buf[256];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  set_thread_error(buf);
-  return code;
-}
-
-bool misaligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
-
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -1154,33 +1141,6 @@ int check_matrix(const void* p, uint64_t stride, uint64_t dim, const char* name)
   return SCAPE_OK;
 }
 
-bool ranges_meet(const void* p, uint64_t n, const void* q, uint64_t m) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return p && q && n && m && a < b + m && b < a + n;
-}
-
-// Launches behind the kernel in front of it, which it waits for on the GPU; in clusters.
-template <class K, class... A>
-cudaError_t launch_behind(K kernel, unsigned grid, unsigned block, uint32_t smem, int cluster, cudaStream_t s,
-                          const A&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2] = {};
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)cluster;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  const cudaError_t last = cudaGetLastError();
-  return e != cudaSuccess ? e : last;
-}
-
 template <int JOB, int DT, int CG, bool KEEP = false>
 cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mwa, const CUtensorMap& mwb,
                            const CUtensorMap& mo, const CeArgs& a, uint64_t tiles, cudaStream_t s) {
@@ -1195,7 +1155,7 @@ cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const C
   }
   unsigned grid = (unsigned)a.grid;  // (BACK divides its work by it)
   if (JOB != BACK) grid = (unsigned)std::min<uint64_t>(std::max<uint64_t>(tiles, 1), grid);
-  return launch_behind(product<JOB, DT, CG, KEEP>, grid * CG, kThreads, kSmem, CG, s, ma, mb, mwa, mwb, mo, a);
+  return launch_clusters(product<JOB, DT, CG, KEEP>, grid * CG, kThreads, kSmem, CG, s, ma, mb, mwa, mwb, mo, a);
 }
 
 template <int DT, int CG>
@@ -1268,7 +1228,7 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
   ra.bad = q->bad_count;
   ra.target = DT == SCAPE_F16 ? 16384.0f : 1.0f;
   cudaError_t e = launch_behind(take_rows, (unsigned)std::max<uint64_t>(ceil_div(q->rows, (uint64_t)ra.chunk), 1),
-                                kRowThreads, 0, 1, s, ra);
+                                kRowThreads, s, ra);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "take_rows: %s", cudaGetErrorString(e));
 
   a.v0 = 0;
@@ -1281,7 +1241,7 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
   e = c.kept ? launch_product<LOSS, DT, CG, true>(along_h, along_w, along_h, along_w, out_g, a, loss_tiles, s)
              : launch_product<LOSS, DT, CG>(along_h, along_w, along_h, along_w, along_w, a, loss_tiles, s);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "product (loss): %s", cudaGetErrorString(e));
-  e = launch_behind(row_losses, (unsigned)ceil_div(std::max<uint64_t>(q->rows, 1), 8), 256, 0, 1, s, a);
+  e = launch_behind(row_losses, (unsigned)ceil_div(std::max<uint64_t>(q->rows, 1), 8), 256, s, a);
   if (e != cudaSuccess) return fail(SCAPE_ECUDA, "row_losses: %s", cudaGetErrorString(e));
   if (!grad) return SCAPE_OK;
 
@@ -1299,7 +1259,7 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
     if (p < c.kept) {
       a.g0 = (int64_t)(p * c.cap);
       a.bn = (int)c.bn;
-      e = launch_behind(grad_kept<DT>, 4u * (unsigned)num_sms(), 256, 0, 1, s, a);
+      e = launch_behind(grad_kept<DT>, 4u * (unsigned)num_sms(), 256, s, a);
     } else {  // (the kept ones are done with)
       a.g0 = 0;
       a.bn = kN;
@@ -1307,7 +1267,7 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
     }
     if (e == cudaSuccess)
       e = launch_product<BACK, DT, CG>(along_g, across_w, across_g, across_h, out_w, a, 0, s);
-    if (e == cudaSuccess) e = launch_behind(join_parts<DT, CG>, 4u * (unsigned)num_sms(), 256, 0, 1, s, a);
+    if (e == cudaSuccess) e = launch_behind(join_parts<DT, CG>, 4u * (unsigned)num_sms(), 256, s, a);
     if (e != cudaSuccess) return fail(SCAPE_ECUDA, "product (gradient): %s", cudaGetErrorString(e));
   }
   return SCAPE_OK;

@@ -35,9 +35,8 @@
 // host; 524288 tokens 82 us, 55 % of the copy bandwidth; 65536 x 256 bf16 23 us, fp32
 // 41 us (49 %).
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 
+#include "host.cuh"
 #include "objective.cuh"
 #include "scape_kernels.cuh"
 
@@ -708,18 +707,6 @@ __global__ __launch_bounds__(kThreads, 2) void route_grad(const RouteArgs a) {
     }
   }
 }
-
-int fail(int code, const char* fmt, ...) {
-  char buf[256];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  set_thread_error(buf);
-  return code;
-}
-
-bool misaligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
 int check_route(const scape_route_args* q) {
   if (!q) return fail(SCAPE_EINVAL, "args is NULL");

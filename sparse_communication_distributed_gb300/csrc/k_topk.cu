@@ -32,9 +32,8 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 
+#include "host.cuh"
 #include "objective.cuh"
 #include "scape_kernels.cuh"
 
@@ -552,16 +551,6 @@ cudaError_t launch_dt(TopkArgs& a, cudaStream_t s) {
   if (a.V <= (kNarrowVecs - 1) * Elem<DT>::kPerVec && a.k <= 256) return launch_groups<DT, Narrow>(a, s);
   const bool longer = a.V > 4 * (Wide::kSmem - 3 * 4096) / 16 * Elem<DT>::kPerVec;
   return longer ? launch_groups<DT, Large>(a, s) : launch_groups<DT, Wide>(a, s);
-}
-
-int fail(int code, const char* fmt, ...) {
-  char buf[256];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  set_thread_error(buf);
-  return code;
 }
 
 }  // namespace

@@ -11,16 +11,17 @@
 // looks the address up with cudaGetSymbolAddress (with that device current),
 // clears the array once and keeps the address.
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <mutex>
 
 #include "../../include/scape.h"
+#include "host.cuh"
 #include "scape_kernels.cuh"
 
 #define SCAPE_API extern "C" __attribute__((visibility("default")))
 
 namespace {
+
+using scape::fail;
 
 constexpr uint64_t kMaxChunks = 65536;  // 256 KiB of flags
 constexpr int kMaxDevices = 64;
@@ -30,16 +31,6 @@ static __device__ __align__(256) uint32_t g_noalloc_scratch[kMaxChunks + 64];
 
 std::mutex g_mu;
 uint32_t* g_scratch_ptr[kMaxDevices] = {};
-
-int fail(int code, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  scape::set_thread_error(buf);
-  return code;
-}
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
