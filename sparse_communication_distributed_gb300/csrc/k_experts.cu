@@ -260,7 +260,7 @@ struct RowArgs {
   int64_t bytes;    // of a row
   int64_t tokens, rows;
   int k;
-  int slices;       // parts of a row that are worked on apart
+  int slices;       // parts of a row that are worked on apart (dispatch, combine)
   const int32_t* slots;
   const int32_t* source;
   const float* weights;
@@ -481,13 +481,17 @@ int check_rows(int dtype, uint64_t tokens, int k, uint64_t rows, uint64_t dim) {
   return SCAPE_OK;
 }
 
-void fill(RowArgs& a, int dtype, uint64_t tokens, int k, uint64_t rows, uint64_t dim, int unit, int units) {
+void fill(RowArgs& a, int dtype, uint64_t tokens, int k, uint64_t rows, uint64_t dim) {
   a.bytes = (int64_t)(dim * size_of(dtype));
   a.tokens = (int64_t)tokens;
   a.rows = (int64_t)rows;
   a.k = k;
+}
+
+// Parts of a row of "bytes", "units" units a lane each.
+int slices_of(int64_t bytes, int unit, int units) {
   const int64_t part = 32 * (int64_t)unit * units;
-  a.slices = (int)((a.bytes + part - 1) / part);
+  return (int)((bytes + part - 1) / part);
 }
 
 bool grid_of(int64_t warps, unsigned& grid) {
@@ -567,7 +571,9 @@ SCAPE_API int scape_expert_dispatch(const void* x, int dtype, uint64_t tokens, u
     return fail(SCAPE_EINVAL, "out must not overlap x");
   RowArgs a{};
   const int unit = unit_of(dtype, dim * es, {row_stride * es, reinterpret_cast<uintptr_t>(x), reinterpret_cast<uintptr_t>(out)});
-  fill(a, dtype, tokens, k, rows, dim, unit, unit == 16 ? units16_of(dim * es, kUnits16) : kUnitsSmall);
+  const int units = unit == 16 ? units16_of(dim * es, kUnits16) : kUnitsSmall;
+  fill(a, dtype, tokens, k, rows, dim);
+  a.slices = slices_of(a.bytes, unit, units);
   a.x = static_cast<const char*>(x);
   a.out = static_cast<char*>(out);
   a.stride = (int64_t)(row_stride * es);
@@ -578,7 +584,6 @@ SCAPE_API int scape_expert_dispatch(const void* x, int dtype, uint64_t tokens, u
   if (!grid_of(a.row_warps + (a.rows + kEmptyRows - 1) / kEmptyRows, grid)) return fail(SCAPE_EINVAL, "too many rows");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  const int units = units16_of(dim * es, kUnits16);
   if (unit == 16)
     e = units == 1   ? launch_behind(dispatch_rows<16, 1>, grid, kThreads, s, a)
         : units == 2 ? launch_behind(dispatch_rows<16, 2>, grid, kThreads, s, a)
@@ -633,7 +638,8 @@ SCAPE_API int scape_expert_combine(const void* y, int dtype, uint64_t rows, uint
   if (ranges_meet(y, rows * dim * es, out, tokens * dim * es)) return fail(SCAPE_EINVAL, "out must not overlap y");
   RowArgs a{};
   const int unit = unit_of(dtype, dim * es, {reinterpret_cast<uintptr_t>(y), reinterpret_cast<uintptr_t>(out)});
-  fill(a, dtype, tokens, k, rows, dim, unit, combine_units(unit, k));
+  fill(a, dtype, tokens, k, rows, dim);
+  a.slices = slices_of(a.bytes, unit, combine_units(unit, k));
   a.x = static_cast<const char*>(y);
   a.out = static_cast<char*>(out);
   a.slots = slots;
@@ -663,7 +669,7 @@ SCAPE_API int scape_expert_combine_backward(const void* d_out, const void* y, in
   RowArgs a{};
   const int unit = unit_of(dtype, dim * es, {reinterpret_cast<uintptr_t>(y), reinterpret_cast<uintptr_t>(d_out),
                                              reinterpret_cast<uintptr_t>(d_y)});
-  fill(a, dtype, tokens, k, rows, dim, unit, unit == 16 ? units16_of(dim * es, kUnits16) : kUnitsSmall);
+  fill(a, dtype, tokens, k, rows, dim);
   a.x = static_cast<const char*>(y);
   a.d_out = static_cast<const char*>(d_out);
   a.out = static_cast<char*>(d_y);
