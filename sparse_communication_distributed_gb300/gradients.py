@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 from array import array
+from collections.abc import Iterable
 
 from . import objective as _o
 from .scape import GradsArgs
@@ -25,6 +26,8 @@ def _flat(grads, name: str):
         for worker in grads:
             if isinstance(worker, _o.torch.Tensor):
                 raise ValueError(f"{name} must not mix tensors and lists")
+            if not isinstance(worker, Iterable):  # (a parameter without a gradient, say)
+                raise ValueError(f"{name} must hold tensors or lists of them, not {type(worker).__name__}")
             flat.extend(worker)
             first.append(len(flat))
         return flat, first

@@ -136,3 +136,15 @@ def test_clip_rejects_overlap(lib, ptrs, out, types, what):
     arr = None if out is None else (ctypes.c_uint64 * 2)(*out)
     says(lib, lib.scape_clip_grads(ctypes.byref(a), 1.0, None if arr is None else ctypes.addressof(arr), types, P, P,
                                    1 << 30, None), what)
+
+
+@pytest.mark.parametrize("worker", [None, 1.0])
+def test_a_parameter_without_a_gradient(worker):
+    torch = pytest.importorskip("torch")
+    from sparse_communication_distributed_gb300 import gradients, objective
+    objective._load()
+    for grads in ([worker], [[torch.zeros(3)], worker]):
+        with pytest.raises(ValueError, match=type(worker).__name__):
+            gradients._flat(grads, "grads")
+    with pytest.raises(ValueError, match=type(worker).__name__):
+        gradients._describe([torch.zeros(3), worker], "grads", -1)
