@@ -499,7 +499,8 @@ int scape_route_backward(const scape_route_args* args, const int32_t* idx, const
  *
  * hidden and weight have one type, bf16 or fp16, and so have their gradients.
  * Products are of 16-bit operands added up in fp32, those over the vocabulary and over the
- * rows 8192 at a time; statistics and losses are fp32.
+ * rows 8192 at a time, those over a dim of more than 1280 1024 at a time; statistics and
+ * losses are fp32.
  * G is rounded to the operands' type (after dividing the weights by the largest of
  * them; for fp16 its entries then keep their precision down to 2^-28), each gradient
  * once more.  Where the logits are kept between the loss and the gradient, the

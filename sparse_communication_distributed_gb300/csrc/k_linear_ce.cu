@@ -135,9 +135,18 @@ struct Unit {
 // chain the fp16 d_hidden of 32000 words with a common direction was 2.99e-4 off and is
 // 2.30e-4 (2.08e-4: its own rounding), d_weight of 8 M rows 3.1e-3 and is 2.0e-4.
 constexpr int kChain = 128;
-template <int JOB>
+// Sums over dim, of logits, are taken in chains where they are long (LONG: dim > kLongDim): of 1024
+// terms, 64 additions, added up in the registers of the epilogue, which for that has those
+// of the other warps.  Losses of 1000 rows, 32000 words, dim 4096: 1.6e-6 (bf16) and 1.9e-6 (fp16) off in one
+// chain, 3.8e-7 and 4.6e-7 so (fp32 throughout: 4.3e-7 and 5.1e-7); dim 1280 in one 3.7e-7
+// and 5.0e-7.  It costs: loss of 16384 x 2048 1.18 -> 1.20 ms, of 8192 x 4096, 131072 words 4.5 -> 4.7,
+// gradient of 512 x 2048 183 -> 188 us.  (72 registers for the others and 216: spills in the
+// thread that issues the products, 4096 x 2048 in 330 us instead of 314.)
+constexpr int kLossChain = 16, kLongDim = 1280;
+constexpr int kRegsOthers = 88, kRegsEpilogue = 208;  // of a thread: 128 x 88 + 256 x 208 = 384 x 168 at the launch
+template <int JOB, bool LONG>
 __device__ __forceinline__ int chain_end(const Unit& u, int k) {  // ... of the chain that begins at k
-  return JOB == BACK ? min(u.k1, k + kChain) : u.k1;
+  return JOB == BACK ? min(u.k1, k + kChain) : LONG ? min(u.k1, k + kLossChain) : u.k1;
 }
 
 // The units of a CTA (or pair), one after the other.
@@ -350,11 +359,12 @@ __device__ __forceinline__ void kept8(const uint4 v, float by, float (&f)[8]) {
 
 // What a warp of the epilogue does with its 32 rows and 128 columns of a unit, in tensor
 // memory at "tmem" ("empty": there were no products, all is 0).  BACK: begin, end: of the
-// unit's chains this is the first, the last; me: the CTA (or pair).
-template <int JOB, int DT, int CG, bool KEEP>
+// unit's chains this is the first, the last; me: the CTA (or pair).  LONG: the sums of all
+// chains, in registers.
+template <int JOB, int DT, int CG, bool KEEP, bool LONG>
 __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map_out, const Unit& u, int live, int me,
                                          int rank, int half, int quarter, int lane, uint32_t tmem, bool empty, bool begin,
-                                         bool end, uint32_t out) {
+                                         bool end, uint32_t out, float (&sums)[2][LONG ? 64 : 1]) {
   const int r0 = u.m * Shape<CG>::kRows + rank * kM + quarter * 32, r = r0 + lane;
   float f[32];
   auto fetch = [&](int c) {
@@ -381,18 +391,15 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
     const int first = u.n * a.bn + half * 128;
     float m = neg_inf(), y = 0.0f;
     bool mine = false;
-    float l[64];
-    auto logits = [&](int c) {  // 64 of them; words that there are not are out of the running
+    auto mask = [&](float (&l)[64], int c) {  // words that there are not are out of the running
       const int w0 = first + 64 * c;
-      tmem_load(tmem + (uint32_t)(64 * c), l);
       if (w0 + 64 > end) {
 #pragma unroll
         for (int i = 0; i < 64; i++)
           if (w0 + i >= end) l[i] = neg_inf();
       }
     };
-    for (int c = 0; c < 2 && first + 64 * c < end; c++) {
-      logits(c);
+    auto find = [&](const float (&l)[64], int c) {
       const int w0 = first + 64 * c;
       if (label >= w0 && label < min(w0 + 64, end)) {
         mine = true;
@@ -402,15 +409,12 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
       }
 #pragma unroll
       for (int i = 0; i < 64; i++) m = fmaxf(m, l[i]);
-    }
-    // (tensor memory is read a second time: that costs less than adjusting sums and what
-    // is kept to a maximum that grows)
-    const float by = shift_of(m);
-    const bool keep = KEEP && first < a.keep;
-    const int p = keep ? first / a.piece : 0;
+    };
+    float by = 0.0f;
+    bool keep = false;
+    int p = 0;
     pair_t sum = pair(0.0f, 0.0f);
-    for (int c = 0; c < 2 && first + 64 * c < end; c++) {
-      logits(c);
+    auto add_up = [&](const float (&l)[64], int c) {
       const int x = first + 64 * c - p * a.piece;
       if (KEEP && CG == 2 && keep) reuse();
 #pragma unroll
@@ -433,6 +437,36 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
         }
       }
       if (KEEP && CG == 2 && keep) send(x, (int)(p * a.cap) + r0);
+    };
+    auto begin_sum = [&]() {
+      by = shift_of(m);
+      keep = KEEP && first < a.keep;
+      p = keep ? first / a.piece : 0;
+    };
+    if constexpr (LONG) {
+      const bool one = first < end, two = first + 64 < end;
+      if (one) mask(sums[0], 0), find(sums[0], 0);
+      if (two) mask(sums[1], 1), find(sums[1], 1);
+      begin_sum();
+      if (one) add_up(sums[0], 0);
+      if (two) add_up(sums[1], 1);
+    } else {
+      float l[64];
+      auto logits = [&](int c) {
+        tmem_load(tmem + (uint32_t)(64 * c), l);
+        mask(l, c);
+      };
+      for (int c = 0; c < 2 && first + 64 * c < end; c++) {
+        logits(c);
+        find(l, c);
+      }
+      // (tensor memory is read a second time: that costs less than adjusting sums and what
+      // is kept to a maximum that grows)
+      begin_sum();
+      for (int c = 0; c < 2 && first + 64 * c < end; c++) {
+        logits(c);
+        add_up(l, c);
+      }
     }
     const float s = sum.x + sum.y;
     if (r < live) {
@@ -444,9 +478,8 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
     const int label = on ? a.label[r] : -1;
     const float2 st = on ? a.stats[r] : make_float2(0.0f, 0.0f);
     const float w = on ? a.weight[r] * a.scale[0] : 0.0f;
-    for (int c = 0; c < 4; c++) {
+    auto quarter_of = [&](int c) {  // 32 words, in f
       const int c0 = u.n * kN + half * 128 + 32 * c, w0 = a.v0 + c0;
-      fetch(c);
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
         const pair_t x = add2(pair(f[i], f[i + 1]), pair(-st.x, -st.x));
@@ -471,6 +504,19 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
       if (!(c & 1)) reuse();
       stage32<DT>(out, lane, c & 1, f);
       if (c & 1) send(c0 - 32, (int)a.g0 + r0);
+    };
+    if constexpr (LONG) {
+#pragma unroll
+      for (int c = 0; c < 4; c++) {
+#pragma unroll
+        for (int i = 0; i < 32; i++) f[i] = sums[c / 2][32 * (c % 2) + i];
+        quarter_of(c);
+      }
+    } else {
+      for (int c = 0; c < 4; c++) {
+        fetch(c);
+        quarter_of(c);
+      }
     }
   } else {
     const float un = a.scale[1];
@@ -553,7 +599,7 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
 // 2048 in 1.09 ms (1.97 PFLOP/s) alone, 4.07 ms for loss and gradient, one call behind the
 // other.  Tiles of one CTA alone took 10 % more.  The epilogue is hidden from a dim of 768
 // on; at 512 it takes as long as the products.
-template <int JOB, int DT, int CG, bool KEEP>
+template <int JOB, int DT, int CG, bool KEEP, bool LONG>
 __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ CUtensorMap map_a,
                                                        const __grid_constant__ CUtensorMap map_b,
                                                        const __grid_constant__ CUtensorMap map_wa,  // dW's operands
@@ -625,99 +671,120 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
   const int live = *a.live;
   const Work<JOB, CG> work(a, live);
   Unit t;
-
-  if (warp == 0 && lane == 0) {
-    if (live == 0)  // no row after all: the stages are completed and left
-      for (int s = 0; s < early; s++) {
-        load_box<CG>(buf + s * stage, &map_a, 0, 0, full(s));
-        bar_wait(full(s), 0, &gone);
-      }
-    int s = 0;
-    uint32_t ph = 0;
-    bool ok = true;
-    for (int j = 0; ok && work.get(first, step, j, t); j++) {
-      const int m0 = t.m * S::kRows + rank * kM, n0 = t.n * cols + rank * (cols / CG);
-      for (int k = t.k0; k < t.k1; k++) {
-        const bool begun = early > 0;
-        if (!begun && !(ok = bar_wait(free_(s), ph ^ 1u, &gone))) break;
-        const uint32_t sa = buf + s * stage, sb = sa + bytes_a;
-        const uint32_t bar = CG == 2 ? bar_of(full(s), 0) : full(s);
-        if (rank == 0 && !begun) bar_expect(full(s), ((t.dw ? kM : a.bm) * kK * 2 + bytes_b) * CG);
-        if (JOB != BACK) {
-          load_box<CG>(sa, &map_a, k * kK, m0, bar);
-          if (begun) early--;
-          else load_box<CG>(sb, &map_b, k * kK, a.v0 + n0, bar);
-        } else if (!t.dw) {
-          load_box<CG>(sa, &map_a, k * kK, (int)a.g0 + m0, bar);
-#pragma unroll
-          for (int i = 0; i < S::kCols / 64; i++) load_box<CG>(sb + i * 8192, &map_b, n0 + 64 * i, a.v0 + k * kK, bar);
-        } else {
-#pragma unroll
-          for (int i = 0; i < kM / 64; i++) load_box<CG>(sa + i * 8192, &map_wa, m0 + 64 * i, (int)a.g0 + k * kK, bar);
-#pragma unroll
-          for (int i = 0; i < S::kCols / 64; i++) load_box<CG>(sb + i * 8192, &map_wb, n0 + 64 * i, k * kK, bar);
+  __syncwarp();
+  if (warp < 4) {
+    if constexpr (LONG) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOthers));
+    if (warp == 0 && lane == 0) {
+      if (live == 0)  // no row after all: the stages are completed and left
+        for (int s = 0; s < early; s++) {
+          load_box<CG>(buf + s * stage, &map_a, 0, 0, full(s));
+          bar_wait(full(s), 0, &gone);
         }
-        if (++s == stages) {
-          s = 0;
-          ph ^= 1u;
-        }
-      }
-    }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
-    int s = 0, n = 0;
-    uint32_t ph = 0;
-    bool ok = true;
-    for (int j = 0; ok && work.get(first, step, j, t); j++) {
-      if (t.k0 >= t.k1) continue;  // nothing to multiply: no accumulator
-      const bool across_a = JOB == BACK && t.dw;
-      const uint32_t kind = product_of(DT == SCAPE_BF16, across_a, JOB == BACK, S::kRows, cols);
-      for (int k = t.k0; ok && k < t.k1;) {
-        const int acc = n & 1;
-        if (!(ok = bar_wait(taken(acc), ((n >> 1) & 1) ^ 1, &gone))) break;
-        n++;
-        fence_after();
-        const uint32_t d = tmem + acc * kN;
-        const int k0 = k, k1 = chain_end<JOB>(t, k);
-        for (; k < k1; k++) {
-#ifdef SCAPE_DEBUG_CHECKS
-          if (a.lost == 1 + JOB && blockIdx.x == 0 && !(ok = bar_wait(smem_at(&bars[2 * kMax + 4]), 0, &gone))) break;
-#endif
-          if (!(ok = bar_wait(full(s), ph, &gone))) break;
-          fence_after();
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int j = 0; ok && work.get(first, step, j, t); j++) {
+        const int m0 = t.m * S::kRows + rank * kM, n0 = t.n * cols + rank * (cols / CG);
+        for (int k = t.k0; k < t.k1; k++) {
+          const bool begun = early > 0;
+          if (!begun && !(ok = bar_wait(free_(s), ph ^ 1u, &gone))) break;
           const uint32_t sa = buf + s * stage, sb = sa + bytes_a;
-          // 16 elements of K: 32 bytes along a row, or 16 rows of 128 bytes
-          const uint64_t oa = across_a ? operand(sa, 8192, 1024) : operand(sa, 16, 1024);
-          const uint64_t ob = JOB == BACK ? operand(sb, 8192, 1024) : operand(sb, 16, 1024);
+          const uint32_t bar = CG == 2 ? bar_of(full(s), 0) : full(s);
+          if (rank == 0 && !begun) bar_expect(full(s), ((t.dw ? kM : a.bm) * kK * 2 + bytes_b) * CG);
+          if (JOB != BACK) {
+            load_box<CG>(sa, &map_a, k * kK, m0, bar);
+            if (begun) early--;
+            else load_box<CG>(sb, &map_b, k * kK, a.v0 + n0, bar);
+          } else if (!t.dw) {
+            load_box<CG>(sa, &map_a, k * kK, (int)a.g0 + m0, bar);
 #pragma unroll
-          for (int i = 0; i < kK / 16; i++)
-            mma<CG>(d, oa + i * (across_a ? 128 : 2), ob + i * (JOB == BACK ? 128 : 2), kind, k > k0 || i > 0);
-          commit<CG>(free_(s));
+            for (int i = 0; i < S::kCols / 64; i++) load_box<CG>(sb + i * 8192, &map_b, n0 + 64 * i, a.v0 + k * kK, bar);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kM / 64; i++) load_box<CG>(sa + i * 8192, &map_wa, m0 + 64 * i, (int)a.g0 + k * kK, bar);
+#pragma unroll
+            for (int i = 0; i < S::kCols / 64; i++) load_box<CG>(sb + i * 8192, &map_wb, n0 + 64 * i, k * kK, bar);
+          }
           if (++s == stages) {
             s = 0;
             ph ^= 1u;
           }
         }
-        if (ok) commit<CG>(ready(acc));
+      }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      int s = 0, n = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int j = 0; ok && work.get(first, step, j, t); j++) {
+        if (t.k0 >= t.k1) continue;  // nothing to multiply: no accumulator
+        const bool across_a = JOB == BACK && t.dw;
+        const uint32_t kind = product_of(DT == SCAPE_BF16, across_a, JOB == BACK, S::kRows, cols);
+        for (int k = t.k0; ok && k < t.k1;) {
+          const int acc = n & 1;
+          if (!(ok = bar_wait(taken(acc), ((n >> 1) & 1) ^ 1, &gone))) break;
+          n++;
+          fence_after();
+          const uint32_t d = tmem + acc * kN;
+          const int k0 = k, k1 = chain_end<JOB, LONG>(t, k);
+          for (; k < k1; k++) {
+#ifdef SCAPE_DEBUG_CHECKS
+            if (a.lost == 1 + JOB && blockIdx.x == 0 && !(ok = bar_wait(smem_at(&bars[2 * kMax + 4]), 0, &gone))) break;
+#endif
+            if (!(ok = bar_wait(full(s), ph, &gone))) break;
+            fence_after();
+            const uint32_t sa = buf + s * stage, sb = sa + bytes_a;
+            // 16 elements of K: 32 bytes along a row, or 16 rows of 128 bytes
+            const uint64_t oa = across_a ? operand(sa, 8192, 1024) : operand(sa, 16, 1024);
+            const uint64_t ob = JOB == BACK ? operand(sb, 8192, 1024) : operand(sb, 16, 1024);
+#pragma unroll
+            for (int i = 0; i < kK / 16; i++)
+              mma<CG>(d, oa + i * (across_a ? 128 : 2), ob + i * (JOB == BACK ? 128 : 2), kind, k > k0 || i > 0);
+            commit<CG>(free_(s));
+            if (++s == stages) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+          if (ok) commit<CG>(ready(acc));
+        }
       }
     }
-  } else if (warp >= 4) {
+  } else {
+    if constexpr (LONG) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpilogue));
     const int half = (warp - 4) >> 2, quarter = warp & 3;
     int n = 0;
     const uint32_t out = buf + kRing + (warp - 4) * kOutBytes;
     bool ok = true;
+    float sums[2][LONG ? 64 : 1];
     for (int j = 0; ok && work.get(first, step, j, t); j++) {
       const bool empty = t.k0 >= t.k1;
       for (int k = t.k0, k1;; k = k1) {
-        k1 = chain_end<JOB>(t, k);
+        k1 = chain_end<JOB, LONG>(t, k);
         const int acc = n & 1;
         if (!empty) {
           if (!(ok = bar_wait(ready(acc), (n >> 1) & 1, &gone))) break;
           fence_after();
         }
         __syncwarp();
-        epilogue<JOB, DT, CG, KEEP>(a, &map_out, t, live, first, (int)rank, half, quarter, lane,
-                                    tmem + acc * kN + half * 128 + ((uint32_t)(quarter * 32) << 16), empty, k == t.k0,
-                                    k1 == t.k1, out);
+        const uint32_t at = tmem + acc * kN + half * 128 + ((uint32_t)(quarter * 32) << 16);
+        auto finish = [&]() {
+          epilogue<JOB, DT, CG, KEEP, LONG>(a, &map_out, t, live, first, (int)rank, half, quarter, lane, at, empty, k == t.k0,
+                                            k1 == t.k1, out, sums);
+        };
+        if constexpr (LONG) {
+#pragma unroll
+          for (int c = 0; c < 4; c++) {
+            float f[32];
+            tmem_load(at + 32 * c, f);
+#pragma unroll
+            for (int i = 0; i < 32; i++) {
+              float& x = sums[c / 2][32 * (c % 2) + i];
+              x = k == t.k0 ? f[i] : x + f[i];
+            }
+          }
+        } else {
+          finish();
+        }
         if (!empty) {
           fence_before();
           __syncwarp();
@@ -727,7 +794,10 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
           }
           n++;
         }
-        if (k1 == t.k1) break;
+        if (k1 == t.k1) {
+          if constexpr (LONG) finish();
+          break;
+        }
       }
     }
     if (lane == 0) store_done();
@@ -1141,21 +1211,35 @@ int check_matrix(const void* p, uint64_t stride, uint64_t dim, const char* name)
   return SCAPE_OK;
 }
 
-template <int JOB, int DT, int CG, bool KEEP = false>
-cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mwa, const CUtensorMap& mwb,
+template <int JOB, int DT, int CG, bool KEEP, bool LONG>
+cudaError_t launch_one(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mwa, const CUtensorMap& mwb,
                            const CUtensorMap& mo, const CeArgs& a, uint64_t tiles, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
-    e = cudaFuncSetAttribute(product<JOB, DT, CG, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    e = cudaFuncSetAttribute(product<JOB, DT, CG, KEEP, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
+    if (LONG) {  // (the epilogue would wait for registers that there are not)
+      cudaFuncAttributes fa{};
+      e = cudaFuncGetAttributes(&fa, product<JOB, DT, CG, KEEP, LONG>);
+      if (e != cudaSuccess) return e;
+      if (fa.numRegs * kThreads < 128 * kRegsOthers + (kThreads - 128) * kRegsEpilogue) return cudaErrorInvalidConfiguration;
+    }
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
   }
   unsigned grid = (unsigned)a.grid;  // (BACK divides its work by it)
   if (JOB != BACK) grid = (unsigned)std::min<uint64_t>(std::max<uint64_t>(tiles, 1), grid);
-  return launch_clusters(product<JOB, DT, CG, KEEP>, grid * CG, kThreads, kSmem, CG, s, ma, mb, mwa, mwb, mo, a);
+  return launch_clusters(product<JOB, DT, CG, KEEP, LONG>, grid * CG, kThreads, kSmem, CG, s, ma, mb, mwa, mwb, mo, a);
+}
+
+template <int JOB, int DT, int CG, bool KEEP = false>
+cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mwa, const CUtensorMap& mwb,
+                           const CUtensorMap& mo, const CeArgs& a, uint64_t tiles, cudaStream_t s) {
+  if constexpr (JOB != BACK)
+    if (a.D > kLongDim) return launch_one<JOB, DT, CG, KEEP, true>(ma, mb, mwa, mwb, mo, a, tiles, s);
+  return launch_one<JOB, DT, CG, KEEP, false>(ma, mb, mwa, mwb, mo, a, tiles, s);
 }
 
 template <int DT, int CG>

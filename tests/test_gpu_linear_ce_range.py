@@ -230,3 +230,75 @@ def test_row_weights_near_the_end_of_32_bits(exponent, dtype):
             want = b.double() * 2.0 ** exponent
             ok = (want.abs() < 3e38) & (b.abs() > 2.0 ** -100)
             assert torch.equal(a.double()[ok], want[ok])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [1344, 4096, 16384])
+@pytest.mark.parametrize("T", [100, 300])
+def test_losses_of_long_rows(T, D, dtype):
+    # Labels with a logit of about -16, to which products of one sign add up; all other words are next to 0.  The tensor cores add
+    # eight products at a time at least and cut off 2^-23 of the sum so far at most.  In chains of 1024 products, each of which
+    # makes 1024 / D of the logit and is half of it on average, that is 128 2^-23 / 2 of the logit whatever D is; one
+    # rounding more a chain
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    V = 2000
+    H = (4 + 0.25 * torch.randn(T, D, generator=gen, device="cuda")).to(DT[dtype])
+    W = 1e-4 * torch.randn(V, D, generator=gen, device="cuda")
+    W[:50] = -16 / (4 * D) * (1 + 0.1 * torch.rand(50, D, generator=gen, device="cuda"))
+    W = W.to(DT[dtype])
+    y = torch.randint(50, (T,), generator=gen, device="cuda")
+    loss = pkg.linear_ce(H, W, y)
+    x = H.double() @ W.double().T
+    label = x.gather(1, y[:, None])
+    want = (torch.logsumexp(x, 1, keepdim=True) - label).squeeze(1)
+    others, most = float(x[:, 50:].abs().max()), float(label.abs().max())
+    rms = float((loss.double() - want).square().mean().sqrt())
+    assert rms <= U * (128 * (most + 2 * others) + D / 1024 * most + 2 * 24) + lse_tol(V), rms
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_long_rows_in_kept_and_recomputed_pieces(dtype):
+    # three pieces, the last one worked out again; dim in two chains
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    T, D, V = 20000, 1344, 30001
+    H = (torch.randn(T, D, generator=gen, device="cuda") + 0.5).to(DT[dtype])
+    W = (torch.randn(V, D, generator=gen, device="cuda") / math.sqrt(D)).to(DT[dtype])
+    y = torch.randint(V, (T,), generator=gen, device="cuda")
+    loss, dh, dw = pkg.linear_ce_grad(H, W, y)
+    w, rh, rw = W.double(), [], torch.zeros(V, D, dtype=torch.float64, device="cuda")
+    for r in range(0, T, 4000):
+        h, at = H[r:r + 4000].double(), y[r:r + 4000, None]
+        x = h @ w.T
+        lse = torch.logsumexp(x, 1, keepdim=True)
+        off = (loss[r:r + 4000, None].double() - (lse - x.gather(1, at))).abs()
+        # (logits of up to 6, 128 additions a chain)
+        assert float(off.max()) <= 2 * 128 * 2.0 ** -23 * float(x.abs().max()) + 2 * lse_tol(V)
+        G = x.sub_(lse).exp_()
+        G.scatter_add_(1, at, torch.full(at.shape, -1.0, dtype=G.dtype, device="cuda"))
+        rh.append(G @ w)
+        rw += G.T @ h
+    for got, want in ((dh, torch.cat(rh)), (dw, rw)):
+        assert float((got.double() - want).norm() / want.norm()) <= 2 * ROUND[dtype]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,D", [(1, 8), (100, 4096), (33, 24), (300, 2048), (700, 40)])
+def test_certain_labels_lose_nothing(T, D, dtype):
+    # what is taken from a logit is in the maximum as well: the loss of a certain label is 0, not below
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    V = 600
+    H = (1 + torch.rand(T, D, generator=gen, device="cuda")).to(DT[dtype])
+    W = torch.zeros(V, D, device="cuda", dtype=DT[dtype])
+    y = torch.randint(V // 2, (T,), generator=gen, device="cuda")
+    W[:V // 2] = 0.1 * torch.randn(V // 2, D, generator=gen, device="cuda").to(DT[dtype])
+    W[V // 2] = 300 / D
+    y[::2] = V // 2
+    loss = pkg.linear_ce(H, W, y)
+    x = H.double() @ W.double().T
+    want = torch.logsumexp(x, 1) - x.gather(1, y[:, None]).squeeze(1)
+    assert bool((loss >= 0).all())
+    sure = want < 1e-20
+    assert bool(sure[::2].any()) and bool(loss[sure].eq(0).all())
+    # (the likeliest word's logit, of products of one sign, eight of which are added at least: D / 8 additions that cut off 2^-23
+    # of it at most; where it is not the label's, this is in the loss)
+    assert float(((loss - want).abs() - D / 8 * 2.0 ** -23 * x.amax(1) - 1e-6 * want - U * 600).max()) <= 0
