@@ -108,7 +108,8 @@ struct CeArgs {
 __device__ __forceinline__ int up_div(int x, int y) { return (x + y - 1) / y; }
 
 // Tiles of a product, in the order in which they are worked on: up to kGroup rows of tiles
-// at a time, down first, in groups of equal height.
+// at a time, down first, in groups of equal height.  (17 rows of tiles, loss of 4352 x 32000, dim
+// 2048: 322 us, with groups of 16 and of one 329 to 335.)
 struct Tiles {
   int mt, nt, kb;  // kb: blocks of the sum
   __device__ __forceinline__ int count() const { return mt * nt; }
@@ -139,9 +140,9 @@ constexpr int kChain = 128;
 // terms, 64 additions, added up in the registers of the epilogue, which for that has those
 // of the other warps.  Losses of 1000 rows, 32000 words, dim 4096: 1.6e-6 (bf16) and 1.9e-6 (fp16) off in one
 // chain, 3.8e-7 and 4.6e-7 so (fp32 throughout: 4.3e-7 and 5.1e-7); dim 1280 in one 3.7e-7
-// and 5.0e-7.  It costs: loss of 16384 x 2048 1.18 -> 1.20 ms, of 8192 x 4096, 131072 words 4.5 -> 4.7,
-// gradient of 512 x 2048 183 -> 188 us.  (72 registers for the others and 216: spills in the
-// thread that issues the products, 4096 x 2048 in 330 us instead of 314.)
+// and 5.0e-7.  It costs 3 % of a loss of dim 2048 in cycles, 9 % where the logits are kept (one chain
+// in this form: -1 and 5 %; two of 24 and 8 blocks: as two of 16).  (72 registers for the
+// others and 216: spills in the thread that issues the products, 4096 x 2048 in 330 us instead of 314.)
 constexpr int kLossChain = 16, kLongDim = 1280;
 constexpr int kRegsOthers = 88, kRegsEpilogue = 208;  // of a thread: 128 x 88 + 256 x 208 = 384 x 168 at the launch
 template <int JOB, bool LONG>
@@ -177,9 +178,13 @@ struct Work {
 constexpr int kMaxParts = 2;         // of each product, per CTA
 // (Where rows make several chains of a tile of dW, the second half of the places for parts of dH
 // holds the CTAs' sums of chains; where dH is not split, it is free anyway.)
-// What a unit costs beside its blocks, in blocks: of pairs (512 rows: 175 us, with 6 181, with
-// 8 184), of CTAs alone, whose blocks wait for HBM (16 rows: 108 us, with 0.5 116, with 3
-// 115, with 6 124); and what writing and adding up a CTA's part costs, on all CTAs.
+// What a unit costs beside its blocks, in blocks: of pairs, of CTAs alone, whose blocks wait
+// for HBM; and what writing and adding up a CTA's part costs, on all CTAs.  Gradients with 32000 words in
+// a graph, us, with 4 and 1.5 | 1 and 0.5 | 8 and 4:
+//   16 rows    dim 1024  73.8 |  78.1 |  73.8   dim 4096 177.6 | 187.6 | 184.3
+//   200 rows   dim 1024  96.3 | 102.7 | 102.5   dim 4096 222.0 | 244.4 | 233.7
+//   512 rows   dim 2048 179.5 | 191.6 | 189.5   dim 4096 312.9 | 328.7 | 332.3
+// (100 rows of dim 4096: 195, 191, 205; from 1300 rows on all three within noise)
 constexpr float kUnitCost = 4.0f, kUnitCostOne = 1.5f, kPartCost = 0.14f;
 template <int CG>
 struct Work<BACK, CG> {
@@ -340,9 +345,9 @@ __device__ __forceinline__ uint32_t keep2(pair_t s) {
   const float a = fmaxf(fmaxf(hi.x, lo.x), kInt), b = fmaxf(fmaxf(hi.y, lo.y), kInt);
   return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
 }
-// Eight exponentials 2^(s + by) of a vector of codes.
+// Eight exponentials 2^(s + by) times "scale" of a vector of codes.
 template <int DT>
-__device__ __forceinline__ void kept8(const uint4 v, float by, float (&f)[8]) {
+__device__ __forceinline__ void kept8(const uint4 v, float by, float scale, float (&f)[8]) {
   using K = Kept<DT>;
   const float hi0 = by - kHigh0 / K::kHigh, lo0 = by - K::kLow0 / K::kLow;
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -352,8 +357,9 @@ __device__ __forceinline__ void kept8(const uint4 v, float by, float (&f)[8]) {
                                __uint_as_float(__byte_perm(w[i], 0x4B000000u, 0x7632))), pair(-kInt, -kInt));
     const pair_t hi = fma2(c, pair(1.0f / K::kHigh, 1.0f / K::kHigh), pair(hi0, hi0));
     const pair_t lo = fma2(c, pair(1.0f / K::kLow, 1.0f / K::kLow), pair(lo0, lo0));
-    f[2 * i] = ex2(fminf(hi.x, lo.x));
-    f[2 * i + 1] = ex2(fminf(hi.y, lo.y));
+    const pair_t e = mul2(ex2_2(pair(fminf(hi.x, lo.x), fminf(hi.y, lo.y))), pair(scale, scale));
+    f[2 * i] = e.x;
+    f[2 * i + 1] = e.y;
   }
 }
 
@@ -593,12 +599,12 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
 
 // Warp 0 copies tiles to shared memory, warp 1 (of a pair's first CTA) issues the products,
 // warp 2 allocates tensor memory, warps 4 to 11 are the epilogue: two accumulators let it
-// work on one tile during the products of the next.  The products follow one another
-// without a pause (4864 x 32000 x 4096: 1.027 M cycles of 1.024 M at the full rate), so
-// that the time of large calls is the clock's, which the power limit sets: 16384 x 32000 x
-// 2048 in 1.09 ms (1.97 PFLOP/s) alone, 4.07 ms for loss and gradient, one call behind the
-// other.  Tiles of one CTA alone took 10 % more.  The epilogue is hidden from a dim of 768
-// on; at 512 it takes as long as the products.
+// work on one tile during the products of the next.  Cycles of a loss of 9728 x 32000: with a
+// dim of 1280 757 K, 831 K where the logits are kept (640 K at the tensor cores' full rate), of 2048
+// 1186 K and 1328 K (1024 K); each 256 of dim are 132 to 137 K (128 K), the rest is the epilogue in the
+// way of the products, and all of it below a dim of 512.  The time of large calls is that of the clock,
+// which the power limit sets: 16384 x 32000 x 2048 in 1.12 ms (1.92 PFLOP/s) alone, 4.1 to 4.3 ms with both
+// gradients.  Tiles of one CTA alone took 10 % more.
 template <int JOB, int DT, int CG, bool KEEP, bool LONG>
 __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ CUtensorMap map_a,
                                                        const __grid_constant__ CUtensorMap map_b,
@@ -952,16 +958,18 @@ __global__ __launch_bounds__(256) void row_losses(const CeArgs a) {
 
 // G of a piece in the place of what was kept of its logits, s:
 //   p = 2^(s + (m_part - m) log2e - log2 sum),  G = w (p - [label]), w scaled
-// A warp has a run of a row, four vectors a lane.  Bound by HBM: 4096 x 50257 at 5.4 TB/s.
+// A warp has a run of a row, six vectors a lane.  Bound by HBM and by the arithmetic of the codes:
+// 4096 x 50257 in 135 us (6.1 TB/s), with four vectors and four CTAs an SM 139, with five 155.
 template <int DT>
-__global__ __launch_bounds__(256, 4) void grad_kept(const CeArgs a) {
+__global__ __launch_bounds__(256, 3) void grad_kept(const CeArgs a) {
   using E = Elem<DT>;
-  constexpr int kVecs = 4, kRun = 32 * kVecs;
+  constexpr int kVecs = 6, kRun = 32 * kVecs;
   grid_launch_dependents();
   grid_dependency_wait();
   const int live = *a.live, lane = threadIdx.x & 31;
-  const int64_t rows = up_div(live, kK) * kK;                          // (as many as the sums of dW take; dH's own rows of tiles are not read)
-  const int vecs = a.piece / 8, runs = (vecs + kRun - 1) / kRun;       // (beside the last word, too)
+  const int64_t rows = up_div(live, kK) * kK;                     // (as many as the sums of dW take: those of dH
+                                                                  // that have no row are not looked at)
+  const int vecs = a.piece / 8, runs = (vecs + kRun - 1) / kRun;  // (beside the last word, too)
   const float scale = a.scale[0];
   for (int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); item < rows * runs; item += (int64_t)gridDim.x * 8) {
     const int r = (int)(item / runs), v0 = (int)(item - (int64_t)r * runs) * kRun + lane;
@@ -993,9 +1001,7 @@ __global__ __launch_bounds__(256, 4) void grad_kept(const CeArgs a) {
       if (v >= vecs) break;
       float x[8];
       if (left > 0) {
-        kept8<DT>(e[i], __fmaf_rn(m[i] - st.x, kLog2e, -st.y), x);
-#pragma unroll
-        for (int j = 0; j < 8; j++) x[j] *= w;
+        kept8<DT>(e[i], __fmaf_rn(m[i] - st.x, kLog2e, -st.y), w, x);
         if (left < 8) {
 #pragma unroll
           for (int j = 0; j < 8; j++)
@@ -1125,8 +1131,8 @@ struct Cut {
 
 // G takes at most this much, so that a gradient needs little memory beside its results:
 // of a piece, and of all pieces that are there at once (kept ones; the others come one
-// after the other).  Pieces of half and of twice the size: 16384 x 32000 in 4.50 and 4.44 ms
-// instead of 4.40.
+// after the other).  Pieces of half and of twice the size: 16384 x 32000 in 4.44 and 4.28 ms
+// instead of 4.10.
 constexpr uint64_t kPieceBytes = 512ull << 20, kAllBytes = 1024ull << 20;
 
 uint64_t ceil_div(uint64_t x, uint64_t y) { return (x + y - 1) / y; }
@@ -1343,7 +1349,7 @@ int run(const scape_linear_ce_args* q, const Cut& c, const Layout& l, char* ws, 
     if (p < c.kept) {
       a.g0 = (int64_t)(p * c.cap);
       a.bn = (int)c.bn;
-      e = launch_behind(grad_kept<DT>, 4u * (unsigned)num_sms(), 256, s, a);
+      e = launch_behind(grad_kept<DT>, 3u * (unsigned)num_sms(), 256, s, a);
     } else {  // (the kept ones are done with)
       a.g0 = 0;
       a.bn = kN;
