@@ -140,9 +140,9 @@ constexpr int kChain = 128;
 // terms, 64 additions, added up in the registers of the epilogue, which for that has those
 // of the other warps.  Losses of 1000 rows, 32000 words, dim 4096: 1.6e-6 (bf16) and 1.9e-6 (fp16) off in one
 // chain, 3.8e-7 and 4.6e-7 so (fp32 throughout: 4.3e-7 and 5.1e-7); dim 1280 in one 3.7e-7
-// and 5.0e-7.  It costs 3 % of a loss of dim 2048 in cycles, 9 % where the logits are kept (one chain
-// in this form: -1 and 5 %; two of 24 and 8 blocks: as two of 16).  (72 registers for the
-// others and 216: spills in the thread that issues the products, 4096 x 2048 in 330 us instead of 314.)
+// and 5.0e-7.  It costs 4 % of the cycles of a loss of dim 2048 whose logits are kept, else nothing
+// (the epilogue's instructions count: chains added up by 512 of them a warp's tile instead of 64 cost 3 %
+// and 10 %; so do spills in the thread that issues the products, with 72 registers for it and 216).
 constexpr int kLossChain = 16, kLongDim = 1280;
 constexpr int kRegsOthers = 88, kRegsEpilogue = 208;  // of a thread: 128 x 88 + 256 x 208 = 384 x 168 at the launch
 template <int JOB, bool LONG>
@@ -601,7 +601,7 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
 // warp 2 allocates tensor memory, warps 4 to 11 are the epilogue: two accumulators let it
 // work on one tile during the products of the next.  Cycles of a loss of 9728 x 32000: with a
 // dim of 1280 757 K, 831 K where the logits are kept (640 K at the tensor cores' full rate), of 2048
-// 1186 K and 1328 K (1024 K); each 256 of dim are 132 to 137 K (128 K), the rest is the epilogue in the
+// 1152 K and 1260 K (1024 K); each 256 of dim are 132 to 137 K (128 K), the rest is the epilogue in the
 // way of the products, and all of it below a dim of 512.  The time of large calls is that of the clock,
 // which the power limit sets: 16384 x 32000 x 2048 in 1.12 ms (1.92 PFLOP/s) alone, 4.1 to 4.3 ms with both
 // gradients.  Tiles of one CTA alone took 10 % more.
@@ -778,14 +778,21 @@ __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ C
                                             k1 == t.k1, out, sums);
         };
         if constexpr (LONG) {
+          if (k == t.k0) {
+            tmem_load(at, sums[0]);
+            tmem_load(at + 64, sums[1]);
+          } else {
 #pragma unroll
-          for (int c = 0; c < 4; c++) {
-            float f[32];
-            tmem_load(at + 32 * c, f);
+            for (int c = 0; c < 4; c++) {
+              float f[32];
+              tmem_load(at + 32 * c, f);
 #pragma unroll
-            for (int i = 0; i < 32; i++) {
-              float& x = sums[c / 2][32 * (c % 2) + i];
-              x = k == t.k0 ? f[i] : x + f[i];
+              for (int i = 0; i < 32; i += 2) {
+                float *x = &sums[c / 2][32 * (c % 2) + i], *y = x + 1;
+                const pair_t both = add2(pair(*x, *y), pair(f[i], f[i + 1]));
+                *x = both.x;
+                *y = both.y;
+              }
             }
           }
         } else {
