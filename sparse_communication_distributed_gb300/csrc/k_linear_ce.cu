@@ -603,7 +603,7 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const CUtensorMap* map
 // dim of 1280 757 K, 831 K where the logits are kept (640 K at the tensor cores' full rate), of 2048
 // 1152 K and 1260 K (1024 K); each 256 of dim are 132 to 137 K (128 K), the rest is the epilogue in the
 // way of the products, and all of it below a dim of 512.  The time of large calls is that of the clock,
-// which the power limit sets: 16384 x 32000 x 2048 in 1.12 ms (1.92 PFLOP/s) alone, 4.1 to 4.3 ms with both
+// which the power limit sets: 16384 x 32000 x 2048 in 1.12 ms (1.92 PFLOP/s) alone, 4.2 to 4.3 ms with both
 // gradients.  Tiles of one CTA alone took 10 % more.
 template <int JOB, int DT, int CG, bool KEEP, bool LONG>
 __global__ __launch_bounds__(kThreads, 1) void product(const __grid_constant__ CUtensorMap map_a,
