@@ -331,7 +331,7 @@ template <> struct Kept<SCAPE_BF16> {  // codes of the two lines at s = 0, codes
   static constexpr float kHigh = 1024.0f, kLow = 204.75f, kLow0 = 26211.0f;
 };
 template <> struct Kept<SCAPE_F16> {
-  static constexpr float kHigh = 3072.0f, kLow = 1024.0f, kLow0 = 40959.0f;
+  static constexpr float kHigh = 3064.0f, kLow = 1024.0f, kLow0 = 41055.0f;
 };
 constexpr float kHigh0 = 65535.0f;
 constexpr float kInt = 8388608.0f;  // 2^23: a sum with it is rounded to a whole number, its low bits
